@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_float, c_int32, c_size_t, c_void_p
+from ctypes import POINTER, c_float, c_int32, c_int64, c_size_t, c_void_p
 
 import torch
 
@@ -48,6 +48,18 @@ class SchedEntry(ctypes.Structure):
     """Mirror of ``cp_sched_entry``."""
 
     _fields_ = [("step", c_int32), ("seq", c_int32), ("start", c_int32), ("rows", c_int32)]
+
+
+class QKPrep(ctypes.Structure):
+    """Mirror of ``cp_qk_prep``."""
+
+    _fields_ = [("rot_dim", c_int32), ("interleaved", c_int32), ("eps", c_float)]
+
+
+class Q4Cache(ctypes.Structure):
+    """Mirror of ``cp_q4_cache``; made by :func:`q4_cache`, it keeps its tensors alive."""
+
+    _fields_ = [("k_codes", c_void_p), ("v_codes", c_void_p), ("k_params", c_void_p), ("v_params", c_void_p)]
 
 
 class CPError(RuntimeError):
@@ -97,12 +109,27 @@ def lib():
         L.cp_status_string.argtypes = [c_int32]
         L.cp_selftest_bounded_wait.argtypes = [P, P, P]
         L.cp_abi_version.argtypes = []
+        I, L64 = c_int32, c_int64
+        L.cp_qk_norm_rope.argtypes = [POINTER(LayerDesc), POINTER(QKPrep), P, L64, P, L64, P, P, P, P, P, P, I, I, P,
+                                      P, P]
+        L.cp_qk_norm_rope_append.argtypes = [POINTER(LayerDesc), POINTER(QKPrep), P, L64, P, L64, P, L64, P, P, P, P,
+                                             P, I, I, P, P, P, P, P, I, P, P]
+        L.cp_kv_append_q4.argtypes = [POINTER(LayerDesc), P, P, P, I, I, POINTER(Q4Cache), P, P, I, P, P]
+        L.cp_kv_read_q4.argtypes = [POINTER(LayerDesc), POINTER(Q4Cache), P, P, P, I, I, I, P, P, P, P]
+        L.cp_chunk_attn_q4.argtypes = [POINTER(LayerDesc), P, POINTER(Q4Cache), P, P, P, I, I, I, P, P, c_size_t, I,
+                                       P, P]
+        L.cp_mixed_step_q4.argtypes = [POINTER(LayerDesc), P, P, P, POINTER(Q4Cache), P, P, P, I, I, I, P, P,
+                                       c_size_t, I, P, P]
+        L.cp_workspace_size_q4.argtypes = [POINTER(LayerDesc), I, I, I]
+        L.cp_workspace_size_q4.restype = c_size_t
         L.cp_status_string.restype = ctypes.c_char_p
         for name in ("cp_kv_append", "cp_pad_chunk", "cp_prefill_chunk_attn", "cp_prefill_chunk",
                      "cp_mixed_step", "cp_mixed_step_overlap", "cp_prefill_varlen", "cp_prefill_varlen_overlap",
                      "cp_chunk_plan",
                      "cp_query_ladder", "cp_query_width", "cp_aligned_length", "cp_rolling_mask",
-                     "cp_schedule", "cp_abi_version", "cp_selftest_bounded_wait"):
+                     "cp_schedule", "cp_abi_version", "cp_selftest_bounded_wait",
+                     "cp_qk_norm_rope", "cp_qk_norm_rope_append", "cp_kv_append_q4", "cp_kv_read_q4",
+                     "cp_chunk_attn_q4", "cp_mixed_step_q4"):
             getattr(L, name).restype = c_int32
         _lib = L
     return _lib
@@ -246,6 +273,180 @@ def cp_mixed_step_noalloc(desc, q, k_new, v_new, k_pages, v_pages, block_table, 
                                     num_seqs, total_rows, max_ctx, _ptr(out), _ptr(dev_status),
                                     _stream(stream, q))
     _check(s, "cp_mixed_step_noalloc")
+
+
+# ---- queries and keys before attention, and the cache held in 4 bits.  Beyond
+# marshalling, these refuse (CPError, CP_ERR_INVALID_ARG) a tensor whose type,
+# device or strides are not what the call takes, instead of reading it wrongly.
+
+def _refuse(where):
+    raise CPError(CP_ERR_INVALID_ARG, where)
+
+
+def _arg(where, t, dtype, numel=None, none=False):
+    """Pointer of a dense CUDA tensor of `dtype` with at least `numel` elements (raw handles pass)."""
+    if t is None:
+        return None if none else _refuse(where)
+    if isinstance(t, int):
+        return t
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or (numel is not None and t.numel() < numel):
+        _refuse(where)
+    return t.data_ptr()
+
+
+def _layer_dtype(desc):
+    return torch.bfloat16 if desc.dtype == CP_BF16 else torch.float16 if desc.dtype == CP_F16 else torch.float32
+
+
+def _rows_arg(where, t, desc, heads, total_rows):
+    """(pointer, row stride in elements) of rows [..., heads, D]: a head row is dense, and one stride leads from
+    each row to the next."""
+    if t is None or isinstance(t, int):
+        return t, 0
+    if (t.dtype != _layer_dtype(desc) or not t.is_cuda or t.dim() < 2
+            or tuple(t.shape[-2:]) != (heads, desc.head_dim) or t.numel() != total_rows * heads * desc.head_dim):
+        _refuse(where)
+    if t.is_contiguous() or t.numel() == 0:
+        return t.data_ptr(), 0
+    if t.stride(-1) != 1 or (heads > 1 and t.stride(-2) != desc.head_dim):
+        _refuse(where)
+    stride = size = None  # of the rows so far, from the last dimension of rows
+    for n, st in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+        if n == 1:
+            continue
+        if stride is None:
+            stride, size = st, n
+        elif st == stride * size:
+            size *= n
+        else:
+            _refuse(where)
+    return t.data_ptr(), stride or 0
+
+
+def qk_prep(rot_dim, interleaved=False, eps=1e-6) -> QKPrep:
+    return QKPrep(rot_dim, 1 if interleaved else 0, eps)
+
+
+def q4_cache(k_codes, v_codes, k_params, v_params) -> Q4Cache:
+    """The arrays of a 4-bit cache: uint8 codes [..., D / 2] and params [..., D / 32, 2] of the layer's type."""
+    for c, p in ((k_codes, k_params), (v_codes, v_params)):
+        if (c.dtype != torch.uint8 or p.dtype not in (torch.bfloat16, torch.float16) or not c.is_contiguous()
+                or not p.is_contiguous() or not c.is_cuda or not p.is_cuda or p.dim() < 2 or p.shape[-1] != 2
+                or tuple(c.shape) != (*p.shape[:-2], p.shape[-2] * 16)):
+            _refuse("q4_cache")
+    if k_codes.shape != v_codes.shape or k_params.dtype != v_params.dtype:
+        _refuse("q4_cache")
+    c = Q4Cache(k_codes.data_ptr(), v_codes.data_ptr(), k_params.data_ptr(), v_params.data_ptr())
+    c.tensors = (k_codes, v_codes, k_params, v_params)
+    return c
+
+
+def _q4_arg(where, desc, cache):
+    """The cache, with arrays as large as desc says."""
+    tensors = getattr(cache, "tensors", None)
+    if tensors is not None:
+        paged = desc.kind == CP_CACHE_PAGED
+        slots = desc.num_pages * desc.page_size if paged else desc.batch * desc.capacity
+        if tensors[2].dtype != _layer_dtype(desc) or tensors[0].numel() < slots * desc.num_kv_heads * (desc.head_dim // 2):
+            _refuse(where)
+    return ctypes.byref(cache)
+
+
+def _seq_args(where, desc, lens, cu_rows, block_table, num_seqs):
+    table = num_seqs * desc.max_blocks if desc.kind == CP_CACHE_PAGED else None
+    return (_arg(where, lens, torch.int32, num_seqs), _arg(where, cu_rows, torch.int32, num_seqs + 1, none=True),
+            _arg(where, block_table, torch.int32, table, none=True))
+
+
+def cp_qk_norm_rope(desc, prep, q, k, q_out, k_out, num_seqs, total_rows, q_weight=None, k_weight=None, inv_freq=None,
+                    positions=None, seqlens_k=None, cu_rows=None, stream=None):
+    """Norm of every query and key head and rotary position, one pass (see include/cp_api.h).  q and k may be
+    slices of a projection's rows."""
+    w, dt = "cp_qk_norm_rope", _layer_dtype(desc)
+    pq, sq = _rows_arg(w, q, desc, desc.num_q_heads, total_rows)
+    pk, sk = _rows_arg(w, k, desc, desc.num_kv_heads, total_rows)
+    d = desc.head_dim
+    s = lib().cp_qk_norm_rope(
+        ctypes.byref(desc), ctypes.byref(prep), pq, sq, pk, sk, _arg(w, q_weight, dt, d, none=True),
+        _arg(w, k_weight, dt, d, none=True), _arg(w, inv_freq, torch.float32, prep.rot_dim // 2, none=True),
+        _arg(w, positions, torch.int32, total_rows, none=True), _arg(w, seqlens_k, torch.int32, num_seqs, none=True),
+        _arg(w, cu_rows, torch.int32, num_seqs + 1, none=True), num_seqs, total_rows,
+        _arg(w, q_out, dt, total_rows * desc.num_q_heads * d, none=True),
+        _arg(w, k_out, dt, total_rows * desc.num_kv_heads * d, none=True), _stream(stream, q, k))
+    _check(s, w)
+
+
+def cp_qk_norm_rope_append(desc, prep, q, k_new, v_new, q_out, k_cache, v_cache, seqlens_k, num_seqs, total_rows,
+                           max_ctx, q_weight=None, k_weight=None, inv_freq=None, positions=None, cu_rows=None,
+                           block_table=None, dev_status=None, stream=None):
+    """cp_qk_norm_rope with the keys and values into their cache slots (see include/cp_api.h)."""
+    w, dt = "cp_qk_norm_rope_append", _layer_dtype(desc)
+    pq, sq = _rows_arg(w, q, desc, desc.num_q_heads, total_rows)
+    pk, sk = _rows_arg(w, k_new, desc, desc.num_kv_heads, total_rows)
+    pv, sv = _rows_arg(w, v_new, desc, desc.num_kv_heads, total_rows)
+    d = desc.head_dim
+    slots = desc.num_pages * desc.page_size if desc.kind == CP_CACHE_PAGED else desc.batch * desc.capacity
+    lens, cu, table = _seq_args(w, desc, seqlens_k, cu_rows, block_table, num_seqs)
+    s = lib().cp_qk_norm_rope_append(
+        ctypes.byref(desc), ctypes.byref(prep), pq, sq, pk, sk, pv, sv, _arg(w, q_weight, dt, d, none=True),
+        _arg(w, k_weight, dt, d, none=True), _arg(w, inv_freq, torch.float32, prep.rot_dim // 2, none=True),
+        _arg(w, positions, torch.int32, total_rows, none=True), cu, num_seqs, total_rows,
+        _arg(w, q_out, dt, total_rows * desc.num_q_heads * d),
+        _arg(w, k_cache, dt, slots * desc.num_kv_heads * d), _arg(w, v_cache, dt, slots * desc.num_kv_heads * d), lens,
+        table, max_ctx, _ptr(dev_status), _stream(stream, q))
+    _check(s, w)
+
+
+def cp_kv_append_q4(desc, k_new, v_new, cache, seqlens_k, num_seqs, total_rows, max_ctx, cu_rows=None,
+                    block_table=None, dev_status=None, stream=None):
+    """Rows into a 4-bit cache (see include/cp_api.h)."""
+    w, dt, n = "cp_kv_append_q4", _layer_dtype(desc), total_rows * desc.num_kv_heads * desc.head_dim
+    lens, cu, table = _seq_args(w, desc, seqlens_k, cu_rows, block_table, num_seqs)
+    s = lib().cp_kv_append_q4(ctypes.byref(desc), _arg(w, k_new, dt, n), _arg(w, v_new, dt, n), cu, num_seqs,
+                              total_rows, _q4_arg(w, desc, cache), lens, table, max_ctx, _ptr(dev_status),
+                              _stream(stream, k_new))
+    _check(s, w)
+
+
+def cp_kv_read_q4(desc, cache, starts, num_seqs, total_rows, max_ctx, k_out, v_out, cu_rows=None, block_table=None,
+                  dev_status=None, stream=None):
+    """The values that rows of a 4-bit cache stand for (see include/cp_api.h)."""
+    w, dt, n = "cp_kv_read_q4", _layer_dtype(desc), total_rows * desc.num_kv_heads * desc.head_dim
+    lens, cu, table = _seq_args(w, desc, starts, cu_rows, block_table, num_seqs)
+    s = lib().cp_kv_read_q4(ctypes.byref(desc), _q4_arg(w, desc, cache), lens, table, cu, num_seqs, total_rows, max_ctx,
+                            _arg(w, k_out, dt, n, none=True), _arg(w, v_out, dt, n, none=True), _ptr(dev_status),
+                            _stream(stream, k_out, v_out))
+    _check(s, w)
+
+
+def cp_chunk_attn_q4(desc, q, cache, seqlens_k, num_seqs, total_rows, max_ctx, out, workspace, cu_rows=None,
+                     block_table=None, commit=True, dev_status=None, stream=None):
+    """Causal attention over a 4-bit cache (see include/cp_api.h)."""
+    w, dt, n = "cp_chunk_attn_q4", _layer_dtype(desc), total_rows * desc.num_q_heads * desc.head_dim
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    lens, cu, table = _seq_args(w, desc, seqlens_k, cu_rows, block_table, num_seqs)
+    s = lib().cp_chunk_attn_q4(ctypes.byref(desc), _arg(w, q, dt, n), _q4_arg(w, desc, cache), lens, table, cu,
+                               num_seqs, total_rows, max_ctx, _arg(w, out, dt, n), _ptr(workspace), ws_bytes,
+                               1 if commit else 0, _ptr(dev_status), _stream(stream, q))
+    _check(s, w)
+
+
+def cp_mixed_step_q4(desc, q, k_new, v_new, cache, seqlens_k, num_seqs, total_rows, max_ctx, out, workspace,
+                     cu_rows=None, block_table=None, commit=True, dev_status=None, stream=None):
+    """Append, attention and advance of a step over a 4-bit cache in one call (see include/cp_api.h)."""
+    w, dt, d = "cp_mixed_step_q4", _layer_dtype(desc), desc.head_dim
+    nq, nk = total_rows * desc.num_q_heads * d, total_rows * desc.num_kv_heads * d
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    lens, cu, table = _seq_args(w, desc, seqlens_k, cu_rows, block_table, num_seqs)
+    s = lib().cp_mixed_step_q4(ctypes.byref(desc), _arg(w, q, dt, nq), _arg(w, k_new, dt, nk), _arg(w, v_new, dt, nk),
+                               _q4_arg(w, desc, cache), table, cu, lens, num_seqs, total_rows, max_ctx,
+                               _arg(w, out, dt, nq), _ptr(workspace), ws_bytes, 1 if commit else 0, _ptr(dev_status),
+                               _stream(stream, q))
+    _check(s, w)
+
+
+def cp_workspace_size_q4(desc, total_rows, max_ctx, num_seqs) -> int:
+    return int(lib().cp_workspace_size_q4(ctypes.byref(desc), total_rows, max_ctx, num_seqs))
 
 
 def cp_noalloc_scratch_bytes() -> int:

@@ -1,0 +1,322 @@
+// cp_api_q4.cu -- the C ABI of the query/key preparation and of the 4-bit
+// cache: argument checks and launches.  Every argument is checked before
+// anything is enqueued.
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include <cuda_runtime.h>
+
+#include "cp_host.h"
+#include "cp_internal.h"
+#include "cp_q4.h"
+
+using namespace cp;
+
+namespace {
+
+// The rows of a call: cu_rows, or equal rows when that is NULL.
+int rows_of(const int32_t* cu_rows, int32_t num_seqs, int32_t total_rows, SeqRows* out) {
+  if (num_seqs <= 0 || total_rows < 0) return CP_ERR_INVALID_ARG;
+  if (!cu_rows && total_rows % num_seqs != 0) return CP_ERR_INVALID_ARG;
+  *out = SeqRows{num_seqs, cu_rows ? 0 : total_rows / num_seqs, cu_rows};
+  return CP_OK;
+}
+
+// Most rows a sequence of the call can have (every listed one has at least one).
+int64_t most_rows(const SeqRows& r, int32_t total_rows) {
+  if (r.rows_uniform > 0) return r.rows_uniform;
+  return total_rows >= r.num_seqs ? (int64_t)total_rows - r.num_seqs + 1 : total_rows;
+}
+
+bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
+}
+
+// A row stride in elements: 0 = dense; else at least the row and whole 16-byte pieces.
+int stride_of(int64_t given, int64_t dense, int es, long long* out) {
+  if (given != 0 && (given < dense || given % (16 / es) != 0)) return CP_ERR_INVALID_ARG;
+  if (given > (INT64_MAX >> 34)) return CP_ERR_UNSUPPORTED;  // stride * rows * bytes stays within 64 bits
+  *out = given ? given : dense;
+  return CP_OK;
+}
+
+// The checks that cp_qk_norm_rope and its append share; fills *a.
+int rope_check(const cp_layer_desc* d, const cp_qk_prep* p, const void* q, int64_t q_stride, const void* k,
+               int64_t k_stride, const void* q_weight, const void* k_weight, const float* inv_freq, void* q_out,
+               RopeArgs* a, int32_t total_rows) {
+  const int r = check_desc(d, false);
+  if (r != CP_OK) return r;
+  if (!p || !std::isfinite(p->eps) || p->eps < 0.f || (p->interleaved != 0 && p->interleaved != 1))
+    return CP_ERR_INVALID_ARG;
+  if (p->rot_dim < 0 || p->rot_dim > d->head_dim) return CP_ERR_INVALID_ARG;
+  if (p->rot_dim % 16 != 0) return CP_ERR_UNSUPPORTED;
+  const int es = esize_of(d->dtype);
+  long long qs, ks;
+  int e = stride_of(q_stride, (int64_t)d->num_q_heads * d->head_dim, es, &qs);
+  if (e != CP_OK) return e;
+  e = stride_of(k_stride, (int64_t)d->num_kv_heads * d->head_dim, es, &ks);
+  if (e != CP_OK) return e;
+  if ((q != nullptr) != (q_out != nullptr)) return CP_ERR_INVALID_ARG;
+  if (total_rows > 0 && p->rot_dim > 0 && !inv_freq) return CP_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(q_weight) || !aligned16(k_weight) || !aligned16(q_out) ||
+      (reinterpret_cast<uintptr_t>(inv_freq) & 3u))
+    return CP_ERR_INVALID_ARG;
+  std::memset(a, 0, sizeof(*a));
+  a->hq = q ? d->num_q_heads : 0;
+  a->hkv = k ? d->num_kv_heads : 0;
+  a->half = p->rot_dim / 2;
+  a->interleaved = p->interleaved != 0;
+  a->eps = p->eps;
+  a->total_rows = total_rows;
+  a->q = q;
+  a->k = k;
+  a->q_stride = qs;
+  a->k_stride = ks;
+  a->q_weight = q_weight;
+  a->k_weight = k_weight;
+  a->inv_freq = inv_freq;
+  a->q_out = q_out;
+  return CP_OK;
+}
+
+// Bytes that `rows` rows of `width` elements `stride` apart span.
+int64_t span(int64_t rows, int64_t stride, int64_t width, int es) {
+  return rows > 0 ? ((rows - 1) * stride + width) * es : 0;
+}
+
+// Where the call's rows may go: CONTIG, ROLLING and PAGED limits of a call with
+// a host bound on positions.
+int cache_check(const cp_layer_desc* d, const SeqRows& rows, int32_t total_rows, const int32_t* block_table,
+                int32_t max_ctx) {
+  if (max_ctx <= 0) return CP_ERR_INVALID_ARG;
+  if (d->kind == CP_CACHE_PAGED) {
+    if (!block_table) return CP_ERR_INVALID_ARG;
+  } else if (rows.num_seqs > d->batch) {
+    return CP_ERR_INVALID_ARG;
+  }
+  if (d->kind == CP_CACHE_ROLLING) {
+    if (most_rows(rows, total_rows) > d->capacity) return CP_ERR_CAPACITY;
+  } else if ((int64_t)max_ctx > layout_limit(d)) {
+    return CP_ERR_CAPACITY;
+  }
+  return CP_OK;
+}
+
+// Layers and caches that may be held in 4 bits, and the cache's arrays.
+int q4_check(const cp_layer_desc* d, const cp_q4_cache* c) {
+  const int r = check_desc(d, false);
+  if (r != CP_OK) return r;
+  if (d->dtype == CP_F32 || d->kind == CP_CACHE_ROLLING) return CP_ERR_UNSUPPORTED;
+  if (!c || !c->k_codes || !c->v_codes || !c->k_params || !c->v_params) return CP_ERR_INVALID_ARG;
+  if (!aligned16(c->k_codes) || !aligned16(c->v_codes) || !aligned16(c->k_params) || !aligned16(c->v_params))
+    return CP_ERR_INVALID_ARG;
+  return CP_OK;
+}
+
+Q4Args q4_args(const cp_layer_desc* d, const cp_q4_cache* c, const SeqRows& rows, int32_t total_rows,
+               const int32_t* past, const int32_t* block_table, int32_t max_ctx, int32_t* dev_status) {
+  Q4Args a;
+  std::memset(&a, 0, sizeof(a));
+  a.hkv = d->num_kv_heads;
+  a.rows = rows;
+  a.total_rows = total_rows;
+  a.cache = make_cache(d, block_table);
+  a.past = past;
+  a.max_ctx = max_ctx;
+  a.k_codes = static_cast<uint8_t*>(c->k_codes);
+  a.v_codes = static_cast<uint8_t*>(c->v_codes);
+  a.k_params = static_cast<uint32_t*>(c->k_params);
+  a.v_params = static_cast<uint32_t*>(c->v_params);
+  a.status = dev_status;
+  return a;
+}
+
+// The checks of cp_chunk_attn_q4 and cp_mixed_step_q4, but for the new rows.
+int q4_attn_check(const cp_layer_desc* d, const void* q, const cp_q4_cache* c, const int32_t* seqlens_k,
+                  const int32_t* block_table, const int32_t* cu_rows, int32_t num_seqs, int32_t total_rows,
+                  int32_t max_ctx, const void* out, const void* workspace, size_t workspace_bytes, SeqRows* rows) {
+  int r = q4_check(d, c);
+  if (r != CP_OK) return r;
+  r = rows_of(cu_rows, num_seqs, total_rows, rows);
+  if (r != CP_OK) return r;
+  const int G = d->num_q_heads / d->num_kv_heads;
+  if (G > 16 || (G & (G - 1))) return CP_ERR_UNSUPPORTED;
+  if (total_rows == 0) return CP_OK;
+  if (!q || !out || !seqlens_k || !aligned16(q) || !aligned16(out)) return CP_ERR_INVALID_ARG;
+  r = cache_check(d, *rows, total_rows, block_table, max_ctx);
+  if (r != CP_OK) return r;
+  const size_t need = cp_workspace_size_q4(d, total_rows, max_ctx, num_seqs);
+  if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return CP_ERR_WORKSPACE;
+  return CP_OK;
+}
+
+int q4_attention(const cp_layer_desc* d, const void* q, const cp_q4_cache* c, const int32_t* past,
+                 const int32_t* block_table, const SeqRows& rows, int32_t total_rows, int32_t max_ctx, void* out,
+                 int32_t* dev_status, cudaStream_t st) {
+  Q4AttnArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.hq = d->num_q_heads;
+  a.hkv = d->num_kv_heads;
+  a.group = a.hq / a.hkv;
+  a.scale_log2 = scale_log2(d);
+  a.rows = rows;
+  a.total_rows = total_rows;
+  a.cache = make_cache(d, block_table);
+  a.past = past;
+  a.max_ctx = max_ctx;
+  a.q = q;
+  a.k_codes = static_cast<const uint8_t*>(c->k_codes);
+  a.v_codes = static_cast<const uint8_t*>(c->v_codes);
+  a.k_params = static_cast<const uint32_t*>(c->k_params);
+  a.v_params = static_cast<const uint32_t*>(c->v_params);
+  a.out = out;
+  a.status = dev_status;
+  return launch_result(launch_q4_attn_rows(a, d->dtype, d->head_dim, st));
+}
+
+}  // namespace
+
+extern "C" {
+
+int cp_qk_norm_rope(const cp_layer_desc* desc, const cp_qk_prep* prep, const void* q, int64_t q_row_stride,
+                    const void* k, int64_t k_row_stride, const void* q_weight, const void* k_weight,
+                    const float* inv_freq, const int32_t* positions, const int32_t* seqlens_k,
+                    const int32_t* cu_rows, int32_t num_seqs, int32_t total_rows, void* q_out, void* k_out,
+                    void* stream) {
+  RopeArgs a;
+  int r = rope_check(desc, prep, q, q_row_stride, k, k_row_stride, q_weight, k_weight, inv_freq, q_out, &a, total_rows);
+  if (r != CP_OK) return r;
+  if ((k != nullptr) != (k_out != nullptr) || !aligned16(k_out)) return CP_ERR_INVALID_ARG;
+  if (positions) {
+    if (total_rows < 0) return CP_ERR_INVALID_ARG;
+    a.rows = SeqRows{1, total_rows, nullptr};
+  } else {
+    r = rows_of(cu_rows, num_seqs, total_rows, &a.rows);
+    if (r != CP_OK) return r;
+    if (total_rows > 0 && !seqlens_k) return CP_ERR_INVALID_ARG;
+  }
+  if (total_rows == 0 || (!q && !k)) return CP_OK;
+  // Outputs may be their own dense inputs and overlap nothing else.
+  const int es = esize_of(desc->dtype);
+  const int64_t wq = (int64_t)desc->num_q_heads * desc->head_dim, wk = (int64_t)desc->num_kv_heads * desc->head_dim;
+  const int64_t nq = q ? span(total_rows, a.q_stride, wq, es) : 0, nk = k ? span(total_rows, a.k_stride, wk, es) : 0;
+  const int64_t oq = q ? span(total_rows, wq, wq, es) : 0, ok = k ? span(total_rows, wk, wk, es) : 0;
+  if (q && overlap(q_out, oq, q, nq) && !(q_out == q && a.q_stride == wq)) return CP_ERR_INVALID_ARG;
+  if (k && overlap(k_out, ok, k, nk) && !(k_out == k && a.k_stride == wk)) return CP_ERR_INVALID_ARG;
+  if (q && k && (overlap(q_out, oq, k, nk) || overlap(k_out, ok, q, nq) || overlap(q_out, oq, k_out, ok)))
+    return CP_ERR_INVALID_ARG;
+  a.positions = positions;
+  a.past = seqlens_k;
+  a.k_out = k_out;
+  return launch_result(launch_qk_rope(a, desc->dtype, desc->head_dim, static_cast<cudaStream_t>(stream)));
+}
+
+int cp_qk_norm_rope_append(const cp_layer_desc* desc, const cp_qk_prep* prep, const void* q, int64_t q_row_stride,
+                           const void* k_new, int64_t k_row_stride, const void* v_new, int64_t v_row_stride,
+                           const void* q_weight, const void* k_weight, const float* inv_freq,
+                           const int32_t* positions, const int32_t* cu_rows, int32_t num_seqs, int32_t total_rows,
+                           void* q_out, void* k_cache, void* v_cache, const int32_t* seqlens_k,
+                           const int32_t* block_table, int32_t max_ctx, int32_t* dev_status, void* stream) {
+  RopeArgs a;
+  int r = rope_check(desc, prep, q, q_row_stride, k_new, k_row_stride, q_weight, k_weight, inv_freq, q_out, &a,
+                     total_rows);
+  if (r != CP_OK) return r;
+  r = rows_of(cu_rows, num_seqs, total_rows, &a.rows);
+  if (r != CP_OK) return r;
+  const int es = esize_of(desc->dtype);
+  const int64_t wq = (int64_t)desc->num_q_heads * desc->head_dim, wk = (int64_t)desc->num_kv_heads * desc->head_dim;
+  r = stride_of(v_row_stride, wk, es, &a.v_stride);
+  if (r != CP_OK) return r;
+  if (total_rows == 0) return CP_OK;
+  if (!q || !k_new || !v_new || !k_cache || !v_cache || !seqlens_k) return CP_ERR_INVALID_ARG;
+  if (!aligned16(v_new) || !aligned16(k_cache) || !aligned16(v_cache)) return CP_ERR_INVALID_ARG;
+  r = cache_check(desc, a.rows, total_rows, block_table, max_ctx);
+  if (r != CP_OK) return r;
+  const int64_t nq = span(total_rows, a.q_stride, wq, es), oq = span(total_rows, wq, wq, es);
+  if (overlap(q_out, oq, q, nq) && !(q_out == q && a.q_stride == wq)) return CP_ERR_INVALID_ARG;
+  if (overlap(q_out, oq, k_new, span(total_rows, a.k_stride, wk, es)) ||
+      overlap(q_out, oq, v_new, span(total_rows, a.v_stride, wk, es)))
+    return CP_ERR_INVALID_ARG;
+  a.positions = positions;
+  a.past = seqlens_k;
+  a.v = v_new;
+  a.cache = make_cache(desc, block_table);
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.max_ctx = max_ctx;
+  a.status = dev_status;
+  return launch_result(launch_qk_rope(a, desc->dtype, desc->head_dim, static_cast<cudaStream_t>(stream)));
+}
+
+int cp_kv_append_q4(const cp_layer_desc* desc, const void* k_new, const void* v_new, const int32_t* cu_rows,
+                    int32_t num_seqs, int32_t total_rows, const cp_q4_cache* cache, const int32_t* seqlens_k,
+                    const int32_t* block_table, int32_t max_ctx, int32_t* dev_status, void* stream) {
+  int r = q4_check(desc, cache);
+  if (r != CP_OK) return r;
+  SeqRows rows;
+  r = rows_of(cu_rows, num_seqs, total_rows, &rows);
+  if (r != CP_OK || total_rows == 0) return r;
+  if (!k_new || !v_new || !seqlens_k || !aligned16(k_new) || !aligned16(v_new)) return CP_ERR_INVALID_ARG;
+  r = cache_check(desc, rows, total_rows, block_table, max_ctx);
+  if (r != CP_OK) return r;
+  Q4Args a = q4_args(desc, cache, rows, total_rows, seqlens_k, block_table, max_ctx, dev_status);
+  a.k_new = k_new;
+  a.v_new = v_new;
+  return launch_result(launch_q4_append(a, desc->dtype, desc->head_dim, static_cast<cudaStream_t>(stream)));
+}
+
+int cp_kv_read_q4(const cp_layer_desc* desc, const cp_q4_cache* cache, const int32_t* starts,
+                  const int32_t* block_table, const int32_t* cu_rows, int32_t num_seqs, int32_t total_rows,
+                  int32_t max_ctx, void* k_out, void* v_out, int32_t* dev_status, void* stream) {
+  int r = q4_check(desc, cache);
+  if (r != CP_OK) return r;
+  SeqRows rows;
+  r = rows_of(cu_rows, num_seqs, total_rows, &rows);
+  if (r != CP_OK || total_rows == 0) return r;
+  if (!starts || !aligned16(k_out) || !aligned16(v_out)) return CP_ERR_INVALID_ARG;
+  r = cache_check(desc, rows, total_rows, block_table, max_ctx);
+  if (r != CP_OK) return r;
+  if (!k_out && !v_out) return CP_OK;
+  Q4Args a = q4_args(desc, cache, rows, total_rows, starts, block_table, max_ctx, dev_status);
+  a.k_out = k_out;
+  a.v_out = v_out;
+  return launch_result(launch_q4_read(a, desc->dtype, desc->head_dim, static_cast<cudaStream_t>(stream)));
+}
+
+size_t cp_workspace_size_q4(const cp_layer_desc* desc, int32_t total_rows, int32_t max_ctx, int32_t num_seqs) {
+  if (check_desc(desc, false) != CP_OK || total_rows <= 0 || max_ctx <= 0 || num_seqs <= 0) return 0;
+  return 0;
+}
+
+int cp_chunk_attn_q4(const cp_layer_desc* desc, const void* q, const cp_q4_cache* cache, int32_t* seqlens_k,
+                     const int32_t* block_table, const int32_t* cu_rows, int32_t num_seqs, int32_t total_rows,
+                     int32_t max_ctx, void* out, void* workspace, size_t workspace_bytes, int32_t commit,
+                     int32_t* dev_status, void* stream) {
+  SeqRows rows;
+  int r = q4_attn_check(desc, q, cache, seqlens_k, block_table, cu_rows, num_seqs, total_rows, max_ctx, out, workspace,
+                        workspace_bytes, &rows);
+  if (r != CP_OK || total_rows == 0) return r;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  r = q4_attention(desc, q, cache, seqlens_k, block_table, rows, total_rows, max_ctx, out, dev_status, st);
+  if (r != CP_OK || !commit) return r;
+  return launch_result(launch_commit(seqlens_k, rows, rows.rows_uniform > 0 ? rows.rows_uniform : -1, dev_status, st));
+}
+
+int cp_mixed_step_q4(const cp_layer_desc* desc, const void* q, const void* k_new, const void* v_new,
+                     const cp_q4_cache* cache, const int32_t* block_table, const int32_t* cu_rows,
+                     int32_t* seqlens_k, int32_t num_seqs, int32_t total_rows, int32_t max_ctx, void* out,
+                     void* workspace, size_t workspace_bytes, int32_t commit, int32_t* dev_status, void* stream) {
+  SeqRows rows;
+  int r = q4_attn_check(desc, q, cache, seqlens_k, block_table, cu_rows, num_seqs, total_rows, max_ctx, out, workspace,
+                        workspace_bytes, &rows);
+  if (r != CP_OK || total_rows == 0) return r;
+  r = cp_kv_append_q4(desc, k_new, v_new, cu_rows, num_seqs, total_rows, cache, seqlens_k, block_table, max_ctx,
+                      dev_status, stream);
+  if (r != CP_OK) return r;
+  return cp_chunk_attn_q4(desc, q, cache, seqlens_k, block_table, cu_rows, num_seqs, total_rows, max_ctx, out,
+                          workspace, workspace_bytes, commit, dev_status, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,81 @@
+// cp_q4.h -- argument blocks and launchers of the query/key preparation and of
+// the 4-bit cache.  Every pointer is a device pointer.
+#pragma once
+
+#include "cp_internal.h"
+
+namespace cp {
+
+// Norm and rotation of the query and key heads (cp_qk_norm_rope), and, when
+// k_cache is set, the keys and values into their cache slots.
+struct RopeArgs {
+  int hq, hkv;             // 0: that tensor is skipped
+  int pairs;               // lanes of a head row that rotate (see qk_rope.cu)
+  int half;                // first channel of the second half (rot_dim / 2), half-split pairs
+  bool interleaved;
+  float eps;
+  SeqRows rows;
+  int total_rows;
+  const void* q;
+  const void* k;
+  const void* v;           // append only
+  long long q_stride, k_stride, v_stride;  // elements from a row to the next
+  const void* q_weight;    // [D] or nullptr
+  const void* k_weight;
+  const float* inv_freq;
+  const int* positions;    // [total_rows] or nullptr: past + row within the sequence
+  const int* past;
+  void* q_out;
+  void* k_out;             // dense rows, without an append
+  CacheView cache;
+  int cache_hkv;           // KV heads of the cache
+  void* k_cache;
+  void* v_cache;
+  int max_ctx;
+  int* status;
+};
+
+// Rows into or out of a 4-bit cache.
+struct Q4Args {
+  int hkv;
+  SeqRows rows;
+  int total_rows;
+  CacheView cache;
+  const int* past;         // position of each sequence's first row
+  int max_ctx;
+  uint8_t* k_codes;        // [..., D / 2]
+  uint8_t* v_codes;
+  uint32_t* k_params;      // [..., D / 32]: scale in the low half, smallest value in the high half
+  uint32_t* v_params;
+  const void* k_new;       // append: rows in
+  const void* v_new;
+  void* k_out;             // read: rows out (either may be nullptr)
+  void* v_out;
+  int* past_snapshot;      // optional [num_seqs]: CTA 0 copies past[] here
+  int* status;
+};
+
+// Attention over a 4-bit cache.
+struct Q4AttnArgs {
+  int hq, hkv, group;
+  float scale_log2;        // softmax scale * log2(e)
+  SeqRows rows;
+  int total_rows;
+  CacheView cache;
+  const int* past;
+  int max_ctx;
+  const void* q;           // [total_rows, hq, D]
+  const uint8_t* k_codes;
+  const uint8_t* v_codes;
+  const uint32_t* k_params;
+  const uint32_t* v_params;
+  void* out;
+  int* status;
+};
+
+cudaError_t launch_qk_rope(const RopeArgs& a, int dtype, int d, cudaStream_t st);
+cudaError_t launch_q4_append(const Q4Args& a, int dtype, int d, cudaStream_t st);
+cudaError_t launch_q4_read(const Q4Args& a, int dtype, int d, cudaStream_t st);
+cudaError_t launch_q4_attn_rows(const Q4AttnArgs& a, int dtype, int d, cudaStream_t st);
+
+}  // namespace cp

@@ -1,0 +1,209 @@
+// qk_rope.cu -- norm of every query and key head and rotary position, in one
+// pass over the rows, and optionally the keys and values into their cache.
+//
+//   y = x * rsqrt(mean(x^2) + eps) * w;  (a, b) -> (a cos u - b sin u, b cos u + a sin u)
+//
+// Each element is read once and written once and costs a few operations, so
+// the pass is bound by bytes.  A head row of D channels belongs to LPR lanes,
+// each holding two 16-byte chunks of it, chosen so that both members of every
+// rotated pair are in one lane: with half-split pairs lane l < P holds chunks l
+// and l + P (P = rot_dim / 2 channels in chunks) and the lanes from P on take the
+// unrotated chunks two by two; with adjacent pairs lane l holds chunks 2l and
+// 2l + 1.  Either way lane l < P rotates EPC pairs, of frequencies l * EPC on, and
+// the others none, so no channel crosses lanes and the only shuffles are the
+// sum of squares over LPR lanes.  A warp takes RPW = 32 / LPR head rows of one
+// token at a time; the token's sines and cosines are computed once per warp,
+// each row group taking EPC / RPW of the pairs.
+//
+// Angles: inv_freq is turned into a 64-bit fixed-point fraction of a turn per
+// position (integer product of its significand with 2^66 / 2 pi), so
+// position * step mod 2^64 is the angle mod one turn for any int32 position,
+// with no reduction error to speak of.  Its top 32 bits go to sincospif: the
+// angle's error is below 2^-23 (half a unit of the fraction's float), whatever
+// the position.
+#include <cstdint>
+
+#include "cp_q4.h"
+#include "cp_rows.cuh"
+
+namespace cp {
+namespace {
+
+// Turns per position, as a 64-bit fraction (mod one turn), of |f| radians per
+// position: f = m 2^e, and m * (2^66 / 2 pi) fits 88 bits.
+__device__ __forceinline__ uint64_t turn_step(float f) {
+  constexpr uint64_t kTurns66 = 11743562013128004906ull;  // 2^66 / (2 pi)
+  const uint32_t b = __float_as_uint(f);
+  const int ex = (b >> 23) & 255;
+  const uint64_t m = (b & 0x7fffffu) | (ex ? 0x800000u : 0u);
+  const int shift = 152 - (ex ? ex : 1);  // right shift of m * kTurns66: 2 - e
+  const uint64_t hi = __umul64hi(m, kTurns66), lo = m * kTurns66;
+  uint64_t r;
+  if (shift >= 128) r = 0;
+  else if (shift >= 64) r = hi >> (shift - 64);
+  else if (shift > 0) r = (hi << (64 - shift)) | (lo >> shift);
+  else r = shift > -64 ? lo << -shift : 0;
+  return (b >> 31) ? 0 - r : r;
+}
+
+template <typename T, int D>
+struct RopeShape {
+  static constexpr int kPer16 = 16 / (int)sizeof(T);  // EPC: channels of a chunk
+  static constexpr int kLanes = D / (2 * kPer16);     // LPR
+  static constexpr int kRows = 32 / kLanes;           // RPW
+  static constexpr int kShare = kPer16 / kRows;       // pairs whose angle a row group computes
+  static_assert(kShare >= 1, "a warp's row groups share a lane's pairs evenly");
+};
+
+constexpr int kRopeThreads = 128;
+
+// per_warp: head-row blocks (of kRows rows) a warp takes; splits: warps per token.
+template <typename T, int D, bool kAppend>
+__global__ void __launch_bounds__(kRopeThreads) qk_rope_kernel(const RopeArgs a, int per_warp, int splits) {
+  using S = RopeShape<T, D>;
+  constexpr int E = S::kPer16, L = S::kLanes, R = S::kRows;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const long long w = ((long long)blockIdx.x * kRopeThreads + threadIdx.x) >> 5;
+  const int t = (int)(w / splits);
+  if (t >= a.total_rows) return;
+  const int l = lane % L, rg = lane / L;
+  const bool rot = l < a.pairs;
+
+  // Chunks of this lane within a head row.
+  int c0 = 2 * l, c1 = 2 * l + 1;
+  if (!a.interleaved && rot) {
+    c0 = l;
+    c1 = l + a.pairs;
+  }
+  long long pos = 0;  // position within the sequence, from the cached length
+  int s = 0;
+  if (kAppend || !a.positions) {
+    s = row_seq(a.rows, t);
+    pos = (long long)a.past[s] + t - seq_row0(a.rows, s);
+  }
+  const long long ang = a.positions ? a.positions[t] : pos;
+
+  float cs[E], sn[E];
+  if (a.pairs > 0) {
+    float c[S::kShare], n[S::kShare];
+#pragma unroll
+    for (int i = 0; i < S::kShare; ++i) {
+      c[i] = 1.f;
+      n[i] = 0.f;
+      if (rot) {
+        const uint64_t turns = (uint64_t)ang * turn_step(a.inv_freq[l * E + rg * S::kShare + i]);
+        sincospif((float)(int)(turns >> 32) * 0x1p-31f, &n[i], &c[i]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      cs[e] = __shfl_sync(0xffffffffu, c[e % S::kShare], (e / S::kShare) * L + l);
+      sn[e] = __shfl_sync(0xffffffffu, n[e % S::kShare], (e / S::kShare) * L + l);
+    }
+  }
+
+  const int heads = a.hq + a.hkv + (kAppend ? a.hkv : 0);
+  const int h_begin = (int)(w % splits) * per_warp * R, h_end = min(heads, h_begin + per_warp * R);
+  for (int h0 = h_begin; h0 < h_end; h0 += R) {
+    const int h = h0 + rg;
+    const bool on = h < h_end;
+    const bool is_q = h < a.hq, is_v = kAppend && h >= a.hq + a.hkv;
+    const int g = is_q ? h : is_v ? h - a.hq - a.hkv : h - a.hq;
+    const T* src = is_q ? static_cast<const T*>(a.q) + t * a.q_stride
+                 : is_v ? static_cast<const T*>(a.v) + t * a.v_stride
+                        : static_cast<const T*>(a.k) + t * a.k_stride;
+    const uint4* in = reinterpret_cast<const uint4*>(src + (long long)g * D);
+    uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
+    if (on) {
+      v0 = in[c0];
+      v1 = in[c1];
+    }
+    const T* wt = static_cast<const T*>(is_q ? a.q_weight : a.k_weight);
+    float x0[E], x1[E];
+    unpack16<T>(v0, x0);
+    unpack16<T>(v1, x1);
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) ss += x0[e] * x0[e] + x1[e] * x1[e];
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (!is_v) {
+      if (wt) {
+        const float r = rsqrtf(ss * (1.f / D) + a.eps);
+        float w0[E], w1[E];
+        unpack16<T>(reinterpret_cast<const uint4*>(wt)[c0], w0);
+        unpack16<T>(reinterpret_cast<const uint4*>(wt)[c1], w1);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          x0[e] = x0[e] * r * w0[e];
+          x1[e] = x1[e] * r * w1[e];
+        }
+      }
+      if (rot) {
+        if (a.interleaved) {
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) {
+            const float p = x0[2 * e], q = x0[2 * e + 1], u = x1[2 * e], z = x1[2 * e + 1];
+            x0[2 * e] = p * cs[e] - q * sn[e];
+            x0[2 * e + 1] = q * cs[e] + p * sn[e];
+            x1[2 * e] = u * cs[e + E / 2] - z * sn[e + E / 2];
+            x1[2 * e + 1] = z * cs[e + E / 2] + u * sn[e + E / 2];
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const float p = x0[e], q = x1[e];
+            x0[e] = p * cs[e] - q * sn[e];
+            x1[e] = q * cs[e] + p * sn[e];
+          }
+        }
+      }
+      v0 = pack16<T>(x0);
+      v1 = pack16<T>(x1);
+    }
+    if (!on) continue;
+    T* dst;
+    if (is_q) {
+      dst = static_cast<T*>(a.q_out) + ((long long)t * a.hq + g) * D;
+    } else if (!kAppend) {
+      dst = static_cast<T*>(a.k_out) + ((long long)t * a.hkv + g) * D;
+    } else {
+      const long long row = cache_row(a.cache, a.hkv, s, g, pos, a.max_ctx);
+      if (row < 0) {
+        if (a.status && l == 0) atomicOr(a.status, CP_DEV_BOUNDS);
+        continue;
+      }
+      dst = static_cast<T*>(is_v ? a.v_cache : a.k_cache) + row * D;
+    }
+    reinterpret_cast<uint4*>(dst)[c0] = v0;
+    reinterpret_cast<uint4*>(dst)[c1] = v1;
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch_t(RopeArgs a, cudaStream_t st) {
+  using S = RopeShape<T, D>;
+  a.pairs = a.half / S::kPer16;
+  const int heads = a.hq + a.hkv + (a.k_cache ? a.hkv : 0);
+  const int blocks = (heads + S::kRows - 1) / S::kRows;
+  const int per_warp = blocks, splits = 1;
+  const long long warps = (long long)a.total_rows * splits;
+  const long long grid = (warps * 32 + kRopeThreads - 1) / kRopeThreads;
+  if (grid >= (1ll << 31)) return cudaErrorInvalidValue;
+  if (a.k_cache)
+    return launch_pdl(qk_rope_kernel<T, D, true>, dim3((unsigned)grid), dim3(kRopeThreads), 0, st, a, per_warp, splits);
+  return launch_pdl(qk_rope_kernel<T, D, false>, dim3((unsigned)grid), dim3(kRopeThreads), 0, st, a, per_warp, splits);
+}
+
+}  // namespace
+
+cudaError_t launch_qk_rope(const RopeArgs& a, int dtype, int d, cudaStream_t st) {
+  if (a.total_rows == 0 || a.hq + a.hkv == 0) return cudaSuccess;
+  if (dtype == CP_F32) return d == 64 ? launch_t<float, 64>(a, st) : launch_t<float, 128>(a, st);
+  if (dtype == CP_BF16) return d == 64 ? launch_t<__nv_bfloat16, 64>(a, st) : launch_t<__nv_bfloat16, 128>(a, st);
+  return d == 64 ? launch_t<__half, 64>(a, st) : launch_t<__half, 128>(a, st);
+}
+
+}  // namespace cp

@@ -354,6 +354,169 @@ size_t cp_noalloc_scratch_bytes(void);
 size_t cp_workspace_size(const cp_layer_desc* desc, int32_t max_rows, int32_t max_ctx,
                          int32_t num_seqs);
 
+/* ---- queries and keys before attention: norm per head and rotary position ---- */
+
+/* What cp_qk_norm_rope does to each head's D channels. */
+typedef struct {
+  int32_t rot_dim;     /* channels rotated (the first rot_dim): a multiple of 16, 0 .. head_dim; 0 = none */
+  int32_t interleaved; /* 0: channel i pairs with i + rot_dim / 2;  1: channel 2i pairs with 2i + 1        */
+  float eps;           /* added to the mean square; finite, >= 0                                            */
+} cp_qk_prep;
+
+/* cp_qk_norm_rope -- root-mean-square norm of every query and key head and the
+ * rotary position embedding, in one pass.
+ *
+ * For each row t and head, with x its D channels in 32 bits:
+ *   y = x / sqrt(mean(x^2) + eps) * w     (w = q_weight or k_weight [D]; NULL: y = x, no norm)
+ *   (a, b) -> (a cos u - b sin u, b cos u + a sin u) for the pairs i = 0 .. rot_dim / 2 - 1 of
+ *   the first rot_dim channels, u = position(t) * inv_freq[i];  other channels: y
+ * rounded once, to the layer's type, at the end.  The angle is exact for every
+ * int32 position: it is reduced in 64-bit fixed-point turns before its sine and
+ * cosine are taken.
+ *   q, k          device rows of [Hq, D] and [Hkv, D]; row t starts row_stride
+ *                 elements after row t - 1 (0 = dense; else at least the row's
+ *                 own elements and a multiple of 16 bytes), so that both may be
+ *                 slices of one projection's output.  q with q_out, or k with
+ *                 k_out, may be NULL: that tensor is skipped.
+ *   q_weight, k_weight  device [D] of the layer's type, or NULL
+ *   inv_freq      device float [rot_dim / 2], finite (NULL when rot_dim is 0)
+ *   positions     device int32 [total_rows], or NULL: the position of row t is
+ *                 then seqlens_k[s] + (its row within sequence s), with the rows
+ *                 of the sequences given by cu_rows (device int32 [num_seqs + 1]
+ *                 as in cp_mixed_step) or, when that is NULL, total_rows /
+ *                 num_seqs rows each.  With positions given, seqlens_k and
+ *                 cu_rows are not read and may be NULL.
+ *   q_out, k_out  device [total_rows, Hq, D] and [total_rows, Hkv, D], dense.
+ *                 q_out may be q itself (dense), k_out may be k; any other
+ *                 overlap returns CP_ERR_INVALID_ARG.
+ * desc gives the type, the heads and head_dim; its cache fields are checked as
+ * always but not used. */
+int cp_qk_norm_rope(const cp_layer_desc* desc, const cp_qk_prep* prep, const void* q, int64_t q_row_stride,
+                    const void* k, int64_t k_row_stride, const void* q_weight, const void* k_weight,
+                    const float* inv_freq, const int32_t* positions, const int32_t* seqlens_k,
+                    const int32_t* cu_rows, int32_t num_seqs, int32_t total_rows, void* q_out, void* k_out,
+                    void* stream);
+
+/* cp_qk_norm_rope_append -- cp_qk_norm_rope with the finished keys, and the
+ * values, written straight to their cache slots: what cp_qk_norm_rope followed
+ * by the append writes, bit for bit, in one launch.
+ *
+ * Row t of sequence s goes to absolute position seqlens_k[s] + (its row within
+ * the sequence), in any kind of cache (slots as in cp_kv_append); seqlens_k is
+ * not modified (cp_prefill_chunk_attn commits it).  `positions` (may be NULL)
+ * sets the rotation's position only.
+ *   v_new         device rows of [Hkv, D] with v_row_stride, copied bit for bit
+ *   cu_rows       NULL for total_rows / num_seqs rows each
+ *   q_out         device [total_rows, Hq, D], dense (q itself, when dense)
+ *   max_ctx       host bound on seqlens_k[s] + rows of s; a row whose position
+ *                 is not in [0, max_ctx) is not appended and sets CP_DEV_BOUNDS
+ *                 (its q_out is still written).  CONTIG: num_seqs <= batch and
+ *                 max_ctx <= capacity; PAGED: max_ctx <= max_blocks * page_size;
+ *                 ROLLING: num_seqs <= batch and no sequence may have more rows
+ *                 than capacity.
+ * The caches must not overlap q, k_new, v_new or q_out. */
+int cp_qk_norm_rope_append(const cp_layer_desc* desc, const cp_qk_prep* prep, const void* q, int64_t q_row_stride,
+                           const void* k_new, int64_t k_row_stride, const void* v_new, int64_t v_row_stride,
+                           const void* q_weight, const void* k_weight, const float* inv_freq,
+                           const int32_t* positions, const int32_t* cu_rows, int32_t num_seqs, int32_t total_rows,
+                           void* q_out, void* k_cache, void* v_cache, const int32_t* seqlens_k,
+                           const int32_t* block_table, int32_t max_ctx, int32_t* dev_status, void* stream);
+
+/* ---- a cache held in 4 bits ---- */
+
+/* A CONTIG or PAGED cache of desc whose rows are held in 4 bits (bf16 and fp16
+ * layers; 160 bytes for the K and V row of a 128-channel head instead of 512).
+ * Each row's channels are cut into groups of CP_Q4_GROUP.  A group stores its
+ * smallest value m and a scale s, both in the layer's type, and a code c of 0 ..
+ * 15 for each channel; the channel stands for m + c * s, rounded once to the
+ * layer's type.  With lo and hi the group's smallest and largest values:
+ *   m = lo,  s = (hi - lo) / 15 in 32 bits, then cut toward zero to the layer's
+ *   type (so m + 15 s never exceeds hi),  c = (x - m) / s in 32 bits, rounded to
+ *   the nearest whole number (ties to even), at most 15;  s = 0: c = 0.
+ * A group that holds a NaN or an infinity, or whose hi - lo overflows 32 bits,
+ * gets s = NaN: all its channels read as NaN.
+ *   codes         uint8 [B, Hkv, capacity, D / 2] (CONTIG) or
+ *                 [num_pages, Hkv, page_size, D / 2] (PAGED): every 8 channels
+ *                 are one 32-bit word (little-endian), channel 8w + 2i in bits
+ *                 [4i, 4i + 4) and channel 8w + 2i + 1 in bits [16 + 4i, 20 + 4i)
+ *   params        the layer's type [..., D / CP_Q4_GROUP, 2]: (s, m) of each group
+ * All four device pointers are 16-byte aligned. */
+#define CP_Q4_GROUP 32
+typedef struct {
+  void* k_codes;
+  void* v_codes;
+  void* k_params;
+  void* v_params;
+} cp_q4_cache;
+
+/* cp_kv_append_q4 -- cp_kv_append into a 4-bit cache.
+ *   k_new, v_new  device [total_rows, Hkv, D], dense
+ *   cu_rows       device int32 [num_seqs + 1] (rows of sequence s as in
+ *                 cp_mixed_step), or NULL: total_rows / num_seqs rows each
+ *   seqlens_k     device int32 [num_seqs]: position of each sequence's first
+ *                 row; not modified
+ *   block_table   device int32 [num_seqs, max_blocks] (PAGED, else NULL)
+ *   max_ctx       host bound on seqlens_k[s] + rows of s; a row outside it, or
+ *                 whose page id is out of range, is skipped and sets CP_DEV_BOUNDS
+ * CONTIG: num_seqs <= batch.  ROLLING caches and fp32 layers return
+ * CP_ERR_UNSUPPORTED (so do the other calls on a 4-bit cache). */
+int cp_kv_append_q4(const cp_layer_desc* desc, const void* k_new, const void* v_new, const int32_t* cu_rows,
+                    int32_t num_seqs, int32_t total_rows, const cp_q4_cache* cache, const int32_t* seqlens_k,
+                    const int32_t* block_table, int32_t max_ctx, int32_t* dev_status, void* stream);
+
+/* cp_kv_read_q4 -- the values that rows of a 4-bit cache stand for: row t of
+ * sequence s is position starts[s] + (its row within the sequence), read to row
+ * t of k_out and v_out [total_rows, Hkv, D] in the layer's type (either may be
+ * NULL).  Rows of the sequences, starts (device int32 [num_seqs]), block_table,
+ * max_ctx and dev_status as in cp_kv_append_q4; a skipped row is left unwritten.
+ * For moving a cache elsewhere, or carrying on a sequence on the 16-bit paths. */
+int cp_kv_read_q4(const cp_layer_desc* desc, const cp_q4_cache* cache, const int32_t* starts,
+                  const int32_t* block_table, const int32_t* cu_rows, int32_t num_seqs, int32_t total_rows,
+                  int32_t max_ctx, void* k_out, void* v_out, int32_t* dev_status, void* stream);
+
+/* cp_chunk_attn_q4 -- causal attention of query rows over a 4-bit cache.
+ *
+ * Row i of sequence s is the query at position p = seqlens_k[s] + i and attends
+ * to the values that positions [0, p] stand for (its own chunk's rows, appended
+ * by cp_kv_append_q4, among them); otherwise as cp_prefill_chunk_attn.
+ *   q, out        device [total_rows, Hq, D]
+ *   cu_rows       device int32 [num_seqs + 1], every sequence with at least one
+ *                 row (one without sets CP_DEV_BOUNDS), or NULL: total_rows /
+ *                 num_seqs rows each
+ *   max_ctx       host bound on seqlens_k[s] + rows of s; a sequence outside it
+ *                 is skipped (its rows of out are left as they were) and sets
+ *                 CP_DEV_BOUNDS
+ *   workspace     device scratch, 16-byte aligned, of at least
+ *                 cp_workspace_size_q4(desc, total_rows, max_ctx, num_seqs)
+ *                 bytes; its contents before the call do not matter.  Calls
+ *                 whose work overlaps on the GPU need separate workspaces.
+ *   commit        not 0: seqlens_k[s] += rows of s after the attention
+ * Paths: sequences of one row, and calls with equal rows of at most 16 / G each,
+ * take a memory-bound split-KV path that reads the cache once for all of a KV
+ * head's rows; the others a tensor-core path.  Hq / Hkv must be 1, 2, 4, 8 or 16.
+ * A row's result depends only on its own sequence.  Slots past a sequence's
+ * positions may hold anything.  A non-finite value of a visible key makes the
+ * rows that see it non-finite, and may make rows before it so that share its
+ * 128-key tile. */
+int cp_chunk_attn_q4(const cp_layer_desc* desc, const void* q, const cp_q4_cache* cache, int32_t* seqlens_k,
+                     const int32_t* block_table, const int32_t* cu_rows, int32_t num_seqs, int32_t total_rows,
+                     int32_t max_ctx, void* out, void* workspace, size_t workspace_bytes, int32_t commit,
+                     int32_t* dev_status, void* stream);
+
+/* cp_mixed_step_q4 -- one token-budget step over a 4-bit cache: cp_kv_append_q4
+ * of every row, cp_chunk_attn_q4 of every row and, when commit is not 0, the
+ * advance of seqlens_k, in one call with the same results.  Arguments as in
+ * those two. */
+int cp_mixed_step_q4(const cp_layer_desc* desc, const void* q, const void* k_new, const void* v_new,
+                     const cp_q4_cache* cache, const int32_t* block_table, const int32_t* cu_rows,
+                     int32_t* seqlens_k, int32_t num_seqs, int32_t total_rows, int32_t max_ctx, void* out,
+                     void* workspace, size_t workspace_bytes, int32_t commit, int32_t* dev_status, void* stream);
+
+/* cp_workspace_size_q4 -- bytes of device scratch cp_chunk_attn_q4 and
+ * cp_mixed_step_q4 need for total_rows rows of num_seqs sequences with contexts
+ * of up to max_ctx keys (0 for arguments those calls would refuse). */
+size_t cp_workspace_size_q4(const cp_layer_desc* desc, int32_t total_rows, int32_t max_ctx, int32_t num_seqs);
+
 /* ---- host-side integer helpers (no GPU work) ---- */
 
 /* cp_chunk_plan -- chunk sizes of an n_tokens prompt at width `chunk`
