@@ -31,12 +31,15 @@ __global__ void __launch_bounds__(kWarps * 32) q4_attn_rows_kernel(const Q4AttnA
   __shared__ float sq[kWarps][D];
   pdl_launch_dependents();
   pdl_wait();
+  if (a.commit_lens && blockIdx.x == 0)  // `past` is a copy: the lengths may advance at once
+    for (int i = threadIdx.x; i < a.rows.num_seqs; i += kWarps * 32) a.commit_lens[i] += seq_rows(a.rows, i);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long id = (long long)blockIdx.x * kWarps + warp;
   const int t = (int)(id / a.hq), h = (int)(id % a.hq);
   if (t >= a.total_rows) return;
   const int s = row_seq(a.rows, t), g = h / a.group;
   const int rows = seq_rows(a.rows, s), past = a.past[s], r = t - seq_row0(a.rows, s);
+  if (rows < a.min_rows) return;
   if (past < 0 || (long long)past + rows > a.max_ctx || r < 0 || r >= rows) {
     if (a.status && lane == 0) atomicOr(a.status, CP_DEV_BOUNDS);
     return;

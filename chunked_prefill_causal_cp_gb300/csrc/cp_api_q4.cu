@@ -1,6 +1,7 @@
 // cp_api_q4.cu -- the C ABI of the query/key preparation and of the 4-bit
 // cache: argument checks and launches.  Every argument is checked before
 // anything is enqueued.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -133,10 +134,41 @@ Q4Args q4_args(const cp_layer_desc* d, const cp_q4_cache* c, const SeqRows& rows
   return a;
 }
 
+// How an attention call over a 4-bit cache runs: the rows per sequence that take
+// the split path, and where its workspace goes -- a copy of the lengths in
+// whole 256-byte blocks (cp_mixed_step_q4), then the split path's parts when a
+// context may need more than one split.
+struct Q4Plan {
+  int dec_rows;            // rows of a sequence on the split path
+  bool split, tensor;      // which paths have sequences
+  int max_splits;
+  int64_t parts;           // (row, head, split) parts, 0 when every context fits one split
+  int64_t lens_bytes;
+  double bytes;            // in floating point: absurd sizes must not wrap
+};
+
+Q4Plan q4_plan(const cp_layer_desc* d, bool ragged, int32_t num_seqs, int32_t total_rows, int32_t max_ctx) {
+  Q4Plan p;
+  const int64_t most = decode_max_rows(d->num_q_heads / d->num_kv_heads);
+  const int64_t uniform = total_rows / num_seqs;
+  p.dec_rows = !ragged && uniform >= 1 && uniform <= most ? (int)uniform : 1;
+  p.split = ragged || uniform == p.dec_rows;
+  p.tensor = ragged ? total_rows > num_seqs : !p.split;
+  p.max_splits = (int)(((int64_t)max_ctx + kQ4Split - 1) / kQ4Split);
+  p.lens_bytes = ((int64_t)num_seqs * 4 + 255) / 256 * 256;
+  const double parts = !p.split || p.max_splits == 1
+                           ? 0.0
+                           : (double)num_seqs * p.dec_rows * d->num_q_heads * p.max_splits;
+  p.bytes = (double)p.lens_bytes + parts * (d->head_dim + 2) * sizeof(float);
+  p.parts = p.bytes < 4e18 ? (int64_t)parts : 0;
+  return p;
+}
+
 // The checks of cp_chunk_attn_q4 and cp_mixed_step_q4, but for the new rows.
 int q4_attn_check(const cp_layer_desc* d, const void* q, const cp_q4_cache* c, const int32_t* seqlens_k,
                   const int32_t* block_table, const int32_t* cu_rows, int32_t num_seqs, int32_t total_rows,
-                  int32_t max_ctx, const void* out, const void* workspace, size_t workspace_bytes, SeqRows* rows) {
+                  int32_t max_ctx, const void* out, const void* workspace, size_t workspace_bytes, SeqRows* rows,
+                  Q4Plan* plan) {
   int r = q4_check(d, c);
   if (r != CP_OK) return r;
   r = rows_of(cu_rows, num_seqs, total_rows, rows);
@@ -147,14 +179,19 @@ int q4_attn_check(const cp_layer_desc* d, const void* q, const cp_q4_cache* c, c
   if (!q || !out || !seqlens_k || !aligned16(q) || !aligned16(out)) return CP_ERR_INVALID_ARG;
   r = cache_check(d, *rows, total_rows, block_table, max_ctx);
   if (r != CP_OK) return r;
+  *plan = q4_plan(d, cu_rows != nullptr, num_seqs, total_rows, max_ctx);
+  if (d->num_q_heads > 65535 || (int64_t)num_seqs * plan->max_splits > INT32_MAX ||
+      (int64_t)num_seqs * plan->dec_rows > INT32_MAX)
+    return CP_ERR_UNSUPPORTED;
   const size_t need = cp_workspace_size_q4(d, total_rows, max_ctx, num_seqs);
-  if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return CP_ERR_WORKSPACE;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < need) return CP_ERR_WORKSPACE;
   return CP_OK;
 }
 
-int q4_attention(const cp_layer_desc* d, const void* q, const cp_q4_cache* c, const int32_t* past,
-                 const int32_t* block_table, const SeqRows& rows, int32_t total_rows, int32_t max_ctx, void* out,
-                 int32_t* dev_status, cudaStream_t st) {
+// The attention itself; `commit` (may be NULL): the lengths to advance, of which `past` is then a copy.
+int q4_attention(const cp_layer_desc* d, const Q4Plan& p, const void* q, const cp_q4_cache* c, const int32_t* past,
+                 int32_t* commit, const int32_t* block_table, const SeqRows& rows, int32_t total_rows, int32_t max_ctx,
+                 void* out, void* workspace, int32_t* dev_status, cudaStream_t st) {
   Q4AttnArgs a;
   std::memset(&a, 0, sizeof(a));
   a.hq = d->num_q_heads;
@@ -173,6 +210,19 @@ int q4_attention(const cp_layer_desc* d, const void* q, const cp_q4_cache* c, co
   a.v_params = static_cast<const uint32_t*>(c->v_params);
   a.out = out;
   a.status = dev_status;
+  a.dec_rows = p.dec_rows;
+  a.min_rows = p.split ? p.dec_rows + 1 : 1;
+  a.max_splits = p.max_splits;
+  a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.lens_bytes);
+  a.part_ml = a.part_o + p.parts * d->head_dim;
+  if (p.split) {
+    a.commit_lens = commit;
+    const int r = launch_result(launch_q4_decode(a, d->dtype, d->head_dim, st));
+    if (r != CP_OK || !p.tensor) return r;
+    a.commit_lens = nullptr;
+  } else {
+    a.commit_lens = commit;
+  }
   return launch_result(launch_q4_attn_rows(a, d->dtype, d->head_dim, st));
 }
 
@@ -287,7 +337,12 @@ int cp_kv_read_q4(const cp_layer_desc* desc, const cp_q4_cache* cache, const int
 
 size_t cp_workspace_size_q4(const cp_layer_desc* desc, int32_t total_rows, int32_t max_ctx, int32_t num_seqs) {
   if (check_desc(desc, false) != CP_OK || total_rows <= 0 || max_ctx <= 0 || num_seqs <= 0) return 0;
-  return 0;
+  const int G = desc->num_q_heads / desc->num_kv_heads;
+  if (G > 16) return 0;
+  // Ragged rows, or equal ones: whichever needs more.
+  double bytes = q4_plan(desc, true, num_seqs, total_rows, max_ctx).bytes;
+  if (total_rows % num_seqs == 0) bytes = std::max(bytes, q4_plan(desc, false, num_seqs, total_rows, max_ctx).bytes);
+  return bytes < 4e18 ? (size_t)bytes : SIZE_MAX;
 }
 
 int cp_chunk_attn_q4(const cp_layer_desc* desc, const void* q, const cp_q4_cache* cache, int32_t* seqlens_k,
@@ -295,13 +350,15 @@ int cp_chunk_attn_q4(const cp_layer_desc* desc, const void* q, const cp_q4_cache
                      int32_t max_ctx, void* out, void* workspace, size_t workspace_bytes, int32_t commit,
                      int32_t* dev_status, void* stream) {
   SeqRows rows;
+  Q4Plan plan;
   int r = q4_attn_check(desc, q, cache, seqlens_k, block_table, cu_rows, num_seqs, total_rows, max_ctx, out, workspace,
-                        workspace_bytes, &rows);
+                        workspace_bytes, &rows, &plan);
   if (r != CP_OK || total_rows == 0) return r;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  r = q4_attention(desc, q, cache, seqlens_k, block_table, rows, total_rows, max_ctx, out, dev_status, st);
+  r = q4_attention(desc, plan, q, cache, seqlens_k, nullptr, block_table, rows, total_rows, max_ctx, out, workspace,
+                   dev_status, st);
   if (r != CP_OK || !commit) return r;
-  return launch_result(launch_commit(seqlens_k, rows, rows.rows_uniform > 0 ? rows.rows_uniform : -1, dev_status, st));
+  return launch_result(launch_commit(seqlens_k, rows, rows.rows_uniform > 0 ? rows.rows_uniform : -1, nullptr, st));
 }
 
 int cp_mixed_step_q4(const cp_layer_desc* desc, const void* q, const void* k_new, const void* v_new,
@@ -309,14 +366,22 @@ int cp_mixed_step_q4(const cp_layer_desc* desc, const void* q, const void* k_new
                      int32_t* seqlens_k, int32_t num_seqs, int32_t total_rows, int32_t max_ctx, void* out,
                      void* workspace, size_t workspace_bytes, int32_t commit, int32_t* dev_status, void* stream) {
   SeqRows rows;
+  Q4Plan plan;
   int r = q4_attn_check(desc, q, cache, seqlens_k, block_table, cu_rows, num_seqs, total_rows, max_ctx, out, workspace,
-                        workspace_bytes, &rows);
+                        workspace_bytes, &rows, &plan);
   if (r != CP_OK || total_rows == 0) return r;
-  r = cp_kv_append_q4(desc, k_new, v_new, cu_rows, num_seqs, total_rows, cache, seqlens_k, block_table, max_ctx,
-                      dev_status, stream);
+  if (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new)) return CP_ERR_INVALID_ARG;
+  // The append keeps a copy of the lengths for the attention to read, so that
+  // the attention's first kernel may advance the lengths themselves.
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Q4Args ap = q4_args(desc, cache, rows, total_rows, seqlens_k, block_table, max_ctx, dev_status);
+  ap.k_new = k_new;
+  ap.v_new = v_new;
+  ap.past_snapshot = static_cast<int*>(workspace);
+  r = launch_result(launch_q4_append(ap, desc->dtype, desc->head_dim, st));
   if (r != CP_OK) return r;
-  return cp_chunk_attn_q4(desc, q, cache, seqlens_k, block_table, cu_rows, num_seqs, total_rows, max_ctx, out,
-                          workspace, workspace_bytes, commit, dev_status, stream);
+  return q4_attention(desc, plan, q, cache, ap.past_snapshot, commit ? seqlens_k : nullptr, block_table, rows,
+                      total_rows, max_ctx, out, workspace, dev_status, st);
 }
 
 }  // extern "C"

@@ -6,6 +6,10 @@
 
 namespace cp {
 
+// Keys per split of the rows that read a 4-bit cache split along its keys.
+// Fixed, so a row's result never depends on what shares the launch.
+constexpr int kQ4Split = 512;
+
 // Norm and rotation of the query and key heads (cp_qk_norm_rope), and, when
 // k_cache is set, the keys and values into their cache slots.
 struct RopeArgs {
@@ -71,11 +75,18 @@ struct Q4AttnArgs {
   const uint32_t* v_params;
   void* out;
   int* status;
+  int min_rows;            // tensor-core kernel: sequences with fewer rows are skipped (the split path has them)
+  int dec_rows;            // split path: takes the sequences of exactly this many rows (dec_rows * group <= 16)
+  int max_splits;
+  float* part_o;           // [num_seqs * dec_rows, hq, max_splits, D] unnormalised parts
+  float* part_ml;          // [num_seqs * dec_rows, hq, max_splits, 2] their maximum (log2 domain) and sum
+  int* commit_lens;        // optional: CTA (0, 0) advances these lengths by each sequence's rows (`past` is a copy)
 };
 
 cudaError_t launch_qk_rope(const RopeArgs& a, int dtype, int d, cudaStream_t st);
 cudaError_t launch_q4_append(const Q4Args& a, int dtype, int d, cudaStream_t st);
 cudaError_t launch_q4_read(const Q4Args& a, int dtype, int d, cudaStream_t st);
 cudaError_t launch_q4_attn_rows(const Q4AttnArgs& a, int dtype, int d, cudaStream_t st);
+cudaError_t launch_q4_decode(const Q4AttnArgs& a, int dtype, int d, cudaStream_t st);
 
 }  // namespace cp
