@@ -18,7 +18,7 @@ LIB = os.path.join(PKG, "libcp.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 SOURCES = ["cp_api.cu", "plan.cpp", "kv_append.cu", "attn_f32.cu", "attn_tc.cu", "decode.cu", "noalloc.cu",
-           "selftest.cu", "qk_rope.cu", "kv_q4.cu", "attn_q4.cu", "decode_q4.cu", "cp_api_q4.cu"]
+           "selftest.cu", "qk_rope.cu", "kv_q4.cu", "attn_q4_tc.cu", "decode_q4.cu", "cp_api_q4.cu"]
 
 
 def _nvcc():

@@ -142,6 +142,7 @@ struct Q4Plan {
   int dec_rows;            // rows of a sequence on the split path
   bool split, tensor;      // which paths have sequences
   int max_splits;
+  int64_t pairs;           // pairs of Q tiles on the tensor-core path, at most
   int64_t parts;           // (row, head, split) parts, 0 when every context fits one split
   int64_t lens_bytes;
   double bytes;            // in floating point: absurd sizes must not wrap
@@ -155,6 +156,8 @@ Q4Plan q4_plan(const cp_layer_desc* d, bool ragged, int32_t num_seqs, int32_t to
   p.split = ragged || uniform == p.dec_rows;
   p.tensor = ragged ? total_rows > num_seqs : !p.split;
   p.max_splits = (int)(((int64_t)max_ctx + kQ4Split - 1) / kQ4Split);
+  const int64_t ppt = 2 * (kTcBlockM / std::max(d->num_q_heads / d->num_kv_heads, 1));  // tokens of a pair
+  p.pairs = !p.tensor ? 0 : ragged ? (total_rows + ppt - 1) / ppt + num_seqs : num_seqs * ((uniform + ppt - 1) / ppt);
   p.lens_bytes = ((int64_t)num_seqs * 4 + 255) / 256 * 256;
   const double parts = !p.split || p.max_splits == 1
                            ? 0.0
@@ -181,7 +184,7 @@ int q4_attn_check(const cp_layer_desc* d, const void* q, const cp_q4_cache* c, c
   if (r != CP_OK) return r;
   *plan = q4_plan(d, cu_rows != nullptr, num_seqs, total_rows, max_ctx);
   if (d->num_q_heads > 65535 || (int64_t)num_seqs * plan->max_splits > INT32_MAX ||
-      (int64_t)num_seqs * plan->dec_rows > INT32_MAX)
+      (int64_t)num_seqs * plan->dec_rows > INT32_MAX || 2 * plan->pairs > INT32_MAX)
     return CP_ERR_UNSUPPORTED;
   const size_t need = cp_workspace_size_q4(d, total_rows, max_ctx, num_seqs);
   if (!workspace || !aligned16(workspace) || workspace_bytes < need) return CP_ERR_WORKSPACE;
@@ -223,7 +226,7 @@ int q4_attention(const cp_layer_desc* d, const Q4Plan& p, const void* q, const c
   } else {
     a.commit_lens = commit;
   }
-  return launch_result(launch_q4_attn_rows(a, d->dtype, d->head_dim, st));
+  return launch_result(launch_q4_tc(a, d->dtype, d->head_dim, (int)p.pairs, st));
 }
 
 }  // namespace

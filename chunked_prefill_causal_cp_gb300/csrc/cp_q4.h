@@ -86,7 +86,9 @@ struct Q4AttnArgs {
 cudaError_t launch_qk_rope(const RopeArgs& a, int dtype, int d, cudaStream_t st);
 cudaError_t launch_q4_append(const Q4Args& a, int dtype, int d, cudaStream_t st);
 cudaError_t launch_q4_read(const Q4Args& a, int dtype, int d, cudaStream_t st);
-cudaError_t launch_q4_attn_rows(const Q4AttnArgs& a, int dtype, int d, cudaStream_t st);
+// Split path: the sequences of exactly a.dec_rows rows, parts and their merge.
 cudaError_t launch_q4_decode(const Q4AttnArgs& a, int dtype, int d, cudaStream_t st);
+// Tensor-core path: the sequences of at least a.min_rows rows; pairs_bound: pairs of 128-row Q tiles to cover.
+cudaError_t launch_q4_tc(const Q4AttnArgs& a, int dtype, int d, int pairs_bound, cudaStream_t st);
 
 }  // namespace cp
