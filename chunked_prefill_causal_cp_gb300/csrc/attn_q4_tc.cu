@@ -7,21 +7,22 @@
 // the 16-bit kernel (attn_tc.cu): 128-row Q tiles of 128 / G tokens x G heads, a
 // cluster of two CTAs owning a pair of Q tiles, each CTA holding both and
 // walking every other 128-key tile, so that a tile is converted once for 256
-// rows.  In place of the TMA producer three warps convert: a thread takes one
-// group of 32 channels of one key (16 bytes of codes, one pair of parameters),
-// turns each word into four pairs of 16-bit values (and-or, subtract, fused
+// rows.  In place of the TMA producer seven warps convert: a thread takes one
+// group of 32 channels of one key (16 bytes of codes, one pair of parameters,
+// copied ahead to shared memory by cp.async), turns each word into four pairs of 16-bit values (and-or, subtract, fused
 // multiply-add) and stores them, 16 bytes at a time, where the 128-byte-swizzled
-// operand wants them.  The next tile's codes are in registers before the current
-// one is converted.  The values are rounded to 16 bits once, as the cache's
+// operand wants them.  The next tile's codes are on their way before the current
+// one's are all converted (held in registers instead, they spilled and the loads
+// ran one after another: 4 times as long).  The values are rounded to 16 bits once, as the cache's
 // format defines them; the tensor cores take both operands in the layer's type.
 // Keys past the sequence's positions, and keys on a bad page, are written as
 // zeros, so nothing unwritten reaches a product; their scores are masked.
 //
-// Warp roles (384 threads per CTA, three warpgroups):
-//   warps 0, 2, 3  conversion (warp 0 also issues the Q tiles' TMA loads)
+// Warp roles (512 threads per CTA, four warpgroups):
+//   warps 0, 2-7   conversion (warp 0 also issues the Q tiles' TMA loads)
 //   warp 1         TMEM allocation and MMA issue:  S0 = Q0 K^T, S1 = Q1 K^T,
 //                  O0 += P0 V, O1 += P1 V per tile
-//   warps 4-7, 8-11  softmax of Q tile 0 and 1, a thread per row
+//   warps 8-11, 12-15  softmax of Q tile 0 and 1, a thread per row
 // TMEM: group w has [256w, 256w + 128) for S and P, [256w + 128, + D) for O.
 // The MMA warp issues S_w(i + 1) after O_w += P_w(i) V(i), and tcgen05 operations of
 // one thread complete in order, so S_w(i + 1) complete means P_w(i) may be
@@ -48,15 +49,16 @@
 namespace cp {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kConvThreads = 96;
-// Register split: compiled at kRegsLaunch a thread (the most 384 threads may
-// have); the control warpgroup drops to kRegsControl and hands the rest to the
-// softmax warpgroups.
-constexpr int kRegsLaunch = 168;
-constexpr int kRegsControl = 104;
-constexpr int kRegsSoftmax = 200;
-static_assert(128 * kRegsControl + 256 * kRegsSoftmax == kThreads * kRegsLaunch, "the split must add up");
+constexpr int kThreads = 512;
+constexpr int kConvWarps = 7;
+constexpr int kConvThreads = kConvWarps * 32;
+// Register split: compiled at kRegsLaunch a thread (the most 512 threads may
+// have); the two control warpgroups drop to kRegsControl and hand the rest to
+// the softmax warpgroups.
+constexpr int kRegsLaunch = 128;
+constexpr int kRegsControl = 72;
+constexpr int kRegsSoftmax = 184;
+static_assert(256 * kRegsControl + 256 * kRegsSoftmax == kThreads * kRegsLaunch, "the split must add up");
 constexpr int kStages = 2;
 constexpr uint32_t kBlockBytes = 128 * 128;  // [128 rows][64 x 16-bit] = 16 KB
 constexpr uint32_t kTmemCols = 512;
@@ -64,7 +66,7 @@ constexpr float kRescaleLog2 = 8.0f;
 
 struct __align__(16) Q4Barriers {
   uint64_t q_full[2];
-  uint64_t k_full[kStages], v_full[kStages], kv_empty[kStages];
+  uint64_t k_full[kStages], v_full[kStages], k_empty[kStages], v_empty[kStages];
   uint64_t s_full[2], p_ready[2];
   uint64_t o_final;
   uint64_t merge_full[4];  // column chunk c of the peer's part for this CTA's rows has landed
@@ -82,7 +84,10 @@ struct Q4Smem {
   static constexpr uint32_t k_off = q_off + 2 * DB * kBlockBytes;
   static constexpr uint32_t v_off = k_off + kStages * DB * kBlockBytes;
   static constexpr uint32_t bar_off = v_off + kStages * DB * kBlockBytes;
-  static constexpr uint32_t alloc = bar_off + sizeof(Q4Barriers) + 1024;  // slack for 1024-byte alignment
+  static constexpr uint32_t raw_off = bar_off + sizeof(Q4Barriers);  // codes and parameters on their way (see Conv)
+  static constexpr uint32_t raw_bytes = 2u * ((128 * D / 32 + kConvThreads - 1) / kConvThreads) * kConvThreads * 20u;
+  static constexpr uint32_t alloc = raw_off + raw_bytes + 1024;  // slack for 1024-byte alignment
+  static_assert(alloc <= 232448, "one CTA's shared memory");
   // After the main loop the K stages hold the outgoing part, the V stages the
   // peer's: 128 rows x D fp32 as D / 32 column chunks.
   static constexpr int kMergeChunks = D / 32;
@@ -152,52 +157,85 @@ __device__ __forceinline__ bool find_pair(const Q4AttnArgs& a, int ppt, int w, i
   return false;
 }
 
+// 16- or 4-byte asynchronous copies to shared memory; `on` false: zeros, nothing is read.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4(void* dst, const void* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // A thread's share of a tile of K or V: groups of 32 channels, thread ct taking
-// groups ct, ct + 96, ... of the tile's 128 keys x D / 32.
+// groups ct, ct + kConvThreads, ... of the tile's 128 keys x D / 32.  The codes pass through
+// slots of shared memory that only this thread writes and reads, so a copy needs
+// no barrier, and no registers while it is in flight.
 template <typename T, int D>
 struct Conv {
   static constexpr int kGroups = D / 32;
   static constexpr int kItems = 128 * kGroups;
   static constexpr int kPer = (kItems + kConvThreads - 1) / kConvThreads;
-  uint4 w[kPer];
-  uint32_t p[kPer];
+  struct Slots {
+    uint4 w[kPer][kConvThreads];
+    uint32_t p[kPer][kConvThreads];
+  };
 
-  // Codes and parameters of keys j0 + (item / kGroups) < n; others are zeros.
-  __device__ __forceinline__ void load(const Q4AttnArgs& a, const uint8_t* codes, const uint32_t* params, int s, int g,
-                                       int j0, int n, int ct) {
+  // Cache row of the tile's first key (contiguous), or of each of its pages in
+  // lane's turn (-1: a bad page, or none).
+  static __device__ __forceinline__ long long tile_rows(const Q4AttnArgs& a, int s, int g, int j0, int n) {
+    if (a.cache.kind != CP_CACHE_PAGED) return ((long long)s * a.hkv + g) * a.cache.capacity + j0;
+    const int lane = threadIdx.x & 31, key = j0 + lane * a.cache.page_size;
+    if (lane * a.cache.page_size >= kTcBlockN || key >= n) return -1;
+    const long long row = cache_row(a.cache, a.hkv, s, g, key, a.max_ctx);
+    if (row < 0 && a.status) atomicOr(a.status, CP_DEV_BOUNDS);
+    return row;
+  }
+
+  // Starts the copies of keys j0 + (item / kGroups) < n; others become zeros.
+  static __device__ __forceinline__ void load(const Q4AttnArgs& a, const uint8_t* codes, const uint32_t* params,
+                                              long long rows, int j0, int n, int ct, Slots& x) {
+    const bool paged = a.cache.kind == CP_CACHE_PAGED;
+    const int lps = 31 - __clz(a.cache.page_size | 1);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int item = ct + i * kConvThreads;
-      const int key = j0 + item / kGroups, grp = item % kGroups;
-      w[i] = make_uint4(0, 0, 0, 0);
-      p[i] = 0;
-      if ((kItems % kConvThreads == 0 || item < kItems) && key < n) {
-        const long long row = cache_row(a.cache, a.hkv, s, g, key, a.max_ctx);
-        if (row >= 0) {
-          w[i] = __ldg(reinterpret_cast<const uint4*>(codes + row * (D / 2)) + grp);
-          p[i] = __ldg(params + row * kGroups + grp);
-        } else if (a.status) {
-          atomicOr(a.status, CP_DEV_BOUNDS);
-        }
+      if (kItems % kConvThreads != 0 && item >= kItems) break;  // whole warps
+      const int key = item / kGroups, grp = item % kGroups;
+      long long row = rows + key;
+      bool on = j0 + key < n;
+      if (paged) {
+        const long long page_row = __shfl_sync(0xffffffffu, rows, key >> lps);
+        row = page_row + (key & (a.cache.page_size - 1));
+        on = on && page_row >= 0;
       }
+      if (!on) row = 0;
+      cp_async16(&x.w[i][ct], codes + row * (D / 2) + grp * 16, on);
+      cp_async4(&x.p[i][ct], params + row * kGroups + grp, on);
     }
+    cp_async_commit();
   }
 
   // The values into a stage: key row of 128 bytes in 64-channel block grp / 2,
   // 16-byte chunks XOR-swizzled by key mod 8.  Groups of the second block store
   // their chunks in another order, so the eight threads of a store phase (two keys,
   // four groups) fall on distinct banks.
-  __device__ __forceinline__ void store(uint8_t* stage, int ct) const {
+  static __device__ __forceinline__ void store(const Slots& from, uint8_t* stage, int ct) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int item = ct + i * kConvThreads;
       if (kItems % kConvThreads != 0 && item >= kItems) break;
       const int key = item / kGroups, grp = item % kGroups;
-      const uint32_t s2 = q4_scale2(p[i]), m2 = q4_low2(p[i]);
+      const uint4 w = from.w[i][ct];
+      const uint32_t s2 = q4_scale2(from.p[i][ct]), m2 = q4_low2(from.p[i][ct]);
       const bool second = grp >> 1;
       uint8_t* row = stage + (grp >> 1) * kBlockBytes + key * 128;
-      const uint32_t x[4] = {second ? w[i].z : w[i].x, second ? w[i].w : w[i].y, second ? w[i].x : w[i].z,
-                             second ? w[i].y : w[i].w};
+      const uint32_t x[4] = {second ? w.z : w.x, second ? w.w : w.y, second ? w.x : w.z, second ? w.y : w.w};
       const int c0 = (grp & 1) * 4;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -239,7 +277,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bar->k_full[i], kConvThreads);
       mbar_init(&bar->v_full[i], kConvThreads);
-      mbar_init(&bar->kv_empty[i], 1);
+      mbar_init(&bar->k_empty[i], 1);
+      mbar_init(&bar->v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar->q_full[i], 1);
@@ -302,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int c = 0; c < L::kMergeChunks; ++c)  // chunk 0 also brings the peer's (max, sum)
       mbar_arrive_expect_tx(&bar->merge_full[c], L::kChunkBytes + (c == 0 ? 256u * 4u : 0u));
 
-  if (warp < 4) {
+  if (warp < 8) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
   if (warp != 1) {
     // ================================================================ conversion
@@ -312,22 +351,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int db = 0; db < DB; ++db)
           tma_load_3d(sQ + (w * DB + db) * kBlockBytes, &tm_q, &bar->q_full[w], db * 64, g * G, row0 + t0 + w * rpt);
       }
-    const int ct = (warp == 0 ? 0 : warp - 1) * 32 + lane;
-    Conv<T, D> ck, cv;
-    if (nmine > 0) ck.load(a, a.k_codes, a.k_params, s, g, rank * kTcBlockN, n, ct);
+    // The tile's groups do not divide evenly: the warps that take one more of K are not those of V.
+    const int cw = warp == 0 ? 0 : warp - 1;
+    const int ck = cw * 32 + lane, cv = (cw + 5) % kConvWarps * 32 + lane;
+    using C = Conv<T, D>;
+    auto* raw = reinterpret_cast<typename C::Slots*>(smem + L::raw_off);  // K's and V's
+    long long rows_at = 0;  // of the tile whose copies start next
+    if (nmine > 0) {
+      const int j0 = rank * kTcBlockN;
+      rows_at = C::tile_rows(a, s, g, j0, n);
+      C::load(a, a.k_codes, a.k_params, rows_at, j0, n, ck, raw[0]);
+      C::load(a, a.v_codes, a.v_params, rows_at, j0, n, cv, raw[1]);
+    }
     for (int i = 0; i < nmine; ++i) {
       const int st = i & 1;
-      const int j0 = (rank + 2 * i) * kTcBlockN;
-      cv.load(a, a.v_codes, a.v_params, s, g, j0, n, ct);
-      if (!warp_wait(&bar->kv_empty[st], ((i >> 1) & 1) ^ 1, abort_flag, a.status)) break;
-      ck.store(sK + st * DB * kBlockBytes, ct);
+      const int j1 = (rank + 2 * i + 2) * kTcBlockN;  // this CTA's next tile
+      const bool more = i + 1 < nmine;
+      if (more) rows_at = C::tile_rows(a, s, g, j1, n);
+      const uint32_t free_ph = ((i >> 1) & 1) ^ 1;
+      if (!warp_wait(&bar->k_empty[st], free_ph, abort_flag, a.status)) break;
+      cp_async_wait<1>();  // K of this tile
+      C::store(raw[0], sK + st * DB * kBlockBytes, ck);
       fence_proxy_async_smem();  // the tensor cores read the stage through the async proxy
       mbar_arrive(&bar->k_full[st]);
-      if (i + 1 < nmine) ck.load(a, a.k_codes, a.k_params, s, g, j0 + 2 * kTcBlockN, n, ct);
-      cv.store(sV + st * DB * kBlockBytes, ct);
+      if (more) C::load(a, a.k_codes, a.k_params, rows_at, j1, n, ck, raw[0]);
+      else cp_async_commit();  // the groups stay in step
+      if (!warp_wait(&bar->v_empty[st], free_ph, abort_flag, a.status)) break;
+      cp_async_wait<1>();  // V of this tile
+      C::store(raw[1], sV + st * DB * kBlockBytes, cv);
       fence_proxy_async_smem();
       mbar_arrive(&bar->v_full[st]);
+      if (more) C::load(a, a.v_codes, a.v_params, rows_at, j1, n, cv, raw[1]);
+      else cp_async_commit();
     }
+    cp_async_wait<0>();
     if (threadIdx.x == 0 && nmine > 0 && *abort_flag) {
       // Let the Q copies in flight land before the CTA's shared memory is released.
       volatile int zero = 0;
@@ -372,6 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         issue_qk(1, 0);
       }
     }
+    if (ok) mma_commit_elect(&bar->k_empty[0]);  // K's stage is free long before V's
     for (int i = 0; ok && i < nmine; ++i) {
       const bool more = i + 1 < nmine;
       if (!wait(&bar->p_ready[0], i & 1)) break;
@@ -388,8 +446,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         issue_pv(1, i);
       }
-      mma_commit_elect(&bar->kv_empty[i & 1]);
-      if (more && q1) issue_qk(1, i + 1);
+      mma_commit_elect(&bar->v_empty[i & 1]);
+      if (more) {
+        if (q1) issue_qk(1, i + 1);
+        mma_commit_elect(&bar->k_empty[(i + 1) & 1]);
+      }
     }
     // o_final: every MMA issued has completed (the epilogue and the TMEM release wait for it).
     mma_commit_elect(&bar->o_final);
@@ -405,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
   // ================================================================ softmax groups
-  const int grp = (warp - 4) >> 2;          // Q tile of this group
+  const int grp = (warp - 8) >> 2;          // Q tile of this group
   const int quarter = warp & 3;             // TMEM lanes [32*quarter, +32)
   const int mrow = quarter * 32 + lane;     // this thread's row of its Q tile
   const int tok = t0 + grp * rpt + mrow / G;
