@@ -225,7 +225,7 @@ struct Conv {
   // 16-byte chunks XOR-swizzled by key mod 8.  Groups of the second block store
   // their chunks in another order, so the eight threads of a store phase (two keys,
   // four groups) fall on distinct banks.
-  static __device__ __forceinline__ void store(const Slots& from, uint8_t* stage, int ct) {
+  static __device__ __forceinline__ void store(const Slots& from, uint8_t* stage, int ct, uint32_t magic) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int item = ct + i * kConvThreads;
@@ -240,8 +240,8 @@ struct Conv {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int chunk = c0 + (k ^ (second ? 2 : 0));
-        const uint4 v = make_uint4(q4_pair<T>(x[k], s2, m2), q4_pair<T>(x[k] >> 4, s2, m2),
-                                   q4_pair<T>(x[k] >> 8, s2, m2), q4_pair<T>(x[k] >> 12, s2, m2));
+        const uint4 v = make_uint4(q4_pair<T>(x[k], s2, m2, magic), q4_pair<T>(x[k] >> 4, s2, m2, magic),
+                                   q4_pair<T>(x[k] >> 8, s2, m2, magic), q4_pair<T>(x[k] >> 12, s2, m2, magic));
         *reinterpret_cast<uint4*>(row + ((chunk ^ (key & 7)) * 16)) = v;
       }
     }
@@ -355,6 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cw = warp == 0 ? 0 : warp - 1;
     const int ck = cw * 32 + lane, cv = (cw + 5) % kConvWarps * 32 + lane;
     using C = Conv<T, D>;
+    const uint32_t magic = q4_magic<T>();
     auto* raw = reinterpret_cast<typename C::Slots*>(smem + L::raw_off);  // K's and V's
     long long rows_at = 0;  // of the tile whose copies start next
     if (nmine > 0) {
@@ -371,14 +372,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t free_ph = ((i >> 1) & 1) ^ 1;
       if (!warp_wait(&bar->k_empty[st], free_ph, abort_flag, a.status)) break;
       cp_async_wait<1>();  // K of this tile
-      C::store(raw[0], sK + st * DB * kBlockBytes, ck);
+      C::store(raw[0], sK + st * DB * kBlockBytes, ck, magic);
       fence_proxy_async_smem();  // the tensor cores read the stage through the async proxy
       mbar_arrive(&bar->k_full[st]);
       if (more) C::load(a, a.k_codes, a.k_params, rows_at, j1, n, ck, raw[0]);
       else cp_async_commit();  // the groups stay in step
       if (!warp_wait(&bar->v_empty[st], free_ph, abort_flag, a.status)) break;
       cp_async_wait<1>();  // V of this tile
-      C::store(raw[1], sV + st * DB * kBlockBytes, cv);
+      C::store(raw[1], sV + st * DB * kBlockBytes, cv, magic);
       fence_proxy_async_smem();
       mbar_arrive(&bar->v_full[st]);
       if (more) C::load(a, a.v_codes, a.v_params, rows_at, j1, n, cv, raw[1]);

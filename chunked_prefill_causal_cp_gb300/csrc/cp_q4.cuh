@@ -22,14 +22,22 @@ struct Two<__half> {
   static constexpr uint32_t kMagic = 0x64006400u;  // 1024
 };
 
+// The offset in a register that the compiler does not know to be constant: with
+// two constants the and-or below came out as two instructions.
+template <typename T>
+__device__ __forceinline__ uint32_t q4_magic() {
+  return Two<T>::kMagic + (blockDim.x >> 16);
+}
+
 // Codes in bits [0, 4) and [16, 20) of `w` (other bits may be set) -> m + c * s
 // for both, rounded once: the code goes under an exponent whose last place is
 // one, the offset is subtracted exactly, and one fused multiply-add follows.
 template <typename T>
-__device__ __forceinline__ uint32_t q4_pair(uint32_t w, uint32_t s2, uint32_t m2) {
+__device__ __forceinline__ uint32_t q4_pair(uint32_t w, uint32_t s2, uint32_t m2, uint32_t magic) {
   typedef typename Two<T>::type V;
-  uint32_t x = (w & 0x000f000fu) | Two<T>::kMagic, off = Two<T>::kMagic;
-  const V c = __hsub2(*reinterpret_cast<V*>(&x), *reinterpret_cast<V*>(&off));
+  uint32_t x;
+  asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;" : "=r"(x) : "r"(w), "r"(magic));  // (w & mask) | magic
+  const V c = __hsub2(*reinterpret_cast<V*>(&x), *reinterpret_cast<V*>(&magic));
   const V r = __hfma2(c, *reinterpret_cast<V*>(&s2), *reinterpret_cast<V*>(&m2));
   return *reinterpret_cast<const uint32_t*>(&r);
 }

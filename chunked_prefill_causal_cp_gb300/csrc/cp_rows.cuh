@@ -27,15 +27,17 @@ __device__ __forceinline__ int row_seq(const SeqRows& r, int row) {
 // or -1 when the host bound or the layout does not allow the position.
 __device__ __forceinline__ long long cache_row(const CacheView& c, int hkv, int s, int g, long long pos, int max_ctx) {
   if (pos < 0 || pos >= max_ctx) return -1;
+  const int p = (int)pos;  // below max_ctx
   if (c.kind == CP_CACHE_PAGED) {
-    const long long blk = pos / c.page_size;
+    const int lps = 31 - __clz(c.page_size);  // a power of two
+    const int blk = p >> lps;
     if (blk >= c.max_blocks) return -1;
     const int page = c.block_table[(long long)s * c.max_blocks + blk];
     if (page < 0 || page >= c.num_pages) return -1;
-    return ((long long)page * hkv + g) * c.page_size + pos % c.page_size;
+    return (((long long)page * hkv + g) << lps) + (p & (c.page_size - 1));
   }
-  if (c.kind == CP_CACHE_CONTIG && pos >= c.capacity) return -1;
-  return ((long long)s * hkv + g) * c.capacity + (c.kind == CP_CACHE_ROLLING ? pos % c.capacity : pos);
+  if (c.kind == CP_CACHE_CONTIG && p >= c.capacity) return -1;
+  return ((long long)s * hkv + g) * c.capacity + (c.kind == CP_CACHE_ROLLING ? p % c.capacity : p);
 }
 
 // A 32-bit word of two 16-bit elements, or one fp32, as floats and back.

@@ -4,22 +4,31 @@
 // A decode row reads its sequence's cache once and does about 13 operations of
 // attention per byte, so the path is bound by the bytes of the cache (160 per
 // key and KV head at 128 channels) as long as the codes turn into matrix
-// operands quickly enough.  One CTA takes 512 keys of a (sequence, KV head), four
-// warps 128 each; the k rows of the sequence times the G heads of the group
-// (k * G <= 16) ride in the columns of m16n8k16 products, so every row shares one
-// read of the cache and one conversion of its codes.
+// operands quickly enough: at full bandwidth an SM has some 28 instructions per
+// key, and turning 256 codes into 16-bit values takes 15 of them.  One CTA takes
+// 512 keys of a (sequence, KV head), four warps 128 each; the k rows of the
+// sequence times the G heads of the group (k * G <= 16) ride in the columns of
+// m16n8k16 products, so every row shares one read of the cache and one
+// conversion of its codes.  A warp walks its keys 16 at a time, in a rolled loop
+// (unrolled over the whole range, the code outgrew the instruction cache and
+// took 585 instructions a tile):
+//   Copies: the tile's codes and parameters come through a four-stage ring of
+//   shared memory of the warp's own, by cp.async, three tiles ahead.
 //   Scores: S^T[16 keys x 8 columns] = K Q^T.  Lane (g, q) = (lane / 4, lane % 4)
-//   holds keys g and g + 8 of a tile and the words of D / 4 channels from q * D / 4
-//   on: one load, one group's parameters, and every pair of codes of a word
-//   (adjacent channels, as stored) is one operand register.  The query is loaded
-//   in the same order; the sum over channels does not depend on it.
-//   Softmax: each warp's own maximum per column over its 128 keys, weights in 16
-//   bits for the product with V (the tensor cores take both operands in the
-//   layer's type), their sum in fp32.
-//   Output: O^T[16 channels x 8 columns] += V^T P^T.  Lane (g, q) holds keys 2q,
+//   holds keys g and g + 8 and the words of D / 4 channels from q * D / 4 on: one
+//   load, one group's parameters, and every pair of codes of a word (adjacent
+//   channels, as stored) is one operand register.  The query is loaded in the
+//   same order; the sum over channels does not depend on it.
+//   Softmax: a running maximum per column, raised only when a score passes it by
+//   more than 2^8 (a vote per tile; the sums are in fp32 and a weight is at most
+//   2^8), weights in 16 bits for the product with V (the tensor cores take both
+//   operands in the layer's type).
+//   Output: O^T[16 channels x 8 columns] += V^T P^T.  The weights reach their
+//   operand layout by an 8 x 8 transpose between lanes.  Lane (g, q) holds keys 2q,
 //   2q + 1, 2q + 8, 2q + 9 and the words of D / 8 channels from g * D / 8 on; a byte
 //   permute of two keys' words puts the same channel of both keys side by side,
-//   4 bits at a time, ready for the same conversion.
+//   4 bits at a time, ready for the same conversion.  V's rows are placed in the
+//   ring so that these loads fall on distinct banks.
 //   The four warps' parts are merged in warp order; a sequence that fits one
 //   split is finished there, others write their part for the combine kernel,
 //   which merges the splits in order.  A row's result depends on its own
@@ -37,29 +46,38 @@ namespace cp {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kWarpKeys = kQ4Split / kWarps;  // 128
+constexpr int kWarpKeys = kQ4Split / kWarps;
 constexpr int kTiles = kWarpKeys / 16;
-constexpr int kPStride = kWarpKeys + 8;       // 16-bit P row stride: conflict-free fragment reads
-constexpr int kAhead = 4;                     // K tiles in flight per warp
+constexpr int kRing = 4;                      // stages of a warp's ring, one 16-key tile each
+static_assert(kTiles <= 32, "a lane knows one tile's place");
 
-__device__ __forceinline__ uint32_t ldg32(const void* p) {
+// N bytes of an asynchronous copy to shared memory; `on` false: zeros, nothing is read.
+template <int N>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool on) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(on ? 8 : 0) : "memory");
+}
+
+// The 8 x 8 matrix of 16-bit elements that a warp holds (lane: row lane / 4, columns 2 (lane % 4) and the next), transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
-  asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(r) : "l"(p));
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
 
-// N consecutive words that are read once.
-template <int N>
-__device__ __forceinline__ void ldg_words(const void* p, uint32_t (&w)[N]) {
-  if constexpr (N == 4)
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "l"(p));
-  else if constexpr (N == 2)
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
-  else
-    w[0] = ldg32(p);
-}
+// A stage of a warp's ring.
+template <int D>
+struct Stage {
+  static constexpr int kRow = D / 2, kPar = D / 8;  // bytes of a key's codes and parameters
+  static constexpr int k = 0, v = 16 * kRow, kp = 32 * kRow, vp = kp + 16 * kPar, bytes = vp + 16 * kPar;
+  // V's place of 16-byte chunk c of a key: four keys two apart are read at once, and must not share banks.
+  static __device__ __forceinline__ int v_at(int key, int c) {
+    if (D == 128) return ((key & 12) | ((key & 1) << 1) | ((key >> 1) & 1)) * kRow + (c ^ ((key >> 1) & 2)) * 16;
+    return ((key & 8) | ((key & 1) << 2) | ((key >> 1) & 3)) * kRow + c * 16;
+  }
+};
 
 // D (16x8, fp32) += A (16x16, row) * B (16x8, col), 16-bit inputs.
 template <typename T>
@@ -80,22 +98,15 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
   }
 }
 
-// 16-bit bits of x in the low half.
-template <typename T>
-__device__ __forceinline__ uint16_t bits16(float x) {
-  const float two[2] = {x, 0.f};
-  return (uint16_t)Pack<T>::store(two);
-}
-
 template <typename T, int D, int NF>
-__global__ void __launch_bounds__(kWarps * 32, NF == 1 ? 4 : 3) q4_split_kernel(const Q4AttnArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, NF == 1 ? 5 : D == 64 ? 4 : 3) q4_split_kernel(const Q4AttnArgs a) {
   constexpr int NC = 8 * NF;     // (row, head) columns
   constexpr int KW = D / 32;     // score phase: words of a lane's channels
   constexpr int VW = D / 64;     // output phase
-  constexpr int kRowBytes = D / 2, kRowGroups = D / 32;
-  // A warp's output part takes the place of its own weights once it has read them.
-  constexpr int kWarpWords = NC * (D > kPStride / 2 ? D : kPStride / 2);
-  __shared__ __align__(16) float sWarp[kWarps][kWarpWords];
+  using S = Stage<D>;
+  // A warp's ring, whose place its output part takes at the end.
+  constexpr int kWarpBytes = kRing * S::bytes > NC * D * 4 ? kRing * S::bytes : NC * D * 4;
+  __shared__ __align__(128) uint8_t sWarp[kWarps][kWarpBytes];
   __shared__ float sM[kWarps][NC], sL[kWarps][NC];
 
   pdl_launch_dependents();
@@ -120,21 +131,54 @@ __global__ void __launch_bounds__(kWarps * 32, NF == 1 ? 4 : 3) q4_split_kernel(
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g8 = lane >> 2, q4 = lane & 3;
-  const int G = a.group, ncols = kr * G;
-  const int kw = warp * kWarpKeys;                                        // the warp's first key in the split
-  const int nkw = max(0, min(min(n - k0, kQ4Split) - kw, kWarpKeys));     // its keys
+  const int G = a.group, ncols = kr * G, lg = 31 - __clz(G);  // G is a power of two
+  const int kw = k0 + warp * kWarpKeys;              // the warp's first key
+  const int nkw = max(0, min(n - kw, kWarpKeys));    // its keys
   const int ntile = (nkw + 15) / 16;
-  const bool paged = a.cache.kind == CP_CACHE_PAGED;
-  const int ps = a.cache.page_size;
 
   // First cache row of each of the warp's tiles (a page holds whole tiles): lane t has tile t's, -1 for a bad page.
   long long my_row = -1;
   if (lane < ntile) {
-    const int key = k0 + kw + 16 * lane;
-    my_row = cache_row(a.cache, a.hkv, s, gk, key, a.max_ctx);
+    my_row = cache_row(a.cache, a.hkv, s, gk, kw + 16 * lane, a.max_ctx);
     if (my_row < 0 && a.status) atomicOr(a.status, CP_DEV_BOUNDS);
   }
-  auto tile_row = [&](int t) -> long long { return __shfl_sync(0xffffffffu, my_row, t); };
+
+  const uint32_t bad_tiles = __ballot_sync(0xffffffffu, lane < ntile && my_row < 0);
+  const uint32_t magic = q4_magic<T>();
+
+  // ---- copies: lane's pieces of a tile
+  const uint32_t ring = smem_u32(sWarp[warp]);
+  constexpr int kChunks = D / 32;                    // 16-byte pieces of a key's codes
+  constexpr int kIter = 16 * kChunks / 32;           // pieces of K (and of V) per lane
+  const bool v_par = lane >= 16;                     // lanes 0-15 copy K's parameters, 16-31 V's
+  const uint8_t* par = reinterpret_cast<const uint8_t*>(v_par ? a.v_params : a.k_params) + (lane & 15) * S::kPar;
+  const uint8_t* kc = a.k_codes + lane * 16;
+  const uint8_t* vc = a.v_codes + lane * 16;
+  auto copy = [&](int t) {
+    if (t < ntile) {
+      const long long row = __shfl_sync(0xffffffffu, my_row, t);
+      const int left = row < 0 ? 0 : nkw - 16 * t;   // keys of the tile
+      const long long at = row < 0 ? 0 : row;
+      const uint32_t st = ring + (t % kRing) * S::bytes;
+      const uint8_t *k = kc + at * S::kRow, *v = vc + at * S::kRow;
+      const uint32_t pd = st + (v_par ? S::vp : S::kp) + (lane & 15) * S::kPar;
+      auto pieces = [&](auto some) {  // the tile's first `left` keys, or all 16
+#pragma unroll
+        for (int i = 0; i < kIter; ++i) {
+          const int e = lane + 32 * i, key = e / kChunks, c = e % kChunks;
+          const bool on = !some || key < left;
+          cp_async<16>(st + S::k + e * 16, k + i * 512, on);
+          cp_async<16>(st + S::v + S::v_at(key, c), v + i * 512, on);
+        }
+        cp_async<S::kPar>(pd, par + at * S::kPar, !some || (lane & 15) < left);
+      };
+      if (left >= 16) pieces(std::false_type());
+      else pieces(std::true_type());
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int t = 0; t < kRing - 1; ++t) copy(t);
 
   // Query fragments: column 8f + g8 = (row, head), zero past the call's columns.
   uint4 qf[NF][KW];
@@ -143,189 +187,162 @@ __global__ void __launch_bounds__(kWarps * 32, NF == 1 ? 4 : 3) q4_split_kernel(
     const int c = 8 * f + g8;
     const bool on = c < ncols;
     const uint4* q = reinterpret_cast<const uint4*>(
-        static_cast<const T*>(a.q) + ((long long)(row0 + (on ? c / G : 0)) * a.hq + gk * G + (on ? c % G : 0)) * D);
+        static_cast<const T*>(a.q) + ((long long)(row0 + (on ? c >> lg : 0)) * a.hq + gk * G + (on ? c & (G - 1) : 0)) * D);
 #pragma unroll
     for (int w = 0; w < KW; ++w) qf[f][w] = on ? q[q4 * KW + w] : make_uint4(0, 0, 0, 0);
   }
-
-  // ---- scores: keys g8 and g8 + 8 of each tile, columns 8f + 2q4 and 8f + 2q4 + 1
-  struct KTile {
-    uint32_t w[2][KW], p[2];
-  };
-  auto load_k = [&](int t, KTile& x) {
-    const long long row = tile_row(t);
+  float m[NF][2], l[NF][2], o[NF][VW * 4][4];
+  int lim[NF][2];  // last key of the warp that column 8f + 2q4 + e sees
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      if (row >= 0 && 16 * t + g8 + 8 * r < nkw) {
-        const long long at = row + g8 + 8 * r;
-        ldg_words<KW>(a.k_codes + at * kRowBytes + q4 * (4 * KW), x.w[r]);
-        x.p[r] = ldg32(a.k_params + at * kRowGroups + q4 * KW / 4);
-      } else {
-#pragma unroll
-        for (int w = 0; w < KW; ++w) x.w[r][w] = 0;
-        x.p[r] = 0;
-      }
-    }
-  };
-  float sc[kTiles][NF][4];
-  float mx[NF][2];
-  int lim[NF][2];  // last key of the split that column 8f + 2q4 + e sees; -1: none
-#pragma unroll
-  for (int f = 0; f < NF; ++f)
+  for (int f = 0; f < NF; ++f) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      mx[f][e] = -INFINITY;
-      const int c = 8 * f + 2 * q4 + e;
-      lim[f][e] = c < ncols ? past + c / G - k0 - kw : -1;
+      m[f][e] = -INFINITY;
+      l[f][e] = 0.f;
+      lim[f][e] = past + min((8 * f + 2 * q4 + e) >> lg, kr - 1) - kw;
     }
-  KTile kb[kAhead];
 #pragma unroll
-  for (int t = 0; t < kAhead - 1; ++t) load_k(t, kb[t]);
-#pragma unroll
-  for (int t = 0; t < kTiles; ++t) {
-    if (t + kAhead - 1 < kTiles) load_k(t + kAhead - 1, kb[(t + kAhead - 1) % kAhead]);
-    const KTile& x = kb[t % kAhead];
-    const bool have = tile_row(t) >= 0;
+    for (int b = 0; b < VW * 4; ++b) o[f][b][0] = o[f][b][1] = o[f][b][2] = o[f][b][3] = 0.f;
+  }
+
+#pragma unroll 1
+  for (int t = 0; t < ntile; ++t) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+    __syncwarp();  // every lane's copies of this tile have landed, and its reads of the stage that the next copy takes are done
+    copy(t + kRing - 1);
+    const uint8_t* st = sWarp[warp] + (t % kRing) * S::bytes;
+
+    // ---- scores: keys g8 and g8 + 8, columns 8f + 2q4 and 8f + 2q4 + 1
     float c[NF][4];
 #pragma unroll
     for (int f = 0; f < NF; ++f) c[f][0] = c[f][1] = c[f][2] = c[f][3] = 0.f;
-    if (t < ntile) {  // the same for the whole warp
-      const uint32_t s0 = q4_scale2(x.p[0]), m0 = q4_low2(x.p[0]), s1 = q4_scale2(x.p[1]), m1 = q4_low2(x.p[1]);
+    {
+      uint32_t w[2][KW];
+      uint32_t p[2];
 #pragma unroll
-      for (int w = 0; w < KW; ++w)
+      for (int r = 0; r < 2; ++r) {
+        const uint8_t* x = st + S::k + (g8 + 8 * r) * S::kRow + q4 * (4 * KW);
+        if constexpr (KW == 4) *reinterpret_cast<uint4*>(w[r]) = *reinterpret_cast<const uint4*>(x);
+        else *reinterpret_cast<uint2*>(w[r]) = *reinterpret_cast<const uint2*>(x);
+        p[r] = *reinterpret_cast<const uint32_t*>(st + S::kp + (g8 + 8 * r) * S::kPar + q4 * KW / 4 * 4);
+      }
+      const uint32_t s0 = q4_scale2(p[0]), m0 = q4_low2(p[0]), s1 = q4_scale2(p[1]), m1 = q4_low2(p[1]);
+#pragma unroll
+      for (int i = 0; i < KW; ++i)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const uint32_t a0 = q4_pair<T>(x.w[0][w] >> (8 * u), s0, m0), a1 = q4_pair<T>(x.w[1][w] >> (8 * u), s1, m1);
-          const uint32_t a2 = q4_pair<T>(x.w[0][w] >> (8 * u + 4), s0, m0);
-          const uint32_t a3 = q4_pair<T>(x.w[1][w] >> (8 * u + 4), s1, m1);
+          const uint32_t a0 = q4_pair<T>(w[0][i] >> (8 * u), s0, m0, magic), a1 = q4_pair<T>(w[1][i] >> (8 * u), s1, m1, magic);
+          const uint32_t a2 = q4_pair<T>(w[0][i] >> (8 * u + 4), s0, m0, magic);
+          const uint32_t a3 = q4_pair<T>(w[1][i] >> (8 * u + 4), s1, m1, magic);
 #pragma unroll
           for (int f = 0; f < NF; ++f)
-            mma16816<T>(c[f], a0, a1, a2, a3, u ? qf[f][w].z : qf[f][w].x, u ? qf[f][w].w : qf[f][w].y);
+            mma16816<T>(c[f], a0, a1, a2, a3, u ? qf[f][i].z : qf[f][i].x, u ? qf[f][i].w : qf[f][i].y);
         }
     }
-    const int j0 = 16 * t + g8, j1 = j0 + 8;
-#pragma unroll
-    for (int f = 0; f < NF; ++f) {
-      sc[t][f][0] = have && j0 <= lim[f][0] && j0 < nkw ? c[f][0] * a.scale_log2 : -INFINITY;
-      sc[t][f][1] = have && j0 <= lim[f][1] && j0 < nkw ? c[f][1] * a.scale_log2 : -INFINITY;
-      sc[t][f][2] = have && j1 <= lim[f][0] && j1 < nkw ? c[f][2] * a.scale_log2 : -INFINITY;
-      sc[t][f][3] = have && j1 <= lim[f][1] && j1 < nkw ? c[f][3] * a.scale_log2 : -INFINITY;
-      mx[f][0] = fmaxf(mx[f][0], fmaxf(sc[t][f][0], sc[t][f][2]));
-      mx[f][1] = fmaxf(mx[f][1], fmaxf(sc[t][f][1], sc[t][f][3]));
-    }
-  }
-
-  // ---- values: the first tiles are in flight while the softmax runs
-  struct VTile {
-    uint32_t w[4][VW], p[4];
-  };
-  auto load_v = [&](int t, VTile& x) {
-    const long long row = tile_row(t);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int kt = 2 * q4 + (r & 1) + 8 * (r >> 1);  // 2q, 2q + 1, 2q + 8, 2q + 9
-      if (row >= 0 && 16 * t + kt < nkw) {
-        const long long at = row + kt;
-        ldg_words<VW>(a.v_codes + at * kRowBytes + g8 * (4 * VW), x.w[r]);
-        x.p[r] = ldg32(a.v_params + at * kRowGroups + g8 * VW / 4);
-      } else {
-#pragma unroll
-        for (int w = 0; w < VW; ++w) x.w[r][w] = 0;
-        x.p[r] = 0;
-      }
-    }
-  };
-  constexpr int kAheadV = 3;
-  VTile vb[kAheadV];
-#pragma unroll
-  for (int t = 0; t < kAheadV - 1; ++t) load_v(t, vb[t]);
-
-  float l[NF][2];
-  uint16_t(*pw)[kPStride] = reinterpret_cast<uint16_t(*)[kPStride]>(sWarp[warp]);
-#pragma unroll
-  for (int f = 0; f < NF; ++f) {
-    // A NaN score must not vanish: fmaxf drops it, the sum below keeps it.
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-      mx[f][0] = fmaxf(mx[f][0], __shfl_xor_sync(0xffffffffu, mx[f][0], o));
-      mx[f][1] = fmaxf(mx[f][1], __shfl_xor_sync(0xffffffffu, mx[f][1], o));
-    }
-    const float z0 = mx[f][0] == -INFINITY ? 0.f : mx[f][0], z1 = mx[f][1] == -INFINITY ? 0.f : mx[f][1];
-    l[f][0] = l[f][1] = 0.f;
-    const int c0 = 8 * f + 2 * q4;
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
-      const float p0 = ex2_approx(sc[t][f][0] - z0), p1 = ex2_approx(sc[t][f][1] - z1);
-      const float p2 = ex2_approx(sc[t][f][2] - z0), p3 = ex2_approx(sc[t][f][3] - z1);
-      l[f][0] += p0 + p2;
-      l[f][1] += p1 + p3;
-      pw[c0][16 * t + g8] = bits16<T>(p0);
-      pw[c0 + 1][16 * t + g8] = bits16<T>(p1);
-      pw[c0][16 * t + g8 + 8] = bits16<T>(p2);
-      pw[c0 + 1][16 * t + g8 + 8] = bits16<T>(p3);
-    }
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-      l[f][0] += __shfl_xor_sync(0xffffffffu, l[f][0], o);
-      l[f][1] += __shfl_xor_sync(0xffffffffu, l[f][1], o);
-    }
-  }
-  __syncwarp();
-
-  // ---- output: channels 8(VW g8 + m) + 2i (+1) for columns 8f + 2q4, 8f + 2q4 + 1
-  float o[NF][VW * 4][4];
-#pragma unroll
-  for (int f = 0; f < NF; ++f)
-#pragma unroll
-    for (int b = 0; b < VW * 4; ++b) o[f][b][0] = o[f][b][1] = o[f][b][2] = o[f][b][3] = 0.f;
-#pragma unroll
-  for (int t = 0; t < kTiles; ++t) {
-    if (t + kAheadV - 1 < kTiles) load_v(t + kAheadV - 1, vb[(t + kAheadV - 1) % kAheadV]);
-    if (t < ntile) {
-      const VTile& x = vb[t % kAheadV];
-      const uint32_t s01 = __byte_perm(x.p[0], x.p[1], 0x5410), m01 = __byte_perm(x.p[0], x.p[1], 0x7632);
-      const uint32_t s23 = __byte_perm(x.p[2], x.p[3], 0x5410), m23 = __byte_perm(x.p[2], x.p[3], 0x7632);
-      uint32_t b[NF][2];
+    const int j1 = 16 * t + g8 + 8;
+    const bool bad = (bad_tiles >> t) & 1;
+    if (bad || 16 * t + 15 > past - kw) {  // a bad page, or keys that row 0 does not see
 #pragma unroll
       for (int f = 0; f < NF; ++f) {
-        b[f][0] = *reinterpret_cast<const uint32_t*>(&pw[8 * f + g8][16 * t + 2 * q4]);
-        b[f][1] = *reinterpret_cast<const uint32_t*>(&pw[8 * f + g8][16 * t + 2 * q4 + 8]);
+        if (bad || j1 - 8 > lim[f][0]) c[f][0] = -INFINITY;
+        if (bad || j1 - 8 > lim[f][1]) c[f][1] = -INFINITY;
+        if (bad || j1 > lim[f][0]) c[f][2] = -INFINITY;
+        if (bad || j1 > lim[f][1]) c[f][3] = -INFINITY;
       }
+    }
+
+    // ---- softmax: raise the maxima when a score passes one by more than 2^8
+    bool grow = false;
+    float mx[NF][2];
 #pragma unroll
-      for (int m = 0; m < VW; ++m) {
-        const uint32_t e01 = __byte_perm(x.w[0][m], x.w[1][m], 0x5410);  // even channels of keys 0, 1
-        const uint32_t d01 = __byte_perm(x.w[0][m], x.w[1][m], 0x7632);  // odd channels
-        const uint32_t e23 = __byte_perm(x.w[2][m], x.w[3][m], 0x5410);
-        const uint32_t d23 = __byte_perm(x.w[2][m], x.w[3][m], 0x7632);
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mx[f][e] = fmaxf(c[f][e], c[f][e + 2]) * a.scale_log2;
+        grow = grow || mx[f][e] > m[f][e] + 8.f;
+      }
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = fmaxf(mx[f][e], m[f][e]);
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+          const float k = m[f][e] == -INFINITY ? 0.f : ex2_approx(m[f][e] - x);
+          m[f][e] = x;
+          l[f][e] *= k;
+#pragma unroll
+          for (int b = 0; b < VW * 4; ++b) {
+            o[f][b][e] *= k;
+            o[f][b][e + 2] *= k;
+          }
+        }
+    }
+    uint32_t b0[NF], b1[NF];
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      const float z0 = m[f][0] == -INFINITY ? 0.f : -m[f][0], z1 = m[f][1] == -INFINITY ? 0.f : -m[f][1];
+      const float p[4] = {ex2_approx(fmaf(c[f][0], a.scale_log2, z0)), ex2_approx(fmaf(c[f][1], a.scale_log2, z1)),
+                          ex2_approx(fmaf(c[f][2], a.scale_log2, z0)), ex2_approx(fmaf(c[f][3], a.scale_log2, z1))};
+      l[f][0] += p[0] + p[2];
+      l[f][1] += p[1] + p[3];
+      b0[f] = transpose8x8(Pack<T>::store(p));
+      b1[f] = transpose8x8(Pack<T>::store(p + 2));
+    }
+
+    // ---- output: channels 8(VW g8 + m) + 2i (+1) for columns 8f + 2q4, 8f + 2q4 + 1
+    {
+      uint32_t w[4][VW], p[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int key = 2 * q4 + (r & 1) + 8 * (r >> 1);  // 2q, 2q + 1, 2q + 8, 2q + 9
+        const uint8_t* x = st + S::v + S::v_at(key, g8 * VW / 4) + g8 * VW % 4 * 4;
+        if constexpr (VW == 2) *reinterpret_cast<uint2*>(w[r]) = *reinterpret_cast<const uint2*>(x);
+        else w[r][0] = *reinterpret_cast<const uint32_t*>(x);
+        p[r] = *reinterpret_cast<const uint32_t*>(st + S::vp + key * S::kPar + g8 * VW / 4 * 4);
+      }
+      const uint32_t s01 = __byte_perm(p[0], p[1], 0x5410), m01 = __byte_perm(p[0], p[1], 0x7632);
+      const uint32_t s23 = __byte_perm(p[2], p[3], 0x5410), m23 = __byte_perm(p[2], p[3], 0x7632);
+#pragma unroll
+      for (int k = 0; k < VW; ++k) {
+        const uint32_t e01 = __byte_perm(w[0][k], w[1][k], 0x5410);  // even channels of keys 0, 1
+        const uint32_t d01 = __byte_perm(w[0][k], w[1][k], 0x7632);  // odd channels
+        const uint32_t e23 = __byte_perm(w[2][k], w[3][k], 0x5410);
+        const uint32_t d23 = __byte_perm(w[2][k], w[3][k], 0x7632);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t a0 = q4_pair<T>(e01 >> (4 * i), s01, m01), a1 = q4_pair<T>(d01 >> (4 * i), s01, m01);
-          const uint32_t a2 = q4_pair<T>(e23 >> (4 * i), s23, m23), a3 = q4_pair<T>(d23 >> (4 * i), s23, m23);
+          const uint32_t a0 = q4_pair<T>(e01 >> (4 * i), s01, m01, magic), a1 = q4_pair<T>(d01 >> (4 * i), s01, m01, magic);
+          const uint32_t a2 = q4_pair<T>(e23 >> (4 * i), s23, m23, magic), a3 = q4_pair<T>(d23 >> (4 * i), s23, m23, magic);
 #pragma unroll
-          for (int f = 0; f < NF; ++f) mma16816<T>(o[f][m * 4 + i], a0, a1, a2, a3, b[f][0], b[f][1]);
+          for (int f = 0; f < NF; ++f) mma16816<T>(o[f][k * 4 + i], a0, a1, a2, a3, b0[f], b1[f]);
         }
       }
     }
   }
-  __syncwarp();  // the weights are read
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncwarp();  // the ring is read
   float(*ow)[D] = reinterpret_cast<float(*)[D]>(sWarp[warp]);
 #pragma unroll
   for (int f = 0; f < NF; ++f) {
     const int c0 = 8 * f + 2 * q4;
 #pragma unroll
-    for (int m = 0; m < VW; ++m)
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) l[f][e] += __shfl_xor_sync(0xffffffffu, l[f][e], d);
+#pragma unroll
+    for (int k = 0; k < VW; ++k)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int d0 = 8 * (VW * g8 + m) + 2 * i;
-        if (c0 < ncols)
-          *reinterpret_cast<float2*>(&ow[c0][d0]) = make_float2(o[f][m * 4 + i][0], o[f][m * 4 + i][2]);
+        const int d0 = 8 * (VW * g8 + k) + 2 * i;
+        if (c0 < ncols) *reinterpret_cast<float2*>(&ow[c0][d0]) = make_float2(o[f][k * 4 + i][0], o[f][k * 4 + i][2]);
         if (c0 + 1 < ncols)
-          *reinterpret_cast<float2*>(&ow[c0 + 1][d0]) = make_float2(o[f][m * 4 + i][1], o[f][m * 4 + i][3]);
+          *reinterpret_cast<float2*>(&ow[c0 + 1][d0]) = make_float2(o[f][k * 4 + i][1], o[f][k * 4 + i][3]);
       }
     if (g8 == 0) {
-      sM[warp][c0] = mx[f][0];
+      sM[warp][c0] = m[f][0];
       sL[warp][c0] = l[f][0];
-      sM[warp][c0 + 1] = mx[f][1];
+      sM[warp][c0 + 1] = m[f][1];
       sL[warp][c0 + 1] = l[f][1];
     }
   }
@@ -335,22 +352,22 @@ __global__ void __launch_bounds__(kWarps * 32, NF == 1 ? 4 : 3) q4_split_kernel(
   const bool whole = a.max_splits == 1;
   for (int i = threadIdx.x; i < ncols * (D / 4); i += kWarps * 32) {
     const int c = i / (D / 4), d4 = i % (D / 4);
-    float m = -INFINITY;
+    float mc = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sM[w][c]);
-    const float z = m == -INFINITY ? 0.f : m;
+    for (int w = 0; w < kWarps; ++w) mc = fmaxf(mc, sM[w][c]);
+    const float z = mc == -INFINITY ? 0.f : mc;
     float v[4] = {0.f, 0.f, 0.f, 0.f}, lsum = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float k = ex2_approx(sM[w][c] - z);
-      const float4 p = *reinterpret_cast<const float4*>(&sWarp[w][c * D + 4 * d4]);
+      const float4 p = reinterpret_cast<const float4*>(sWarp[w])[c * (D / 4) + d4];
       v[0] = fmaf(k, p.x, v[0]);
       v[1] = fmaf(k, p.y, v[1]);
       v[2] = fmaf(k, p.z, v[2]);
       v[3] = fmaf(k, p.w, v[3]);
       lsum = fmaf(k, sL[w][c], lsum);
     }
-    const long long row = row0 + c / G, h = gk * G + c % G;
+    const long long row = row0 + (c >> lg), h = gk * G + (c & (G - 1));
     if (whole) {
       const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
       const float r[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
@@ -359,10 +376,10 @@ __global__ void __launch_bounds__(kWarps * 32, NF == 1 ? 4 : 3) q4_split_kernel(
       b.y = Pack<T>::store(r + 2);
       *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (row * a.hq + h) * D + 4 * d4) = b;
     } else {
-      const long long part = (((long long)s * kr + c / G) * a.hq + h) * a.max_splits + split;
+      const long long part = (((long long)s * kr + (c >> lg)) * a.hq + h) * a.max_splits + split;
       *reinterpret_cast<float4*>(a.part_o + part * D + 4 * d4) = make_float4(v[0], v[1], v[2], v[3]);
       if (d4 == 0) {
-        a.part_ml[part * 2] = m;
+        a.part_ml[part * 2] = mc;
         a.part_ml[part * 2 + 1] = lsum;
       }
     }
