@@ -155,7 +155,7 @@ Q4Plan q4_plan(const cp_layer_desc* d, bool ragged, int32_t num_seqs, int32_t to
   p.dec_rows = !ragged && uniform >= 1 && uniform <= most ? (int)uniform : 1;
   p.split = ragged || uniform == p.dec_rows;
   p.tensor = ragged ? total_rows > num_seqs : !p.split;
-  p.max_splits = (int)(((int64_t)max_ctx + kQ4Split - 1) / kQ4Split);
+  p.max_splits = q4_max_splits(max_ctx);
   const int64_t ppt = 2 * (kTcBlockM / std::max(d->num_q_heads / d->num_kv_heads, 1));  // tokens of a pair
   p.pairs = !p.tensor ? 0 : ragged ? (total_rows + ppt - 1) / ppt + num_seqs : num_seqs * ((uniform + ppt - 1) / ppt);
   p.lens_bytes = ((int64_t)num_seqs * 4 + 255) / 256 * 256;

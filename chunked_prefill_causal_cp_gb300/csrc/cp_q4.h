@@ -6,9 +6,21 @@
 
 namespace cp {
 
-// Keys per split of the rows that read a 4-bit cache split along its keys.
-// Fixed, so a row's result never depends on what shares the launch.
-constexpr int kQ4Split = 512;
+// Keys per split of a sequence of n keys on the split path: few for a short
+// context, where the wait for one CTA's walk is what counts (one row over 1025
+// keys: 24 us from call to result against 32 with 1024), more for a long one, whose
+// set-up and parts cost less then (4 x 100001 keys: 121 us against 156 with 256).
+// By the sequence's own length alone, so a row's result never depends on what
+// shares the launch.
+__host__ __device__ inline int q4_split_keys(int n) { return n <= 2048 ? 256 : n <= 16384 ? 512 : 1024; }
+__host__ __device__ inline int q4_splits(int n) { return (n - 1) / q4_split_keys(n) + 1; }
+// Most splits of any sequence of up to `ctx` keys.
+inline int q4_max_splits(int ctx) {
+  int m = q4_splits(ctx);
+  if (ctx > 2048) m = m > q4_splits(2048) ? m : q4_splits(2048);
+  if (ctx > 16384) m = m > q4_splits(16384) ? m : q4_splits(16384);
+  return m;
+}
 
 // Norm and rotation of the query and key heads (cp_qk_norm_rope), and, when
 // k_cache is set, the keys and values into their cache slots.

@@ -6,7 +6,7 @@
 // key and KV head at 128 channels) as long as the codes turn into matrix
 // operands quickly enough: at full bandwidth an SM has some 28 instructions per
 // key, and turning 256 codes into 16-bit values takes 15 of them.  One CTA takes
-// 512 keys of a (sequence, KV head), four warps 128 each; the k rows of the
+// 256 to 1024 keys of a (sequence, KV head), four warps a quarter each; the k rows of the
 // sequence times the G heads of the group (k * G <= 16) ride in the columns of
 // m16n8k16 products, so every row shares one read of the cache and one
 // conversion of its codes.  A warp walks its keys 16 at a time, in a rolled loop
@@ -46,10 +46,7 @@ namespace cp {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kWarpKeys = kQ4Split / kWarps;
-constexpr int kTiles = kWarpKeys / 16;
 constexpr int kRing = 4;                      // stages of a warp's ring, one 16-key tile each
-static_assert(kTiles <= 32, "a lane knows one tile's place");
 
 // N bytes of an asynchronous copy to shared memory; `on` false: zeros, nothing is read.
 template <int N>
@@ -99,7 +96,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 }
 
 template <typename T, int D, int NF>
-__global__ void __launch_bounds__(kWarps * 32, NF == 1 ? 5 : D == 64 ? 4 : 3) q4_split_kernel(const Q4AttnArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, NF == 1 ? 4 : D == 64 ? 4 : 3) q4_split_kernel(const Q4AttnArgs a) {
   constexpr int NC = 8 * NF;     // (row, head) columns
   constexpr int KW = D / 32;     // score phase: words of a lane's channels
   constexpr int VW = D / 64;     // output phase
@@ -126,14 +123,14 @@ __global__ void __launch_bounds__(kWarps * 32, NF == 1 ? 5 : D == 64 ? 4 : 3) q4
     return;
   }
   const int n = past + kr;  // keys, this call's rows among them
-  const int k0 = split * kQ4Split;
-  if (k0 >= n) return;
+  const int split_keys = q4_split_keys(n), warp_keys = split_keys / kWarps;  // at most 256: a lane knows one tile's place
+  if (split > (n - 1) / split_keys) return;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g8 = lane >> 2, q4 = lane & 3;
   const int G = a.group, ncols = kr * G, lg = 31 - __clz(G);  // G is a power of two
-  const int kw = k0 + warp * kWarpKeys;              // the warp's first key
-  const int nkw = max(0, min(n - kw, kWarpKeys));    // its keys
+  const int kw = split * split_keys + warp * warp_keys;  // the warp's first key
+  const int nkw = max(0, min(n - kw, warp_keys));        // its keys
   const int ntile = (nkw + 15) / 16;
 
   // First cache row of each of the warp's tiles (a page holds whole tiles): lane t has tile t's, -1 for a bad page.
@@ -349,7 +346,7 @@ __global__ void __launch_bounds__(kWarps * 32, NF == 1 ? 5 : D == 64 ? 4 : 3) q4
   __syncthreads();
 
   // ---- the split's part: the warps' parts merged in warp order
-  const bool whole = a.max_splits == 1;
+  const bool whole = n <= split_keys;
   for (int i = threadIdx.x; i < ncols * (D / 4); i += kWarps * 32) {
     const int c = i / (D / 4), d4 = i % (D / 4);
     float mc = -INFINITY;
@@ -400,7 +397,8 @@ __global__ void __launch_bounds__(8 * D / 4) q4_combine_kernel(const Q4AttnArgs 
   if (seq_rows(a.rows, s) != kr) return;
   const int past = a.past[s], row0 = seq_row0(a.rows, s);
   if (past < 0 || (long long)past + kr > a.max_ctx || row0 < 0 || row0 > a.total_rows - kr) return;
-  const int nsplit = (past + r + kQ4Split) / kQ4Split;  // of the past + r + 1 keys the row sees
+  const int nsplit = q4_splits(past + kr);  // the last may hold keys of later rows only: a part of weight 0
+  if (nsplit == 1) return;                  // finished by the split kernel
   const int slice = threadIdx.x / C4, d4 = threadIdx.x % C4;
   const long long base = (((long long)s * kr + r) * a.hq + h) * a.max_splits;
   float m = -INFINITY, l = 0.f;
