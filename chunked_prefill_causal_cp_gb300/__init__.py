@@ -283,32 +283,63 @@ def _refuse(where):
     raise CPError(CP_ERR_INVALID_ARG, where)
 
 
-def _arg(where, t, dtype, numel=None, none=False):
-    """Pointer of a dense CUDA tensor of `dtype` with at least `numel` elements (raw handles pass)."""
-    if t is None:
-        return None if none else _refuse(where)
-    if isinstance(t, int):
+def _device(where, *tensors):
+    """Index of the first tensor's device, which has to be the current one: the library launches there."""
+    for t in tensors:
+        if isinstance(t, torch.Tensor):
+            dev = t.get_device()
+            if dev < 0 or dev != torch._C._cuda_getDevice():
+                _refuse(where)
+            return dev
+    return 0
+
+
+def _on(dev, stream):
+    """The given stream, or the device's current one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _arg(where, t, dtype, numel, dev):
+    """Pointer of a dense tensor of `dtype` on `dev` with at least `numel` elements (raw handles pass)."""
+    if isinstance(t, torch.Tensor):
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() >= numel:
+            return t.data_ptr()
+    elif isinstance(t, int):
         return t
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or (numel is not None and t.numel() < numel):
-        _refuse(where)
-    return t.data_ptr()
+    _refuse(where)
 
 
-def _layer_dtype(desc):
-    return torch.bfloat16 if desc.dtype == CP_BF16 else torch.float16 if desc.dtype == CP_F16 else torch.float32
+def _opt(where, t, dtype, numel, dev):
+    """The same, or None."""
+    return None if t is None else _arg(where, t, dtype, numel, dev)
 
 
-def _rows_arg(where, t, desc, heads, total_rows):
-    """(pointer, row stride in elements) of rows [..., heads, D]: a head row is dense, and one stride leads from
-    each row to the next."""
+_LAYER_DTYPE = {code: dtype for dtype, code in DTYPE_CODE.items()}
+
+
+def _workspace(where, t, dev):
+    """Pointer and bytes of a workspace."""
     if t is None or isinstance(t, int):
         return t, 0
-    if (t.dtype != _layer_dtype(desc) or not t.is_cuda or t.dim() < 2
-            or tuple(t.shape[-2:]) != (heads, desc.head_dim) or t.numel() != total_rows * heads * desc.head_dim):
+    if t.get_device() != dev or not t.is_contiguous():
         _refuse(where)
-    if t.is_contiguous() or t.numel() == 0:
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _rows_arg(where, t, desc, heads, total_rows, dev):
+    """(pointer, row stride in elements) of rows [..., heads, D]: a head row is dense, and one stride leads from
+    each row to the next.  None and raw handles pass as they are (dense)."""
+    if t is None or isinstance(t, int):
+        return t, 0
+    d, n, shape = desc.head_dim, t.numel(), t.shape
+    if (t.dtype is not _LAYER_DTYPE.get(desc.dtype) or t.get_device() != dev or len(shape) < 2 or shape[-1] != d
+            or shape[-2] != heads or n != total_rows * heads * d):
+        _refuse(where)
+    if n == 0 or t.is_contiguous():
         return t.data_ptr(), 0
-    if t.stride(-1) != 1 or (heads > 1 and t.stride(-2) != desc.head_dim):
+    if t.stride(-1) != 1 or (heads > 1 and t.stride(-2) != d):
         _refuse(where)
     stride = size = None  # of the rows so far, from the last dimension of rows
     for n, st in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
@@ -320,6 +351,8 @@ def _rows_arg(where, t, desc, heads, total_rows):
             size *= n
         else:
             _refuse(where)
+    if stride is not None and stride < 1:  # an expanded tensor's rows: 0 would read as dense
+        _refuse(where)
     return t.data_ptr(), stride or 0
 
 
@@ -341,38 +374,38 @@ def q4_cache(k_codes, v_codes, k_params, v_params) -> Q4Cache:
     return c
 
 
-def _q4_arg(where, desc, cache):
+def _q4_arg(where, desc, cache, dev):
     """The cache, with arrays as large as desc says."""
     tensors = getattr(cache, "tensors", None)
     if tensors is not None:
-        paged = desc.kind == CP_CACHE_PAGED
-        slots = desc.num_pages * desc.page_size if paged else desc.batch * desc.capacity
-        if tensors[2].dtype != _layer_dtype(desc) or tensors[0].numel() < slots * desc.num_kv_heads * (desc.head_dim // 2):
+        slots = desc.num_pages * desc.page_size if desc.kind == CP_CACHE_PAGED else desc.batch * desc.capacity
+        codes, params = tensors[0], tensors[2]
+        if (params.dtype is not _LAYER_DTYPE.get(desc.dtype) or codes.get_device() != dev
+                or codes.numel() < slots * desc.num_kv_heads * (desc.head_dim // 2)):
             _refuse(where)
     return ctypes.byref(cache)
 
 
-def _seq_args(where, desc, lens, cu_rows, block_table, num_seqs):
-    table = num_seqs * desc.max_blocks if desc.kind == CP_CACHE_PAGED else None
-    return (_arg(where, lens, torch.int32, num_seqs), _arg(where, cu_rows, torch.int32, num_seqs + 1, none=True),
-            _arg(where, block_table, torch.int32, table, none=True))
+def _seq_args(where, desc, lens, cu_rows, block_table, num_seqs, dev):
+    return (_arg(where, lens, torch.int32, num_seqs, dev), _opt(where, cu_rows, torch.int32, num_seqs + 1, dev),
+            _opt(where, block_table, torch.int32, num_seqs * desc.max_blocks, dev))
 
 
 def cp_qk_norm_rope(desc, prep, q, k, q_out, k_out, num_seqs, total_rows, q_weight=None, k_weight=None, inv_freq=None,
                     positions=None, seqlens_k=None, cu_rows=None, stream=None):
     """Norm of every query and key head and rotary position, one pass (see include/cp_api.h).  q and k may be
     slices of a projection's rows."""
-    w, dt = "cp_qk_norm_rope", _layer_dtype(desc)
-    pq, sq = _rows_arg(w, q, desc, desc.num_q_heads, total_rows)
-    pk, sk = _rows_arg(w, k, desc, desc.num_kv_heads, total_rows)
-    d = desc.head_dim
+    w, dt, d, i32 = "cp_qk_norm_rope", _LAYER_DTYPE.get(desc.dtype), desc.head_dim, torch.int32
+    hq, hkv = desc.num_q_heads, desc.num_kv_heads
+    dev = _device(w, q, k)
+    pq, sq = _rows_arg(w, q, desc, hq, total_rows, dev)
+    pk, sk = _rows_arg(w, k, desc, hkv, total_rows, dev)
     s = lib().cp_qk_norm_rope(
-        ctypes.byref(desc), ctypes.byref(prep), pq, sq, pk, sk, _arg(w, q_weight, dt, d, none=True),
-        _arg(w, k_weight, dt, d, none=True), _arg(w, inv_freq, torch.float32, prep.rot_dim // 2, none=True),
-        _arg(w, positions, torch.int32, total_rows, none=True), _arg(w, seqlens_k, torch.int32, num_seqs, none=True),
-        _arg(w, cu_rows, torch.int32, num_seqs + 1, none=True), num_seqs, total_rows,
-        _arg(w, q_out, dt, total_rows * desc.num_q_heads * d, none=True),
-        _arg(w, k_out, dt, total_rows * desc.num_kv_heads * d, none=True), _stream(stream, q, k))
+        ctypes.byref(desc), ctypes.byref(prep), pq, sq, pk, sk, _opt(w, q_weight, dt, d, dev),
+        _opt(w, k_weight, dt, d, dev), _opt(w, inv_freq, torch.float32, prep.rot_dim // 2, dev),
+        _opt(w, positions, i32, total_rows, dev), _opt(w, seqlens_k, i32, num_seqs, dev),
+        _opt(w, cu_rows, i32, num_seqs + 1, dev), num_seqs, total_rows, _opt(w, q_out, dt, total_rows * hq * d, dev),
+        _opt(w, k_out, dt, total_rows * hkv * d, dev), _on(dev, stream))
     _check(s, w)
 
 
@@ -380,68 +413,72 @@ def cp_qk_norm_rope_append(desc, prep, q, k_new, v_new, q_out, k_cache, v_cache,
                            max_ctx, q_weight=None, k_weight=None, inv_freq=None, positions=None, cu_rows=None,
                            block_table=None, dev_status=None, stream=None):
     """cp_qk_norm_rope with the keys and values into their cache slots (see include/cp_api.h)."""
-    w, dt = "cp_qk_norm_rope_append", _layer_dtype(desc)
-    pq, sq = _rows_arg(w, q, desc, desc.num_q_heads, total_rows)
-    pk, sk = _rows_arg(w, k_new, desc, desc.num_kv_heads, total_rows)
-    pv, sv = _rows_arg(w, v_new, desc, desc.num_kv_heads, total_rows)
-    d = desc.head_dim
-    slots = desc.num_pages * desc.page_size if desc.kind == CP_CACHE_PAGED else desc.batch * desc.capacity
-    lens, cu, table = _seq_args(w, desc, seqlens_k, cu_rows, block_table, num_seqs)
+    w, dt, d, i32 = "cp_qk_norm_rope_append", _LAYER_DTYPE.get(desc.dtype), desc.head_dim, torch.int32
+    hq, hkv = desc.num_q_heads, desc.num_kv_heads
+    dev = _device(w, q, k_new, v_new)
+    pq, sq = _rows_arg(w, q, desc, hq, total_rows, dev)
+    pk, sk = _rows_arg(w, k_new, desc, hkv, total_rows, dev)
+    pv, sv = _rows_arg(w, v_new, desc, hkv, total_rows, dev)
+    size = (desc.num_pages * desc.page_size if desc.kind == CP_CACHE_PAGED else desc.batch * desc.capacity) * hkv * d
+    lens, cu, table = _seq_args(w, desc, seqlens_k, cu_rows, block_table, num_seqs, dev)
     s = lib().cp_qk_norm_rope_append(
-        ctypes.byref(desc), ctypes.byref(prep), pq, sq, pk, sk, pv, sv, _arg(w, q_weight, dt, d, none=True),
-        _arg(w, k_weight, dt, d, none=True), _arg(w, inv_freq, torch.float32, prep.rot_dim // 2, none=True),
-        _arg(w, positions, torch.int32, total_rows, none=True), cu, num_seqs, total_rows,
-        _arg(w, q_out, dt, total_rows * desc.num_q_heads * d),
-        _arg(w, k_cache, dt, slots * desc.num_kv_heads * d), _arg(w, v_cache, dt, slots * desc.num_kv_heads * d), lens,
-        table, max_ctx, _ptr(dev_status), _stream(stream, q))
+        ctypes.byref(desc), ctypes.byref(prep), pq, sq, pk, sk, pv, sv, _opt(w, q_weight, dt, d, dev),
+        _opt(w, k_weight, dt, d, dev), _opt(w, inv_freq, torch.float32, prep.rot_dim // 2, dev),
+        _opt(w, positions, i32, total_rows, dev), cu, num_seqs, total_rows, _arg(w, q_out, dt, total_rows * hq * d, dev),
+        _arg(w, k_cache, dt, size, dev), _arg(w, v_cache, dt, size, dev), lens, table, max_ctx,
+        _opt(w, dev_status, i32, 1, dev), _on(dev, stream))
     _check(s, w)
 
 
 def cp_kv_append_q4(desc, k_new, v_new, cache, seqlens_k, num_seqs, total_rows, max_ctx, cu_rows=None,
                     block_table=None, dev_status=None, stream=None):
     """Rows into a 4-bit cache (see include/cp_api.h)."""
-    w, dt, n = "cp_kv_append_q4", _layer_dtype(desc), total_rows * desc.num_kv_heads * desc.head_dim
-    lens, cu, table = _seq_args(w, desc, seqlens_k, cu_rows, block_table, num_seqs)
-    s = lib().cp_kv_append_q4(ctypes.byref(desc), _arg(w, k_new, dt, n), _arg(w, v_new, dt, n), cu, num_seqs,
-                              total_rows, _q4_arg(w, desc, cache), lens, table, max_ctx, _ptr(dev_status),
-                              _stream(stream, k_new))
+    w, dt, n = "cp_kv_append_q4", _LAYER_DTYPE.get(desc.dtype), total_rows * desc.num_kv_heads * desc.head_dim
+    dev = _device(w, k_new, v_new)
+    lens, cu, table = _seq_args(w, desc, seqlens_k, cu_rows, block_table, num_seqs, dev)
+    s = lib().cp_kv_append_q4(ctypes.byref(desc), _arg(w, k_new, dt, n, dev), _arg(w, v_new, dt, n, dev), cu, num_seqs,
+                              total_rows, _q4_arg(w, desc, cache, dev), lens, table, max_ctx,
+                              _opt(w, dev_status, torch.int32, 1, dev), _on(dev, stream))
     _check(s, w)
 
 
 def cp_kv_read_q4(desc, cache, starts, num_seqs, total_rows, max_ctx, k_out, v_out, cu_rows=None, block_table=None,
                   dev_status=None, stream=None):
     """The values that rows of a 4-bit cache stand for (see include/cp_api.h)."""
-    w, dt, n = "cp_kv_read_q4", _layer_dtype(desc), total_rows * desc.num_kv_heads * desc.head_dim
-    lens, cu, table = _seq_args(w, desc, starts, cu_rows, block_table, num_seqs)
-    s = lib().cp_kv_read_q4(ctypes.byref(desc), _q4_arg(w, desc, cache), lens, table, cu, num_seqs, total_rows, max_ctx,
-                            _arg(w, k_out, dt, n, none=True), _arg(w, v_out, dt, n, none=True), _ptr(dev_status),
-                            _stream(stream, k_out, v_out))
+    w, dt, n = "cp_kv_read_q4", _LAYER_DTYPE.get(desc.dtype), total_rows * desc.num_kv_heads * desc.head_dim
+    dev = _device(w, starts)
+    lens, cu, table = _seq_args(w, desc, starts, cu_rows, block_table, num_seqs, dev)
+    s = lib().cp_kv_read_q4(ctypes.byref(desc), _q4_arg(w, desc, cache, dev), lens, table, cu, num_seqs, total_rows,
+                            max_ctx, _opt(w, k_out, dt, n, dev), _opt(w, v_out, dt, n, dev),
+                            _opt(w, dev_status, torch.int32, 1, dev), _on(dev, stream))
     _check(s, w)
 
 
 def cp_chunk_attn_q4(desc, q, cache, seqlens_k, num_seqs, total_rows, max_ctx, out, workspace, cu_rows=None,
                      block_table=None, commit=True, dev_status=None, stream=None):
     """Causal attention over a 4-bit cache (see include/cp_api.h)."""
-    w, dt, n = "cp_chunk_attn_q4", _layer_dtype(desc), total_rows * desc.num_q_heads * desc.head_dim
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    lens, cu, table = _seq_args(w, desc, seqlens_k, cu_rows, block_table, num_seqs)
-    s = lib().cp_chunk_attn_q4(ctypes.byref(desc), _arg(w, q, dt, n), _q4_arg(w, desc, cache), lens, table, cu,
-                               num_seqs, total_rows, max_ctx, _arg(w, out, dt, n), _ptr(workspace), ws_bytes,
-                               1 if commit else 0, _ptr(dev_status), _stream(stream, q))
+    w, dt, n = "cp_chunk_attn_q4", _LAYER_DTYPE.get(desc.dtype), total_rows * desc.num_q_heads * desc.head_dim
+    dev = _device(w, q, out)
+    ws, ws_bytes = _workspace(w, workspace, dev)
+    lens, cu, table = _seq_args(w, desc, seqlens_k, cu_rows, block_table, num_seqs, dev)
+    s = lib().cp_chunk_attn_q4(ctypes.byref(desc), _arg(w, q, dt, n, dev), _q4_arg(w, desc, cache, dev), lens, table,
+                               cu, num_seqs, total_rows, max_ctx, _arg(w, out, dt, n, dev), ws, ws_bytes,
+                               1 if commit else 0, _opt(w, dev_status, torch.int32, 1, dev), _on(dev, stream))
     _check(s, w)
 
 
 def cp_mixed_step_q4(desc, q, k_new, v_new, cache, seqlens_k, num_seqs, total_rows, max_ctx, out, workspace,
                      cu_rows=None, block_table=None, commit=True, dev_status=None, stream=None):
     """Append, attention and advance of a step over a 4-bit cache in one call (see include/cp_api.h)."""
-    w, dt, d = "cp_mixed_step_q4", _layer_dtype(desc), desc.head_dim
+    w, dt, d = "cp_mixed_step_q4", _LAYER_DTYPE.get(desc.dtype), desc.head_dim
     nq, nk = total_rows * desc.num_q_heads * d, total_rows * desc.num_kv_heads * d
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    lens, cu, table = _seq_args(w, desc, seqlens_k, cu_rows, block_table, num_seqs)
-    s = lib().cp_mixed_step_q4(ctypes.byref(desc), _arg(w, q, dt, nq), _arg(w, k_new, dt, nk), _arg(w, v_new, dt, nk),
-                               _q4_arg(w, desc, cache), table, cu, lens, num_seqs, total_rows, max_ctx,
-                               _arg(w, out, dt, nq), _ptr(workspace), ws_bytes, 1 if commit else 0, _ptr(dev_status),
-                               _stream(stream, q))
+    dev = _device(w, q, out)
+    ws, ws_bytes = _workspace(w, workspace, dev)
+    lens, cu, table = _seq_args(w, desc, seqlens_k, cu_rows, block_table, num_seqs, dev)
+    s = lib().cp_mixed_step_q4(ctypes.byref(desc), _arg(w, q, dt, nq, dev), _arg(w, k_new, dt, nk, dev),
+                               _arg(w, v_new, dt, nk, dev), _q4_arg(w, desc, cache, dev), table, cu, lens, num_seqs,
+                               total_rows, max_ctx, _arg(w, out, dt, nq, dev), ws, ws_bytes, 1 if commit else 0,
+                               _opt(w, dev_status, torch.int32, 1, dev), _on(dev, stream))
     _check(s, w)
 
 

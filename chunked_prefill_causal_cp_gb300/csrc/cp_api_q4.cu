@@ -106,10 +106,11 @@ int cache_check(const cp_layer_desc* d, const SeqRows& rows, int32_t total_rows,
 }
 
 // Layers and caches that may be held in 4 bits, and the cache's arrays.
-int q4_check(const cp_layer_desc* d, const cp_q4_cache* c) {
+int q4_check(const cp_layer_desc* d, const cp_q4_cache* c, int32_t total_rows) {
   const int r = check_desc(d, false);
   if (r != CP_OK) return r;
   if (d->dtype == CP_F32 || d->kind == CP_CACHE_ROLLING) return CP_ERR_UNSUPPORTED;
+  if (total_rows > 0 && (int64_t)total_rows * d->num_kv_heads > INT32_MAX) return CP_ERR_UNSUPPORTED;
   if (!c || !c->k_codes || !c->v_codes || !c->k_params || !c->v_params) return CP_ERR_INVALID_ARG;
   if (!aligned16(c->k_codes) || !aligned16(c->v_codes) || !aligned16(c->k_params) || !aligned16(c->v_params))
     return CP_ERR_INVALID_ARG;
@@ -172,7 +173,7 @@ int q4_attn_check(const cp_layer_desc* d, const void* q, const cp_q4_cache* c, c
                   const int32_t* block_table, const int32_t* cu_rows, int32_t num_seqs, int32_t total_rows,
                   int32_t max_ctx, const void* out, const void* workspace, size_t workspace_bytes, SeqRows* rows,
                   Q4Plan* plan) {
-  int r = q4_check(d, c);
+  int r = q4_check(d, c, total_rows);
   if (r != CP_OK) return r;
   r = rows_of(cu_rows, num_seqs, total_rows, rows);
   if (r != CP_OK) return r;
@@ -306,7 +307,7 @@ int cp_qk_norm_rope_append(const cp_layer_desc* desc, const cp_qk_prep* prep, co
 int cp_kv_append_q4(const cp_layer_desc* desc, const void* k_new, const void* v_new, const int32_t* cu_rows,
                     int32_t num_seqs, int32_t total_rows, const cp_q4_cache* cache, const int32_t* seqlens_k,
                     const int32_t* block_table, int32_t max_ctx, int32_t* dev_status, void* stream) {
-  int r = q4_check(desc, cache);
+  int r = q4_check(desc, cache, total_rows);
   if (r != CP_OK) return r;
   SeqRows rows;
   r = rows_of(cu_rows, num_seqs, total_rows, &rows);
@@ -323,7 +324,7 @@ int cp_kv_append_q4(const cp_layer_desc* desc, const void* k_new, const void* v_
 int cp_kv_read_q4(const cp_layer_desc* desc, const cp_q4_cache* cache, const int32_t* starts,
                   const int32_t* block_table, const int32_t* cu_rows, int32_t num_seqs, int32_t total_rows,
                   int32_t max_ctx, void* k_out, void* v_out, int32_t* dev_status, void* stream) {
-  int r = q4_check(desc, cache);
+  int r = q4_check(desc, cache, total_rows);
   if (r != CP_OK) return r;
   SeqRows rows;
   r = rows_of(cu_rows, num_seqs, total_rows, &rows);

@@ -9,8 +9,10 @@
 // from the inputs alone.  Each lane writes one 32-bit word of codes, the first
 // lane of a group its scale and smallest value.  Reading is the reverse: m + c s
 // in fp32 (c s is exact) rounded once.  Both are bound by bytes.
+#include <cmath>
 #include <cstdint>
 
+#include "cp_q4.cuh"
 #include "cp_q4.h"
 #include "cp_rows.cuh"
 
@@ -59,12 +61,27 @@ __device__ __forceinline__ void quantize(const uint4& v, uint32_t& word, uint32_
   Pack<T>::load(sb, s2);
   const float s = s2[0];
   word = 0;
-  if (s > 0.f) {
+  if (!(s > 0.f)) return;
+  // The quotient's rounding decides a code only near a half: a product with the
+  // reciprocal is within 2^-22 of it (two roundings of up to 2^4), so anything
+  // further than 2^-20 from a half rounds alike, and the rest divides.  Adding
+  // 1.5 * 2^23 rounds to a whole number, ties to even, in the low bits.
+  const float inv = __fdiv_rn(1.f, s);
+  float q[8], near = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float c = fminf(rintf(__fdiv_rn(__fadd_rn(x[i], -lo), s)), 15.f);
-      word |= (uint32_t)c << (4 * (i >> 1) + 16 * (i & 1));
-    }
+  for (int i = 0; i < 8; ++i) {
+    q[i] = __fmul_rn(__fadd_rn(x[i], -lo), inv);
+    const float r = __fadd_rn(__fadd_rn(q[i], 12582912.f), -12582912.f);
+    near = fmaxf(near, fabsf(__fadd_rn(q[i], -r)));
+  }
+  if (!(near < 0.5f - 0x1p-20f) || !(inv < INFINITY)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(__fadd_rn(x[i], -lo), s);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t c = __float_as_uint(__fadd_rn(fminf(q[i], 15.f), 12582912.f)) & 15u;
+    word |= c << (4 * (i >> 1) + 16 * (i & 1));
   }
 }
 
@@ -75,20 +92,19 @@ __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(const Q4Args a) {
   pdl_wait();
   if (a.past_snapshot && blockIdx.x == 0)
     for (int s = threadIdx.x; s < a.rows.num_seqs; s += kQ4Threads) a.past_snapshot[s] = a.past[s];
-  const long long id = (long long)blockIdx.x * kQ4Threads + threadIdx.x;
-  const long long row = id / V;
-  const int c = (int)(id % V);
-  const bool on = row < (long long)a.total_rows * a.hkv;
+  const uint32_t row = blockIdx.x * (uint32_t)(kQ4Threads / V) + threadIdx.x / V;  // at most INT32_MAX + a block's
+  const int c = threadIdx.x % V;
+  const bool on = row < (uint32_t)a.total_rows * (uint32_t)a.hkv;
   uint4 kv = make_uint4(0, 0, 0, 0), vv = kv;
   if (on) {
-    kv = static_cast<const uint4*>(a.k_new)[row * V + c];
-    vv = static_cast<const uint4*>(a.v_new)[row * V + c];
+    kv = static_cast<const uint4*>(a.k_new)[(long long)row * V + c];
+    vv = static_cast<const uint4*>(a.v_new)[(long long)row * V + c];
   }
   uint32_t kw, kp, vw, vp;
   quantize<T>(kv, kw, kp);  // shuffles: every lane takes part
   quantize<T>(vv, vw, vp);
   if (!on) return;
-  const int t = (int)(row / a.hkv), g = (int)(row % a.hkv);
+  const int t = (int)(row / (uint32_t)a.hkv), g = (int)(row % (uint32_t)a.hkv);
   const int s = row_seq(a.rows, t);
   const long long dst = cache_row(a.cache, a.hkv, s, g, (long long)a.past[s] + t - seq_row0(a.rows, s), a.max_ctx);
   if (dst < 0) {
@@ -104,13 +120,10 @@ __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(const Q4Args a) {
 }
 
 template <typename T>
-__device__ __forceinline__ uint4 dequantize(uint32_t word, uint32_t params) {
-  float sm[2], x[8];
-  Pack<T>::load(params, sm);
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    x[i] = fmaf((float)((word >> (4 * (i >> 1) + 16 * (i & 1))) & 15u), sm[0], sm[1]);
-  return pack16<T>(x);
+__device__ __forceinline__ uint4 dequantize(uint32_t word, uint32_t params, uint32_t magic) {
+  const uint32_t s2 = q4_scale2(params), m2 = q4_low2(params);
+  return make_uint4(q4_pair<T>(word, s2, m2, magic), q4_pair<T>(word >> 4, s2, m2, magic),
+                    q4_pair<T>(word >> 8, s2, m2, magic), q4_pair<T>(word >> 12, s2, m2, magic));
 }
 
 template <typename T, int D>
@@ -118,11 +131,10 @@ __global__ void __launch_bounds__(kQ4Threads) q4_read_kernel(const Q4Args a) {
   constexpr int V = D / 8;
   pdl_launch_dependents();
   pdl_wait();
-  const long long id = (long long)blockIdx.x * kQ4Threads + threadIdx.x;
-  const long long row = id / V;
-  const int c = (int)(id % V);
-  if (row >= (long long)a.total_rows * a.hkv) return;
-  const int t = (int)(row / a.hkv), g = (int)(row % a.hkv);
+  const uint32_t row = blockIdx.x * (uint32_t)(kQ4Threads / V) + threadIdx.x / V;
+  const int c = threadIdx.x % V;
+  if (row >= (uint32_t)a.total_rows * (uint32_t)a.hkv) return;
+  const int t = (int)(row / (uint32_t)a.hkv), g = (int)(row % (uint32_t)a.hkv);
   const int s = row_seq(a.rows, t);
   const long long src = cache_row(a.cache, a.hkv, s, g, (long long)a.past[s] + t - seq_row0(a.rows, s), a.max_ctx);
   if (src < 0) {
@@ -130,19 +142,19 @@ __global__ void __launch_bounds__(kQ4Threads) q4_read_kernel(const Q4Args a) {
     return;
   }
   if (a.k_out)
-    static_cast<uint4*>(a.k_out)[row * V + c] =
-        dequantize<T>(reinterpret_cast<const uint32_t*>(a.k_codes)[src * V + c], a.k_params[src * (V / 4) + c / 4]);
+    static_cast<uint4*>(a.k_out)[(long long)row * V + c] =
+        dequantize<T>(reinterpret_cast<const uint32_t*>(a.k_codes)[src * V + c], a.k_params[src * (V / 4) + c / 4], q4_magic<T>());
   if (a.v_out)
-    static_cast<uint4*>(a.v_out)[row * V + c] =
-        dequantize<T>(reinterpret_cast<const uint32_t*>(a.v_codes)[src * V + c], a.v_params[src * (V / 4) + c / 4]);
+    static_cast<uint4*>(a.v_out)[(long long)row * V + c] =
+        dequantize<T>(reinterpret_cast<const uint32_t*>(a.v_codes)[src * V + c], a.v_params[src * (V / 4) + c / 4], q4_magic<T>());
 }
 
 template <typename K>
 cudaError_t launch_rows(K kernel, const Q4Args& a, int d, cudaStream_t st) {
-  const long long threads = (long long)a.total_rows * a.hkv * (d / 8);
-  if (threads == 0) return cudaSuccess;
-  const long long grid = (threads + kQ4Threads - 1) / kQ4Threads;
-  if (grid >= (1ll << 31)) return cudaErrorInvalidValue;
+  const long long rows = (long long)a.total_rows * a.hkv, per = kQ4Threads / (d / 8);
+  if (rows == 0) return cudaSuccess;
+  if (rows > INT32_MAX) return cudaErrorInvalidValue;
+  const long long grid = (rows + per - 1) / per;
   return launch_pdl(kernel, dim3((unsigned)grid), dim3(kQ4Threads), 0, st, a);
 }
 

@@ -21,6 +21,7 @@
 // with no reduction error to speak of.  Its top 32 bits go to sincospif: the
 // angle's error is below 2^-23 (half a unit of the fraction's float), whatever
 // the position.
+#include <algorithm>
 #include <cstdint>
 
 #include "cp_q4.h"
@@ -57,17 +58,18 @@ struct RopeShape {
 
 constexpr int kRopeThreads = 128;
 
-// per_warp: head-row blocks (of kRows rows) a warp takes; splits: warps per token.
+// A warp takes per_warp blocks of kRows head rows of one token: all of them, or
+// the blockIdx.y-th share.
 template <typename T, int D, bool kAppend>
-__global__ void __launch_bounds__(kRopeThreads) qk_rope_kernel(const RopeArgs a, int per_warp, int splits) {
+__global__ void __launch_bounds__(kRopeThreads) qk_rope_kernel(const RopeArgs a, int per_warp) {
   using S = RopeShape<T, D>;
   constexpr int E = S::kPer16, L = S::kLanes, R = S::kRows;
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const long long w = ((long long)blockIdx.x * kRopeThreads + threadIdx.x) >> 5;
-  const int t = (int)(w / splits);
-  if (t >= a.total_rows) return;
+  const long long t_wide = ((long long)blockIdx.x * kRopeThreads + threadIdx.x) >> 5;
+  if (t_wide >= a.total_rows) return;
+  const int t = (int)t_wide;
   const int l = lane % L, rg = lane / L;
   const bool rot = l < a.pairs;
 
@@ -77,6 +79,22 @@ __global__ void __launch_bounds__(kRopeThreads) qk_rope_kernel(const RopeArgs a,
     c0 = l;
     c1 = l + a.pairs;
   }
+  // Head rows in order: queries, keys, values (append).  The next block's loads are
+  // on their way while a block is worked on, the first one's before the angles.
+  const int heads = a.hq + a.hkv + (kAppend ? a.hkv : 0);
+  const int h_begin = (int)blockIdx.y * per_warp * R, h_end = min(heads, h_begin + per_warp * R);
+  uint4 n0 = make_uint4(0, 0, 0, 0), n1 = n0;
+  auto load = [&](int h) {
+    if (h >= h_end) return;
+    const T* src;
+    if (h < a.hq) src = static_cast<const T*>(a.q) + t * a.q_stride + (long long)h * D;
+    else if (h < a.hq + a.hkv) src = static_cast<const T*>(a.k) + t * a.k_stride + (long long)(h - a.hq) * D;
+    else src = static_cast<const T*>(a.v) + t * a.v_stride + (long long)(h - a.hq - a.hkv) * D;
+    n0 = reinterpret_cast<const uint4*>(src)[c0];
+    n1 = reinterpret_cast<const uint4*>(src)[c1];
+  };
+  load(h_begin + rg);
+
   long long pos = 0;  // position within the sequence, from the cached length
   int s = 0;
   if (kAppend || !a.positions) {
@@ -104,23 +122,13 @@ __global__ void __launch_bounds__(kRopeThreads) qk_rope_kernel(const RopeArgs a,
     }
   }
 
-  const int heads = a.hq + a.hkv + (kAppend ? a.hkv : 0);
-  const int h_begin = (int)(w % splits) * per_warp * R, h_end = min(heads, h_begin + per_warp * R);
   for (int h0 = h_begin; h0 < h_end; h0 += R) {
     const int h = h0 + rg;
     const bool on = h < h_end;
     const bool is_q = h < a.hq, is_v = kAppend && h >= a.hq + a.hkv;
     const int g = is_q ? h : is_v ? h - a.hq - a.hkv : h - a.hq;
-    const T* src = is_q ? static_cast<const T*>(a.q) + t * a.q_stride
-                 : is_v ? static_cast<const T*>(a.v) + t * a.v_stride
-                        : static_cast<const T*>(a.k) + t * a.k_stride;
-    const uint4* in = reinterpret_cast<const uint4*>(src + (long long)g * D);
-    uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
-    if (on) {
-      v0 = in[c0];
-      v1 = in[c1];
-    }
-    const T* wt = static_cast<const T*>(is_q ? a.q_weight : a.k_weight);
+    uint4 v0 = n0, v1 = n1;
+    load(h + R);
     float x0[E], x1[E];
     unpack16<T>(v0, x0);
     unpack16<T>(v1, x1);
@@ -129,6 +137,7 @@ __global__ void __launch_bounds__(kRopeThreads) qk_rope_kernel(const RopeArgs a,
     for (int e = 0; e < E; ++e) ss += x0[e] * x0[e] + x1[e] * x1[e];
 #pragma unroll
     for (int o = 1; o < L; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const T* wt = static_cast<const T*>(is_q ? a.q_weight : a.k_weight);
     if (!is_v) {
       if (wt) {
         const float r = rsqrtf(ss * (1.f / D) + a.eps);
@@ -188,13 +197,15 @@ cudaError_t launch_t(RopeArgs a, cudaStream_t st) {
   a.pairs = a.half / S::kPer16;
   const int heads = a.hq + a.hkv + (a.k_cache ? a.hkv : 0);
   const int blocks = (heads + S::kRows - 1) / S::kRows;
-  const int per_warp = blocks, splits = 1;
-  const long long warps = (long long)a.total_rows * splits;
-  const long long grid = (warps * 32 + kRopeThreads - 1) / kRopeThreads;
-  if (grid >= (1ll << 31)) return cudaErrorInvalidValue;
-  if (a.k_cache)
-    return launch_pdl(qk_rope_kernel<T, D, true>, dim3((unsigned)grid), dim3(kRopeThreads), 0, st, a, per_warp, splits);
-  return launch_pdl(qk_rope_kernel<T, D, false>, dim3((unsigned)grid), dim3(kRopeThreads), 0, st, a, per_warp, splits);
+  // One warp per token does a token's angles once; with fewer tokens than warps
+  // that fill the GPU (152 SMs x 32), a token's blocks are shared out over more.
+  const int splits = std::min<long long>(blocks, (152 * 32 + a.total_rows - 1) / a.total_rows);
+  const int per_warp = (blocks + splits - 1) / splits;
+  const dim3 grid((unsigned)(((long long)a.total_rows * 32 + kRopeThreads - 1) / kRopeThreads),
+                  (unsigned)((blocks + per_warp - 1) / per_warp));
+  if (grid.y > 65535) return cudaErrorInvalidValue;
+  if (a.k_cache) return launch_pdl(qk_rope_kernel<T, D, true>, grid, dim3(kRopeThreads), 0, st, a, per_warp);
+  return launch_pdl(qk_rope_kernel<T, D, false>, grid, dim3(kRopeThreads), 0, st, a, per_warp);
 }
 
 }  // namespace
