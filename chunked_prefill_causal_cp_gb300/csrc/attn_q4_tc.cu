@@ -85,7 +85,7 @@ struct Q4Smem {
   static constexpr uint32_t v_off = k_off + kStages * DB * kBlockBytes;
   static constexpr uint32_t bar_off = v_off + kStages * DB * kBlockBytes;
   static constexpr uint32_t raw_off = bar_off + sizeof(Q4Barriers);  // codes and parameters on their way (see Conv)
-  static constexpr uint32_t raw_bytes = 2u * ((128 * D / 32 + kConvThreads - 1) / kConvThreads) * kConvThreads * 20u;
+  static constexpr uint32_t raw_bytes = 2u * ((4 * D / 32 + kConvWarps - 1) / kConvWarps) * kConvThreads * 20u;
   static constexpr uint32_t alloc = raw_off + raw_bytes + 1024;  // slack for 1024-byte alignment
   static_assert(alloc <= 232448, "one CTA's shared memory");
   // After the main loop the K stages hold the outgoing part, the V stages the
@@ -172,19 +172,22 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A thread's share of a tile of K or V: groups of 32 channels, thread ct taking
-// groups ct, ct + kConvThreads, ... of the tile's 128 keys x D / 32.  The codes pass through
-// slots of shared memory that only this thread writes and reads, so a copy needs
-// no barrier, and no registers while it is in flight.
+// A warp's share of a tile of K or V: blocks of 32 groups of 32 channels -- kKeys
+// keys, lane kKeys j + k taking group j of the block's key k -- warp cw taking
+// blocks cw, cw + kConvWarps, ....  The codes pass through slots of shared memory
+// that only their own thread writes and reads, so a copy needs no barrier, and no
+// registers while it is in flight.
 template <typename T, int D>
 struct Conv {
   static constexpr int kGroups = D / 32;
-  static constexpr int kItems = 128 * kGroups;
-  static constexpr int kPer = (kItems + kConvThreads - 1) / kConvThreads;
+  static constexpr int kKeys = 32 / kGroups;
+  static constexpr int kBlocks = 128 / kKeys;
+  static constexpr int kPer = (kBlocks + kConvWarps - 1) / kConvWarps;
   struct Slots {
     uint4 w[kPer][kConvThreads];
     uint32_t p[kPer][kConvThreads];
   };
+  static_assert(sizeof(Slots) * 2 == Q4Smem<D>::raw_bytes, "the slots' place");
 
   // Cache row of the tile's first key (contiguous), or of each of its pages in
   // lane's turn (-1: a bad page, or none).
@@ -197,16 +200,17 @@ struct Conv {
     return row;
   }
 
-  // Starts the copies of keys j0 + (item / kGroups) < n; others become zeros.
+  // Starts the copies of keys j0 + ... < n; others become zeros.
   static __device__ __forceinline__ void load(const Q4AttnArgs& a, const uint8_t* codes, const uint32_t* params,
-                                              long long rows, int j0, int n, int ct, Slots& x) {
+                                              long long rows, int j0, int n, int cw, Slots& x) {
     const bool paged = a.cache.kind == CP_CACHE_PAGED;
     const int lps = 31 - __clz(a.cache.page_size | 1);
+    const int lane = threadIdx.x & 31, grp = lane / kKeys;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int item = ct + i * kConvThreads;
-      if (kItems % kConvThreads != 0 && item >= kItems) break;  // whole warps
-      const int key = item / kGroups, grp = item % kGroups;
+      const int blk = cw + i * kConvWarps;
+      if (kBlocks % kConvWarps != 0 && blk >= kBlocks) break;  // whole warps
+      const int key = blk * kKeys + lane % kKeys;
       long long row = rows + key;
       bool on = j0 + key < n;
       if (paged) {
@@ -215,34 +219,29 @@ struct Conv {
         on = on && page_row >= 0;
       }
       if (!on) row = 0;
-      cp_async16(&x.w[i][ct], codes + row * (D / 2) + grp * 16, on);
-      cp_async4(&x.p[i][ct], params + row * kGroups + grp, on);
+      cp_async16(&x.w[i][cw * 32 + lane], codes + row * (D / 2) + grp * 16, on);
+      cp_async4(&x.p[i][cw * 32 + lane], params + row * kGroups + grp, on);
     }
     cp_async_commit();
   }
 
   // The values into a stage: key row of 128 bytes in 64-channel block grp / 2,
-  // 16-byte chunks XOR-swizzled by key mod 8.  Groups of the second block store
-  // their chunks in another order, so the eight threads of a store phase (two keys,
-  // four groups) fall on distinct banks.
-  static __device__ __forceinline__ void store(const Slots& from, uint8_t* stage, int ct, uint32_t magic) {
+  // 16-byte chunks XOR-swizzled by key mod 8: the eight threads of a store phase
+  // hold the same chunk of eight keys, on distinct banks.
+  static __device__ __forceinline__ void store(const Slots& from, uint8_t* stage, int cw, uint32_t magic) {
+    const int lane = threadIdx.x & 31, grp = lane / kKeys, k = lane % kKeys;
+    uint8_t* at = stage + (grp >> 1) * kBlockBytes + (cw * kKeys + k) * 128;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int item = ct + i * kConvThreads;
-      if (kItems % kConvThreads != 0 && item >= kItems) break;
-      const int key = item / kGroups, grp = item % kGroups;
-      const uint4 w = from.w[i][ct];
-      const uint32_t s2 = q4_scale2(from.p[i][ct]), m2 = q4_low2(from.p[i][ct]);
-      const bool second = grp >> 1;
-      uint8_t* row = stage + (grp >> 1) * kBlockBytes + key * 128;
-      const uint32_t x[4] = {second ? w.z : w.x, second ? w.w : w.y, second ? w.x : w.z, second ? w.y : w.w};
-      const int c0 = (grp & 1) * 4;
+      if (kBlocks % kConvWarps != 0 && cw + i * kConvWarps >= kBlocks) break;
+      const uint4 w = from.w[i][cw * 32 + lane];
+      const uint32_t p = from.p[i][cw * 32 + lane];
+      const uint32_t s2 = q4_scale2(p), m2 = q4_low2(p), x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int chunk = c0 + (k ^ (second ? 2 : 0));
-        const uint4 v = make_uint4(q4_pair<T>(x[k], s2, m2, magic), q4_pair<T>(x[k] >> 4, s2, m2, magic),
-                                   q4_pair<T>(x[k] >> 8, s2, m2, magic), q4_pair<T>(x[k] >> 12, s2, m2, magic));
-        *reinterpret_cast<uint4*>(row + ((chunk ^ (key & 7)) * 16)) = v;
+      for (int c = 0; c < 4; ++c) {
+        const uint4 v = make_uint4(q4_pair<T>(x[c], s2, m2, magic), q4_pair<T>(x[c] >> 4, s2, m2, magic),
+                                   q4_pair<T>(x[c] >> 8, s2, m2, magic), q4_pair<T>(x[c] >> 12, s2, m2, magic));
+        *reinterpret_cast<uint4*>(at + i * (kConvWarps * kKeys * 128) + ((((grp & 1) * 4 + c) ^ (k & 7)) * 16)) = v;
       }
     }
   }
@@ -351,9 +350,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int db = 0; db < DB; ++db)
           tma_load_3d(sQ + (w * DB + db) * kBlockBytes, &tm_q, &bar->q_full[w], db * 64, g * G, row0 + t0 + w * rpt);
       }
-    // The tile's groups do not divide evenly: the warps that take one more of K are not those of V.
+    // The tile's blocks do not divide evenly: the warps that take one more of K are not those of V.
     const int cw = warp == 0 ? 0 : warp - 1;
-    const int ck = cw * 32 + lane, cv = (cw + 5) % kConvWarps * 32 + lane;
+    const int ck = cw, cv = (cw + 5) % kConvWarps;
     using C = Conv<T, D>;
     const uint32_t magic = q4_magic<T>();
     auto* raw = reinterpret_cast<typename C::Slots*>(smem + L::raw_off);  // K's and V's
