@@ -11,6 +11,7 @@
 // in fp32 (c s is exact) rounded once.  Both are bound by bytes.
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "cp_q4.cuh"
 #include "cp_q4.h"
@@ -33,57 +34,110 @@ __device__ __forceinline__ uint16_t bits_rz<__half>(float x) {
   return __half_as_ushort(__float2half_rz(x));
 }
 
+// Two fp32 operations in one instruction, each rounded as alone.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 d, a, b;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
+// min and max of two pairs of 16-bit elements; a NaN stays.
+template <typename T>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  typedef typename Two<T>::type V;
+  const V r = __hmin2_nan(*reinterpret_cast<V*>(&a), *reinterpret_cast<V*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  typedef typename Two<T>::type V;
+  const V r = __hmax2_nan(*reinterpret_cast<V*>(&a), *reinterpret_cast<V*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 // Codes of a lane's 8 channels (a word) and its group's params, from all four
 // lanes of the group.
 template <typename T>
 __device__ __forceinline__ void quantize(const uint4& v, uint32_t& word, uint32_t& params) {
-  float x[8];
-  unpack16<T>(v, x);
-  float lo = x[0], hi = x[0], bad = 0.f;  // bad: NaN as soon as a value is not finite
+  // Smallest and largest in 16 bits, the largest as the smallest of the negated: (lo, -hi) in one word.
+  const uint32_t mn = min2<T>(min2<T>(v.x, v.y), min2<T>(v.z, v.w));
+  const uint32_t mx = max2<T>(max2<T>(v.x, v.y), max2<T>(v.z, v.w)) ^ 0x80008000u;
+  uint32_t r = min2<T>(__byte_perm(mn, mx, 0x5410), __byte_perm(mn, mx, 0x7632));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-    bad += x[i] * 0.f;
-  }
-#pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    bad += __shfl_xor_sync(0xffffffffu, bad, o);
-  }
-  const float range = __fadd_rn(hi, -lo);
-  uint16_t sb = bits_rz<T>(__fdiv_rn(range, 15.f));
-  if (!(range <= 3.402823466e38f) || bad != bad) sb = 0x7fffu;  // NaN in both types
-  float m2[2] = {lo, lo};
-  params = (Pack<T>::store(m2) & 0xffff0000u) | sb;
+  for (int o = 1; o < 4; o <<= 1) r = min2<T>(r, __shfl_xor_sync(0xffffffffu, r, o));
+  float ends[2];
+  Pack<T>::load(r, ends);
+  const float lo = ends[0], range = __fadd_rn(-ends[1], -lo);
+  // Quotients as IEEE division has them, in three operations: q0 = a y with y close
+  // to 1 / b, r = a - q0 b (exact: q0 is within a few units of its last place),
+  // q1 = q0 + r y.  Before its rounding q1 is within 2^-18 of a unit of a / b, and
+  // with b of at most 11 significant bits a / b is never within 2^-12 of a unit
+  // of a point halfway between two floats, so q1 rounds as a / b does.
+  float step = __fmul_rn(range, 1.f / 15.f);
+  step = __fmaf_rn(__fmaf_rn(-step, 15.f, range), 1.f / 15.f, step);
+  if (!(range >= 0x1p-80f)) step = __fdiv_rn(range, 15.f);  // (a remainder could underflow)
+  uint32_t sb = bits_rz<T>(step);
+  if (!(range <= 3.402823466e38f)) sb = 0x7fffu;  // NaN in both types
+  params = (r << 16) | sb;
   float s2[2];
   Pack<T>::load(sb, s2);
   const float s = s2[0];
   word = 0;
   if (!(s > 0.f)) return;
-  // The quotient's rounding decides a code only near a half: a product with the
-  // reciprocal is within 2^-22 of it (two roundings of up to 2^4), so anything
-  // further than 2^-20 from a half rounds alike, and the rest divides.  Adding
-  // 1.5 * 2^23 rounds to a whole number, ties to even, in the low bits.
-  const float inv = __fdiv_rn(1.f, s);
-  float q[8], near = 0.f;
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(s));
+  const float2 nlo = make_float2(-lo, -lo), ns = make_float2(-s, -s), y2 = make_float2(y, y);
+  const float2 up = make_float2(12582912.f, 12582912.f), down = make_float2(-12582912.f, -12582912.f);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float2 c[4];
+  // From the type's smallest normal scale on, a quotient is at most 15 (1 + 2^-7), so rounds to 15 at most.
+  if (s >= (std::is_same<T, __half>::value ? 0x1p-14f : 0x1p-80f) && s <= 0x1p100f) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    q[i] = __fmul_rn(__fadd_rn(x[i], -lo), inv);
-    const float r = __fadd_rn(__fadd_rn(q[i], 12582912.f), -12582912.f);
-    near = fmaxf(near, fabsf(__fadd_rn(q[i], -r)));
-  }
-  if (!(near < 0.5f - 0x1p-20f) || !(inv < INFINITY)) {
+    for (int i = 0; i < 4; ++i) {
+      float x[2];
+      Pack<T>::load(w[i], x);
+      const float2 d = add2(make_float2(x[0], x[1]), nlo);
+      float2 q = mul2(d, y2);
+      q = fma2(fma2(q, ns, d), y2, q);
+      c[i] = add2(add2(q, up), down);  // to a whole number, ties to even
+    }
+  } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(__fadd_rn(x[i], -lo), s);
+    for (int i = 0; i < 4; ++i) {
+      float x[2];
+      Pack<T>::load(w[i], x);
+      c[i].x = fminf(rintf(__fdiv_rn(__fadd_rn(x[0], -lo), s)), 15.f);
+      c[i].y = fminf(rintf(__fdiv_rn(__fadd_rn(x[1], -lo), s)), 15.f);
+    }
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t c = __float_as_uint(__fadd_rn(fminf(q[i], 15.f), 12582912.f)) & 15u;
-    word |= c << (4 * (i >> 1) + 16 * (i & 1));
-  }
+  // Even and odd channels' codes as two whole numbers below 2^16.
+  const float2 k16 = make_float2(16.f, 16.f);
+  float2 h = fma2(c[3], k16, c[2]);
+  h = fma2(h, k16, c[1]);
+  h = fma2(h, k16, c[0]);
+  h = add2(h, make_float2(8388608.f, 8388608.f));
+  word = __byte_perm(__float_as_uint(h.x), __float_as_uint(h.y), 0x5410);
 }
+
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(const Q4Args a) {
@@ -92,13 +146,13 @@ __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(const Q4Args a) {
   pdl_wait();
   if (a.past_snapshot && blockIdx.x == 0)
     for (int s = threadIdx.x; s < a.rows.num_seqs; s += kQ4Threads) a.past_snapshot[s] = a.past[s];
-  const uint32_t row = blockIdx.x * (uint32_t)(kQ4Threads / V) + threadIdx.x / V;  // at most INT32_MAX + a block's
+  const uint32_t row = blockIdx.x * (uint32_t)(kQ4Threads / V) + threadIdx.x / V;  // at most INT32_MAX + a CTA's
   const int c = threadIdx.x % V;
   const bool on = row < (uint32_t)a.total_rows * (uint32_t)a.hkv;
   uint4 kv = make_uint4(0, 0, 0, 0), vv = kv;
   if (on) {
-    kv = static_cast<const uint4*>(a.k_new)[(long long)row * V + c];
-    vv = static_cast<const uint4*>(a.v_new)[(long long)row * V + c];
+    kv = __ldg(static_cast<const uint4*>(a.k_new) + (long long)row * V + c);
+    vv = __ldg(static_cast<const uint4*>(a.v_new) + (long long)row * V + c);
   }
   uint32_t kw, kp, vw, vp;
   quantize<T>(kv, kw, kp);  // shuffles: every lane takes part
@@ -141,17 +195,24 @@ __global__ void __launch_bounds__(kQ4Threads) q4_read_kernel(const Q4Args a) {
     if (a.status && c == 0) atomicOr(a.status, CP_DEV_BOUNDS);
     return;
   }
-  if (a.k_out)
-    static_cast<uint4*>(a.k_out)[(long long)row * V + c] =
-        dequantize<T>(reinterpret_cast<const uint32_t*>(a.k_codes)[src * V + c], a.k_params[src * (V / 4) + c / 4], q4_magic<T>());
-  if (a.v_out)
-    static_cast<uint4*>(a.v_out)[(long long)row * V + c] =
-        dequantize<T>(reinterpret_cast<const uint32_t*>(a.v_codes)[src * V + c], a.v_params[src * (V / 4) + c / 4], q4_magic<T>());
+  const uint32_t magic = q4_magic<T>();
+  uint32_t kw = 0, kp = 0, vw = 0, vp = 0;  // every load before the first use
+  if (a.k_out) {
+    kw = reinterpret_cast<const uint32_t*>(a.k_codes)[src * V + c];
+    kp = a.k_params[src * (V / 4) + c / 4];
+  }
+  if (a.v_out) {
+    vw = reinterpret_cast<const uint32_t*>(a.v_codes)[src * V + c];
+    vp = a.v_params[src * (V / 4) + c / 4];
+  }
+  if (a.k_out) static_cast<uint4*>(a.k_out)[(long long)row * V + c] = dequantize<T>(kw, kp, magic);
+  if (a.v_out) static_cast<uint4*>(a.v_out)[(long long)row * V + c] = dequantize<T>(vw, vp, magic);
 }
 
+// `lanes`: threads of a row.
 template <typename K>
-cudaError_t launch_rows(K kernel, const Q4Args& a, int d, cudaStream_t st) {
-  const long long rows = (long long)a.total_rows * a.hkv, per = kQ4Threads / (d / 8);
+cudaError_t launch_rows(K kernel, const Q4Args& a, int lanes, cudaStream_t st) {
+  const long long rows = (long long)a.total_rows * a.hkv, per = kQ4Threads / lanes;
   if (rows == 0) return cudaSuccess;
   if (rows > INT32_MAX) return cudaErrorInvalidValue;
   const long long grid = (rows + per - 1) / per;
@@ -162,18 +223,18 @@ cudaError_t launch_rows(K kernel, const Q4Args& a, int d, cudaStream_t st) {
 
 cudaError_t launch_q4_append(const Q4Args& a, int dtype, int d, cudaStream_t st) {
   if (dtype == CP_BF16)
-    return d == 64 ? launch_rows(q4_append_kernel<__nv_bfloat16, 64>, a, d, st)
-                   : launch_rows(q4_append_kernel<__nv_bfloat16, 128>, a, d, st);
-  return d == 64 ? launch_rows(q4_append_kernel<__half, 64>, a, d, st)
-                 : launch_rows(q4_append_kernel<__half, 128>, a, d, st);
+    return d == 64 ? launch_rows(q4_append_kernel<__nv_bfloat16, 64>, a, 8, st)
+                   : launch_rows(q4_append_kernel<__nv_bfloat16, 128>, a, 16, st);
+  return d == 64 ? launch_rows(q4_append_kernel<__half, 64>, a, 8, st)
+                 : launch_rows(q4_append_kernel<__half, 128>, a, 16, st);
 }
 
 cudaError_t launch_q4_read(const Q4Args& a, int dtype, int d, cudaStream_t st) {
   if (dtype == CP_BF16)
-    return d == 64 ? launch_rows(q4_read_kernel<__nv_bfloat16, 64>, a, d, st)
-                   : launch_rows(q4_read_kernel<__nv_bfloat16, 128>, a, d, st);
-  return d == 64 ? launch_rows(q4_read_kernel<__half, 64>, a, d, st)
-                 : launch_rows(q4_read_kernel<__half, 128>, a, d, st);
+    return d == 64 ? launch_rows(q4_read_kernel<__nv_bfloat16, 64>, a, 8, st)
+                   : launch_rows(q4_read_kernel<__nv_bfloat16, 128>, a, 16, st);
+  return d == 64 ? launch_rows(q4_read_kernel<__half, 64>, a, 8, st)
+                 : launch_rows(q4_read_kernel<__half, 128>, a, 16, st);
 }
 
 }  // namespace cp
