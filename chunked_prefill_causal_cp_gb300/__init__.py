@@ -302,18 +302,13 @@ def _on(dev, stream):
 
 
 def _arg(where, t, dtype, numel, dev):
-    """Pointer of a dense tensor of `dtype` on `dev` with at least `numel` elements (raw handles pass)."""
-    if isinstance(t, torch.Tensor):
-        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() >= numel:
-            return t.data_ptr()
-    elif isinstance(t, int):
+    """Pointer of a dense tensor of `dtype` on `dev` with at least `numel` elements.  None (which the library
+    refuses where it may not be) and raw handles pass."""
+    if t is None or isinstance(t, int):
         return t
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() >= numel:
+        return t.data_ptr()
     _refuse(where)
-
-
-def _opt(where, t, dtype, numel, dev):
-    """The same, or None."""
-    return None if t is None else _arg(where, t, dtype, numel, dev)
 
 
 _LAYER_DTYPE = {code: dtype for dtype, code in DTYPE_CODE.items()}
@@ -387,8 +382,8 @@ def _q4_arg(where, desc, cache, dev):
 
 
 def _seq_args(where, desc, lens, cu_rows, block_table, num_seqs, dev):
-    return (_arg(where, lens, torch.int32, num_seqs, dev), _opt(where, cu_rows, torch.int32, num_seqs + 1, dev),
-            _opt(where, block_table, torch.int32, num_seqs * desc.max_blocks, dev))
+    return (_arg(where, lens, torch.int32, num_seqs, dev), _arg(where, cu_rows, torch.int32, num_seqs + 1, dev),
+            _arg(where, block_table, torch.int32, num_seqs * desc.max_blocks, dev))
 
 
 def cp_qk_norm_rope(desc, prep, q, k, q_out, k_out, num_seqs, total_rows, q_weight=None, k_weight=None, inv_freq=None,
@@ -401,11 +396,11 @@ def cp_qk_norm_rope(desc, prep, q, k, q_out, k_out, num_seqs, total_rows, q_weig
     pq, sq = _rows_arg(w, q, desc, hq, total_rows, dev)
     pk, sk = _rows_arg(w, k, desc, hkv, total_rows, dev)
     s = lib().cp_qk_norm_rope(
-        ctypes.byref(desc), ctypes.byref(prep), pq, sq, pk, sk, _opt(w, q_weight, dt, d, dev),
-        _opt(w, k_weight, dt, d, dev), _opt(w, inv_freq, torch.float32, prep.rot_dim // 2, dev),
-        _opt(w, positions, i32, total_rows, dev), _opt(w, seqlens_k, i32, num_seqs, dev),
-        _opt(w, cu_rows, i32, num_seqs + 1, dev), num_seqs, total_rows, _opt(w, q_out, dt, total_rows * hq * d, dev),
-        _opt(w, k_out, dt, total_rows * hkv * d, dev), _on(dev, stream))
+        ctypes.byref(desc), ctypes.byref(prep), pq, sq, pk, sk, _arg(w, q_weight, dt, d, dev),
+        _arg(w, k_weight, dt, d, dev), _arg(w, inv_freq, torch.float32, prep.rot_dim // 2, dev),
+        _arg(w, positions, i32, total_rows, dev), _arg(w, seqlens_k, i32, num_seqs, dev),
+        _arg(w, cu_rows, i32, num_seqs + 1, dev), num_seqs, total_rows, _arg(w, q_out, dt, total_rows * hq * d, dev),
+        _arg(w, k_out, dt, total_rows * hkv * d, dev), _on(dev, stream))
     _check(s, w)
 
 
@@ -422,11 +417,11 @@ def cp_qk_norm_rope_append(desc, prep, q, k_new, v_new, q_out, k_cache, v_cache,
     size = (desc.num_pages * desc.page_size if desc.kind == CP_CACHE_PAGED else desc.batch * desc.capacity) * hkv * d
     lens, cu, table = _seq_args(w, desc, seqlens_k, cu_rows, block_table, num_seqs, dev)
     s = lib().cp_qk_norm_rope_append(
-        ctypes.byref(desc), ctypes.byref(prep), pq, sq, pk, sk, pv, sv, _opt(w, q_weight, dt, d, dev),
-        _opt(w, k_weight, dt, d, dev), _opt(w, inv_freq, torch.float32, prep.rot_dim // 2, dev),
-        _opt(w, positions, i32, total_rows, dev), cu, num_seqs, total_rows, _arg(w, q_out, dt, total_rows * hq * d, dev),
+        ctypes.byref(desc), ctypes.byref(prep), pq, sq, pk, sk, pv, sv, _arg(w, q_weight, dt, d, dev),
+        _arg(w, k_weight, dt, d, dev), _arg(w, inv_freq, torch.float32, prep.rot_dim // 2, dev),
+        _arg(w, positions, i32, total_rows, dev), cu, num_seqs, total_rows, _arg(w, q_out, dt, total_rows * hq * d, dev),
         _arg(w, k_cache, dt, size, dev), _arg(w, v_cache, dt, size, dev), lens, table, max_ctx,
-        _opt(w, dev_status, i32, 1, dev), _on(dev, stream))
+        _arg(w, dev_status, i32, 1, dev), _on(dev, stream))
     _check(s, w)
 
 
@@ -438,7 +433,7 @@ def cp_kv_append_q4(desc, k_new, v_new, cache, seqlens_k, num_seqs, total_rows, 
     lens, cu, table = _seq_args(w, desc, seqlens_k, cu_rows, block_table, num_seqs, dev)
     s = lib().cp_kv_append_q4(ctypes.byref(desc), _arg(w, k_new, dt, n, dev), _arg(w, v_new, dt, n, dev), cu, num_seqs,
                               total_rows, _q4_arg(w, desc, cache, dev), lens, table, max_ctx,
-                              _opt(w, dev_status, torch.int32, 1, dev), _on(dev, stream))
+                              _arg(w, dev_status, torch.int32, 1, dev), _on(dev, stream))
     _check(s, w)
 
 
@@ -449,8 +444,8 @@ def cp_kv_read_q4(desc, cache, starts, num_seqs, total_rows, max_ctx, k_out, v_o
     dev = _device(w, starts)
     lens, cu, table = _seq_args(w, desc, starts, cu_rows, block_table, num_seqs, dev)
     s = lib().cp_kv_read_q4(ctypes.byref(desc), _q4_arg(w, desc, cache, dev), lens, table, cu, num_seqs, total_rows,
-                            max_ctx, _opt(w, k_out, dt, n, dev), _opt(w, v_out, dt, n, dev),
-                            _opt(w, dev_status, torch.int32, 1, dev), _on(dev, stream))
+                            max_ctx, _arg(w, k_out, dt, n, dev), _arg(w, v_out, dt, n, dev),
+                            _arg(w, dev_status, torch.int32, 1, dev), _on(dev, stream))
     _check(s, w)
 
 
@@ -463,7 +458,7 @@ def cp_chunk_attn_q4(desc, q, cache, seqlens_k, num_seqs, total_rows, max_ctx, o
     lens, cu, table = _seq_args(w, desc, seqlens_k, cu_rows, block_table, num_seqs, dev)
     s = lib().cp_chunk_attn_q4(ctypes.byref(desc), _arg(w, q, dt, n, dev), _q4_arg(w, desc, cache, dev), lens, table,
                                cu, num_seqs, total_rows, max_ctx, _arg(w, out, dt, n, dev), ws, ws_bytes,
-                               1 if commit else 0, _opt(w, dev_status, torch.int32, 1, dev), _on(dev, stream))
+                               1 if commit else 0, _arg(w, dev_status, torch.int32, 1, dev), _on(dev, stream))
     _check(s, w)
 
 
@@ -478,7 +473,7 @@ def cp_mixed_step_q4(desc, q, k_new, v_new, cache, seqlens_k, num_seqs, total_ro
     s = lib().cp_mixed_step_q4(ctypes.byref(desc), _arg(w, q, dt, nq, dev), _arg(w, k_new, dt, nk, dev),
                                _arg(w, v_new, dt, nk, dev), _q4_arg(w, desc, cache, dev), table, cu, lens, num_seqs,
                                total_rows, max_ctx, _arg(w, out, dt, nq, dev), ws, ws_bytes, 1 if commit else 0,
-                               _opt(w, dev_status, torch.int32, 1, dev), _on(dev, stream))
+                               _arg(w, dev_status, torch.int32, 1, dev), _on(dev, stream))
     _check(s, w)
 
 

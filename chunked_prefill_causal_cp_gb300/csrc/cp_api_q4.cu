@@ -183,9 +183,10 @@ int q4_attn_check(const cp_layer_desc* d, const void* q, const cp_q4_cache* c, c
   if (!q || !out || !seqlens_k || !aligned16(q) || !aligned16(out)) return CP_ERR_INVALID_ARG;
   r = cache_check(d, *rows, total_rows, block_table, max_ctx);
   if (r != CP_OK) return r;
+  if (max_ctx > INT32_MAX - 4096) return CP_ERR_UNSUPPORTED;  // key indices run past the context by up to a split
   *plan = q4_plan(d, cu_rows != nullptr, num_seqs, total_rows, max_ctx);
   if (d->num_q_heads > 65535 || (int64_t)num_seqs * plan->max_splits > INT32_MAX ||
-      (int64_t)num_seqs * plan->dec_rows > INT32_MAX || 2 * plan->pairs > INT32_MAX)
+      (double)num_seqs * plan->dec_rows * d->num_q_heads > INT32_MAX || 2 * plan->pairs > INT32_MAX)
     return CP_ERR_UNSUPPORTED;
   const size_t need = cp_workspace_size_q4(d, total_rows, max_ctx, num_seqs);
   if (!workspace || !aligned16(workspace) || workspace_bytes < need) return CP_ERR_WORKSPACE;

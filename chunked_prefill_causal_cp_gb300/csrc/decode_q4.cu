@@ -383,61 +383,75 @@ __global__ void __launch_bounds__(kWarps * 32, NF == 1 ? 4 : D == 64 ? 4 : 3) q4
   }
 }
 
-// A row's splits merged: eight split slices times D / 4 four-channel columns, each slice in split order, then
-// the slices in order.
+// A row's splits merged.  A (row, head) belongs to kSlices groups of D / 4
+// threads, a thread four channels: each group merges every kSlices-th split in
+// order, then the groups' results are merged in order.  Eight groups, whatever the
+// number of splits, so that the order is a row's own (with four, the merge of 98
+// splits took 6 us longer, that of 9 as long).
+constexpr int kCombineThreads = 256, kSlices = 8;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(8 * D / 4) q4_combine_kernel(const Q4AttnArgs a) {
-  constexpr int C4 = D / 4;
-  __shared__ float4 so[8][C4];
-  __shared__ float sm[8], sl[8];
+__global__ void __launch_bounds__(kCombineThreads) q4_combine_kernel(const Q4AttnArgs a) {
+  constexpr int C4 = D / 4, kPer = kCombineThreads / (C4 * kSlices);  // (row, head) pairs of a CTA
+  __shared__ float4 so[kPer][kSlices][C4];
+  __shared__ float sm[kPer][kSlices], sl[kPer][kSlices];
   pdl_launch_dependents();
   pdl_wait();
   const int kr = a.dec_rows;
-  const int s = blockIdx.x / kr, r = blockIdx.x % kr, h = blockIdx.y;
-  if (seq_rows(a.rows, s) != kr) return;
-  const int past = a.past[s], row0 = seq_row0(a.rows, s);
-  if (past < 0 || (long long)past + kr > a.max_ctx || row0 < 0 || row0 > a.total_rows - kr) return;
-  const int nsplit = q4_splits(past + kr);  // the last may hold keys of later rows only: a part of weight 0
-  if (nsplit == 1) return;                  // finished by the split kernel
-  const int slice = threadIdx.x / C4, d4 = threadIdx.x % C4;
-  const long long base = (((long long)s * kr + r) * a.hq + h) * a.max_splits;
+  const int d4 = threadIdx.x % C4, slice = threadIdx.x / C4 % kSlices, pair = threadIdx.x / (C4 * kSlices);
+  const long long id = (long long)blockIdx.x * kPer + pair;  // (sequence, row, head)
+  const long long sr = id / a.hq;
+  const int h = (int)(id % a.hq), s = (int)(sr / kr), r = (int)(sr % kr);
+  bool on = s < a.rows.num_seqs && seq_rows(a.rows, s) == kr;
+  int past = 0, row0 = 0, nsplit = 0;
+  if (on) {
+    past = a.past[s];
+    row0 = seq_row0(a.rows, s);
+    on = past >= 0 && (long long)past + kr <= a.max_ctx && row0 >= 0 && row0 <= a.total_rows - kr;
+    if (on) nsplit = q4_splits(past + kr);  // the last may hold keys of later rows only: a part of weight 0
+    on = on && nsplit > 1;                  // one split: finished by the split kernel
+  }
   float m = -INFINITY, l = 0.f;
   float v[4] = {0.f, 0.f, 0.f, 0.f};
+  if (on) {
+    const long long base = id * a.max_splits;
 #pragma unroll 4
-  for (int i = slice; i < nsplit; i += 8) {
-    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (base + i) * 2);
-    const float4 p = *reinterpret_cast<const float4*>(a.part_o + (base + i) * D + 4 * d4);
-    const float mn = fmaxf(m, ml.x), z = mn == -INFINITY ? 0.f : mn;
-    const float k0 = ex2_approx(m - z), k1 = ex2_approx(ml.x - z);
-    v[0] = v[0] * k0 + p.x * k1;
-    v[1] = v[1] * k0 + p.y * k1;
-    v[2] = v[2] * k0 + p.z * k1;
-    v[3] = v[3] * k0 + p.w * k1;
-    l = l * k0 + ml.y * k1;
-    m = mn;
+    for (int i = slice; i < nsplit; i += kSlices) {
+      const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (base + i) * 2);
+      const float4 p = *reinterpret_cast<const float4*>(a.part_o + (base + i) * D + 4 * d4);
+      const float mn = fmaxf(m, ml.x), z = mn == -INFINITY ? 0.f : mn;
+      const float k0 = ex2_approx(m - z), k1 = ex2_approx(ml.x - z);
+      v[0] = v[0] * k0 + p.x * k1;
+      v[1] = v[1] * k0 + p.y * k1;
+      v[2] = v[2] * k0 + p.z * k1;
+      v[3] = v[3] * k0 + p.w * k1;
+      l = l * k0 + ml.y * k1;
+      m = mn;
+    }
   }
-  so[slice][d4] = make_float4(v[0], v[1], v[2], v[3]);
+  so[pair][slice][d4] = make_float4(v[0], v[1], v[2], v[3]);
   if (d4 == 0) {
-    sm[slice] = m;
-    sl[slice] = l;
+    sm[pair][slice] = m;
+    sl[pair][slice] = l;
   }
   __syncthreads();
   if (slice != 0) return;
   m = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, sm[i]);
+  for (int i = 0; i < kSlices; ++i) m = fmaxf(m, sm[pair][i]);
   const float z = m == -INFINITY ? 0.f : m;
   l = v[0] = v[1] = v[2] = v[3] = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float k = ex2_approx(sm[i] - z);
-    const float4 p = so[i][d4];
+  for (int i = 0; i < kSlices; ++i) {
+    const float k = ex2_approx(sm[pair][i] - z);
+    const float4 p = so[pair][i][d4];
     v[0] = fmaf(k, p.x, v[0]);
     v[1] = fmaf(k, p.y, v[1]);
     v[2] = fmaf(k, p.z, v[2]);
     v[3] = fmaf(k, p.w, v[3]);
-    l = fmaf(k, sl[i], l);
+    l = fmaf(k, sl[pair][i], l);
   }
+  if (!on) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const float o[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
   uint2 b;
@@ -452,8 +466,10 @@ cudaError_t launch_t(const Q4AttnArgs& a, cudaStream_t st) {
   cudaError_t e = a.dec_rows * a.group <= 8 ? launch_pdl(q4_split_kernel<T, D, 1>, grid, dim3(kWarps * 32), 0, st, a)
                                             : launch_pdl(q4_split_kernel<T, D, 2>, grid, dim3(kWarps * 32), 0, st, a);
   if (e != cudaSuccess || a.max_splits == 1) return e;
-  return launch_pdl(q4_combine_kernel<T, D>, dim3((unsigned)(a.rows.num_seqs * a.dec_rows), a.hq), dim3(8 * D / 4), 0,
-                    st, a);
+  constexpr int kPer = kCombineThreads / (D / 4 * kSlices);
+  const long long pairs = (long long)a.rows.num_seqs * a.dec_rows * a.hq;
+  return launch_pdl(q4_combine_kernel<T, D>, dim3((unsigned)((pairs + kPer - 1) / kPer)), dim3(kCombineThreads), 0, st,
+                    a);
 }
 
 }  // namespace

@@ -479,13 +479,15 @@ int cp_kv_read_q4(const cp_layer_desc* desc, const cp_q4_cache* cache, const int
  * Row i of sequence s is the query at position p = seqlens_k[s] + i and attends
  * to the values that positions [0, p] stand for (its own chunk's rows, appended
  * by cp_kv_append_q4, among them); otherwise as cp_prefill_chunk_attn.
- *   q, out        device [total_rows, Hq, D]
+ *   q, out        device [total_rows, Hq, D]; out must not overlap q, the
+ *                 cache or the workspace
  *   cu_rows       device int32 [num_seqs + 1], every sequence with at least one
  *                 row (one without sets CP_DEV_BOUNDS), or NULL: total_rows /
  *                 num_seqs rows each
- *   max_ctx       host bound on seqlens_k[s] + rows of s; a sequence outside it
- *                 is skipped (its rows of out are left as they were) and sets
- *                 CP_DEV_BOUNDS
+ *   max_ctx       host bound on seqlens_k[s] + rows of s, below 2^31 - 4096; a
+ *                 sequence outside it is skipped (its rows of out are left as they
+ *                 were) and sets CP_DEV_BOUNDS.  A page id out of range sets it
+ *                 too, is not read, and leaves the sequence's results unspecified
  *   workspace     device scratch, 16-byte aligned, of at least
  *                 cp_workspace_size_q4(desc, total_rows, max_ctx, num_seqs)
  *                 bytes; its contents before the call do not matter.  Calls

@@ -238,6 +238,130 @@ def test_a_row_depends_on_its_own_sequence_only():
         assert torch.equal(o, out[r0:r0 + rows[i]])
 
 
+def test_slots_past_four_billion_bytes():
+    """The last sequence's codes start more than 2^32 bytes into the cache."""
+    hq, hkv, d, n, cap = 8, 8, 128, 3, 2_900_001
+    lead = (n, hkv, cap)
+    kc, vc = (torch.empty(*lead, d // 2, dtype=torch.uint8, device="cuda") for _ in range(2))
+    kp, vp = (torch.empty(*lead, d // 32, 2, dtype=BF16, device="cuda") for _ in range(2))
+    assert kc.numel() > 2 ** 32
+    desc = cp.layer_desc(BF16, n, hq, hkv, d, capacity=cap)
+    cache = cp.q4_cache(kc, vc, kp, vp)
+    rows, past, small = [1, 40, 33], [0, 0, 0], Cache4(BF16, hq, hkv, d, n, 64)
+    for r in (rows, [1, 1, 60]):
+        t = sum(r)
+        g = torch.Generator().manual_seed(t)
+        q, k, v = (torch.randn(t, hkv, d, generator=g).bfloat16().cuda() for _ in range(3))
+        outs = []
+        for dsc, c, mc in ((desc, cache, cap), (small.desc, small.arg, 64)):
+            out, lens, st = torch.empty_like(q), _ints(past), torch.zeros(1, dtype=torch.int32, device="cuda")
+            ws = torch.empty(cp.cp_workspace_size_q4(dsc, t, mc, n), dtype=torch.uint8, device="cuda")
+            cp.cp_mixed_step_q4(dsc, q, k, v, c, lens, n, t, mc, out, ws, cu_rows=_cu(r), dev_status=st)
+            assert int(st) == 0 and lens.tolist() == r
+            outs.append(out)
+        assert torch.equal(outs[0], outs[1])
+        ko, vo = torch.empty_like(k), torch.empty_like(v)
+        cp.cp_kv_read_q4(desc, cache, _ints(past), n, t, cap, ko, vo, cu_rows=_cu(r))
+        k2, v2 = torch.empty_like(k), torch.empty_like(v)
+        cp.cp_kv_read_q4(small.desc, small.arg, _ints(past), n, t, 64, k2, v2, cu_rows=_cu(r))
+        assert torch.equal(ko, k2) and torch.equal(vo, v2)
+
+
+def _step_buffers(rows, past, seed):
+    c = Cache4(BF16, 8, 2, 128, len(rows), 700, page=32, seed=seed)
+    c.fill(past, seed=seed)
+    g = torch.Generator().manual_seed(seed)
+    q, k, v = (torch.randn(sum(rows), h, 128, generator=g).bfloat16().cuda() for h in (8, 2, 2))
+    return c, q, k, v
+
+
+def test_captured_and_replayed_and_on_another_stream():
+    """A step captured on a side stream, replayed on new inputs, equals the same steps made one by one."""
+    rows, past = [1, 30, 1, 290], [512, 0, 77, 300]
+    t, n = sum(rows), len(rows)
+    c, q, k, v = _step_buffers(rows, past, 1)
+    e, _, _, _ = _step_buffers(rows, past, 1)
+    out, ref, lens, cu = torch.empty_like(q), torch.empty_like(q), _ints(past), _cu(rows)
+    ws, ws2 = c.workspace(t, 600), c.workspace(t, 600)
+    kw = dict(cu_rows=cu, commit=False)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        cp.cp_mixed_step_q4(c.desc, q, k, v, c.arg, lens, n, t, 600, out, ws, block_table=c.table, **kw)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        cp.cp_mixed_step_q4(c.desc, q, k, v, c.arg, lens, n, t, 600, out, ws, block_table=c.table, **kw)
+    for seed in (5, 6):
+        g = torch.Generator().manual_seed(seed)
+        for x in (q, k, v):
+            x.copy_(torch.randn(x.shape, generator=g).bfloat16())
+        out.fill_(float("nan"))
+        ws.fill_(255)
+        graph.replay()
+        cp.cp_mixed_step_q4(e.desc, q, k, v, e.arg, lens, n, t, 600, ref, ws2, block_table=e.table, **kw)
+        assert torch.equal(out, ref)
+        assert torch.equal(c.kc, e.kc) and torch.equal(c.vc, e.vc)
+    check_attention(c, q, out, past, rows)
+
+
+def test_two_calls_at_once_on_two_streams():
+    rows, past = [1, 1, 200], [600, 44, 333]
+    t, n = sum(rows), len(rows)
+    sets = [_step_buffers(rows, past, s) for s in (3, 4)]
+    outs, wss = [torch.empty_like(s[1]) for s in sets], [s[0].workspace(t, 640) for s in sets]
+    lens, cu = [_ints(past), _ints(past)], _cu(rows)
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for i, (c, q, k, v) in enumerate(sets):
+            cp.cp_mixed_step_q4(c.desc, q, k, v, c.arg, lens[i], n, t, 640, outs[i], wss[i], cu_rows=cu,
+                                block_table=c.table, commit=False, stream=streams[i])
+    torch.cuda.synchronize()
+    for (c, q, _, _), out in zip(sets, outs):
+        check_attention(c, q, out, past, rows)
+
+
+def test_rows_without_a_sequence_and_a_sequence_without_rows():
+    """A listed sequence with no rows is reported; rows past the last sequence's stay as they were."""
+    c = Cache4(BF16, 4, 2, 64, 3, 64)
+    c.fill([40, 40, 40])
+    q = torch.randn(45, 4, 64, device="cuda").bfloat16()
+    out = torch.full_like(q, 3.0)
+    cp.cp_chunk_attn_q4(c.desc, q, c.arg, _ints([10, 10, 10]), 3, 45, 64, out, c.workspace(45, 64), commit=False,
+                        cu_rows=_ints([0, 20, 20, 41]), dev_status=c.status)
+    assert int(c.status) == cp.CP_DEV_BOUNDS
+    assert (out[41:] == 3.0).all()
+    check_attention(c, q[:20], out[:20], [10], [20], seqs=[0])
+    check_attention(c, q[20:41], out[20:41], [10], [21], seqs=[2])
+
+
+def test_binding_refuses_wrong_tensors():
+    c = Cache4(BF16, 4, 2, 64, 2, 64)
+    c.fill([64, 64])
+    q = torch.randn(2, 4, 64, device="cuda").bfloat16()
+    out, lens, ws = torch.empty_like(q), _ints([5, 5]), c.workspace(2, 64)
+    good = dict(q=q, cache=c.arg, lens=lens, out=out, ws=ws, desc=c.desc)
+
+    def call(**kw):
+        a = {**good, **kw}
+        cp.cp_chunk_attn_q4(a["desc"], a["q"], a["cache"], a["lens"], 2, 2, 64, a["out"], a["ws"], commit=False)
+
+    call()
+    bigger = cp.layer_desc(BF16, 3, 4, 2, 64, capacity=64)
+    halves = torch.empty(2, 4, 128, device="cuda").bfloat16()[..., :64]
+    for kw in (dict(q=q.half()), dict(q=q.cpu()), dict(q=q[:1]), dict(q=halves), dict(out=halves), dict(lens=lens.long()),
+               dict(lens=lens[:1]), dict(ws=ws[:16]), dict(desc=bigger),
+               dict(desc=cp.layer_desc(F16, 2, 4, 2, 64, capacity=64))):
+        with pytest.raises(cp.CPError):
+            call(**kw)
+    x = torch.randn(4, 4, 64, device="cuda").bfloat16()
+    kv = torch.randn(4, 2, 64, device="cuda").bfloat16()
+    for bad in (x[:1].expand(4, 4, 64), x.transpose(0, 1), x[::2], x[..., :32]):
+        with pytest.raises(cp.CPError):
+            cp.cp_qk_norm_rope(c.desc, cp.qk_prep(0), bad, kv, torch.empty_like(x), torch.empty_like(kv), 1, 4, seqlens_k=lens)
+
+
 def test_prompt_then_decode_with_norm_and_rotation():
     """The operators as they are used together: chunks of two prompts and then decode rows; every step norms and
     rotates its queries and keys, then appends and attends."""
