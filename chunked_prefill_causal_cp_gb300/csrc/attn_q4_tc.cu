@@ -73,6 +73,7 @@ struct __align__(16) Q4Barriers {
   uint64_t peer_free;      // the peer's K/V stages may receive this CTA's part
   uint32_t tmem_base;
   int abort;
+  int bad_tile[kStages];   // the last tile of the stage with a non-finite V group, of those that hide keys from a row
   __align__(16) float peer_ml[256];  // the peer's maximum [0, 128) and sum [128, 256) of this CTA's rows
   __align__(16) float out_ml[256];   // this CTA's for the peer's rows
 };
@@ -177,7 +178,7 @@ __device__ __forceinline__ void cp_async_wait() {
 // blocks cw, cw + kConvWarps, ....  The codes pass through slots of shared memory
 // that only their own thread writes and reads, so a copy needs no barrier, and no
 // registers while it is in flight.
-template <typename T, int D>
+template <typename T, int D, bool kPaged>
 struct Conv {
   static constexpr int kGroups = D / 32;
   static constexpr int kKeys = 32 / kGroups;
@@ -189,53 +190,63 @@ struct Conv {
   };
   static_assert(sizeof(Slots) * 2 == Q4Smem<D>::raw_bytes, "the slots' place");
 
-  // Cache row of the tile's first key (contiguous), or of each of its pages in
-  // lane's turn (-1: a bad page, or none).
-  static __device__ __forceinline__ long long tile_rows(const Q4AttnArgs& a, int s, int g, int j0, int n) {
-    if (a.cache.kind != CP_CACHE_PAGED) return ((long long)s * a.hkv + g) * a.cache.capacity + j0;
-    const int lane = threadIdx.x & 31, key = j0 + lane * a.cache.page_size;
-    if (lane * a.cache.page_size >= kTcBlockN || key >= n) return -1;
-    const long long row = cache_row(a.cache, a.hkv, s, g, key, a.max_ctx);
-    if (row < 0 && a.status) atomicOr(a.status, CP_DEV_BOUNDS);
-    return row;
+  // Page of each of the tile's pages, in lane's turn (-1: a bad page, or none).
+  static __device__ __forceinline__ int tile_pages(const Q4AttnArgs& a, int s, int j0, int n) {
+    const int lane = threadIdx.x & 31, lps = 31 - __clz(a.cache.page_size);
+    const int key = j0 + (lane << lps), blk = key >> lps;
+    if ((lane << lps) >= kTcBlockN || key >= n) return -1;
+    int page = blk < a.cache.max_blocks ? a.cache.block_table[(long long)s * a.cache.max_blocks + blk] : -1;
+    if (page < 0 || page >= a.cache.num_pages) {
+      page = -1;
+      if (a.status) atomicOr(a.status, CP_DEV_BOUNDS);
+    }
+    return page;
   }
 
   // Starts the copies of keys j0 + ... < n; others become zeros.
-  static __device__ __forceinline__ void load(const Q4AttnArgs& a, const uint8_t* codes, const uint32_t* params,
-                                              long long rows, int j0, int n, int cw, Slots& x) {
-    const bool paged = a.cache.kind == CP_CACHE_PAGED;
-    const int lps = 31 - __clz(a.cache.page_size | 1);
-    const int lane = threadIdx.x & 31, grp = lane / kKeys;
+  static __device__ __forceinline__ void load(const Q4AttnArgs& a, const uint8_t* codes, const uint32_t* params, int s,
+                                              int g, int pages, int j0, int n, int cw, Slots& x) {
+    const int lane = threadIdx.x & 31, grp = lane / kKeys, key0 = cw * kKeys + lane % kKeys;
+    const int ps = a.cache.page_size, lps = kPaged ? 31 - __clz(ps) : 0;
+    const uint8_t* par = reinterpret_cast<const uint8_t*>(params);
+    // Bytes of codes before the tile's (page's) first row; a row has a quarter as many bytes of parameters.
+    const long long base = kPaged ? (long long)(g << lps) * (D / 2)
+                                  : (((long long)s * a.hkv + g) * a.cache.capacity + j0 + key0) * (D / 2);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int blk = cw + i * kConvWarps;
-      if (kBlocks % kConvWarps != 0 && blk >= kBlocks) break;  // whole warps
-      const int key = blk * kKeys + lane % kKeys;
-      long long row = rows + key;
+      if (kBlocks % kConvWarps != 0 && cw + i * kConvWarps >= kBlocks) break;  // whole warps
+      const int key = key0 + i * (kConvWarps * kKeys);
       bool on = j0 + key < n;
-      if (paged) {
-        const long long page_row = __shfl_sync(0xffffffffu, rows, key >> lps);
-        row = page_row + (key & (a.cache.page_size - 1));
-        on = on && page_row >= 0;
+      long long at = base + i * (kConvWarps * kKeys * (D / 2));
+      if constexpr (kPaged) {
+        const int page = __shfl_sync(0xffffffffu, pages, key >> lps);
+        on = on && page >= 0;
+        at = base + (long long)page * (a.hkv * ps * (D / 2)) + (key & (ps - 1)) * (D / 2);
       }
-      if (!on) row = 0;
-      cp_async16(&x.w[i][cw * 32 + lane], codes + row * (D / 2) + grp * 16, on);
-      cp_async4(&x.p[i][cw * 32 + lane], params + row * kGroups + grp, on);
+      if (!on) at = 0;
+      cp_async16(&x.w[i][cw * 32 + lane], codes + at + grp * 16, on);
+      cp_async4(&x.p[i][cw * 32 + lane], par + (at >> 2) + grp * 4, on);
     }
     cp_async_commit();
   }
 
   // The values into a stage: key row of 128 bytes in 64-channel block grp / 2,
   // 16-byte chunks XOR-swizzled by key mod 8: the eight threads of a store phase
-  // hold the same chunk of eight keys, on distinct banks.
-  static __device__ __forceinline__ void store(const Slots& from, uint8_t* stage, int cw, uint32_t magic) {
+  // hold the same chunk of eight keys, on distinct banks.  With `guard`, groups that
+  // are not finite are stored as zeros; true if there were any.
+  static __device__ __forceinline__ bool store(const Slots& from, uint8_t* stage, int cw, uint32_t magic, bool guard) {
+    bool bad = false;
     const int lane = threadIdx.x & 31, grp = lane / kKeys, k = lane % kKeys;
     uint8_t* at = stage + (grp >> 1) * kBlockBytes + (cw * kKeys + k) * 128;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       if (kBlocks % kConvWarps != 0 && cw + i * kConvWarps >= kBlocks) break;
       const uint4 w = from.w[i][cw * 32 + lane];
-      const uint32_t p = from.p[i][cw * 32 + lane];
+      uint32_t p = from.p[i][cw * 32 + lane];
+      if (guard && q4_nonfinite<T>(p)) {
+        p = 0;
+        bad = true;
+      }
       const uint32_t s2 = q4_scale2(p), m2 = q4_low2(p), x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -244,10 +255,11 @@ struct Conv {
         *reinterpret_cast<uint4*>(at + i * (kConvWarps * kKeys * 128) + ((((grp & 1) * 4 + c) ^ (k & 7)) * 16)) = v;
       }
     }
+    return bad;
   }
 };
 
-template <typename T, int D>
+template <typename T, int D, bool kPaged>
 __global__ void __launch_bounds__(kThreads, 1)
     q4_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_o,
                  const Q4AttnArgs a) {
@@ -288,6 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int c = 0; c < L::kMergeChunks; ++c) mbar_init(&bar->merge_full[c], 1);
     mbar_init(&bar->peer_free, 1);
     bar->abort = 0;
+    for (int i = 0; i < kStages; ++i) bar->bad_tile[i] = -1;
     fence_barrier_init();
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_o);
@@ -353,35 +366,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The tile's blocks do not divide evenly: the warps that take one more of K are not those of V.
     const int cw = warp == 0 ? 0 : warp - 1;
     const int ck = cw, cv = (cw + 5) % kConvWarps;
-    using C = Conv<T, D>;
+    using C = Conv<T, D, kPaged>;
     const uint32_t magic = q4_magic<T>();
     auto* raw = reinterpret_cast<typename C::Slots*>(smem + L::raw_off);  // K's and V's
-    long long rows_at = 0;  // of the tile whose copies start next
+    int pages = -1;  // of the tile whose copies start next
     if (nmine > 0) {
       const int j0 = rank * kTcBlockN;
-      rows_at = C::tile_rows(a, s, g, j0, n);
-      C::load(a, a.k_codes, a.k_params, rows_at, j0, n, ck, raw[0]);
-      C::load(a, a.v_codes, a.v_params, rows_at, j0, n, cv, raw[1]);
+      if (kPaged) pages = C::tile_pages(a, s, j0, n);
+      C::load(a, a.k_codes, a.k_params, s, g, pages, j0, n, ck, raw[0]);
+      C::load(a, a.v_codes, a.v_params, s, g, pages, j0, n, cv, raw[1]);
     }
     for (int i = 0; i < nmine; ++i) {
       const int st = i & 1;
       const int j1 = (rank + 2 * i + 2) * kTcBlockN;  // this CTA's next tile
       const bool more = i + 1 < nmine;
-      if (more) rows_at = C::tile_rows(a, s, g, j1, n);
+      if (kPaged && more) pages = C::tile_pages(a, s, j1, n);
       const uint32_t free_ph = ((i >> 1) & 1) ^ 1;
       if (!warp_wait(&bar->k_empty[st], free_ph, abort_flag, a.status)) break;
       cp_async_wait<1>();  // K of this tile
-      C::store(raw[0], sK + st * DB * kBlockBytes, ck, magic);
+      C::store(raw[0], sK + st * DB * kBlockBytes, ck, magic, false);
       fence_proxy_async_smem();  // the tensor cores read the stage through the async proxy
       mbar_arrive(&bar->k_full[st]);
-      if (more) C::load(a, a.k_codes, a.k_params, rows_at, j1, n, ck, raw[0]);
+      if (more) C::load(a, a.k_codes, a.k_params, s, g, pages, j1, n, ck, raw[0]);
       else cp_async_commit();  // the groups stay in step
       if (!warp_wait(&bar->v_empty[st], free_ph, abort_flag, a.status)) break;
       cp_async_wait<1>();  // V of this tile
-      C::store(raw[1], sV + st * DB * kBlockBytes, cv, magic);
+      // A tile with keys that some row of the pair does not see: 0 * NaN must not reach that row's sum.
+      const int tile = rank + 2 * i;
+      const bool guard = tile * kTcBlockN + kTcBlockN - 1 > past + t0;
+      if (C::store(raw[1], sV + st * DB * kBlockBytes, cv, magic, guard)) bar->bad_tile[st] = tile;
       fence_proxy_async_smem();
       mbar_arrive(&bar->v_full[st]);
-      if (more) C::load(a, a.v_codes, a.v_params, rows_at, j1, n, cv, raw[1]);
+      if (more) C::load(a, a.v_codes, a.v_params, s, g, pages, j1, n, cv, raw[1]);
       else cp_async_commit();
     }
     cp_async_wait<0>();
@@ -541,6 +557,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st32(o_col + 32 * c, ov);
         }
       }
+      // A non-finite V group stands as zeros where keys are hidden from a row of the pair: the rows that see it
+      // become NaN by their sum.
+      const int tile = rank + 2 * i;
+      if (tile * kTcBlockN + kTcBlockN - 1 > past + t0) {
+        if (!warp_wait(&bar->v_full[i & 1], (i >> 1) & 1, abort_flag, a.status)) { alive = false; break; }
+        if (*static_cast<volatile int*>(&bar->bad_tile[i & 1]) == tile) {
+          for (int c = 0; c < min(c_hi, kTcBlockN); ++c) {
+            const long long row = cache_row(a.cache, a.hkv, s, g, tile * kTcBlockN + c, a.max_ctx);
+            for (int j = 0; row >= 0 && j < D / 32; ++j)
+              if (q4_nonfinite<T>(a.v_params[row * (D / 32) + j])) l_run = __int_as_float(0x7fffffff);
+          }
+        }
+      }
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&bar->p_ready[grp]);
@@ -600,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float wA = (mA == -INFINITY) ? 0.f : ex2_approx(mA - mm);
     const float wB = (mB == -INFINITY) ? 0.f : ex2_approx(mB - mm);
     const float lsum = lA * wA + lB * wB;
-    const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
+    const float inv = lsum == 0.f ? 0.f : 1.f / lsum;  // a NaN stays
     // A tile whose rows all belong to this sequence leaves through a TMA store
     // from the (now unused) Q buffer; a ragged tile row by row.
     const int tile_tok0 = t0 + rank * rpt;
@@ -669,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kPaged>
 cudaError_t launch_t(const Q4AttnArgs& a, const CUtensorMap& tq, const CUtensorMap& to, int pairs_bound,
                      cudaStream_t st) {
   // D = 64 would fit two CTAs per SM, but each CTA takes all 512 TMEM columns;
@@ -686,10 +715,10 @@ cudaError_t launch_t(const Q4AttnArgs& a, const CUtensorMap& tq, const CUtensorM
     // The register split is only sound at the per-thread count it was sized
     // for: refuse to launch a build that came out at another count.
     cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, q4_tc_kernel<T, D>);
+    e = cudaFuncGetAttributes(&fa, q4_tc_kernel<T, D, kPaged>);
     if (e != cudaSuccess) return e;
     if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidDeviceFunction;
-    e = cudaFuncSetAttribute(q4_tc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(q4_tc_kernel<T, D, kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     ready_mask.fetch_or(bit, std::memory_order_release);
   }
@@ -707,7 +736,7 @@ cudaError_t launch_t(const Q4AttnArgs& a, const CUtensorMap& tq, const CUtensorM
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, q4_tc_kernel<T, D>, tq, to, a);
+  e = cudaLaunchKernelEx(&cfg, q4_tc_kernel<T, D, kPaged>, tq, to, a);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
@@ -721,11 +750,12 @@ cudaError_t launch_q4_tc(const Q4AttnArgs& a, int dtype, int d, int pairs_bound,
   if (!encode_3d(&tq, dtype, a.q, d, a.hq, a.total_rows, 64, a.group, kTcBlockM / a.group) ||
       !encode_3d(&to, dtype, a.out, d, a.hq, a.total_rows, 64, a.group, kTcBlockM / a.group))
     return cudaErrorInvalidValue;
+  const bool paged = a.cache.kind == CP_CACHE_PAGED;
   if (dtype == CP_BF16)
-    return d == 64 ? launch_t<__nv_bfloat16, 64>(a, tq, to, pairs_bound, st)
-                   : launch_t<__nv_bfloat16, 128>(a, tq, to, pairs_bound, st);
-  return d == 64 ? launch_t<__half, 64>(a, tq, to, pairs_bound, st)
-                 : launch_t<__half, 128>(a, tq, to, pairs_bound, st);
+    return d == 64 ? (paged ? launch_t<__nv_bfloat16, 64, true> : launch_t<__nv_bfloat16, 64, false>)(a, tq, to, pairs_bound, st)
+                   : (paged ? launch_t<__nv_bfloat16, 128, true> : launch_t<__nv_bfloat16, 128, false>)(a, tq, to, pairs_bound, st);
+  return d == 64 ? (paged ? launch_t<__half, 64, true> : launch_t<__half, 64, false>)(a, tq, to, pairs_bound, st)
+                 : (paged ? launch_t<__half, 128, true> : launch_t<__half, 128, false>)(a, tq, to, pairs_bound, st);
 }
 
 }  // namespace cp

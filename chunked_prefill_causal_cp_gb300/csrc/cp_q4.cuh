@@ -14,11 +14,13 @@ struct Two;
 template <>
 struct Two<__nv_bfloat16> {
   typedef __nv_bfloat162 type;
+  static constexpr uint32_t kExponent = 0x7f80u;
   static constexpr uint32_t kMagic = 0x43004300u;  // 128: a code in the low mantissa bits is 128 + code
 };
 template <>
 struct Two<__half> {
   typedef __half2 type;
+  static constexpr uint32_t kExponent = 0x7c00u;
   static constexpr uint32_t kMagic = 0x64006400u;  // 1024
 };
 
@@ -45,5 +47,12 @@ __device__ __forceinline__ uint32_t q4_pair(uint32_t w, uint32_t s2, uint32_t m2
 // (s, m) of one group -> the pairs (s, s) and (m, m).
 __device__ __forceinline__ uint32_t q4_scale2(uint32_t params) { return __byte_perm(params, params, 0x1010); }
 __device__ __forceinline__ uint32_t q4_low2(uint32_t params) { return __byte_perm(params, params, 0x3232); }
+
+// Whether a group's scale or smallest value is a NaN or an infinity.
+template <typename T>
+__device__ __forceinline__ bool q4_nonfinite(uint32_t params) {
+  constexpr uint32_t kExp = Two<T>::kExponent;
+  return (params & kExp) == kExp || ((params >> 16) & kExp) == kExp;
+}
 
 }  // namespace cp

@@ -95,7 +95,8 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
   }
 }
 
-template <typename T, int D, int NF>
+// kOne: sequences of one row, which sees every key.
+template <typename T, int D, int NF, bool kOne>
 __global__ void __launch_bounds__(kWarps * 32, NF == 1 ? 4 : D == 64 ? 4 : 3) q4_split_kernel(const Q4AttnArgs a) {
   constexpr int NC = 8 * NF;     // (row, head) columns
   constexpr int KW = D / 32;     // score phase: words of a lane's channels
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(kWarps * 32, NF == 1 ? 4 : D == 64 ? 4 : 3) q4
   const int rows = seq_rows(a.rows, s);
   const bool reports = a.status && split == 0 && gk == 0 && threadIdx.x == 0;
   if (reports && rows < 1) atomicOr(a.status, CP_DEV_BOUNDS);
-  const int kr = a.dec_rows;
+  const int kr = kOne ? 1 : a.dec_rows;
   if (rows != kr) return;
   const int past = a.past[s];
   const int row0 = seq_row0(a.rows, s);
@@ -236,16 +237,34 @@ __global__ void __launch_bounds__(kWarps * 32, NF == 1 ? 4 : D == 64 ? 4 : 3) q4
             mma16816<T>(c[f], a0, a1, a2, a3, u ? qf[f][i].z : qf[f][i].x, u ? qf[f][i].w : qf[f][i].y);
         }
     }
-    const int j1 = 16 * t + g8 + 8;
     const bool bad = (bad_tiles >> t) & 1;
     if (bad || 16 * t + 15 > past - kw) {  // a bad page, or keys that row 0 does not see
+      // A V group of such a key that is not finite becomes zeros, so that 0 * NaN does not reach the rows that do
+      // not see it; the rows that do become NaN by their sum.
+      const int jv = 16 * t + (lane & 15);
+      bool nan_v = false;
+      if (!kOne && jv > past - kw && jv < nkw) {
+        uint32_t* vp = reinterpret_cast<uint32_t*>(sWarp[warp] + (t % kRing) * S::bytes + S::vp + (lane & 15) * S::kPar);
 #pragma unroll
-      for (int f = 0; f < NF; ++f) {
-        if (bad || j1 - 8 > lim[f][0]) c[f][0] = -INFINITY;
-        if (bad || j1 - 8 > lim[f][1]) c[f][1] = -INFINITY;
-        if (bad || j1 > lim[f][0]) c[f][2] = -INFINITY;
-        if (bad || j1 > lim[f][1]) c[f][3] = -INFINITY;
+        for (int i = 0; i < S::kPar / 4; ++i)
+          if (q4_nonfinite<T>(vp[i])) nan_v = true;
       }
+      const uint32_t nan_keys = __ballot_sync(0xffffffffu, nan_v);  // bits 0-15: the tile's keys
+      if (nan_v) {
+        uint32_t* vp = reinterpret_cast<uint32_t*>(sWarp[warp] + (t % kRing) * S::bytes + S::vp + (lane & 15) * S::kPar);
+#pragma unroll
+        for (int i = 0; i < S::kPar / 4; ++i)
+          if (q4_nonfinite<T>(vp[i])) vp[i] = 0;
+      }
+      __syncwarp();
+#pragma unroll
+      for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool sees = 16 * t + g8 + 8 * (e >> 1) <= lim[f][e & 1];
+          if (bad || !sees) c[f][e] = -INFINITY;
+          else if ((nan_keys >> (g8 + 8 * (e >> 1))) & 1) l[f][e & 1] = __int_as_float(0x7fffffff);
+        }
     }
 
     // ---- softmax: raise the maxima when a score passes one by more than 2^8
@@ -463,8 +482,10 @@ __global__ void __launch_bounds__(kCombineThreads) q4_combine_kernel(const Q4Att
 template <typename T, int D>
 cudaError_t launch_t(const Q4AttnArgs& a, cudaStream_t st) {
   const dim3 grid((unsigned)(a.rows.num_seqs * (long long)a.max_splits), a.hkv);
-  cudaError_t e = a.dec_rows * a.group <= 8 ? launch_pdl(q4_split_kernel<T, D, 1>, grid, dim3(kWarps * 32), 0, st, a)
-                                            : launch_pdl(q4_split_kernel<T, D, 2>, grid, dim3(kWarps * 32), 0, st, a);
+  const bool one = a.dec_rows == 1, wide = a.dec_rows * a.group > 8;
+  const auto kernel = wide ? (one ? q4_split_kernel<T, D, 2, true> : q4_split_kernel<T, D, 2, false>)
+                           : (one ? q4_split_kernel<T, D, 1, true> : q4_split_kernel<T, D, 1, false>);
+  const cudaError_t e = launch_pdl(kernel, grid, dim3(kWarps * 32), 0, st, a);
   if (e != cudaSuccess || a.max_splits == 1) return e;
   constexpr int kPer = kCombineThreads / (D / 4 * kSlices);
   const long long pairs = (long long)a.rows.num_seqs * a.dec_rows * a.hq;

@@ -497,9 +497,8 @@ int cp_kv_read_q4(const cp_layer_desc* desc, const cp_q4_cache* cache, const int
  * take a memory-bound split-KV path that reads the cache once for all of a KV
  * head's rows; the others a tensor-core path.  Hq / Hkv must be 1, 2, 4, 8 or 16.
  * A row's result depends only on its own sequence.  Slots past a sequence's
- * positions may hold anything.  A non-finite value of a visible key makes the
- * rows that see it non-finite, and may make rows before it so that share its
- * 128-key tile. */
+ * positions may hold anything.  A non-finite value makes the rows that see its
+ * key non-finite (in its channels or in all), and no other row. */
 int cp_chunk_attn_q4(const cp_layer_desc* desc, const void* q, const cp_q4_cache* cache, int32_t* seqlens_k,
                      const int32_t* block_table, const int32_t* cu_rows, int32_t num_seqs, int32_t total_rows,
                      int32_t max_ctx, void* out, void* workspace, size_t workspace_bytes, int32_t commit,

@@ -238,6 +238,27 @@ def test_a_row_depends_on_its_own_sequence_only():
         assert torch.equal(o, out[r0:r0 + rows[i]])
 
 
+@pytest.mark.parametrize("dtype,hq,d", [(BF16, 8, 128), (F16, 4, 64)])
+@pytest.mark.parametrize("rows,past", [(1, 300), (2, 127), (4, 510), (40, 100), (200, 77), (300, 0)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_non_finite_key_reaches_the_rows_that_see_it_only(dtype, hq, d, rows, past, value):
+    hkv, at = hq // 2, past + rows // 2  # the key of a row in the middle of the call's
+    n = past + rows
+    outs = []
+    for which in (None, "v", "k"):
+        c = Cache4(dtype, hq, hkv, d, 1, 700)
+        g = torch.Generator().manual_seed(7)
+        k, v = (torch.randn(n, hkv, d, generator=g).to(dtype).cuda() for _ in range(2))
+        if which:
+            {"k": k, "v": v}[which][at, :, 3] = value
+        cp.cp_kv_append_q4(c.desc, k, v, c.arg, _ints([0]), 1, n, n)
+        outs.append(_attend(c, [rows], [past], uniform=True)[1])
+    seen = at - past
+    for out in outs[1:]:
+        assert torch.equal(out[:seen], outs[0][:seen])
+        assert (~torch.isfinite(out[seen:]).all(-1)).all()
+
+
 def test_slots_past_four_billion_bytes():
     """The last sequence's codes start more than 2^32 bytes into the cache."""
     hq, hkv, d, n, cap = 8, 8, 128, 3, 2_900_001
