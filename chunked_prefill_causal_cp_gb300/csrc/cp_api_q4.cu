@@ -52,7 +52,7 @@ int rope_check(const cp_layer_desc* d, const cp_qk_prep* p, const void* q, int64
   if (!p || !std::isfinite(p->eps) || p->eps < 0.f || (p->interleaved != 0 && p->interleaved != 1))
     return CP_ERR_INVALID_ARG;
   if (p->rot_dim < 0 || p->rot_dim > d->head_dim) return CP_ERR_INVALID_ARG;
-  if (p->rot_dim % 16 != 0) return CP_ERR_UNSUPPORTED;
+  if (p->rot_dim % 16 != 0 || d->num_q_heads > 65535) return CP_ERR_UNSUPPORTED;
   const int es = esize_of(d->dtype);
   long long qs, ks;
   int e = stride_of(q_stride, (int64_t)d->num_q_heads * d->head_dim, es, &qs);

@@ -6,8 +6,8 @@
 // key and KV head at 128 channels) as long as the codes turn into matrix
 // operands quickly enough: at full bandwidth an SM has some 28 instructions per
 // key, and turning 256 codes into 16-bit values takes 15 of them.  One CTA takes
-// 256 to 1024 keys of a (sequence, KV head), four warps a quarter each; the k rows of the
-// sequence times the G heads of the group (k * G <= 16) ride in the columns of
+// 256 to 1024 keys of a (sequence, KV head), four warps a quarter each; the k rows
+// of the sequence times the G heads of the group (k * G <= 16) ride in the columns of
 // m16n8k16 products, so every row shares one read of the cache and one
 // conversion of its codes.  A warp walks its keys 16 at a time, in a rolled loop
 // (unrolled over the whole range, the code outgrew the instruction cache and
@@ -33,6 +33,13 @@
 //   split is finished there, others write their part for the combine kernel,
 //   which merges the splits in order.  A row's result depends on its own
 //   sequence only.
+//
+// Measured (32/8 heads x 128, bf16): 4 rows over 100001 keys in 113.5 us, of which the
+// merge 6, 4.5 TB/s, 0.67 of a plain copy's rate; DRAM reads equal the cache's bytes;
+// issue slots 70% busy, the integer pipe about 55%.  Leaving out the subtraction,
+// the mask, the shift or the multiply-add of the conversion alone gained 6 to 14%
+// each: the conversion as a whole is what is left.  Two tiles an iteration, three
+// or six ring stages, eight warps, and three, five or six CTAs an SM were no faster.
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
