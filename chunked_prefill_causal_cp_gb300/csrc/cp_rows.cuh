@@ -23,6 +23,13 @@ __device__ __forceinline__ int row_seq(const SeqRows& r, int row) {
   return lo;
 }
 
+// Place of a row within its sequence s, or -1 when it belongs to none (rows
+// before the first offset or from the last one on: a padded batch).
+__device__ __forceinline__ int row_place(const SeqRows& r, int s, int row) {
+  const int i = row - seq_row0(r, s);
+  return i < seq_rows(r, s) ? i : -1;
+}
+
 // Index of the (position, KV head) row of sequence s in a cache array, in rows,
 // or -1 when the host bound or the layout does not allow the position.
 __device__ __forceinline__ long long cache_row(const CacheView& c, int hkv, int s, int g, long long pos, int max_ctx) {

@@ -138,8 +138,9 @@ __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(const Q4Args a) {
   quantize<T>(vv, vw, vp);
   if (!on) return;
   const int t = (int)(row / (uint32_t)a.hkv), g = (int)(row % (uint32_t)a.hkv);
-  const int s = row_seq(a.rows, t);
-  const long long dst = cache_row(a.cache, a.hkv, s, g, (long long)a.past[s] + t - seq_row0(a.rows, s), a.max_ctx);
+  const int s = row_seq(a.rows, t), i = row_place(a.rows, s, t);
+  if (i < 0) return;
+  const long long dst = cache_row(a.cache, a.hkv, s, g, (long long)a.past[s] + i, a.max_ctx);
   if (dst < 0) {
     if (a.status && c == 0) atomicOr(a.status, CP_DEV_BOUNDS);
     return;
@@ -168,8 +169,9 @@ __global__ void __launch_bounds__(kQ4Threads) q4_read_kernel(const Q4Args a) {
   const int c = threadIdx.x % V;
   if (row >= (uint32_t)a.total_rows * (uint32_t)a.hkv) return;
   const int t = (int)(row / (uint32_t)a.hkv), g = (int)(row % (uint32_t)a.hkv);
-  const int s = row_seq(a.rows, t);
-  const long long src = cache_row(a.cache, a.hkv, s, g, (long long)a.past[s] + t - seq_row0(a.rows, s), a.max_ctx);
+  const int s = row_seq(a.rows, t), i = row_place(a.rows, s, t);
+  if (i < 0) return;
+  const long long src = cache_row(a.cache, a.hkv, s, g, (long long)a.past[s] + i, a.max_ctx);
   if (src < 0) {
     if (a.status && c == 0) atomicOr(a.status, CP_DEV_BOUNDS);
     return;

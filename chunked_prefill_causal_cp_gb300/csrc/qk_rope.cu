@@ -104,7 +104,9 @@ __global__ void __launch_bounds__(kRopeThreads, 6) qk_rope_kernel(const RopeArgs
   int s = 0;
   if (kAppend || !a.positions) {
     s = row_seq(a.rows, t);
-    pos = (long long)a.past[s] + t - seq_row0(a.rows, s);
+    const int i = row_place(a.rows, s, t);
+    if (i < 0) return;  // the whole warp has this token
+    pos = (long long)a.past[s] + i;
   }
   const long long ang = a.positions ? a.positions[t] : pos;
 

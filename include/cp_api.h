@@ -384,8 +384,10 @@ typedef struct {
  *                 then seqlens_k[s] + (its row within sequence s), with the rows
  *                 of the sequences given by cu_rows (device int32 [num_seqs + 1]
  *                 as in cp_mixed_step) or, when that is NULL, total_rows /
- *                 num_seqs rows each.  With positions given, seqlens_k and
- *                 cu_rows are not read and may be NULL.
+ *                 num_seqs rows each.  Rows from cu_rows[num_seqs] on (a padded
+ *                 batch) are left as they were in the outputs.  With positions
+ *                 given, seqlens_k and cu_rows are not read and may be NULL, and
+ *                 every row is taken.
  *   q_out, k_out  device [total_rows, Hq, D] and [total_rows, Hkv, D], dense.
  *                 q_out may be q itself (dense), k_out may be k; any other
  *                 overlap returns CP_ERR_INVALID_ARG.
@@ -406,7 +408,8 @@ int cp_qk_norm_rope(const cp_layer_desc* desc, const cp_qk_prep* prep, const voi
  * not modified (cp_prefill_chunk_attn commits it).  `positions` (may be NULL)
  * sets the rotation's position only.
  *   v_new         device rows of [Hkv, D] with v_row_stride, copied bit for bit
- *   cu_rows       NULL for total_rows / num_seqs rows each
+ *   cu_rows       as above; rows from cu_rows[num_seqs] on are not taken,
+ *                 whether positions are given or not
  *   q_out         device [total_rows, Hq, D], dense (q itself, when dense)
  *   max_ctx       host bound on seqlens_k[s] + rows of s; a row whose position
  *                 is not in [0, max_ctx) is not appended and sets CP_DEV_BOUNDS
@@ -452,7 +455,8 @@ typedef struct {
 /* cp_kv_append_q4 -- cp_kv_append into a 4-bit cache.
  *   k_new, v_new  device [total_rows, Hkv, D], dense
  *   cu_rows       device int32 [num_seqs + 1] (rows of sequence s as in
- *                 cp_mixed_step), or NULL: total_rows / num_seqs rows each
+ *                 cp_mixed_step; rows from cu_rows[num_seqs] on, a padded batch,
+ *                 are not taken), or NULL: total_rows / num_seqs rows each
  *   seqlens_k     device int32 [num_seqs]: position of each sequence's first
  *                 row; not modified
  *   block_table   device int32 [num_seqs, max_blocks] (PAGED, else NULL)
@@ -483,7 +487,8 @@ int cp_kv_read_q4(const cp_layer_desc* desc, const cp_q4_cache* cache, const int
  *                 cache or the workspace
  *   cu_rows       device int32 [num_seqs + 1], every sequence with at least one
  *                 row (one without sets CP_DEV_BOUNDS), or NULL: total_rows /
- *                 num_seqs rows each
+ *                 num_seqs rows each.  Rows of out from cu_rows[num_seqs] on are
+ *                 left as they were
  *   max_ctx       host bound on seqlens_k[s] + rows of s, below 2^31 - 4096; a
  *                 sequence outside it is skipped (its rows of out are left as they
  *                 were) and sets CP_DEV_BOUNDS.  A page id out of range sets it

@@ -357,6 +357,39 @@ def test_rows_without_a_sequence_and_a_sequence_without_rows():
     check_attention(c, q[20:41], out[20:41], [10], [21], seqs=[2])
 
 
+def test_a_padded_batch():
+    """total_rows past the last sequence's: the rows there go nowhere, in every call."""
+    rows, past, t = [1, 30, 2], [40, 0, 17], 64
+    n, cu, lens = sum(rows), _cu(rows), _ints(past)
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn(t, 8 * 64, generator=g).bfloat16().cuda()
+    q, k, v = (y.unflatten(1, (-1, 64)) for y in x.split([4 * 64, 2 * 64, 2 * 64], 1))
+    freq = torch.ones(32, device="cuda")
+    c, e = (Cache4(BF16, 4, 2, 64, 3, 64, page=16) for _ in range(2))
+    for y in (c, e):
+        y.fill([p + 1 for p in past])
+    got = []
+    for cache, m in ((c, t), (e, n)):
+        q2, k2 = torch.full((t, 4, 64), 3.0).bfloat16().cuda(), torch.full((t, 2, 64), 3.0).bfloat16().cuda()
+        out, back = torch.full_like(q2, 3.0), torch.full_like(k2, 3.0)
+        kw = dict(cu_rows=cu)
+        cp.cp_qk_norm_rope(cache.desc, cp.qk_prep(64), q[:m], k[:m], q2, k2, 3, m, inv_freq=freq, seqlens_k=lens, **kw)
+        kw.update(block_table=cache.table, dev_status=cache.status)
+        cp.cp_mixed_step_q4(cache.desc, q2[:m], k2[:m], v[:m].contiguous(), cache.arg, lens, 3, m, 64, out,
+                            cache.workspace(m, 64), commit=False, **kw)
+        cp.cp_kv_read_q4(cache.desc, cache.arg, lens, 3, m, 64, None, back, **kw)
+        qa, kc = torch.full_like(q2, 3.0), torch.full((cache.pages, 2, 16, 64), 3.0).bfloat16().cuda()
+        vc = torch.full_like(kc, 3.0)
+        cp.cp_qk_norm_rope_append(cache.desc, cp.qk_prep(64), q[:m], k[:m], v[:m], qa, kc, vc, lens, 3, m, 64,
+                                  inv_freq=freq, **kw)
+        assert int(cache.status) == 0
+        got.append([q2, k2, out, back, qa, kc, vc, *(y.view(torch.uint8) for y in cache.arg.tensors)])
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    for y in got[0][:5]:
+        assert (y[n:] == 3.0).all()
+
+
 def test_binding_refuses_wrong_tensors():
     c = Cache4(BF16, 4, 2, 64, 2, 64)
     c.fill([64, 64])
