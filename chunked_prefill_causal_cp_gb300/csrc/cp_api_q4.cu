@@ -343,7 +343,7 @@ int cp_kv_read_q4(const cp_layer_desc* desc, const cp_q4_cache* cache, const int
 size_t cp_workspace_size_q4(const cp_layer_desc* desc, int32_t total_rows, int32_t max_ctx, int32_t num_seqs) {
   if (check_desc(desc, false) != CP_OK || total_rows <= 0 || max_ctx <= 0 || num_seqs <= 0) return 0;
   const int G = desc->num_q_heads / desc->num_kv_heads;
-  if (G > 16) return 0;
+  if (G > 16 || (G & (G - 1)) || desc->dtype == CP_F32 || desc->kind == CP_CACHE_ROLLING) return 0;
   // Ragged rows, or equal ones: whichever needs more.
   double bytes = q4_plan(desc, true, num_seqs, total_rows, max_ctx).bytes;
   if (total_rows % num_seqs == 0) bytes = std::max(bytes, q4_plan(desc, false, num_seqs, total_rows, max_ctx).bytes);

@@ -102,10 +102,12 @@ __global__ void __launch_bounds__(kRopeThreads, 6) qk_rope_kernel(const RopeArgs
 
   long long pos = 0;  // position within the sequence, from the cached length
   int s = 0;
+  bool older = false;  // a ring: newer rows of this call take the row's slot
   if (kAppend || !a.positions) {
     s = row_seq(a.rows, t);
     const int i = row_place(a.rows, s, t);
     if (i < 0) return;  // the whole warp has this token
+    older = kAppend && a.cache.kind == CP_CACHE_ROLLING && seq_rows(a.rows, s) - i > a.cache.capacity;
     pos = (long long)a.past[s] + i;
   }
   const long long ang = a.positions ? a.positions[t] : pos;
@@ -195,7 +197,8 @@ __global__ void __launch_bounds__(kRopeThreads, 6) qk_rope_kernel(const RopeArgs
     } else if (!kAppend) {
       dst = static_cast<T*>(a.k_out) + ((long long)t * a.hkv + g) * D;
     } else {
-      const long long row = cache_row(a.cache, a.hkv, s, g, pos, a.max_ctx);
+      // (A ring holds a sequence's newest rows; the host's bound on them trusts that every sequence has one.)
+      const long long row = older ? -1 : cache_row(a.cache, a.hkv, s, g, pos, a.max_ctx);
       if (row < 0) {
         if (a.status && l == 0) atomicOr(a.status, CP_DEV_BOUNDS);
         continue;

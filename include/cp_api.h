@@ -501,9 +501,9 @@ int cp_kv_read_q4(const cp_layer_desc* desc, const cp_q4_cache* cache, const int
  * Paths: sequences of one row, and calls with equal rows of at most 16 / G each,
  * take a memory-bound split-KV path that reads the cache once for all of a KV
  * head's rows; the others a tensor-core path.  Hq / Hkv must be 1, 2, 4, 8 or 16.
- * On either path a row's result depends only on its own sequence.  Slots past a sequence's
- * positions may hold anything.  A non-finite value makes the rows that see its
- * key non-finite (in its channels or in all), and no other row. */
+ * On either path a row's result depends only on its own sequence.  Slots past a
+ * sequence's positions may hold anything.  A non-finite value makes the rows that
+ * see its key non-finite (in its channels or in all), and no other row. */
 int cp_chunk_attn_q4(const cp_layer_desc* desc, const void* q, const cp_q4_cache* cache, int32_t* seqlens_k,
                      const int32_t* block_table, const int32_t* cu_rows, int32_t num_seqs, int32_t total_rows,
                      int32_t max_ctx, void* out, void* workspace, size_t workspace_bytes, int32_t commit,

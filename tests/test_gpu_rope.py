@@ -173,3 +173,18 @@ def test_append_reports_positions_out_of_bounds_and_touches_nothing_there():
     pos = np.concatenate([np.arange(p, p + r) for p in (14, 30, -3)])
     _check(q, qo, w[0], pos, f64(_freqs(64)), 64, False, 1e-6, BF16)
     assert torch.equal(vc[2, :, 14:].transpose(0, 1), v[4:6])
+
+
+def test_ring_with_more_rows_than_slots_keeps_the_newest():
+    """Sequences without rows slip past the host's bound; the ring then takes the newest rows and reports."""
+    hq, hkv, d, cap = 2, 2, 64, 4
+    q, k, v, _ = _inputs(BF16, 6, hq, hkv, d, 6, False)
+    desc = cp.layer_desc(BF16, 3, hq, hkv, d, cp.CP_CACHE_ROLLING, capacity=cap)
+    kc = torch.full((3, hkv, cap, d), 9.0).bfloat16().cuda()
+    vc, qo, status = torch.full_like(kc, 9.0), torch.empty_like(q), torch.zeros(1, dtype=torch.int32, device="cuda")
+    cp.cp_qk_norm_rope_append(desc, cp.qk_prep(0), q, k, v, qo, kc, vc, torch.zeros(3, dtype=torch.int32, device="cuda"), 3,
+                              6, 6, cu_rows=torch.tensor([0, 0, 0, 6], dtype=torch.int32, device="cuda"), dev_status=status)
+    assert int(status) == cp.CP_DEV_BOUNDS and torch.equal(qo, q)
+    assert (vc[:2] == 9.0).all()
+    for pos in range(2, 6):
+        assert torch.equal(vc[2, :, pos % cap], v[pos]) and torch.equal(kc[2, :, pos % cap], k[pos])

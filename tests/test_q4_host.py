@@ -129,6 +129,20 @@ def test_q4_refusals(call):
         assert f(desc=_desc(num_q_heads=32, num_kv_heads=1)) == UNSUP
 
 
+def test_workspace_is_asked_for_and_has_to_be_there():
+    d = _desc()
+    need = cp.cp_workspace_size_q4(d, 8, 1024, 4)
+    assert need > 0 and cp.cp_workspace_size_q4(d, 4, 1024, 4) <= need
+    for call in ("attn", "step"):
+        assert _q4(call, ws=None) == WS and _q4(call, ws_bytes=need - 1) == WS and _q4(call, ws=FAKE + 8) == WS
+    for bad in (_desc(dtype=torch.float32), _desc(kind=cp.CP_CACHE_ROLLING), _desc(num_q_heads=6), _desc(head_dim=96)):
+        assert cp.cp_workspace_size_q4(bad, 8, 1024, 4) == 0
+    assert cp.cp_workspace_size_q4(d, 0, 1024, 4) == 0 and cp.cp_workspace_size_q4(d, 8, 0, 4) == 0
+    huge = _paged(batch=0)
+    assert cp.cp_workspace_size_q4(huge, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1) > 2 ** 40
+    assert _q4("attn", desc=_desc(capacity=2 ** 31 - 1), max_ctx=2 ** 31 - 2) == UNSUP
+
+
 def test_a_step_refuses_missing_rows_before_it_starts():
     d, c = _desc(), _cache()
     for k, v in ((None, FAKE), (FAKE, None), (FAKE + 2, FAKE)):
