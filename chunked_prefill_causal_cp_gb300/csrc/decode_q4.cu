@@ -30,8 +30,9 @@
 //   4 bits at a time, ready for the same conversion.  V's rows are placed in the
 //   ring so that these loads fall on distinct banks.
 //   The four warps' parts are merged in warp order; a sequence that fits one
-//   split is finished there, others write their part for the combine kernel,
-//   which merges the splits in order.  A row's result depends on its own
+//   split is finished there, others write their part, and the splits are merged in
+//   a fixed order by the combine kernel (by the last CTA of a (sequence, KV head) to
+//   finish, counted by tickets, it took as long).  A row's result depends on its own
 //   sequence only.
 //
 // Measured (32/8 heads x 128, bf16): 4 rows over 100001 keys in 113.5 us, of which the
@@ -409,12 +410,50 @@ __global__ void __launch_bounds__(kWarps * 32, NF == 1 ? 4 : D == 64 ? 4 : 3) q4
   }
 }
 
-// A row's splits merged.  A (row, head) belongs to kSlices groups of D / 4
-// threads, a thread four channels: each group merges every kSlices-th split in
-// order, then the groups' results are merged in order.  Eight groups, whatever the
-// number of splits, so that the order is a row's own (with four, the merge of 98
-// splits took 6 us longer, that of 9 as long).
-constexpr int kCombineThreads = 256, kSlices = 8;
+// A row's splits are merged in eight slices -- split i in slice i % 8, a slice's
+// splits in order -- and the slices in order, whatever the number of splits: the
+// order is the row's own.  (With four slices, the merge of 98 splits took 6 us
+// longer, that of 9 as long.)  A (row, head) belongs to kSlices groups of D / 4
+// threads, a group a slice, a thread four channels.
+constexpr int kSlices = 8;
+
+// Four channels of a merge in progress: unnormalised output, maximum, sum.
+struct Part {
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  float m = -INFINITY, l = 0.f;
+
+  // Adds a split: its maximum and sum, and its four channels.
+  __device__ __forceinline__ void add(const float2& ml, const float4& p) {
+    const float mn = fmaxf(m, ml.x), z = mn == -INFINITY ? 0.f : mn;
+    const float k0 = ex2_approx(m - z), k1 = ex2_approx(ml.x - z);
+    v[0] = v[0] * k0 + p.x * k1;
+    v[1] = v[1] * k0 + p.y * k1;
+    v[2] = v[2] * k0 + p.z * k1;
+    v[3] = v[3] * k0 + p.w * k1;
+    l = l * k0 + ml.y * k1;
+    m = mn;
+  }
+  // Adds a slice to a sum of slices whose common maximum is z.
+  __device__ __forceinline__ void add_scaled(const float4& p, float pm, float pl, float z) {
+    const float k = ex2_approx(pm - z);
+    v[0] = fmaf(k, p.x, v[0]);
+    v[1] = fmaf(k, p.y, v[1]);
+    v[2] = fmaf(k, p.z, v[2]);
+    v[3] = fmaf(k, p.w, v[3]);
+    l = fmaf(k, pl, l);
+  }
+  template <typename T>
+  __device__ __forceinline__ void write(T* out) const {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float o[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
+    uint2 b;
+    b.x = Pack<T>::store(o);
+    b.y = Pack<T>::store(o + 2);
+    *reinterpret_cast<uint2*>(out) = b;
+  }
+};
+
+constexpr int kCombineThreads = 256;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kCombineThreads) q4_combine_kernel(const Q4AttnArgs a) {
@@ -437,53 +476,29 @@ __global__ void __launch_bounds__(kCombineThreads) q4_combine_kernel(const Q4Att
     if (on) nsplit = q4_splits(past + kr);  // the last may hold keys of later rows only: a part of weight 0
     on = on && nsplit > 1;                  // one split: finished by the split kernel
   }
-  float m = -INFINITY, l = 0.f;
-  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  Part part;
   if (on) {
-    const long long base = id * a.max_splits;
 #pragma unroll 4
     for (int i = slice; i < nsplit; i += kSlices) {
-      const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (base + i) * 2);
-      const float4 p = *reinterpret_cast<const float4*>(a.part_o + (base + i) * D + 4 * d4);
-      const float mn = fmaxf(m, ml.x), z = mn == -INFINITY ? 0.f : mn;
-      const float k0 = ex2_approx(m - z), k1 = ex2_approx(ml.x - z);
-      v[0] = v[0] * k0 + p.x * k1;
-      v[1] = v[1] * k0 + p.y * k1;
-      v[2] = v[2] * k0 + p.z * k1;
-      v[3] = v[3] * k0 + p.w * k1;
-      l = l * k0 + ml.y * k1;
-      m = mn;
+      const long long at = id * a.max_splits + i;
+      part.add(__ldcg(reinterpret_cast<const float2*>(a.part_ml + at * 2)),
+               __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + 4 * d4)));
     }
   }
-  so[pair][slice][d4] = make_float4(v[0], v[1], v[2], v[3]);
+  so[pair][slice][d4] = make_float4(part.v[0], part.v[1], part.v[2], part.v[3]);
   if (d4 == 0) {
-    sm[pair][slice] = m;
-    sl[pair][slice] = l;
+    sm[pair][slice] = part.m;
+    sl[pair][slice] = part.l;
   }
   __syncthreads();
-  if (slice != 0) return;
-  m = -INFINITY;
+  if (slice != 0 || !on) return;
+  Part all;
 #pragma unroll
-  for (int i = 0; i < kSlices; ++i) m = fmaxf(m, sm[pair][i]);
-  const float z = m == -INFINITY ? 0.f : m;
-  l = v[0] = v[1] = v[2] = v[3] = 0.f;
+  for (int i = 0; i < kSlices; ++i) all.m = fmaxf(all.m, sm[pair][i]);
+  const float z = all.m == -INFINITY ? 0.f : all.m;
 #pragma unroll
-  for (int i = 0; i < kSlices; ++i) {
-    const float k = ex2_approx(sm[pair][i] - z);
-    const float4 p = so[pair][i][d4];
-    v[0] = fmaf(k, p.x, v[0]);
-    v[1] = fmaf(k, p.y, v[1]);
-    v[2] = fmaf(k, p.z, v[2]);
-    v[3] = fmaf(k, p.w, v[3]);
-    l = fmaf(k, sl[pair][i], l);
-  }
-  if (!on) return;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const float o[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
-  uint2 b;
-  b.x = Pack<T>::store(o);
-  b.y = Pack<T>::store(o + 2);
-  *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + ((long long)(row0 + r) * a.hq + h) * D + 4 * d4) = b;
+  for (int i = 0; i < kSlices; ++i) all.add_scaled(so[pair][i][d4], sm[pair][i], sl[pair][i], z);
+  all.write(static_cast<T*>(a.out) + ((long long)(row0 + r) * a.hq + h) * D + 4 * d4);
 }
 
 template <typename T, int D>
