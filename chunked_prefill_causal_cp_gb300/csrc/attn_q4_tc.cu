@@ -256,12 +256,14 @@ struct Conv {
         p = 0;
         bad = true;
       }
-      const uint32_t s2 = q4_scale2(p), m2 = q4_low2(p), x[4] = {w.x, w.y, w.z, w.w};
+      const Q4Scale sm = q4_scale<T>(q4_scale2(p), q4_low2(p));
+      const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const uint4 v = make_uint4(q4_pair<T>(x[c], s2, m2, magic), q4_pair<T>(x[c] >> 4, s2, m2, magic),
-                                   q4_pair<T>(x[c] >> 8, s2, m2, magic), q4_pair<T>(x[c] >> 12, s2, m2, magic));
-        *reinterpret_cast<uint4*>(at + i * (kConvWarps * kKeys * 128) + ((((grp & 1) * 4 + c) ^ (k & 7)) * 16)) = v;
+        uint32_t v[4];
+        q4_four<T>(x[c], sm, magic, v);
+        *reinterpret_cast<uint4*>(at + i * (kConvWarps * kKeys * 128) + ((((grp & 1) * 4 + c) ^ (k & 7)) * 16)) =
+            make_uint4(v[0], v[1], v[2], v[3]);
       }
     }
     return bad;

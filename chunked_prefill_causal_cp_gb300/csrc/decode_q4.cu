@@ -232,18 +232,18 @@ __global__ void __launch_bounds__(kWarps * 32, NF == 1 ? 4 : D == 64 ? 4 : 3) q4
         else *reinterpret_cast<uint2*>(w[r]) = *reinterpret_cast<const uint2*>(x);
         p[r] = *reinterpret_cast<const uint32_t*>(st + S::kp + (g8 + 8 * r) * S::kPar + q4 * KW / 4 * 4);
       }
-      const uint32_t s0 = q4_scale2(p[0]), m0 = q4_low2(p[0]), s1 = q4_scale2(p[1]), m1 = q4_low2(p[1]);
+      const Q4Scale p0 = q4_scale<T>(q4_scale2(p[0]), q4_low2(p[0])), p1 = q4_scale<T>(q4_scale2(p[1]), q4_low2(p[1]));
 #pragma unroll
-      for (int i = 0; i < KW; ++i)
+      for (int i = 0; i < KW; ++i) {
+        uint32_t x0[4], x1[4];
+        q4_four<T>(w[0][i], p0, magic, x0);
+        q4_four<T>(w[1][i], p1, magic, x1);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint32_t a0 = q4_pair<T>(w[0][i] >> (8 * u), s0, m0, magic), a1 = q4_pair<T>(w[1][i] >> (8 * u), s1, m1, magic);
-          const uint32_t a2 = q4_pair<T>(w[0][i] >> (8 * u + 4), s0, m0, magic);
-          const uint32_t a3 = q4_pair<T>(w[1][i] >> (8 * u + 4), s1, m1, magic);
-#pragma unroll
-          for (int f = 0; f < NF; ++f)
-            mma16816<T>(c[f], a0, a1, a2, a3, u ? qf[f][i].z : qf[f][i].x, u ? qf[f][i].w : qf[f][i].y);
+        for (int f = 0; f < NF; ++f) {
+          mma16816<T>(c[f], x0[0], x1[0], x0[1], x1[1], qf[f][i].x, qf[f][i].y);
+          mma16816<T>(c[f], x0[2], x1[2], x0[3], x1[3], qf[f][i].z, qf[f][i].w);
         }
+      }
     }
     const bool bad = (bad_tiles >> t) & 1;
     if (bad || 16 * t + 15 > past - kw) {  // a bad page, or keys that row 0 does not see
@@ -326,21 +326,19 @@ __global__ void __launch_bounds__(kWarps * 32, NF == 1 ? 4 : D == 64 ? 4 : 3) q4
         else w[r][0] = *reinterpret_cast<const uint32_t*>(x);
         p[r] = *reinterpret_cast<const uint32_t*>(st + S::vp + key * S::kPar + g8 * VW / 4 * 4);
       }
-      const uint32_t s01 = __byte_perm(p[0], p[1], 0x5410), m01 = __byte_perm(p[0], p[1], 0x7632);
-      const uint32_t s23 = __byte_perm(p[2], p[3], 0x5410), m23 = __byte_perm(p[2], p[3], 0x7632);
+      const Q4Scale p01 = q4_scale<T>(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[0], p[1], 0x7632));
+      const Q4Scale p23 = q4_scale<T>(__byte_perm(p[2], p[3], 0x5410), __byte_perm(p[2], p[3], 0x7632));
 #pragma unroll
       for (int k = 0; k < VW; ++k) {
-        const uint32_t e01 = __byte_perm(w[0][k], w[1][k], 0x5410);  // even channels of keys 0, 1
-        const uint32_t d01 = __byte_perm(w[0][k], w[1][k], 0x7632);  // odd channels
-        const uint32_t e23 = __byte_perm(w[2][k], w[3][k], 0x5410);
-        const uint32_t d23 = __byte_perm(w[2][k], w[3][k], 0x7632);
+        uint32_t e01[4], d01[4], e23[4], d23[4];  // even and odd channels of keys 0, 1 and of keys 2, 3
+        q4_four<T>(__byte_perm(w[0][k], w[1][k], 0x5410), p01, magic, e01);
+        q4_four<T>(__byte_perm(w[0][k], w[1][k], 0x7632), p01, magic, d01);
+        q4_four<T>(__byte_perm(w[2][k], w[3][k], 0x5410), p23, magic, e23);
+        q4_four<T>(__byte_perm(w[2][k], w[3][k], 0x7632), p23, magic, d23);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t a0 = q4_pair<T>(e01 >> (4 * i), s01, m01, magic), a1 = q4_pair<T>(d01 >> (4 * i), s01, m01, magic);
-          const uint32_t a2 = q4_pair<T>(e23 >> (4 * i), s23, m23, magic), a3 = q4_pair<T>(d23 >> (4 * i), s23, m23, magic);
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int f = 0; f < NF; ++f) mma16816<T>(o[f][k * 4 + i], a0, a1, a2, a3, b0[f], b1[f]);
-        }
+          for (int f = 0; f < NF; ++f) mma16816<T>(o[f][k * 4 + i], e01[i], d01[i], e23[i], d23[i], b0[f], b1[f]);
       }
     }
   }

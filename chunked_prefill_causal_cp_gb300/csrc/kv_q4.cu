@@ -155,9 +155,9 @@ __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(const Q4Args a) {
 
 template <typename T>
 __device__ __forceinline__ uint4 dequantize(uint32_t word, uint32_t params, uint32_t magic) {
-  const uint32_t s2 = q4_scale2(params), m2 = q4_low2(params);
-  return make_uint4(q4_pair<T>(word, s2, m2, magic), q4_pair<T>(word >> 4, s2, m2, magic),
-                    q4_pair<T>(word >> 8, s2, m2, magic), q4_pair<T>(word >> 12, s2, m2, magic));
+  uint32_t r[4];
+  q4_four<T>(word, q4_scale<T>(q4_scale2(params), q4_low2(params)), magic, r);
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 template <typename T, int D>
