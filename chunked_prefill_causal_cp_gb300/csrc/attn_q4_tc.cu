@@ -10,8 +10,7 @@
 // rows.  In place of the TMA producer seven warps convert: a thread takes one
 // group of 32 channels of one key (16 bytes of codes, one pair of parameters,
 // copied ahead to shared memory by cp.async), turns each word into four pairs of
-// 16-bit values (and-or, subtract, fused multiply-add) and stores them, 16 bytes
-// at a time, where the 128-byte-swizzled operand wants them.  The next tile's
+// 16-bit values (cp_q4.cuh) and stores them, 16 bytes at a time, where the 128-byte-swizzled operand wants them.  The next tile's
 // codes are on their way before the current one's are all converted (held in
 // registers instead, they spilled, the loads ran one after another and the kernel
 // took 1.8 times as long).  The values are rounded to 16 bits once, as the cache's
@@ -30,13 +29,13 @@
 // overwritten and O_w rescaled.  O is rescaled only when a row's maximum has grown
 // by more than 2^8.
 //
-// Measured (32/8 heads x 128, bf16): 8128 rows over 8128 cached keys in 1.35 ms, 1.20
-// PFLOP/s, 0.64 of the measured bf16 rate; the 16-bit kernel takes about 1.21 ms for
+// Measured (32/8 heads x 128, bf16): 8128 rows over 8128 cached keys in 1.31 ms, 1.24
+// PFLOP/s, 0.66 of the measured bf16 rate; the 16-bit kernel takes about 1.21 ms for
 // the same rows.  Copies that leave work out: no conversion 1.22 ms, no conversion
 // and no copies of codes 1.15 ms -- the conversion's instructions compete with
 // the softmax's.  On the way: three conversion warps 2.0 ms; lanes by group, with
-// reordered stores, 1.44 ms; 56 / 64 / 80 / 88 control registers 1.67 / 1.35 / 1.38 /
-// 1.41 ms.
+// reordered stores, 1.44 ms; 56 / 64 / 80 / 88 control registers 1.67 / 1.32 / 1.31 /
+// 1.41 ms; twice the blocks for the warp beside the MMA warp 1.36 against 1.32 ms.
 //
 // Merge: each CTA's (max, sum, unnormalised O) of the Q tile that its peer
 // finishes goes to the peer in 16 KB column chunks over distributed shared

@@ -8,10 +8,11 @@ namespace cp {
 
 // Keys per split of a sequence of n keys on the split path: few for a short
 // context, where the wait for one CTA's walk is what counts (one row over 1025
-// keys: 24 us from call to result against 32 with 1024), more for a long one, whose
-// set-up and parts cost less then (4 x 100001 keys: 121 us against 156 with 256).
-// By the sequence's own length alone, so a row's result never depends on what
-// shares the launch.
+// keys: 6.6 us with 256, 8.2 with 512; over 8001 keys: 8.9 with 512, 12.1 with 1024),
+// more for a long one, whose set-up and parts cost less then (4 x 100001 keys: 121
+// us with 1024 against 132 with 512; 64 rows over 512 to 8191 keys would gain 3% from
+// 1024 beyond 4096).  By the sequence's own length alone, so a row's result never
+// depends on what shares the launch.
 __host__ __device__ inline int q4_split_keys(int n) { return n <= 2048 ? 256 : n <= 16384 ? 512 : 1024; }
 __host__ __device__ inline int q4_splits(int n) { return (n - 1) / q4_split_keys(n) + 1; }
 // Most splits of any sequence of up to `ctx` keys.

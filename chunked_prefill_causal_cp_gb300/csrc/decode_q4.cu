@@ -5,7 +5,7 @@
 // attention per byte, so the path is bound by the bytes of the cache (160 per
 // key and KV head at 128 channels) as long as the codes turn into matrix
 // operands quickly enough: at full bandwidth an SM has some 28 instructions per
-// key, and turning 256 codes into 16-bit values takes 15 of them.  One CTA takes
+// key, and turning 256 codes into 16-bit values takes 13 of them.  One CTA takes
 // 256 to 1024 keys of a (sequence, KV head), four warps a quarter each; the k rows
 // of the sequence times the G heads of the group (k * G <= 16) ride in the columns of
 // m16n8k16 products, so every row shares one read of the cache and one
@@ -35,12 +35,13 @@
 //   finish, counted by tickets, it took as long).  A row's result depends on its own
 //   sequence only.
 //
-// Measured (32/8 heads x 128, bf16): 4 rows over 100001 keys in 113.5 us, of which the
-// merge 6, 4.5 TB/s, 0.67 of a plain copy's rate; DRAM reads equal the cache's bytes;
-// issue slots 70% busy, the integer pipe about 55%.  Leaving out the subtraction,
-// the mask, the shift or the multiply-add of the conversion alone gained 6 to 14%
-// each: the conversion as a whole is what is left.  Two tiles an iteration, three
-// or six ring stages, eight warps, and three, five or six CTAs an SM were no faster.
+// Measured (32/8 heads x 128, bf16): 4 rows over 100001 keys in 106.7 us, of which
+// the split kernel 104, 4.8 TB/s, 0.71 of a plain copy's rate; DRAM reads equal the
+// cache's bytes; 400 instructions a tile, issue slots 69% busy.  Leaving out the
+// subtraction, the mask, the shift or the multiply-add of the conversion alone
+// gained 6 to 14% each (before the shifts went, 7%): the conversion as a whole is
+// what is left.  Two tiles an iteration, three or six ring stages, eight warps,
+// three, five or six CTAs an SM, and KV heads side by side in the grid were no faster.
 #include <cmath>
 #include <cstdint>
 #include <type_traits>

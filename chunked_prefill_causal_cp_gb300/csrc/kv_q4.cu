@@ -10,8 +10,8 @@
 // 32-bit word of codes, the first lane of a group its scale and smallest value.
 // Reading is the reverse: m + c s, rounded once.
 // Both are bound by bytes in principle; the append is held back by its arithmetic
-// (issue slots 72% busy).  8192 rows of 8 KV heads x 128 in bf16, append and read:
-// 18.4 us for 88 MB, 4.8 TB/s; with two IEEE divisions a channel pair it was 26.6 us,
+// (issue slots 73% busy).  8192 rows of 8 KV heads x 128 in bf16, append and read:
+// 18.6 us for 88 MB, 4.7 TB/s; with two IEEE divisions a channel pair it was 26.6 us,
 // with a division near halves only 22.9 (half the warps meet an exact half).
 // Two or four rows a thread were slower (23.9 and 26.5 us against 22.9).
 #include <cmath>
