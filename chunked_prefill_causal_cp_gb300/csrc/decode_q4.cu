@@ -35,8 +35,8 @@
 //   finish, counted by tickets, it took as long).  A row's result depends on its own
 //   sequence only.
 //
-// Measured (32/8 heads x 128, bf16): 4 rows over 100001 keys in 106.7 us, of which
-// the split kernel 104, 4.8 TB/s, 0.71 of a plain copy's rate; DRAM reads equal the
+// Measured (32/8 heads x 128, bf16): 4 rows over 100001 keys in 105.6 us, of which
+// the split kernel 103, 4.85 TB/s, 0.72 of a plain copy's rate; DRAM reads equal the
 // cache's bytes; 400 instructions a tile, issue slots 69% busy.  Leaving out the
 // subtraction, the mask, the shift or the multiply-add of the conversion alone
 // gained 6 to 14% each (before the shifts went, 7%): the conversion as a whole is
@@ -169,18 +169,13 @@ __global__ void __launch_bounds__(kWarps * 32, NF == 1 ? 4 : D == 64 ? 4 : 3) q4
       const uint32_t st = ring + (t % kRing) * S::bytes;
       const uint8_t *k = kc + at * S::kRow, *v = vc + at * S::kRow;
       const uint32_t pd = st + (v_par ? S::vp : S::kp) + (lane & 15) * S::kPar;
-      auto pieces = [&](auto some) {  // the tile's first `left` keys, or all 16
 #pragma unroll
-        for (int i = 0; i < kIter; ++i) {
-          const int e = lane + 32 * i, key = e / kChunks, c = e % kChunks;
-          const bool on = !some || key < left;
-          cp_async<16>(st + S::k + e * 16, k + i * 512, on);
-          cp_async<16>(st + S::v + S::v_at(key, c), v + i * 512, on);
-        }
-        cp_async<S::kPar>(pd, par + at * S::kPar, !some || (lane & 15) < left);
-      };
-      if (left >= 16) pieces(std::false_type());
-      else pieces(std::true_type());
+      for (int i = 0; i < kIter; ++i) {
+        const int e = lane + 32 * i, key = e / kChunks, c = e % kChunks;
+        cp_async<16>(st + S::k + e * 16, k + i * 512, key < left);
+        cp_async<16>(st + S::v + S::v_at(key, c), v + i * 512, key < left);
+      }
+      cp_async<S::kPar>(pd, par + at * S::kPar, (lane & 15) < left);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };

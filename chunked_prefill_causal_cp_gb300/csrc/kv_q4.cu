@@ -130,8 +130,8 @@ __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(const Q4Args a) {
   const bool on = row < (uint32_t)a.total_rows * (uint32_t)a.hkv;
   uint4 kv = make_uint4(0, 0, 0, 0), vv = kv;
   if (on) {
-    kv = __ldg(static_cast<const uint4*>(a.k_new) + (long long)row * V + c);
-    vv = __ldg(static_cast<const uint4*>(a.v_new) + (long long)row * V + c);
+    kv = static_cast<const uint4*>(a.k_new)[(long long)row * V + c];
+    vv = static_cast<const uint4*>(a.v_new)[(long long)row * V + c];
   }
   uint32_t kw, kp, vw, vp;
   quantize<T>(kv, kw, kp);  // shuffles: every lane takes part
