@@ -41,7 +41,9 @@
 // subtraction, the mask, the shift or the multiply-add of the conversion alone
 // gained 6 to 14% each (before the shifts went, 7%): the conversion as a whole is
 // what is left.  Two tiles an iteration, three or six ring stages, eight warps,
-// three, five or six CTAs an SM, and KV heads side by side in the grid were no faster.
+// three, five or six CTAs an SM, and KV heads side by side in the grid were no faster;
+// splits merged in a cluster instead of by the combine kernel took 5.7 instead of 6.6 us
+// for one row over 1025 keys, but 53 instead of 35 for 64 rows over up to 2000.
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
