@@ -188,8 +188,7 @@ int q4_attn_check(const cp_layer_desc* d, const void* q, const cp_q4_cache* c, c
   if (d->num_q_heads > 65535 || (int64_t)num_seqs * plan->max_splits > INT32_MAX ||
       (double)num_seqs * plan->dec_rows * d->num_q_heads > INT32_MAX || 2 * plan->pairs > INT32_MAX)
     return CP_ERR_UNSUPPORTED;
-  const size_t need = cp_workspace_size_q4(d, total_rows, max_ctx, num_seqs);
-  if (!workspace || !aligned16(workspace) || workspace_bytes < need) return CP_ERR_WORKSPACE;
+  if (!workspace || !aligned16(workspace) || (double)workspace_bytes < plan->bytes) return CP_ERR_WORKSPACE;
   return CP_OK;
 }
 
@@ -344,9 +343,12 @@ size_t cp_workspace_size_q4(const cp_layer_desc* desc, int32_t total_rows, int32
   if (check_desc(desc, false) != CP_OK || total_rows <= 0 || max_ctx <= 0 || num_seqs <= 0) return 0;
   const int G = desc->num_q_heads / desc->num_kv_heads;
   if (G > 16 || (G & (G - 1)) || desc->dtype == CP_F32 || desc->kind == CP_CACHE_ROLLING) return 0;
-  // Ragged rows, or equal ones: whichever needs more.
-  double bytes = q4_plan(desc, true, num_seqs, total_rows, max_ctx).bytes;
-  if (total_rows % num_seqs == 0) bytes = std::max(bytes, q4_plan(desc, false, num_seqs, total_rows, max_ctx).bytes);
+  // The split path's rows of any call within these bounds: one of every sequence,
+  // or up to 16 / G of each in a call of equal rows.
+  const int64_t rows = std::max<int64_t>(num_seqs, std::min<int64_t>(total_rows, (int64_t)num_seqs * decode_max_rows(G)));
+  const int splits = q4_max_splits(max_ctx);
+  const double parts = splits > 1 ? (double)rows * desc->num_q_heads * splits : 0.0;
+  const double bytes = (double)(((int64_t)num_seqs * 4 + 255) / 256 * 256) + parts * (desc->head_dim + 2) * sizeof(float);
   return bytes < 4e18 ? (size_t)bytes : SIZE_MAX;
 }
 

@@ -518,9 +518,11 @@ int cp_mixed_step_q4(const cp_layer_desc* desc, const void* q, const void* k_new
                      int32_t* seqlens_k, int32_t num_seqs, int32_t total_rows, int32_t max_ctx, void* out,
                      void* workspace, size_t workspace_bytes, int32_t commit, int32_t* dev_status, void* stream);
 
-/* cp_workspace_size_q4 -- bytes of device scratch cp_chunk_attn_q4 and
- * cp_mixed_step_q4 need for total_rows rows of num_seqs sequences with contexts
- * of up to max_ctx keys (0 for arguments those calls would refuse). */
+/* cp_workspace_size_q4 -- bytes of device scratch that always suffice for
+ * cp_chunk_attn_q4 and cp_mixed_step_q4 with up to total_rows rows of up to
+ * num_seqs sequences and contexts of up to max_ctx keys: a copy of the lengths,
+ * and the split path's parts of up to 16 / G rows per sequence (0 for arguments
+ * those calls would refuse). */
 size_t cp_workspace_size_q4(const cp_layer_desc* desc, int32_t total_rows, int32_t max_ctx, int32_t num_seqs);
 
 /* ---- host-side integer helpers (no GPU work) ---- */

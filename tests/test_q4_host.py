@@ -132,9 +132,15 @@ def test_q4_refusals(call):
 def test_workspace_is_asked_for_and_has_to_be_there():
     d = _desc()
     need = cp.cp_workspace_size_q4(d, 8, 1024, 4)
-    assert need > 0 and cp.cp_workspace_size_q4(d, 4, 1024, 4) <= need
     for call in ("attn", "step"):
         assert _q4(call, ws=None) == WS and _q4(call, ws_bytes=need - 1) == WS and _q4(call, ws=FAKE + 8) == WS
+        assert _q4(call, t=4, n=2, ws_bytes=255) == WS
+    # What suffices for some bounds suffices for every call within them.
+    sizes = {(t, m, n): cp.cp_workspace_size_q4(d, t, m, n) for t in (1, 4, 7, 16, 700) for n in (1, 2, 4)
+             for m in (1, 256, 257, 1024, 2048, 2049, 16384, 16385, 40000)}
+    for (t, m, n), size in sizes.items():
+        for (t2, m2, n2), size2 in sizes.items():
+            assert t2 > t or m2 > m or n2 > n or size2 <= size
     for bad in (_desc(dtype=torch.float32), _desc(kind=cp.CP_CACHE_ROLLING), _desc(num_q_heads=6), _desc(head_dim=96)):
         assert cp.cp_workspace_size_q4(bad, 8, 1024, 4) == 0
     assert cp.cp_workspace_size_q4(d, 0, 1024, 4) == 0 and cp.cp_workspace_size_q4(d, 8, 0, 4) == 0
