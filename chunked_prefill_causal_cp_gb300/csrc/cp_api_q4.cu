@@ -142,6 +142,7 @@ Q4Args q4_args(const cp_layer_desc* d, const cp_q4_cache* c, const SeqRows& rows
 struct Q4Plan {
   int dec_rows;            // rows of a sequence on the split path
   bool split, tensor;      // which paths have sequences
+  bool by_row;             // ragged, no more rows than sequences: the split path takes every row, as single rows
   int max_splits;
   int64_t pairs;           // pairs of Q tiles on the tensor-core path, at most
   int64_t parts;           // (row, head, split) parts, 0 when every context fits one split
@@ -155,7 +156,10 @@ Q4Plan q4_plan(const cp_layer_desc* d, bool ragged, int32_t num_seqs, int32_t to
   const int64_t uniform = total_rows / num_seqs;
   p.dec_rows = !ragged && uniform >= 1 && uniform <= most ? (int)uniform : 1;
   p.split = ragged || uniform == p.dec_rows;
-  p.tensor = ragged ? total_rows > num_seqs : !p.split;
+  // With a row in every sequence no more rows than sequences means one each; with a
+  // sequence without rows others may have several, which the split path then takes.
+  p.by_row = ragged && total_rows <= num_seqs;
+  p.tensor = ragged ? !p.by_row : !p.split;
   p.max_splits = q4_max_splits(max_ctx);
   const int64_t ppt = 2 * (kTcBlockM / std::max(d->num_q_heads / d->num_kv_heads, 1));  // tokens of a pair
   p.pairs = !p.tensor ? 0 : ragged ? (total_rows + ppt - 1) / ppt + num_seqs : num_seqs * ((uniform + ppt - 1) / ppt);
@@ -215,6 +219,7 @@ int q4_attention(const cp_layer_desc* d, const Q4Plan& p, const void* q, const c
   a.out = out;
   a.status = dev_status;
   a.dec_rows = p.dec_rows;
+  a.by_row = p.by_row;
   a.min_rows = p.split ? p.dec_rows + 1 : 1;
   a.max_splits = p.max_splits;
   a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.lens_bytes);

@@ -90,6 +90,7 @@ struct Q4AttnArgs {
   int* status;
   int min_rows;            // tensor-core kernel: sequences with fewer rows are skipped (the split path has them)
   int dec_rows;            // split path: takes the sequences of exactly this many rows (dec_rows * group <= 16)
+  bool by_row;             // split path, dec_rows 1: takes every row of the call (no more than num_seqs), one by one
   int max_splits;
   float* part_o;           // [num_seqs * dec_rows, hq, max_splits, D] unnormalised parts
   float* part_ml;          // [num_seqs * dec_rows, hq, max_splits, 2] their maximum (log2 domain) and sum

@@ -35,7 +35,7 @@
 //   finish, counted by tickets, it took as long).  A row's result depends on its own
 //   sequence only.
 //
-// Measured (32/8 heads x 128, bf16): 4 rows over 100001 keys in 105.6 us, of which
+// Measured (32/8 heads x 128, bf16): 4 rows over 100001 keys in 105.0 us, of which
 // the split kernel 103, 4.85 TB/s, 0.72 of a plain copy's rate; DRAM reads equal the
 // cache's bytes; 400 instructions a tile, issue slots 69% busy.  Leaving out the
 // subtraction, the mask, the shift or the multiply-add of the conversion alone
@@ -106,7 +106,50 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
   }
 }
 
-// kOne: sequences of one row, which sees every key.
+// The rows that a slot of the split path's grid takes: kr of them, from place `first`
+// of sequence s on, a sequence of n rows.
+struct SlotRows {
+  int s, first, n;
+  int past, row0;  // keys before the slot's first row, and that row's place in the call
+};
+
+// (Out of line: a well-formed call never comes here.)
+__device__ __noinline__ SlotRows slot_of_row(SeqRows rows, int row) {
+  SlotRows r;
+  r.s = row_seq(rows, row);
+  r.first = row_place(rows, r.s, row);
+  r.n = seq_rows(rows, r.s);
+  return r;
+}
+
+// Slot i takes sequence i, if that has exactly kr rows.  by_row, for a ragged call with
+// no more rows than sequences: it takes row i, whichever sequence that belongs to.  In a
+// batch of single rows that is the same; where some sequences have no rows, so others
+// may have several, every row still finds a slot (no tensor-core kernel follows).
+__device__ __forceinline__ bool slot_rows(const Q4AttnArgs& a, int i, int kr, bool by_row, SlotRows& r) {
+  r.s = i;
+  r.first = 0;
+  r.n = seq_rows(a.rows, i);
+  if (!by_row) return r.n == kr;
+  if (r.n != 1 || seq_row0(a.rows, i) != i) {
+    if (i >= a.total_rows) return false;
+    r = slot_of_row(a.rows, i);
+    if (r.first < 0) return false;
+  }
+  return true;
+}
+
+// Whether the call's bounds allow the slot's sequence; its place, if so.
+__device__ __forceinline__ bool slot_place(const Q4AttnArgs& a, SlotRows& r) {
+  r.past = a.past[r.s];
+  r.row0 = seq_row0(a.rows, r.s);
+  if (r.past < 0 || (long long)r.past + r.n > a.max_ctx || r.row0 < 0 || r.row0 > a.total_rows - r.n) return false;
+  r.past += r.first;
+  r.row0 += r.first;
+  return true;
+}
+
+// kOne: single rows, which see every key.
 template <typename T, int D, int NF, bool kOne>
 __global__ void __launch_bounds__(kWarps * 32, NF == 1 ? 4 : D == 64 ? 4 : 3) q4_split_kernel(const Q4AttnArgs a) {
   constexpr int NC = 8 * NF;     // (row, head) columns
@@ -119,21 +162,20 @@ __global__ void __launch_bounds__(kWarps * 32, NF == 1 ? 4 : D == 64 ? 4 : 3) q4
   __shared__ float sM[kWarps][NC], sL[kWarps][NC];
 
   pdl_launch_dependents();
-  const int split = blockIdx.x % a.max_splits, s = blockIdx.x / a.max_splits, gk = blockIdx.y;
+  const int split = blockIdx.x % a.max_splits, slot = blockIdx.x / a.max_splits, gk = blockIdx.y;
   pdl_wait();  // everything below reads what earlier kernels wrote
   if (a.commit_lens && blockIdx.x == 0 && blockIdx.y == 0)  // `past` is a copy: the lengths may advance at once
     for (int i = threadIdx.x; i < a.rows.num_seqs; i += kWarps * 32) a.commit_lens[i] += seq_rows(a.rows, i);
-  const int rows = seq_rows(a.rows, s);
   const bool reports = a.status && split == 0 && gk == 0 && threadIdx.x == 0;
-  if (reports && rows < 1) atomicOr(a.status, CP_DEV_BOUNDS);
+  if (reports && seq_rows(a.rows, slot) < 1) atomicOr(a.status, CP_DEV_BOUNDS);
   const int kr = kOne ? 1 : a.dec_rows;
-  if (rows != kr) return;
-  const int past = a.past[s];
-  const int row0 = seq_row0(a.rows, s);
-  if (past < 0 || (long long)past + kr > a.max_ctx || row0 < 0 || row0 > a.total_rows - kr) {
+  SlotRows mine;
+  if (!slot_rows(a, slot, kr, kOne && a.by_row, mine)) return;
+  if (!slot_place(a, mine)) {
     if (reports) atomicOr(a.status, CP_DEV_BOUNDS);
     return;
   }
+  const int s = mine.s, past = mine.past, row0 = mine.row0;
   const int n = past + kr;  // keys, this call's rows among them
   const int split_keys = q4_split_keys(n), warp_keys = split_keys / kWarps;  // at most 256: a lane knows one tile's place
   if (split > (n - 1) / split_keys) return;
@@ -396,7 +438,7 @@ __global__ void __launch_bounds__(kWarps * 32, NF == 1 ? 4 : D == 64 ? 4 : 3) q4
       b.y = Pack<T>::store(r + 2);
       *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (row * a.hq + h) * D + 4 * d4) = b;
     } else {
-      const long long part = (((long long)s * kr + (c >> lg)) * a.hq + h) * a.max_splits + split;
+      const long long part = (((long long)slot * kr + (c >> lg)) * a.hq + h) * a.max_splits + split;
       *reinterpret_cast<float4*>(a.part_o + part * D + 4 * d4) = make_float4(v[0], v[1], v[2], v[3]);
       if (d4 == 0) {
         a.part_ml[part * 2] = mc;
@@ -460,25 +502,38 @@ __global__ void __launch_bounds__(kCombineThreads) q4_combine_kernel(const Q4Att
   pdl_wait();
   const int kr = a.dec_rows;
   const int d4 = threadIdx.x % C4, slice = threadIdx.x / C4 % kSlices, pair = threadIdx.x / (C4 * kSlices);
-  const long long id = (long long)blockIdx.x * kPer + pair;  // (sequence, row, head)
+  const long long id = (long long)blockIdx.x * kPer + pair;  // (slot, row, head)
   const long long sr = id / a.hq;
-  const int h = (int)(id % a.hq), s = (int)(sr / kr), r = (int)(sr % kr);
-  bool on = s < a.rows.num_seqs && seq_rows(a.rows, s) == kr;
-  int past = 0, row0 = 0, nsplit = 0;
+  const int h = (int)(id % a.hq), slot = (int)(sr / kr), r = (int)(sr % kr);
+  SlotRows mine;
+  bool on = slot < a.rows.num_seqs && slot_rows(a, slot, kr, a.by_row, mine);
+  int row0 = 0, nsplit = 0;
   if (on) {
-    past = a.past[s];
-    row0 = seq_row0(a.rows, s);
-    on = past >= 0 && (long long)past + kr <= a.max_ctx && row0 >= 0 && row0 <= a.total_rows - kr;
-    if (on) nsplit = q4_splits(past + kr);  // the last may hold keys of later rows only: a part of weight 0
-    on = on && nsplit > 1;                  // one split: finished by the split kernel
+    on = slot_place(a, mine);
+    row0 = mine.row0;
+    if (on) nsplit = q4_splits(mine.past + kr);  // the last may hold keys of later rows only: a part of weight 0
+    on = on && nsplit > 1;                       // one split: finished by the split kernel
   }
   Part part;
   if (on) {
-#pragma unroll 4
-    for (int i = slice; i < nsplit; i += kSlices) {
-      const long long at = id * a.max_splits + i;
-      part.add(__ldcg(reinterpret_cast<const float2*>(a.part_ml + at * 2)),
-               __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + 4 * d4)));
+    // Four splits' loads on their way together, written out: an unrolled loop came out with them one by one
+    // (the merge of 98 splits 4 us longer).
+    constexpr int kAhead = 4;
+    for (int i0 = slice; i0 < nsplit; i0 += kAhead * kSlices) {
+      float2 ml[kAhead];
+      float4 p[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const long long at = id * a.max_splits + i0 + j * kSlices;
+        if (i0 + j * kSlices >= nsplit) break;
+        ml[j] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + at * 2));
+        p[j] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + 4 * d4));
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (i0 + j * kSlices >= nsplit) break;
+        part.add(ml[j], p[j]);
+      }
     }
   }
   so[pair][slice][d4] = make_float4(part.v[0], part.v[1], part.v[2], part.v[3]);

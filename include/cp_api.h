@@ -486,9 +486,9 @@ int cp_kv_read_q4(const cp_layer_desc* desc, const cp_q4_cache* cache, const int
  *   q, out        device [total_rows, Hq, D]; out must not overlap q, the
  *                 cache or the workspace
  *   cu_rows       device int32 [num_seqs + 1], every sequence with at least one
- *                 row (one without sets CP_DEV_BOUNDS), or NULL: total_rows /
- *                 num_seqs rows each.  Rows of out from cu_rows[num_seqs] on are
- *                 left as they were
+ *                 row (one without sets CP_DEV_BOUNDS; the others are computed all
+ *                 the same), or NULL: total_rows / num_seqs rows each.  Rows of out
+ *                 from cu_rows[num_seqs] on are left as they were
  *   max_ctx       host bound on seqlens_k[s] + rows of s, below 2^31 - 4096; a
  *                 sequence outside it is skipped (its rows of out are left as they
  *                 were) and sets CP_DEV_BOUNDS.  A page id out of range sets it

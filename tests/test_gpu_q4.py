@@ -456,3 +456,43 @@ def test_prompt_then_decode_with_norm_and_rotation():
         span = np.ptp(want.reshape(-1, hkv, d // 32, 32), axis=-1)
         off = np.abs(k - want).reshape(-1, hkv, d // 32, 32).max(-1)
         assert (off <= 0.62 * span / 15 + 2.0 ** -7 * np.abs(want).max()).all()
+
+
+@pytest.mark.parametrize("rows", [[0, 2], [2, 0], [1, 0, 2], [0, 0, 3, 1], [0, 0, 0, 2, 1, 0, 0], [1, 1, 1]])
+@pytest.mark.parametrize("hq,hkv,d,dtype,page", [(8, 2, 128, BF16, 16), (4, 4, 64, F16, 0)])
+def test_fewer_rows_than_sequences(rows, hq, hkv, d, dtype, page):
+    """Listed sequences without rows are reported; every row of the others is computed, however few there are."""
+    n, t = len(rows), sum(rows)
+    past = [300, 40, 600, 17, 513, 5, 250][:n]
+    g = torch.Generator().manual_seed(t)
+    q, k, v = (torch.randn(t, h, d, generator=g).to(dtype).cuda() for h in (hq, hkv, hkv))
+    outs = []
+    for step in (False, True):
+        c = Cache4(dtype, hq, hkv, d, n, 640, page)
+        c.fill(past)
+        out, lens, ws = torch.full_like(q, float("nan")), _ints(past), c.workspace(t, 640)
+        kw = dict(cu_rows=_cu(rows), block_table=c.table, dev_status=c.status)
+        if step:
+            cp.cp_mixed_step_q4(c.desc, q, k, v, c.arg, lens, n, t, 640, out, ws, **kw)
+        else:
+            cp.cp_kv_append_q4(c.desc, k, v, c.arg, lens, n, t, 640, **kw)
+            cp.cp_chunk_attn_q4(c.desc, q, c.arg, lens, n, t, 640, out, ws, **kw)
+        assert int(c.status) == (cp.CP_DEV_BOUNDS if 0 in rows else 0)
+        assert lens.tolist() == [p + r for p, r in zip(past, rows)]
+        keep = [i for i in range(n) if rows[i]]
+        check_attention(c, q, out, [past[i] for i in keep], [rows[i] for i in keep], seqs=keep)
+        outs.append(out)
+    assert torch.equal(*outs)
+
+
+def test_fewer_rows_than_sequences_out_of_bounds():
+    """A sequence whose rows do not all fit is left alone as a whole, its first row too."""
+    c = Cache4(BF16, 4, 2, 64, 4, 128)
+    c.fill([128] * 4)
+    q = torch.randn(4, 4, 64, device="cuda").bfloat16()
+    out = torch.full_like(q, 5.0)
+    cp.cp_chunk_attn_q4(c.desc, q, c.arg, _ints([10, 127, 10, 30]), 4, 4, 128, out, c.workspace(4, 128), commit=False,
+                        cu_rows=_ints([0, 0, 2, 2, 4]), dev_status=c.status)
+    assert int(c.status) == cp.CP_DEV_BOUNDS
+    assert (out[:2] == 5.0).all()
+    check_attention(c, q[2:], out[2:], [30], [2], seqs=[3])
