@@ -16,16 +16,18 @@
 // cosines are computed once per warp, each row group taking EPC / RPW of the pairs.
 // The arithmetic is in packed pairs of fp32.
 // Measured (32/8 heads x 128, bf16, rows of a fused projection): 8192 rows in
-// 29.8 us, 5.6 TB/s of the bytes read and written, 0.83 of a plain copy's rate (with
+// 30.1 us, 5.6 TB/s of the bytes read and written, 0.83 of a plain copy's rate (with
 // 79 registers and fewer CTAs an SM 32.6 us, with 64 or fewer 29.9 to 35); one row
 // 2.3 us, a launch's length.
 //
 // Angles: inv_freq is turned into a 64-bit fixed-point fraction of a turn per
 // position (integer product of its significand with 2^66 / 2 pi), so
 // position * step mod 2^64 is the angle mod one turn for any int32 position,
-// with no reduction error to speak of.  Its top 32 bits go to sincospif: the
-// angle's error is below 2^-23 (half a unit of the fraction's float), whatever
-// the position.
+// with no reduction error to speak of.  The nearest quarter turn comes off in whole
+// numbers too, and the top 32 bits of the rest, at most an eighth of a turn, go to
+// sincospif as a float: the angle's error is below 2^-25 (half a unit of that float,
+// 2^-25.4, and the cut bits), whatever the position.  (With the whole turn as one float it
+// was 2^-23.3, and 8192 rows took 29.9 instead of 30.1 us.)
 #include <algorithm>
 #include <cstdint>
 
@@ -50,6 +52,16 @@ __device__ __forceinline__ uint64_t turn_step(float f) {
   else if (shift > 0) r = (hi << (64 - shift)) | (lo >> shift);
   else r = shift > -64 ? lo << -shift : 0;
   return (b >> 31) ? 0 - r : r;
+}
+
+// Sine and cosine of a fraction of a turn.
+__device__ __forceinline__ void sincos_turns(uint64_t turns, float* sn, float* cs) {
+  float s, c;
+  sincospif((float)(int)(turns >> 30) * 0x1p-33f, &s, &c);  // the rest: bits 30 to 61, signed
+  const uint32_t q = (uint32_t)((turns + (1ull << 61)) >> 62);
+  const float a = q & 1 ? c : s, b = q & 1 ? s : c;  // of q quarter turns more
+  *sn = q & 2 ? -a : a;
+  *cs = (q + 1) & 2 ? -b : b;
 }
 
 template <typename T, int D>
@@ -122,8 +134,7 @@ __global__ void __launch_bounds__(kRopeThreads, 6) qk_rope_kernel(const RopeArgs
       c[i] = 1.f;
       n[i] = 0.f;
       if (rot) {
-        const uint64_t turns = (uint64_t)ang * turn_step(a.inv_freq[l * E + rg * S::kShare + i]);
-        sincospif((float)(int)(turns >> 32) * 0x1p-31f, &n[i], &c[i]);
+        sincos_turns((uint64_t)ang * turn_step(a.inv_freq[l * E + rg * S::kShare + i]), &n[i], &c[i]);
       }
     }
     auto of = [&](const float* x, int e) {

@@ -370,9 +370,9 @@ typedef struct {
  *   y = x / sqrt(mean(x^2) + eps) * w     (w = q_weight or k_weight [D]; NULL: y = x, no norm)
  *   (a, b) -> (a cos u - b sin u, b cos u + a sin u) for the pairs i = 0 .. rot_dim / 2 - 1 of
  *   the first rot_dim channels, u = position(t) * inv_freq[i];  other channels: y
- * rounded once, to the layer's type, at the end.  The angle is exact for every
- * int32 position: it is reduced in 64-bit fixed-point turns before its sine and
- * cosine are taken.
+ * rounded once, to the layer's type, at the end.  The angle is within 2^-25 for every
+ * int32 position: it is reduced in 64-bit fixed-point turns, down to an eighth of a
+ * turn, before its sine and cosine are taken.
  *   q, k          device rows of [Hq, D] and [Hkv, D]; row t starts row_stride
  *                 elements after row t - 1 (0 = dense; else at least the row's
  *                 own elements and a multiple of 16 bytes), so that both may be

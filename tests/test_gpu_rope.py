@@ -188,3 +188,36 @@ def test_ring_with_more_rows_than_slots_keeps_the_newest():
     assert (vc[:2] == 9.0).all()
     for pos in range(2, 6):
         assert torch.equal(vc[2, :, pos % cap], v[pos]) and torch.equal(kc[2, :, pos % cap], k[pos])
+
+
+def test_angles_to_the_last_places():
+    """(1, 0) turned by an angle is its cosine and sine: an ulp of the function's own (CUDA's bound for sincospif) and
+    an angle within 2^-25, wherever in the turn it falls."""
+    t, d = 4096, 128
+    g = torch.Generator().manual_seed(31)
+    pos = torch.randint(-2 ** 31, 2 ** 31, (t,), generator=g, dtype=torch.int64)
+    pos[:2048] = torch.arange(2048)
+    x = torch.zeros(t, 1, d)
+    x[..., :d // 2] = 1
+    x = x.cuda()
+    freq = torch.cat([_freqs(64), torch.rand(32, generator=g).cuda() * 3])
+    y = torch.empty_like(x)
+    cp.cp_qk_norm_rope(_desc(F32, 1, 1, d), cp.qk_prep(d), x, None, y, None, 1, t, inv_freq=freq,
+                       positions=pos.int().cuda())
+    u = _reduced(pos.numpy(), f64(freq))
+    for got, want, slope in ((y[:, 0, :d // 2], np.cos(u), np.sin(u)), (y[:, 0, d // 2:], np.sin(u), np.cos(u))):
+        tol = np.spacing(np.abs(want).astype(np.float32)).astype(np.float64) + 2.0 ** -25 * np.abs(slope)
+        off = np.abs(f64(got) - want)
+        assert (off <= tol).all(), float((off / tol).max())
+
+
+def _reduced(pos, freq):
+    """pos * freq in [0, 2 pi), by whole-number arithmetic: a product of floats has no error in 64 bits, but whole turns
+    taken off it there would."""
+    two_pi = 0x6487ED5110B4611A62633145C06E0E68948127044533E63A0105DF  # 2 pi * 2^212
+    out = np.empty((len(pos), len(freq)))
+    for j, f in enumerate(freq.tolist()):
+        num, den = f.as_integer_ratio()
+        for i, p in enumerate(pos.tolist()):
+            out[i, j] = ((p * num << 212) // den) % two_pi / 2 ** 212
+    return out
