@@ -229,7 +229,7 @@ cudaError_t launch_t(RopeArgs a, cudaStream_t st) {
   const int blocks = (heads + S::kRows - 1) / S::kRows;
   // One warp per token does a token's angles once; with fewer tokens than warps
   // that fill the GPU (152 SMs x 32), a token's blocks are shared out over more.
-  const int splits = std::min<long long>(blocks, (152 * 32 + a.total_rows - 1) / a.total_rows);
+  const int splits = (int)std::min<long long>(blocks, (152LL * 32 + a.total_rows - 1) / a.total_rows);
   const int per_warp = (blocks + splits - 1) / splits;
   const dim3 grid((unsigned)(((long long)a.total_rows * 32 + kRopeThreads - 1) / kRopeThreads),
                   (unsigned)((blocks + per_warp - 1) / per_warp));

@@ -1,6 +1,9 @@
 """Refusals of the query/key preparation and of the 4-bit cache's calls, made on
 the host before anything is enqueued, and the 64-bit restatement's own pins."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -195,3 +198,23 @@ def test_norm_rope_pins():
     assert np.allclose(y[0, 0, :2], [3 / r, 4 / r]) and np.allclose(y[1, 0, :2], [-4 / r, 3 / r])
     y, _ = q4.norm_rope(x, None, [0, 1], np.array([np.pi / 2] * 8), 16, False, 0.0)
     assert np.allclose(y[1, 0, [0, 8, 1, 9]], [0, 3, 0, 4])
+
+
+HUGE_ROWS = """
+import ctypes, sys
+import chunked_prefill_causal_cp_gb300 as cp
+d, p = cp.layer_desc(cp.CP_BF16, 1, 4, 1, 128, capacity=64), cp.qk_prep(0)
+at = [i << 50 for i in range(1, 5)]
+for t in (2 ** 31 - 1, 2 ** 31 - 4863, 2 ** 31 - 4864):
+    s = cp.lib().cp_qk_norm_rope(ctypes.byref(d), ctypes.byref(p), at[0], 0, at[1], 0, None, None, None, at[0], None, None,
+                                 1, t, at[2], at[3], None)
+    assert s == cp.CP_ERR_CUDA, s
+"""
+
+
+def test_any_number_of_rows_is_answered_with_a_status():
+    """In a process of its own, as a fault on the host would end it, and without a GPU, as its buffers are none."""
+    env = {**os.environ, "CUDA_VISIBLE_DEVICES": ""}
+    r = subprocess.run([sys.executable, "-c", HUGE_ROWS], env=env, cwd=os.path.dirname(os.path.dirname(__file__)),
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, (r.returncode, r.stderr)
