@@ -356,13 +356,15 @@ def qk_prep(rot_dim, interleaved=False, eps=1e-6) -> QKPrep:
 
 
 def q4_cache(k_codes, v_codes, k_params, v_params) -> Q4Cache:
-    """The arrays of a 4-bit cache: uint8 codes [..., D / 2] and params [..., D / 32, 2] of the layer's type."""
+    """The arrays of a 4-bit cache, on one device: uint8 codes [..., D / 2] and params [..., D / 32, 2] of the layer's
+    type."""
     for c, p in ((k_codes, k_params), (v_codes, v_params)):
         if (c.dtype != torch.uint8 or p.dtype not in (torch.bfloat16, torch.float16) or not c.is_contiguous()
                 or not p.is_contiguous() or not c.is_cuda or not p.is_cuda or p.dim() < 2 or p.shape[-1] != 2
                 or tuple(c.shape) != (*p.shape[:-2], p.shape[-2] * 16)):
             _refuse("q4_cache")
-    if k_codes.shape != v_codes.shape or k_params.dtype != v_params.dtype:
+    if (k_codes.shape != v_codes.shape or k_params.dtype != v_params.dtype
+            or len({x.get_device() for x in (k_codes, v_codes, k_params, v_params)}) != 1):
         _refuse("q4_cache")
     c = Q4Cache(k_codes.data_ptr(), v_codes.data_ptr(), k_params.data_ptr(), v_params.data_ptr())
     c.tensors = (k_codes, v_codes, k_params, v_params)

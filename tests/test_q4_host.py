@@ -218,3 +218,31 @@ def test_any_number_of_rows_is_answered_with_a_status():
     r = subprocess.run([sys.executable, "-c", HUGE_ROWS], env=env, cwd=os.path.dirname(os.path.dirname(__file__)),
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, (r.returncode, r.stderr)
+
+
+class On:
+    """A CPU tensor that says it is on another device."""
+
+    def __init__(self, t, dev):
+        self.t, self.dev, self.is_cuda = t, dev, dev >= 0
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def get_device(self):
+        return self.dev
+
+
+def test_a_cache_lies_on_one_device():
+    codes, params = torch.zeros(1, 2, 16, 64, dtype=torch.uint8), torch.zeros(1, 2, 16, 4, 2, dtype=torch.bfloat16)
+    make = lambda devs: cp.q4_cache(*(On(t.clone(), dev) for t, dev in zip((codes, codes, params, params), devs)))  # noqa: E731
+    cache = make((1, 1, 1, 1))
+    desc = _desc(batch=1, capacity=16)
+    assert cp._q4_arg("call", desc, cache, 1)
+    for dev in (0, 2, -1):
+        with pytest.raises(cp.CPError):
+            cp._q4_arg("call", desc, cache, dev)
+    for other in range(4):
+        with pytest.raises(cp.CPError) as e:
+            make([0 if i == other else 1 for i in range(4)])
+        assert e.value.status == INVALID
