@@ -284,14 +284,15 @@ def _refuse(where):
 
 
 def _device(where, *tensors):
-    """Index of the first tensor's device, which has to be the current one: the library launches there."""
+    """Index of the first tensor's device, which has to be the current one: the library launches there.  The current one
+    when all are raw handles."""
     for t in tensors:
         if isinstance(t, torch.Tensor):
             dev = t.get_device()
             if dev < 0 or dev != torch._C._cuda_getDevice():
                 _refuse(where)
             return dev
-    return 0
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
 
 
 def _on(dev, stream):

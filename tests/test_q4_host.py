@@ -246,3 +246,16 @@ def test_a_cache_lies_on_one_device():
         with pytest.raises(cp.CPError) as e:
             make([0 if i == other else 1 for i in range(4)])
         assert e.value.status == INVALID
+
+
+def test_without_a_tensor_among_the_rows_the_current_device_is_the_calls(monkeypatch):
+    """Raw handles for the rows and tensors for the rest: those have to be where the call launches."""
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
+    assert cp._device("call", FAKE, None) == 1
+    lens = torch.zeros(4, dtype=torch.int32)
+    assert cp._arg("call", On(lens, 1), torch.int32, 4, cp._device("call", FAKE)) == lens.data_ptr()
+    with pytest.raises(cp.CPError):
+        cp._arg("call", On(lens, 0), torch.int32, 4, cp._device("call", FAKE))
+    with pytest.raises(cp.CPError):
+        cp._device("call", On(lens, 0))
