@@ -257,5 +257,3 @@ def test_without_a_tensor_among_the_rows_the_current_device_is_the_calls(monkeyp
     assert cp._arg("call", On(lens, 1), torch.int32, 4, cp._device("call", FAKE)) == lens.data_ptr()
     with pytest.raises(cp.CPError):
         cp._arg("call", On(lens, 0), torch.int32, 4, cp._device("call", FAKE))
-    with pytest.raises(cp.CPError):
-        cp._device("call", On(lens, 0))
