@@ -30,6 +30,12 @@ int64_t most_rows(const SeqRows& r, int32_t total_rows) {
   return total_rows >= r.num_seqs ? (int64_t)total_rows - r.num_seqs + 1 : total_rows;
 }
 
+// Whether every array of 32-bit numbers starts on its own boundary.
+template <typename... P>
+bool aligned4(const P*... p) {
+  return ((reinterpret_cast<uintptr_t>(p) | ...) & 3u) == 0;
+}
+
 bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
@@ -62,7 +68,7 @@ int rope_check(const cp_layer_desc* d, const cp_qk_prep* p, const void* q, int64
   if ((q != nullptr) != (q_out != nullptr)) return CP_ERR_INVALID_ARG;
   if (total_rows > 0 && p->rot_dim > 0 && !inv_freq) return CP_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(q_weight) || !aligned16(k_weight) || !aligned16(q_out) ||
-      (reinterpret_cast<uintptr_t>(inv_freq) & 3u))
+      !aligned4(inv_freq))
     return CP_ERR_INVALID_ARG;
   std::memset(a, 0, sizeof(*a));
   a->hq = q ? d->num_q_heads : 0;
@@ -175,8 +181,8 @@ Q4Plan q4_plan(const cp_layer_desc* d, bool ragged, int32_t num_seqs, int32_t to
 // The checks of cp_chunk_attn_q4 and cp_mixed_step_q4, but for the new rows.
 int q4_attn_check(const cp_layer_desc* d, const void* q, const cp_q4_cache* c, const int32_t* seqlens_k,
                   const int32_t* block_table, const int32_t* cu_rows, int32_t num_seqs, int32_t total_rows,
-                  int32_t max_ctx, const void* out, const void* workspace, size_t workspace_bytes, SeqRows* rows,
-                  Q4Plan* plan) {
+                  int32_t max_ctx, const void* out, const void* workspace, size_t workspace_bytes, const int32_t* dev_status,
+                  SeqRows* rows, Q4Plan* plan) {
   int r = q4_check(d, c, total_rows);
   if (r != CP_OK) return r;
   r = rows_of(cu_rows, num_seqs, total_rows, rows);
@@ -184,7 +190,9 @@ int q4_attn_check(const cp_layer_desc* d, const void* q, const cp_q4_cache* c, c
   const int G = d->num_q_heads / d->num_kv_heads;
   if (G > 16 || (G & (G - 1))) return CP_ERR_UNSUPPORTED;
   if (total_rows == 0) return CP_OK;
-  if (!q || !out || !seqlens_k || !aligned16(q) || !aligned16(out)) return CP_ERR_INVALID_ARG;
+  if (!q || !out || !seqlens_k || !aligned16(q) || !aligned16(out) ||
+      !aligned4(seqlens_k, cu_rows, block_table, dev_status))
+    return CP_ERR_INVALID_ARG;
   r = cache_check(d, *rows, total_rows, block_table, max_ctx);
   if (r != CP_OK) return r;
   if (max_ctx > INT32_MAX - 4096) return CP_ERR_UNSUPPORTED;  // key indices run past the context by up to a split
@@ -248,6 +256,7 @@ int cp_qk_norm_rope(const cp_layer_desc* desc, const cp_qk_prep* prep, const voi
   int r = rope_check(desc, prep, q, q_row_stride, k, k_row_stride, q_weight, k_weight, inv_freq, q_out, &a, total_rows);
   if (r != CP_OK) return r;
   if ((k != nullptr) != (k_out != nullptr) || !aligned16(k_out)) return CP_ERR_INVALID_ARG;
+  if (!aligned4(positions, seqlens_k, cu_rows)) return CP_ERR_INVALID_ARG;
   if (positions) {
     if (total_rows < 0) return CP_ERR_INVALID_ARG;
     a.rows = SeqRows{1, total_rows, nullptr};
@@ -290,7 +299,9 @@ int cp_qk_norm_rope_append(const cp_layer_desc* desc, const cp_qk_prep* prep, co
   if (r != CP_OK) return r;
   if (total_rows == 0) return CP_OK;
   if (!q || !k_new || !v_new || !k_cache || !v_cache || !seqlens_k) return CP_ERR_INVALID_ARG;
-  if (!aligned16(v_new) || !aligned16(k_cache) || !aligned16(v_cache)) return CP_ERR_INVALID_ARG;
+  if (!aligned16(v_new) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned4(positions, seqlens_k, cu_rows, block_table, dev_status))
+    return CP_ERR_INVALID_ARG;
   r = cache_check(desc, a.rows, total_rows, block_table, max_ctx);
   if (r != CP_OK) return r;
   const int64_t nq = span(total_rows, a.q_stride, wq, es), oq = span(total_rows, wq, wq, es);
@@ -317,7 +328,9 @@ int cp_kv_append_q4(const cp_layer_desc* desc, const void* k_new, const void* v_
   SeqRows rows;
   r = rows_of(cu_rows, num_seqs, total_rows, &rows);
   if (r != CP_OK || total_rows == 0) return r;
-  if (!k_new || !v_new || !seqlens_k || !aligned16(k_new) || !aligned16(v_new)) return CP_ERR_INVALID_ARG;
+  if (!k_new || !v_new || !seqlens_k || !aligned16(k_new) || !aligned16(v_new) ||
+      !aligned4(seqlens_k, cu_rows, block_table, dev_status))
+    return CP_ERR_INVALID_ARG;
   r = cache_check(desc, rows, total_rows, block_table, max_ctx);
   if (r != CP_OK) return r;
   Q4Args a = q4_args(desc, cache, rows, total_rows, seqlens_k, block_table, max_ctx, dev_status);
@@ -334,7 +347,8 @@ int cp_kv_read_q4(const cp_layer_desc* desc, const cp_q4_cache* cache, const int
   SeqRows rows;
   r = rows_of(cu_rows, num_seqs, total_rows, &rows);
   if (r != CP_OK || total_rows == 0) return r;
-  if (!starts || !aligned16(k_out) || !aligned16(v_out)) return CP_ERR_INVALID_ARG;
+  if (!starts || !aligned16(k_out) || !aligned16(v_out) || !aligned4(starts, cu_rows, block_table, dev_status))
+    return CP_ERR_INVALID_ARG;
   r = cache_check(desc, rows, total_rows, block_table, max_ctx);
   if (r != CP_OK) return r;
   if (!k_out && !v_out) return CP_OK;
@@ -364,7 +378,7 @@ int cp_chunk_attn_q4(const cp_layer_desc* desc, const void* q, const cp_q4_cache
   SeqRows rows;
   Q4Plan plan;
   int r = q4_attn_check(desc, q, cache, seqlens_k, block_table, cu_rows, num_seqs, total_rows, max_ctx, out, workspace,
-                        workspace_bytes, &rows, &plan);
+                        workspace_bytes, dev_status, &rows, &plan);
   if (r != CP_OK || total_rows == 0) return r;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   r = q4_attention(desc, plan, q, cache, seqlens_k, nullptr, block_table, rows, total_rows, max_ctx, out, workspace,
@@ -380,7 +394,7 @@ int cp_mixed_step_q4(const cp_layer_desc* desc, const void* q, const void* k_new
   SeqRows rows;
   Q4Plan plan;
   int r = q4_attn_check(desc, q, cache, seqlens_k, block_table, cu_rows, num_seqs, total_rows, max_ctx, out, workspace,
-                        workspace_bytes, &rows, &plan);
+                        workspace_bytes, dev_status, &rows, &plan);
   if (r != CP_OK || total_rows == 0) return r;
   if (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new)) return CP_ERR_INVALID_ARG;
   // The append keeps a copy of the lengths for the attention to read, so that

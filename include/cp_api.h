@@ -354,6 +354,10 @@ size_t cp_noalloc_scratch_bytes(void);
 size_t cp_workspace_size(const cp_layer_desc* desc, int32_t max_rows, int32_t max_ctx,
                          int32_t num_seqs);
 
+/* In the calls from here to cp_mixed_step_q4 a device array of 32-bit numbers (lengths,
+ * offsets, positions, page ids, frequencies, dev_status) starts on a 4-byte boundary,
+ * every other one on a 16-byte boundary; any other pointer returns CP_ERR_INVALID_ARG. */
+
 /* ---- queries and keys before attention: norm per head and rotary position ---- */
 
 /* What cp_qk_norm_rope does to each head's D channels. */

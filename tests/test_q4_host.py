@@ -257,3 +257,29 @@ def test_without_a_tensor_among_the_rows_the_current_device_is_the_calls(monkeyp
     assert cp._arg("call", On(lens, 1), torch.int32, 4, cp._device("call", FAKE)) == lens.data_ptr()
     with pytest.raises(cp.CPError):
         cp._arg("call", On(lens, 0), torch.int32, 4, cp._device("call", FAKE))
+
+
+def test_whole_number_arguments_lie_on_their_own_boundaries():
+    """Lengths, offsets, positions, page ids and status off a 4-byte boundary: a load there would be a fault on the GPU."""
+    L, odd = cp.lib(), FAKE + 2
+    desc, paged, prep, cache = _desc(), _paged(), cp.qk_prep(128), _cache()
+    q, k, v, qo, ko = (i * FAKE for i in range(1, 6))
+    rope = dict(pos=None, lens=FAKE, cu=FAKE)
+    for name in rope:
+        a = {**rope, name: odd}
+        assert L.cp_qk_norm_rope(ctypes.byref(desc), ctypes.byref(prep), q, 0, k, 0, None, None, FAKE, a["pos"], a["lens"],
+                                 a["cu"], 4, 8, qo, ko, None) == INVALID
+    full = dict(pos=FAKE, cu=FAKE, lens=FAKE, table=FAKE, status=FAKE)
+    for name in full:
+        a = {**full, name: odd}
+        assert L.cp_qk_norm_rope_append(ctypes.byref(paged), ctypes.byref(prep), q, 0, k, 0, v, 0, None, None, FAKE, a["pos"],
+                                        a["cu"], 4, 8, qo, FAKE, FAKE, a["lens"], a["table"], 128, a["status"],
+                                        None) == INVALID
+        if name == "pos":
+            continue
+        d, c, rows = ctypes.byref(paged), ctypes.byref(cache), (a["cu"], 4, 8)
+        ws = (FAKE, 1 << 40, 1, a["status"], None)
+        assert L.cp_kv_append_q4(d, k, v, *rows, c, a["lens"], a["table"], 128, a["status"], None) == INVALID
+        assert L.cp_kv_read_q4(d, c, a["lens"], a["table"], *rows, 128, k, v, a["status"], None) == INVALID
+        assert L.cp_chunk_attn_q4(d, q, c, a["lens"], a["table"], *rows, 128, qo, *ws) == INVALID
+        assert L.cp_mixed_step_q4(d, q, k, v, c, a["table"], a["cu"], a["lens"], 4, 8, 128, qo, *ws) == INVALID
