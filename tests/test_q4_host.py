@@ -283,3 +283,55 @@ def test_whole_number_arguments_lie_on_their_own_boundaries():
         assert L.cp_kv_read_q4(d, c, a["lens"], a["table"], *rows, 128, k, v, a["status"], None) == INVALID
         assert L.cp_chunk_attn_q4(d, q, c, a["lens"], a["table"], *rows, 128, qo, *ws) == INVALID
         assert L.cp_mixed_step_q4(d, q, k, v, c, a["table"], a["cu"], a["lens"], 4, 8, 128, qo, *ws) == INVALID
+
+
+def test_binding_takes_what_fits_and_nothing_else():
+    """Each check of a tensor by itself, on a device (-1, the CPU's) that all of them share."""
+    bf16, i32 = torch.bfloat16, torch.int32
+    x = torch.zeros(8, 8, 128, dtype=bf16)
+    assert cp._arg("call", x, bf16, x.numel(), -1) == x.data_ptr()
+    assert cp._arg("call", x, bf16, 5, -1) == x.data_ptr()  # room to spare
+    assert cp._arg("call", None, bf16, 5, -1) is None and cp._arg("call", FAKE, bf16, 5, -1) == FAKE
+    for bad, dtype, n, dev in ((x, i32, 8, -1), (x, bf16, x.numel() + 1, -1), (x, bf16, 8, 0), (x[:, :4], bf16, 8, -1),
+                               (x.transpose(0, 1), bf16, 8, -1), (x.half(), bf16, 8, -1)):
+        with pytest.raises(cp.CPError) as e:
+            cp._arg("call", bad, dtype, n, dev)
+        assert e.value.status == INVALID
+
+    desc = _desc()
+    rows = lambda t, n=8, heads=8, dev=-1: cp._rows_arg("call", t, desc, heads, n, dev)  # noqa: E731
+    fused = torch.zeros(8, 10 * 128, dtype=bf16)
+    q, k = (y.unflatten(1, (-1, 128)) for y in fused.split([8 * 128, 2 * 128], 1))
+    assert rows(x) == (x.data_ptr(), 0) and rows(q) == (fused.data_ptr(), 1280)
+    assert rows(k, heads=2) == (fused.data_ptr() + 2 * 1024, 1280)
+    assert rows(q.unflatten(0, (2, 4))) == (fused.data_ptr(), 1280) and rows(q[:1], 1) == (fused.data_ptr(), 0)
+    assert rows(q[::2], 4) == (fused.data_ptr(), 2560) and rows(q[:0], 0)[1] == 0
+    assert rows(torch.zeros(8, 1, 256, dtype=bf16)[..., :128], heads=1)[1] == 256
+    one = torch.zeros(1, 8, 128, dtype=bf16)
+    for bad, n, heads, dev in ((x.half(), 8, 8, -1), (x, 8, 8, 0), (x, 7, 8, -1), (x, 8, 4, -1), (x.flatten(1), 8, 8, -1),
+                               (x.transpose(0, 1), 8, 8, -1), (x.flatten(), 8, 8, -1), (one.expand(8, 8, 128), 8, 8, -1),
+                               (torch.zeros(8, 8, 256, dtype=bf16)[..., ::2], 8, 8, -1),
+                               (torch.zeros(8, 8, 256, dtype=bf16)[..., :128], 8, 8, -1),
+                               (torch.zeros(3, 8, 8, 128, dtype=bf16)[:, :4][::2], 8, 8, -1)):
+        with pytest.raises(cp.CPError) as e:
+            rows(bad, n, heads, dev)
+        assert e.value.status == INVALID
+
+    codes, params = torch.zeros(1, 2, 16, 64, dtype=torch.uint8), torch.zeros(1, 2, 16, 4, 2, dtype=bf16)
+    make = lambda kc=codes, vc=codes, kp=params, vp=params: cp.q4_cache(*(On(t, 0) for t in (kc, vc, kp, vp)))  # noqa: E731
+    assert make().k_codes == codes.data_ptr()
+    for kw in (dict(kc=codes.int()), dict(vp=params.float()), dict(kp=params.half()), dict(kc=codes[..., :32]),
+               dict(vc=codes[:, :1]), dict(vp=params[..., :1]), dict(kp=params.transpose(1, 2)), dict(vc=codes.transpose(1, 2)),
+               dict(vc=codes[:, :1], vp=params[:, :1])):
+        with pytest.raises(cp.CPError) as e:
+            make(**kw)
+        assert e.value.status == INVALID
+    cache = make()
+    assert cp._q4_arg("call", _desc(batch=1, capacity=16), cache, 0)
+    for desc in (_desc(batch=1, capacity=17), _desc(batch=2, capacity=16), _desc(batch=1, capacity=16, dtype=torch.float16)):
+        with pytest.raises(cp.CPError) as e:
+            cp._q4_arg("call", desc, cache, 0)
+        assert e.value.status == INVALID
+    with pytest.raises(cp.CPError):
+        cp._workspace("call", torch.zeros(16, 16, dtype=torch.uint8).t()[:3], -1)
+    assert cp._workspace("call", params, -1) == (params.data_ptr(), params.numel() * 2)
