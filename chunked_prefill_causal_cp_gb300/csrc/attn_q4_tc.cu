@@ -10,11 +10,13 @@
 // rows.  In place of the TMA producer seven warps convert: a thread takes one
 // group of 32 channels of one key (16 bytes of codes, one pair of parameters,
 // copied ahead to shared memory by cp.async), turns each word into four pairs of
-// 16-bit values (cp_q4.cuh) and stores them, 16 bytes at a time, where the 128-byte-swizzled operand wants them.  The next tile's
-// codes are on their way before the current one's are all converted (held in
-// registers instead, they spilled, the loads ran one after another and the kernel
-// took 1.8 times as long).  The values are rounded to 16 bits once, as the cache's
-// format defines them; the tensor cores take both operands in the layer's type.
+// 16-bit values (cp_q4.cuh) and stores them, 16 bytes at a time, where the
+// 128-byte-swizzled operand wants them.  The next tile's codes are on their way before
+// the current one's are all converted (held in registers instead, they spilled, the
+// loads ran one after another and the kernel took 1.8 times as long; as it is, 60
+// bytes a thread spill at 128 channels).  The values are rounded to 16 bits once, as
+// the cache's format defines them.  The softmax's weights are rounded to 16 bits too,
+// as the tensor cores take both operands in the layer's type; their sum is not.
 // Keys past the sequence's positions, and keys on a bad page, are written as
 // zeros, so nothing unwritten reaches a product; their scores are masked.
 //
@@ -30,7 +32,7 @@
 // by more than 2^8.
 //
 // Measured (32/8 heads x 128, bf16): 8128 rows over 8128 cached keys in 1.31 ms, 1.24
-// PFLOP/s, 0.66 of the measured bf16 rate; the 16-bit kernel takes about 1.21 ms for
+// PFLOP/s, 0.65 of the measured bf16 rate; the 16-bit kernel takes about 1.21 ms for
 // the same rows.  Copies that leave work out: no conversion 1.22 ms, no conversion
 // and no copies of codes 1.15 ms -- the conversion's instructions compete with
 // the softmax's.  On the way: three conversion warps 2.0 ms; lanes by group, with

@@ -45,7 +45,6 @@ struct RopeArgs {
   void* q_out;
   void* k_out;             // dense rows, without an append
   CacheView cache;
-  int cache_hkv;           // KV heads of the cache
   void* k_cache;
   void* v_cache;
   int max_ctx;

@@ -21,8 +21,8 @@
 //   same order; the sum over channels does not depend on it.
 //   Softmax: a running maximum per column, raised only when a score passes it by
 //   more than 2^8 (a vote per tile; the sums are in fp32 and a weight is at most
-//   2^8), weights in 16 bits for the product with V (the tensor cores take both
-//   operands in the layer's type).
+//   2^8), weights rounded to 16 bits for the product with V (the tensor cores take
+//   both operands in the layer's type), not for their sum.
 //   Output: O^T[16 channels x 8 columns] += V^T P^T.  The weights reach their
 //   operand layout by an 8 x 8 transpose between lanes.  Lane (g, q) holds keys 2q,
 //   2q + 1, 2q + 8, 2q + 9 and the words of D / 8 channels from g * D / 8 on; a byte
@@ -36,8 +36,9 @@
 //   sequence only.
 //
 // Measured (32/8 heads x 128, bf16): 4 rows over 100001 keys in 105.0 us, of which
-// the split kernel 103, 4.85 TB/s, 0.72 of a plain copy's rate; DRAM reads equal the
-// cache's bytes; 400 instructions a tile, issue slots 69% busy.  Leaving out the
+// the split kernel 103, 4.88 TB/s, 0.72 of a plain copy's rate; DRAM reads equal the
+// cache's bytes; 400 instructions a tile, issue slots 68% busy.  Four sequences of 4 rows
+// (16 columns, three CTAs an SM) take 163 us, of 2 rows (8 columns) 119.  Leaving out the
 // subtraction, the mask, the shift or the multiply-add of the conversion alone
 // gained 6 to 14% each (before the shifts went, 7%): the conversion as a whole is
 // what is left.  Two tiles an iteration, three or six ring stages, eight warps,

@@ -10,9 +10,10 @@
 // 32-bit word of codes, the first lane of a group its scale and smallest value.
 // Reading is the reverse: m + c s, rounded once.
 // Both are bound by bytes in principle; the append is held back by its arithmetic
-// (issue slots 73% busy).  8192 rows of 8 KV heads x 128 in bf16, append and read:
-// 18.6 us for 88 MB, 4.7 TB/s; with two IEEE divisions a channel pair it was 26.6 us,
-// with a division near halves only 22.9 (half the warps meet an exact half).
+// (issue slots 73% busy).  8192 rows of 8 KV heads x 128 in bf16: the append 11.2 us
+// and the read 7.5, 44 MB each (3.9 and 5.9 TB/s); one after the other 18.8 us.  With two
+// IEEE divisions a channel pair the two took 26.6 us, with a division near halves only 22.9
+// (half the warps meet an exact half).
 // Two or four rows a thread were slower (23.9 and 26.5 us against 22.9).
 #include <cmath>
 #include <cstdint>

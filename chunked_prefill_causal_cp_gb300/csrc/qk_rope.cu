@@ -16,7 +16,7 @@
 // cosines are computed once per warp, each row group taking EPC / RPW of the pairs.
 // The arithmetic is in packed pairs of fp32.
 // Measured (32/8 heads x 128, bf16, rows of a fused projection): 8192 rows in
-// 30.1 us, 5.6 TB/s of the bytes read and written, 0.83 of a plain copy's rate (with
+// 30.1 us, 5.6 TB/s of the bytes read and written, 0.82 of a plain copy's rate (with
 // 79 registers and fewer CTAs an SM 32.6 us, with 64 or fewer 29.9 to 35); one row
 // 2.3 us, a launch's length.
 //

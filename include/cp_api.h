@@ -375,8 +375,8 @@ typedef struct {
  *   (a, b) -> (a cos u - b sin u, b cos u + a sin u) for the pairs i = 0 .. rot_dim / 2 - 1 of
  *   the first rot_dim channels, u = position(t) * inv_freq[i];  other channels: y
  * rounded once, to the layer's type, at the end.  The angle is within 2^-25 for every
- * int32 position: it is reduced in 64-bit fixed-point turns, down to an eighth of a
- * turn, before its sine and cosine are taken.
+ * int32 position (and |inv_freq| of up to 1024): it is reduced in 64-bit fixed-point
+ * turns, down to an eighth of a turn, before its sine and cosine are taken.
  *   q, k          device rows of [Hq, D] and [Hkv, D]; row t starts row_stride
  *                 elements after row t - 1 (0 = dense; else at least the row's
  *                 own elements and a multiple of 16 bytes), so that both may be
@@ -505,9 +505,13 @@ int cp_kv_read_q4(const cp_layer_desc* desc, const cp_q4_cache* cache, const int
  * Paths: sequences of one row, and calls with equal rows of at most 16 / G each,
  * take a memory-bound split-KV path that reads the cache once for all of a KV
  * head's rows; the others a tensor-core path.  Hq / Hkv must be 1, 2, 4, 8 or 16.
- * On either path a row's result depends only on its own sequence.  Slots past a
- * sequence's positions may hold anything.  A non-finite value makes the rows that
- * see its key non-finite (in its channels or in all), and no other row. */
+ * On either path a row's result depends only on its own sequence (a sequence of 2 ..
+ * 16 / G rows may differ in its last bits between a call of equal rows and a ragged
+ * one, which take different paths).  Scores, softmax sums and outputs are held in 32
+ * bits; the softmax's weights are rounded to the layer's type for their product with
+ * the values, as on the 16-bit caches.  Slots past a sequence's positions may hold
+ * anything.  A non-finite value makes the rows that see its key non-finite (in its
+ * channels or in all), and no other row. */
 int cp_chunk_attn_q4(const cp_layer_desc* desc, const void* q, const cp_q4_cache* cache, int32_t* seqlens_k,
                      const int32_t* block_table, const int32_t* cu_rows, int32_t num_seqs, int32_t total_rows,
                      int32_t max_ctx, void* out, void* workspace, size_t workspace_bytes, int32_t commit,
