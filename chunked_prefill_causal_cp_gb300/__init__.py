@@ -29,6 +29,7 @@ CP_DEV_TIMEOUT = 2
 
 CP_F32, CP_BF16, CP_F16 = 0, 1, 2
 CP_CACHE_CONTIG, CP_CACHE_ROLLING, CP_CACHE_PAGED = 0, 1, 2
+CP_TREE_MAX = 128
 
 DTYPE_CODE = {torch.float32: CP_F32, torch.bfloat16: CP_BF16, torch.float16: CP_F16}
 
@@ -60,6 +61,16 @@ class Q4Cache(ctypes.Structure):
     """Mirror of ``cp_q4_cache``; made by :func:`q4_cache`, it keeps its tensors alive."""
 
     _fields_ = [("k_codes", c_void_p), ("v_codes", c_void_p), ("k_params", c_void_p), ("v_params", c_void_p)]
+
+
+class LatentDesc(ctypes.Structure):
+    """Mirror of ``cp_latent_desc``."""
+
+    _fields_ = [
+        ("dtype", c_int32), ("batch", c_int32), ("num_heads", c_int32), ("latent_dim", c_int32), ("rope_dim", c_int32),
+        ("nope_dim", c_int32), ("v_dim", c_int32), ("kind", c_int32), ("capacity", c_int32), ("page_size", c_int32),
+        ("num_pages", c_int32), ("max_blocks", c_int32), ("scale", c_float),
+    ]
 
 
 class CPError(RuntimeError):
@@ -122,6 +133,18 @@ def lib():
                                        c_size_t, I, P, P]
         L.cp_workspace_size_q4.argtypes = [POINTER(LayerDesc), I, I, I]
         L.cp_workspace_size_q4.restype = c_size_t
+        LD = POINTER(LatentDesc)
+        L.cp_latent_append.argtypes = [LD, POINTER(QKPrep), P, L64, P, L64, P, P, P, P, L64, L64, P, L64, L64, P, I, I,
+                                       P, P, P, I, P, P]
+        L.cp_latent_attn.argtypes = [LD, P, P, P, P, P, P, I, I, I, P, P, c_size_t, I, P, P]
+        L.cp_workspace_size_latent.argtypes = [LD, I, I, I]
+        L.cp_workspace_size_latent.restype = c_size_t
+        L.cp_latent_chunk_attn.argtypes = [LD, P, P, L64, L64, P, L64, P, L64, L64, P, P, I, I, I, P, P, P]
+        L.cp_tree_attn.argtypes = [POINTER(LayerDesc), P, P, P, P, P, P, P, I, I, I, P, P, c_size_t, P, P]
+        L.cp_workspace_size_tree.argtypes = [POINTER(LayerDesc), I, I, I]
+        L.cp_workspace_size_tree.restype = c_size_t
+        L.cp_tree_commit.argtypes = [POINTER(LayerDesc), P, P, P, P, P, P, I, I, I, I, P, P]
+        L.cp_latent_tree_commit.argtypes = [LD, P, P, P, P, P, I, I, I, I, P, P]
         L.cp_status_string.restype = ctypes.c_char_p
         for name in ("cp_kv_append", "cp_pad_chunk", "cp_prefill_chunk_attn", "cp_prefill_chunk",
                      "cp_mixed_step", "cp_mixed_step_overlap", "cp_prefill_varlen", "cp_prefill_varlen_overlap",
@@ -129,7 +152,8 @@ def lib():
                      "cp_query_ladder", "cp_query_width", "cp_aligned_length", "cp_rolling_mask",
                      "cp_schedule", "cp_abi_version", "cp_selftest_bounded_wait",
                      "cp_qk_norm_rope", "cp_qk_norm_rope_append", "cp_kv_append_q4", "cp_kv_read_q4",
-                     "cp_chunk_attn_q4", "cp_mixed_step_q4"):
+                     "cp_chunk_attn_q4", "cp_mixed_step_q4", "cp_latent_append", "cp_latent_attn",
+                     "cp_latent_chunk_attn", "cp_tree_attn", "cp_tree_commit", "cp_latent_tree_commit"):
             getattr(L, name).restype = c_int32
         _lib = L
     return _lib
@@ -482,6 +506,146 @@ def cp_mixed_step_q4(desc, q, k_new, v_new, cache, seqlens_k, num_seqs, total_ro
 
 def cp_workspace_size_q4(desc, total_rows, max_ctx, num_seqs) -> int:
     return int(lib().cp_workspace_size_q4(ctypes.byref(desc), total_rows, max_ctx, num_seqs))
+
+
+# ---- latent caches and drafted trees; tensors are refused as in the calls above.
+
+def latent_desc(dtype, batch, num_heads, latent_dim, rope_dim, nope_dim=128, v_dim=128, kind=CP_CACHE_CONTIG, capacity=0,
+                page_size=0, num_pages=0, max_blocks=0, scale=0.0) -> LatentDesc:
+    code = DTYPE_CODE[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
+    return LatentDesc(code, batch, num_heads, latent_dim, rope_dim, nope_dim, v_dim, kind, capacity, page_size, num_pages,
+                      max_blocks, scale)
+
+
+def _strided_arg(where, t, dtype, shape, dev):
+    """(pointer, strides of all but the last dimension) of a tensor of exactly this shape whose last dimension is dense
+    and whose strides lead forward.  None and raw handles pass as they are (dense)."""
+    lead = len(shape) - 1
+    if t is None or isinstance(t, int):
+        return (t, *(0,) * lead)
+    if t.dtype is not dtype or t.get_device() != dev or tuple(t.shape) != shape:
+        _refuse(where)
+    if t.numel() == 0 or t.is_contiguous():
+        return (t.data_ptr(), *(0,) * lead)
+    if t.stride(-1) != 1 and shape[-1] > 1:
+        _refuse(where)
+    strides, dense = [], shape[-1]
+    for n, st in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:  # a dimension of one has any stride: the least that the call takes
+            st = dense
+        if st < dense:
+            _refuse(where)
+        strides.append(st)
+        dense = st * n
+    return (t.data_ptr(), *reversed(strides))
+
+
+def _slots(desc):
+    return desc.num_pages * desc.page_size if desc.kind == CP_CACHE_PAGED else desc.batch * desc.capacity
+
+
+def cp_latent_append(desc, prep, latent, k_rope, cache, seqlens_k, num_seqs, total_rows, max_ctx, weight=None,
+                     inv_freq=None, positions=None, q_rope=None, q_out=None, cu_rows=None, block_table=None,
+                     dev_status=None, stream=None):
+    """Norm of the latents [T, C], rotary position of the shared keys [T, R] and of the queries' parts [T, H, R], rows
+    into a latent cache (see include/cp_api.h).  All of them may be slices of projections' rows, q_out [T, H, R] of a
+    buffer of wider heads."""
+    w, dt, c, r, i32 = "cp_latent_append", _LAYER_DTYPE.get(desc.dtype), desc.latent_dim, desc.rope_dim, torch.int32
+    dev = _device(w, latent)
+    pl, sl = _strided_arg(w, latent, dt, (total_rows, c), dev)
+    pk, sk = _strided_arg(w, k_rope, dt, (total_rows, r), dev)
+    pq, qr, qh = _strided_arg(w, q_rope, dt, (total_rows, desc.num_heads, r), dev)
+    po, outr, outh = _strided_arg(w, q_out, dt, (total_rows, desc.num_heads, r), dev)
+    lens, cu, table = _seq_args(w, desc, seqlens_k, cu_rows, block_table, num_seqs, dev)
+    s = lib().cp_latent_append(
+        ctypes.byref(desc), ctypes.byref(prep), pl, sl, pk, sk, _arg(w, weight, dt, c, dev),
+        _arg(w, inv_freq, torch.float32, prep.rot_dim // 2, dev), _arg(w, positions, i32, total_rows, dev), pq, qr, qh,
+        po, outr, outh, cu, num_seqs, total_rows, _arg(w, cache, dt, _slots(desc) * (c + r), dev), lens, table, max_ctx,
+        _arg(w, dev_status, i32, 1, dev), _on(dev, stream))
+    _check(s, w)
+
+
+def cp_latent_attn(desc, q, cache, seqlens_k, num_seqs, total_rows, max_ctx, out, workspace, parents=None, cu_rows=None,
+                   block_table=None, commit=True, dev_status=None, stream=None):
+    """Attention over a latent cache, absorbed form: rows that follow one another, or with `parents` (and commit=False)
+    the nodes of drafted trees (see include/cp_api.h)."""
+    w, dt, c, r, i32 = "cp_latent_attn", _LAYER_DTYPE.get(desc.dtype), desc.latent_dim, desc.rope_dim, torch.int32
+    n = total_rows * desc.num_heads
+    dev = _device(w, q, out)
+    ws, ws_bytes = _workspace(w, workspace, dev)
+    lens, cu, table = _seq_args(w, desc, seqlens_k, cu_rows, block_table, num_seqs, dev)
+    s = lib().cp_latent_attn(
+        ctypes.byref(desc), _arg(w, q, dt, n * (c + r), dev), _arg(w, cache, dt, _slots(desc) * (c + r), dev), lens, table,
+        _arg(w, parents, i32, total_rows, dev), cu, num_seqs, total_rows, max_ctx, _arg(w, out, dt, n * c, dev), ws,
+        ws_bytes, 1 if commit else 0, _arg(w, dev_status, i32, 1, dev), _on(dev, stream))
+    _check(s, w)
+
+
+def cp_workspace_size_latent(desc, total_rows, max_ctx, num_seqs) -> int:
+    return int(lib().cp_workspace_size_latent(ctypes.byref(desc), total_rows, max_ctx, num_seqs))
+
+
+def cp_latent_chunk_attn(desc, q, k_nope, k_rope, v, out, num_seqs, total_rows, total_keys, cu_rows=None, cu_keys=None,
+                         dev_status=None, stream=None):
+    """Attention of prompt chunks over expanded keys [N, H, nope_dim], shared rotated keys [N, R] and values [N, H,
+    v_dim], which may be slices of wider rows (see include/cp_api.h)."""
+    w, dt, h = "cp_latent_chunk_attn", _LAYER_DTYPE.get(desc.dtype), desc.num_heads
+    dn, r, dv, i32 = desc.nope_dim, desc.rope_dim, desc.v_dim, torch.int32
+    dev = _device(w, q, out)
+    pk, kr, kh = _strided_arg(w, k_nope, dt, (total_keys, h, dn), dev)
+    pr, rr = _strided_arg(w, k_rope, dt, (total_keys, r), dev)
+    pv, vr, vh = _strided_arg(w, v, dt, (total_keys, h, dv), dev)
+    s = lib().cp_latent_chunk_attn(
+        ctypes.byref(desc), _arg(w, q, dt, total_rows * h * (dn + r), dev), pk, kr, kh, pr, rr, pv, vr, vh,
+        _arg(w, cu_rows, i32, num_seqs + 1, dev), _arg(w, cu_keys, i32, num_seqs + 1, dev), num_seqs, total_rows,
+        total_keys, _arg(w, out, dt, total_rows * h * dv, dev), _arg(w, dev_status, i32, 1, dev), _on(dev, stream))
+    _check(s, w)
+
+
+def cp_tree_attn(desc, q, k_cache, v_cache, seqlens_k, parents, num_seqs, total_rows, max_ctx, out, workspace,
+                 cu_rows=None, block_table=None, dev_status=None, stream=None):
+    """Attention of a drafted tree's nodes over a K/V cache (see include/cp_api.h)."""
+    w, dt, d, i32 = "cp_tree_attn", _LAYER_DTYPE.get(desc.dtype), desc.head_dim, torch.int32
+    n, size = total_rows * desc.num_q_heads * d, _slots(desc) * desc.num_kv_heads * d
+    dev = _device(w, q, out)
+    ws, ws_bytes = _workspace(w, workspace, dev)
+    lens, cu, table = _seq_args(w, desc, seqlens_k, cu_rows, block_table, num_seqs, dev)
+    s = lib().cp_tree_attn(
+        ctypes.byref(desc), _arg(w, q, dt, n, dev), _arg(w, k_cache, dt, size, dev), _arg(w, v_cache, dt, size, dev), lens,
+        table, _arg(w, parents, i32, total_rows, dev), cu, num_seqs, total_rows, max_ctx, _arg(w, out, dt, n, dev), ws,
+        ws_bytes, _arg(w, dev_status, i32, 1, dev), _on(dev, stream))
+    _check(s, w)
+
+
+def cp_workspace_size_tree(desc, total_rows, max_ctx, num_seqs) -> int:
+    return int(lib().cp_workspace_size_tree(ctypes.byref(desc), total_rows, max_ctx, num_seqs))
+
+
+def cp_tree_commit(desc, k_cache, v_cache, path, counts, seqlens_k, num_seqs, max_path, max_ctx, block_table=None,
+                   commit=True, dev_status=None, stream=None):
+    """The rows of each sequence's accepted path moved to their places in a K/V cache (see include/cp_api.h)."""
+    w, dt, i32 = "cp_tree_commit", _LAYER_DTYPE.get(desc.dtype), torch.int32
+    size = _slots(desc) * desc.num_kv_heads * desc.head_dim
+    dev = _device(w, k_cache, v_cache)
+    lens, _, table = _seq_args(w, desc, seqlens_k, None, block_table, num_seqs, dev)
+    s = lib().cp_tree_commit(
+        ctypes.byref(desc), _arg(w, k_cache, dt, size, dev), _arg(w, v_cache, dt, size, dev),
+        _arg(w, path, i32, num_seqs * max_path, dev), _arg(w, counts, i32, num_seqs, dev), lens, table, num_seqs, max_path,
+        max_ctx, 1 if commit else 0, _arg(w, dev_status, i32, 1, dev), _on(dev, stream))
+    _check(s, w)
+
+
+def cp_latent_tree_commit(desc, cache, path, counts, seqlens_k, num_seqs, max_path, max_ctx, block_table=None,
+                          commit=True, dev_status=None, stream=None):
+    """cp_tree_commit on a latent cache (see include/cp_api.h)."""
+    w, dt, i32 = "cp_latent_tree_commit", _LAYER_DTYPE.get(desc.dtype), torch.int32
+    dev = _device(w, cache)
+    lens, _, table = _seq_args(w, desc, seqlens_k, None, block_table, num_seqs, dev)
+    s = lib().cp_latent_tree_commit(
+        ctypes.byref(desc), _arg(w, cache, dt, _slots(desc) * (desc.latent_dim + desc.rope_dim), dev),
+        _arg(w, path, i32, num_seqs * max_path, dev), _arg(w, counts, i32, num_seqs, dev), lens, table, num_seqs, max_path,
+        max_ctx, 1 if commit else 0, _arg(w, dev_status, i32, 1, dev), _on(dev, stream))
+    _check(s, w)
 
 
 def cp_noalloc_scratch_bytes() -> int:

@@ -64,6 +64,64 @@ inline float scale_log2(const cp_layer_desc* d) {
   return (float)(sc * 1.4426950408889634);  // log2(e)
 }
 
+// ---- checks that the calls on rows of several sequences share
+
+// The rows of a call: cu_rows, or equal rows when that is NULL.
+inline int rows_of(const int32_t* cu_rows, int32_t num_seqs, int32_t total_rows, SeqRows* out) {
+  if (num_seqs <= 0 || total_rows < 0) return CP_ERR_INVALID_ARG;
+  if (!cu_rows && total_rows % num_seqs != 0) return CP_ERR_INVALID_ARG;
+  *out = SeqRows{num_seqs, cu_rows ? 0 : total_rows / num_seqs, cu_rows};
+  return CP_OK;
+}
+
+// Most rows a sequence of the call can have (every listed one has at least one).
+inline int64_t most_rows(const SeqRows& r, int32_t total_rows) {
+  if (r.rows_uniform > 0) return r.rows_uniform;
+  return total_rows >= r.num_seqs ? (int64_t)total_rows - r.num_seqs + 1 : total_rows;
+}
+
+// Whether every array of 32-bit numbers starts on its own boundary.
+template <typename... P>
+inline bool aligned4(const P*... p) {
+  return ((reinterpret_cast<uintptr_t>(p) | ...) & 3u) == 0;
+}
+
+inline bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
+}
+
+// A row stride in elements: 0 = dense; else at least the row and whole 16-byte pieces.
+inline int stride_of(int64_t given, int64_t dense, int es, long long* out) {
+  if (given != 0 && (given < dense || given % (16 / es) != 0)) return CP_ERR_INVALID_ARG;
+  if (given > (INT64_MAX >> 34)) return CP_ERR_UNSUPPORTED;  // stride * rows * bytes stays within 64 bits
+  *out = given ? given : dense;
+  return CP_OK;
+}
+
+// Bytes that `rows` rows of `width` elements `stride` apart span.
+inline int64_t span(int64_t rows, int64_t stride, int64_t width, int es) {
+  return rows > 0 ? ((rows - 1) * stride + width) * es : 0;
+}
+
+// Where the call's rows may go: CONTIG, ROLLING and PAGED limits of a call with
+// a host bound on positions.
+inline int cache_check(const cp_layer_desc* d, const SeqRows& rows, int32_t total_rows, const int32_t* block_table,
+                       int32_t max_ctx) {
+  if (max_ctx <= 0) return CP_ERR_INVALID_ARG;
+  if (d->kind == CP_CACHE_PAGED) {
+    if (!block_table) return CP_ERR_INVALID_ARG;
+  } else if (rows.num_seqs > d->batch) {
+    return CP_ERR_INVALID_ARG;
+  }
+  if (d->kind == CP_CACHE_ROLLING) {
+    if (most_rows(rows, total_rows) > d->capacity) return CP_ERR_CAPACITY;
+  } else if ((int64_t)max_ctx > layout_limit(d)) {
+    return CP_ERR_CAPACITY;
+  }
+  return CP_OK;
+}
+
 // ---- tensor maps (driver entry point fetched through the runtime)
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,

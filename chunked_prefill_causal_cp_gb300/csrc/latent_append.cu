@@ -1,0 +1,151 @@
+// latent_append.cu -- rows into a latent cache: norm of the latents, rotary
+// position of the shared keys and of the queries' rotated parts.
+//
+//   x[0, C) = c * rsqrt(mean(c^2) + eps) * w;  (a, b) -> (a cos u - b sin u, b cos u + a sin u)
+//
+// A warp takes a token (or, with few tokens, a share of its heads).  The latent's
+// 16-byte chunks are spread over its lanes, two a lane at most; a head's R
+// channels belong to R / 16 lanes of two chunks each, chosen so that both members
+// of every rotated pair are in one lane (half-split pairs: chunks l and l + P;
+// adjacent pairs: chunks 2l and 2l + 1; the lanes from P on hold unrotated chunks
+// two by two), so nothing but the sum of squares crosses lanes.  Lane j computes the
+// sine and cosine of the token's pair j once, and the others fetch them by shuffles.
+#include <algorithm>
+#include <cstdint>
+
+#include "cp_latent.h"
+#include "cp_rope.cuh"
+#include "cp_rows.cuh"
+
+namespace cp {
+namespace {
+
+constexpr int kThreads = 128;
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentAppendArgs a, int per_warp) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const long long t_wide = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 5;
+  if (t_wide >= a.total_rows) return;
+  const int t = (int)t_wide;
+  const int s = row_seq(a.rows, t), place = row_place(a.rows, s, t);
+  if (place < 0) return;  // a padded batch's row: the whole warp has it
+  const long long pos = (long long)a.past[s] + place;
+  const long long row = cache_row(a.cache, 1, s, 0, pos, a.max_ctx);
+  T* dst = static_cast<T*>(a.dst) + row * (a.c + a.r);
+  if (blockIdx.y == 0) {
+    if (row < 0) {
+      if (a.status && lane == 0) atomicOr(a.status, CP_DEV_BOUNDS);
+    } else {
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.latent) + t * a.latent_stride);
+      const int n = a.c / 8;
+      uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (lane + 32 * i < n) v[i] = src[lane + 32 * i];
+      if (a.weight) {
+        float x[2][8], ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          unpack16<T>(v[i], x[i]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) ss = fmaf(x[i][e], x[i][e], ss);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float k = rsqrtf(ss / (float)a.c + a.eps);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (lane + 32 * i >= n) continue;
+          float w[8];
+          unpack16<T>(reinterpret_cast<const uint4*>(a.weight)[lane + 32 * i], w);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[i][e] = x[i][e] * k * w[e];
+          v[i] = pack16<T>(x[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (lane + 32 * i < n) reinterpret_cast<uint4*>(dst)[lane + 32 * i] = v[i];
+    }
+  }
+  if (a.r == 0) return;
+
+  // ---- rotated parts: head h < H is a query's, head H the key's
+  const int L = a.r / 16, R = 32 / L;  // lanes of a head, heads of a step
+  const int l = lane % L, rg = lane / L;
+  const bool rot = l < a.pairs;
+  float sn = 0.f, cs = 1.f;
+  if (lane < a.pairs * 8)
+    sincos_turns((uint64_t)(a.positions ? (long long)a.positions[t] : pos) * turn_step(a.inv_freq[lane]), &sn, &cs);
+  float c[8], n[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    c[e] = __shfl_sync(0xffffffffu, cs, (l * 8 + e) & 31);
+    n[e] = __shfl_sync(0xffffffffu, sn, (l * 8 + e) & 31);
+  }
+  int c0 = 2 * l, c1 = 2 * l + 1;
+  if (!a.interleaved && rot) {
+    c0 = l;
+    c1 = l + a.pairs;
+  }
+  const int h_begin = (int)blockIdx.y * per_warp * R, h_end = min(a.heads + 1, h_begin + per_warp * R);
+  for (int h = h_begin + rg; h < h_end; h += R) {
+    if (rg >= R) break;  // 32 is not a multiple of L
+    const bool is_k = h == a.heads;
+    const uint4* src = reinterpret_cast<const uint4*>(
+        is_k ? static_cast<const T*>(a.k_rope) + t * a.k_stride : static_cast<const T*>(a.q) + t * a.q_row + h * a.q_head);
+    uint4 v0 = src[c0], v1 = src[c1];
+    if (rot) {
+      float x[8], y[8];
+      unpack16<T>(v0, x);
+      unpack16<T>(v1, y);
+      if (a.interleaved) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float p = x[2 * e], q = x[2 * e + 1], u = y[2 * e], w = y[2 * e + 1];
+          x[2 * e] = p * c[e] - q * n[e];
+          x[2 * e + 1] = q * c[e] + p * n[e];
+          y[2 * e] = u * c[e + 4] - w * n[e + 4];
+          y[2 * e + 1] = w * c[e + 4] + u * n[e + 4];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float p = x[e], q = y[e];
+          x[e] = p * c[e] - q * n[e];
+          y[e] = q * c[e] + p * n[e];
+        }
+      }
+      v0 = pack16<T>(x);
+      v1 = pack16<T>(y);
+    }
+    if (is_k && row < 0) continue;
+    uint4* out = reinterpret_cast<uint4*>(is_k ? dst + a.c : static_cast<T*>(a.q_out) + t * a.out_row + h * a.out_head);
+    out[c0] = v0;
+    out[c1] = v1;
+  }
+}
+
+template <typename T>
+cudaError_t launch_t(const LatentAppendArgs& a, cudaStream_t st) {
+  const int blocks = a.r ? (a.heads + 1 + 32 / (a.r / 16) - 1) / (32 / (a.r / 16)) : 1;
+  // One warp per token computes a token's angles once; with fewer tokens than warps that fill the
+  // GPU (152 SMs x 32), a token's blocks are shared out over more.
+  const int splits = (int)std::min<long long>(blocks, (152LL * 32 + a.total_rows - 1) / a.total_rows);
+  const int per_warp = (blocks + splits - 1) / splits;
+  const dim3 grid((unsigned)(((long long)a.total_rows * 32 + kThreads - 1) / kThreads),
+                  (unsigned)((blocks + per_warp - 1) / per_warp));
+  return launch_pdl(latent_append_kernel<T>, grid, dim3(kThreads), 0, st, a, per_warp);
+}
+
+}  // namespace
+
+cudaError_t launch_latent_append(const LatentAppendArgs& a, int dtype, cudaStream_t st) {
+  if (a.total_rows == 0) return cudaSuccess;
+  return dtype == CP_BF16 ? launch_t<__nv_bfloat16>(a, st) : launch_t<__half>(a, st);
+}
+
+}  // namespace cp

@@ -533,6 +533,198 @@ int cp_mixed_step_q4(const cp_layer_desc* desc, const void* q, const void* k_new
  * those calls would refuse). */
 size_t cp_workspace_size_q4(const cp_layer_desc* desc, int32_t total_rows, int32_t max_ctx, int32_t num_seqs);
 
+/* ---- latent caches: keys and values of all heads from one shared vector a token ---- */
+
+/* In the calls from here to cp_tree_commit, as in those above: a device array of 32-bit
+ * numbers starts on a 4-byte boundary, every other one on a 16-byte boundary, and any
+ * other pointer returns CP_ERR_INVALID_ARG. */
+
+/* A layer whose cache holds, for each position, one row of latent_dim + rope_dim
+ * channels that all heads share: a latent x[0, C), of which a head's key and value
+ * are linear maps, and a rotated key part x[C, C + R).
+ *   cache         CONTIG [B, capacity, C + R] or PAGED [num_pages, page_size, C + R]
+ * Two forms of its attention:
+ *   absorbed      a head's key map is folded into its query and its value map into
+ *                 what follows: scores are products of queries of C + R channels with
+ *                 the cache's rows, outputs are mixtures of latents (cp_latent_attn).
+ *                 The cache is read once for all heads: single tokens, short chunks
+ *                 and drafted trees.
+ *   expanded      keys and values of the whole context are multiplied out for every
+ *                 head first (a plain matrix product); scores cost nope_dim + rope_dim
+ *                 channels instead of C + R, outputs v_dim instead of C
+ *                 (cp_latent_chunk_attn): prompt chunks. */
+typedef struct {
+  int32_t dtype;      /* CP_BF16 or CP_F16                                              */
+  int32_t batch;      /* B, sequences of a CONTIG cache                                 */
+  int32_t num_heads;  /* H                                                              */
+  int32_t latent_dim; /* C: 128, 256, 384 or 512                                        */
+  int32_t rope_dim;   /* R: a multiple of 16, 0 .. 64                                   */
+  int32_t nope_dim;   /* channels of an expanded key beside its rotated part: 64 or 128 */
+  int32_t v_dim;      /* channels of an expanded value: 64 or 128                       */
+  int32_t kind;       /* CP_CACHE_CONTIG or CP_CACHE_PAGED                              */
+  int32_t capacity;   /* CONTIG: slots per sequence                                     */
+  int32_t page_size;  /* PAGED: tokens per page (16, 32, 64 or 128)                     */
+  int32_t num_pages;  /* PAGED: pages in the pool                                       */
+  int32_t max_blocks; /* PAGED: columns of block_table                                  */
+  float scale;        /* softmax scale; 0 selects 1/sqrt(nope_dim + rope_dim)           */
+} cp_latent_desc;
+
+/* cp_latent_append -- root-mean-square norm of the latents, rotary position of the
+ * shared keys (and of the queries' rotated parts), rows into the cache, one launch.
+ *
+ * For each row t, with c its latent and k its R key channels, in 32 bits:
+ *   x[0, C)     = c / sqrt(mean(c^2) + eps) * weight     (weight NULL: c bit for bit)
+ *   x[C, C + R) = k, its first prep->rot_dim channels rotated as by cp_qk_norm_rope
+ * rounded once; x goes to position seqlens_k[s] + (row within sequence s) of the cache.
+ *   latent        device rows of C channels, latent_row_stride elements apart (0 =
+ *                 dense; else at least C and a multiple of 16 bytes)
+ *   k_rope        device rows of R channels, likewise (NULL when R is 0), so that both
+ *                 may be slices of one projection's output
+ *   q_rope, q_out device [total_rows, H, R] with row and head strides in elements (0 =
+ *                 dense; else multiples of 16 bytes, a head stride of at least R and a
+ *                 row stride of at least H head strides): each head's R channels are
+ *                 rotated like k into q_out, which may lie behind the absorbed queries
+ *                 in rows of C + R.  Both NULL: skipped.  q_out may be q_rope itself
+ *                 with the same strides; any other overlap of their rows, or of q_out
+ *                 with the latents or keys, is the caller's to avoid.
+ *   prep          rot_dim: 0 .. R, a multiple of 16
+ *   weight        device [C] of the layer's type, or NULL
+ *   inv_freq, positions, cu_rows, block_table, max_ctx, dev_status as in
+ *                 cp_qk_norm_rope_append (a row outside max_ctx or on a bad page is not
+ *                 appended and sets CP_DEV_BOUNDS; its q_out is still written; rows from
+ *                 cu_rows[num_seqs] on are left as they were)
+ * seqlens_k is not modified.  CONTIG: num_seqs <= batch. */
+int cp_latent_append(const cp_latent_desc* desc, const cp_qk_prep* prep, const void* latent, int64_t latent_row_stride,
+                     const void* k_rope, int64_t k_row_stride, const void* weight, const float* inv_freq,
+                     const int32_t* positions, const void* q_rope, int64_t q_row_stride, int64_t q_head_stride,
+                     void* q_out, int64_t out_row_stride, int64_t out_head_stride, const int32_t* cu_rows,
+                     int32_t num_seqs, int32_t total_rows, void* cache, const int32_t* seqlens_k,
+                     const int32_t* block_table, int32_t max_ctx, int32_t* dev_status, void* stream);
+
+/* Most rows that a sequence of a call with `parents` may have. */
+#define CP_TREE_MAX 128
+
+/* cp_latent_attn -- attention over a latent cache, absorbed form.
+ *
+ * Row i of sequence s, head h:  o = sum_j softmax_j(scale * q[t, h] . x_j) x_j[0, C)
+ * over the positions j that the row sees:
+ *   parents NULL  [0, seqlens_k[s] + i], as in cp_prefill_chunk_attn
+ *   parents       a tree of drafted tokens: device int32 [total_rows], the place
+ *                 within the sequence's rows of row i's parent (less than i), or -1 for
+ *                 a child of the cached context.  The row sees [0, seqlens_k[s]), its
+ *                 ancestors and itself; row i's own position in the cache is
+ *                 seqlens_k[s] + i, whatever its depth.  A parent out of range sets
+ *                 CP_DEV_BOUNDS and counts as -1; a sequence of more than CP_TREE_MAX
+ *                 rows is skipped and sets CP_DEV_BOUNDS.
+ *   q             device [total_rows, H, C + R], dense;  out  [total_rows, H, C]; out
+ *                 must not overlap q (CP_ERR_INVALID_ARG), the cache or the workspace
+ *   cache         holds the call's own rows already (cp_latent_append)
+ *   cu_rows       device int32 [num_seqs + 1], or NULL: total_rows / num_seqs rows each.
+ *                 A sequence without rows sets CP_DEV_BOUNDS; the others are computed
+ *                 all the same.  Rows of out from cu_rows[num_seqs] on are left as they
+ *                 were
+ *   max_ctx       host bound on seqlens_k[s] + rows of s, below 2^31 - 4096; a sequence
+ *                 outside it is skipped (its rows of out are left as they were) and sets
+ *                 CP_DEV_BOUNDS.  A page id out of range sets it too, is not read, and
+ *                 leaves the sequence's results unspecified
+ *   workspace     device scratch, 16-byte aligned, of at least
+ *                 cp_workspace_size_latent(desc, total_rows, max_ctx, num_seqs) bytes; its
+ *                 contents before the call do not matter (NULL when that size is 0).
+ *                 Calls whose work overlaps on the GPU need separate workspaces
+ *   commit        not 0: seqlens_k[s] += rows of s after the attention (with parents:
+ *                 CP_ERR_INVALID_ARG; cp_latent_tree_commit advances them)
+ * A row's result depends only on its own sequence.  Scores, softmax sums and outputs are
+ * held in 32 bits; the softmax's weights are rounded to the layer's type for their
+ * product with the latents.  Slots past a sequence's positions may hold anything.  A NaN,
+ * or an infinite value (x[0, C), v), makes the rows that see its position non-finite (in
+ * its channels or in all), and no other row; an infinite key makes a score infinite: +inf
+ * makes the row NaN, -inf weighs nothing. */
+int cp_latent_attn(const cp_latent_desc* desc, const void* q, const void* cache, int32_t* seqlens_k,
+                   const int32_t* block_table, const int32_t* parents, const int32_t* cu_rows, int32_t num_seqs,
+                   int32_t total_rows, int32_t max_ctx, void* out, void* workspace, size_t workspace_bytes,
+                   int32_t commit, int32_t* dev_status, void* stream);
+
+/* cp_workspace_size_latent -- bytes of device scratch that always suffice for
+ * cp_latent_attn with up to total_rows rows of up to num_seqs sequences and contexts of
+ * up to max_ctx positions: the parts of contexts that are split (0 for arguments that the
+ * call would refuse). */
+size_t cp_workspace_size_latent(const cp_latent_desc* desc, int32_t total_rows, int32_t max_ctx, int32_t num_seqs);
+
+/* cp_latent_chunk_attn -- attention of prompt chunks over expanded keys and values.
+ *
+ * Sequence s has query rows [cu_rows[s], cu_rows[s+1]) and keys [cu_keys[s],
+ * cu_keys[s+1]), n of them; its r rows are the last r positions, so row i sees keys
+ * [0, n - r + i] (a row that sees none, r > n, gets zeros):
+ *   o[t, h] = sum_j softmax_j(scale * (q[t, h, 0:N] . k_nope[j, h] + q[t, h, N:] . k_rope[j])) v[j, h]
+ * with N = nope_dim.
+ *   q             device [total_rows, H, N + R], dense;  out  [total_rows, H, v_dim],
+ *                 dense; out must not overlap q (CP_ERR_INVALID_ARG), the keys or values
+ *   k_nope, v     device [total_keys, H, N] and [total_keys, H, v_dim] with row and head
+ *                 strides in elements (0 = dense; else multiples of 16 bytes, a head
+ *                 stride of at least the channels, a row stride of at least H head
+ *                 strides), so that both may be slices of one product's output
+ *   k_rope        device rows of R channels, k_rope_stride elements apart (0 = dense;
+ *                 NULL when R is 0): it may be the cache's own rows
+ *   cu_rows, cu_keys  device int32 [num_seqs + 1], both given, or both NULL: total_rows /
+ *                 num_seqs rows and total_keys / num_seqs keys each.  A sequence whose
+ *                 rows or keys are not within the totals, or that has no rows, sets
+ *                 CP_DEV_BOUNDS and is skipped; rows from cu_rows[num_seqs] on are left as
+ *                 they were
+ * The description's cache fields are checked as always but not used; nothing is
+ * allocated, and no workspace is needed.  Precision and non-finite values as in
+ * cp_latent_attn. */
+int cp_latent_chunk_attn(const cp_latent_desc* desc, const void* q, const void* k_nope, int64_t k_row_stride,
+                         int64_t k_head_stride, const void* k_rope, int64_t k_rope_stride, const void* v,
+                         int64_t v_row_stride, int64_t v_head_stride, const int32_t* cu_rows, const int32_t* cu_keys,
+                         int32_t num_seqs, int32_t total_rows, int32_t total_keys, void* out, int32_t* dev_status,
+                         void* stream);
+
+/* ---- trees of drafted tokens ---- */
+
+/* cp_tree_attn -- attention of a drafted tree's nodes over a K/V cache.
+ *
+ * The nodes of sequence s are its rows; their keys and values are in the cache at
+ * positions seqlens_k[s] + i already (cp_kv_append, or cp_qk_norm_rope_append with each
+ * node's depth in `positions`).  Node i attends to the cached context [0, seqlens_k[s]),
+ * its ancestors and itself; otherwise as cp_prefill_chunk_attn.  bf16 and fp16 layers
+ * with CONTIG and PAGED caches (others return CP_ERR_UNSUPPORTED), Hq / Hkv up to 64.
+ *   q, out        device [total_rows, Hq, D]
+ *   parents       device int32 [total_rows], as in cp_latent_attn; not NULL
+ *   workspace     at least cp_workspace_size_tree(...) bytes, as in cp_latent_attn
+ * Rows of the sequences, max_ctx, dev_status, results of rows on their own, precision and
+ * non-finite values as in cp_latent_attn.  seqlens_k is not modified (cp_tree_commit). */
+int cp_tree_attn(const cp_layer_desc* desc, const void* q, const void* k_cache, const void* v_cache,
+                 const int32_t* seqlens_k, const int32_t* block_table, const int32_t* parents, const int32_t* cu_rows,
+                 int32_t num_seqs, int32_t total_rows, int32_t max_ctx, void* out, void* workspace,
+                 size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* cp_workspace_size_tree -- bytes of device scratch that always suffice for cp_tree_attn
+ * within these bounds (0 for arguments that the call would refuse). */
+size_t cp_workspace_size_tree(const cp_layer_desc* desc, int32_t total_rows, int32_t max_ctx, int32_t num_seqs);
+
+/* cp_tree_commit -- keeps the accepted path of each sequence's drafted tree.
+ *
+ * The keys and values at positions seqlens_k[s] + path[s, j] move to seqlens_k[s] + j,
+ * for j = 0 .. counts[s] - 1; bit-exact copies, and nothing else in the cache is touched.
+ * Any type, CONTIG and PAGED caches (ROLLING: CP_ERR_UNSUPPORTED).
+ *   path          device int32 [num_seqs, max_path]: the accepted nodes' places within
+ *                 the sequence's rows, ascending (a parent comes before its children)
+ *   counts        device int32 [num_seqs]: 0 .. max_path (0: nothing is kept)
+ *   max_ctx       host bound on seqlens_k[s] + every place + 1
+ *   commit        not 0: seqlens_k[s] += counts[s] (a model's last layer, where its
+ *                 layers share one array)
+ * A sequence with a count, a place or a position out of range, places that do not
+ * ascend, or a page id out of range among those it needs, is left as it was, its length
+ * too, and sets CP_DEV_BOUNDS. */
+int cp_tree_commit(const cp_layer_desc* desc, void* k_cache, void* v_cache, const int32_t* path, const int32_t* counts,
+                   int32_t* seqlens_k, const int32_t* block_table, int32_t num_seqs, int32_t max_path, int32_t max_ctx,
+                   int32_t commit, int32_t* dev_status, void* stream);
+
+/* cp_latent_tree_commit -- cp_tree_commit on a latent cache. */
+int cp_latent_tree_commit(const cp_latent_desc* desc, void* cache, const int32_t* path, const int32_t* counts,
+                          int32_t* seqlens_k, const int32_t* block_table, int32_t num_seqs, int32_t max_path,
+                          int32_t max_ctx, int32_t commit, int32_t* dev_status, void* stream);
+
 /* ---- host-side integer helpers (no GPU work) ---- */
 
 /* cp_chunk_plan -- chunk sizes of an n_tokens prompt at width `chunk`
