@@ -43,11 +43,11 @@ int strides_of(int64_t row, int64_t head, int64_t heads, int64_t width, int es, 
   return stride_of(row, *head_out * heads, es, row_out);
 }
 
-// The checks of attention over few rows' caches that both kinds share.
-int rows_attn_check(const cp_layer_desc* d, int dqk, int dv, const void* q, const void* k, const void* v,
-                    const int32_t* seqlens_k, const int32_t* block_table, const int32_t* parents, const int32_t* cu_rows,
-                    int32_t num_seqs, int32_t total_rows, int32_t max_ctx, const void* out, const int32_t* dev_status,
-                    SeqRows* rows) {
+// The checks and the launch of attention of few rows that both kinds of cache share.
+int rows_attention(const cp_layer_desc* d, bool latent, int dqk, int dv, float scale, const void* q, const void* k,
+                   const void* v, const int32_t* seqlens_k, const int32_t* block_table, const int32_t* parents,
+                   const int32_t* cu_rows, int32_t num_seqs, int32_t total_rows, int32_t max_ctx, void* out,
+                   void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream, SeqRows* rows) {
   int r = rows_of(cu_rows, num_seqs, total_rows, rows);
   if (r != CP_OK || total_rows == 0) return r;
   if (!q || !k || !v || !out || !seqlens_k || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) ||
@@ -60,13 +60,10 @@ int rows_attn_check(const cp_layer_desc* d, int dqk, int dv, const void* q, cons
   if (d->num_q_heads > 65535 || (int64_t)total_rows * d->num_q_heads > INT32_MAX / 4) return CP_ERR_UNSUPPORTED;
   const int64_t pairs = (int64_t)total_rows * d->num_q_heads;
   if (overlap(out, pairs * dv * 2, q, pairs * dqk * 2)) return CP_ERR_INVALID_ARG;
-  return CP_OK;
-}
-
-RowsAttnArgs rows_args(const cp_layer_desc* d, int dqk, int dv, float scale, const SeqRows& rows, int32_t total_rows,
-                       const void* q, const void* k, const void* v, const int32_t* seqlens_k,
-                       const int32_t* block_table, const int32_t* parents, int32_t max_ctx, void* out,
-                       int32_t* dev_status) {
+  const RowsPlan p = rows_plan(d->num_q_heads, d->num_kv_heads, latent, dv, cu_rows == nullptr, num_seqs, total_rows, max_ctx);
+  if ((double)p.tiles * p.max_splits > INT32_MAX || (double)p.tiles * p.tile_rows > INT32_MAX || p.slots > INT32_MAX)
+    return CP_ERR_UNSUPPORTED;
+  if (p.bytes > 0 && (!workspace || !aligned16(workspace) || (double)workspace_bytes < p.bytes)) return CP_ERR_WORKSPACE;
   RowsAttnArgs a;
   std::memset(&a, 0, sizeof(a));
   a.hq = d->num_q_heads;
@@ -75,7 +72,7 @@ RowsAttnArgs rows_args(const cp_layer_desc* d, int dqk, int dv, float scale, con
   a.dqk = dqk;
   a.dv = dv;
   a.scale_log2 = scale;
-  a.rows = rows;
+  a.rows = *rows;
   a.total_rows = total_rows;
   a.cache = make_cache(d, block_table);
   a.past = seqlens_k;
@@ -86,7 +83,23 @@ RowsAttnArgs rows_args(const cp_layer_desc* d, int dqk, int dv, float scale, con
   a.v = v;
   a.out = out;
   a.status = dev_status;
-  return a;
+  a.latent = latent;
+  a.q_rows = p.q_rows;
+  a.tile_rows = p.tile_rows;
+  a.nr = p.nr;
+  a.tiles_bound = (int)p.tiles;
+  a.max_splits = p.max_splits;
+  a.part_slots = (int)p.slots;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = a.part_o + p.slots * a.hkv * p.nr * dv;
+  return launch_result(launch_rows_attn(a, d->dtype, static_cast<cudaStream_t>(stream)));
+}
+
+size_t rows_workspace(const cp_layer_desc* d, bool latent, int dv, int32_t total_rows, int32_t max_ctx, int32_t num_seqs) {
+  if (total_rows <= 0 || max_ctx <= 0 || num_seqs <= 0) return 0;
+  // Ragged rows: no call of equal rows within the bounds has more tiles.
+  const double bytes = rows_plan(d->num_q_heads, d->num_kv_heads, latent, dv, false, num_seqs, total_rows, max_ctx).bytes;
+  return bytes < 4e18 ? (size_t)bytes : SIZE_MAX;
 }
 
 int tree_check(const cp_layer_desc* d) {
@@ -195,23 +208,19 @@ int cp_latent_attn(const cp_latent_desc* desc, const void* q, const void* cache,
   int r = latent_check(desc, &d);
   if (r != CP_OK) return r;
   if (parents && commit) return CP_ERR_INVALID_ARG;
-  const int dqk = desc->latent_dim + desc->rope_dim, dv = desc->latent_dim;
   SeqRows rows;
-  r = rows_attn_check(&d, dqk, dv, q, cache, cache, seqlens_k, block_table, parents, cu_rows, num_seqs, total_rows,
-                      max_ctx, out, dev_status, &rows);
-  if (r != CP_OK || total_rows == 0) return r;
-  const RowsAttnArgs a = rows_args(&d, dqk, dv, latent_scale_log2(desc), rows, total_rows, q, cache, cache, seqlens_k,
-                                   block_table, parents, max_ctx, out, dev_status);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  r = launch_result(launch_rows_attn(a, d.dtype, st));
-  if (r != CP_OK || !commit) return r;
-  return launch_result(launch_commit(seqlens_k, rows, rows.rows_uniform > 0 ? rows.rows_uniform : -1, nullptr, st));
+  r = rows_attention(&d, true, desc->latent_dim + desc->rope_dim, desc->latent_dim, latent_scale_log2(desc), q, cache,
+                     cache, seqlens_k, block_table, parents, cu_rows, num_seqs, total_rows, max_ctx, out, workspace,
+                     workspace_bytes, dev_status, stream, &rows);
+  if (r != CP_OK || total_rows == 0 || !commit) return r;
+  return launch_result(launch_commit(seqlens_k, rows, rows.rows_uniform > 0 ? rows.rows_uniform : -1, nullptr,
+                                     static_cast<cudaStream_t>(stream)));
 }
 
 size_t cp_workspace_size_latent(const cp_latent_desc* desc, int32_t total_rows, int32_t max_ctx, int32_t num_seqs) {
   cp_layer_desc d;
-  if (latent_check(desc, &d) != CP_OK || total_rows <= 0 || max_ctx <= 0 || num_seqs <= 0) return 0;
-  return 0;
+  if (latent_check(desc, &d) != CP_OK) return 0;
+  return rows_workspace(&d, true, desc->latent_dim, total_rows, max_ctx, num_seqs);
 }
 
 int cp_latent_chunk_attn(const cp_latent_desc* desc, const void* q, const void* k_nope, int64_t k_row_stride,
@@ -264,21 +273,18 @@ int cp_tree_attn(const cp_layer_desc* desc, const void* q, const void* k_cache, 
                  const int32_t* seqlens_k, const int32_t* block_table, const int32_t* parents, const int32_t* cu_rows,
                  int32_t num_seqs, int32_t total_rows, int32_t max_ctx, void* out, void* workspace,
                  size_t workspace_bytes, int32_t* dev_status, void* stream) {
-  int r = tree_check(desc);
+  const int r = tree_check(desc);
   if (r != CP_OK) return r;
   if (total_rows > 0 && !parents) return CP_ERR_INVALID_ARG;
   SeqRows rows;
-  r = rows_attn_check(desc, desc->head_dim, desc->head_dim, q, k_cache, v_cache, seqlens_k, block_table, parents,
-                      cu_rows, num_seqs, total_rows, max_ctx, out, dev_status, &rows);
-  if (r != CP_OK || total_rows == 0) return r;
-  const RowsAttnArgs a = rows_args(desc, desc->head_dim, desc->head_dim, scale_log2(desc), rows, total_rows, q, k_cache,
-                                   v_cache, seqlens_k, block_table, parents, max_ctx, out, dev_status);
-  return launch_result(launch_rows_attn(a, desc->dtype, static_cast<cudaStream_t>(stream)));
+  return rows_attention(desc, false, desc->head_dim, desc->head_dim, scale_log2(desc), q, k_cache, v_cache, seqlens_k,
+                        block_table, parents, cu_rows, num_seqs, total_rows, max_ctx, out, workspace, workspace_bytes,
+                        dev_status, stream, &rows);
 }
 
 size_t cp_workspace_size_tree(const cp_layer_desc* desc, int32_t total_rows, int32_t max_ctx, int32_t num_seqs) {
-  if (tree_check(desc) != CP_OK || total_rows <= 0 || max_ctx <= 0 || num_seqs <= 0) return 0;
-  return 0;
+  if (tree_check(desc) != CP_OK) return 0;
+  return rows_workspace(desc, false, desc->head_dim, total_rows, max_ctx, num_seqs);
 }
 
 int cp_tree_commit(const cp_layer_desc* desc, void* k_cache, void* v_cache, const int32_t* path, const int32_t* counts,

@@ -31,6 +31,32 @@ struct LatentAppendArgs {
   int* status;
 };
 
+// Splits of a sequence of n keys whose rows make nt tiles: few keys a split for a
+// short context, where the wait for one CTA's walk is what counts, more for a long
+// one, and no more CTAs than fill the GPU twice when the sequence has many tiles.  By
+// the sequence's own sizes alone, so a row's result never depends on what shares the
+// launch.
+constexpr int kRowsMaxSlots = 304;  // (tile, split) parts of a sequence, at most: twice 152 SMs
+__host__ __device__ inline int rows_split_base(int n) { return n <= 2048 ? 128 : n <= 8192 ? 256 : n <= 16384 ? 512 : 1024; }
+__host__ __device__ inline int rows_splits(int n, int nt) {
+  const int cap = kRowsMaxSlots / nt, k = (n - 1) / rows_split_base(n) + 1;
+  return cap <= 1 ? 1 : k < cap ? k : cap;
+}
+// Keys of each split: whole tiles of 64.
+__host__ __device__ inline int rows_split_keys(int n, int splits) { return ((n - 1) / splits + 64) & ~63; }
+// Most splits of a sequence of up to ctx keys and nt tiles, and the parts it may need.
+__host__ __device__ inline int rows_max_splits(int ctx, int nt) {
+  int m = rows_splits(ctx, nt);
+  const int steps[3] = {2048, 8192, 16384};
+  for (int i = 0; i < 3; ++i)
+    if (ctx > steps[i] && rows_splits(steps[i], nt) > m) m = rows_splits(steps[i], nt);
+  return m;
+}
+__host__ __device__ inline int rows_slots(int nt, int max_one) {  // max_one: rows_max_splits(ctx, 1)
+  const int cap = nt > kRowsMaxSlots ? 1 : kRowsMaxSlots / nt, m = max_one < cap ? max_one : cap;
+  return m > 1 ? nt * m : 0;
+}
+
 // Attention of few rows over a long cache (cp_latent_attn, cp_tree_attn).  A
 // latent cache is one KV head whose group is all heads and whose values are its
 // keys' first dv channels.
@@ -49,7 +75,26 @@ struct RowsAttnArgs {
   const void* v;
   void* out;               // [total_rows, hq, dv]
   int* status;
+  bool latent;
+  int q_rows;              // pairs of a tile that the call can have, at most
+  int tile_rows;           // (row, head) pairs of a tile: nr, or whole tokens' if hkv > 1
+  int nr;                  // pairs a tile has room for: 64 or 128, by the layer alone
+  int tiles_bound;         // tiles of the call, at most
+  int max_splits;          // of any sequence
+  int part_slots;          // parts that the workspace has room for
+  float* part_o;           // [part_slots, nr, dv] unnormalised parts
+  float* part_ml;          // [part_slots, nr, 2] their maximum (log2 domain) and sum
 };
+
+// How such a call runs, from its host bounds.
+struct RowsPlan {
+  int nr, tile_rows, q_rows;
+  long long tiles;         // at most
+  int max_splits;
+  long long slots;         // parts, at most
+  double bytes;            // of workspace; in floating point: absurd sizes must not wrap
+};
+RowsPlan rows_plan(int hq, int hkv, bool latent, int dv, bool uniform, long long num_seqs, long long total_rows, int max_ctx);
 
 // Attention of chunks over expanded keys and values (cp_latent_chunk_attn).
 struct ExpandedArgs {

@@ -137,6 +137,17 @@ def test_latent_single_tokens_at_every_kind_of_length(past):
     x.check(q, out, [past, past // 2], [1, 1])
 
 
+@pytest.mark.parametrize("seqs,rows,heads", [(1, 1, 8), (1, 1, 64), (1, 1, 128), (1, 16, 8), (3, 4, 32), (1, 100, 5)])
+def test_latent_equal_rows_that_fill_their_tiles(seqs, rows, heads):
+    past = [316, 0, 1500][:seqs]
+    x = Cache(F16, heads, seqs, 1700, latent=256, rope=32)
+    x.fill([p + rows for p in past])
+    q = x.queries(seqs * rows)
+    out = x.attend(q, past, [rows] * seqs, uniform=True)
+    assert int(x.status) == 0
+    x.check(q, out, past, [rows] * seqs)
+
+
 @pytest.mark.parametrize("dtype,kw", [(BF16, dict(heads=32, kv=8, d=128)), (F16, dict(heads=6, kv=2, d=64, page=16)),
                                       (BF16, dict(heads=64, kv=1, d=128, page=64)), (F16, dict(heads=5, kv=5, d=128, page=128)),
                                       (BF16, dict(heads=14, kv=2, d=64)), (F16, dict(heads=16, latent=512, rope=64, page=32)),
