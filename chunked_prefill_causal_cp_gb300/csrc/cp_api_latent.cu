@@ -61,7 +61,7 @@ int rows_attention(const cp_layer_desc* d, bool latent, int dqk, int dv, float s
   const int64_t pairs = (int64_t)total_rows * d->num_q_heads;
   if (overlap(out, pairs * dv * 2, q, pairs * dqk * 2)) return CP_ERR_INVALID_ARG;
   const RowsPlan p = rows_plan(d->num_q_heads, d->num_kv_heads, latent, dv, cu_rows == nullptr, num_seqs, total_rows, max_ctx);
-  if ((double)p.tiles * p.max_splits > INT32_MAX || (double)p.tiles * p.tile_rows > INT32_MAX || p.slots > INT32_MAX)
+  if ((double)p.tiles * p.max_splits * d->num_kv_heads > INT32_MAX || (double)p.tiles * p.tile_rows > INT32_MAX || p.slots > INT32_MAX)
     return CP_ERR_UNSUPPORTED;
   if (p.bytes > 0 && (!workspace || !aligned16(workspace) || (double)workspace_bytes < p.bytes)) return CP_ERR_WORKSPACE;
   RowsAttnArgs a;

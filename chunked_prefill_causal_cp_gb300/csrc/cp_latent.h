@@ -31,12 +31,11 @@ struct LatentAppendArgs {
   int* status;
 };
 
-// Splits of a sequence of n keys whose rows make nt tiles: few keys a split for a
-// short context, where the wait for one CTA's walk is what counts, more for a long
-// one, and no more CTAs than fill the GPU twice when the sequence has many tiles.  By
-// the sequence's own sizes alone, so a row's result never depends on what shares the
-// launch.
-constexpr int kRowsMaxSlots = 304;  // (tile, split) parts of a sequence, at most: twice 152 SMs
+// Splits of a sequence of n keys whose rows make nt tiles (of every KV head): few keys a
+// split for a short context, where the wait for one CTA's walk is what counts, more for a
+// long one, and no more than kRowsMaxSlots (tile, split) pairs a sequence.  By the
+// sequence's own sizes alone, so a row's result never depends on what shares the launch.
+constexpr int kRowsMaxSlots = 304;  // twice 152 SMs
 __host__ __device__ inline int rows_split_base(int n) { return n <= 2048 ? 128 : n <= 8192 ? 256 : n <= 16384 ? 512 : 1024; }
 __host__ __device__ inline int rows_splits(int n, int nt) {
   const int cap = kRowsMaxSlots / nt, k = (n - 1) / rows_split_base(n) + 1;
