@@ -19,7 +19,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 SOURCES = ["cp_api.cu", "plan.cpp", "kv_append.cu", "attn_f32.cu", "attn_tc.cu", "decode.cu", "noalloc.cu",
            "selftest.cu", "qk_rope.cu", "kv_q4.cu", "attn_q4_tc.cu", "decode_q4.cu", "cp_api_q4.cu",
-           "latent_append.cu", "tree_commit.cu", "attn_rows.cu", "attn_expanded.cu", "cp_api_latent.cu"]
+           "latent_append.cu", "tree_commit.cu", "attn_latent.cu", "attn_tree.cu", "attn_expanded.cu", "cp_api_latent.cu"]
 
 
 def _nvcc():

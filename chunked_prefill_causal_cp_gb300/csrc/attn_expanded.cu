@@ -1,108 +1,111 @@
-// attn_expanded.cu -- attention of chunks over expanded keys and values.
+// attn_expanded.cu -- attention of prompt chunks over expanded keys and values of a
+// latent cache, on the kernel of attn_pairs.cuh.
 //
-// One warp a (row, head), lanes over channels, keys one by one with a running
-// maximum and sum.
-#include <cmath>
-#include <cstdint>
-
-#include "cp_latent.h"
-#include "cp_ptx.cuh"
-#include "cp_rows.cuh"
+// Every head has keys and values of its own (and the rotated part of the keys in
+// common), so a Q tile is 128 tokens of one head, and a score's product runs over
+// nope_dim + rope_dim channels, the rotated part as 64 of which those past rope_dim
+// are zeros.  The path is bound by the tensor cores.  Items are handed out with the
+// most keys first, heads fastest.
+#include "attn_pairs.cuh"
 
 namespace cp {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kChunks = 3;  // 16-byte chunks of a row a lane holds: up to 768 channels
+using pairs::Item;
 
-// A warp's running softmax; lane holds chunks lane, lane + 32, lane + 64 of a row.
-template <typename T>
-struct Walk {
-  float q[kChunks][8], o[kChunks][8];
-  float m = -INFINITY, l = 0.f;
+struct ExpandedWork : pairs::WorkBase {
+  static constexpr bool kPaged = false, kExpanded = true;
+  SeqRows keys;
+  int total_keys;
 
-  __device__ __forceinline__ void init() {
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) q[i][e] = o[i][e] = 0.f;
+  __device__ __forceinline__ int items(int r) const { return (r - 1) / (2 * tok_tile) + 1; }
+  __device__ __forceinline__ bool bounds(int s, int& r, int& row0, int& n, int& key0) const {
+    r = seq_rows(rows, s);
+    if (r < 1) return false;
+    row0 = seq_row0(rows, s);
+    n = keys.rows_uniform >= 0 ? keys.rows_uniform : keys.cu_rows[s + 1] - keys.cu_rows[s];
+    key0 = keys.rows_uniform >= 0 ? s * keys.rows_uniform : keys.cu_rows[s];
+    return row0 >= 0 && row0 <= total_rows - r && n >= 0 && key0 >= 0 && key0 <= total_keys - n;
   }
-  __device__ __forceinline__ float dot(int i, const uint4& w) const {
-    float x[8], d = 0.f;
-    unpack16<T>(w, x);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) d = fmaf(q[i][e], x[e], d);
-    return d;
+  __device__ __forceinline__ long long weight(int s, bool report) const {
+    int r, row0, n, key0;
+    if (!bounds(s, r, row0, n, key0)) {
+      if (report && status && r >= 1) atomicOr(status, CP_DEV_BOUNDS);
+      return 0;
+    }
+    return (long long)items(r) * hq;
   }
-  __device__ __forceinline__ void key(float d, float scale, const T* v, int dv) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) d += __shfl_xor_sync(0xffffffffu, d, k);
-    const float sc = d * scale, mn = fmaxf(m, sc), z = mn == -INFINITY ? 0.f : mn;
-    const float k0 = ex2_approx(m - z), p = ex2_approx(sc - z);
-    l = l * k0 + p;
-    m = mn;
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i)
-      if ((lane + 32 * i) * 8 < dv) {
-        float x[8];
-        unpack16<T>(reinterpret_cast<const uint4*>(v)[lane + 32 * i], x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[i][e] = fmaf(p, x[e], o[i][e] * k0);
-      }
-  }
-  __device__ __forceinline__ void write(T* out, int dv) {
-    const int lane = threadIdx.x & 31;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i)
-      if ((lane + 32 * i) * 8 < dv) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[i][e] *= inv;
-        reinterpret_cast<uint4*>(out)[lane + 32 * i] = pack16<T>(o[i]);
-      }
+  __device__ __forceinline__ bool make(int s, long long idx, long long, Item& x) const {
+    int n;
+    if (!bounds(s, x.rows, x.row0, n, x.key0)) return false;
+    x.s = s;
+    x.g = (int)(idx % hq);
+    x.t0 = (items(x.rows) - 1 - (int)(idx / hq)) * 2 * tok_tile;
+    x.past = n - x.rows;
+    x.j_begin = 0;
+    const int seen = x.past + min(x.rows, x.t0 + 2 * tok_tile);  // by the item's last row
+    x.ntiles = seen > 0 ? (seen + pairs::kKeys - 1) / pairs::kKeys : 0;
+    x.all = x.past + x.t0 + 1;
+    x.whole = 1;
+    x.part = 0;
+    return true;
   }
 };
 
+// 3-D tensor of 16-bit elements with strides in elements, in 128-byte-swizzled boxes of 64 channels.
+bool encode_strided(CUtensorMap* m, int dtype, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, int64_t s1, int64_t s2,
+                    uint32_t b1, uint32_t b2) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {d0, d1, d2}, strides[2] = {(cuuint64_t)s1 * 2, (cuuint64_t)s2 * 2};
+  const cuuint32_t box[3] = {64, b1, b2}, estr[3] = {1, 1, 1};
+  return fn(m, dtype == CP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads) expanded_kernel(const ExpandedArgs a) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const long long w = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 5;
-  if (w == 0)
-    for (int s = lane; s < a.rows.num_seqs; s += 32)
-      if (seq_rows(a.rows, s) < 1 && a.status) atomicOr(a.status, CP_DEV_BOUNDS);
-  const int t = (int)(w / a.heads), h = (int)(w % a.heads);
-  if (t >= a.total_rows) return;
-  const int s = row_seq(a.rows, t), i = row_place(a.rows, s, t), r = seq_rows(a.rows, s), row0 = seq_row0(a.rows, s);
-  if (i < 0) return;
-  const int key0 = seq_row0(a.keys, s), n = seq_rows(a.keys, s);
-  if (row0 < 0 || row0 > a.total_rows - r || n < 0 || key0 < 0 || key0 > a.total_keys - n) {
-    if (a.status && lane == 0) atomicOr(a.status, CP_DEV_BOUNDS);
-    return;
+cudaError_t launch_type(const ExpandedArgs& a, int dtype, cudaStream_t st) {
+  ExpandedWork wk;
+  wk.hq = wk.hkv = a.heads;
+  wk.group = 1;
+  wk.tok_tile = 128;
+  wk.scale_log2 = a.scale_log2;
+  wk.rows = a.rows;
+  wk.total_rows = a.total_rows;
+  wk.out = a.out;
+  wk.status = a.status;
+  wk.part_o = wk.part_ml = nullptr;
+  wk.page_size = wk.num_pages = wk.max_blocks = 0;
+  wk.dn = a.dn;
+  wk.block_table = wk.parents = nullptr;
+  wk.keys = a.keys;
+  if (a.keys.cu_rows) wk.keys.rows_uniform = -1;
+  wk.total_keys = a.total_keys;
+  pairs::Maps tm;
+  const uint64_t H = a.heads, N = a.total_keys;
+  if (!encode_3d(&tm.q, dtype, a.q, a.dn + a.r, H, a.total_rows, 64, 1, 128)) return cudaErrorInvalidValue;
+  tm.k = tm.kr = tm.v = tm.q;  // without keys nothing is loaded
+  if (N > 0) {
+    if (!encode_strided(&tm.k, dtype, a.k_nope, a.dn, H, N, a.k_head, a.k_row, 1, 128) ||
+        !encode_strided(&tm.v, dtype, a.v, a.dv, H, N, a.v_head, a.v_row, 1, 128) ||
+        (a.r > 0 && !encode_strided(&tm.kr, dtype, a.k_rope, a.r, N, 1, a.r_row, a.r_row, 128, 1)))
+      return cudaErrorInvalidValue;
   }
-  Walk<T> x;
-  x.init();
-  const int d = a.dn + a.r;
-  const T* q = static_cast<const T*>(a.q) + ((long long)t * a.heads + h) * d;
-  if (lane * 8 < d) unpack16<T>(reinterpret_cast<const uint4*>(q)[lane], x.q[0]);
-  for (int j = 0; j <= n - r + i; ++j) {
-    const T* k = static_cast<const T*>(a.k_nope) + (key0 + j) * a.k_row + h * a.k_head;
-    if (lane * 8 >= a.dn) k = static_cast<const T*>(a.k_rope) + (key0 + j) * a.r_row - a.dn;
-    const float p = lane * 8 < d ? x.dot(0, reinterpret_cast<const uint4*>(k)[lane]) : 0.f;
-    x.key(p, a.scale_log2, static_cast<const T*>(a.v) + (key0 + j) * a.v_row + h * a.v_head, a.dv);
+  const long long items = ((long long)a.total_rows / 256 + a.rows.num_seqs) * a.heads;
+  const int nqb = a.dn / 64 + (a.r > 0 ? 1 : 0);
+  if (a.dv == 64) {
+    if (nqb == 1) return pairs::launch<T, 1, 1>(tm, wk, items, st);
+    return nqb == 2 ? pairs::launch<T, 2, 1>(tm, wk, items, st) : pairs::launch<T, 3, 1>(tm, wk, items, st);
   }
-  x.write(static_cast<T*>(a.out) + ((long long)t * a.heads + h) * a.dv, a.dv);
+  if (nqb == 1) return pairs::launch<T, 1, 2>(tm, wk, items, st);
+  return nqb == 2 ? pairs::launch<T, 2, 2>(tm, wk, items, st) : pairs::launch<T, 3, 2>(tm, wk, items, st);
 }
 
 }  // namespace
 
 cudaError_t launch_expanded(const ExpandedArgs& a, int dtype, cudaStream_t st) {
-  const long long warps = (long long)a.total_rows * a.heads;
-  const dim3 grid((unsigned)((warps + 3) / 4));
-  if (dtype == CP_BF16) return launch_pdl(expanded_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, st, a);
-  return launch_pdl(expanded_kernel<__half>, grid, dim3(kThreads), 0, st, a);
+  return dtype == CP_BF16 ? launch_type<__nv_bfloat16>(a, dtype, st) : launch_type<__half>(a, dtype, st);
 }
 
 }  // namespace cp

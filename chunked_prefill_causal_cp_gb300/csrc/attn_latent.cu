@@ -1,0 +1,760 @@
+// attn_latent.cu -- attention over a latent cache in the absorbed form, on the sm_103a
+// tensor cores (TMA, tcgen05, TMEM), split along the keys.
+//
+// A position's row of up to 512 + 64 channels is the key and, without its last
+// channels, the value of every head: it is read once for a tile of (row, head)
+// pairs, and the path is bound by the cache's bytes until the pairs are many.  64 keys
+// are 72 KB, of which shared memory holds two beside 64 pairs' queries, and an output of
+// 512 channels leaves TMEM room for 64 pairs only if the channels lie over its lanes.
+// Hence
+//   S[pairs x 64 keys] = Q K^T     A = Q, B = K, both K-major: a pair's scores are a
+//                                  TMEM lane, two threads' with 32 keys each
+//   P -> shared memory             [pair][64 keys] in 16 bits, one swizzled 128-byte row
+//   O^T[128 channels x pairs] += V^T P^T   A = V as it lies (MN-major), B = P (K-major),
+//                                  a block of TMEM columns for each 128 channels
+// A raised maximum scales a column of O^T, which all lanes hold: the threads vote each
+// tile (a barrier that ORs), and only when some maximum grew by more than 2^8 do they
+// fetch the factors from shared memory and pass over O.
+//
+// One persistent CTA an SM, 384 threads: warp 0 TMA producer, warp 1 TMEM and MMA issue,
+// warp 2 scheduling (finds the CTA's items, two ahead), warps 4-11 softmax and output.
+// A stage's blocks of 64 channels land, and are given back, in up to three groups -- 256
+// channels, the next 256, the rotated part -- so that scores begin with the first group,
+// the rotated part is refilled while the softmax runs, and the first values while the
+// others are still multiplied: with two stages the way of a tile through load, scores,
+// softmax and output is what the kernel waits for, not any one of them.
+//
+// What a row does not see: its scores become -inf by a 64-bit mask of the tile's
+// columns (a tree's row: its ancestors, 128 bits found by walking the parents once).
+// Its weight 0 must not meet a NaN or an infinity in V: slots past the sequence are
+// overwritten with zeros in shared memory, and so are rows of the call's own
+// positions that hold a non-finite value; the pairs that see such a one become NaN by
+// their sum.
+//
+// Splits leave unnormalised fp32 parts and (maximum, sum) in the workspace, which the
+// combine kernel merges in a fixed order.
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstddef>
+#include <cstdint>
+#include <type_traits>
+
+#include "cp_host.h"
+#include "cp_items.cuh"
+#include "cp_latent.h"
+#include "cp_ptx.cuh"
+#include "cp_rows.cuh"
+
+namespace cp {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kTile = 64;                 // keys of a tile
+constexpr uint32_t kBlock = kTile * 128;  // bytes of 64 keys x 64 channels
+constexpr int kMaxStages = 6;
+constexpr int kGroups = 3;                // of a stage's blocks, at most
+constexpr uint32_t kSmem = 232448;        // of a CTA, at most
+constexpr float kRescaleLog2 = 8.0f;
+
+// A (tile of pairs, split) of the call: what the scheduling warp hands to the others.
+struct Item {
+  int ntiles;               // tiles of keys; -1: no more items
+  int s;                    // sequence
+  int row0, rows, past;     // its first row, rows, positions before them
+  int first, pairs;         // first (row, head) pair of the sequence, pairs of the tile
+  int j_begin, j_end;       // keys
+  int whole;                // not split: finished here
+  int part;                 // else: its part
+};
+
+struct __align__(16) Shared {
+  uint64_t item_full[2], item_empty[2], q_full, q_empty, full[kMaxStages][kGroups], empty[kMaxStages][kGroups], s_full[2],
+      p_ready, pv_done, o_free, all_done;
+  uint32_t tmem_base;
+  int abort;
+  Item item[2];
+  uint32_t bad[2][8];         // keys of the tile with a non-finite value, 8 a warp
+  union __align__(16) {
+    int parent[CP_TREE_MAX];  // before an item's walk
+    struct {                  // during it
+      float alpha[128];       // the factor of a pair's column for its raised maximum
+      float top[2][128];      // maximum of a pair's 32 scores of this tile, by half
+    };
+    struct {                  // after it
+      float inv[128];         // 1 / sum of a pair
+      float sum[2][128];      // of a pair's weights, by half
+    };
+  };
+};
+static_assert(offsetof(Shared, alpha) % 16 == 0, "the factors are read four at a time");
+
+// Shared memory: Q, stages, P, Shared.
+struct Layout {
+  uint32_t stage_bytes, p_off, ctl_off, alloc;
+  int nqb, nvb;             // blocks of 64 channels: of a row, of its value
+  int ngroups, stages;
+};
+
+Layout layout_of(int dqk, int dv, int nr) {
+  Layout l;
+  l.nqb = (dqk + 63) / 64;
+  l.nvb = dv / 64;
+  l.ngroups = (l.nvb + 3) / 4 + (l.nqb > l.nvb);
+  l.stage_bytes = (uint32_t)l.nqb * kBlock;
+  const uint32_t q = (uint32_t)l.nqb * nr * 128, fixed = q + nr * 128 + (uint32_t)sizeof(Shared);
+  l.stages = std::min<int>((kSmem - fixed) / l.stage_bytes, kMaxStages);
+  l.p_off = q + l.stages * l.stage_bytes;
+  l.ctl_off = l.p_off + nr * 128;
+  l.alloc = l.ctl_off + (uint32_t)sizeof(Shared);
+  return l;
+}
+
+// The call's items: (tile of pairs, split) of each sequence, tile fastest, so that the
+// tiles that read the same keys run at the same time.
+struct Work : RowsAttnArgs {
+  // A sequence within the call's bounds: its rows, positions before them, first row.
+  __device__ __forceinline__ bool bounds(int s, int& r, int& p, int& row0) const {
+    r = seq_rows(rows, s);
+    if (r < 1) return false;
+    p = past[s];
+    row0 = seq_row0(rows, s);
+    return p >= 0 && (long long)p + r <= max_ctx && row0 >= 0 && row0 <= total_rows - r && !(parents && r > CP_TREE_MAX);
+  }
+  __device__ __forceinline__ int tiles(int r) const { return (r * hq - 1) / nr + 1; }
+  __device__ __forceinline__ long long weight(int s, bool report) const {
+    int r, p, row0;
+    if (!bounds(s, r, p, row0)) {
+      if (report && status && r >= 1) atomicOr(status, CP_DEV_BOUNDS);
+      return 0;
+    }
+    const int nt = tiles(r);
+    return (long long)nt * rows_splits(p + r, nt);
+  }
+  __device__ __forceinline__ bool make(int s, long long idx, long long r_all, Item& x) const {
+    if (!bounds(s, x.rows, x.past, x.row0)) return false;
+    const int n = x.past + x.rows, nt = tiles(x.rows), splits = rows_splits(n, nt), keys = rows_split_keys(n, splits);
+    const int split = (int)idx / nt;
+    x.s = s;
+    x.first = (int)(idx - (long long)split * nt) * nr;
+    x.pairs = min(nr, x.rows * hq - x.first);
+    x.j_begin = split * keys;
+    const int seen = x.past + (x.first + x.pairs - 1) / hq + 1;  // by the tile's last row
+    x.j_end = (int)min((long long)seen, (long long)x.j_begin + keys);
+    x.ntiles = (x.j_end - x.j_begin + kTile - 1) / kTile;
+    x.whole = splits == 1;
+    x.part = (int)r_all;
+    if (!x.whole && r_all >= part_slots) {
+      if (status && (threadIdx.x & 31) == 0) atomicOr(status, CP_DEV_BOUNDS);
+      return false;
+    }
+    return x.j_end > x.j_begin;
+  }
+};
+
+// Barriers of the eight softmax warps, one of which also ORs a predicate.
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ bool softmax_any(bool x) {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+               : "=r"(r)
+               : "r"((uint32_t)x)
+               : "memory");
+  return r != 0;
+}
+
+template <typename T, bool kPaged>
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const Work a, const Layout L) {
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sStage = smem + (uint32_t)L.nqb * a.nr * 128;
+  uint8_t* sP = smem + L.p_off;
+  Shared* sh = reinterpret_cast<Shared*>(smem + L.ctl_off);
+
+  pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // ---- set-up that reads no global memory: it may overlap the previous kernel
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->item_full[i], 1);
+      mbar_init(&sh->item_empty[i], 10);  // warps 0, 1 and the eight of softmax
+      mbar_init(&sh->s_full[i], 1);
+    }
+    mbar_init(&sh->q_full, 1);
+    mbar_init(&sh->q_empty, 1);
+    for (int i = 0; i < L.stages; ++i)
+      for (int j = 0; j < kGroups; ++j) {
+        mbar_init(&sh->full[i][j], 1);
+        mbar_init(&sh->empty[i][j], 1);
+      }
+    mbar_init(&sh->p_ready, 256);
+    mbar_init(&sh->pv_done, 1);
+    mbar_init(&sh->o_free, 256);
+    mbar_init(&sh->all_done, 1);
+    sh->abort = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+  }
+  if (warp == 1) {
+    tmem_alloc(&sh->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem_base;
+  volatile int* abort_flag = &sh->abort;
+  auto wait = [&](uint64_t* b, uint32_t parity) { return warp_wait(b, parity, abort_flag, a.status); };
+  // Item k of this CTA, as every role takes it: false when there are no more.
+  auto take = [&](int k, Item& x) {
+    if (!wait(&sh->item_full[k & 1], (k >> 1) & 1)) return false;
+    x = sh->item[k & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh->item_empty[k & 1]);
+    return x.ntiles >= 0;
+  };
+  // A group's blocks: values four at a time, then the rotated part.
+  const int vgroups = (L.nvb + 3) / 4;
+  auto group_first = [&](int j) { return j < vgroups ? 4 * j : L.nvb; };
+  auto group_end = [&](int j) { return j < vgroups ? min(4 * j + 4, L.nvb) : L.nqb; };
+  pdl_wait();  // everything below reads what earlier kernels wrote
+
+  if (warp == 2) {
+    // ================================================================ scheduling
+    ItemCursor<Work> cur(a);
+    Item x;
+    for (int k = 0;; ++k) {
+      const bool more = cur.next(a, x);
+      if (k >= 2 && !wait(&sh->item_empty[k & 1], ((k >> 1) & 1) ^ 1)) break;
+      if (lane == 0) {
+        if (!more) x.ntiles = -1;
+        sh->item[k & 1] = x;
+        mbar_arrive(&sh->item_full[k & 1]);
+      }
+      if (!more) break;
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    if (blockIdx.x == 0 && a.status && a.rows.rows_uniform <= 0)
+      for (int s = lane; s < a.rows.num_seqs; s += 32)
+        if (seq_rows(a.rows, s) < 1) atomicOr(a.status, CP_DEV_BOUNDS);
+  } else if (warp == 0) {
+    // ================================================================ producer
+    const int ps = kPaged ? min(a.cache.page_size, kTile) : kTile, lps = kPaged ? 31 - __clz(a.cache.page_size) : 0;
+    const int npg = kTile / ps;  // boxes of a block
+    int gt = 0, queries = 0;     // tiles, items' queries issued so far
+    int landed = 0;              // groups of tile gt that were issued, after an abort
+    bool ok = true;
+    Item x;
+    for (int k = 0; ok && take(k, x); ++k) {
+      if (k > 0) ok = wait(&sh->q_empty, (k - 1) & 1);
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&sh->q_full, L.nqb * a.q_rows * 128);
+        for (int b = 0; b < L.nqb; ++b) tma_load_3d(smem + b * a.nr * 128, &tm_q, &sh->q_full, b * 64, x.row0 * a.hq + x.first, 0);
+      }
+      __syncwarp();
+      queries = k + 1;
+      for (int i = 0; i < x.ntiles; ++i, ++gt) {
+        const int st = gt % L.stages;
+        const int j0 = x.j_begin + i * kTile;
+        // This lane's boxes: idx = lane, lane + 32, ...: page idx % npg of block idx / npg.
+        int plane = x.s, off = j0;
+        if (kPaged) {
+          const int key = j0 + (lane % npg) * ps, blk = key >> lps;
+          plane = a.cache.num_pages;  // out of range: zeros
+          if (key < x.j_end) {
+            const int page = blk < a.cache.max_blocks ? a.cache.block_table[(long long)x.s * a.cache.max_blocks + blk] : -1;
+            if (page >= 0 && page < a.cache.num_pages) plane = page;
+            else if (a.status && lane < npg) atomicOr(a.status, CP_DEV_BOUNDS);
+          }
+          off = key & (a.cache.page_size - 1);
+        }
+        for (int e = 0; e < L.ngroups; ++e) {
+          const int j = e == 0 ? L.ngroups - 1 : e - 1;  // the last group is free first
+          if (gt >= L.stages) ok = wait(&sh->empty[st][j], ((gt / L.stages) & 1) ^ 1);
+          if (!ok) break;
+          const int b0 = group_first(j), nb = group_end(j) - b0;
+          if (lane == 0) mbar_arrive_expect_tx(&sh->full[st][j], nb * kBlock);
+          __syncwarp();
+          for (int idx = lane; idx < npg * nb; idx += 32) {  // npg divides 32: the page stays the lane's
+            const int b = b0 + idx / npg;
+            tma_load_3d(sStage + st * L.stage_bytes + b * kBlock + (idx % npg) * ps * 128, &tm_k, &sh->full[st][j], b * 64, off,
+                        plane);
+          }
+          landed = e + 1;
+        }
+        if (!ok) break;
+        landed = 0;
+      }
+    }
+    // Every copy has landed before shared memory is released, also after an abort.
+    volatile int zero = 0;
+    if (queries > 0) mbar_wait(&sh->q_full, (queries - 1) & 1, &zero, a.status);
+    for (int i = max(0, gt - L.stages + (landed ? 1 : 0)); i < gt; ++i)
+      for (int j = 0; j < L.ngroups; ++j) mbar_wait(&sh->full[i % L.stages][j], (i / L.stages) & 1, &zero, a.status);
+    for (int e = 0; e < L.ngroups; ++e) {  // of a tile left halfway: its first groups, the others' last phase
+      const int j = e == 0 ? L.ngroups - 1 : e - 1, i = e < landed ? gt : gt - L.stages;
+      if (landed && i >= 0) mbar_wait(&sh->full[i % L.stages][j], (i / L.stages) & 1, &zero, a.status);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ================================================================ MMA issuer
+    // What the addresses of an MMA come from is broadcast, so that the compiler keeps it in uniform registers and the
+    // MMAs issue back to back.
+    auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+    auto test = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test(b, parity)) != 0; };
+    const uint32_t idesc_qk = make_idesc_f16(kBf16, 128, kTile, false);
+    const uint64_t q_desc = make_sdesc_sw128(smem_u32(smem), 16, 1024);
+    const uint64_t k_desc = make_sdesc_sw128(smem_u32(sStage), 16, 1024);
+    const uint64_t v_desc = make_sdesc_sw128(smem_u32(sStage), kBlock, 1024);
+    const uint64_t p_desc = make_sdesc_sw128(smem_u32(sP), 16, 1024);
+    const uint32_t q_step = (uint32_t)a.nr * 8;  // of a descriptor: 16 bytes
+    const uint32_t tm = (uint32_t)uniform((int)tmem);
+    int g0 = 0;  // tiles of the items before
+    bool ok = true;
+    Item x;
+    for (int k = 0; ok && take(k, x); ++k) {
+      const int ntiles = uniform(x.ntiles);
+      const uint32_t idesc_pv = make_idesc_f16(kBf16, 128, (uniform(x.pairs) + 15) & ~15, false) | (1u << 15);  // A MN-major
+      ok = wait(&sh->q_full, k & 1);
+      int next = 0, part = 0;  // tile, and group in order of arrival, whose scores are issued next
+      for (int i = 0; ok && i < ntiles; ++i) {
+        uint64_t t0 = 0;
+        for (uint32_t it = 1;; ++it) {
+          if (next < ntiles && next <= i + 1) {
+            const int gn = g0 + next, st = gn % L.stages, j = part == 0 ? L.ngroups - 1 : part - 1;
+            if (test(&sh->full[st][j], (gn / L.stages) & 1)) {
+              tc_fence_after();
+              const uint32_t d = tm + 64u * (gn & 1);
+              const int b0 = group_first(j), b1 = group_end(j);
+              uint32_t q = (uint32_t)q_desc + b0 * q_step;
+              uint32_t kd = (uint32_t)k_desc + (((uint32_t)st * L.stage_bytes + b0 * kBlock) >> 4);
+              for (int b = b0; b < b1; ++b, q += q_step, kd += kBlock >> 4)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  mma_ss_lo(d, q + 2 * kk, (uint32_t)(q_desc >> 32), kd + 2 * kk, (uint32_t)(k_desc >> 32), idesc_qk,
+                            part | (b - b0) | kk);
+              if (++part == L.ngroups) {
+                mma_commit_elect(&sh->s_full[gn & 1]);
+                if (vgroups < L.ngroups) mma_commit_elect(&sh->empty[st][L.ngroups - 1]);  // the rotated part is read
+                part = 0;
+                if (++next == ntiles) mma_commit_elect(&sh->q_empty);
+              }
+              continue;
+            }
+          }
+          if (next > i && test(&sh->p_ready, (g0 + i) & 1)) break;
+          if ((it & 63u) == 0) {
+            int stop = 0;
+            if (lane == 0) {
+              stop = *abort_flag;
+              if (t0 == 0) t0 = global_timer_ns();
+              if (!stop && global_timer_ns() - t0 > kWaitLimitNs) {
+                *abort_flag = stop = 1;
+                if (a.status) atomicOr(a.status, CP_DEV_TIMEOUT);
+              }
+            }
+            if (uniform(stop)) {
+              ok = false;
+              break;
+            }
+          }
+        }
+        if (ok && i == 0 && k > 0) ok = wait(&sh->o_free, (k - 1) & 1);  // the item before has left O
+        if (!ok) break;
+        tc_fence_after();
+        const int st = (g0 + i) % L.stages;
+        uint32_t vd = (uint32_t)v_desc + (((uint32_t)st * L.stage_bytes) >> 4), d = tm + 128u;
+        for (int b = 0; b < L.nvb; b += 2, vd += kBlock >> 3, d += a.nr) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ss_lo(d, vd + 128 * kk, (uint32_t)(v_desc >> 32), (uint32_t)p_desc + 2 * kk, (uint32_t)(p_desc >> 32), idesc_pv,
+                      i | kk);
+          if (b % 4 == 2 || b + 2 >= L.nvb) mma_commit_elect(&sh->empty[st][b / 4]);
+        }
+        mma_commit_elect(&sh->pv_done);
+      }
+      g0 += ntiles;
+    }
+    mma_commit_elect(&sh->all_done);
+    volatile int zero = 0;  // wait even after an abort: MMAs may still be in flight
+    mbar_wait(&sh->all_done, 0, &zero, a.status);
+    __syncwarp();
+  } else {
+    // ================================================================ softmax, output
+    const int half = (warp - 4) >> 2, quarter = warp & 3;
+    const int m = quarter * 32 + lane;  // this thread's pair of the tile, with keys [32 half, + 32)
+    const int me = half * 128 + m;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const int nob = L.nvb / 2;
+    int gt = 0;
+    Item x;
+    for (int k = 0;; ++k) {
+      // After a wait that gave up, an item's walk goes on without waiting, so that its barriers stay whole; its output is
+      // not written, and the warps leave together.
+      bool alive = take(k, x);
+      if (softmax_any(!alive)) break;
+      const int n = x.past + x.rows;  // positions written, this call's rows among them
+      const bool row_ok = m < x.pairs, active = quarter * 32 < x.pairs;
+      const int tok = (x.first + m) / a.hq;
+      uint64_t see_lo = 0, see_hi = 0;  // a tree's row: the call's rows that it sees
+      if (a.parents) {
+        if (me < x.rows) {
+          int up = a.parents[x.row0 + me];
+          if (up < -1 || up >= me) {
+            up = -1;
+            if (a.status) atomicOr(a.status, CP_DEV_BOUNDS);
+          }
+          sh->parent[me] = up;
+        }
+        softmax_sync();
+        for (int j = row_ok ? tok : -1; j >= 0; j = sh->parent[j]) {
+          if (j < 64) see_lo |= 1ull << j;
+          else see_hi |= 1ull << (j - 64);
+        }
+        softmax_sync();  // the factors take the parents' place
+      }
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int i = 0; i < x.ntiles; ++i, ++gt) {
+        const int j0 = x.j_begin + i * kTile;
+        alive = alive && wait(&sh->s_full[gt & 1], (gt >> 1) & 1);
+        tc_fence_after();
+        uint32_t sv[32];
+        uint64_t vis = 0;
+        float mx = -INFINITY;
+        if (active) {
+          tmem_ld32(tmem + lane_off + 64u * (gt & 1) + 32u * half, sv);
+          tmem_wait_ld();
+          if (row_ok) {
+            const int c = x.past - j0 + (a.parents ? 0 : tok + 1);  // columns [0, c) are seen
+            vis = c >= 64 ? ~0ull : c > 0 ? (1ull << c) - 1 : 0;
+            if (a.parents && c < 64) vis |= bits_from(see_lo, see_hi, -c);
+          }
+          if (vis != ~0ull) {
+            const uint32_t v = (uint32_t)(vis >> (32 * half));
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!((v >> c) & 1)) sv[c] = __float_as_uint(-INFINITY);
+          }
+          float m4[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            m4[0] = fmax3(m4[0], __uint_as_float(sv[c + 0]), __uint_as_float(sv[c + 1]));
+            m4[1] = fmax3(m4[1], __uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3]));
+          }
+          mx = fmaxf(m4[0], m4[1]);
+        }
+        sh->top[half][m] = mx;
+        softmax_sync();
+        float alpha = 1.f;
+        if (active) {
+          const float mx2 = fmaxf(mx, sh->top[half ^ 1][m]) * a.scale_log2;  // scale > 0: it commutes
+          const bool first = m_run == -INFINITY;
+          if (mx2 > m_run + kRescaleLog2 || (first && mx2 != -INFINITY)) {
+            if (!first) alpha = ex2_approx(m_run - mx2);  // first: nothing but zeros so far
+            m_run = mx2;
+          }
+          const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+          float ps[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            float x0 = __uint_as_float(sv[2 * c]), x1 = __uint_as_float(sv[2 * c + 1]);
+            ffma2(x0, x1, a.scale_log2, neg_m);
+            x0 = ex2_approx(x0);
+            x1 = ex2_approx(x1);
+            fadd2(ps[2 * (c & 1)], ps[2 * (c & 1) + 1], x0, x1);
+            sv[c] = pack2<T>(x0, x1);
+          }
+          l_run = l_run * alpha + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
+        }
+        if (half == 0) sh->alpha[m] = alpha;
+        const bool scale = softmax_any(alpha != 1.f);
+        // The product of the tile before is complete: P may be overwritten, O rescaled.
+        if (i > 0) alive = alive && wait(&sh->pv_done, (gt - 1) & 1);
+        if (scale) {
+          if (i > 0) {
+            tc_fence_after();
+            for (int b = half; b < nob; b += 2)
+              for (int c = 0; c < x.pairs; c += 32) {
+                const uint32_t col = tmem + lane_off + 128u + (uint32_t)(b * a.nr + c);
+                uint32_t ov[32];
+                tmem_ld32(col, ov);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                  const float4 f = *reinterpret_cast<const float4*>(&sh->alpha[c + e]);
+                  ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f.x);
+                  ov[e + 1] = __float_as_uint(__uint_as_float(ov[e + 1]) * f.y);
+                  ov[e + 2] = __float_as_uint(__uint_as_float(ov[e + 2]) * f.z);
+                  ov[e + 3] = __float_as_uint(__uint_as_float(ov[e + 3]) * f.w);
+                }
+                tmem_st32(col, ov);
+              }
+            tmem_wait_st();
+          }
+          softmax_sync();  // the factors are read
+        }
+        if (active) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint4*>(sP + m * 128 + (((4 * half + c) ^ (m & 7)) * 16)) =
+                make_uint4(sv[4 * c], sv[4 * c + 1], sv[4 * c + 2], sv[4 * c + 3]);
+        }
+        // ---- values that must not meet a weight of 0
+        if (j0 + kTile > n || (x.rows > 1 && j0 + kTile > x.past)) {
+          const int st = gt % L.stages;
+          for (int j = 0; j < vgroups; ++j) alive = alive && wait(&sh->full[st][j], (gt / L.stages) & 1);
+          const int key = me >> 2, part = me & 3;  // four threads a key
+          const int chunks = L.nvb * 8;            // its 16-byte chunks, in an order that spreads the threads over the banks
+          auto chunk = [&](int c) {
+            const int d = (c + key) & 7;
+            return reinterpret_cast<uint4*>(sStage + st * L.stage_bytes + (c >> 3) * kBlock + key * 128 + d * 16);
+          };
+          const bool gone = j0 + key >= n;
+          bool bad = gone;
+          if (!bad && x.rows > 1 && j0 + key >= x.past)
+            for (int c = part; c < chunks; c += 4) bad = bad || nonfinite8<T>(*chunk(c));
+          bad = __shfl_xor_sync(0xffffffffu, bad, 1) || bad;
+          bad = __shfl_xor_sync(0xffffffffu, bad, 2) || bad;
+          if (bad)
+            for (int c = part; c < chunks; c += 4) *chunk(c) = make_uint4(0, 0, 0, 0);
+          const uint32_t four = __ballot_sync(0xffffffffu, bad && !gone);  // four bits a key
+          if (lane == 0) sh->bad[gt & 1][warp - 4] = four;
+          softmax_sync();
+          uint64_t any = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t y = sh->bad[gt & 1][e];
+            if (y)
+              for (int c = 0; c < 8; ++c)
+                if ((y >> (4 * c)) & 1) any |= 1ull << (8 * e + c);
+          }
+          if (any & vis) l_run = __int_as_float(0x7fffffff);
+        }
+        fence_proxy_async_smem();  // the tensor cores read P and V through the async proxy
+        tc_fence_before();
+        mbar_arrive(&sh->p_ready);
+      }
+
+      // ---- output: a lane holds a channel of each 128, its pairs in the columns
+      alive = alive && wait(&sh->pv_done, (gt - 1) & 1);
+      tc_fence_after();
+      sh->sum[half][m] = l_run;
+      if (softmax_any(!alive)) break;
+      if (half == 0) {
+        const float l = l_run + sh->sum[1][m];
+        sh->inv[m] = l == 0.f ? 0.f : 1.f / l;  // a NaN stays
+        if (!x.whole && row_ok) *reinterpret_cast<float2*>(a.part_ml + ((long long)x.part * a.nr + m) * 2) = make_float2(m_run, l);
+      }
+      softmax_sync();
+      if (x.whole) {
+        for (int b = half; b < nob; b += 2) {
+          T* out = static_cast<T*>(a.out) + ((long long)x.row0 * a.hq + x.first) * a.dv + b * 128 + m;
+          for (int c = 0; c < x.pairs; c += 32) {
+            uint32_t ov[32];
+            tmem_ld32(tmem + lane_off + 128u + (uint32_t)(b * a.nr + c), ov);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e, out += a.dv) {
+              if (c + e >= x.pairs) break;
+              const float y[2] = {__uint_as_float(ov[e]) * sh->inv[c + e], 0.f};
+              *reinterpret_cast<uint16_t*>(out) = (uint16_t)Pack<T>::store(y);
+            }
+          }
+        }
+      } else {
+        for (int b = half; b < nob; b += 2) {
+          float* part = a.part_o + (long long)x.part * a.nr * a.dv + b * 128 + m;
+          for (int c = 0; c < x.pairs; c += 32) {
+            uint32_t ov[32];
+            tmem_ld32(tmem + lane_off + 128u + (uint32_t)(b * a.nr + c), ov);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e, part += a.dv) *part = __uint_as_float(ov[e]);  // up to 31 pairs more than there are: room that nobody reads
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&sh->o_free);
+      softmax_sync();  // the sums are read: their place is free
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// A pair's splits are merged in four slices -- split i in slice i % 4, a slice's in
+// order -- and the slices in order.  dv threads a pair: a slice is dv / 4 of them, a
+// thread four channels.
+constexpr int kSlices = 4;
+
+template <typename T>
+__global__ void __launch_bounds__(512) latent_combine_kernel(const Work a, const int per) {
+  __shared__ float4 so[512];
+  __shared__ float2 sml[4 * kSlices];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int groups = (a.q_rows + per - 1) / per, lane = threadIdx.x & 31;
+  int w = blockIdx.x / groups;  // tile of the call
+  long long base = 0;           // items before its sequence
+  int s = -1, tile = 0;
+  for (int q0 = 0; q0 < a.rows.num_seqs && s < 0; q0 += 32) {
+    const int q = q0 + lane;
+    int r, p, row0;
+    long long tiles = 0, weight = 0;
+    if (q < a.rows.num_seqs && a.bounds(q, r, p, row0)) {
+      tiles = a.tiles(r);
+      weight = tiles * rows_splits(p + r, (int)tiles);
+    }
+    long long inc = tiles, upto = weight;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, inc, o), u = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) {
+        inc += v;
+        upto += u;
+      }
+    }
+    const long long total = __shfl_sync(0xffffffffu, inc, 31);
+    if (w < total) {
+      const int at = __ffs(__ballot_sync(0xffffffffu, inc > w)) - 1;
+      s = q0 + at;
+      tile = (int)(w - __shfl_sync(0xffffffffu, inc - tiles, at));
+      base += __shfl_sync(0xffffffffu, upto - weight, at);
+    } else {
+      w -= (int)total;
+      base += __shfl_sync(0xffffffffu, upto, 31);
+    }
+  }
+  int r, p, row0;
+  if (s < 0 || !a.bounds(s, r, p, row0)) return;  // the same for all threads
+  const int nt = a.tiles(r), splits = rows_splits(p + r, nt), keys = rows_split_keys(p + r, splits);
+  if (splits == 1 || base + (long long)nt * splits > a.part_slots) return;
+  const int first = tile * a.nr, pairs = min(a.nr, r * a.hq - first);
+  const int used = (p + (first + pairs - 1) / a.hq) / keys + 1;  // splits that hold keys of the tile
+  const int c4 = a.dv / 4, mine = threadIdx.x / a.dv, slice = threadIdx.x % a.dv / c4, d4 = threadIdx.x % c4;
+  const int m = blockIdx.x % groups * per + mine;
+  const bool on = m < pairs;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  float mx = -INFINITY, l = 0.f;
+  if (on) {
+    constexpr int kAhead = 4;
+    for (int i0 = slice; i0 < used; i0 += kAhead * kSlices) {
+      float2 ml[kAhead];
+      float4 x[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int i = i0 + j * kSlices;
+        if (i >= used) break;
+        const long long row = (base + (long long)i * nt + tile) * a.nr + m;
+        ml[j] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + row * 2));
+        x[j] = __ldcg(reinterpret_cast<const float4*>(a.part_o + row * a.dv + 4 * d4));
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (i0 + j * kSlices >= used) break;
+        const float mn = fmaxf(mx, ml[j].x), z = mn == -INFINITY ? 0.f : mn;
+        const float k0 = ex2_approx(mx - z), k1 = ex2_approx(ml[j].x - z);
+        v.x = v.x * k0 + x[j].x * k1;
+        v.y = v.y * k0 + x[j].y * k1;
+        v.z = v.z * k0 + x[j].z * k1;
+        v.w = v.w * k0 + x[j].w * k1;
+        l = l * k0 + ml[j].y * k1;
+        mx = mn;
+      }
+    }
+  }
+  so[threadIdx.x] = v;
+  if (d4 == 0) sml[mine * kSlices + slice] = make_float2(mx, l);
+  __syncthreads();
+  if (slice != 0 || !on) return;
+  mx = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kSlices; ++i) mx = fmaxf(mx, sml[mine * kSlices + i].x);
+  const float z = mx == -INFINITY ? 0.f : mx;
+  v = make_float4(0.f, 0.f, 0.f, 0.f);
+  l = 0.f;
+#pragma unroll
+  for (int i = 0; i < kSlices; ++i) {
+    const float4 x = so[threadIdx.x + i * c4];
+    const float2 y = sml[mine * kSlices + i];
+    const float k = ex2_approx(y.x - z);
+    v.x = fmaf(k, x.x, v.x);
+    v.y = fmaf(k, x.y, v.y);
+    v.z = fmaf(k, x.z, v.z);
+    v.w = fmaf(k, x.w, v.w);
+    l = fmaf(k, y.y, l);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float o[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+  uint2 b;
+  b.x = Pack<T>::store(o);
+  b.y = Pack<T>::store(o + 2);
+  *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + ((long long)row0 * a.hq + first + m) * a.dv + 4 * d4) = b;
+}
+
+template <typename T, bool kPaged>
+cudaError_t launch_t(const RowsAttnArgs& args, int dtype, cudaStream_t st) {
+  Work a;
+  static_cast<RowsAttnArgs&>(a) = args;
+  const Layout l = layout_of(a.dqk, a.dv, a.nr);
+  CUtensorMap tq, tk;
+  const CacheView& c = a.cache;
+  const uint64_t slots = kPaged ? c.page_size : c.capacity, planes = kPaged ? c.num_pages : a.rows.num_seqs;
+  if (!encode_3d(&tq, dtype, a.q, a.dqk, (uint64_t)a.total_rows * a.hq, 1, 64, a.q_rows, 1) ||
+      !encode_3d(&tk, dtype, a.k, a.dqk, slots, planes, 64, kPaged ? std::min(c.page_size, kTile) : kTile, 1))
+    return cudaErrorInvalidValue;
+  // Raise the dynamic shared-memory limit once per device, so later calls --
+  // including ones being captured into a CUDA graph -- only launch.
+  static std::atomic<uint64_t> ready_mask{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(ready_mask.load(std::memory_order_acquire) & bit)) {
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, latent_kernel<T, kPaged>);
+    if (e != cudaSuccess) return e;
+    if (fa.sharedSizeBytes != 0) return cudaErrorInvalidDeviceFunction;  // the swizzled tiles start at its beginning
+    e = cudaFuncSetAttribute(latent_kernel<T, kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e != cudaSuccess) return e;
+    ready_mask.fetch_or(bit, std::memory_order_release);
+  }
+  const uint32_t smem = std::max(l.alloc, 120u * 1024u);  // one CTA an SM: each takes all of TMEM
+  const dim3 grid((unsigned)std::min<long long>((long long)a.tiles_bound * a.max_splits, 152));
+  e = launch_pdl(latent_kernel<T, kPaged>, grid, dim3(kThreads), smem, st, tq, tk, a, l);
+  if (e != cudaSuccess || a.max_splits == 1) return e;
+  const int per = std::max(1, 256 / a.dv);
+  return launch_pdl(latent_combine_kernel<T>, dim3((unsigned)(a.tiles_bound * ((a.q_rows + per - 1) / per))), dim3(per * a.dv), 0, st,
+                    a, per);
+}
+
+}  // namespace
+
+RowsPlan rows_plan(int heads, int dv, bool uniform, long long num_seqs, long long total_rows, int max_ctx) {
+  RowsPlan p;
+  const long long pairs = (uniform ? total_rows / num_seqs : total_rows) * heads;  // of a sequence, at most
+  p.nr = dv > 256 ? 64 : 128;  // what the output's columns of TMEM leave room for
+  p.q_rows = (int)std::min<long long>(p.nr, pairs);
+  p.tiles = uniform ? num_seqs * ((pairs + p.nr - 1) / p.nr) : pairs / p.nr + 1 + num_seqs;
+  p.max_splits = rows_max_splits(max_ctx, 1);
+  // A sequence's items: its tiles, or, split, no more than kRowsItems.
+  p.slots = p.max_splits == 1 ? 0 : std::min(p.tiles * p.max_splits, p.tiles + num_seqs * kRowsItems);
+  p.bytes = (double)p.slots * p.nr * (dv + 2) * sizeof(float);
+  return p;
+}
+
+cudaError_t launch_rows_attn(const RowsAttnArgs& a, int dtype, cudaStream_t st) {
+  const bool paged = a.cache.kind == CP_CACHE_PAGED;
+  if (dtype == CP_BF16) return paged ? launch_t<__nv_bfloat16, true>(a, dtype, st) : launch_t<__nv_bfloat16, false>(a, dtype, st);
+  return paged ? launch_t<__half, true>(a, dtype, st) : launch_t<__half, false>(a, dtype, st);
+}
+
+}  // namespace cp

@@ -1,0 +1,604 @@
+// attn_pairs.cuh -- attention of up to 256 query rows at a time over 128-key
+// tiles on the sm_103a tensor cores (TMA, tcgen05, TMEM): drafted trees over a K/V
+// cache (attn_tree.cu) and chunks over expanded keys and values
+// (attn_expanded.cu).
+//
+// An item is a pair of 128-row Q tiles (each whole tokens of G heads) of one
+// sequence and KV head, over a range of its keys; every K/V tile that a CTA loads
+// serves both Q tiles.  One persistent CTA an SM, 384 threads:
+//   warp 0      TMA producer: an item's Q tiles, then for each 128-key tile its K and V
+//               in units of 64 channels (16 KB) through a ring of as many units as fit
+//   warp 1      MMA issue:  S_w = Q_w K^T, O_w += P_w V for Q tile w = 0, 1
+//   warp 2      scheduling: finds this CTA's items, two ahead of the others
+//   warp 3      fills the control warpgroup, whose registers go to the others
+//   warps 4-7, 8-11  softmax of Q tile 0 and 1, a thread a row
+// TMEM: Q tile w has [256w, 256w + 128) for S and, over it, P in 16 bits;
+// [256w + 128, + channels) for O.  S_w(i + 1) is issued after O_w += P_w(i) V(i), and
+// tcgen05 operations of one thread complete in order, so S_w(i + 1) complete means
+// that P_w(i) may be overwritten and O_w rescaled -- which happens only when a row's
+// maximum has grown by more than 2^8.
+//
+// What a row does not see: its scores become -inf by a mask of the tile's columns (a
+// tree's row: its ancestors, 128 bits found by walking the parents once).  Its weight
+// 0 must not meet a NaN or an infinity in V: in tiles with keys that some row of
+// the item does not see, V rows past the sequence, and those that hold a non-finite
+// value, are overwritten with zeros in shared memory; the rows that see such a key
+// become NaN by their sum.
+#pragma once
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstddef>
+#include <cstdint>
+#include <type_traits>
+
+#include "cp_host.h"
+#include "cp_items.cuh"
+#include "cp_latent.h"
+#include "cp_ptx.cuh"
+#include "cp_rows.cuh"
+
+namespace cp {
+namespace pairs {
+
+constexpr int kThreads = 384;
+constexpr int kKeys = 128;                // keys of a tile
+constexpr uint32_t kUnit = 128 * 128;     // bytes of 128 rows x 64 channels
+constexpr int kMaxUnits = 12;
+constexpr uint32_t kSmem = 232448;        // of a CTA, at most
+constexpr float kRescaleLog2 = 8.0f;
+// Register split: compiled at kRegsLaunch a thread (the most 384 threads may have); the
+// control warpgroup drops to kRegsControl and hands the rest to the softmax warpgroups.
+constexpr int kRegsLaunch = 168;
+constexpr int kRegsControl = 72;
+constexpr int kRegsSoftmax = 216;
+static_assert(128 * kRegsControl + 256 * kRegsSoftmax == kThreads * kRegsLaunch, "the split must add up");
+
+// What the scheduling warp hands to the others.
+struct Item {
+  int ntiles;               // tiles of keys; 0: rows that see none; -1: no more items
+  int s, g;                 // sequence, KV head
+  int row0, key0;           // the sequence's first row and (expanded) first key
+  int rows, past;           // its rows, keys before its first row (negative: the first rows see none)
+  int t0;                   // the item's first token
+  int j_begin;              // its first key
+  int all;                  // keys that every row of the item sees: [0, all)
+  int whole;                // not split: finished here
+  int part;                 // else: its part
+};
+
+struct __align__(16) Shared {
+  uint64_t item_full[2], item_empty[2], q_full[2], q_empty, full[kMaxUnits], empty[kMaxUnits], s_full[2], p_ready[2],
+      o_done[2], o_free[2], all_done;
+  uint32_t tmem_base;
+  int abort;
+  Item item[2];
+  int parent[2][CP_TREE_MAX];               // of a softmax warpgroup each
+  __align__(16) uint16_t bad[2][8];         // keys of the tile with a non-finite value, 16 each
+};
+
+template <int NQB>
+struct Layout {
+  static constexpr uint32_t q_bytes = 2u * NQB * kUnit;
+  static constexpr int fit = (int)((kSmem - q_bytes - sizeof(Shared)) / kUnit);
+  static constexpr int units = fit < kMaxUnits ? fit : kMaxUnits;
+  static constexpr uint32_t ctl_off = q_bytes + units * kUnit;
+  static constexpr uint32_t alloc = ctl_off + (uint32_t)sizeof(Shared);
+};
+
+struct Maps {
+  CUtensorMap q, k, kr, v;
+};
+
+template <int kId>
+__device__ __forceinline__ void group_sync(int threads) {
+  asm volatile("bar.sync %0, %1;" ::"n"(kId), "r"(threads) : "memory");
+}
+
+// What a call is about: TreeWork (attn_tree.cu) and ExpandedWork (attn_expanded.cu) add
+// kPaged and kExpanded, and say how many items a sequence has (`weight`, 0 for one that is
+// skipped) and what its idx-th is (`make`).
+struct WorkBase {
+  int hq, hkv, group;
+  int tok_tile;            // tokens of a Q tile
+  float scale_log2;
+  SeqRows rows;
+  int total_rows;
+  void* out;               // [total_rows, hq, channels]
+  int* status;
+  float* part_o;           // [parts][channels / 4][256 rows][4]
+  float* part_ml;          // [parts][256 rows][2]: maximum (log2 domain), sum
+  int page_size, num_pages, max_blocks, dn;
+  const int* block_table;
+  const int* parents;
+
+  __device__ void report_empty(int lane) const {
+    if (status && rows.rows_uniform <= 0)
+      for (int s = lane; s < rows.num_seqs; s += 32)
+        if (seq_rows(rows, s) < 1) atomicOr(status, CP_DEV_BOUNDS);
+  }
+};
+
+template <typename T, int NQB, int NVB, typename Work>
+__global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constant__ Maps tm, const Work wk) {
+  using L = Layout<NQB>;
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  constexpr uint32_t kIdescQK = make_idesc_f16(kBf16, 128, kKeys, false);
+  constexpr uint32_t kIdescPV = make_idesc_f16(kBf16, 128, NVB * 64, true);
+  constexpr int kRing = L::units;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sRing = smem + L::q_bytes;
+  Shared* sh = reinterpret_cast<Shared*>(smem + L::ctl_off);
+
+  pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // ---- set-up that reads no global memory: it may overlap the previous kernel
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->item_full[i], 1);
+      mbar_init(&sh->item_empty[i], 10);  // warps 0, 1 and the eight of softmax
+      mbar_init(&sh->q_full[i], 1);
+      mbar_init(&sh->s_full[i], 1);
+      mbar_init(&sh->p_ready[i], 128);
+      mbar_init(&sh->o_done[i], 1);
+      mbar_init(&sh->o_free[i], 128);
+    }
+    mbar_init(&sh->q_empty, 1);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&sh->full[i], 1);
+      mbar_init(&sh->empty[i], 1);
+    }
+    mbar_init(&sh->all_done, 1);
+    sh->abort = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tm.q);
+    tma_prefetch_desc(&tm.k);
+    tma_prefetch_desc(&tm.v);
+    if (Work::kExpanded) tma_prefetch_desc(&tm.kr);
+  }
+  if (warp == 1) {
+    tmem_alloc(&sh->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem_base;
+  volatile int* abort_flag = &sh->abort;
+  auto wait = [&](uint64_t* b, uint32_t parity) { return warp_wait(b, parity, abort_flag, wk.status); };
+  // Item k of this CTA, as every role takes it: false when there are no more.
+  auto take = [&](int k, Item& x) {
+    if (!wait(&sh->item_full[k & 1], (k >> 1) & 1)) return false;
+    x = sh->item[k & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh->item_empty[k & 1]);
+    return x.ntiles >= 0;
+  };
+  pdl_wait();  // everything below reads what earlier kernels wrote
+
+  if (warp < 4) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
+  if (warp == 2) {
+    // ================================================================ scheduling
+    ItemCursor<Work> cur(wk);
+    int k = 0;
+    bool ok = true;
+    Item x;
+    while (ok) {
+      const bool more = cur.next(wk, x);
+      if (k >= 2) ok = wait(&sh->item_empty[k & 1], ((k >> 1) & 1) ^ 1);
+      if (!ok) break;
+      if (lane == 0) {
+        if (!more) x.ntiles = -1;
+        sh->item[k & 1] = x;
+        mbar_arrive(&sh->item_full[k & 1]);
+      }
+      if (!more) break;
+      ++k;
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    if (blockIdx.x == 0) wk.report_empty(lane);
+  } else if (warp == 0) {
+    // ================================================================ producer
+    const int ps = Work::kPaged ? wk.page_size : kKeys, lps = 31 - __clz(ps);
+    const int npg = kKeys / ps;  // boxes of a unit
+    int u = 0;                   // units issued so far
+    int queries = 0;             // items whose queries were loaded
+    uint32_t last_q1 = 0;        // loads of Q tile 1
+    bool ok = true;
+    Item x;
+    for (int k = 0; ok && take(k, x); ++k) {
+      if (x.ntiles == 0) continue;
+      if (queries > 0) ok = wait(&sh->q_empty, (queries - 1) & 1);
+      if (!ok) break;
+      const bool q1 = x.t0 + wk.tok_tile < x.rows;
+      if (lane == 0)
+        for (int w = 0; w < (q1 ? 2 : 1); ++w) {
+          mbar_arrive_expect_tx(&sh->q_full[w], NQB * wk.tok_tile * wk.group * 128);
+          for (int b = 0; b < NQB; ++b)
+            tma_load_3d(smem + (w * NQB + b) * kUnit, &tm.q, &sh->q_full[w], b * 64, x.g * wk.group,
+                        x.row0 + x.t0 + w * wk.tok_tile);
+        }
+      __syncwarp();
+      ++queries;
+      last_q1 += q1;
+      for (int i = 0; ok && i < x.ntiles; ++i) {
+        const int j0 = x.j_begin + i * kKeys;
+        int plane = x.s * wk.hkv + x.g, off = j0;
+        if (Work::kPaged) {
+          const int key = j0 + (lane % npg) * ps, blk = key >> lps;
+          plane = wk.num_pages * wk.hkv;  // out of range: zeros
+          if (key < x.past + x.rows) {
+            const int page = blk < wk.max_blocks ? wk.block_table[(long long)x.s * wk.max_blocks + blk] : -1;
+            if (page >= 0 && page < wk.num_pages) plane = page * wk.hkv + x.g;
+            else if (wk.status && lane < npg) atomicOr(wk.status, CP_DEV_BOUNDS);
+          }
+          off = 0;
+        }
+        for (int e = 0; e < NQB + NVB; ++e, ++u) {
+          const int slot = u % kRing;
+          if (u >= kRing) ok = wait(&sh->empty[slot], ((u / kRing) & 1) ^ 1);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&sh->full[slot], kUnit);
+          __syncwarp();
+          uint8_t* dst = sRing + slot * kUnit;
+          const bool v = e >= NQB;
+          if (Work::kExpanded) {
+            if (lane == 0) {
+              if (v) tma_load_3d(dst, &tm.v, &sh->full[slot], (e - NQB) * 64, x.g, x.key0 + j0);
+              else if (e * 64 < wk.dn) tma_load_3d(dst, &tm.k, &sh->full[slot], e * 64, x.g, x.key0 + j0);
+              else tma_load_3d(dst, &tm.kr, &sh->full[slot], 0, x.key0 + j0, 0);
+            }
+          } else if (lane < npg) {
+            tma_load_3d(dst + lane * ps * 128, v ? &tm.v : &tm.k, &sh->full[slot], (v ? e - NQB : e) * 64, off, plane);
+          }
+        }
+      }
+    }
+    // Every copy has landed before shared memory is released, also after an abort.
+    volatile int zero = 0;
+    if (queries > 0) mbar_wait(&sh->q_full[0], (queries - 1) & 1, &zero, wk.status);
+    if (last_q1 > 0) mbar_wait(&sh->q_full[1], (last_q1 - 1) & 1, &zero, wk.status);
+    for (int i = max(0, u - kRing); i < u; ++i) mbar_wait(&sh->full[i % kRing], (i / kRing) & 1, &zero, wk.status);
+    __syncwarp();
+  } else {
+    // ================================================================ MMA issuer
+    // The whole warp runs the loop, converged; one elected lane issues.
+    auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+    const uint64_t q_desc = make_sdesc_sw128(smem_u32(smem), 16, 1024);
+    const uint64_t k_desc = make_sdesc_sw128(smem_u32(sRing), 16, 1024);
+    const uint32_t tm0 = (uint32_t)uniform((int)tmem);
+    int u0 = 0;   // first unit of the tile whose K comes next
+    uint32_t pq = 0, pp = 0, po = 0, begun = 0;  // bit w: parity of the Q tiles and P tiles taken, of the outputs begun; any begun
+    bool ok = true;
+    Item x;
+    auto slot_of = [](int u) { return u % kRing; };
+    auto unit_full = [&](int u) { return wait(&sh->full[slot_of(u)], (u / kRing) & 1); };
+    // S_w = Q_w K^T with K in units u ..; waits for them when `first`.
+    auto issue_qk = [&](int w, int u, bool first) {
+      for (int b = 0; b < NQB; ++b) {
+        if (first) {
+          if (!unit_full(u + b)) return false;
+          tc_fence_after();
+        }
+        const uint32_t q = (uint32_t)q_desc + (((uint32_t)(w * NQB + b) * kUnit) >> 4);
+        const uint32_t kd = (uint32_t)k_desc + (((uint32_t)slot_of(u + b) * kUnit) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ss_lo(tm0 + 256u * w, q + 2 * kk, (uint32_t)(q_desc >> 32), kd + 2 * kk, (uint32_t)(k_desc >> 32), kIdescQK,
+                    b | kk);
+      }
+      mma_commit_elect(&sh->s_full[w]);
+      return true;
+    };
+    // O_w += P_w V: V's 64-channel units lie where the ring has them, so their step may be negative.
+    auto issue_pv = [&](int w, int u, bool acc) {
+      const int a = slot_of(u), b = NVB > 1 ? slot_of(u + 1) : a;
+      const uint64_t d = make_sdesc_sw128(smem_u32(sRing), 16, 1024);
+      if (NVB == 1 || b == a + 1) {
+        const uint64_t v = make_sdesc_sw128(smem_u32(sRing) + (uint32_t)a * kUnit, kUnit, 1024);
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          mma_ts_elect(tm0 + 256u * w + 128u, tm0 + 256u * w + kk * 8, v + ((kk * 2048) >> 4), kIdescPV, acc || kk > 0);
+      } else {  // the ring's end lies between them: 64 channels at a time
+        constexpr uint32_t kIdescHalf = make_idesc_f16(kBf16, 128, 64, true);
+        for (int h = 0; h < 2; ++h) {
+          const uint64_t v = d + (((uint32_t)(h ? b : a) * kUnit) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            mma_ts_elect(tm0 + 256u * w + 128u + 64u * h, tm0 + 256u * w + kk * 8, v + ((kk * 2048) >> 4), kIdescHalf,
+                         acc || kk > 0);
+        }
+      }
+    };
+    for (int k = 0; ok && take(k, x); ++k) {
+      const int ntiles = uniform(x.ntiles);
+      if (ntiles == 0) continue;
+      const bool q1 = uniform(x.t0 + wk.tok_tile < x.rows) != 0;
+      const int nw = q1 ? 2 : 1;
+      for (int w = 0; ok && w < nw; ++w) {
+        ok = wait(&sh->q_full[w], (pq >> w) & 1);
+        pq ^= 1u << w;
+        tc_fence_after();
+        ok = ok && issue_qk(w, u0, w == 0);
+      }
+      if (!ok) break;
+      for (int b = 0; b < NQB; ++b) mma_commit_elect(&sh->empty[slot_of(u0 + b)]);
+      if (ntiles == 1) mma_commit_elect(&sh->q_empty);
+      for (int i = 0; ok && i < ntiles; ++i) {
+        const int v0 = u0 + NQB, u1 = v0 + NVB;  // this tile's V, the next tile's K
+        for (int w = 0; ok && w < nw; ++w) {
+          ok = wait(&sh->p_ready[w], (pp >> w) & 1);
+          pp ^= 1u << w;
+          if (ok && w == 0)
+            for (int b = 0; ok && b < NVB; ++b) ok = unit_full(v0 + b);
+          if (ok && i == 0 && ((begun >> w) & 1)) ok = wait(&sh->o_free[w], ((po >> w) & 1) ^ 1);  // the output before has left TMEM
+          if (!ok) break;
+          tc_fence_after();
+          issue_pv(w, v0, i > 0);
+          if (i == 0) {
+            po ^= 1u << w;
+            begun |= 1u << w;
+          }
+          if (i + 1 == ntiles) mma_commit_elect(&sh->o_done[w]);
+          if (w == nw - 1)
+            for (int b = 0; b < NVB; ++b) mma_commit_elect(&sh->empty[slot_of(v0 + b)]);
+          if (i + 1 < ntiles) ok = issue_qk(w, u1, w == 0);
+        }
+        if (!ok) break;
+        if (i + 1 < ntiles)
+          for (int b = 0; b < NQB; ++b) mma_commit_elect(&sh->empty[slot_of(u1 + b)]);
+        if (i + 2 == ntiles) mma_commit_elect(&sh->q_empty);  // the last scores of the item are issued
+        u0 = u1;
+      }
+    }
+    mma_commit_elect(&sh->all_done);
+    volatile int zero = 0;  // wait even after an abort: MMAs may still be in flight
+    mbar_wait(&sh->all_done, 0, &zero, wk.status);
+    __syncwarp();
+  }
+  } else {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+  // ================================================================ softmax, output
+  const int w = (warp - 4) >> 2;            // Q tile of this warpgroup
+  const int quarter = warp & 3;             // TMEM lanes [32 * quarter, + 32)
+  const int m = quarter * 32 + lane;        // this thread's row of its Q tile
+  const uint32_t s_col = tmem + ((uint32_t)(quarter * 32) << 16) + 256u * w, o_col = s_col + 128u;
+  const int mtok = m / wk.group, mhead = m % wk.group;
+  int v_unit = NQB;     // first unit of the tile's V
+  int ns = 0, no = 0;   // score tiles, outputs so far
+  Item x;
+  // After a wait that gave up, an item's walk goes on without waiting, so that its barriers stay whole; its output is not
+  // written, and the warps leave together.
+  for (int k = 0;; ++k) {
+    bool alive = take(k, x) && !*abort_flag;
+    int any;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 4, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(any)
+                 : "r"((uint32_t)!alive)
+                 : "memory");
+    if (any) break;
+    const bool q1 = x.t0 + wk.tok_tile < x.rows;
+    const int tok = x.t0 + w * wk.tok_tile + mtok;  // this row's token
+    const bool row_ok = mtok < wk.tok_tile && tok < x.rows;
+    const int n = x.past + x.rows;
+    if (w == 1 && !q1) {
+      v_unit += x.ntiles * (NQB + NVB);
+      continue;
+    }
+    uint64_t see_lo = 0, see_hi = 0;  // a tree's row: the call's rows that it sees
+    if (!Work::kExpanded) {
+      if (m < x.rows) {
+        int up = wk.parents[x.row0 + m];
+        if (up < -1 || up >= m) {
+          up = -1;
+          if (wk.status) atomicOr(wk.status, CP_DEV_BOUNDS);
+        }
+        sh->parent[w][m] = up;
+      }
+      if (w == 0) group_sync<1>(128);
+      else group_sync<2>(128);
+      for (int j = row_ok ? tok : -1; j >= 0; j = sh->parent[w][j]) {
+        if (j < 64) see_lo |= 1ull << j;
+        else see_hi |= 1ull << (j - 64);
+      }
+      if (w == 0) group_sync<1>(128);  // the next item's parents take their place
+      else group_sync<2>(128);
+    }
+    const int seen = Work::kExpanded ? x.past + tok + 1 : x.past;  // keys [0, seen) are seen, and in a tree the row's ancestors
+    float m_run = -INFINITY, l_run = 0.f;
+    for (int i = 0; i < x.ntiles; ++i, ++ns, v_unit += NQB + NVB) {
+      alive = alive && wait(&sh->s_full[w], ns & 1);
+      tc_fence_after();
+      uint32_t sv[128];
+      tmem_ld32(s_col + 0, &sv[0]);
+      tmem_ld32(s_col + 32, &sv[32]);
+      tmem_ld32(s_col + 64, &sv[64]);
+      tmem_ld32(s_col + 96, &sv[96]);
+      tmem_wait_ld();
+      const int j0 = x.j_begin + i * kKeys;
+      const bool guard = j0 + kKeys > x.all;  // keys that some row of the item does not see
+      uint64_t vis[2] = {~0ull, ~0ull};
+      if (guard) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int c = seen - j0 - 64 * h;  // columns [0, c) of this half are seen
+          vis[h] = !row_ok ? 0 : c >= 64 ? ~0ull : c > 0 ? (1ull << c) - 1 : 0;
+          if (!Work::kExpanded && row_ok && c < 64) vis[h] |= bits_from(see_lo, see_hi, -c);
+        }
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (!((vis[c >> 6] >> (c & 63)) & 1)) sv[c] = __float_as_uint(-INFINITY);
+      }
+      float mx;
+      {
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 128; c += 8) {
+          m4[0] = fmax3(m4[0], __uint_as_float(sv[c + 0]), __uint_as_float(sv[c + 1]));
+          m4[1] = fmax3(m4[1], __uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3]));
+          m4[2] = fmax3(m4[2], __uint_as_float(sv[c + 4]), __uint_as_float(sv[c + 5]));
+          m4[3] = fmax3(m4[3], __uint_as_float(sv[c + 6]), __uint_as_float(sv[c + 7]));
+        }
+        mx = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
+      }
+      const float mx2 = mx * wk.scale_log2;  // scale > 0, so the max commutes with it
+      const bool grow = mx2 > m_run + kRescaleLog2 || (m_run == -INFINITY && mx2 != -INFINITY);
+      const float m_new = grow ? mx2 : m_run;
+      const float alpha = grow ? (m_run == -INFINITY ? 0.f : ex2_approx(m_run - m_new)) : 1.f;
+      const float neg_m = m_new == -INFINITY ? 0.f : -m_new;
+      float ps[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < 64; ++c) {
+        float x0 = __uint_as_float(sv[2 * c]), x1 = __uint_as_float(sv[2 * c + 1]);
+        ffma2(x0, x1, wk.scale_log2, neg_m);
+        x0 = ex2_approx(x0);
+        x1 = ex2_approx(x1);
+        fadd2(ps[2 * (c & 1)], ps[2 * (c & 1) + 1], x0, x1);
+        sv[c] = pack2<T>(x0, x1);
+      }
+      l_run = l_run * alpha + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
+      m_run = m_new;
+      tmem_st32(s_col + 0, &sv[0]);
+      tmem_st32(s_col + 32, &sv[32]);
+      // O holds P V of the earlier tiles (complete: see the ordering note above).
+      if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+        for (int c = 0; c < 2 * NVB; ++c) {
+          uint32_t ov[32];
+          tmem_ld32(o_col + 32 * c, ov);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+          tmem_st32(o_col + 32 * c, ov);
+        }
+      }
+      if (guard) {
+        // ---- values that must not meet a weight of 0: the threads of the item's Q tiles share the tile's keys
+        for (int b = 0; b < NVB; ++b) alive = alive && wait(&sh->full[(v_unit + b) % kRing], ((v_unit + b) / kRing) & 1);
+        const int per = q1 ? 2 : 1, me = w * 128 + m;   // threads of a key; this one
+        const int key = me / per, part = me % per;
+        const bool gone = j0 + key >= n;
+        bool bad = gone;
+        constexpr int kChunks = NVB * 8;  // 16-byte chunks of a key
+        auto chunk = [&](int c) {         // in an order that spreads the threads over the banks
+          c = (c + key) % kChunks;
+          return reinterpret_cast<uint4*>(sRing + ((v_unit + c / 8) % kRing) * kUnit + key * 128 + (c & 7) * 16);
+        };
+        if (!bad && j0 + key >= x.all)
+          for (int c = part; c < kChunks; c += per) bad = bad || nonfinite8<T>(*chunk(c));
+        if (per == 2) bad = __shfl_xor_sync(0xffffffffu, bad, 1) || bad;
+        if (bad)
+          for (int c = part; c < kChunks; c += per) *chunk(c) = make_uint4(0, 0, 0, 0);
+        uint32_t bits = __ballot_sync(0xffffffffu, bad && !gone);
+        if (lane == 0) {
+          if (per == 2) {
+            sh->bad[i & 1][me / 32] = (uint16_t)even_bits(bits);
+          } else {
+            sh->bad[i & 1][2 * quarter] = (uint16_t)bits;
+            sh->bad[i & 1][2 * quarter + 1] = (uint16_t)(bits >> 16);
+          }
+        }
+        fence_proxy_async_smem();  // the tensor cores read V through the async proxy
+        group_sync<3>(128 * per);
+        const uint4 y = *reinterpret_cast<const uint4*>(sh->bad[i & 1]);
+        if ((vis[0] & (y.x | (uint64_t)y.y << 32)) | (vis[1] & (y.z | (uint64_t)y.w << 32))) l_run = __int_as_float(0x7fffffff);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&sh->p_ready[w]);
+    }
+
+    // ---- output
+    if (x.ntiles > 0) alive = alive && wait(&sh->o_done[w], no & 1);
+    tc_fence_after();
+    const bool write = row_ok && alive;
+    const long long row = (long long)(x.row0 + tok) * wk.hq + x.g * wk.group + mhead;
+    if (x.whole) {
+      const float inv = l_run == 0.f ? 0.f : 1.f / l_run;  // a NaN stays
+      uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(wk.out) + row * (NVB * 64));
+#pragma unroll
+      for (int c = 0; c < 2 * NVB; ++c) {
+        uint32_t ov[32];
+        if (x.ntiles > 0) {
+          tmem_ld32(o_col + 32 * c, ov);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) ov[e] = 0;
+        }
+        if (write) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t y[4];
+#pragma unroll
+            for (int f = 0; f < 4; ++f)
+              y[f] = pack2<T>(__uint_as_float(ov[8 * e + 2 * f]) * inv, __uint_as_float(ov[8 * e + 2 * f + 1]) * inv);
+            out[4 * c + e] = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        }
+      }
+    } else {
+      // [16-byte piece][256 rows]: a warp's stores are 512 bytes in a row.
+      if (write) *reinterpret_cast<float2*>(wk.part_ml + ((long long)x.part * 256 + w * 128 + m) * 2) = make_float2(m_run, l_run);
+      float4* part = reinterpret_cast<float4*>(wk.part_o) + ((long long)x.part * (NVB * 16)) * 256 + w * 128 + m;
+#pragma unroll
+      for (int c = 0; c < 2 * NVB; ++c) {
+        uint32_t ov[32];
+        tmem_ld32(o_col + 32 * c, ov);
+        tmem_wait_ld();
+        if (write) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            part[(8 * c + e) * 256] = make_float4(__uint_as_float(ov[4 * e]), __uint_as_float(ov[4 * e + 1]),
+                                                  __uint_as_float(ov[4 * e + 2]), __uint_as_float(ov[4 * e + 3]));
+        }
+      }
+    }
+    if (x.ntiles > 0) {
+      ++no;
+      tc_fence_before();
+      mbar_arrive(&sh->o_free[w]);
+    }
+    if (!alive) *abort_flag = 1;
+  }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <typename T, int NQB, int NVB, typename Work>
+cudaError_t launch(const Maps& tm, const Work& wk, long long items, cudaStream_t st) {
+  using L = Layout<NQB>;
+  static_assert(L::units >= NQB + NVB, "a tile fits the ring");
+  const auto kernel = pairs_kernel<T, NQB, NVB, Work>;
+  // Raise the dynamic shared-memory limit once per device, so later calls --
+  // including ones being captured into a CUDA graph -- only launch.
+  static std::atomic<uint64_t> ready_mask{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  constexpr uint32_t smem = L::alloc > 120u * 1024u ? L::alloc : 120u * 1024u;  // one CTA an SM: each takes all of TMEM
+  if (!(ready_mask.load(std::memory_order_acquire) & bit)) {
+    // The register split is only sound at the per-thread count it was sized
+    // for: refuse to launch a build that came out at another count.
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kernel);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs != kRegsLaunch || fa.sharedSizeBytes != 0) return cudaErrorInvalidDeviceFunction;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    ready_mask.fetch_or(bit, std::memory_order_release);
+  }
+  return launch_pdl(kernel, dim3((unsigned)std::min<long long>(items, 152)), dim3(kThreads), smem, st, tm, wk);
+}
+
+}  // namespace pairs
+}  // namespace cp

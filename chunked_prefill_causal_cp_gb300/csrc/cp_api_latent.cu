@@ -60,10 +60,18 @@ int rows_attention(const cp_layer_desc* d, bool latent, int dqk, int dv, float s
   if (d->num_q_heads > 65535 || (int64_t)total_rows * d->num_q_heads > INT32_MAX / 4) return CP_ERR_UNSUPPORTED;
   const int64_t pairs = (int64_t)total_rows * d->num_q_heads;
   if (overlap(out, pairs * dv * 2, q, pairs * dqk * 2)) return CP_ERR_INVALID_ARG;
-  const RowsPlan p = rows_plan(d->num_q_heads, d->num_kv_heads, latent, dv, cu_rows == nullptr, num_seqs, total_rows, max_ctx);
-  if ((double)p.tiles * p.max_splits * d->num_kv_heads > INT32_MAX || (double)p.tiles * p.tile_rows > INT32_MAX || p.slots > INT32_MAX)
-    return CP_ERR_UNSUPPORTED;
-  if (p.bytes > 0 && (!workspace || !aligned16(workspace) || (double)workspace_bytes < p.bytes)) return CP_ERR_WORKSPACE;
+  RowsPlan p{};
+  TreePlan tp{};
+  if (latent) {
+    p = rows_plan(d->num_q_heads, dv, cu_rows == nullptr, num_seqs, total_rows, max_ctx);
+    if ((double)p.tiles * p.max_splits > INT32_MAX || (double)p.tiles * p.nr > INT32_MAX || p.slots > INT32_MAX)
+      return CP_ERR_UNSUPPORTED;
+  } else {
+    tp = tree_plan(d->num_q_heads, d->num_kv_heads, dv, cu_rows == nullptr, num_seqs, total_rows, max_ctx);
+    if (tp.items > INT32_MAX || tp.tiles > INT32_MAX / 16) return CP_ERR_UNSUPPORTED;
+  }
+  const double need = latent ? p.bytes : tp.bytes;
+  if (need > 0 && (!workspace || !aligned16(workspace) || (double)workspace_bytes < need)) return CP_ERR_WORKSPACE;
   RowsAttnArgs a;
   std::memset(&a, 0, sizeof(a));
   a.hq = d->num_q_heads;
@@ -83,22 +91,25 @@ int rows_attention(const cp_layer_desc* d, bool latent, int dqk, int dv, float s
   a.v = v;
   a.out = out;
   a.status = dev_status;
-  a.latent = latent;
+  a.part_o = static_cast<float*>(workspace);
+  if (!latent) {
+    a.part_ml = a.part_o + tp.slots * 256 * dv;
+    return launch_result(launch_tree(a, tp, d->dtype, static_cast<cudaStream_t>(stream)));
+  }
   a.q_rows = p.q_rows;
-  a.tile_rows = p.tile_rows;
   a.nr = p.nr;
   a.tiles_bound = (int)p.tiles;
   a.max_splits = p.max_splits;
   a.part_slots = (int)p.slots;
-  a.part_o = static_cast<float*>(workspace);
-  a.part_ml = a.part_o + p.slots * a.hkv * p.nr * dv;
+  a.part_ml = a.part_o + p.slots * p.nr * dv;
   return launch_result(launch_rows_attn(a, d->dtype, static_cast<cudaStream_t>(stream)));
 }
 
 size_t rows_workspace(const cp_layer_desc* d, bool latent, int dv, int32_t total_rows, int32_t max_ctx, int32_t num_seqs) {
   if (total_rows <= 0 || max_ctx <= 0 || num_seqs <= 0) return 0;
   // Ragged rows: no call of equal rows within the bounds has more tiles.
-  const double bytes = rows_plan(d->num_q_heads, d->num_kv_heads, latent, dv, false, num_seqs, total_rows, max_ctx).bytes;
+  const double bytes = latent ? rows_plan(d->num_q_heads, dv, false, num_seqs, total_rows, max_ctx).bytes
+                              : tree_plan(d->num_q_heads, d->num_kv_heads, dv, false, num_seqs, total_rows, max_ctx).bytes;
   return bytes < 4e18 ? (size_t)bytes : SIZE_MAX;
 }
 

@@ -31,29 +31,43 @@ struct LatentAppendArgs {
   int* status;
 };
 
-// Splits of a sequence of n keys whose rows make nt tiles (of every KV head): few keys a
-// split for a short context, where the wait for one CTA's walk is what counts, more for a
-// long one, and no more than kRowsMaxSlots (tile, split) pairs a sequence.  By the
-// sequence's own sizes alone, so a row's result never depends on what shares the launch.
-constexpr int kRowsMaxSlots = 304;  // twice 152 SMs
+// Splits of a sequence of n positions whose (row, head) pairs make nt tiles, over a latent
+// cache: few keys a split for a short context, where the wait for one CTA's walk is what
+// counts, more for a long one, whose parts cost less then, and no more than kRowsItems
+// (tile, split) items.  By the sequence's own sizes alone, so a row's result never
+// depends on what shares the launch.
+constexpr int kRowsItems = 304;  // twice the SMs
 __host__ __device__ inline int rows_split_base(int n) { return n <= 2048 ? 128 : n <= 8192 ? 256 : n <= 16384 ? 512 : 1024; }
 __host__ __device__ inline int rows_splits(int n, int nt) {
-  const int cap = kRowsMaxSlots / nt, k = (n - 1) / rows_split_base(n) + 1;
+  const int cap = kRowsItems / nt, k = (n - 1) / rows_split_base(n) + 1;
   return cap <= 1 ? 1 : k < cap ? k : cap;
 }
 // Keys of each split: whole tiles of 64.
 __host__ __device__ inline int rows_split_keys(int n, int splits) { return ((n - 1) / splits + 64) & ~63; }
-// Most splits of a sequence of up to ctx keys and nt tiles, and the parts it may need.
-__host__ __device__ inline int rows_max_splits(int ctx, int nt) {
+// Most splits of a sequence of up to ctx positions and nt tiles.
+inline int rows_max_splits(int ctx, int nt) {
   int m = rows_splits(ctx, nt);
   const int steps[3] = {2048, 8192, 16384};
-  for (int i = 0; i < 3; ++i)
-    if (ctx > steps[i] && rows_splits(steps[i], nt) > m) m = rows_splits(steps[i], nt);
+  for (int s : steps)
+    if (ctx > s && rows_splits(s, nt) > m) m = rows_splits(s, nt);
   return m;
 }
-__host__ __device__ inline int rows_slots(int nt, int max_one) {  // max_one: rows_max_splits(ctx, 1)
-  const int cap = nt > kRowsMaxSlots ? 1 : kRowsMaxSlots / nt, m = max_one < cap ? max_one : cap;
-  return m > 1 ? nt * m : 0;
+
+// The same for a drafted tree over a K/V cache, nt pairs of Q tiles times KV heads, in
+// whole tiles of 128 keys.
+constexpr int kTreeItems = 152;  // (pair, KV head, split) items of a split sequence, at most: the SMs
+__host__ __device__ inline int tree_split_base(int n) { return n <= 2048 ? 128 : n <= 4096 ? 256 : n <= 8192 ? 512 : n <= 16384 ? 1024 : 2048; }
+__host__ __device__ inline int tree_splits(int n, int nt) {
+  const int cap = kTreeItems / nt, k = (n - 1) / tree_split_base(n) + 1;
+  return cap <= 1 ? 1 : k < cap ? k : cap;
+}
+__host__ __device__ inline int tree_split_keys(int n, int splits) { return ((n - 1) / splits + 128) & ~127; }
+inline int tree_max_splits(int ctx, int nt) {
+  int m = tree_splits(ctx, nt);
+  const int steps[4] = {2048, 4096, 8192, 16384};
+  for (int s : steps)
+    if (ctx > s && tree_splits(s, nt) > m) m = tree_splits(s, nt);
+  return m;
 }
 
 // Attention of few rows over a long cache (cp_latent_attn, cp_tree_attn).  A
@@ -74,9 +88,8 @@ struct RowsAttnArgs {
   const void* v;
   void* out;               // [total_rows, hq, dv]
   int* status;
-  bool latent;
+  // A latent cache's (cp_latent_attn):
   int q_rows;              // pairs of a tile that the call can have, at most
-  int tile_rows;           // (row, head) pairs of a tile: nr, or whole tokens' if hkv > 1
   int nr;                  // pairs a tile has room for: 64 or 128, by the layer alone
   int tiles_bound;         // tiles of the call, at most
   int max_splits;          // of any sequence
@@ -87,13 +100,24 @@ struct RowsAttnArgs {
 
 // How such a call runs, from its host bounds.
 struct RowsPlan {
-  int nr, tile_rows, q_rows;
+  int nr, q_rows;
   long long tiles;         // at most
   int max_splits;
   long long slots;         // parts, at most
   double bytes;            // of workspace; in floating point: absurd sizes must not wrap
 };
-RowsPlan rows_plan(int hq, int hkv, bool latent, int dv, bool uniform, long long num_seqs, long long total_rows, int max_ctx);
+// How a call of drafted trees over a K/V cache runs.
+struct TreePlan {
+  int tok_tile;            // tokens of a Q tile
+  long long tiles, items;  // Q tiles, items, at most
+  int max_splits;
+  long long slots;         // parts, at most
+  double bytes;
+};
+TreePlan tree_plan(int hq, int hkv, int dv, bool uniform, long long num_seqs, long long total_rows, int max_ctx);
+cudaError_t launch_tree(const RowsAttnArgs& a, const TreePlan& p, int dtype, cudaStream_t st);
+
+RowsPlan rows_plan(int heads, int dv, bool uniform, long long num_seqs, long long total_rows, int max_ctx);
 
 // Attention of chunks over expanded keys and values (cp_latent_chunk_attn).
 struct ExpandedArgs {
