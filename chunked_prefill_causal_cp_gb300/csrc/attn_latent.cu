@@ -8,13 +8,15 @@
 // 512 channels leaves TMEM room for 64 pairs only if the channels lie over its lanes.
 // Hence
 //   S[pairs x 64 keys] = Q K^T     A = Q, B = K, both K-major: a pair's scores are a
-//                                  TMEM lane, two threads' with 32 keys each
+//                                  TMEM lane, two threads' with 32 keys each.  Up to 64
+//                                  pairs are an M of 64, whose rows lie in the lower 16
+//                                  lanes of each quarter of TMEM
 //   P -> shared memory             [pair][64 keys] in 16 bits, one swizzled 128-byte row
 //   O^T[128 channels x pairs] += V^T P^T   A = V as it lies (MN-major), B = P (K-major),
 //                                  a block of TMEM columns for each 128 channels
 // A raised maximum scales a column of O^T, which all lanes hold: the threads vote each
-// tile (a barrier that ORs), and only when some maximum grew by more than 2^8 do they
-// fetch the factors from shared memory and pass over O.
+// tile (a barrier that ORs), and only when some score passes its pair's maximum by more
+// than 2^8 do they exchange maxima, leave the factors in shared memory and pass over O.
 //
 // One persistent CTA an SM, 384 threads: warp 0 TMA producer, warp 1 TMEM and MMA issue,
 // warp 2 scheduling (finds the CTA's items, two ahead), warps 4-11 softmax and output.
@@ -152,6 +154,19 @@ struct Work : RowsAttnArgs {
   }
 };
 
+// A place in the ring of stages, and how often it came round (divisions by the number of stages, made where the MMAs
+// are issued, took longer than the MMAs).
+struct Ring {
+  int stage = 0;
+  uint32_t turn = 0;  // parity
+  __device__ __forceinline__ void advance(int stages) {
+    if (++stage == stages) {
+      stage = 0;
+      turn ^= 1u;
+    }
+  }
+};
+
 // Barriers of the eight softmax warps, one of which also ORs a predicate.
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ bool softmax_any(bool x) {
@@ -244,8 +259,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ================================================================ producer
     const int ps = kPaged ? min(a.cache.page_size, kTile) : kTile, lps = kPaged ? 31 - __clz(a.cache.page_size) : 0;
     const int npg = kTile / ps;  // boxes of a block
+    Ring ring;
     int gt = 0, queries = 0;     // tiles, items' queries issued so far
-    int landed = 0;              // groups of tile gt that were issued, after an abort
+    uint32_t begun = 0, phase = 0;  // bit kGroups * stage + group: any copy begun, parity of their number
     bool ok = true;
     Item x;
     for (int k = 0; ok && take(k, x); ++k) {
@@ -257,8 +273,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       queries = k + 1;
-      for (int i = 0; i < x.ntiles; ++i, ++gt) {
-        const int st = gt % L.stages;
+      for (int i = 0; ok && i < x.ntiles; ++i, ++gt, ring.advance(L.stages)) {
+        const int st = ring.stage;
         const int j0 = x.j_begin + i * kTile;
         // This lane's boxes: idx = lane, lane + 32, ...: page idx % npg of block idx / npg.
         int plane = x.s, off = j0;
@@ -274,9 +290,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int e = 0; e < L.ngroups; ++e) {
           const int j = e == 0 ? L.ngroups - 1 : e - 1;  // the last group is free first
-          if (gt >= L.stages) ok = wait(&sh->empty[st][j], ((gt / L.stages) & 1) ^ 1);
+          if (gt >= L.stages) ok = wait(&sh->empty[st][j], ring.turn ^ 1);
           if (!ok) break;
           const int b0 = group_first(j), nb = group_end(j) - b0;
+          begun |= 1u << (kGroups * st + j);
+          phase ^= 1u << (kGroups * st + j);
           if (lane == 0) mbar_arrive_expect_tx(&sh->full[st][j], nb * kBlock);
           __syncwarp();
           for (int idx = lane; idx < npg * nb; idx += 32) {  // npg divides 32: the page stays the lane's
@@ -284,21 +302,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_3d(sStage + st * L.stage_bytes + b * kBlock + (idx % npg) * ps * 128, &tm_k, &sh->full[st][j], b * 64, off,
                         plane);
           }
-          landed = e + 1;
         }
-        if (!ok) break;
-        landed = 0;
       }
     }
     // Every copy has landed before shared memory is released, also after an abort.
     volatile int zero = 0;
     if (queries > 0) mbar_wait(&sh->q_full, (queries - 1) & 1, &zero, a.status);
-    for (int i = max(0, gt - L.stages + (landed ? 1 : 0)); i < gt; ++i)
-      for (int j = 0; j < L.ngroups; ++j) mbar_wait(&sh->full[i % L.stages][j], (i / L.stages) & 1, &zero, a.status);
-    for (int e = 0; e < L.ngroups; ++e) {  // of a tile left halfway: its first groups, the others' last phase
-      const int j = e == 0 ? L.ngroups - 1 : e - 1, i = e < landed ? gt : gt - L.stages;
-      if (landed && i >= 0) mbar_wait(&sh->full[i % L.stages][j], (i / L.stages) & 1, &zero, a.status);
-    }
+    for (int i = 0; i < kMaxStages * kGroups; ++i)
+      if ((begun >> i) & 1) mbar_wait(&sh->full[i / kGroups][i % kGroups], ((phase >> i) & 1) ^ 1, &zero, a.status);
     __syncwarp();
   } else if (warp == 1) {
     // ================================================================ MMA issuer
@@ -306,47 +317,49 @@ __global__ void __launch_bounds__(kThreads, 1)
     // MMAs issue back to back.
     auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
     auto test = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test(b, parity)) != 0; };
-    const uint32_t idesc_qk = make_idesc_f16(kBf16, 128, kTile, false);
     const uint64_t q_desc = make_sdesc_sw128(smem_u32(smem), 16, 1024);
     const uint64_t k_desc = make_sdesc_sw128(smem_u32(sStage), 16, 1024);
     const uint64_t v_desc = make_sdesc_sw128(smem_u32(sStage), kBlock, 1024);
     const uint64_t p_desc = make_sdesc_sw128(smem_u32(sP), 16, 1024);
     const uint32_t q_step = (uint32_t)a.nr * 8;  // of a descriptor: 16 bytes
     const uint32_t tm = (uint32_t)uniform((int)tmem);
-    int g0 = 0;  // tiles of the items before
+    const uint32_t stage_step = L.stage_bytes >> 4;
+    Ring qk, pv;             // of the tile whose scores, whose output is issued next
+    uint32_t tiles = 0;      // scores issued so far
+    uint32_t p_phase = 0;    // parity of the next P
     bool ok = true;
     Item x;
-    for (int k = 0; ok && take(k, x); ++k) {
+    for (int k = 0; ok && uniform(take(k, x)); ++k) {
       const int ntiles = uniform(x.ntiles);
+      const uint32_t idesc_qk = make_idesc_f16(kBf16, uniform(x.pairs) <= 64 ? 64 : 128, kTile, false);
       const uint32_t idesc_pv = make_idesc_f16(kBf16, 128, (uniform(x.pairs) + 15) & ~15, false) | (1u << 15);  // A MN-major
       ok = wait(&sh->q_full, k & 1);
       int next = 0, part = 0;  // tile, and group in order of arrival, whose scores are issued next
       for (int i = 0; ok && i < ntiles; ++i) {
         uint64_t t0 = 0;
         for (uint32_t it = 1;; ++it) {
-          if (next < ntiles && next <= i + 1) {
-            const int gn = g0 + next, st = gn % L.stages, j = part == 0 ? L.ngroups - 1 : part - 1;
-            if (test(&sh->full[st][j], (gn / L.stages) & 1)) {
-              tc_fence_after();
-              const uint32_t d = tm + 64u * (gn & 1);
-              const int b0 = group_first(j), b1 = group_end(j);
-              uint32_t q = (uint32_t)q_desc + b0 * q_step;
-              uint32_t kd = (uint32_t)k_desc + (((uint32_t)st * L.stage_bytes + b0 * kBlock) >> 4);
-              for (int b = b0; b < b1; ++b, q += q_step, kd += kBlock >> 4)
+          if (next > i && test(&sh->p_ready, p_phase)) break;  // first: it gives stages back
+          const int j = part == 0 ? L.ngroups - 1 : part - 1;
+          if (next < ntiles && next <= i + 1 && test(&sh->full[qk.stage][j], qk.turn)) {
+            tc_fence_after();
+            const uint32_t d = tm + 64u * (tiles & 1);
+            const int b0 = group_first(j), b1 = group_end(j);
+            uint32_t q = (uint32_t)q_desc + b0 * q_step, kd = (uint32_t)k_desc + qk.stage * stage_step + b0 * (kBlock >> 4);
+            for (int b = b0; b < b1; ++b, q += q_step, kd += kBlock >> 4)
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                  mma_ss_lo(d, q + 2 * kk, (uint32_t)(q_desc >> 32), kd + 2 * kk, (uint32_t)(k_desc >> 32), idesc_qk,
-                            part | (b - b0) | kk);
-              if (++part == L.ngroups) {
-                mma_commit_elect(&sh->s_full[gn & 1]);
-                if (vgroups < L.ngroups) mma_commit_elect(&sh->empty[st][L.ngroups - 1]);  // the rotated part is read
-                part = 0;
-                if (++next == ntiles) mma_commit_elect(&sh->q_empty);
-              }
-              continue;
+              for (int kk = 0; kk < 4; ++kk)
+                mma_ss_lo(d, q + 2 * kk, (uint32_t)(q_desc >> 32), kd + 2 * kk, (uint32_t)(k_desc >> 32), idesc_qk,
+                          part | (b - b0) | kk);
+            if (++part == L.ngroups) {
+              mma_commit_elect(&sh->s_full[tiles & 1]);
+              if (vgroups < L.ngroups) mma_commit_elect(&sh->empty[qk.stage][L.ngroups - 1]);  // the rotated part is read
+              part = 0;
+              ++tiles;
+              qk.advance(L.stages);
+              if (++next == ntiles) mma_commit_elect(&sh->q_empty);
             }
+            continue;
           }
-          if (next > i && test(&sh->p_ready, (g0 + i) & 1)) break;
           if ((it & 63u) == 0) {
             int stop = 0;
             if (lane == 0) {
@@ -365,19 +378,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok && i == 0 && k > 0) ok = wait(&sh->o_free, (k - 1) & 1);  // the item before has left O
         if (!ok) break;
+        p_phase ^= 1u;
         tc_fence_after();
-        const int st = (g0 + i) % L.stages;
-        uint32_t vd = (uint32_t)v_desc + (((uint32_t)st * L.stage_bytes) >> 4), d = tm + 128u;
+        uint32_t vd = (uint32_t)v_desc + pv.stage * stage_step, d = tm + 128u;
         for (int b = 0; b < L.nvb; b += 2, vd += kBlock >> 3, d += a.nr) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_ss_lo(d, vd + 128 * kk, (uint32_t)(v_desc >> 32), (uint32_t)p_desc + 2 * kk, (uint32_t)(p_desc >> 32), idesc_pv,
                       i | kk);
-          if (b % 4 == 2 || b + 2 >= L.nvb) mma_commit_elect(&sh->empty[st][b / 4]);
+          if ((b & 2) || b + 2 >= L.nvb) mma_commit_elect(&sh->empty[pv.stage][b >> 2]);
         }
         mma_commit_elect(&sh->pv_done);
+        pv.advance(L.stages);
       }
-      g0 += ntiles;
     }
     mma_commit_elect(&sh->all_done);
     volatile int zero = 0;  // wait even after an abort: MMAs may still be in flight
@@ -386,11 +399,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ================================================================ softmax, output
     const int half = (warp - 4) >> 2, quarter = warp & 3;
-    const int m = quarter * 32 + lane;  // this thread's pair of the tile, with keys [32 half, + 32)
-    const int me = half * 128 + m;
+    const int me = half * 128 + quarter * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const int nob = L.nvb / 2;
     int gt = 0;
+    Ring ring;
     Item x;
     for (int k = 0;; ++k) {
       // After a wait that gave up, an item's walk goes on without waiting, so that its barriers stay whole; its output is
@@ -398,7 +411,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool alive = take(k, x);
       if (softmax_any(!alive)) break;
       const int n = x.past + x.rows;  // positions written, this call's rows among them
-      const bool row_ok = m < x.pairs, active = quarter * 32 < x.pairs;
+      // This thread's pair of the tile, with keys [32 half, + 32) of each 64.
+      const bool narrow = x.pairs <= 64;  // an M of 64
+      const int m = narrow ? quarter * 16 + (lane & 15) : quarter * 32 + lane;
+      const bool row_ok = m < x.pairs && !(narrow && lane >= 16), active = quarter * (narrow ? 16 : 32) < x.pairs;
       const int tok = (x.first + m) / a.hq;
       uint64_t see_lo = 0, see_hi = 0;  // a tree's row: the call's rows that it sees
       if (a.parents) {
@@ -418,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         softmax_sync();  // the factors take the parents' place
       }
       float m_run = -INFINITY, l_run = 0.f;
-      for (int i = 0; i < x.ntiles; ++i, ++gt) {
+      for (int i = 0; i < x.ntiles; ++i, ++gt, ring.advance(L.stages)) {
         const int j0 = x.j_begin + i * kTile;
         alive = alive && wait(&sh->s_full[gt & 1], (gt >> 1) & 1);
         tc_fence_after();
@@ -447,16 +463,47 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           mx = fmaxf(m4[0], m4[1]);
         }
-        sh->top[half][m] = mx;
-        softmax_sync();
-        float alpha = 1.f;
-        if (active) {
-          const float mx2 = fmaxf(mx, sh->top[half ^ 1][m]) * a.scale_log2;  // scale > 0: it commutes
-          const bool first = m_run == -INFINITY;
-          if (mx2 > m_run + kRescaleLog2 || (first && mx2 != -INFINITY)) {
-            if (!first) alpha = ex2_approx(m_run - mx2);  // first: nothing but zeros so far
-            m_run = mx2;
+        mx *= a.scale_log2;  // scale > 0: it commutes
+        const bool raise = softmax_any(row_ok && (mx > m_run + kRescaleLog2 || (m_run == -INFINITY && mx != -INFINITY)));
+        if (raise) {
+          // The two halves of a pair agree on its maximum; what is smaller than the threshold stays.
+          if (row_ok) sh->top[half][m] = mx;
+          softmax_sync();
+          float alpha = 1.f;
+          if (row_ok) {
+            mx = fmaxf(mx, sh->top[half ^ 1][m]);
+            if (mx > m_run + kRescaleLog2 || (m_run == -INFINITY && mx != -INFINITY)) {
+              if (m_run != -INFINITY) alpha = ex2_approx(m_run - mx);  // else nothing but zeros so far
+              m_run = mx;
+              l_run *= alpha;
+            }
+            if (half == 0) sh->alpha[m] = alpha;
           }
+          if (i > 0) {
+            softmax_sync();
+            alive = alive && wait(&sh->pv_done, (gt - 1) & 1);
+            tc_fence_after();
+            for (int b = half; b < nob; b += 2)
+              for (int c = 0; c < x.pairs; c += 32) {
+                const uint32_t col = tmem + lane_off + 128u + (uint32_t)(b * a.nr + c);
+                uint32_t ov[32];
+                tmem_ld32(col, ov);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                  const float4 f = *reinterpret_cast<const float4*>(&sh->alpha[c + e]);  // of no pair: of no matter
+                  ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f.x);
+                  ov[e + 1] = __float_as_uint(__uint_as_float(ov[e + 1]) * f.y);
+                  ov[e + 2] = __float_as_uint(__uint_as_float(ov[e + 2]) * f.z);
+                  ov[e + 3] = __float_as_uint(__uint_as_float(ov[e + 3]) * f.w);
+                }
+                tmem_st32(col, ov);
+              }
+            tmem_wait_st();
+          }
+          softmax_sync();  // maxima and factors are read
+        }
+        if (active) {
           const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
           float ps[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -468,36 +515,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             fadd2(ps[2 * (c & 1)], ps[2 * (c & 1) + 1], x0, x1);
             sv[c] = pack2<T>(x0, x1);
           }
-          l_run = l_run * alpha + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
+          l_run += (ps[0] + ps[1]) + (ps[2] + ps[3]);
         }
-        if (half == 0) sh->alpha[m] = alpha;
-        const bool scale = softmax_any(alpha != 1.f);
-        // The product of the tile before is complete: P may be overwritten, O rescaled.
+        // The product of the tile before is complete: P may be overwritten.
         if (i > 0) alive = alive && wait(&sh->pv_done, (gt - 1) & 1);
-        if (scale) {
-          if (i > 0) {
-            tc_fence_after();
-            for (int b = half; b < nob; b += 2)
-              for (int c = 0; c < x.pairs; c += 32) {
-                const uint32_t col = tmem + lane_off + 128u + (uint32_t)(b * a.nr + c);
-                uint32_t ov[32];
-                tmem_ld32(col, ov);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                  const float4 f = *reinterpret_cast<const float4*>(&sh->alpha[c + e]);
-                  ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f.x);
-                  ov[e + 1] = __float_as_uint(__uint_as_float(ov[e + 1]) * f.y);
-                  ov[e + 2] = __float_as_uint(__uint_as_float(ov[e + 2]) * f.z);
-                  ov[e + 3] = __float_as_uint(__uint_as_float(ov[e + 3]) * f.w);
-                }
-                tmem_st32(col, ov);
-              }
-            tmem_wait_st();
-          }
-          softmax_sync();  // the factors are read
-        }
-        if (active) {
+        if (active && !(narrow && lane >= 16)) {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
             *reinterpret_cast<uint4*>(sP + m * 128 + (((4 * half + c) ^ (m & 7)) * 16)) =
@@ -505,8 +527,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // ---- values that must not meet a weight of 0
         if (j0 + kTile > n || (x.rows > 1 && j0 + kTile > x.past)) {
-          const int st = gt % L.stages;
-          for (int j = 0; j < vgroups; ++j) alive = alive && wait(&sh->full[st][j], (gt / L.stages) & 1);
+          const int st = ring.stage;
+          for (int j = 0; j < vgroups; ++j) alive = alive && wait(&sh->full[st][j], ring.turn);
           const int key = me >> 2, part = me & 3;  // four threads a key
           const int chunks = L.nvb * 8;            // its 16-byte chunks, in an order that spreads the threads over the banks
           auto chunk = [&](int c) {
@@ -542,17 +564,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- output: a lane holds a channel of each 128, its pairs in the columns
       alive = alive && wait(&sh->pv_done, (gt - 1) & 1);
       tc_fence_after();
-      sh->sum[half][m] = l_run;
+      if (row_ok) sh->sum[half][m] = l_run;
       if (softmax_any(!alive)) break;
-      if (half == 0) {
+      if (half == 0 && row_ok) {
         const float l = l_run + sh->sum[1][m];
         sh->inv[m] = l == 0.f ? 0.f : 1.f / l;  // a NaN stays
-        if (!x.whole && row_ok) *reinterpret_cast<float2*>(a.part_ml + ((long long)x.part * a.nr + m) * 2) = make_float2(m_run, l);
+        if (!x.whole) *reinterpret_cast<float2*>(a.part_ml + ((long long)x.part * a.nr + m) * 2) = make_float2(m_run, l);
       }
       softmax_sync();
       if (x.whole) {
         for (int b = half; b < nob; b += 2) {
-          T* out = static_cast<T*>(a.out) + ((long long)x.row0 * a.hq + x.first) * a.dv + b * 128 + m;
+          T* out = static_cast<T*>(a.out) + ((long long)x.row0 * a.hq + x.first) * a.dv + b * 128 + quarter * 32 + lane;
           for (int c = 0; c < x.pairs; c += 32) {
             uint32_t ov[32];
             tmem_ld32(tmem + lane_off + 128u + (uint32_t)(b * a.nr + c), ov);
@@ -567,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         for (int b = half; b < nob; b += 2) {
-          float* part = a.part_o + (long long)x.part * a.nr * a.dv + b * 128 + m;
+          float* part = a.part_o + (long long)x.part * a.nr * a.dv + b * 128 + quarter * 32 + lane;
           for (int c = 0; c < x.pairs; c += 32) {
             uint32_t ov[32];
             tmem_ld32(tmem + lane_off + 128u + (uint32_t)(b * a.nr + c), ov);

@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
         }
       }
     };
-    for (int k = 0; ok && take(k, x); ++k) {
+    for (int k = 0; ok && uniform(take(k, x)); ++k) {
       const int ntiles = uniform(x.ntiles);
       if (ntiles == 0) continue;
       const bool q1 = uniform(x.t0 + wk.tok_tile < x.rows) != 0;
