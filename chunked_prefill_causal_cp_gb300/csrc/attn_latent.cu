@@ -2,29 +2,30 @@
 // tensor cores (TMA, tcgen05, TMEM), split along the keys.
 //
 // A position's row of up to 512 + 64 channels is the key and, without its last
-// channels, the value of every head: it is read once for a tile of (row, head)
+// channels, the value of every head: it is read once for a tile of 64 (row, head)
 // pairs, and the path is bound by the cache's bytes until the pairs are many.  64 keys
 // are 72 KB, of which shared memory holds two beside 64 pairs' queries, and an output of
 // 512 channels leaves TMEM room for 64 pairs only if the channels lie over its lanes.
 // Hence
-//   S[pairs x 64 keys] = Q K^T     A = Q, B = K, both K-major: a pair's scores are a
-//                                  TMEM lane, two threads' with 32 keys each.  Up to 64
-//                                  pairs are an M of 64, whose rows lie in the lower 16
-//                                  lanes of each quarter of TMEM
+//   S[64 pairs x 64 keys] = Q K^T  A = Q, B = K, both K-major, an M of 64, whose rows lie
+//                                  in the lower 16 lanes of each quarter of TMEM
 //   P -> shared memory             [pair][64 keys] in 16 bits, one swizzled 128-byte row
 //   O^T[128 channels x pairs] += V^T P^T   A = V as it lies (MN-major), B = P (K-major),
 //                                  a block of TMEM columns for each 128 channels
-// A raised maximum scales a column of O^T, which all lanes hold: the threads vote each
-// tile (a barrier that ORs), and only when some score passes its pair's maximum by more
-// than 2^8 do they exchange maxima, leave the factors in shared memory and pass over O.
+// An MMA takes as long as its operands take out of shared memory (128 bytes a clock: 32
+// clocks of the first kind, 48 of the second with 64 pairs), 1920 clocks a tile of 512 +
+// 64 channels, beside 576 for the copies into it.
+// Four threads share a pair's scores of a tile, 16 keys each.  A raised maximum scales a
+// column of O^T, which all lanes hold: the threads vote each tile (a barrier that ORs),
+// and only when some score passes its pair's maximum by more than 2^8 do they exchange
+// maxima, leave the factors in shared memory and pass over O.
 //
 // One persistent CTA an SM, 384 threads: warp 0 TMA producer, warp 1 TMEM and MMA issue,
 // warp 2 scheduling (finds the CTA's items, two ahead), warps 4-11 softmax and output.
-// A stage's blocks of 64 channels land, and are given back, in up to three groups -- 256
-// channels, the next 256, the rotated part -- so that scores begin with the first group,
-// the rotated part is refilled while the softmax runs, and the first values while the
-// others are still multiplied: with two stages the way of a tile through load, scores,
-// softmax and output is what the kernel waits for, not any one of them.
+// A stage's blocks of 64 channels land, and are given back, in two groups -- the first
+// 256 channels and the rotated part, and the next 256 -- so that with only two stages
+// the first half of a tile's scores fills the wait for the softmax of the one before, and
+// the first half of its values is refilled while the second is still multiplied.
 //
 // What a row does not see: its scores become -inf by a 64-bit mask of the tile's
 // columns (a tree's row: its ancestors, 128 bits found by walking the parents once).
@@ -55,7 +56,8 @@ constexpr int kThreads = 384;
 constexpr int kTile = 64;                 // keys of a tile
 constexpr uint32_t kBlock = kTile * 128;  // bytes of 64 keys x 64 channels
 constexpr int kMaxStages = 6;
-constexpr int kGroups = 3;                // of a stage's blocks, at most
+constexpr int kPairs = 64;                // (row, head) pairs of a tile
+constexpr int kGroups = 2;                // of a stage's blocks, at most
 constexpr uint32_t kSmem = 232448;        // of a CTA, at most
 constexpr float kRescaleLog2 = 8.0f;
 
@@ -80,12 +82,12 @@ struct __align__(16) Shared {
   union __align__(16) {
     int parent[CP_TREE_MAX];  // before an item's walk
     struct {                  // during it
-      float alpha[128];       // the factor of a pair's column for its raised maximum
-      float top[2][128];      // maximum of a pair's 32 scores of this tile, by half
+      float alpha[kPairs];    // the factor of a pair's column for its raised maximum
+      float top[4][kPairs];   // maximum of a pair's 16 scores of this tile, by part
     };
     struct {                  // after it
-      float inv[128];         // 1 / sum of a pair
-      float sum[2][128];      // of a pair's weights, by half
+      float inv[kPairs];      // 1 / sum of a pair
+      float sum[4][kPairs];   // of a pair's weights, by part
     };
   };
 };
@@ -98,16 +100,16 @@ struct Layout {
   int ngroups, stages;
 };
 
-Layout layout_of(int dqk, int dv, int nr) {
+Layout layout_of(int dqk, int dv) {
   Layout l;
   l.nqb = (dqk + 63) / 64;
   l.nvb = dv / 64;
-  l.ngroups = (l.nvb + 3) / 4 + (l.nqb > l.nvb);
+  l.ngroups = (l.nvb + 3) / 4;
   l.stage_bytes = (uint32_t)l.nqb * kBlock;
-  const uint32_t q = (uint32_t)l.nqb * nr * 128, fixed = q + nr * 128 + (uint32_t)sizeof(Shared);
+  const uint32_t q = (uint32_t)l.nqb * kPairs * 128, fixed = q + kPairs * 128 + (uint32_t)sizeof(Shared);
   l.stages = std::min<int>((kSmem - fixed) / l.stage_bytes, kMaxStages);
   l.p_off = q + l.stages * l.stage_bytes;
-  l.ctl_off = l.p_off + nr * 128;
+  l.ctl_off = l.p_off + kPairs * 128;
   l.alloc = l.ctl_off + (uint32_t)sizeof(Shared);
   return l;
 }
@@ -123,7 +125,7 @@ struct Work : RowsAttnArgs {
     row0 = seq_row0(rows, s);
     return p >= 0 && (long long)p + r <= max_ctx && row0 >= 0 && row0 <= total_rows - r && !(parents && r > CP_TREE_MAX);
   }
-  __device__ __forceinline__ int tiles(int r) const { return (r * hq - 1) / nr + 1; }
+  __device__ __forceinline__ int tiles(int r) const { return (r * hq - 1) / kPairs + 1; }
   __device__ __forceinline__ long long weight(int s, bool report) const {
     int r, p, row0;
     if (!bounds(s, r, p, row0)) {
@@ -138,8 +140,8 @@ struct Work : RowsAttnArgs {
     const int n = x.past + x.rows, nt = tiles(x.rows), splits = rows_splits(n, nt), keys = rows_split_keys(n, splits);
     const int split = (int)idx / nt;
     x.s = s;
-    x.first = (int)(idx - (long long)split * nt) * nr;
-    x.pairs = min(nr, x.rows * hq - x.first);
+    x.first = (int)(idx - (long long)split * nt) * kPairs;
+    x.pairs = min(kPairs, x.rows * hq - x.first);
     x.j_begin = split * keys;
     const int seen = x.past + (x.first + x.pairs - 1) / hq + 1;  // by the tile's last row
     x.j_end = (int)min((long long)seen, (long long)x.j_begin + keys);
@@ -183,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const Work a, const Layout L) {
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* sStage = smem + (uint32_t)L.nqb * a.nr * 128;
+  uint8_t* sStage = smem + (uint32_t)L.nqb * kPairs * 128;
   uint8_t* sP = smem + L.p_off;
   Shared* sh = reinterpret_cast<Shared*>(smem + L.ctl_off);
 
@@ -230,10 +232,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) mbar_arrive(&sh->item_empty[k & 1]);
     return x.ntiles >= 0;
   };
-  // A group's blocks: values four at a time, then the rotated part.
-  const int vgroups = (L.nvb + 3) / 4;
-  auto group_first = [&](int j) { return j < vgroups ? 4 * j : L.nvb; };
-  auto group_end = [&](int j) { return j < vgroups ? min(4 * j + 4, L.nvb) : L.nqb; };
+  // A group's blocks: values four at a time; the first group also has the rotated part, behind them all.
+  auto group_blocks = [&](int j) { return min(4, L.nvb - 4 * j) + (j == 0 ? L.nqb - L.nvb : 0); };
+  auto block_of = [&](int j, int e) { return j == 0 && e >= min(4, L.nvb) ? L.nvb : 4 * j + e; };
   pdl_wait();  // everything below reads what earlier kernels wrote
 
   if (warp == 2) {
@@ -269,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       if (lane == 0) {
         mbar_arrive_expect_tx(&sh->q_full, L.nqb * a.q_rows * 128);
-        for (int b = 0; b < L.nqb; ++b) tma_load_3d(smem + b * a.nr * 128, &tm_q, &sh->q_full, b * 64, x.row0 * a.hq + x.first, 0);
+        for (int b = 0; b < L.nqb; ++b) tma_load_3d(smem + b * kPairs * 128, &tm_q, &sh->q_full, b * 64, x.row0 * a.hq + x.first, 0);
       }
       __syncwarp();
       queries = k + 1;
@@ -288,17 +289,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           off = key & (a.cache.page_size - 1);
         }
-        for (int e = 0; e < L.ngroups; ++e) {
-          const int j = e == 0 ? L.ngroups - 1 : e - 1;  // the last group is free first
+        for (int j = 0; ok && j < L.ngroups; ++j) {
           if (gt >= L.stages) ok = wait(&sh->empty[st][j], ring.turn ^ 1);
           if (!ok) break;
-          const int b0 = group_first(j), nb = group_end(j) - b0;
+          const int nb = group_blocks(j);
           begun |= 1u << (kGroups * st + j);
           phase ^= 1u << (kGroups * st + j);
           if (lane == 0) mbar_arrive_expect_tx(&sh->full[st][j], nb * kBlock);
           __syncwarp();
           for (int idx = lane; idx < npg * nb; idx += 32) {  // npg divides 32: the page stays the lane's
-            const int b = b0 + idx / npg;
+            const int b = block_of(j, idx / npg);
             tma_load_3d(sStage + st * L.stage_bytes + b * kBlock + (idx % npg) * ps * 128, &tm_k, &sh->full[st][j], b * 64, off,
                         plane);
           }
@@ -312,94 +312,106 @@ __global__ void __launch_bounds__(kThreads, 1)
       if ((begun >> i) & 1) mbar_wait(&sh->full[i / kGroups][i % kGroups], ((phase >> i) & 1) ^ 1, &zero, a.status);
     __syncwarp();
   } else if (warp == 1) {
-    // ================================================================ MMA issuer
-    // What the addresses of an MMA come from is broadcast, so that the compiler keeps it in uniform registers and the
-    // MMAs issue back to back.
-    auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
-    auto test = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test(b, parity)) != 0; };
-    const uint64_t q_desc = make_sdesc_sw128(smem_u32(smem), 16, 1024);
-    const uint64_t k_desc = make_sdesc_sw128(smem_u32(sStage), 16, 1024);
-    const uint64_t v_desc = make_sdesc_sw128(smem_u32(sStage), kBlock, 1024);
-    const uint64_t p_desc = make_sdesc_sw128(smem_u32(sP), 16, 1024);
-    const uint32_t q_step = (uint32_t)a.nr * 8;  // of a descriptor: 16 bytes
-    const uint32_t tm = (uint32_t)uniform((int)tmem);
-    const uint32_t stage_step = L.stage_bytes >> 4;
-    Ring qk, pv;             // of the tile whose scores, whose output is issued next
-    uint32_t tiles = 0;      // scores issued so far
-    uint32_t p_phase = 0;    // parity of the next P
-    bool ok = true;
-    Item x;
-    for (int k = 0; ok && uniform(take(k, x)); ++k) {
-      const int ntiles = uniform(x.ntiles);
-      const uint32_t idesc_qk = make_idesc_f16(kBf16, uniform(x.pairs) <= 64 ? 64 : 128, kTile, false);
-      const uint32_t idesc_pv = make_idesc_f16(kBf16, 128, (uniform(x.pairs) + 15) & ~15, false) | (1u << 15);  // A MN-major
-      ok = wait(&sh->q_full, k & 1);
-      int next = 0, part = 0;  // tile, and group in order of arrival, whose scores are issued next
-      for (int i = 0; ok && i < ntiles; ++i) {
-        uint64_t t0 = 0;
-        for (uint32_t it = 1;; ++it) {
-          if (next > i && test(&sh->p_ready, p_phase)) break;  // first: it gives stages back
-          const int j = part == 0 ? L.ngroups - 1 : part - 1;
-          if (next < ntiles && next <= i + 1 && test(&sh->full[qk.stage][j], qk.turn)) {
-            tc_fence_after();
-            const uint32_t d = tm + 64u * (tiles & 1);
-            const int b0 = group_first(j), b1 = group_end(j);
-            uint32_t q = (uint32_t)q_desc + b0 * q_step, kd = (uint32_t)k_desc + qk.stage * stage_step + b0 * (kBlock >> 4);
-            for (int b = b0; b < b1; ++b, q += q_step, kd += kBlock >> 4)
+    // ================================================================ MMA issuer: one thread
+    if (lane == 0) {
+      auto wait1 = [&](uint64_t* b, uint32_t parity) { return mbar_wait(b, parity, abort_flag, a.status); };
+      constexpr uint32_t kQStep = kPairs * 8, kKStep = kBlock >> 4;  // of a descriptor: 16 bytes
+      constexpr uint32_t kIdescQK = make_idesc_f16(kBf16, 64, kTile, false);
+      const uint64_t q_desc = make_sdesc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t v_desc = make_sdesc_sw128(smem_u32(sStage), kBlock, 1024);
+      const uint32_t q_lo = (uint32_t)q_desc, k_hi = (uint32_t)(q_desc >> 32);  // Q, K and P differ in their addresses only
+      const uint32_t k_lo = (uint32_t)make_sdesc_sw128(smem_u32(sStage), 16, 1024);
+      const uint32_t p_lo = (uint32_t)make_sdesc_sw128(smem_u32(sP), 16, 1024);
+      const uint32_t v_lo = (uint32_t)v_desc, v_hi = (uint32_t)(v_desc >> 32), stage_step = L.stage_bytes >> 4;
+      const int nvb = L.nvb;
+      const bool rotated = L.nqb > nvb;
+      // Scores over the kN blocks from Q at q, K at kd on; `acc`: added to what is there.
+      auto scores = [&](auto kN, uint32_t d, uint32_t q, uint32_t kd, uint32_t acc) {
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_ss_lo(d, q + 2 * kk, (uint32_t)(q_desc >> 32), kd + 2 * kk, (uint32_t)(k_desc >> 32), idesc_qk,
-                          part | (b - b0) | kk);
-            if (++part == L.ngroups) {
-              mma_commit_elect(&sh->s_full[tiles & 1]);
-              if (vgroups < L.ngroups) mma_commit_elect(&sh->empty[qk.stage][L.ngroups - 1]);  // the rotated part is read
-              part = 0;
-              ++tiles;
-              qk.advance(L.stages);
-              if (++next == ntiles) mma_commit_elect(&sh->q_empty);
-            }
-            continue;
-          }
-          if ((it & 63u) == 0) {
-            int stop = 0;
-            if (lane == 0) {
-              stop = *abort_flag;
-              if (t0 == 0) t0 = global_timer_ns();
-              if (!stop && global_timer_ns() - t0 > kWaitLimitNs) {
-                *abort_flag = stop = 1;
-                if (a.status) atomicOr(a.status, CP_DEV_TIMEOUT);
-              }
-            }
-            if (uniform(stop)) {
-              ok = false;
-              break;
-            }
-          }
-        }
-        if (ok && i == 0 && k > 0) ok = wait(&sh->o_free, (k - 1) & 1);  // the item before has left O
-        if (!ok) break;
-        p_phase ^= 1u;
+        for (int e = 0; e < decltype(kN)::value * 4; ++e)
+          mma_ss_lo(d, q + (e >> 2) * kQStep + 2 * (e & 3), k_hi, kd + (e >> 2) * kKStep + 2 * (e & 3), k_hi, kIdescQK,
+                    e ? 1u : acc);
+      };
+      // Output of kN x 128 channels from V at vd on into the columns at d.
+      auto output = [&](auto kN, uint32_t d, uint32_t vd, uint32_t idesc, uint32_t acc) {
+#pragma unroll
+        for (int e = 0; e < decltype(kN)::value * 4; ++e)
+          mma_ss_lo(d + (e >> 2) * kPairs, vd + (e >> 2) * (2 * kKStep) + 128 * (e & 3), v_hi, p_lo + 2 * (e & 3), k_hi, idesc,
+                    e & 3 ? 1u : acc);
+      };
+      using One = std::integral_constant<int, 1>;
+      using Two = std::integral_constant<int, 2>;
+      using Four = std::integral_constant<int, 4>;
+      Ring qk, pv;           // of the tile whose scores, whose output is issued next
+      uint32_t s_buf = 0;    // S of the next scores
+      uint32_t p_phase = 0;  // parity of the next P
+      bool ok = true;
+      // Group j of the next tile's scores.
+      auto group = [&](int j) {
+        if (!wait1(&sh->full[qk.stage][j], qk.turn)) return false;
         tc_fence_after();
-        uint32_t vd = (uint32_t)v_desc + pv.stage * stage_step, d = tm + 128u;
-        for (int b = 0; b < L.nvb; b += 2, vd += kBlock >> 3, d += a.nr) {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_ss_lo(d, vd + 128 * kk, (uint32_t)(v_desc >> 32), (uint32_t)p_desc + 2 * kk, (uint32_t)(p_desc >> 32), idesc_pv,
-                      i | kk);
-          if ((b & 2) || b + 2 >= L.nvb) mma_commit_elect(&sh->empty[pv.stage][b >> 2]);
+        const uint32_t d = tmem + 64u * s_buf, kd = k_lo + qk.stage * stage_step;
+        if (j == 0) {
+          if (nvb >= 4) scores(Four(), d, q_lo, kd, 0);
+          else scores(Two(), d, q_lo, kd, 0);
+          if (rotated) scores(One(), d, q_lo + nvb * kQStep, kd + nvb * kKStep, 1);
+        } else if (nvb == 8) {
+          scores(Four(), d, q_lo + 4 * kQStep, kd + 4 * kKStep, 1);
+        } else {
+          scores(Two(), d, q_lo + 4 * kQStep, kd + 4 * kKStep, 1);
         }
-        mma_commit_elect(&sh->pv_done);
-        pv.advance(L.stages);
+        if (j + 1 == L.ngroups) {
+          mma_commit(&sh->s_full[s_buf]);
+          s_buf ^= 1u;
+          qk.advance(L.stages);
+        }
+        return true;
+      };
+      // With two stages the second group comes after the output that gave it room.
+      const int early = L.stages > 2 ? L.ngroups : 1;
+      for (int k = 0; ok; ++k) {
+        if (!wait1(&sh->item_full[k & 1], (k >> 1) & 1)) break;
+        const int ntiles = sh->item[k & 1].ntiles;
+        const uint32_t idesc_pv = make_idesc_f16(kBf16, 128, (sh->item[k & 1].pairs + 15) & ~15, false) | (1u << 15);  // A MN-major
+        mbar_arrive(&sh->item_empty[k & 1]);
+        if (ntiles < 0) break;
+        ok = wait1(&sh->q_full, k & 1);
+        for (int j = 0; ok && j < L.ngroups; ++j) ok = group(j);
+        if (ntiles == 1) mma_commit(&sh->q_empty);
+        for (int i = 0; ok && i < ntiles; ++i) {
+          const bool more = i + 1 < ntiles;
+          for (int j = 0; ok && more && j < early; ++j) ok = group(j);
+          ok = ok && wait1(&sh->p_ready, p_phase);
+          if (ok && i == 0 && k > 0) ok = wait1(&sh->o_free, (k - 1) & 1);  // the item before has left O
+          if (!ok) break;
+          p_phase ^= 1u;
+          tc_fence_after();
+          const uint32_t vd = v_lo + pv.stage * stage_step, d = tmem + 128u, acc = i > 0;
+          if (nvb >= 4) output(Two(), d, vd, idesc_pv, acc);
+          else output(One(), d, vd, idesc_pv, acc);
+          mma_commit(&sh->empty[pv.stage][0]);
+          if (nvb > 4) {
+            if (nvb == 8) output(Two(), d + 2 * kPairs, vd + 4 * kKStep, idesc_pv, acc);
+            else output(One(), d + 2 * kPairs, vd + 4 * kKStep, idesc_pv, acc);
+            mma_commit(&sh->empty[pv.stage][1]);
+          }
+          mma_commit(&sh->pv_done);
+          pv.advance(L.stages);
+          for (int j = early; ok && more && j < L.ngroups; ++j) ok = group(j);
+          if (i + 2 == ntiles) mma_commit(&sh->q_empty);  // the item's last scores are issued
+        }
       }
+      mma_commit(&sh->all_done);
+      volatile int zero = 0;  // wait even after an abort: MMAs may still be in flight
+      mbar_wait(&sh->all_done, 0, &zero, a.status);
     }
-    mma_commit_elect(&sh->all_done);
-    volatile int zero = 0;  // wait even after an abort: MMAs may still be in flight
-    mbar_wait(&sh->all_done, 0, &zero, a.status);
     __syncwarp();
   } else {
     // ================================================================ softmax, output
     const int half = (warp - 4) >> 2, quarter = warp & 3;
     const int me = half * 128 + quarter * 32 + lane;
+    // This thread's pair of a tile, with keys [16 part, + 16) of each 64.
+    const int m = quarter * 16 + (lane & 15), part = 2 * half + (lane >> 4);
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const int nob = L.nvb / 2;
     int gt = 0;
@@ -411,10 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool alive = take(k, x);
       if (softmax_any(!alive)) break;
       const int n = x.past + x.rows;  // positions written, this call's rows among them
-      // This thread's pair of the tile, with keys [32 half, + 32) of each 64.
-      const bool narrow = x.pairs <= 64;  // an M of 64
-      const int m = narrow ? quarter * 16 + (lane & 15) : quarter * 32 + lane;
-      const bool row_ok = m < x.pairs && !(narrow && lane >= 16), active = quarter * (narrow ? 16 : 32) < x.pairs;
+      const bool row_ok = m < x.pairs, active = quarter * 16 < x.pairs;
       const int tok = (x.first + m) / a.hq;
       uint64_t see_lo = 0, see_hi = 0;  // a tree's row: the call's rows that it sees
       if (a.parents) {
@@ -438,46 +447,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int j0 = x.j_begin + i * kTile;
         alive = alive && wait(&sh->s_full[gt & 1], (gt >> 1) & 1);
         tc_fence_after();
-        uint32_t sv[32];
+        uint32_t sv[16];
         uint64_t vis = 0;
         float mx = -INFINITY;
         if (active) {
-          tmem_ld32(tmem + lane_off + 64u * (gt & 1) + 32u * half, sv);
+          tmem_ld16x2<16>(tmem + lane_off + 64u * (gt & 1) + 32u * half, sv);
           tmem_wait_ld();
-          if (row_ok) {
-            const int c = x.past - j0 + (a.parents ? 0 : tok + 1);  // columns [0, c) are seen
-            vis = c >= 64 ? ~0ull : c > 0 ? (1ull << c) - 1 : 0;
-            if (a.parents && c < 64) vis |= bits_from(see_lo, see_hi, -c);
-          }
-          if (vis != ~0ull) {
-            const uint32_t v = (uint32_t)(vis >> (32 * half));
+          const int c = x.past - j0 + (a.parents ? 0 : tok + 1);  // columns [0, c) are seen
+          vis = c >= 64 || !row_ok ? ~0ull : c > 0 ? (1ull << c) - 1 : 0;
+          if (a.parents && c < 64) vis |= bits_from(see_lo, see_hi, -c);
+          const uint32_t v = (uint32_t)(vis >> (16 * part)) & 0xffffu;
+          if (v != 0xffffu) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (!((v >> c) & 1)) sv[c] = __float_as_uint(-INFINITY);
+            for (int e = 0; e < 16; ++e)
+              if (!((v >> e) & 1)) sv[e] = __float_as_uint(-INFINITY);
           }
           float m4[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < 32; c += 4) {
-            m4[0] = fmax3(m4[0], __uint_as_float(sv[c + 0]), __uint_as_float(sv[c + 1]));
-            m4[1] = fmax3(m4[1], __uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3]));
+          for (int e = 0; e < 16; e += 4) {
+            m4[0] = fmax3(m4[0], __uint_as_float(sv[e + 0]), __uint_as_float(sv[e + 1]));
+            m4[1] = fmax3(m4[1], __uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3]));
           }
           mx = fmaxf(m4[0], m4[1]);
         }
         mx *= a.scale_log2;  // scale > 0: it commutes
         const bool raise = softmax_any(row_ok && (mx > m_run + kRescaleLog2 || (m_run == -INFINITY && mx != -INFINITY)));
         if (raise) {
-          // The two halves of a pair agree on its maximum; what is smaller than the threshold stays.
-          if (row_ok) sh->top[half][m] = mx;
+          // A pair's four threads agree on its maximum; one that no score passes by the threshold stays.
+          if (row_ok) sh->top[part][m] = mx;
           softmax_sync();
           float alpha = 1.f;
           if (row_ok) {
-            mx = fmaxf(mx, sh->top[half ^ 1][m]);
+            mx = fmaxf(fmaxf(sh->top[0][m], sh->top[1][m]), fmaxf(sh->top[2][m], sh->top[3][m]));
             if (mx > m_run + kRescaleLog2 || (m_run == -INFINITY && mx != -INFINITY)) {
               if (m_run != -INFINITY) alpha = ex2_approx(m_run - mx);  // else nothing but zeros so far
               m_run = mx;
               l_run *= alpha;
             }
-            if (half == 0) sh->alpha[m] = alpha;
+            if (part == 0) sh->alpha[m] = alpha;
           }
           if (i > 0) {
             softmax_sync();
@@ -485,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             for (int b = half; b < nob; b += 2)
               for (int c = 0; c < x.pairs; c += 32) {
-                const uint32_t col = tmem + lane_off + 128u + (uint32_t)(b * a.nr + c);
+                const uint32_t col = tmem + lane_off + 128u + (uint32_t)(b * kPairs + c);
                 uint32_t ov[32];
                 tmem_ld32(col, ov);
                 tmem_wait_ld();
@@ -507,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
           float ps[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
+          for (int c = 0; c < 8; ++c) {
             float x0 = __uint_as_float(sv[2 * c]), x1 = __uint_as_float(sv[2 * c + 1]);
             ffma2(x0, x1, a.scale_log2, neg_m);
             x0 = ex2_approx(x0);
@@ -519,17 +526,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // The product of the tile before is complete: P may be overwritten.
         if (i > 0) alive = alive && wait(&sh->pv_done, (gt - 1) & 1);
-        if (active && !(narrow && lane >= 16)) {
+        if (active) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            *reinterpret_cast<uint4*>(sP + m * 128 + (((4 * half + c) ^ (m & 7)) * 16)) =
+          for (int c = 0; c < 2; ++c)
+            *reinterpret_cast<uint4*>(sP + m * 128 + (((2 * part + c) ^ (m & 7)) * 16)) =
                 make_uint4(sv[4 * c], sv[4 * c + 1], sv[4 * c + 2], sv[4 * c + 3]);
         }
         // ---- values that must not meet a weight of 0
         if (j0 + kTile > n || (x.rows > 1 && j0 + kTile > x.past)) {
           const int st = ring.stage;
-          for (int j = 0; j < vgroups; ++j) alive = alive && wait(&sh->full[st][j], ring.turn);
-          const int key = me >> 2, part = me & 3;  // four threads a key
+          for (int j = 0; j < L.ngroups; ++j) alive = alive && wait(&sh->full[st][j], ring.turn);
+          const int key = me >> 2, own = me & 3;   // four threads a key
           const int chunks = L.nvb * 8;            // its 16-byte chunks, in an order that spreads the threads over the banks
           auto chunk = [&](int c) {
             const int d = (c + key) & 7;
@@ -538,11 +545,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool gone = j0 + key >= n;
           bool bad = gone;
           if (!bad && x.rows > 1 && j0 + key >= x.past)
-            for (int c = part; c < chunks; c += 4) bad = bad || nonfinite8<T>(*chunk(c));
+            for (int c = own; c < chunks; c += 4) bad = bad || nonfinite8<T>(*chunk(c));
           bad = __shfl_xor_sync(0xffffffffu, bad, 1) || bad;
           bad = __shfl_xor_sync(0xffffffffu, bad, 2) || bad;
           if (bad)
-            for (int c = part; c < chunks; c += 4) *chunk(c) = make_uint4(0, 0, 0, 0);
+            for (int c = own; c < chunks; c += 4) *chunk(c) = make_uint4(0, 0, 0, 0);
           const uint32_t four = __ballot_sync(0xffffffffu, bad && !gone);  // four bits a key
           if (lane == 0) sh->bad[gt & 1][warp - 4] = four;
           softmax_sync();
@@ -564,12 +571,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- output: a lane holds a channel of each 128, its pairs in the columns
       alive = alive && wait(&sh->pv_done, (gt - 1) & 1);
       tc_fence_after();
-      if (row_ok) sh->sum[half][m] = l_run;
+      if (row_ok) sh->sum[part][m] = l_run;
       if (softmax_any(!alive)) break;
-      if (half == 0 && row_ok) {
-        const float l = l_run + sh->sum[1][m];
+      if (part == 0 && row_ok) {
+        const float l = (l_run + sh->sum[1][m]) + (sh->sum[2][m] + sh->sum[3][m]);
         sh->inv[m] = l == 0.f ? 0.f : 1.f / l;  // a NaN stays
-        if (!x.whole) *reinterpret_cast<float2*>(a.part_ml + ((long long)x.part * a.nr + m) * 2) = make_float2(m_run, l);
+        if (!x.whole) *reinterpret_cast<float2*>(a.part_ml + ((long long)x.part * kPairs + m) * 2) = make_float2(m_run, l);
       }
       softmax_sync();
       if (x.whole) {
@@ -577,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           T* out = static_cast<T*>(a.out) + ((long long)x.row0 * a.hq + x.first) * a.dv + b * 128 + quarter * 32 + lane;
           for (int c = 0; c < x.pairs; c += 32) {
             uint32_t ov[32];
-            tmem_ld32(tmem + lane_off + 128u + (uint32_t)(b * a.nr + c), ov);
+            tmem_ld32(tmem + lane_off + 128u + (uint32_t)(b * kPairs + c), ov);
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e, out += a.dv) {
@@ -589,13 +596,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         for (int b = half; b < nob; b += 2) {
-          float* part = a.part_o + (long long)x.part * a.nr * a.dv + b * 128 + quarter * 32 + lane;
+          float* to = a.part_o + (long long)x.part * kPairs * a.dv + b * 128 + quarter * 32 + lane;
           for (int c = 0; c < x.pairs; c += 32) {
             uint32_t ov[32];
-            tmem_ld32(tmem + lane_off + 128u + (uint32_t)(b * a.nr + c), ov);
+            tmem_ld32(tmem + lane_off + 128u + (uint32_t)(b * kPairs + c), ov);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e, part += a.dv) *part = __uint_as_float(ov[e]);  // up to 31 pairs more than there are: room that nobody reads
+            for (int e = 0; e < 32; ++e, to += a.dv) *to = __uint_as_float(ov[e]);  // up to 31 pairs more than there are: room that nobody reads
           }
         }
       }
@@ -659,7 +666,7 @@ __global__ void __launch_bounds__(512) latent_combine_kernel(const Work a, const
   if (s < 0 || !a.bounds(s, r, p, row0)) return;  // the same for all threads
   const int nt = a.tiles(r), splits = rows_splits(p + r, nt), keys = rows_split_keys(p + r, splits);
   if (splits == 1 || base + (long long)nt * splits > a.part_slots) return;
-  const int first = tile * a.nr, pairs = min(a.nr, r * a.hq - first);
+  const int first = tile * kPairs, pairs = min(kPairs, r * a.hq - first);
   const int used = (p + (first + pairs - 1) / a.hq) / keys + 1;  // splits that hold keys of the tile
   const int c4 = a.dv / 4, mine = threadIdx.x / a.dv, slice = threadIdx.x % a.dv / c4, d4 = threadIdx.x % c4;
   const int m = blockIdx.x % groups * per + mine;
@@ -675,7 +682,7 @@ __global__ void __launch_bounds__(512) latent_combine_kernel(const Work a, const
       for (int j = 0; j < kAhead; ++j) {
         const int i = i0 + j * kSlices;
         if (i >= used) break;
-        const long long row = (base + (long long)i * nt + tile) * a.nr + m;
+        const long long row = (base + (long long)i * nt + tile) * kPairs + m;
         ml[j] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + row * 2));
         x[j] = __ldcg(reinterpret_cast<const float4*>(a.part_o + row * a.dv + 4 * d4));
       }
@@ -726,7 +733,7 @@ template <typename T, bool kPaged>
 cudaError_t launch_t(const RowsAttnArgs& args, int dtype, cudaStream_t st) {
   Work a;
   static_cast<RowsAttnArgs&>(a) = args;
-  const Layout l = layout_of(a.dqk, a.dv, a.nr);
+  const Layout l = layout_of(a.dqk, a.dv);
   CUtensorMap tq, tk;
   const CacheView& c = a.cache;
   const uint64_t slots = kPaged ? c.page_size : c.capacity, planes = kPaged ? c.num_pages : a.rows.num_seqs;
@@ -763,13 +770,13 @@ cudaError_t launch_t(const RowsAttnArgs& args, int dtype, cudaStream_t st) {
 RowsPlan rows_plan(int heads, int dv, bool uniform, long long num_seqs, long long total_rows, int max_ctx) {
   RowsPlan p;
   const long long pairs = (uniform ? total_rows / num_seqs : total_rows) * heads;  // of a sequence, at most
-  p.nr = dv > 256 ? 64 : 128;  // what the output's columns of TMEM leave room for
-  p.q_rows = (int)std::min<long long>(p.nr, pairs);
-  p.tiles = uniform ? num_seqs * ((pairs + p.nr - 1) / p.nr) : pairs / p.nr + 1 + num_seqs;
+  p.q_rows = (int)std::min<long long>(kPairs, pairs);
+  p.tiles = uniform ? num_seqs * ((pairs + kPairs - 1) / kPairs) : pairs / kPairs + 1 + num_seqs;
   p.max_splits = rows_max_splits(max_ctx, 1);
   // A sequence's items: its tiles, or, split, no more than kRowsItems.
   p.slots = p.max_splits == 1 ? 0 : std::min(p.tiles * p.max_splits, p.tiles + num_seqs * kRowsItems);
-  p.bytes = (double)p.slots * p.nr * (dv + 2) * sizeof(float);
+  p.part_floats = (double)p.slots * kPairs * dv;
+  p.bytes = (double)p.slots * kPairs * (dv + 2) * sizeof(float);
   return p;
 }
 

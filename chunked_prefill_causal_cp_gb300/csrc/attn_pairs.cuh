@@ -7,8 +7,9 @@
 // sequence and KV head, over a range of its keys; every K/V tile that a CTA loads
 // serves both Q tiles.  One persistent CTA an SM, 384 threads:
 //   warp 0      TMA producer: an item's Q tiles, then for each 128-key tile its K and V
-//               in units of 64 channels (16 KB) through a ring of as many units as fit
-//   warp 1      MMA issue:  S_w = Q_w K^T, O_w += P_w V for Q tile w = 0, 1
+//               in units of 64 channels (16 KB) through a ring of as many units as fit;
+//               a tile's K, and its V, land and are given back as one
+//   warp 1      MMA issue, one thread:  S_w = Q_w K^T, O_w += P_w V for Q tile w = 0, 1
 //   warp 2      scheduling: finds this CTA's items, two ahead of the others
 //   warp 3      fills the control warpgroup, whose registers go to the others
 //   warps 4-7, 8-11  softmax of Q tile 0 and 1, a thread a row
@@ -46,6 +47,7 @@ constexpr int kThreads = 384;
 constexpr int kKeys = 128;                // keys of a tile
 constexpr uint32_t kUnit = 128 * 128;     // bytes of 128 rows x 64 channels
 constexpr int kMaxUnits = 12;
+constexpr int kMaxTiles = 7;              // of the ring, whole or in part
 constexpr uint32_t kSmem = 232448;        // of a CTA, at most
 constexpr float kRescaleLog2 = 8.0f;
 // Register split: compiled at kRegsLaunch a thread (the most 384 threads may have); the
@@ -69,8 +71,8 @@ struct Item {
 };
 
 struct __align__(16) Shared {
-  uint64_t item_full[2], item_empty[2], q_full[2], q_empty, full[kMaxUnits], empty[kMaxUnits], s_full[2], p_ready[2],
-      o_done[2], o_free[2], all_done;
+  uint64_t item_full[2], item_empty[2], q_full[2], q_empty, k_full[kMaxTiles], v_full[kMaxTiles], k_empty[kMaxTiles],
+      v_empty[kMaxTiles], s_full[2], p_ready[2], o_done[2], o_free[2], all_done;
   uint32_t tmem_base;
   int abort;
   Item item[2];
@@ -126,7 +128,10 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr uint32_t kIdescQK = make_idesc_f16(kBf16, 128, kKeys, false);
   constexpr uint32_t kIdescPV = make_idesc_f16(kBf16, 128, NVB * 64, true);
-  constexpr int kRing = L::units;
+  // Tile t's barriers are t mod kTiles: a tile's K is loaded only when units of the tile kTiles - 1 before it are given
+  // back, so no barrier is a phase ahead of those who wait for it.
+  constexpr int kRing = L::units, kTile = NQB + NVB, kTiles = kRing / kTile + 1;
+  static_assert(kTiles <= kMaxTiles, "barriers");
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sRing = smem + L::q_bytes;
   Shared* sh = reinterpret_cast<Shared*>(smem + L::ctl_off);
@@ -145,9 +150,11 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
       mbar_init(&sh->o_free[i], 128);
     }
     mbar_init(&sh->q_empty, 1);
-    for (int i = 0; i < kRing; ++i) {
-      mbar_init(&sh->full[i], 1);
-      mbar_init(&sh->empty[i], 1);
+    for (int i = 0; i < kTiles; ++i) {
+      mbar_init(&sh->k_full[i], 1);
+      mbar_init(&sh->v_full[i], 1);
+      mbar_init(&sh->k_empty[i], 1);
+      mbar_init(&sh->v_empty[i], 1);
     }
     mbar_init(&sh->all_done, 1);
     sh->abort = 0;
@@ -204,7 +211,8 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
     // ================================================================ producer
     const int ps = Work::kPaged ? wk.page_size : kKeys, lps = 31 - __clz(ps);
     const int npg = kKeys / ps;  // boxes of a unit
-    int u = 0;                   // units issued so far
+    int t = 0;                   // tiles issued so far
+    int issued = 0;              // groups: K and V of each tile
     int queries = 0;             // items whose queries were loaded
     uint32_t last_q1 = 0;        // loads of Q tile 1
     bool ok = true;
@@ -237,126 +245,146 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
           }
           off = 0;
         }
-        for (int e = 0; e < NQB + NVB; ++e, ++u) {
-          const int slot = u % kRing;
-          if (u >= kRing) ok = wait(&sh->empty[slot], ((u / kRing) & 1) ^ 1);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&sh->full[slot], kUnit);
+        for (int v = 0; ok && v < 2; ++v) {  // K, V
+          const int n = v ? NVB : NQB, u = t * kTile + (v ? NQB : 0);
+          // The units before them in the ring, the last of which is given back last.
+          const int old = u + n - 1 - kRing;
+          if (old >= 0) {
+            const int to = old / kTile;
+            ok = wait(old % kTile < NQB ? &sh->k_empty[to % kTiles] : &sh->v_empty[to % kTiles], (to / kTiles) & 1);
+            if (!ok) break;
+          }
+          uint64_t* bar = v ? &sh->v_full[t % kTiles] : &sh->k_full[t % kTiles];
+          ++issued;
+          if (lane == 0) mbar_arrive_expect_tx(bar, n * kUnit);
           __syncwarp();
-          uint8_t* dst = sRing + slot * kUnit;
-          const bool v = e >= NQB;
-          if (Work::kExpanded) {
-            if (lane == 0) {
-              if (v) tma_load_3d(dst, &tm.v, &sh->full[slot], (e - NQB) * 64, x.g, x.key0 + j0);
-              else if (e * 64 < wk.dn) tma_load_3d(dst, &tm.k, &sh->full[slot], e * 64, x.g, x.key0 + j0);
-              else tma_load_3d(dst, &tm.kr, &sh->full[slot], 0, x.key0 + j0, 0);
-            }
-          } else if (lane < npg) {
-            tma_load_3d(dst + lane * ps * 128, v ? &tm.v : &tm.k, &sh->full[slot], (v ? e - NQB : e) * 64, off, plane);
+          for (int idx = lane; idx < npg * n; idx += 32) {  // npg divides 32: the page stays the lane's
+            const int e = idx / npg;
+            uint8_t* dst = sRing + (u + e) % kRing * kUnit + (idx % npg) * ps * 128;
+            if (!Work::kExpanded) tma_load_3d(dst, v ? &tm.v : &tm.k, bar, e * 64, off, plane);
+            else if (v) tma_load_3d(dst, &tm.v, bar, e * 64, x.g, x.key0 + j0);
+            else if (e * 64 < wk.dn) tma_load_3d(dst, &tm.k, bar, e * 64, x.g, x.key0 + j0);
+            else tma_load_3d(dst, &tm.kr, bar, 0, x.key0 + j0, 0);
           }
         }
+        if (ok) ++t;
       }
     }
     // Every copy has landed before shared memory is released, also after an abort.
     volatile int zero = 0;
     if (queries > 0) mbar_wait(&sh->q_full[0], (queries - 1) & 1, &zero, wk.status);
     if (last_q1 > 0) mbar_wait(&sh->q_full[1], (last_q1 - 1) & 1, &zero, wk.status);
-    for (int i = max(0, u - kRing); i < u; ++i) mbar_wait(&sh->full[i % kRing], (i / kRing) & 1, &zero, wk.status);
+    for (int i = max(0, issued - 2 * kTiles); i < issued; ++i) {
+      const int of = i / 2;
+      mbar_wait(i & 1 ? &sh->v_full[of % kTiles] : &sh->k_full[of % kTiles], (of / kTiles) & 1, &zero, wk.status);
+    }
     __syncwarp();
   } else {
-    // ================================================================ MMA issuer
-    // The whole warp runs the loop, converged; one elected lane issues.
-    auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
-    const uint64_t q_desc = make_sdesc_sw128(smem_u32(smem), 16, 1024);
-    const uint64_t k_desc = make_sdesc_sw128(smem_u32(sRing), 16, 1024);
-    const uint32_t tm0 = (uint32_t)uniform((int)tmem);
-    int u0 = 0;   // first unit of the tile whose K comes next
-    uint32_t pq = 0, pp = 0, po = 0, begun = 0;  // bit w: parity of the Q tiles and P tiles taken, of the outputs begun; any begun
-    bool ok = true;
-    Item x;
-    auto slot_of = [](int u) { return u % kRing; };
-    auto unit_full = [&](int u) { return wait(&sh->full[slot_of(u)], (u / kRing) & 1); };
-    // S_w = Q_w K^T with K in units u ..; waits for them when `first`.
-    auto issue_qk = [&](int w, int u, bool first) {
-      for (int b = 0; b < NQB; ++b) {
-        if (first) {
-          if (!unit_full(u + b)) return false;
-          tc_fence_after();
+    // ================================================================ MMA issuer: one thread
+    if (lane == 0) {
+      auto wait1 = [&](uint64_t* b, uint32_t parity) { return mbar_wait(b, parity, abort_flag, wk.status); };
+      constexpr uint32_t kStep = kUnit >> 4;  // of a descriptor: 16 bytes
+      const uint64_t q_desc = make_sdesc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t v_desc = make_sdesc_sw128(smem_u32(sRing), kUnit, 1024);
+      const uint32_t q_lo = (uint32_t)q_desc, k_hi = (uint32_t)(q_desc >> 32);  // Q and K differ in their addresses only
+      const uint32_t k_lo = (uint32_t)make_sdesc_sw128(smem_u32(sRing), 16, 1024);
+      const uint32_t v_lo = (uint32_t)v_desc, v_hi = (uint32_t)(v_desc >> 32);
+      auto wrap = [](int slot) { return slot >= kRing ? slot - kRing : slot; };
+      // Of the tile whose K, whose V comes next: its barriers, their parity; the ring's slot of its first unit.
+      int kt = 0, vt = 0, k_slot = 0, v_slot = NQB % kRing;
+      uint32_t k_turn = 0, v_turn = 0;
+      uint32_t pq = 0, pp = 0, po = 0, begun = 0;  // bit w: parity of the Q tiles and P tiles taken, of the outputs begun; any begun
+      bool ok = true;
+      auto scores = [&](int w) {  // S_w = Q_w K^T
+        const uint32_t d = tmem + 256u * w, q = q_lo + (uint32_t)w * (NQB * kStep);
+#pragma unroll
+        for (int b = 0; b < NQB; ++b) {
+          const uint32_t kd = k_lo + (uint32_t)wrap(k_slot + b) * kStep;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) mma_ss_lo(d, q + b * kStep + 2 * kk, k_hi, kd + 2 * kk, k_hi, kIdescQK, b | kk);
         }
-        const uint32_t q = (uint32_t)q_desc + (((uint32_t)(w * NQB + b) * kUnit) >> 4);
-        const uint32_t kd = (uint32_t)k_desc + (((uint32_t)slot_of(u + b) * kUnit) >> 4);
+        mma_commit(&sh->s_full[w]);
+      };
+      auto output = [&](int w, uint32_t acc) {  // O_w += P_w V
+        const uint32_t s = tmem + 256u * w, o = s + 128u;
+        if (NVB == 1 || v_slot + 1 < kRing) {
+          const uint32_t v = v_lo + (uint32_t)v_slot * kStep;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_ss_lo(tm0 + 256u * w, q + 2 * kk, (uint32_t)(q_desc >> 32), kd + 2 * kk, (uint32_t)(k_desc >> 32), kIdescQK,
-                    b | kk);
-      }
-      mma_commit_elect(&sh->s_full[w]);
-      return true;
-    };
-    // O_w += P_w V: V's 64-channel units lie where the ring has them, so their step may be negative.
-    auto issue_pv = [&](int w, int u, bool acc) {
-      const int a = slot_of(u), b = NVB > 1 ? slot_of(u + 1) : a;
-      const uint64_t d = make_sdesc_sw128(smem_u32(sRing), 16, 1024);
-      if (NVB == 1 || b == a + 1) {
-        const uint64_t v = make_sdesc_sw128(smem_u32(sRing) + (uint32_t)a * kUnit, kUnit, 1024);
-#pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          mma_ts_elect(tm0 + 256u * w + 128u, tm0 + 256u * w + kk * 8, v + ((kk * 2048) >> 4), kIdescPV, acc || kk > 0);
-      } else {  // the ring's end lies between them: 64 channels at a time
-        constexpr uint32_t kIdescHalf = make_idesc_f16(kBf16, 128, 64, true);
-        for (int h = 0; h < 2; ++h) {
-          const uint64_t v = d + (((uint32_t)(h ? b : a) * kUnit) >> 4);
+          for (int kk = 0; kk < kKeys / 16; ++kk) mma_ts_lo(o, s + kk * 8, v + 128 * kk, v_hi, kIdescPV, kk ? 1u : acc);
+        } else {  // the ring's end lies between V's units: 64 channels at a time
+          constexpr uint32_t kIdescHalf = make_idesc_f16(kBf16, 128, 64, true);
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma_ts_elect(tm0 + 256u * w + 128u + 64u * h, tm0 + 256u * w + kk * 8, v + ((kk * 2048) >> 4), kIdescHalf,
-                         acc || kk > 0);
+            mma_ts_lo(o, s + kk * 8, v_lo + (uint32_t)v_slot * kStep + 128 * kk, v_hi, kIdescHalf, kk ? 1u : acc);
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk) mma_ts_lo(o + 64u, s + kk * 8, v_lo + 128 * kk, v_hi, kIdescHalf, kk ? 1u : acc);
         }
-      }
-    };
-    for (int k = 0; ok && uniform(take(k, x)); ++k) {
-      const int ntiles = uniform(x.ntiles);
-      if (ntiles == 0) continue;
-      const bool q1 = uniform(x.t0 + wk.tok_tile < x.rows) != 0;
-      const int nw = q1 ? 2 : 1;
-      for (int w = 0; ok && w < nw; ++w) {
-        ok = wait(&sh->q_full[w], (pq >> w) & 1);
-        pq ^= 1u << w;
-        tc_fence_after();
-        ok = ok && issue_qk(w, u0, w == 0);
-      }
-      if (!ok) break;
-      for (int b = 0; b < NQB; ++b) mma_commit_elect(&sh->empty[slot_of(u0 + b)]);
-      if (ntiles == 1) mma_commit_elect(&sh->q_empty);
-      for (int i = 0; ok && i < ntiles; ++i) {
-        const int v0 = u0 + NQB, u1 = v0 + NVB;  // this tile's V, the next tile's K
+      };
+      auto k_done = [&] {
+        mma_commit(&sh->k_empty[kt]);
+        k_slot = wrap(k_slot + kTile);
+        if (++kt == kTiles) {
+          kt = 0;
+          k_turn ^= 1u;
+        }
+      };
+      for (int k = 0; ok; ++k) {
+        if (!wait1(&sh->item_full[k & 1], (k >> 1) & 1)) break;
+        const int ntiles = sh->item[k & 1].ntiles;
+        const int nw = sh->item[k & 1].t0 + wk.tok_tile < sh->item[k & 1].rows ? 2 : 1;
+        mbar_arrive(&sh->item_empty[k & 1]);
+        if (ntiles < 0) break;
+        if (ntiles == 0) continue;
         for (int w = 0; ok && w < nw; ++w) {
-          ok = wait(&sh->p_ready[w], (pp >> w) & 1);
-          pp ^= 1u << w;
-          if (ok && w == 0)
-            for (int b = 0; ok && b < NVB; ++b) ok = unit_full(v0 + b);
-          if (ok && i == 0 && ((begun >> w) & 1)) ok = wait(&sh->o_free[w], ((po >> w) & 1) ^ 1);  // the output before has left TMEM
+          ok = wait1(&sh->q_full[w], (pq >> w) & 1);
+          pq ^= 1u << w;
+          if (ok && w == 0) ok = wait1(&sh->k_full[kt], k_turn);
           if (!ok) break;
           tc_fence_after();
-          issue_pv(w, v0, i > 0);
-          if (i == 0) {
-            po ^= 1u << w;
-            begun |= 1u << w;
-          }
-          if (i + 1 == ntiles) mma_commit_elect(&sh->o_done[w]);
-          if (w == nw - 1)
-            for (int b = 0; b < NVB; ++b) mma_commit_elect(&sh->empty[slot_of(v0 + b)]);
-          if (i + 1 < ntiles) ok = issue_qk(w, u1, w == 0);
+          scores(w);
         }
         if (!ok) break;
-        if (i + 1 < ntiles)
-          for (int b = 0; b < NQB; ++b) mma_commit_elect(&sh->empty[slot_of(u1 + b)]);
-        if (i + 2 == ntiles) mma_commit_elect(&sh->q_empty);  // the last scores of the item are issued
-        u0 = u1;
+        k_done();
+        if (ntiles == 1) mma_commit(&sh->q_empty);
+        for (int i = 0; ok && i < ntiles; ++i) {
+          const bool more = i + 1 < ntiles;
+          for (int w = 0; w < nw; ++w) {
+            ok = wait1(&sh->p_ready[w], (pp >> w) & 1);
+            pp ^= 1u << w;
+            if (ok && w == 0) ok = wait1(&sh->v_full[vt], v_turn);
+            if (ok && i == 0 && ((begun >> w) & 1)) ok = wait1(&sh->o_free[w], ((po >> w) & 1) ^ 1);  // the output before has left TMEM
+            if (!ok) break;
+            tc_fence_after();
+            output(w, i > 0);
+            if (!more) mma_commit(&sh->o_done[w]);
+            if (w == nw - 1) mma_commit(&sh->v_empty[vt]);
+            if (more) {
+              if (w == 0) {
+                ok = wait1(&sh->k_full[kt], k_turn);
+                if (!ok) break;
+                tc_fence_after();
+              }
+              scores(w);
+            }
+            if (i == 0) {
+              po ^= 1u << w;
+              begun |= 1u << w;
+            }
+          }
+          if (!ok) break;
+          v_slot = wrap(v_slot + kTile);
+          if (++vt == kTiles) {
+            vt = 0;
+            v_turn ^= 1u;
+          }
+          if (more) k_done();
+          if (i + 2 == ntiles) mma_commit(&sh->q_empty);  // the item's last scores are issued
+        }
       }
+      mma_commit(&sh->all_done);
+      volatile int zero = 0;  // wait even after an abort: MMAs may still be in flight
+      mbar_wait(&sh->all_done, 0, &zero, wk.status);
     }
-    mma_commit_elect(&sh->all_done);
-    volatile int zero = 0;  // wait even after an abort: MMAs may still be in flight
-    mbar_wait(&sh->all_done, 0, &zero, wk.status);
     __syncwarp();
   }
   } else {
@@ -367,8 +395,8 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
   const int m = quarter * 32 + lane;        // this thread's row of its Q tile
   const uint32_t s_col = tmem + ((uint32_t)(quarter * 32) << 16) + 256u * w, o_col = s_col + 128u;
   const int mtok = m / wk.group, mhead = m % wk.group;
-  int v_unit = NQB;     // first unit of the tile's V
-  int ns = 0, no = 0;   // score tiles, outputs so far
+  int t = 0;            // the CTA's tiles so far
+  int ns = 0, no = 0;   // score tiles, outputs of this Q tile so far
   Item x;
   // After a wait that gave up, an item's walk goes on without waiting, so that its barriers stay whole; its output is not
   // written, and the warps leave together.
@@ -385,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
     const bool row_ok = mtok < wk.tok_tile && tok < x.rows;
     const int n = x.past + x.rows;
     if (w == 1 && !q1) {
-      v_unit += x.ntiles * (NQB + NVB);
+      t += x.ntiles;
       continue;
     }
     uint64_t see_lo = 0, see_hi = 0;  // a tree's row: the call's rows that it sees
@@ -409,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
     }
     const int seen = Work::kExpanded ? x.past + tok + 1 : x.past;  // keys [0, seen) are seen, and in a tree the row's ancestors
     float m_run = -INFINITY, l_run = 0.f;
-    for (int i = 0; i < x.ntiles; ++i, ++ns, v_unit += NQB + NVB) {
+    for (int i = 0; i < x.ntiles; ++i, ++ns, ++t) {
       alive = alive && wait(&sh->s_full[w], ns & 1);
       tc_fence_after();
       uint32_t sv[128];
@@ -477,7 +505,8 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
       }
       if (guard) {
         // ---- values that must not meet a weight of 0: the threads of the item's Q tiles share the tile's keys
-        for (int b = 0; b < NVB; ++b) alive = alive && wait(&sh->full[(v_unit + b) % kRing], ((v_unit + b) / kRing) & 1);
+        alive = alive && wait(&sh->v_full[t % kTiles], (t / kTiles) & 1);
+        const int v_unit = t * kTile + NQB;
         const int per = q1 ? 2 : 1, me = w * 128 + m;   // threads of a key; this one
         const int key = me / per, part = me % per;
         const bool gone = j0 + key >= n;

@@ -64,7 +64,7 @@ int rows_attention(const cp_layer_desc* d, bool latent, int dqk, int dv, float s
   TreePlan tp{};
   if (latent) {
     p = rows_plan(d->num_q_heads, dv, cu_rows == nullptr, num_seqs, total_rows, max_ctx);
-    if ((double)p.tiles * p.max_splits > INT32_MAX || (double)p.tiles * p.nr > INT32_MAX || p.slots > INT32_MAX)
+    if ((double)p.tiles * p.max_splits > INT32_MAX || (double)p.tiles * 64 > INT32_MAX || p.slots > INT32_MAX)
       return CP_ERR_UNSUPPORTED;
   } else {
     tp = tree_plan(d->num_q_heads, d->num_kv_heads, dv, cu_rows == nullptr, num_seqs, total_rows, max_ctx);
@@ -97,11 +97,10 @@ int rows_attention(const cp_layer_desc* d, bool latent, int dqk, int dv, float s
     return launch_result(launch_tree(a, tp, d->dtype, static_cast<cudaStream_t>(stream)));
   }
   a.q_rows = p.q_rows;
-  a.nr = p.nr;
   a.tiles_bound = (int)p.tiles;
   a.max_splits = p.max_splits;
   a.part_slots = (int)p.slots;
-  a.part_ml = a.part_o + p.slots * p.nr * dv;
+  a.part_ml = a.part_o + (long long)p.part_floats;
   return launch_result(launch_rows_attn(a, d->dtype, static_cast<cudaStream_t>(stream)));
 }
 

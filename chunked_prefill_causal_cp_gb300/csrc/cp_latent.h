@@ -90,20 +90,20 @@ struct RowsAttnArgs {
   int* status;
   // A latent cache's (cp_latent_attn):
   int q_rows;              // pairs of a tile that the call can have, at most
-  int nr;                  // pairs a tile has room for: 64 or 128, by the layer alone
   int tiles_bound;         // tiles of the call, at most
   int max_splits;          // of any sequence
   int part_slots;          // parts that the workspace has room for
-  float* part_o;           // [part_slots, nr, dv] unnormalised parts
-  float* part_ml;          // [part_slots, nr, 2] their maximum (log2 domain) and sum
+  float* part_o;           // [part_slots, 64, dv] unnormalised parts
+  float* part_ml;          // [part_slots, 64, 2] their maximum (log2 domain) and sum
 };
 
 // How such a call runs, from its host bounds.
 struct RowsPlan {
-  int nr, q_rows;
+  int q_rows;
   long long tiles;         // at most
   int max_splits;
   long long slots;         // parts, at most
+  double part_floats;      // of their outputs
   double bytes;            // of workspace; in floating point: absurd sizes must not wrap
 };
 // How a call of drafted trees over a K/V cache runs.
