@@ -312,99 +312,100 @@ __global__ void __launch_bounds__(kThreads, 1)
       if ((begun >> i) & 1) mbar_wait(&sh->full[i / kGroups][i % kGroups], ((phase >> i) & 1) ^ 1, &zero, a.status);
     __syncwarp();
   } else if (warp == 1) {
-    // ================================================================ MMA issuer: one thread
-    if (lane == 0) {
-      auto wait1 = [&](uint64_t* b, uint32_t parity) { return mbar_wait(b, parity, abort_flag, a.status); };
-      constexpr uint32_t kQStep = kPairs * 8, kKStep = kBlock >> 4;  // of a descriptor: 16 bytes
-      constexpr uint32_t kIdescQK = make_idesc_f16(kBf16, 64, kTile, false);
-      const uint64_t q_desc = make_sdesc_sw128(smem_u32(smem), 16, 1024);
-      const uint64_t v_desc = make_sdesc_sw128(smem_u32(sStage), kBlock, 1024);
-      const uint32_t q_lo = (uint32_t)q_desc, k_hi = (uint32_t)(q_desc >> 32);  // Q, K and P differ in their addresses only
-      const uint32_t k_lo = (uint32_t)make_sdesc_sw128(smem_u32(sStage), 16, 1024);
-      const uint32_t p_lo = (uint32_t)make_sdesc_sw128(smem_u32(sP), 16, 1024);
-      const uint32_t v_lo = (uint32_t)v_desc, v_hi = (uint32_t)(v_desc >> 32), stage_step = L.stage_bytes >> 4;
-      const int nvb = L.nvb;
-      const bool rotated = L.nqb > nvb;
-      // Scores over the kN blocks from Q at q, K at kd on; `acc`: added to what is there.
-      auto scores = [&](auto kN, uint32_t d, uint32_t q, uint32_t kd, uint32_t acc) {
+    // ================================================================ MMA issuer
+    // The whole warp runs the loop, converged; one elected lane issues.  What addresses come from is broadcast.
+    auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+    const uint32_t tm = (uint32_t)uniform((int)tmem);
+    constexpr uint32_t kQStep = kPairs * 8, kKStep = kBlock >> 4;  // of a descriptor: 16 bytes
+    constexpr uint32_t kIdescQK = make_idesc_f16(kBf16, 64, kTile, false);
+    const uint64_t q_desc = make_sdesc_sw128(smem_u32(smem), 16, 1024);
+    const uint64_t v_desc = make_sdesc_sw128(smem_u32(sStage), kBlock, 1024);
+    const uint32_t q_lo = (uint32_t)q_desc, k_hi = (uint32_t)(q_desc >> 32);  // Q, K and P differ in their addresses only
+    const uint32_t k_lo = (uint32_t)make_sdesc_sw128(smem_u32(sStage), 16, 1024);
+    const uint32_t p_lo = (uint32_t)make_sdesc_sw128(smem_u32(sP), 16, 1024);
+    const uint32_t v_lo = (uint32_t)v_desc, v_hi = (uint32_t)(v_desc >> 32), stage_step = L.stage_bytes >> 4;
+    const int nvb = L.nvb;
+    const bool rotated = L.nqb > nvb;
+    // Scores over the kN blocks from Q at q, K at kd on; `acc`: added to what is there.
+    auto scores = [&](auto kN, uint32_t d, uint32_t q, uint32_t kd, uint32_t acc) {
 #pragma unroll
-        for (int e = 0; e < decltype(kN)::value * 4; ++e)
-          mma_ss_lo(d, q + (e >> 2) * kQStep + 2 * (e & 3), k_hi, kd + (e >> 2) * kKStep + 2 * (e & 3), k_hi, kIdescQK,
-                    e ? 1u : acc);
-      };
-      // Output of kN x 128 channels from V at vd on into the columns at d.
-      auto output = [&](auto kN, uint32_t d, uint32_t vd, uint32_t idesc, uint32_t acc) {
+      for (int e = 0; e < decltype(kN)::value * 4; ++e)
+        mma_ss_lo(d, q + (e >> 2) * kQStep + 2 * (e & 3), k_hi, kd + (e >> 2) * kKStep + 2 * (e & 3), k_hi, kIdescQK,
+                  e ? 1u : acc);
+    };
+    // Output of kN x 128 channels from V at vd on into the columns at d.
+    auto output = [&](auto kN, uint32_t d, uint32_t vd, uint32_t idesc, uint32_t acc) {
 #pragma unroll
-        for (int e = 0; e < decltype(kN)::value * 4; ++e)
-          mma_ss_lo(d + (e >> 2) * kPairs, vd + (e >> 2) * (2 * kKStep) + 128 * (e & 3), v_hi, p_lo + 2 * (e & 3), k_hi, idesc,
-                    e & 3 ? 1u : acc);
-      };
-      using One = std::integral_constant<int, 1>;
-      using Two = std::integral_constant<int, 2>;
-      using Four = std::integral_constant<int, 4>;
-      Ring qk, pv;           // of the tile whose scores, whose output is issued next
-      uint32_t s_buf = 0;    // S of the next scores
-      uint32_t p_phase = 0;  // parity of the next P
-      bool ok = true;
-      // Group j of the next tile's scores.
-      auto group = [&](int j) {
-        if (!wait1(&sh->full[qk.stage][j], qk.turn)) return false;
-        tc_fence_after();
-        const uint32_t d = tmem + 64u * s_buf, kd = k_lo + qk.stage * stage_step;
-        if (j == 0) {
-          if (nvb >= 4) scores(Four(), d, q_lo, kd, 0);
-          else scores(Two(), d, q_lo, kd, 0);
-          if (rotated) scores(One(), d, q_lo + nvb * kQStep, kd + nvb * kKStep, 1);
-        } else if (nvb == 8) {
-          scores(Four(), d, q_lo + 4 * kQStep, kd + 4 * kKStep, 1);
-        } else {
-          scores(Two(), d, q_lo + 4 * kQStep, kd + 4 * kKStep, 1);
-        }
-        if (j + 1 == L.ngroups) {
-          mma_commit(&sh->s_full[s_buf]);
-          s_buf ^= 1u;
-          qk.advance(L.stages);
-        }
-        return true;
-      };
-      // With two stages the second group comes after the output that gave it room.
-      const int early = L.stages > 2 ? L.ngroups : 1;
-      for (int k = 0; ok; ++k) {
-        if (!wait1(&sh->item_full[k & 1], (k >> 1) & 1)) break;
-        const int ntiles = sh->item[k & 1].ntiles;
-        const uint32_t idesc_pv = make_idesc_f16(kBf16, 128, (sh->item[k & 1].pairs + 15) & ~15, false) | (1u << 15);  // A MN-major
-        mbar_arrive(&sh->item_empty[k & 1]);
-        if (ntiles < 0) break;
-        ok = wait1(&sh->q_full, k & 1);
-        for (int j = 0; ok && j < L.ngroups; ++j) ok = group(j);
-        if (ntiles == 1) mma_commit(&sh->q_empty);
-        for (int i = 0; ok && i < ntiles; ++i) {
-          const bool more = i + 1 < ntiles;
-          for (int j = 0; ok && more && j < early; ++j) ok = group(j);
-          ok = ok && wait1(&sh->p_ready, p_phase);
-          if (ok && i == 0 && k > 0) ok = wait1(&sh->o_free, (k - 1) & 1);  // the item before has left O
-          if (!ok) break;
-          p_phase ^= 1u;
-          tc_fence_after();
-          const uint32_t vd = v_lo + pv.stage * stage_step, d = tmem + 128u, acc = i > 0;
-          if (nvb >= 4) output(Two(), d, vd, idesc_pv, acc);
-          else output(One(), d, vd, idesc_pv, acc);
-          mma_commit(&sh->empty[pv.stage][0]);
-          if (nvb > 4) {
-            if (nvb == 8) output(Two(), d + 2 * kPairs, vd + 4 * kKStep, idesc_pv, acc);
-            else output(One(), d + 2 * kPairs, vd + 4 * kKStep, idesc_pv, acc);
-            mma_commit(&sh->empty[pv.stage][1]);
-          }
-          mma_commit(&sh->pv_done);
-          pv.advance(L.stages);
-          for (int j = early; ok && more && j < L.ngroups; ++j) ok = group(j);
-          if (i + 2 == ntiles) mma_commit(&sh->q_empty);  // the item's last scores are issued
-        }
+      for (int e = 0; e < decltype(kN)::value * 4; ++e)
+        mma_ss_lo(d + (e >> 2) * kPairs, vd + (e >> 2) * (2 * kKStep) + 128 * (e & 3), v_hi, p_lo + 2 * (e & 3), k_hi, idesc,
+                  e & 3 ? 1u : acc);
+    };
+    using One = std::integral_constant<int, 1>;
+    using Two = std::integral_constant<int, 2>;
+    using Four = std::integral_constant<int, 4>;
+    Ring qk, pv;           // of the tile whose scores, whose output is issued next
+    uint32_t s_buf = 0;    // S of the next scores
+    uint32_t p_phase = 0;  // parity of the next P
+    bool ok = true;
+    // Group j of the next tile's scores.
+    auto group = [&](int j) {
+      if (!wait(&sh->full[qk.stage][j], qk.turn)) return false;
+      tc_fence_after();
+      const uint32_t d = tm + 64u * s_buf, kd = k_lo + qk.stage * stage_step;
+      if (j == 0) {
+        if (nvb >= 4) scores(Four(), d, q_lo, kd, 0);
+        else scores(Two(), d, q_lo, kd, 0);
+        if (rotated) scores(One(), d, q_lo + nvb * kQStep, kd + nvb * kKStep, 1);
+      } else if (nvb == 8) {
+        scores(Four(), d, q_lo + 4 * kQStep, kd + 4 * kKStep, 1);
+      } else {
+        scores(Two(), d, q_lo + 4 * kQStep, kd + 4 * kKStep, 1);
       }
-      mma_commit(&sh->all_done);
-      volatile int zero = 0;  // wait even after an abort: MMAs may still be in flight
-      mbar_wait(&sh->all_done, 0, &zero, a.status);
+      if (j + 1 == L.ngroups) {
+        mma_commit_elect(&sh->s_full[s_buf]);
+        s_buf ^= 1u;
+        qk.advance(L.stages);
+      }
+      return true;
+    };
+    // With two stages the second group comes after the output that gave it room.
+    const int early = L.stages > 2 ? L.ngroups : 1;
+    for (int k = 0; ok; ++k) {
+      if (!wait(&sh->item_full[k & 1], (k >> 1) & 1)) break;
+      const int ntiles = uniform(sh->item[k & 1].ntiles);
+      const uint32_t idesc_pv = make_idesc_f16(kBf16, 128, (uniform(sh->item[k & 1].pairs) + 15) & ~15, false) | (1u << 15);  // A MN-major
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->item_empty[k & 1]);
+      if (ntiles < 0) break;
+      ok = wait(&sh->q_full, k & 1);
+      for (int j = 0; ok && j < L.ngroups; ++j) ok = group(j);
+      if (ntiles == 1) mma_commit_elect(&sh->q_empty);
+      for (int i = 0; ok && i < ntiles; ++i) {
+        const bool more = i + 1 < ntiles;
+        for (int j = 0; ok && more && j < early; ++j) ok = group(j);
+        ok = ok && wait(&sh->p_ready, p_phase);
+        if (ok && i == 0 && k > 0) ok = wait(&sh->o_free, (k - 1) & 1);  // the item before has left O
+        if (!ok) break;
+        p_phase ^= 1u;
+        tc_fence_after();
+        const uint32_t vd = v_lo + pv.stage * stage_step, d = tm + 128u, acc = i > 0;
+        if (nvb >= 4) output(Two(), d, vd, idesc_pv, acc);
+        else output(One(), d, vd, idesc_pv, acc);
+        mma_commit_elect(&sh->empty[pv.stage][0]);
+        if (nvb > 4) {
+          if (nvb == 8) output(Two(), d + 2 * kPairs, vd + 4 * kKStep, idesc_pv, acc);
+          else output(One(), d + 2 * kPairs, vd + 4 * kKStep, idesc_pv, acc);
+          mma_commit_elect(&sh->empty[pv.stage][1]);
+        }
+        mma_commit_elect(&sh->pv_done);
+        pv.advance(L.stages);
+        for (int j = early; ok && more && j < L.ngroups; ++j) ok = group(j);
+        if (i + 2 == ntiles) mma_commit_elect(&sh->q_empty);  // the item's last scores are issued
+      }
     }
+    mma_commit_elect(&sh->all_done);
+    volatile int zero = 0;  // wait even after an abort: MMAs may still be in flight
+    mbar_wait(&sh->all_done, 0, &zero, a.status);
     __syncwarp();
   } else {
     // ================================================================ softmax, output

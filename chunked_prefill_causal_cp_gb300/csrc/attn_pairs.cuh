@@ -9,7 +9,7 @@
 //   warp 0      TMA producer: an item's Q tiles, then for each 128-key tile its K and V
 //               in units of 64 channels (16 KB) through a ring of as many units as fit;
 //               a tile's K, and its V, land and are given back as one
-//   warp 1      MMA issue, one thread:  S_w = Q_w K^T, O_w += P_w V for Q tile w = 0, 1
+//   warp 1      MMA issue:  S_w = Q_w K^T, O_w += P_w V for Q tile w = 0, 1
 //   warp 2      scheduling: finds this CTA's items, two ahead of the others
 //   warp 3      fills the control warpgroup, whose registers go to the others
 //   warps 4-7, 8-11  softmax of Q tile 0 and 1, a thread a row
@@ -280,111 +280,112 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
     }
     __syncwarp();
   } else {
-    // ================================================================ MMA issuer: one thread
-    if (lane == 0) {
-      auto wait1 = [&](uint64_t* b, uint32_t parity) { return mbar_wait(b, parity, abort_flag, wk.status); };
-      constexpr uint32_t kStep = kUnit >> 4;  // of a descriptor: 16 bytes
-      const uint64_t q_desc = make_sdesc_sw128(smem_u32(smem), 16, 1024);
-      const uint64_t v_desc = make_sdesc_sw128(smem_u32(sRing), kUnit, 1024);
-      const uint32_t q_lo = (uint32_t)q_desc, k_hi = (uint32_t)(q_desc >> 32);  // Q and K differ in their addresses only
-      const uint32_t k_lo = (uint32_t)make_sdesc_sw128(smem_u32(sRing), 16, 1024);
-      const uint32_t v_lo = (uint32_t)v_desc, v_hi = (uint32_t)(v_desc >> 32);
-      auto wrap = [](int slot) { return slot >= kRing ? slot - kRing : slot; };
-      // Of the tile whose K, whose V comes next: its barriers, their parity; the ring's slot of its first unit.
-      int kt = 0, vt = 0, k_slot = 0, v_slot = NQB % kRing;
-      uint32_t k_turn = 0, v_turn = 0;
-      uint32_t pq = 0, pp = 0, po = 0, begun = 0;  // bit w: parity of the Q tiles and P tiles taken, of the outputs begun; any begun
-      bool ok = true;
-      auto scores = [&](int w) {  // S_w = Q_w K^T
-        const uint32_t d = tmem + 256u * w, q = q_lo + (uint32_t)w * (NQB * kStep);
+    // ================================================================ MMA issuer
+    // The whole warp runs the loop, converged; one elected lane issues.  What addresses come from is broadcast.
+    auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+    const uint32_t tm0 = (uint32_t)uniform((int)tmem);
+    constexpr uint32_t kStep = kUnit >> 4;  // of a descriptor: 16 bytes
+    const uint64_t q_desc = make_sdesc_sw128(smem_u32(smem), 16, 1024);
+    const uint64_t v_desc = make_sdesc_sw128(smem_u32(sRing), kUnit, 1024);
+    const uint32_t q_lo = (uint32_t)q_desc, k_hi = (uint32_t)(q_desc >> 32);  // Q and K differ in their addresses only
+    const uint32_t k_lo = (uint32_t)make_sdesc_sw128(smem_u32(sRing), 16, 1024);
+    const uint32_t v_lo = (uint32_t)v_desc, v_hi = (uint32_t)(v_desc >> 32);
+    auto wrap = [](int slot) { return slot >= kRing ? slot - kRing : slot; };
+    // Of the tile whose K, whose V comes next: its barriers, their parity; the ring's slot of its first unit.
+    int kt = 0, vt = 0, k_slot = 0, v_slot = NQB % kRing;
+    uint32_t k_turn = 0, v_turn = 0;
+    uint32_t pq = 0, pp = 0, po = 0, begun = 0;  // bit w: parity of the Q tiles and P tiles taken, of the outputs begun; any begun
+    bool ok = true;
+    auto scores = [&](int w) {  // S_w = Q_w K^T
+      const uint32_t d = tm0 + 256u * w, q = q_lo + (uint32_t)w * (NQB * kStep);
 #pragma unroll
-        for (int b = 0; b < NQB; ++b) {
-          const uint32_t kd = k_lo + (uint32_t)wrap(k_slot + b) * kStep;
+      for (int b = 0; b < NQB; ++b) {
+        const uint32_t kd = k_lo + (uint32_t)wrap(k_slot + b) * kStep;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma_ss_lo(d, q + b * kStep + 2 * kk, k_hi, kd + 2 * kk, k_hi, kIdescQK, b | kk);
-        }
-        mma_commit(&sh->s_full[w]);
-      };
-      auto output = [&](int w, uint32_t acc) {  // O_w += P_w V
-        const uint32_t s = tmem + 256u * w, o = s + 128u;
-        if (NVB == 1 || v_slot + 1 < kRing) {
-          const uint32_t v = v_lo + (uint32_t)v_slot * kStep;
+        for (int kk = 0; kk < 4; ++kk) mma_ss_lo(d, q + b * kStep + 2 * kk, k_hi, kd + 2 * kk, k_hi, kIdescQK, b | kk);
+      }
+      mma_commit_elect(&sh->s_full[w]);
+    };
+    auto output = [&](int w, uint32_t acc) {  // O_w += P_w V
+      const uint32_t s = tm0 + 256u * w, o = s + 128u;
+      if (NVB == 1 || v_slot + 1 < kRing) {
+        const uint32_t v = v_lo + (uint32_t)v_slot * kStep;
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk) mma_ts_lo(o, s + kk * 8, v + 128 * kk, v_hi, kIdescPV, kk ? 1u : acc);
-        } else {  // the ring's end lies between V's units: 64 channels at a time
-          constexpr uint32_t kIdescHalf = make_idesc_f16(kBf16, 128, 64, true);
+        for (int kk = 0; kk < kKeys / 16; ++kk) mma_ts_lo(o, s + kk * 8, v + 128 * kk, v_hi, kIdescPV, kk ? 1u : acc);
+      } else {  // the ring's end lies between V's units: 64 channels at a time
+        constexpr uint32_t kIdescHalf = make_idesc_f16(kBf16, 128, 64, true);
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma_ts_lo(o, s + kk * 8, v_lo + (uint32_t)v_slot * kStep + 128 * kk, v_hi, kIdescHalf, kk ? 1u : acc);
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          mma_ts_lo(o, s + kk * 8, v_lo + (uint32_t)v_slot * kStep + 128 * kk, v_hi, kIdescHalf, kk ? 1u : acc);
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk) mma_ts_lo(o + 64u, s + kk * 8, v_lo + 128 * kk, v_hi, kIdescHalf, kk ? 1u : acc);
-        }
-      };
-      auto k_done = [&] {
-        mma_commit(&sh->k_empty[kt]);
-        k_slot = wrap(k_slot + kTile);
-        if (++kt == kTiles) {
-          kt = 0;
-          k_turn ^= 1u;
-        }
-      };
-      for (int k = 0; ok; ++k) {
-        if (!wait1(&sh->item_full[k & 1], (k >> 1) & 1)) break;
-        const int ntiles = sh->item[k & 1].ntiles;
-        const int nw = sh->item[k & 1].t0 + wk.tok_tile < sh->item[k & 1].rows ? 2 : 1;
-        mbar_arrive(&sh->item_empty[k & 1]);
-        if (ntiles < 0) break;
-        if (ntiles == 0) continue;
-        for (int w = 0; ok && w < nw; ++w) {
-          ok = wait1(&sh->q_full[w], (pq >> w) & 1);
-          pq ^= 1u << w;
-          if (ok && w == 0) ok = wait1(&sh->k_full[kt], k_turn);
+        for (int kk = 0; kk < kKeys / 16; ++kk) mma_ts_lo(o + 64u, s + kk * 8, v_lo + 128 * kk, v_hi, kIdescHalf, kk ? 1u : acc);
+      }
+    };
+    auto k_done = [&] {
+      mma_commit_elect(&sh->k_empty[kt]);
+      k_slot = wrap(k_slot + kTile);
+      if (++kt == kTiles) {
+        kt = 0;
+        k_turn ^= 1u;
+      }
+    };
+    for (int k = 0; ok; ++k) {
+      if (!wait(&sh->item_full[k & 1], (k >> 1) & 1)) break;
+      const int ntiles = uniform(sh->item[k & 1].ntiles);
+      const int nw = uniform(sh->item[k & 1].t0 + wk.tok_tile < sh->item[k & 1].rows ? 2 : 1);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->item_empty[k & 1]);
+      if (ntiles < 0) break;
+      if (ntiles == 0) continue;
+      for (int w = 0; ok && w < nw; ++w) {
+        ok = wait(&sh->q_full[w], (pq >> w) & 1);
+        pq ^= 1u << w;
+        if (ok && w == 0) ok = wait(&sh->k_full[kt], k_turn);
+        if (!ok) break;
+        tc_fence_after();
+        scores(w);
+      }
+      if (!ok) break;
+      k_done();
+      if (ntiles == 1) mma_commit_elect(&sh->q_empty);
+      for (int i = 0; ok && i < ntiles; ++i) {
+        const bool more = i + 1 < ntiles;
+        for (int w = 0; w < nw; ++w) {
+          ok = wait(&sh->p_ready[w], (pp >> w) & 1);
+          pp ^= 1u << w;
+          if (ok && w == 0) ok = wait(&sh->v_full[vt], v_turn);
+          if (ok && i == 0 && ((begun >> w) & 1)) ok = wait(&sh->o_free[w], ((po >> w) & 1) ^ 1);  // the output before has left TMEM
           if (!ok) break;
           tc_fence_after();
-          scores(w);
+          output(w, i > 0);
+          if (!more) mma_commit_elect(&sh->o_done[w]);
+          if (w == nw - 1) mma_commit_elect(&sh->v_empty[vt]);
+          if (more) {
+            if (w == 0) {
+              ok = wait(&sh->k_full[kt], k_turn);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            scores(w);
+          }
+          if (i == 0) {
+            po ^= 1u << w;
+            begun |= 1u << w;
+          }
         }
         if (!ok) break;
-        k_done();
-        if (ntiles == 1) mma_commit(&sh->q_empty);
-        for (int i = 0; ok && i < ntiles; ++i) {
-          const bool more = i + 1 < ntiles;
-          for (int w = 0; w < nw; ++w) {
-            ok = wait1(&sh->p_ready[w], (pp >> w) & 1);
-            pp ^= 1u << w;
-            if (ok && w == 0) ok = wait1(&sh->v_full[vt], v_turn);
-            if (ok && i == 0 && ((begun >> w) & 1)) ok = wait1(&sh->o_free[w], ((po >> w) & 1) ^ 1);  // the output before has left TMEM
-            if (!ok) break;
-            tc_fence_after();
-            output(w, i > 0);
-            if (!more) mma_commit(&sh->o_done[w]);
-            if (w == nw - 1) mma_commit(&sh->v_empty[vt]);
-            if (more) {
-              if (w == 0) {
-                ok = wait1(&sh->k_full[kt], k_turn);
-                if (!ok) break;
-                tc_fence_after();
-              }
-              scores(w);
-            }
-            if (i == 0) {
-              po ^= 1u << w;
-              begun |= 1u << w;
-            }
-          }
-          if (!ok) break;
-          v_slot = wrap(v_slot + kTile);
-          if (++vt == kTiles) {
-            vt = 0;
-            v_turn ^= 1u;
-          }
-          if (more) k_done();
-          if (i + 2 == ntiles) mma_commit(&sh->q_empty);  // the item's last scores are issued
+        v_slot = wrap(v_slot + kTile);
+        if (++vt == kTiles) {
+          vt = 0;
+          v_turn ^= 1u;
         }
+        if (more) k_done();
+        if (i + 2 == ntiles) mma_commit_elect(&sh->q_empty);  // the item's last scores are issued
       }
-      mma_commit(&sh->all_done);
-      volatile int zero = 0;  // wait even after an abort: MMAs may still be in flight
-      mbar_wait(&sh->all_done, 0, &zero, wk.status);
     }
+    mma_commit_elect(&sh->all_done);
+    volatile int zero = 0;  // wait even after an abort: MMAs may still be in flight
+    mbar_wait(&sh->all_done, 0, &zero, wk.status);
     __syncwarp();
   }
   } else {

@@ -273,26 +273,28 @@ __device__ __forceinline__ void mma_ts_elect(uint32_t d_tmem, uint32_t a_tmem, u
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// mma_ss with descriptors in halves: only the low ones (the addresses) change from one MMA to the next, and 32-bit sums
-// are all that then lies between two of them.  (The issuing thread's instructions are what an MMA of some 40 clocks waits
-// for: straight code, no divisions and few waits lie between them.)
+// mma_ss_elect and mma_ts_elect with descriptors in halves: only the low ones (the addresses) change from one MMA to the
+// next, and 32-bit sums are all that then lies between two of them.  In straight code, by a converged warp, M = N = 64
+// MMAs issue every 32 clocks, as they execute; by one thread of it every 54, in loops over their addresses every 50 to 115.
 __device__ __forceinline__ void mma_ss_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
                                           uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "{\n\t.reg .pred p, e;\n\t.reg .b32 r;\n\t.reg .b64 a, b;\n\t"
       "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+      "elect.sync r|e, 0xffffffff;\n\t"
       "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
       "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 __device__ __forceinline__ void mma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
                                           uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "{\n\t.reg .pred p, e;\n\t.reg .b32 r;\n\t.reg .b64 b;\n\t"
       "mov.b64 b, {%2, %3};\n\t"
+      "elect.sync r|e, 0xffffffff;\n\t"
       "setp.ne.b32 p, %5, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
