@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
   Shared* sh = reinterpret_cast<Shared*>(smem + L::ctl_off);
 
   pdl_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   // ---- set-up that reads no global memory: it may overlap the previous kernel
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
