@@ -326,23 +326,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t v_lo = (uint32_t)v_desc, v_hi = (uint32_t)(v_desc >> 32), stage_step = L.stage_bytes >> 4;
     const int nvb = L.nvb;
     const bool rotated = L.nqb > nvb;
-    // Scores over the kN blocks from Q at q, K at kd on; `acc`: added to what is there.
-    auto scores = [&](auto kN, uint32_t d, uint32_t q, uint32_t kd, uint32_t acc) {
+    // Scores over n blocks from Q at q, K at kd on; `acc`: added to what is there.
+    auto scores = [&](int n, uint32_t d, uint32_t q, uint32_t kd, uint32_t acc) {
+#pragma unroll 1
+      for (int b = 0; b < n; ++b, q += kQStep, kd += kKStep, acc = 1)
 #pragma unroll
-      for (int e = 0; e < decltype(kN)::value * 4; ++e)
-        mma_ss_lo(d, q + (e >> 2) * kQStep + 2 * (e & 3), k_hi, kd + (e >> 2) * kKStep + 2 * (e & 3), k_hi, kIdescQK,
-                  e ? 1u : acc);
+        for (int e = 0; e < 4; ++e) mma_ss_lo(d, q + 2 * e, k_hi, kd + 2 * e, k_hi, kIdescQK, e ? 1u : acc);
     };
-    // Output of kN x 128 channels from V at vd on into the columns at d.
-    auto output = [&](auto kN, uint32_t d, uint32_t vd, uint32_t idesc, uint32_t acc) {
+    // Output of n x 128 channels from V at vd on into the columns at d.
+    auto output = [&](int n, uint32_t d, uint32_t vd, uint32_t idesc, uint32_t acc) {
+#pragma unroll 1
+      for (int b = 0; b < n; ++b, d += kPairs, vd += 2 * kKStep)
 #pragma unroll
-      for (int e = 0; e < decltype(kN)::value * 4; ++e)
-        mma_ss_lo(d + (e >> 2) * kPairs, vd + (e >> 2) * (2 * kKStep) + 128 * (e & 3), v_hi, p_lo + 2 * (e & 3), k_hi, idesc,
-                  e & 3 ? 1u : acc);
+        for (int e = 0; e < 4; ++e) mma_ss_lo(d, vd + 128 * e, v_hi, p_lo + 2 * e, k_hi, idesc, e ? 1u : acc);
     };
-    using One = std::integral_constant<int, 1>;
-    using Two = std::integral_constant<int, 2>;
-    using Four = std::integral_constant<int, 4>;
+    const int v0 = min(nvb, 4), v1 = nvb - v0;  // blocks of values in the two groups
     Ring qk, pv;           // of the tile whose scores, whose output is issued next
     uint32_t s_buf = 0;    // S of the next scores
     uint32_t p_phase = 0;  // parity of the next P
@@ -353,13 +351,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const uint32_t d = tm + 64u * s_buf, kd = k_lo + qk.stage * stage_step;
       if (j == 0) {
-        if (nvb >= 4) scores(Four(), d, q_lo, kd, 0);
-        else scores(Two(), d, q_lo, kd, 0);
-        if (rotated) scores(One(), d, q_lo + nvb * kQStep, kd + nvb * kKStep, 1);
-      } else if (nvb == 8) {
-        scores(Four(), d, q_lo + 4 * kQStep, kd + 4 * kKStep, 1);
+        scores(v0, d, q_lo, kd, 0);
+        if (rotated) scores(1, d, q_lo + nvb * kQStep, kd + nvb * kKStep, 1);
       } else {
-        scores(Two(), d, q_lo + 4 * kQStep, kd + 4 * kKStep, 1);
+        scores(v1, d, q_lo + 4 * kQStep, kd + 4 * kKStep, 1);
       }
       if (j + 1 == L.ngroups) {
         mma_commit_elect(&sh->s_full[s_buf]);
@@ -389,12 +384,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         p_phase ^= 1u;
         tc_fence_after();
         const uint32_t vd = v_lo + pv.stage * stage_step, d = tm + 128u, acc = i > 0;
-        if (nvb >= 4) output(Two(), d, vd, idesc_pv, acc);
-        else output(One(), d, vd, idesc_pv, acc);
+        output(v0 / 2, d, vd, idesc_pv, acc);
         mma_commit_elect(&sh->empty[pv.stage][0]);
-        if (nvb > 4) {
-          if (nvb == 8) output(Two(), d + 2 * kPairs, vd + 4 * kKStep, idesc_pv, acc);
-          else output(One(), d + 2 * kPairs, vd + 4 * kKStep, idesc_pv, acc);
+        if (v1 > 0) {
+          output(v1 / 2, d + 2 * kPairs, vd + 4 * kKStep, idesc_pv, acc);
           mma_commit_elect(&sh->empty[pv.stage][1]);
         }
         mma_commit_elect(&sh->pv_done);
