@@ -517,27 +517,33 @@ def latent_desc(dtype, batch, num_heads, latent_dim, rope_dim, nope_dim=128, v_d
                       max_blocks, scale)
 
 
-def _strided_arg(where, t, dtype, shape, dev):
-    """(pointer, strides of all but the last dimension) of a tensor of exactly this shape whose last dimension is dense
-    and whose strides lead forward.  None and raw handles pass as they are (dense)."""
-    lead = len(shape) - 1
+def _rows2_arg(where, t, dtype, rows, width, dev):
+    """(pointer, row stride) of rows [rows, width] whose channels are dense and whose stride leads forward.  None and raw
+    handles pass as they are (dense)."""
     if t is None or isinstance(t, int):
-        return (t, *(0,) * lead)
-    if t.dtype is not dtype or t.get_device() != dev or tuple(t.shape) != shape:
-        _refuse(where)
-    if t.numel() == 0 or t.is_contiguous():
-        return (t.data_ptr(), *(0,) * lead)
-    if t.stride(-1) != 1 and shape[-1] > 1:
-        _refuse(where)
-    strides, dense = [], shape[-1]
-    for n, st in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
-        if n == 1:  # a dimension of one has any stride: the least that the call takes
-            st = dense
-        if st < dense:
-            _refuse(where)
-        strides.append(st)
-        dense = st * n
-    return (t.data_ptr(), *reversed(strides))
+        return t, 0
+    if t.dtype is dtype and t.get_device() == dev and t.shape == (rows, width):
+        s0, s1 = t.stride()
+        if rows < 2 or width < 1:  # a single row has any stride
+            s0 = width
+        if s0 >= width and (s1 == 1 or width < 2 or rows < 1):
+            return t.data_ptr(), s0
+    _refuse(where)
+
+
+def _rows3_arg(where, t, dtype, rows, heads, width, dev):
+    """(pointer, row stride, head stride) of [rows, heads, width], as _rows2_arg."""
+    if t is None or isinstance(t, int):
+        return t, 0, 0
+    if t.dtype is dtype and t.get_device() == dev and t.shape == (rows, heads, width):
+        s0, s1, s2 = t.stride()
+        if heads < 2 or rows < 1 or width < 1:
+            s1 = width
+        if rows < 2 or width < 1:
+            s0 = s1 * heads
+        if s1 >= width and s0 >= s1 * heads and (s2 == 1 or width < 2 or rows < 1):
+            return t.data_ptr(), s0, s1
+    _refuse(where)
 
 
 def _slots(desc):
@@ -552,10 +558,10 @@ def cp_latent_append(desc, prep, latent, k_rope, cache, seqlens_k, num_seqs, tot
     buffer of wider heads."""
     w, dt, c, r, i32 = "cp_latent_append", _LAYER_DTYPE.get(desc.dtype), desc.latent_dim, desc.rope_dim, torch.int32
     dev = _device(w, latent)
-    pl, sl = _strided_arg(w, latent, dt, (total_rows, c), dev)
-    pk, sk = _strided_arg(w, k_rope, dt, (total_rows, r), dev)
-    pq, qr, qh = _strided_arg(w, q_rope, dt, (total_rows, desc.num_heads, r), dev)
-    po, outr, outh = _strided_arg(w, q_out, dt, (total_rows, desc.num_heads, r), dev)
+    pl, sl = _rows2_arg(w, latent, dt, total_rows, c, dev)
+    pk, sk = _rows2_arg(w, k_rope, dt, total_rows, r, dev)
+    pq, qr, qh = _rows3_arg(w, q_rope, dt, total_rows, desc.num_heads, r, dev)
+    po, outr, outh = _rows3_arg(w, q_out, dt, total_rows, desc.num_heads, r, dev)
     lens, cu, table = _seq_args(w, desc, seqlens_k, cu_rows, block_table, num_seqs, dev)
     s = lib().cp_latent_append(
         ctypes.byref(desc), ctypes.byref(prep), pl, sl, pk, sk, _arg(w, weight, dt, c, dev),
@@ -592,9 +598,9 @@ def cp_latent_chunk_attn(desc, q, k_nope, k_rope, v, out, num_seqs, total_rows, 
     w, dt, h = "cp_latent_chunk_attn", _LAYER_DTYPE.get(desc.dtype), desc.num_heads
     dn, r, dv, i32 = desc.nope_dim, desc.rope_dim, desc.v_dim, torch.int32
     dev = _device(w, q, out)
-    pk, kr, kh = _strided_arg(w, k_nope, dt, (total_keys, h, dn), dev)
-    pr, rr = _strided_arg(w, k_rope, dt, (total_keys, r), dev)
-    pv, vr, vh = _strided_arg(w, v, dt, (total_keys, h, dv), dev)
+    pk, kr, kh = _rows3_arg(w, k_nope, dt, total_keys, h, dn, dev)
+    pr, rr = _rows2_arg(w, k_rope, dt, total_keys, r, dev)
+    pv, vr, vh = _rows3_arg(w, v, dt, total_keys, h, dv, dev)
     s = lib().cp_latent_chunk_attn(
         ctypes.byref(desc), _arg(w, q, dt, total_rows * h * (dn + r), dev), pk, kr, kh, pr, rr, pv, vr, vh,
         _arg(w, cu_rows, i32, num_seqs + 1, dev), _arg(w, cu_keys, i32, num_seqs + 1, dev), num_seqs, total_rows,

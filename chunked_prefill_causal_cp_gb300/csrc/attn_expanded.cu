@@ -15,6 +15,7 @@ using pairs::Item;
 
 struct ExpandedWork : pairs::WorkBase {
   static constexpr bool kPaged = false, kExpanded = true;
+  using Cursor = TurnCursor<ExpandedWork>;
   SeqRows keys;
   int total_keys;
 
@@ -35,7 +36,7 @@ struct ExpandedWork : pairs::WorkBase {
     }
     return (long long)items(r) * hq;
   }
-  __device__ __forceinline__ bool make(int s, long long idx, long long, Item& x) const {
+  __device__ __forceinline__ bool make(int s, long long idx, Item& x) const {
     int n;
     if (!bounds(s, x.rows, x.row0, n, x.key0)) return false;
     x.s = s;

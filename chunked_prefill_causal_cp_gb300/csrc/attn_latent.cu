@@ -34,8 +34,9 @@
 // positions that hold a non-finite value; the pairs that see such a one become NaN by
 // their sum.
 //
-// Splits leave unnormalised fp32 parts and (maximum, sum) in the workspace, which the
-// combine kernel merges in a fixed order.
+// The CTAs share the tiles of keys of all tiles of pairs out evenly (cp_latent.h); a tile of
+// pairs that several of them have leaves unnormalised fp32 parts and (maximum, sum) in
+// the workspace, which the combine kernel merges in order.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -79,9 +80,9 @@ struct __align__(16) Shared {
   int abort;
   Item item[2];
   uint32_t bad[2][8];         // keys of the tile with a non-finite value, 8 a warp
+  int8_t parent[2][CP_TREE_MAX];  // a tree's, beside its item
   union __align__(16) {
-    int parent[CP_TREE_MAX];  // before an item's walk
-    struct {                  // during it
+    struct {                  // during an item's walk
       float alpha[kPairs];    // the factor of a pair's column for its raised maximum
       float top[4][kPairs];   // maximum of a pair's 16 scores of this tile, by part
     };
@@ -114,8 +115,7 @@ Layout layout_of(int dqk, int dv) {
   return l;
 }
 
-// The call's items: (tile of pairs, split) of each sequence, tile fastest, so that the
-// tiles that read the same keys run at the same time.
+// The call's units: tiles of pairs of each sequence.
 struct Work : RowsAttnArgs {
   // A sequence within the call's bounds: its rows, positions before them, first row.
   __device__ __forceinline__ bool bounds(int s, int& r, int& p, int& row0) const {
@@ -125,34 +125,24 @@ struct Work : RowsAttnArgs {
     row0 = seq_row0(rows, s);
     return p >= 0 && (long long)p + r <= max_ctx && row0 >= 0 && row0 <= total_rows - r && !(parents && r > CP_TREE_MAX);
   }
-  __device__ __forceinline__ int tiles(int r) const { return (r * hq - 1) / kPairs + 1; }
-  __device__ __forceinline__ long long weight(int s, bool report) const {
+  __device__ __forceinline__ int pair_tiles(int r) const { return (r * hq - 1) / kPairs + 1; }
+  __device__ __forceinline__ int units(int s, bool report) const {
     int r, p, row0;
-    if (!bounds(s, r, p, row0)) {
-      if (report && status && r >= 1) atomicOr(status, CP_DEV_BOUNDS);
-      return 0;
-    }
-    const int nt = tiles(r);
-    return (long long)nt * rows_splits(p + r, nt);
+    if (bounds(s, r, p, row0)) return pair_tiles(r);
+    if (report && status && r >= 1) atomicOr(status, CP_DEV_BOUNDS);
+    return 0;
   }
-  __device__ __forceinline__ bool make(int s, long long idx, long long r_all, Item& x) const {
+  __device__ __forceinline__ int key_tiles(int s) const { return (past[s] + seq_rows(rows, s) - 1) / kTile + 1; }
+  __device__ __forceinline__ bool make(int s, int u, int k0, int n, Item& x) const {
     if (!bounds(s, x.rows, x.past, x.row0)) return false;
-    const int n = x.past + x.rows, nt = tiles(x.rows), splits = rows_splits(n, nt), keys = rows_split_keys(n, splits);
-    const int split = (int)idx / nt;
     x.s = s;
-    x.first = (int)(idx - (long long)split * nt) * kPairs;
+    x.first = u * kPairs;
     x.pairs = min(kPairs, x.rows * hq - x.first);
-    x.j_begin = split * keys;
+    x.j_begin = k0 * kTile;
     const int seen = x.past + (x.first + x.pairs - 1) / hq + 1;  // by the tile's last row
-    x.j_end = (int)min((long long)seen, (long long)x.j_begin + keys);
-    x.ntiles = (x.j_end - x.j_begin + kTile - 1) / kTile;
-    x.whole = splits == 1;
-    x.part = (int)r_all;
-    if (!x.whole && r_all >= part_slots) {
-      if (status && (threadIdx.x & 31) == 0) atomicOr(status, CP_DEV_BOUNDS);
-      return false;
-    }
-    return x.j_end > x.j_begin;
+    x.ntiles = seen > x.j_begin ? min((seen - x.j_begin - 1) / kTile + 1, n) : 0;
+    x.j_end = min(seen, x.j_begin + x.ntiles * kTile);
+    return x.ntiles > 0;
   }
 };
 
@@ -225,11 +215,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = &sh->abort;
   auto wait = [&](uint64_t* b, uint32_t parity) { return warp_wait(b, parity, abort_flag, a.status); };
   // Item k of this CTA, as every role takes it: false when there are no more.
+  auto give = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh->item_empty[k & 1]);
+  };
   auto take = [&](int k, Item& x) {
     if (!wait(&sh->item_full[k & 1], (k >> 1) & 1)) return false;
     x = sh->item[k & 1];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh->item_empty[k & 1]);
     return x.ntiles >= 0;
   };
   // A group's blocks: values four at a time; the first group also has the rotated part, behind them all.
@@ -239,11 +231,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 2) {
     // ================================================================ scheduling
-    ItemCursor<Work> cur(a);
+    ShareCursor<Work> cur(a);
     Item x;
     for (int k = 0;; ++k) {
       const bool more = cur.next(a, x);
       if (k >= 2 && !wait(&sh->item_empty[k & 1], ((k >> 1) & 1) ^ 1)) break;
+      if (a.parents && more) {
+        load_parents(a.parents + x.row0, x.rows, a.status, sh->parent[k & 1]);
+        __syncwarp();
+      }
       if (lane == 0) {
         if (!more) x.ntiles = -1;
         sh->item[k & 1] = x;
@@ -266,6 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     Item x;
     for (int k = 0; ok && take(k, x); ++k) {
+      give(k);
       if (k > 0) ok = wait(&sh->q_empty, (k - 1) & 1);
       if (!ok) break;
       if (lane == 0) {
@@ -369,8 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait(&sh->item_full[k & 1], (k >> 1) & 1)) break;
       const int ntiles = uniform(sh->item[k & 1].ntiles);
       const uint32_t idesc_pv = make_idesc_f16(kBf16, 128, (uniform(sh->item[k & 1].pairs) + 15) & ~15, false) | (1u << 15);  // A MN-major
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->item_empty[k & 1]);
+      give(k);
       if (ntiles < 0) break;
       ok = wait(&sh->q_full, k & 1);
       for (int j = 0; ok && j < L.ngroups; ++j) ok = group(j);
@@ -420,22 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool row_ok = m < x.pairs, active = quarter * 16 < x.pairs;
       const int tok = (x.first + m) / a.hq;
       uint64_t see_lo = 0, see_hi = 0;  // a tree's row: the call's rows that it sees
-      if (a.parents) {
-        if (me < x.rows) {
-          int up = a.parents[x.row0 + me];
-          if (up < -1 || up >= me) {
-            up = -1;
-            if (a.status) atomicOr(a.status, CP_DEV_BOUNDS);
-          }
-          sh->parent[me] = up;
-        }
-        softmax_sync();
-        for (int j = row_ok ? tok : -1; j >= 0; j = sh->parent[j]) {
-          if (j < 64) see_lo |= 1ull << j;
-          else see_hi |= 1ull << (j - 64);
-        }
-        softmax_sync();  // the factors take the parents' place
-      }
+      if (a.parents) ancestors(sh->parent[k & 1], row_ok ? tok : -1, see_lo, see_hi);
+      give(k);
       float m_run = -INFINITY, l_run = 0.f;
       for (int i = 0; i < x.ntiles; ++i, ++gt, ring.advance(L.stages)) {
         const int j0 = x.j_begin + i * kTile;
@@ -625,43 +607,39 @@ __global__ void __launch_bounds__(512) latent_combine_kernel(const Work a, const
   pdl_launch_dependents();
   pdl_wait();
   const int groups = (a.q_rows + per - 1) / per, lane = threadIdx.x & 31;
-  int w = blockIdx.x / groups;  // tile of the call
-  long long base = 0;           // items before its sequence
+  int w = blockIdx.x / groups;   // tile of pairs of the call
+  long long all = 0, before = 0;  // tiles of keys of the call; of the sequences before this one
   int s = -1, tile = 0;
-  for (int q0 = 0; q0 < a.rows.num_seqs && s < 0; q0 += 32) {
+  for (int q0 = 0; q0 < a.rows.num_seqs; q0 += 32) {
     const int q = q0 + lane;
     int r, p, row0;
-    long long tiles = 0, weight = 0;
+    long long tiles = 0, sum = 0;
     if (q < a.rows.num_seqs && a.bounds(q, r, p, row0)) {
-      tiles = a.tiles(r);
-      weight = tiles * rows_splits(p + r, (int)tiles);
+      tiles = a.pair_tiles(r);
+      sum = tiles * (kStart + a.key_tiles(q));
     }
-    long long inc = tiles, upto = weight;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, inc, o), u = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) {
-        inc += v;
-        upto += u;
+    const long long own = sum;
+    sum = warp_prefix(sum);
+    if (s < 0) {
+      const long long inc = warp_prefix(tiles), total = __shfl_sync(0xffffffffu, inc, 31);
+      if (w < total) {
+        const int at = __ffs(__ballot_sync(0xffffffffu, inc > w)) - 1;
+        s = q0 + at;
+        tile = (int)(w - __shfl_sync(0xffffffffu, inc - tiles, at));
+        before = all + __shfl_sync(0xffffffffu, sum - own, at);
+      } else {
+        w -= (int)total;
       }
     }
-    const long long total = __shfl_sync(0xffffffffu, inc, 31);
-    if (w < total) {
-      const int at = __ffs(__ballot_sync(0xffffffffu, inc > w)) - 1;
-      s = q0 + at;
-      tile = (int)(w - __shfl_sync(0xffffffffu, inc - tiles, at));
-      base += __shfl_sync(0xffffffffu, upto - weight, at);
-    } else {
-      w -= (int)total;
-      base += __shfl_sync(0xffffffffu, upto, 31);
-    }
+    all += __shfl_sync(0xffffffffu, sum, 31);
   }
   int r, p, row0;
   if (s < 0 || !a.bounds(s, r, p, row0)) return;  // the same for all threads
-  const int nt = a.tiles(r), splits = rows_splits(p + r, nt), keys = rows_split_keys(p + r, splits);
-  if (splits == 1 || base + (long long)nt * splits > a.part_slots) return;
+  const int each = a.key_tiles(s);
+  const UnitShares u(all, before + (long long)tile * (kStart + each), each, a.ctas);
+  if (u.from == u.to) return;  // finished by its one CTA
   const int first = tile * kPairs, pairs = min(kPairs, r * a.hq - first);
-  const int used = (p + (first + pairs - 1) / a.hq) / keys + 1;  // splits that hold keys of the tile
+  const int seen = p + (first + pairs - 1) / a.hq + 1;  // keys of the tile
   const int c4 = a.dv / 4, mine = threadIdx.x / a.dv, slice = threadIdx.x % a.dv / c4, d4 = threadIdx.x % c4;
   const int m = blockIdx.x % groups * per + mine;
   const bool on = m < pairs;
@@ -669,20 +647,22 @@ __global__ void __launch_bounds__(512) latent_combine_kernel(const Work a, const
   float mx = -INFINITY, l = 0.f;
   if (on) {
     constexpr int kAhead = 4;
-    for (int i0 = slice; i0 < used; i0 += kAhead * kSlices) {
+    for (int c0 = u.from + slice; c0 <= u.to; c0 += kAhead * kSlices) {
       float2 ml[kAhead];
       float4 x[kAhead];
+      int n = 0;
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
-        const int i = i0 + j * kSlices;
-        if (i >= used) break;
-        const long long row = (base + (long long)i * nt + tile) * kPairs + m;
+        const int c = c0 + j * kSlices;
+        if (c > u.to || u.start(c) * kTile >= seen) break;
+        const long long row = (long long)u.part(c) * kPairs + m;
         ml[j] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + row * 2));
         x[j] = __ldcg(reinterpret_cast<const float4*>(a.part_o + row * a.dv + 4 * d4));
+        n = j + 1;
       }
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
-        if (i0 + j * kSlices >= used) break;
+        if (j >= n) break;
         const float mn = fmaxf(mx, ml[j].x), z = mn == -INFINITY ? 0.f : mn;
         const float k0 = ex2_approx(mx - z), k1 = ex2_approx(ml[j].x - z);
         v.x = v.x * k0 + x[j].x * k1;
@@ -751,30 +731,30 @@ cudaError_t launch_t(const RowsAttnArgs& args, int dtype, cudaStream_t st) {
     ready_mask.fetch_or(bit, std::memory_order_release);
   }
   const uint32_t smem = std::max(l.alloc, 120u * 1024u);  // one CTA an SM: each takes all of TMEM
-  const dim3 grid((unsigned)std::min<long long>((long long)a.tiles_bound * a.max_splits, 152));
-  e = launch_pdl(latent_kernel<T, kPaged>, grid, dim3(kThreads), smem, st, tq, tk, a, l);
-  if (e != cudaSuccess || a.max_splits == 1) return e;
+  e = launch_pdl(latent_kernel<T, kPaged>, dim3(a.ctas), dim3(kThreads), smem, st, tq, tk, a, l);
+  if (e != cudaSuccess || !a.split) return e;
   const int per = std::max(1, 256 / a.dv);
-  return launch_pdl(latent_combine_kernel<T>, dim3((unsigned)(a.tiles_bound * ((a.q_rows + per - 1) / per))), dim3(per * a.dv), 0, st,
+  return launch_pdl(latent_combine_kernel<T>, dim3((unsigned)(a.tiles * ((a.q_rows + per - 1) / per))), dim3(per * a.dv), 0, st,
                     a, per);
 }
 
 }  // namespace
 
-RowsPlan rows_plan(int heads, int dv, bool uniform, long long num_seqs, long long total_rows, int max_ctx) {
-  RowsPlan p;
+RowsPlan latent_plan(int heads, int dv, bool uniform, long long num_seqs, long long total_rows, int max_ctx) {
+  RowsPlan p{};
   const long long pairs = (uniform ? total_rows / num_seqs : total_rows) * heads;  // of a sequence, at most
+  const int key_tiles = (max_ctx - 1) / kTile + 1;
   p.q_rows = (int)std::min<long long>(kPairs, pairs);
   p.tiles = uniform ? num_seqs * ((pairs + kPairs - 1) / kPairs) : pairs / kPairs + 1 + num_seqs;
-  p.max_splits = rows_max_splits(max_ctx, 1);
-  // A sequence's items: its tiles, or, split, no more than kRowsItems.
-  p.slots = p.max_splits == 1 ? 0 : std::min(p.tiles * p.max_splits, p.tiles + num_seqs * kRowsItems);
-  p.part_floats = (double)p.slots * kPairs * dv;
-  p.bytes = (double)p.slots * kPairs * (dv + 2) * sizeof(float);
+  p.work = (double)p.tiles * (kStart + key_tiles);
+  p.ctas = (int)std::min<double>(p.work, kSms);
+  p.split = key_tiles > 1;
+  p.part_floats = p.split ? 2LL * kSms * kPairs * dv : 0;
+  p.bytes = p.split ? 2LL * kSms * kPairs * (dv + 2) * (long long)sizeof(float) : 0;
   return p;
 }
 
-cudaError_t launch_rows_attn(const RowsAttnArgs& a, int dtype, cudaStream_t st) {
+cudaError_t launch_latent(const RowsAttnArgs& a, int dtype, cudaStream_t st) {
   const bool paged = a.cache.kind == CP_CACHE_PAGED;
   if (dtype == CP_BF16) return paged ? launch_t<__nv_bfloat16, true>(a, dtype, st) : launch_t<__nv_bfloat16, false>(a, dtype, st);
   return paged ? launch_t<__half, true>(a, dtype, st) : launch_t<__half, false>(a, dtype, st);

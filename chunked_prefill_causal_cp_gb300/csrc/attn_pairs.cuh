@@ -72,12 +72,13 @@ struct Item {
 
 struct __align__(16) Shared {
   uint64_t item_full[2], item_empty[2], q_full[2], q_empty, k_full[kMaxTiles], v_full[kMaxTiles], k_empty[kMaxTiles],
-      v_empty[kMaxTiles], s_full[2], p_ready[2], o_done[2], o_free[2], all_done;
+      v_empty[kMaxTiles], s_full[2], p_ready[2], o_done[2], o_free[2], guarded[2], all_done;
   uint32_t tmem_base;
   int abort;
   Item item[2];
-  int parent[2][CP_TREE_MAX];               // of a softmax warpgroup each
-  __align__(16) uint16_t bad[2][8];         // keys of the tile with a non-finite value, 16 each
+  int8_t parent[2][CP_TREE_MAX];            // a tree's, beside its item
+  // Keys of a tile with a non-finite value, 16 each: of tiles that one Q tile looks through, that two do.
+  __align__(16) uint16_t bad[2][2][8];
 };
 
 template <int NQB>
@@ -93,14 +94,8 @@ struct Maps {
   CUtensorMap q, k, kr, v;
 };
 
-template <int kId>
-__device__ __forceinline__ void group_sync(int threads) {
-  asm volatile("bar.sync %0, %1;" ::"n"(kId), "r"(threads) : "memory");
-}
-
 // What a call is about: TreeWork (attn_tree.cu) and ExpandedWork (attn_expanded.cu) add
-// kPaged and kExpanded, and say how many items a sequence has (`weight`, 0 for one that is
-// skipped) and what its idx-th is (`make`).
+// kPaged, kExpanded, and their Cursor with what it asks.
 struct WorkBase {
   int hq, hkv, group;
   int tok_tile;            // tokens of a Q tile
@@ -150,6 +145,8 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
       mbar_init(&sh->o_free[i], 128);
     }
     mbar_init(&sh->q_empty, 1);
+    mbar_init(&sh->guarded[0], 128);
+    mbar_init(&sh->guarded[1], 256);
     for (int i = 0; i < kTiles; ++i) {
       mbar_init(&sh->k_full[i], 1);
       mbar_init(&sh->v_full[i], 1);
@@ -175,11 +172,13 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
   volatile int* abort_flag = &sh->abort;
   auto wait = [&](uint64_t* b, uint32_t parity) { return warp_wait(b, parity, abort_flag, wk.status); };
   // Item k of this CTA, as every role takes it: false when there are no more.
+  auto give = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh->item_empty[k & 1]);
+  };
   auto take = [&](int k, Item& x) {
     if (!wait(&sh->item_full[k & 1], (k >> 1) & 1)) return false;
     x = sh->item[k & 1];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh->item_empty[k & 1]);
     return x.ntiles >= 0;
   };
   pdl_wait();  // everything below reads what earlier kernels wrote
@@ -188,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
   if (warp == 2) {
     // ================================================================ scheduling
-    ItemCursor<Work> cur(wk);
+    typename Work::Cursor cur(wk);
     int k = 0;
     bool ok = true;
     Item x;
@@ -196,6 +195,10 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
       const bool more = cur.next(wk, x);
       if (k >= 2) ok = wait(&sh->item_empty[k & 1], ((k >> 1) & 1) ^ 1);
       if (!ok) break;
+      if (!Work::kExpanded && more) {
+        load_parents(wk.parents + x.row0, x.rows, wk.status, sh->parent[k & 1]);
+        __syncwarp();
+      }
       if (lane == 0) {
         if (!more) x.ntiles = -1;
         sh->item[k & 1] = x;
@@ -218,6 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
     bool ok = true;
     Item x;
     for (int k = 0; ok && take(k, x); ++k) {
+      give(k);
       if (x.ntiles == 0) continue;
       if (queries > 0) ok = wait(&sh->q_empty, (queries - 1) & 1);
       if (!ok) break;
@@ -333,8 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
       if (!wait(&sh->item_full[k & 1], (k >> 1) & 1)) break;
       const int ntiles = uniform(sh->item[k & 1].ntiles);
       const int nw = uniform(sh->item[k & 1].t0 + wk.tok_tile < sh->item[k & 1].rows ? 2 : 1);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->item_empty[k & 1]);
+      give(k);
       if (ntiles < 0) break;
       if (ntiles == 0) continue;
       for (int w = 0; ok && w < nw; ++w) {
@@ -351,10 +354,11 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
       for (int i = 0; ok && i < ntiles; ++i) {
         const bool more = i + 1 < ntiles;
         for (int w = 0; w < nw; ++w) {
-          ok = wait(&sh->p_ready[w], (pp >> w) & 1);
-          pp ^= 1u << w;
-          if (ok && w == 0) ok = wait(&sh->v_full[vt], v_turn);
+          // P last: it comes last, and what follows it is what the softmax waits for.
+          if (w == 0) ok = wait(&sh->v_full[vt], v_turn);
           if (ok && i == 0 && ((begun >> w) & 1)) ok = wait(&sh->o_free[w], ((po >> w) & 1) ^ 1);  // the output before has left TMEM
+          ok = ok && wait(&sh->p_ready[w], (pp >> w) & 1);
+          pp ^= 1u << w;
           if (!ok) break;
           tc_fence_after();
           output(w, i > 0);
@@ -399,42 +403,21 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
   int t = 0;            // the CTA's tiles so far
   int ns = 0, no = 0;   // score tiles, outputs of this Q tile so far
   Item x;
-  // After a wait that gave up, an item's walk goes on without waiting, so that its barriers stay whole; its output is not
-  // written, and the warps leave together.
+  int guards[2] = {0, 0};  // tiles looked through for hidden values so far, by one Q tile, by two
   for (int k = 0;; ++k) {
+    // After a wait that gave up, an item's walk goes on without waiting, and its output is not written.
     bool alive = take(k, x) && !*abort_flag;
-    int any;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 4, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(any)
-                 : "r"((uint32_t)!alive)
-                 : "memory");
-    if (any) break;
+    if (!__all_sync(0xffffffffu, alive)) break;
     const bool q1 = x.t0 + wk.tok_tile < x.rows;
     const int tok = x.t0 + w * wk.tok_tile + mtok;  // this row's token
     const bool row_ok = mtok < wk.tok_tile && tok < x.rows;
     const int n = x.past + x.rows;
+    uint64_t see_lo = 0, see_hi = 0;  // a tree's row: the call's rows that it sees
+    if (!Work::kExpanded) ancestors(sh->parent[k & 1], row_ok ? tok : -1, see_lo, see_hi);
+    give(k);
     if (w == 1 && !q1) {
       t += x.ntiles;
       continue;
-    }
-    uint64_t see_lo = 0, see_hi = 0;  // a tree's row: the call's rows that it sees
-    if (!Work::kExpanded) {
-      if (m < x.rows) {
-        int up = wk.parents[x.row0 + m];
-        if (up < -1 || up >= m) {
-          up = -1;
-          if (wk.status) atomicOr(wk.status, CP_DEV_BOUNDS);
-        }
-        sh->parent[w][m] = up;
-      }
-      if (w == 0) group_sync<1>(128);
-      else group_sync<2>(128);
-      for (int j = row_ok ? tok : -1; j >= 0; j = sh->parent[w][j]) {
-        if (j < 64) see_lo |= 1ull << j;
-        else see_hi |= 1ull << (j - 64);
-      }
-      if (w == 0) group_sync<1>(128);  // the next item's parents take their place
-      else group_sync<2>(128);
     }
     const int seen = Work::kExpanded ? x.past + tok + 1 : x.past;  // keys [0, seen) are seen, and in a tree the row's ancestors
     float m_run = -INFINITY, l_run = 0.f;
@@ -522,18 +505,21 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
         if (per == 2) bad = __shfl_xor_sync(0xffffffffu, bad, 1) || bad;
         if (bad)
           for (int c = part; c < kChunks; c += per) *chunk(c) = make_uint4(0, 0, 0, 0);
-        uint32_t bits = __ballot_sync(0xffffffffu, bad && !gone);
+        const int turn = q1 ? guards[1]++ : guards[0]++;
+        uint16_t* found = sh->bad[q1][turn & 1];
+        const uint32_t bits = __ballot_sync(0xffffffffu, bad && !gone);
         if (lane == 0) {
           if (per == 2) {
-            sh->bad[i & 1][me / 32] = (uint16_t)even_bits(bits);
+            found[me / 32] = (uint16_t)even_bits(bits);
           } else {
-            sh->bad[i & 1][2 * quarter] = (uint16_t)bits;
-            sh->bad[i & 1][2 * quarter + 1] = (uint16_t)(bits >> 16);
+            found[2 * quarter] = (uint16_t)bits;
+            found[2 * quarter + 1] = (uint16_t)(bits >> 16);
           }
         }
         fence_proxy_async_smem();  // the tensor cores read V through the async proxy
-        group_sync<3>(128 * per);
-        const uint4 y = *reinterpret_cast<const uint4*>(sh->bad[i & 1]);
+        mbar_arrive(&sh->guarded[q1]);
+        alive = alive && wait(&sh->guarded[q1], turn & 1);
+        const uint4 y = *reinterpret_cast<const uint4*>(found);
         if ((vis[0] & (y.x | (uint64_t)y.y << 32)) | (vis[1] & (y.z | (uint64_t)y.w << 32))) l_run = __int_as_float(0x7fffffff);
       }
       tmem_wait_st();

@@ -2,8 +2,9 @@
 // attn_pairs.cuh.
 //
 // A tree's up to 128 nodes x G heads are one to a few pairs of Q tiles that read the
-// whole context, so the keys are split; the splits leave unnormalised fp32 parts
-// in the workspace, which the combine kernel merges in order.
+// whole context, and the CTAs share their tiles of keys out evenly (cp_latent.h); a unit
+// of more than one leaves unnormalised fp32 parts in the workspace, which the combine
+// kernel merges in order.
 #include "attn_pairs.cuh"
 
 namespace cp {
@@ -14,49 +15,38 @@ using pairs::Item;
 template <bool kPaged_>
 struct TreeWork : pairs::WorkBase {
   static constexpr bool kPaged = kPaged_, kExpanded = false;
+  using Cursor = ShareCursor<TreeWork>;
   const int* past;
-  int max_ctx;
-  long long part_slots;
+  int max_ctx, ctas;
 
-  // Pairs of Q tiles, and splits, of a sequence of r rows and n positions.
-  __device__ __forceinline__ int items(int r) const { return (r - 1) / (2 * tok_tile) + 1; }
+  // A sequence within the call's bounds: its rows, positions before them, first row.
   __device__ __forceinline__ bool bounds(int s, int& r, int& p, int& row0) const {
     r = seq_rows(rows, s);
     if (r < 1) return false;
     p = past[s];
     row0 = seq_row0(rows, s);
-    const bool ok = p >= 0 && (long long)p + r <= max_ctx && row0 >= 0 && row0 <= total_rows - r && r <= CP_TREE_MAX;
-    return ok;
+    return p >= 0 && (long long)p + r <= max_ctx && row0 >= 0 && row0 <= total_rows - r && r <= CP_TREE_MAX;
   }
-  __device__ __forceinline__ long long weight(int s, bool report) const {
+  __device__ __forceinline__ int q_pairs(int r) const { return (r - 1) / (2 * tok_tile) + 1; }
+  __device__ __forceinline__ int units(int s, bool report) const {
     int r, p, row0;
-    if (!bounds(s, r, p, row0)) {
-      if (report && status && r >= 1) atomicOr(status, CP_DEV_BOUNDS);
-      return 0;
-    }
-    const int nt = items(r) * hkv;
-    return (long long)nt * tree_splits(p + r, nt);
+    if (bounds(s, r, p, row0)) return q_pairs(r) * hkv;
+    if (report && status && r >= 1) atomicOr(status, CP_DEV_BOUNDS);
+    return 0;
   }
-  // Item idx of a sequence: (split, KV head, pair), the pairs that read the same keys side by side.
-  __device__ __forceinline__ bool make(int s, long long idx, long long r_all, Item& x) const {
+  __device__ __forceinline__ int key_tiles(int s) const { return (past[s] + seq_rows(rows, s) - 1) / pairs::kKeys + 1; }
+  // Unit u of a sequence: (KV head, pair of Q tiles).
+  __device__ __forceinline__ bool make(int s, int u, int k0, int n, Item& x) const {
     if (!bounds(s, x.rows, x.past, x.row0)) return false;
-    const int n = x.past + x.rows, ni = items(x.rows), splits = tree_splits(n, ni * hkv), keys = tree_split_keys(n, splits);
-    const int at = (int)(idx % ni), gs = (int)(idx / ni), split = gs / hkv;
+    const int np = q_pairs(x.rows);
     x.s = s;
-    x.g = gs % hkv;
+    x.g = u / np;
     x.key0 = 0;
-    x.t0 = at * 2 * tok_tile;
-    x.j_begin = split * keys;
+    x.t0 = (u - x.g * np) * 2 * tok_tile;
+    x.j_begin = k0 * pairs::kKeys;
     const int seen = x.past + min(x.rows, x.t0 + 2 * tok_tile);  // by the item's last row
-    const int end = (int)min((long long)seen, (long long)x.j_begin + keys);
-    x.ntiles = end > x.j_begin ? (end - x.j_begin + pairs::kKeys - 1) / pairs::kKeys : 0;
+    x.ntiles = seen > x.j_begin ? min((seen - x.j_begin - 1) / pairs::kKeys + 1, n) : 0;
     x.all = x.past + (x.rows == 1 ? 1 : 0);
-    x.whole = splits == 1;
-    x.part = (int)r_all;
-    if (!x.whole && r_all >= part_slots) {
-      if (status && (threadIdx.x & 31) == 0) atomicOr(status, CP_DEV_BOUNDS);
-      return false;
-    }
     return x.ntiles > 0;
   }
 };
@@ -71,63 +61,58 @@ __global__ void __launch_bounds__(kCombineRows * NVB * 16) tree_combine_kernel(c
   const int groups = 128 / kCombineRows;
   const int group = blockIdx.x % groups, g = blockIdx.y, lane = threadIdx.x & 31;
   int w = blockIdx.x / groups;  // Q tile of the call
-  long long base = 0;           // items before its sequence
+  long long all = 0, first = 0;  // tiles of keys of the call; of the sequences before this one
   int s = -1, tile = 0;
-  for (int q0 = 0; q0 < wk.rows.num_seqs && s < 0; q0 += 32) {
+  for (int q0 = 0; q0 < wk.rows.num_seqs; q0 += 32) {
     const int q = q0 + lane;
     int tiles = 0, r, p, row0;
-    long long weight = 0;
+    long long mine = 0;
     if (q < wk.rows.num_seqs && wk.bounds(q, r, p, row0)) {
       tiles = (r - 1) / wk.tok_tile + 1;
-      weight = wk.weight(q, false);
+      mine = (long long)wk.q_pairs(r) * wk.hkv * (kStart + wk.key_tiles(q));
     }
-    int inc = tiles;
-    long long upto = weight;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, inc, o);
-      const long long u = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) {
-        inc += v;
-        upto += u;
+    const long long sum = warp_prefix(mine);
+    if (s < 0) {
+      const int inc = (int)warp_prefix(tiles), total = __shfl_sync(0xffffffffu, inc, 31);
+      if (w < total) {
+        const int at = __ffs(__ballot_sync(0xffffffffu, inc > w)) - 1;
+        s = q0 + at;
+        tile = w - __shfl_sync(0xffffffffu, inc - tiles, at);
+        first = all + __shfl_sync(0xffffffffu, sum - mine, at);
+      } else {
+        w -= total;
       }
     }
-    const int total = __shfl_sync(0xffffffffu, inc, 31);
-    if (w < total) {
-      const int L = __ffs(__ballot_sync(0xffffffffu, inc > w)) - 1;
-      s = q0 + L;
-      tile = w - __shfl_sync(0xffffffffu, inc - tiles, L);
-      base += __shfl_sync(0xffffffffu, upto - weight, L);
-    } else {
-      w -= total;
-      base += __shfl_sync(0xffffffffu, upto, 31);
-    }
+    all += __shfl_sync(0xffffffffu, sum, 31);
   }
   int r, p, row0;
   if (s < 0 || !wk.bounds(s, r, p, row0)) return;
-  const int ni = wk.items(r), splits = tree_splits(p + r, ni * wk.hkv), keys = tree_split_keys(p + r, splits);
-  if (splits == 1 || base + (long long)ni * wk.hkv * splits > wk.part_slots) return;
+  const int item = tile / 2, each = wk.key_tiles(s);
+  const UnitShares u(all, first + ((long long)g * wk.q_pairs(r) + item) * (kStart + each), each, wk.ctas);
+  if (u.from == u.to) return;  // finished by its one CTA
   const int m = group * kCombineRows + threadIdx.x % kCombineRows, c4 = threadIdx.x / kCombineRows;
   const int tok = tile * wk.tok_tile + m / wk.group;
   if (m >= wk.tok_tile * wk.group || tok >= r) return;
-  const int item = tile / 2, row = (tile & 1) * 128 + m;
-  const int seen = p + min(r, (item + 1) * 2 * wk.tok_tile), used = (seen - 1) / keys + 1;  // splits that hold keys of the item
+  const int row = (tile & 1) * 128 + m;
+  const int seen = p + min(r, (item + 1) * 2 * wk.tok_tile);  // keys of the unit
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   float mx = -INFINITY, l = 0.f;
   constexpr int kAhead = 8;
-  for (int i0 = 0; i0 < used; i0 += kAhead) {
+  for (int c0 = u.from; c0 <= u.to; c0 += kAhead) {
     float2 ml[kAhead];
     float4 x[kAhead];
+    int n = 0;
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      if (i0 + j >= used) break;
-      const long long part = base + ((long long)(i0 + j) * wk.hkv + g) * ni + item;
+      if (c0 + j > u.to || u.start(c0 + j) * pairs::kKeys >= seen) break;
+      const long long part = u.part(c0 + j);
       ml[j] = __ldcg(reinterpret_cast<const float2*>(wk.part_ml) + part * 256 + row);
       x[j] = __ldcg(reinterpret_cast<const float4*>(wk.part_o) + (part * (NVB * 16) + c4) * 256 + row);
+      n = j + 1;
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      if (i0 + j >= used) break;
+      if (j >= n) break;
       const float mn = fmaxf(mx, ml[j].x), z = mn == -INFINITY ? 0.f : mn;
       const float k0 = ex2_approx(mx - z), k1 = ex2_approx(ml[j].x - z);
       v.x = v.x * k0 + x[j].x * k1;
@@ -148,12 +133,12 @@ __global__ void __launch_bounds__(kCombineRows * NVB * 16) tree_combine_kernel(c
 }
 
 template <typename T, int NB, bool kPaged>
-cudaError_t launch_t(const RowsAttnArgs& a, const TreePlan& p, int dtype, cudaStream_t st) {
+cudaError_t launch_t(const RowsAttnArgs& a, int dtype, cudaStream_t st) {
   TreeWork<kPaged> wk;
   wk.hq = a.hq;
   wk.hkv = a.hkv;
   wk.group = a.group;
-  wk.tok_tile = p.tok_tile;
+  wk.tok_tile = a.tok_tile;
   wk.scale_log2 = a.scale_log2;
   wk.rows = a.rows;
   wk.total_rows = a.total_rows;
@@ -169,49 +154,48 @@ cudaError_t launch_t(const RowsAttnArgs& a, const TreePlan& p, int dtype, cudaSt
   wk.parents = a.parents;
   wk.past = a.past;
   wk.max_ctx = a.max_ctx;
-  wk.part_slots = p.slots;
+  wk.ctas = a.ctas;
   pairs::Maps tm;
   const CacheView& c = a.cache;
   const uint64_t slots = kPaged ? c.page_size : c.capacity, planes = (uint64_t)(kPaged ? c.num_pages : a.rows.num_seqs) * a.hkv;
   const uint32_t box = kPaged ? c.page_size : pairs::kKeys;
-  if (!encode_3d(&tm.q, dtype, a.q, a.dqk, a.hq, a.total_rows, 64, a.group, p.tok_tile) ||
+  if (!encode_3d(&tm.q, dtype, a.q, a.dqk, a.hq, a.total_rows, 64, a.group, a.tok_tile) ||
       !encode_3d(&tm.k, dtype, a.k, a.dqk, slots, planes, 64, box, 1) ||
       !encode_3d(&tm.v, dtype, a.v, a.dv, slots, planes, 64, box, 1))
     return cudaErrorInvalidValue;
   tm.kr = tm.k;
-  cudaError_t e = pairs::launch<T, NB, NB>(tm, wk, p.items, st);
-  if (e != cudaSuccess || p.max_splits == 1) return e;
-  const dim3 grid((unsigned)(p.tiles * (128 / kCombineRows)), a.hkv);
+  cudaError_t e = pairs::launch<T, NB, NB>(tm, wk, a.ctas, st);
+  if (e != cudaSuccess || !a.split) return e;
+  const dim3 grid((unsigned)(a.tiles * (128 / kCombineRows)), a.hkv);
   return launch_pdl(tree_combine_kernel<T, NB, kPaged>, grid, dim3(kCombineRows * NB * 16), 0, st, wk);
 }
 
 template <typename T>
-cudaError_t launch_type(const RowsAttnArgs& a, const TreePlan& p, int dtype, cudaStream_t st) {
+cudaError_t launch_type(const RowsAttnArgs& a, int dtype, cudaStream_t st) {
   const bool paged = a.cache.kind == CP_CACHE_PAGED;
-  if (a.dv == 64) return paged ? launch_t<T, 1, true>(a, p, dtype, st) : launch_t<T, 1, false>(a, p, dtype, st);
-  return paged ? launch_t<T, 2, true>(a, p, dtype, st) : launch_t<T, 2, false>(a, p, dtype, st);
+  if (a.dv == 64) return paged ? launch_t<T, 1, true>(a, dtype, st) : launch_t<T, 1, false>(a, dtype, st);
+  return paged ? launch_t<T, 2, true>(a, dtype, st) : launch_t<T, 2, false>(a, dtype, st);
 }
 
 }  // namespace
 
-TreePlan tree_plan(int hq, int hkv, int dv, bool uniform, long long num_seqs, long long total_rows, int max_ctx) {
-  TreePlan p;
-  const int group = hq / hkv;
+RowsPlan tree_plan(int hq, int hkv, int dv, bool uniform, long long num_seqs, long long total_rows, int max_ctx) {
+  RowsPlan p{};
+  const int group = hq / hkv, key_tiles = (max_ctx - 1) / pairs::kKeys + 1;
   p.tok_tile = 128 / group;
   const long long rows = std::min<long long>(uniform ? total_rows / num_seqs : total_rows, CP_TREE_MAX);
   const long long each = (rows + p.tok_tile - 1) / p.tok_tile;  // Q tiles of a sequence, at most
   p.tiles = uniform ? num_seqs * each : std::min(total_rows / p.tok_tile + num_seqs, num_seqs * each);
-  const long long most = uniform ? num_seqs * ((each + 1) / 2) : std::min(total_rows / (2 * p.tok_tile) + num_seqs, num_seqs * ((each + 1) / 2));
-  p.max_splits = tree_max_splits(max_ctx, hkv);
-  // A sequence's items: its pairs times KV heads, or, split, no more than kTreeItems.
-  p.items = std::min(most * hkv * p.max_splits, most * hkv + num_seqs * kTreeItems);
-  p.slots = p.max_splits == 1 ? 0 : p.items;
-  p.bytes = (double)p.slots * 256 * (dv + 2) * sizeof(float);
+  p.work = (double)p.tiles * hkv * (kStart + key_tiles);
+  p.ctas = (int)std::min<double>(p.work, kSms);
+  p.split = key_tiles > 1;
+  p.part_floats = p.split ? 2LL * kSms * 256 * dv : 0;
+  p.bytes = p.split ? 2LL * kSms * 256 * (dv + 2) * (long long)sizeof(float) : 0;
   return p;
 }
 
-cudaError_t launch_tree(const RowsAttnArgs& a, const TreePlan& p, int dtype, cudaStream_t st) {
-  return dtype == CP_BF16 ? launch_type<__nv_bfloat16>(a, p, dtype, st) : launch_type<__half>(a, p, dtype, st);
+cudaError_t launch_tree(const RowsAttnArgs& a, int dtype, cudaStream_t st) {
+  return dtype == CP_BF16 ? launch_type<__nv_bfloat16>(a, dtype, st) : launch_type<__half>(a, dtype, st);
 }
 
 }  // namespace cp

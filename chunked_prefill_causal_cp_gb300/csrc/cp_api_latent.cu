@@ -60,18 +60,11 @@ int rows_attention(const cp_layer_desc* d, bool latent, int dqk, int dv, float s
   if (d->num_q_heads > 65535 || (int64_t)total_rows * d->num_q_heads > INT32_MAX / 4) return CP_ERR_UNSUPPORTED;
   const int64_t pairs = (int64_t)total_rows * d->num_q_heads;
   if (overlap(out, pairs * dv * 2, q, pairs * dqk * 2)) return CP_ERR_INVALID_ARG;
-  RowsPlan p{};
-  TreePlan tp{};
-  if (latent) {
-    p = rows_plan(d->num_q_heads, dv, cu_rows == nullptr, num_seqs, total_rows, max_ctx);
-    if ((double)p.tiles * p.max_splits > INT32_MAX || (double)p.tiles * 64 > INT32_MAX || p.slots > INT32_MAX)
-      return CP_ERR_UNSUPPORTED;
-  } else {
-    tp = tree_plan(d->num_q_heads, d->num_kv_heads, dv, cu_rows == nullptr, num_seqs, total_rows, max_ctx);
-    if (tp.items > INT32_MAX || tp.tiles > INT32_MAX / 16) return CP_ERR_UNSUPPORTED;
-  }
-  const double need = latent ? p.bytes : tp.bytes;
-  if (need > 0 && (!workspace || !aligned16(workspace) || (double)workspace_bytes < need)) return CP_ERR_WORKSPACE;
+  const bool uniform = cu_rows == nullptr;
+  const RowsPlan p = latent ? latent_plan(d->num_q_heads, dv, uniform, num_seqs, total_rows, max_ctx)
+                            : tree_plan(d->num_q_heads, d->num_kv_heads, dv, uniform, num_seqs, total_rows, max_ctx);
+  if (p.tiles > INT32_MAX / 64 || p.work > 1e15) return CP_ERR_UNSUPPORTED;  // sums times CTAs stay within 64 bits
+  if (p.bytes > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < (size_t)p.bytes)) return CP_ERR_WORKSPACE;
   RowsAttnArgs a;
   std::memset(&a, 0, sizeof(a));
   a.hq = d->num_q_heads;
@@ -91,25 +84,21 @@ int rows_attention(const cp_layer_desc* d, bool latent, int dqk, int dv, float s
   a.v = v;
   a.out = out;
   a.status = dev_status;
-  a.part_o = static_cast<float*>(workspace);
-  if (!latent) {
-    a.part_ml = a.part_o + tp.slots * 256 * dv;
-    return launch_result(launch_tree(a, tp, d->dtype, static_cast<cudaStream_t>(stream)));
-  }
+  a.ctas = p.ctas;
   a.q_rows = p.q_rows;
-  a.tiles_bound = (int)p.tiles;
-  a.max_splits = p.max_splits;
-  a.part_slots = (int)p.slots;
-  a.part_ml = a.part_o + (long long)p.part_floats;
-  return launch_result(launch_rows_attn(a, d->dtype, static_cast<cudaStream_t>(stream)));
+  a.tok_tile = p.tok_tile;
+  a.tiles = p.tiles;
+  a.split = p.split;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = a.part_o + p.part_floats;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return launch_result(latent ? launch_latent(a, d->dtype, st) : launch_tree(a, d->dtype, st));
 }
 
 size_t rows_workspace(const cp_layer_desc* d, bool latent, int dv, int32_t total_rows, int32_t max_ctx, int32_t num_seqs) {
   if (total_rows <= 0 || max_ctx <= 0 || num_seqs <= 0) return 0;
-  // Ragged rows: no call of equal rows within the bounds has more tiles.
-  const double bytes = latent ? rows_plan(d->num_q_heads, dv, false, num_seqs, total_rows, max_ctx).bytes
-                              : tree_plan(d->num_q_heads, d->num_kv_heads, dv, false, num_seqs, total_rows, max_ctx).bytes;
-  return bytes < 4e18 ? (size_t)bytes : SIZE_MAX;
+  return (size_t)(latent ? latent_plan(d->num_q_heads, dv, false, num_seqs, total_rows, max_ctx).bytes
+                         : tree_plan(d->num_q_heads, d->num_kv_heads, dv, false, num_seqs, total_rows, max_ctx).bytes);
 }
 
 int tree_check(const cp_layer_desc* d) {

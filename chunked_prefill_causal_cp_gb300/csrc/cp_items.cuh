@@ -5,7 +5,7 @@
 #include <cstdint>
 #include <type_traits>
 
-#include "cp_internal.h"
+#include "cp_latent.h"
 #include "cp_rows.cuh"
 
 namespace cp {
@@ -48,24 +48,34 @@ __device__ __forceinline__ uint32_t even_bits(uint32_t x) {
   return (x | x >> 8) & 0xffffu;
 }
 
-// This CTA's items, in order: of all items, numbered over the sequences, those at
-// blockIdx.x, then back and forth in rounds of gridDim.x, so that a CTA with a heavy item
-// in one round has a light one in the next.  A whole warp asks.
+// ---- which items a persistent CTA takes.  A whole warp asks; a lane has the numbers of one of
+// 32 sequences at a time.
+
+// An inclusive prefix sum over the lanes of a warp.
+__device__ __forceinline__ long long warp_prefix(long long v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+// Items by their numbers over the sequences, weight(s) of sequence s (0: it is skipped), of
+// which make(s, i, x) describes the i-th: those at blockIdx.x, then back and forth in
+// rounds of gridDim.x, so that a CTA with a heavy item in one round has a light one in
+// the next.
 template <typename Work>
-struct ItemCursor {
+struct TurnCursor {
   long long base = 0;      // items of the chunks of 32 sequences before
   int q0 = 0, round = 0;
   long long weight, upto;  // of this lane's sequence; items of the chunk up to and including it
-  __device__ __forceinline__ explicit ItemCursor(const Work& wk) { load(wk); }
+  __device__ __forceinline__ explicit TurnCursor(const Work& wk) { load(wk); }
   __device__ __forceinline__ void load(const Work& wk) {
-    const int lane = threadIdx.x & 31;
-    weight = q0 + lane < wk.rows.num_seqs ? wk.weight(q0 + lane, blockIdx.x == 0) : 0;
-    upto = weight;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += v;
-    }
+    const int s = q0 + (threadIdx.x & 31);
+    weight = s < wk.rows.num_seqs ? wk.weight(s, blockIdx.x == 0) : 0;
+    upto = warp_prefix(weight);
   }
   template <typename Item>
   __device__ __forceinline__ bool next(const Work& wk, Item& x) {
@@ -78,11 +88,97 @@ struct ItemCursor {
         if (q0 >= wk.rows.num_seqs) return false;
         load(wk);
       }
-      const int L = __ffs(__ballot_sync(0xffffffffu, upto > r - base)) - 1;
+      const int at = __ffs(__ballot_sync(0xffffffffu, upto > r - base)) - 1;
       ++round;
-      if (wk.make(q0 + L, r - base - __shfl_sync(0xffffffffu, upto - weight, L), r, x)) return true;
+      if (wk.make(q0 + at, r - base - __shfl_sync(0xffffffffu, upto - weight, at), x)) return true;
     }
   }
 };
+
+// This CTA's share of the call's tiles of keys (see cp_latent.h), unit by unit: sequence s has
+// units(s) (0: it is skipped) of key_tiles(s) tiles each; make(s, unit, k0, n, x) describes n
+// tiles of one from tile k0 on.
+template <typename Work>
+struct ShareCursor {
+  long long base = 0;         // of the chunks of 32 sequences before; counted in tiles, kStart a unit among them
+  long long at, end;          // next, the share's end
+  int q0 = 0;
+  long long sum;              // of this lane's sequence: the chunk's up to and including it,
+  int each;                   // of a unit,
+  long long mine;             // of the sequence
+  __device__ __forceinline__ explicit ShareCursor(const Work& wk) {
+    long long all = 0;
+    for (; q0 < wk.rows.num_seqs; q0 += 32) {
+      load(wk, blockIdx.x == 0);
+      all += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    const Shares shares(all, gridDim.x);
+    const int c = min((int)blockIdx.x, shares.ctas);
+    at = shares.begin(c);
+    end = shares.begin(min(c + 1, shares.ctas));
+    const bool again = q0 > 32;  // else the one chunk is here
+    q0 = 0;
+    if (again) load(wk, false);
+  }
+  __device__ __forceinline__ void load(const Work& wk, bool report) {
+    const int s = q0 + (threadIdx.x & 31);
+    const int units = s < wk.rows.num_seqs ? wk.units(s, report) : 0;
+    each = units > 0 ? kStart + wk.key_tiles(s) : 1;
+    mine = (long long)units * each;
+    sum = warp_prefix(mine);
+  }
+  template <typename Item>
+  __device__ __forceinline__ bool next(const Work& wk, Item& x) {
+    while (at < end) {
+      const uint32_t some = __ballot_sync(0xffffffffu, base + sum > at);
+      if (!some) {
+        base += __shfl_sync(0xffffffffu, sum, 31);
+        q0 += 32;
+        if (q0 >= wk.rows.num_seqs) return false;
+        load(wk, false);
+        continue;
+      }
+      const int lane = __ffs(some) - 1, n = __shfl_sync(0xffffffffu, each, lane);
+      const long long off = at - base - __shfl_sync(0xffffffffu, sum - mine, lane), unit = Shares::quotient(off, n);
+      const int o = (int)(off - unit * n), len = (int)min((long long)(n - o), end - at);
+      const int k0 = max(o - kStart, 0), k1 = max(o + len - kStart, 0);
+      x.whole = k0 == 0 && k1 == n - kStart;
+      x.part = 2 * blockIdx.x + (k0 == 0);
+      at += len;
+      if (k1 > k0 && wk.make(q0 + lane, (int)unit, k0, k1 - k0, x)) return true;
+    }
+    return false;
+  }
+};
+
+// The CTAs of a unit of n tiles, first to last, and the tile of keys from which on each has it.
+struct UnitShares {
+  Shares shares;
+  long long first;  // of its tiles, where the shares count
+  int from, to;
+  __device__ __forceinline__ UnitShares(long long all, long long unit, int n, int grid)
+      : shares(all, grid), first(unit + kStart), from(shares.of(first)), to(shares.of(first + n - 1)) {}
+  __device__ __forceinline__ long long start(int c) const { return max(shares.begin(c) - first, 0ll); }
+  __device__ __forceinline__ int part(int c) const { return 2 * c + (shares.begin(c) <= first); }
+};
+
+// A sequence's parents of up to CP_TREE_MAX rows, as bytes: one out of range counts as -1 and sets CP_DEV_BOUNDS.
+__device__ __forceinline__ void load_parents(const int* parents, int rows, int* status, int8_t* to) {
+  for (int m = threadIdx.x & 31; m < rows; m += 32) {
+    int up = parents[m];
+    if (up < -1 || up >= m) {
+      up = -1;
+      if (status) atomicOr(status, CP_DEV_BOUNDS);
+    }
+    to[m] = (int8_t)up;
+  }
+}
+// The rows that row i sees, 128 bits: its ancestors and itself.
+__device__ __forceinline__ void ancestors(const int8_t* parents, int i, uint64_t& lo, uint64_t& hi) {
+  for (int j = i; j >= 0; j = parents[j]) {
+    if (j < 64) lo |= 1ull << j;
+    else hi |= 1ull << (j - 64);
+  }
+}
 
 }  // namespace cp

@@ -31,44 +31,32 @@ struct LatentAppendArgs {
   int* status;
 };
 
-// Splits of a sequence of n positions whose (row, head) pairs make nt tiles, over a latent
-// cache: few keys a split for a short context, where the wait for one CTA's walk is what
-// counts, more for a long one, whose parts cost less then, and no more than kRowsItems
-// (tile, split) items.  By the sequence's own sizes alone, so a row's result never
-// depends on what shares the launch.
-constexpr int kRowsItems = 304;  // twice the SMs
-__host__ __device__ inline int rows_split_base(int n) { return n <= 2048 ? 128 : n <= 8192 ? 256 : n <= 16384 ? 512 : 1024; }
-__host__ __device__ inline int rows_splits(int n, int nt) {
-  const int cap = kRowsItems / nt, k = (n - 1) / rows_split_base(n) + 1;
-  return cap <= 1 ? 1 : k < cap ? k : cap;
-}
-// Keys of each split: whole tiles of 64.
-__host__ __device__ inline int rows_split_keys(int n, int splits) { return ((n - 1) / splits + 64) & ~63; }
-// Most splits of a sequence of up to ctx positions and nt tiles.
-inline int rows_max_splits(int ctx, int nt) {
-  int m = rows_splits(ctx, nt);
-  const int steps[3] = {2048, 8192, 16384};
-  for (int s : steps)
-    if (ctx > s && rows_splits(s, nt) > m) m = rows_splits(s, nt);
-  return m;
-}
-
-// The same for a drafted tree over a K/V cache, nt pairs of Q tiles times KV heads, in
-// whole tiles of 128 keys.
-constexpr int kTreeItems = 152;  // (pair, KV head, split) items of a split sequence, at most: the SMs
-__host__ __device__ inline int tree_split_base(int n) { return n <= 2048 ? 128 : n <= 4096 ? 256 : n <= 8192 ? 512 : n <= 16384 ? 1024 : 2048; }
-__host__ __device__ inline int tree_splits(int n, int nt) {
-  const int cap = kTreeItems / nt, k = (n - 1) / tree_split_base(n) + 1;
-  return cap <= 1 ? 1 : k < cap ? k : cap;
-}
-__host__ __device__ inline int tree_split_keys(int n, int splits) { return ((n - 1) / splits + 128) & ~127; }
-inline int tree_max_splits(int ctx, int nt) {
-  int m = tree_splits(ctx, nt);
-  const int steps[4] = {2048, 4096, 8192, 16384};
-  for (int s : steps)
-    if (ctx > s && tree_splits(s, nt) > m) m = tree_splits(s, nt);
-  return m;
-}
+// How the work of cp_latent_attn and cp_tree_attn is shared out: units -- a tile of pairs, or
+// pair of Q tiles, of a sequence (and KV head), with all its tiles of keys -- lie in a row,
+// which is cut into a share for each CTA, wherever in a unit that is.
+// All CTAs have as much to do, within a tile, whatever the sequences' lengths; a unit
+// that does not end where it began leaves parts, of which a CTA has two at most: of
+// the unit it starts in the middle of, and of the one it does not finish.  (Splits of
+// fixed length, of a sequence's own or by the number of sequences, left the last CTA with
+// 14 to 30% more than the mean, or had as much again in starts, ends and parts.)
+constexpr int kSms = 152;
+constexpr int kStart = 4;  // what the start and end of a unit cost, in tiles
+// The shares of `all` tiles: each CTA's, the first `more` of them one tile longer.
+struct Shares {
+  int ctas;         // that have one: of a grid, at most a CTA for each tile
+  long long least;  // tiles of a share
+  int more;
+  __host__ __device__ Shares(long long all, int grid)
+      : ctas(all < grid ? (all > 1 ? (int)all : 1) : grid), least(quotient(all, ctas)), more((int)(all - least * ctas)) {}
+  __host__ __device__ static long long quotient(long long x, long long y) {  // in 32 bits where they do
+    return ((unsigned long long)(x | y) >> 32) == 0 ? (long long)((unsigned)x / (unsigned)y) : x / y;
+  }
+  __host__ __device__ long long begin(int c) const { return least * c + (c < more ? c : more); }
+  __host__ __device__ int of(long long tile) const {
+    const long long longer = (least + 1) * more;
+    return (int)(tile < longer ? quotient(tile, least + 1) : more + quotient(tile - longer, least));
+  }
+};
 
 // Attention of few rows over a long cache (cp_latent_attn, cp_tree_attn).  A
 // latent cache is one KV head whose group is all heads and whose values are its
@@ -88,36 +76,27 @@ struct RowsAttnArgs {
   const void* v;
   void* out;               // [total_rows, hq, dv]
   int* status;
-  // A latent cache's (cp_latent_attn):
-  int q_rows;              // pairs of a tile that the call can have, at most
-  int tiles_bound;         // tiles of the call, at most
-  int max_splits;          // of any sequence
-  int part_slots;          // parts that the workspace has room for
-  float* part_o;           // [part_slots, 64, dv] unnormalised parts
-  float* part_ml;          // [part_slots, 64, 2] their maximum (log2 domain) and sum
+  // By the host's bounds:
+  int ctas;                // that share the work
+  int q_rows;              // a latent cache's: pairs of a tile that the call can have, at most
+  int tok_tile;            // a tree's: tokens of a Q tile
+  long long tiles;         // of pairs, or Q tiles, at most
+  bool split;              // whether units may be shared by CTAs
+  float* part_o;           // parts: unnormalised outputs,
+  float* part_ml;          // their maximum (log2 domain) and sum
 };
 
 // How such a call runs, from its host bounds.
 struct RowsPlan {
-  int q_rows;
-  long long tiles;         // at most
-  int max_splits;
-  long long slots;         // parts, at most
-  double part_floats;      // of their outputs
-  double bytes;            // of workspace; in floating point: absurd sizes must not wrap
+  int ctas, q_rows, tok_tile;
+  long long tiles;
+  bool split;
+  double work;             // tiles of keys of all units, at most
+  long long part_floats;   // of all parts' outputs
+  long long bytes;         // of workspace
 };
-// How a call of drafted trees over a K/V cache runs.
-struct TreePlan {
-  int tok_tile;            // tokens of a Q tile
-  long long tiles, items;  // Q tiles, items, at most
-  int max_splits;
-  long long slots;         // parts, at most
-  double bytes;
-};
-TreePlan tree_plan(int hq, int hkv, int dv, bool uniform, long long num_seqs, long long total_rows, int max_ctx);
-cudaError_t launch_tree(const RowsAttnArgs& a, const TreePlan& p, int dtype, cudaStream_t st);
-
-RowsPlan rows_plan(int heads, int dv, bool uniform, long long num_seqs, long long total_rows, int max_ctx);
+RowsPlan latent_plan(int heads, int dv, bool uniform, long long num_seqs, long long total_rows, int max_ctx);
+RowsPlan tree_plan(int hq, int hkv, int dv, bool uniform, long long num_seqs, long long total_rows, int max_ctx);
 
 // Attention of chunks over expanded keys and values (cp_latent_chunk_attn).
 struct ExpandedArgs {
@@ -149,7 +128,8 @@ struct CommitArgs {
 };
 
 cudaError_t launch_latent_append(const LatentAppendArgs& a, int dtype, cudaStream_t st);
-cudaError_t launch_rows_attn(const RowsAttnArgs& a, int dtype, cudaStream_t st);
+cudaError_t launch_latent(const RowsAttnArgs& a, int dtype, cudaStream_t st);
+cudaError_t launch_tree(const RowsAttnArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_expanded(const ExpandedArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_tree_commit(const CommitArgs& a, cudaStream_t st);
 

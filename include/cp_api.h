@@ -633,8 +633,10 @@ int cp_latent_append(const cp_latent_desc* desc, const cp_qk_prep* prep, const v
  *                 Calls whose work overlaps on the GPU need separate workspaces
  *   commit        not 0: seqlens_k[s] += rows of s after the attention (with parents:
  *                 CP_ERR_INVALID_ARG; cp_latent_tree_commit advances them)
- * A row's result depends only on its own sequence.  Scores, softmax sums and outputs are
- * held in 32 bits; the softmax's weights are rounded to the layer's type for their
+ * A row's result depends on its own sequence and, in its last bits, on the rows and
+ * positions of the call's other sequences: the keys are shared out over the SMs by
+ * the whole call's sizes (not by its bounds).  Scores, softmax sums and outputs are held in
+ * 32 bits; the softmax's weights are rounded to the layer's type for their
  * product with the latents.  Slots past a sequence's positions may hold anything.  A NaN,
  * or an infinite value (x[0, C), v), makes the rows that see its position non-finite (in
  * its channels or in all), and no other row; an infinite key makes a score infinite: +inf
@@ -691,8 +693,8 @@ int cp_latent_chunk_attn(const cp_latent_desc* desc, const void* q, const void* 
  *   q, out        device [total_rows, Hq, D]
  *   parents       device int32 [total_rows], as in cp_latent_attn; not NULL
  *   workspace     at least cp_workspace_size_tree(...) bytes, as in cp_latent_attn
- * Rows of the sequences, max_ctx, dev_status, results of rows on their own, precision and
- * non-finite values as in cp_latent_attn.  seqlens_k is not modified (cp_tree_commit). */
+ * Rows of the sequences, max_ctx, dev_status, what a row's result depends on, precision
+ * and non-finite values as in cp_latent_attn.  seqlens_k is not modified (cp_tree_commit). */
 int cp_tree_attn(const cp_layer_desc* desc, const void* q, const void* k_cache, const void* v_cache,
                  const int32_t* seqlens_k, const int32_t* block_table, const int32_t* parents, const int32_t* cu_rows,
                  int32_t num_seqs, int32_t total_rows, int32_t max_ctx, void* out, void* workspace,

@@ -181,8 +181,8 @@ BOTH = [dict(heads=16, latent=512, rope=64), dict(heads=8, kv=2, d=128)]
 
 
 @pytest.mark.parametrize("kw", BOTH)
-def test_a_rows_result_is_its_own_sequences(kw):
-    """The same whatever shares the call: alone, in a batch, ragged or of equal rows."""
+def test_a_rows_bits_are_its_own_and_the_sizes(kw):
+    """The same whatever the bounds, rows given as equal or ragged, and the other sequences' values."""
     heads, kw = kw["heads"], {k: v for k, v in kw.items() if k != "heads"}
     n, rows = 12, 13
     past = [0, 5000, 64, 700, 1, 2100, 333, 4096, 90, 17, 3000, 250]
@@ -193,10 +193,29 @@ def test_a_rows_result_is_its_own_sequences(kw):
     out = x.attend(q, past, [rows] * n, parents, uniform=True)
     x.check(q, out, past, [rows] * n, parents)
     assert torch.equal(out, x.attend(q, past, [rows] * n, parents, max_ctx=5200))
-    for s in (0, 1, 5):
-        y = x.empty_out(rows)
-        one = x.attend(q[s * rows:(s + 1) * rows], [past[s]], [rows], [parents[s]], out=y, block_table=x.table[s:s + 1])
-        assert torch.equal(one, out[s * rows:(s + 1) * rows])
+    assert torch.equal(out, x.attend(q, past, [rows] * n, parents))
+    for s in (0, 1, 5, 11):
+        at = slice(s * rows, (s + 1) * rows)
+        other = -q
+        other[at] = q[at]
+        assert torch.equal(x.attend(other, past, [rows] * n, parents)[at], out[at])
+    assert int(x.status) == 0
+
+
+@pytest.mark.parametrize("kw", BOTH)
+@pytest.mark.parametrize("seqs", [1, 2, 40])
+def test_long_contexts_of_few_and_many_sequences(kw, seqs):
+    """Splits of every size: one sequence over all SMs, many sequences of several items each."""
+    heads, kw = kw["heads"], {k: v for k, v in kw.items() if k != "heads"}
+    past = [(7919 * (i + 3)) % 9001 for i in range(seqs)]
+    rows = [1 + (5 * i) % 23 for i in range(seqs)]
+    x = Cache(F16, heads, seqs, 9100, 64, **kw)
+    x.fill([p + r for p, r in zip(past, rows)])
+    q = x.queries(sum(rows))
+    parents = [tree(r, "heap") for r in rows]
+    out = x.attend(q, past, rows, parents)
+    assert int(x.status) == 0
+    x.check(q, out, past, rows, parents)
 
 
 @pytest.mark.parametrize("kw", BOTH)

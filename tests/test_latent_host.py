@@ -109,6 +109,7 @@ def test_attention_refusals(f, desc):
     assert f(desc=desc(**big), table=FAKE, ctx=2 ** 31 - 200) == UNSUP
     assert f(par=FAKE, n=1, t=129) == UNSUP  # a tree's most rows
     assert f(t=2 ** 30) == UNSUP
+    assert f(ctx=1000, ws=None) == WS and f(ctx=1000, ws_bytes=64) == WS and f(ctx=1000, ws=FAKE + 8) == WS
     assert f(t=0) == cp.CP_OK
 
 
@@ -214,17 +215,19 @@ def at(t, shape):
         shape = property(lambda s: t.shape)
         def __getattr__(s, n): return getattr(t, n)
         def get_device(s): return 0
-    return cp._strided_arg("x", T(), D, shape, 0)
+    return cp._rows3_arg("x", T(), D, *shape, 0) if len(shape) == 3 else cp._rows2_arg("x", T(), D, *shape, 0)
 x = torch.zeros(6, 4, 80, dtype=D)
 p = x.data_ptr()
-assert at(x, (6, 4, 80)) == (p, 0, 0)
+assert at(x, (6, 4, 80)) == (p, 320, 80)
 assert at(x[..., 16:], (6, 4, 64)) == (p + 32, 320, 80)
 assert at(x[:1, :, 16:], (1, 4, 64)) == (p + 32, 320, 80)
 assert at(x[:, :1, 16:], (6, 1, 64))[1:] == (320, 64)
+assert at(x[:, 0], (6, 80)) == (p, 320) and at(x[:1, 0, 8:40], (1, 32)) == (p + 16, 32)
 assert at(x[::2], (3, 4, 80)) == (p, 640, 80)
-assert at(x[:0], (0, 4, 80))[1:] == (0, 0)
+assert at(x[:0], (0, 4, 80))[1:] == (320, 80) and at(x[:0, 0], (0, 80))[1:] == (80,)
 bad = [(x, (6, 4, 64)), (x.transpose(0, 1), (4, 6, 80)), (x[..., ::2], (6, 4, 40)), (x[:, :1].expand(6, 4, 80), (6, 4, 80)),
-       (x[:1].expand(6, 4, 80), (6, 4, 80)), (x.float(), (6, 4, 80))]
+       (x[:1].expand(6, 4, 80), (6, 4, 80)), (x.float(), (6, 4, 80)), (x[:1, 0].expand(6, 80), (6, 80)), (x[0].T, (80, 4)),
+       (x[:, 0, ::2], (6, 40)), (x[:, 0], (6, 64))]
 for t, shape in bad:
     try:
         at(t, shape)
