@@ -56,9 +56,8 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kTile = 64;                 // keys of a tile
 constexpr uint32_t kBlock = kTile * 128;  // bytes of 64 keys x 64 channels
-constexpr int kMaxStages = 6;
+constexpr int kMaxSlots = 8;
 constexpr int kPairs = 64;                // (row, head) pairs of a tile
-constexpr int kGroups = 2;                // of a stage's blocks, at most
 constexpr uint32_t kSmem = 232448;        // of a CTA, at most
 constexpr float kRescaleLog2 = 8.0f;
 
@@ -74,7 +73,7 @@ struct Item {
 };
 
 struct __align__(16) Shared {
-  uint64_t item_full[2], item_empty[2], q_full, q_empty, full[kMaxStages][kGroups], empty[kMaxStages][kGroups], s_full[2],
+  uint64_t item_full[2], item_empty[2], q_full, q_empty, full[kMaxSlots], empty[kMaxSlots], s_full[2],
       p_ready, pv_done, o_free, all_done;
   uint32_t tmem_base;
   int abort;
@@ -94,25 +93,34 @@ struct __align__(16) Shared {
 };
 static_assert(offsetof(Shared, alpha) % 16 == 0, "the factors are read four at a time");
 
-// Shared memory: Q, stages, P, Shared.
+// Shared memory: Q, slots of a group of blocks each, slots of a tile's rotated part, P, Shared.
 struct Layout {
-  uint32_t stage_bytes, p_off, ctl_off, alloc;
+  uint32_t q_block, slot_bytes, slots_off, rot_off, p_off, ctl_off, alloc;
   int nqb, nvb;             // blocks of 64 channels: of a row, of its value
-  int ngroups, stages;
+  int ngroups, slots, rot_slots;
 };
 
-Layout layout_of(int dqk, int dv) {
+Layout layout_of(int dqk, int dv, int q_rows) {
   Layout l;
   l.nqb = (dqk + 63) / 64;
   l.nvb = dv / 64;
   l.ngroups = (l.nvb + 3) / 4;
-  l.stage_bytes = (uint32_t)l.nqb * kBlock;
-  const uint32_t q = (uint32_t)l.nqb * kPairs * 128, fixed = q + kPairs * 128 + (uint32_t)sizeof(Shared);
-  l.stages = std::min<int>((kSmem - fixed) / l.stage_bytes, kMaxStages);
-  l.p_off = q + l.stages * l.stage_bytes;
-  l.ctl_off = l.p_off + kPairs * 128;
-  l.alloc = l.ctl_off + (uint32_t)sizeof(Shared);
-  return l;
+  // Rows of Q and P: those that the MMAs' N has.  An MMA's 64 rows of Q go on into what lies
+  // behind them, of no pair.
+  const uint32_t rows = (uint32_t)(q_rows + 15) / 16 * 16;
+  l.q_block = rows * 128;
+  l.slot_bytes = (uint32_t)std::min(l.nvb, 4) * kBlock;
+  l.slots_off = l.nqb * l.q_block;
+  // A group's slot is free again after the output of the tile that had it, and with it the
+  // rotated parts of all tiles before: as many as begin in the other slots.
+  for (l.slots = kMaxSlots;; --l.slots) {
+    l.rot_slots = l.nqb > l.nvb ? (l.slots + l.ngroups - 1) / l.ngroups : 0;
+    l.rot_off = l.slots_off + l.slots * l.slot_bytes;
+    l.p_off = l.rot_off + l.rot_slots * kBlock;
+    l.ctl_off = l.p_off + l.q_block;
+    l.alloc = l.ctl_off + (uint32_t)sizeof(Shared);
+    if (l.alloc <= kSmem) return l;
+  }
 }
 
 // The call's units: tiles of pairs of each sequence.
@@ -146,14 +154,14 @@ struct Work : RowsAttnArgs {
   }
 };
 
-// A place in the ring of stages, and how often it came round (divisions by the number of stages, made where the MMAs
+// A place in the ring of slots, and how often it came round (divisions by the number of slots, made where the MMAs
 // are issued, took longer than the MMAs).
 struct Ring {
-  int stage = 0;
+  int slot = 0;
   uint32_t turn = 0;  // parity
-  __device__ __forceinline__ void advance(int stages) {
-    if (++stage == stages) {
-      stage = 0;
+  __device__ __forceinline__ void advance(int slots) {
+    if (++slot == slots) {
+      slot = 0;
       turn ^= 1u;
     }
   }
@@ -175,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const Work a, const Layout L) {
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* sStage = smem + (uint32_t)L.nqb * kPairs * 128;
+  uint8_t* sSlot = smem + L.slots_off;
   uint8_t* sP = smem + L.p_off;
   Shared* sh = reinterpret_cast<Shared*>(smem + L.ctl_off);
 
@@ -190,11 +198,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&sh->q_full, 1);
     mbar_init(&sh->q_empty, 1);
-    for (int i = 0; i < L.stages; ++i)
-      for (int j = 0; j < kGroups; ++j) {
-        mbar_init(&sh->full[i][j], 1);
-        mbar_init(&sh->empty[i][j], 1);
-      }
+    for (int i = 0; i < L.slots; ++i) {
+      mbar_init(&sh->full[i], 1);
+      mbar_init(&sh->empty[i], 1);
+    }
     mbar_init(&sh->p_ready, 256);
     mbar_init(&sh->pv_done, 1);
     mbar_init(&sh->o_free, 256);
@@ -224,9 +231,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     x = sh->item[k & 1];
     return x.ntiles >= 0;
   };
-  // A group's blocks: values four at a time; the first group also has the rotated part, behind them all.
-  auto group_blocks = [&](int j) { return min(4, L.nvb - 4 * j) + (j == 0 ? L.nqb - L.nvb : 0); };
-  auto block_of = [&](int j, int e) { return j == 0 && e >= min(4, L.nvb) ? L.nvb : 4 * j + e; };
   pdl_wait();  // everything below reads what earlier kernels wrote
 
   if (warp == 2) {
@@ -256,9 +260,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ================================================================ producer
     const int ps = kPaged ? min(a.cache.page_size, kTile) : kTile, lps = kPaged ? 31 - __clz(a.cache.page_size) : 0;
     const int npg = kTile / ps;  // boxes of a block
-    Ring ring;
-    int gt = 0, queries = 0;     // tiles, items' queries issued so far
-    uint32_t begun = 0, phase = 0;  // bit kGroups * stage + group: any copy begun, parity of their number
+    Ring ring, rot;
+    int groups = 0, queries = 0;    // groups, items' queries issued so far
+    uint32_t begun = 0, phase = 0;  // bit of a slot: any copy begun, parity of their number
     bool ok = true;
     Item x;
     for (int k = 0; ok && take(k, x); ++k) {
@@ -267,12 +271,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       if (lane == 0) {
         mbar_arrive_expect_tx(&sh->q_full, L.nqb * a.q_rows * 128);
-        for (int b = 0; b < L.nqb; ++b) tma_load_3d(smem + b * kPairs * 128, &tm_q, &sh->q_full, b * 64, x.row0 * a.hq + x.first, 0);
+        for (int b = 0; b < L.nqb; ++b) tma_load_3d(smem + b * L.q_block, &tm_q, &sh->q_full, b * 64, x.row0 * a.hq + x.first, 0);
       }
       __syncwarp();
       queries = k + 1;
-      for (int i = 0; ok && i < x.ntiles; ++i, ++gt, ring.advance(L.stages)) {
-        const int st = ring.stage;
+      for (int i = 0; ok && i < x.ntiles; ++i, rot.advance(L.rot_slots)) {
         const int j0 = x.j_begin + i * kTile;
         // This lane's boxes: idx = lane, lane + 32, ...: page idx % npg of block idx / npg.
         int plane = x.s, off = j0;
@@ -286,18 +289,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           off = key & (a.cache.page_size - 1);
         }
-        for (int j = 0; ok && j < L.ngroups; ++j) {
-          if (gt >= L.stages) ok = wait(&sh->empty[st][j], ring.turn ^ 1);
+        for (int j = 0; ok && j < L.ngroups; ++j, ++groups, ring.advance(L.slots)) {
+          const int st = ring.slot, nv = min(4, L.nvb - 4 * j);
+          if (groups >= L.slots) ok = wait(&sh->empty[st], ring.turn ^ 1);
           if (!ok) break;
-          const int nb = group_blocks(j);
-          begun |= 1u << (kGroups * st + j);
-          phase ^= 1u << (kGroups * st + j);
-          if (lane == 0) mbar_arrive_expect_tx(&sh->full[st][j], nb * kBlock);
+          const int nb = nv + (j == 0 ? L.nqb - L.nvb : 0);  // the first group also has the rotated part
+          begun |= 1u << st;
+          phase ^= 1u << st;
+          if (lane == 0) mbar_arrive_expect_tx(&sh->full[st], nb * kBlock);
           __syncwarp();
           for (int idx = lane; idx < npg * nb; idx += 32) {  // npg divides 32: the page stays the lane's
-            const int b = block_of(j, idx / npg);
-            tma_load_3d(sStage + st * L.stage_bytes + b * kBlock + (idx % npg) * ps * 128, &tm_k, &sh->full[st][j], b * 64, off,
-                        plane);
+            const int e = idx / npg;
+            uint8_t* to = e < nv ? sSlot + st * L.slot_bytes + e * kBlock : smem + L.rot_off + rot.slot * kBlock;
+            tma_load_3d(to + (idx % npg) * ps * 128, &tm_k, &sh->full[st], (e < nv ? 4 * j + e : L.nvb) * 64, off, plane);
           }
         }
       }
@@ -305,28 +309,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Every copy has landed before shared memory is released, also after an abort.
     volatile int zero = 0;
     if (queries > 0) mbar_wait(&sh->q_full, (queries - 1) & 1, &zero, a.status);
-    for (int i = 0; i < kMaxStages * kGroups; ++i)
-      if ((begun >> i) & 1) mbar_wait(&sh->full[i / kGroups][i % kGroups], ((phase >> i) & 1) ^ 1, &zero, a.status);
+    for (int i = 0; i < kMaxSlots; ++i)
+      if ((begun >> i) & 1) mbar_wait(&sh->full[i], ((phase >> i) & 1) ^ 1, &zero, a.status);
     __syncwarp();
   } else if (warp == 1) {
     // ================================================================ MMA issuer
     // The whole warp runs the loop, converged; one elected lane issues.  What addresses come from is broadcast.
     auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
     const uint32_t tm = (uint32_t)uniform((int)tmem);
-    constexpr uint32_t kQStep = kPairs * 8, kKStep = kBlock >> 4;  // of a descriptor: 16 bytes
+    constexpr uint32_t kKStep = kBlock >> 4;  // of a descriptor: 16 bytes
+    const uint32_t q_step = L.q_block >> 4;
     constexpr uint32_t kIdescQK = make_idesc_f16(kBf16, 64, kTile, false);
     const uint64_t q_desc = make_sdesc_sw128(smem_u32(smem), 16, 1024);
-    const uint64_t v_desc = make_sdesc_sw128(smem_u32(sStage), kBlock, 1024);
+    const uint64_t v_desc = make_sdesc_sw128(smem_u32(sSlot), kBlock, 1024);
     const uint32_t q_lo = (uint32_t)q_desc, k_hi = (uint32_t)(q_desc >> 32);  // Q, K and P differ in their addresses only
-    const uint32_t k_lo = (uint32_t)make_sdesc_sw128(smem_u32(sStage), 16, 1024);
+    const uint32_t k_lo = (uint32_t)make_sdesc_sw128(smem_u32(sSlot), 16, 1024);
+    const uint32_t r_lo = (uint32_t)make_sdesc_sw128(smem_u32(smem) + L.rot_off, 16, 1024);
     const uint32_t p_lo = (uint32_t)make_sdesc_sw128(smem_u32(sP), 16, 1024);
-    const uint32_t v_lo = (uint32_t)v_desc, v_hi = (uint32_t)(v_desc >> 32), stage_step = L.stage_bytes >> 4;
+    const uint32_t v_lo = (uint32_t)v_desc, v_hi = (uint32_t)(v_desc >> 32), slot_step = L.slot_bytes >> 4;
     const int nvb = L.nvb;
     const bool rotated = L.nqb > nvb;
     // Scores over n blocks from Q at q, K at kd on; `acc`: added to what is there.
     auto scores = [&](int n, uint32_t d, uint32_t q, uint32_t kd, uint32_t acc) {
 #pragma unroll 1
-      for (int b = 0; b < n; ++b, q += kQStep, kd += kKStep, acc = 1)
+      for (int b = 0; b < n; ++b, q += q_step, kd += kKStep, acc = 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) mma_ss_lo(d, q + 2 * e, k_hi, kd + 2 * e, k_hi, kIdescQK, e ? 1u : acc);
     };
@@ -338,30 +344,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 4; ++e) mma_ss_lo(d, vd + 128 * e, v_hi, p_lo + 2 * e, k_hi, idesc, e ? 1u : acc);
     };
     const int v0 = min(nvb, 4), v1 = nvb - v0;  // blocks of values in the two groups
-    Ring qk, pv;           // of the tile whose scores, whose output is issued next
+    Ring qk, pv, rot;      // of the group (tile) whose scores, whose output is issued next
     uint32_t s_buf = 0;    // S of the next scores
     uint32_t p_phase = 0;  // parity of the next P
     bool ok = true;
+    auto ready = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test(b, parity)); };
     // Group j of the next tile's scores.
     auto group = [&](int j) {
-      if (!wait(&sh->full[qk.stage][j], qk.turn)) return false;
+      if (!wait(&sh->full[qk.slot], qk.turn)) return false;
       tc_fence_after();
-      const uint32_t d = tm + 64u * s_buf, kd = k_lo + qk.stage * stage_step;
+      const uint32_t d = tm + 64u * s_buf, kd = k_lo + qk.slot * slot_step;
       if (j == 0) {
         scores(v0, d, q_lo, kd, 0);
-        if (rotated) scores(1, d, q_lo + nvb * kQStep, kd + nvb * kKStep, 1);
+        if (rotated) scores(1, d, q_lo + nvb * q_step, r_lo + rot.slot * kKStep, 1);
+        rot.advance(L.rot_slots);
       } else {
-        scores(v1, d, q_lo + 4 * kQStep, kd + 4 * kKStep, 1);
+        scores(v1, d, q_lo + 4 * q_step, kd, 1);
       }
+      qk.advance(L.slots);
       if (j + 1 == L.ngroups) {
         mma_commit_elect(&sh->s_full[s_buf]);
         s_buf ^= 1u;
-        qk.advance(L.stages);
       }
       return true;
     };
-    // With two stages the second group comes after the output that gave it room.
-    const int early = L.stages > 2 ? L.ngroups : 1;
+    // With room for two tiles only the second group comes after the output that gave it its slot.
+    const int early = L.slots > 2 * L.ngroups ? L.ngroups : 1;
     for (int k = 0; ok; ++k) {
       if (!wait(&sh->item_full[k & 1], (k >> 1) & 1)) break;
       const int ntiles = uniform(sh->item[k & 1].ntiles);
@@ -373,22 +381,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ntiles == 1) mma_commit_elect(&sh->q_empty);
       for (int i = 0; ok && i < ntiles; ++i) {
         const bool more = i + 1 < ntiles;
-        for (int j = 0; ok && more && j < early; ++j) ok = group(j);
+        int next = 0;  // group of the next tile's scores
+        for (; ok && more && next < early; ++next) {
+          // Where the keys are late and P is there, P's product comes first: it frees the slots that the next keys wait for.
+          bool product = false;
+          for (int n = 0; n < 4096 && !product && !ready(&sh->full[qk.slot], qk.turn); ++n) product = ready(&sh->p_ready, p_phase);
+          if (product) break;
+          ok = group(next);
+        }
         ok = ok && wait(&sh->p_ready, p_phase);
         if (ok && i == 0 && k > 0) ok = wait(&sh->o_free, (k - 1) & 1);  // the item before has left O
         if (!ok) break;
         p_phase ^= 1u;
         tc_fence_after();
-        const uint32_t vd = v_lo + pv.stage * stage_step, d = tm + 128u, acc = i > 0;
-        output(v0 / 2, d, vd, idesc_pv, acc);
-        mma_commit_elect(&sh->empty[pv.stage][0]);
+        const uint32_t d = tm + 128u, acc = i > 0;
+        output(v0 / 2, d, v_lo + pv.slot * slot_step, idesc_pv, acc);
+        mma_commit_elect(&sh->empty[pv.slot]);
+        pv.advance(L.slots);
         if (v1 > 0) {
-          output(v1 / 2, d + 2 * kPairs, vd + 4 * kKStep, idesc_pv, acc);
-          mma_commit_elect(&sh->empty[pv.stage][1]);
+          output(v1 / 2, d + 2 * kPairs, v_lo + pv.slot * slot_step, idesc_pv, acc);
+          mma_commit_elect(&sh->empty[pv.slot]);
+          pv.advance(L.slots);
         }
         mma_commit_elect(&sh->pv_done);
-        pv.advance(L.stages);
-        for (int j = early; ok && more && j < L.ngroups; ++j) ok = group(j);
+        for (; ok && more && next < L.ngroups; ++next) ok = group(next);
         if (i + 2 == ntiles) mma_commit_elect(&sh->q_empty);  // the item's last scores are issued
       }
     }
@@ -419,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (a.parents) ancestors(sh->parent[k & 1], row_ok ? tok : -1, see_lo, see_hi);
       give(k);
       float m_run = -INFINITY, l_run = 0.f;
-      for (int i = 0; i < x.ntiles; ++i, ++gt, ring.advance(L.stages)) {
+      for (int i = 0; i < x.ntiles; ++i, ++gt) {
         const int j0 = x.j_begin + i * kTile;
         alive = alive && wait(&sh->s_full[gt & 1], (gt >> 1) & 1);
         tc_fence_after();
@@ -510,13 +526,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // ---- values that must not meet a weight of 0
         if (j0 + kTile > n || (x.rows > 1 && j0 + kTile > x.past)) {
-          const int st = ring.stage;
-          for (int j = 0; j < L.ngroups; ++j) alive = alive && wait(&sh->full[st][j], ring.turn);
+          Ring at = ring;
+          for (int j = 0; j < L.ngroups; ++j, at.advance(L.slots)) alive = alive && wait(&sh->full[at.slot], at.turn);
+          const int st = ring.slot, st1 = st + 1 == L.slots ? 0 : st + 1;  // of the tile's groups
           const int key = me >> 2, own = me & 3;   // four threads a key
           const int chunks = L.nvb * 8;            // its 16-byte chunks, in an order that spreads the threads over the banks
           auto chunk = [&](int c) {
             const int d = (c + key) & 7;
-            return reinterpret_cast<uint4*>(sStage + st * L.stage_bytes + (c >> 3) * kBlock + key * 128 + d * 16);
+            return reinterpret_cast<uint4*>(sSlot + (c < 32 ? st : st1) * L.slot_bytes + ((c >> 3) & 3) * kBlock + key * 128 + d * 16);
           };
           const bool gone = j0 + key >= n;
           bool bad = gone;
@@ -542,6 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();  // the tensor cores read P and V through the async proxy
         tc_fence_before();
         mbar_arrive(&sh->p_ready);
+        for (int j = 0; j < L.ngroups; ++j) ring.advance(L.slots);
       }
 
       // ---- output: a lane holds a channel of each 128, its pairs in the columns
@@ -707,7 +725,7 @@ template <typename T, bool kPaged>
 cudaError_t launch_t(const RowsAttnArgs& args, int dtype, cudaStream_t st) {
   Work a;
   static_cast<RowsAttnArgs&>(a) = args;
-  const Layout l = layout_of(a.dqk, a.dv);
+  const Layout l = layout_of(a.dqk, a.dv, a.q_rows);
   CUtensorMap tq, tk;
   const CacheView& c = a.cache;
   const uint64_t slots = kPaged ? c.page_size : c.capacity, planes = kPaged ? c.num_pages : a.rows.num_seqs;
