@@ -18,8 +18,9 @@ struct ExpandedWork : pairs::WorkBase {
   using Cursor = TurnCursor<ExpandedWork>;
   SeqRows keys;
   int total_keys;
+  int item_rows;            // of one Q tile, or two
 
-  __device__ __forceinline__ int items(int r) const { return (r - 1) / (2 * tok_tile) + 1; }
+  __device__ __forceinline__ int items(int r) const { return (r - 1) / item_rows + 1; }
   __device__ __forceinline__ bool bounds(int s, int& r, int& row0, int& n, int& key0) const {
     r = seq_rows(rows, s);
     if (r < 1) return false;
@@ -41,10 +42,11 @@ struct ExpandedWork : pairs::WorkBase {
     if (!bounds(s, x.rows, x.row0, n, x.key0)) return false;
     x.s = s;
     x.g = (int)(idx % hq);
-    x.t0 = (items(x.rows) - 1 - (int)(idx / hq)) * 2 * tok_tile;
+    x.t0 = (items(x.rows) - 1 - (int)(idx / hq)) * item_rows;
+    x.q1 = item_rows > tok_tile && x.t0 + tok_tile < x.rows;
     x.past = n - x.rows;
     x.j_begin = 0;
-    const int seen = x.past + min(x.rows, x.t0 + 2 * tok_tile);  // by the item's last row
+    const int seen = x.past + min(x.rows, x.t0 + item_rows);  // by the item's last row
     x.ntiles = seen > 0 ? (seen + pairs::kKeys - 1) / pairs::kKeys : 0;
     x.all = x.past + x.t0 + 1;
     x.whole = 1;
@@ -93,7 +95,14 @@ cudaError_t launch_type(const ExpandedArgs& a, int dtype, cudaStream_t st) {
         (a.r > 0 && !encode_strided(&tm.kr, dtype, a.k_rope, a.r, N, 1, a.r_row, a.r_row, 128, 1)))
       return cudaErrorInvalidValue;
   }
-  const long long items = ((long long)a.total_rows / 256 + a.rows.num_seqs) * a.heads;
+  const auto items_of = [&](int rows) {  // at most
+    if (a.rows.rows_uniform > 0) return ((long long)(a.rows.rows_uniform - 1) / rows + 1) * a.rows.num_seqs * a.heads;
+    return ((long long)a.total_rows / rows + a.rows.num_seqs) * a.heads;
+  };
+  // A lone Q tile takes two thirds of a pair's time: items are of one where all find an SM
+  // (RAGGED).
+  wk.item_rows = items_of(128) <= kSms ? 128 : 256;
+  const long long items = items_of(wk.item_rows);
   const int nqb = a.dn / 64 + (a.r > 0 ? 1 : 0);
   if (a.dv == 64) {
     if (nqb == 1) return pairs::launch<T, 1, 1>(tm, wk, items, st);

@@ -66,6 +66,7 @@ struct Item {
   int t0;                   // the item's first token
   int j_begin;              // its first key
   int all;                  // keys that every row of the item sees: [0, all)
+  int q1;                   // with a second Q tile
   int whole;                // not split: finished here
   int part;                 // else: its part
 };
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
       if (x.ntiles == 0) continue;
       if (queries > 0) ok = wait(&sh->q_empty, (queries - 1) & 1);
       if (!ok) break;
-      const bool q1 = x.t0 + wk.tok_tile < x.rows;
+      const bool q1 = x.q1;
       if (lane == 0)
         for (int w = 0; w < (q1 ? 2 : 1); ++w) {
           mbar_arrive_expect_tx(&sh->q_full[w], NQB * wk.tok_tile * wk.group * 128);
@@ -336,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
     for (int k = 0; ok; ++k) {
       if (!wait(&sh->item_full[k & 1], (k >> 1) & 1)) break;
       const int ntiles = uniform(sh->item[k & 1].ntiles);
-      const int nw = uniform(sh->item[k & 1].t0 + wk.tok_tile < sh->item[k & 1].rows ? 2 : 1);
+      const int nw = uniform(sh->item[k & 1].q1) + 1;
       give(k);
       if (ntiles < 0) break;
       if (ntiles == 0) continue;
@@ -408,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
     // After a wait that gave up, an item's walk goes on without waiting, and its output is not written.
     bool alive = take(k, x) && !*abort_flag;
     if (!__all_sync(0xffffffffu, alive)) break;
-    const bool q1 = x.t0 + wk.tok_tile < x.rows;
+    const bool q1 = x.q1;
     const int tok = x.t0 + w * wk.tok_tile + mtok;  // this row's token
     const bool row_ok = mtok < wk.tok_tile && tok < x.rows;
     const int n = x.past + x.rows;

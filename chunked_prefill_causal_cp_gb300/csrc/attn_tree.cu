@@ -43,6 +43,7 @@ struct TreeWork : pairs::WorkBase {
     x.g = u / np;
     x.key0 = 0;
     x.t0 = (u - x.g * np) * 2 * tok_tile;
+    x.q1 = x.t0 + tok_tile < x.rows;
     x.j_begin = k0 * pairs::kKeys;
     const int seen = x.past + min(x.rows, x.t0 + 2 * tok_tile);  // by the item's last row
     x.ntiles = seen > x.j_begin ? min((seen - x.j_begin - 1) / pairs::kKeys + 1, n) : 0;
