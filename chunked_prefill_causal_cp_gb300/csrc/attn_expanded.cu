@@ -13,14 +13,15 @@ namespace {
 
 using pairs::Item;
 
+template <bool kLone_>  // items of one Q tile
 struct ExpandedWork : pairs::WorkBase {
-  static constexpr bool kPaged = false, kExpanded = true;
+  static constexpr bool kPaged = false, kExpanded = true, kLone = kLone_;
+  static constexpr int kItemRows = kLone ? 128 : 256;
   using Cursor = TurnCursor<ExpandedWork>;
   SeqRows keys;
   int total_keys;
-  int item_rows;            // of one Q tile, or two
 
-  __device__ __forceinline__ int items(int r) const { return (r - 1) / item_rows + 1; }
+  __device__ __forceinline__ int items(int r) const { return (r - 1) / kItemRows + 1; }
   __device__ __forceinline__ bool bounds(int s, int& r, int& row0, int& n, int& key0) const {
     r = seq_rows(rows, s);
     if (r < 1) return false;
@@ -42,11 +43,11 @@ struct ExpandedWork : pairs::WorkBase {
     if (!bounds(s, x.rows, x.row0, n, x.key0)) return false;
     x.s = s;
     x.g = (int)(idx % hq);
-    x.t0 = (items(x.rows) - 1 - (int)(idx / hq)) * item_rows;
-    x.q1 = item_rows > tok_tile && x.t0 + tok_tile < x.rows;
+    x.t0 = (items(x.rows) - 1 - (int)(idx / hq)) * kItemRows;
+    x.q1 = !kLone && x.t0 + tok_tile < x.rows;
     x.past = n - x.rows;
     x.j_begin = 0;
-    const int seen = x.past + min(x.rows, x.t0 + item_rows);  // by the item's last row
+    const int seen = x.past + min(x.rows, x.t0 + kItemRows);  // by the item's last row
     x.ntiles = seen > 0 ? (seen + pairs::kKeys - 1) / pairs::kKeys : 0;
     x.all = x.past + x.t0 + 1;
     x.whole = 1;
@@ -67,9 +68,9 @@ bool encode_strided(CUtensorMap* m, int dtype, const void* base, uint64_t d0, ui
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T>
-cudaError_t launch_type(const ExpandedArgs& a, int dtype, cudaStream_t st) {
-  ExpandedWork wk;
+template <typename T, bool kLone>
+cudaError_t launch_t(const ExpandedArgs& a, int dtype, long long items, cudaStream_t st) {
+  ExpandedWork<kLone> wk;
   wk.hq = wk.hkv = a.heads;
   wk.group = 1;
   wk.tok_tile = 128;
@@ -95,14 +96,6 @@ cudaError_t launch_type(const ExpandedArgs& a, int dtype, cudaStream_t st) {
         (a.r > 0 && !encode_strided(&tm.kr, dtype, a.k_rope, a.r, N, 1, a.r_row, a.r_row, 128, 1)))
       return cudaErrorInvalidValue;
   }
-  const auto items_of = [&](int rows) {  // at most
-    if (a.rows.rows_uniform > 0) return ((long long)(a.rows.rows_uniform - 1) / rows + 1) * a.rows.num_seqs * a.heads;
-    return ((long long)a.total_rows / rows + a.rows.num_seqs) * a.heads;
-  };
-  // A lone Q tile takes two thirds of a pair's time: items are of one where all find an SM
-  // (RAGGED).
-  wk.item_rows = items_of(128) <= kSms ? 128 : 256;
-  const long long items = items_of(wk.item_rows);
   const int nqb = a.dn / 64 + (a.r > 0 ? 1 : 0);
   if (a.dv == 64) {
     if (nqb == 1) return pairs::launch<T, 1, 1>(tm, wk, items, st);
@@ -110,6 +103,22 @@ cudaError_t launch_type(const ExpandedArgs& a, int dtype, cudaStream_t st) {
   }
   if (nqb == 1) return pairs::launch<T, 1, 2>(tm, wk, items, st);
   return nqb == 2 ? pairs::launch<T, 2, 2>(tm, wk, items, st) : pairs::launch<T, 3, 2>(tm, wk, items, st);
+}
+
+// Items of so many rows, at most.
+long long items_of(const ExpandedArgs& a, int rows) {
+  if (a.rows.rows_uniform > 0) return ((long long)(a.rows.rows_uniform - 1) / rows + 1) * a.rows.num_seqs * a.heads;
+  return ((long long)a.total_rows / rows + a.rows.num_seqs) * a.heads;
+}
+
+// Items are of one Q tile where all find an SM at once: half the work each, at a higher price
+// (a tile of keys 1.05 us for a lone Q tile, 1.75 us for a pair; 8 heads of 1000 rows after
+// 4000: 40 us, as pairs 76; 4 heads of 4864 after 8000, 152 Q tiles: 107 us, as pairs 176).
+// With more, pairs, which read K and V half as often.
+template <typename T>
+cudaError_t launch_type(const ExpandedArgs& a, int dtype, cudaStream_t st) {
+  const long long lone = items_of(a, 128);
+  return lone <= kSms ? launch_t<T, true>(a, dtype, lone, st) : launch_t<T, false>(a, dtype, items_of(a, 256), st);
 }
 
 }  // namespace

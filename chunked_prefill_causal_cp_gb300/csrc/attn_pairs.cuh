@@ -19,6 +19,11 @@
 // that P_w(i) may be overwritten and O_w rescaled -- which happens only when a row's
 // maximum has grown by more than 2^8.
 //
+// A lone Q tile (Work::kLone) has both warpgroups, which take its tiles of keys in turn,
+// S_w(i) = Q K^T and O_w += P_w(i) V with w = i mod 2: the tensor cores compute one's
+// products during the other's softmax, as with a pair.  Their outputs, maxima and sums
+// are joined at the end.
+//
 // What a row does not see: its scores become -inf by a mask of the tile's columns (a
 // tree's row: its ancestors, 128 bits found by walking the parents once).  Its weight
 // 0 must not meet a NaN or an infinity in V: in tiles with keys that some row of
@@ -47,7 +52,7 @@ constexpr int kThreads = 384;
 constexpr int kKeys = 128;                // keys of a tile
 constexpr uint32_t kUnit = 128 * 128;     // bytes of 128 rows x 64 channels
 constexpr int kMaxUnits = 12;
-constexpr int kMaxTiles = 7;              // of the ring, whole or in part
+constexpr int kMaxTiles = 8;              // that have barriers
 constexpr uint32_t kSmem = 232448;        // of a CTA, at most
 constexpr float kRescaleLog2 = 8.0f;
 // Register split: compiled at kRegsLaunch a thread (the most 384 threads may have); the
@@ -73,22 +78,25 @@ struct Item {
 
 struct __align__(16) Shared {
   uint64_t item_full[2], item_empty[2], q_full[2], q_empty, k_full[kMaxTiles], v_full[kMaxTiles], k_empty[kMaxTiles],
-      v_empty[kMaxTiles], s_full[2], p_ready[2], o_done[2], o_free[2], guarded[2], all_done;
+      v_empty[kMaxTiles], s_full[2], p_ready[2], o_done[2], o_free[2], guarded[2], joined, all_done;
   uint32_t tmem_base;
   int abort;
   Item item[2];
   int8_t parent[2][CP_TREE_MAX];            // a tree's, beside its item
-  // Keys of a tile with a non-finite value, 16 each: of tiles that one Q tile looks through, that two do.
+  // Keys of a tile with a non-finite value, 16 each: of tiles that one Q tile looks through, that two do (of a lone
+  // one's: that each warpgroup does).
   __align__(16) uint16_t bad[2][2][8];
 };
 
-template <int NQB>
+template <int NQB, bool kLone>
 struct Layout {
-  static constexpr uint32_t q_bytes = 2u * NQB * kUnit;
-  static constexpr int fit = (int)((kSmem - q_bytes - sizeof(Shared)) / kUnit);
+  static constexpr uint32_t q_bytes = (kLone ? 1u : 2u) * NQB * kUnit;
+  // A lone Q tile's rows: maximum and sum in each warpgroup's keys, of two items in turn.
+  static constexpr uint32_t ml_bytes = kLone ? 2 * 2 * 128 * sizeof(float2) : 0;
+  static constexpr int fit = (int)((kSmem - q_bytes - ml_bytes - sizeof(Shared)) / kUnit);
   static constexpr int units = fit < kMaxUnits ? fit : kMaxUnits;
   static constexpr uint32_t ctl_off = q_bytes + units * kUnit;
-  static constexpr uint32_t alloc = ctl_off + (uint32_t)sizeof(Shared);
+  static constexpr uint32_t ml_off = ctl_off + (uint32_t)sizeof(Shared), alloc = ml_off + ml_bytes;
 };
 
 struct Maps {
@@ -96,7 +104,7 @@ struct Maps {
 };
 
 // What a call is about: TreeWork (attn_tree.cu) and ExpandedWork (attn_expanded.cu) add
-// kPaged, kExpanded, and their Cursor with what it asks.
+// kPaged, kExpanded, kLone, and their Cursor with what it asks.
 struct WorkBase {
   int hq, hkv, group;
   int tok_tile;            // tokens of a Q tile
@@ -120,13 +128,15 @@ struct WorkBase {
 
 template <typename T, int NQB, int NVB, typename Work>
 __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constant__ Maps tm, const Work wk) {
-  using L = Layout<NQB>;
+  using L = Layout<NQB, Work::kLone>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr uint32_t kIdescQK = make_idesc_f16(kBf16, 128, kKeys, false);
   constexpr uint32_t kIdescPV = make_idesc_f16(kBf16, 128, NVB * 64, true);
-  // Tile t's barriers are t mod kTiles: a tile's K is loaded only when units of the tile kTiles - 1 before it are given
-  // back, so no barrier is a phase ahead of those who wait for it.
-  constexpr int kRing = L::units, kTile = NQB + NVB, kTiles = kRing / kTile + 1;
+  // Tile t's barriers are t mod kTiles, and none may be a phase ahead of those who wait for it: t's K and V must not be
+  // loaded before the product with V of tile t - kTiles.  They are loaded when units of tile t - kRing / kTile, or a later
+  // one, are given back, of its K at the earliest; its scores were issued after the product of the tile before, or (a lone
+  // Q tile) the one before that.
+  constexpr int kRing = L::units, kTile = NQB + NVB, kTiles = kRing / kTile + (Work::kLone ? 2 : 1);
   static_assert(kTiles <= kMaxTiles, "barriers");
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sRing = smem + L::q_bytes;
@@ -143,11 +153,12 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
       mbar_init(&sh->s_full[i], 1);
       mbar_init(&sh->p_ready[i], 128);
       mbar_init(&sh->o_done[i], 1);
-      mbar_init(&sh->o_free[i], 128);
+      mbar_init(&sh->o_free[i], Work::kLone ? 256 : 128);
     }
     mbar_init(&sh->q_empty, 1);
     mbar_init(&sh->guarded[0], 128);
-    mbar_init(&sh->guarded[1], 256);
+    mbar_init(&sh->guarded[1], Work::kLone ? 128 : 256);
+    mbar_init(&sh->joined, 256);
     for (int i = 0; i < kTiles; ++i) {
       mbar_init(&sh->k_full[i], 1);
       mbar_init(&sh->v_full[i], 1);
@@ -252,11 +263,14 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
         }
         for (int v = 0; ok && v < 2; ++v) {  // K, V
           const int n = v ? NVB : NQB, u = t * kTile + (v ? NQB : 0);
-          // The units before them in the ring, the last of which is given back last.
+          // The units before them in the ring, the last of which is given back last (but for a lone Q tile: K before the
+          // V of the tile before it).
           const int old = u + n - 1 - kRing;
           if (old >= 0) {
             const int to = old / kTile;
             ok = wait(old % kTile < NQB ? &sh->k_empty[to % kTiles] : &sh->v_empty[to % kTiles], (to / kTiles) & 1);
+            if (Work::kLone && ok && to > 0 && old % kTile < n - 1 && old % kTile < NQB)
+              ok = wait(&sh->v_empty[(to - 1) % kTiles], ((to - 1) / kTiles) & 1);
             if (!ok) break;
           }
           uint64_t* bar = v ? &sh->v_full[t % kTiles] : &sh->k_full[t % kTiles];
@@ -302,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
     uint32_t pq = 0, pp = 0, po = 0, begun = 0;  // bit w: parity of the Q tiles and P tiles taken, of the outputs begun; any begun
     bool ok = true;
     auto scores = [&](int w) {  // S_w = Q_w K^T
-      const uint32_t d = tm0 + 256u * w, q = q_lo + (uint32_t)w * (NQB * kStep);
+      const uint32_t d = tm0 + 256u * w, q = q_lo + (Work::kLone ? 0u : (uint32_t)w * (NQB * kStep));
 #pragma unroll
       for (int b = 0; b < NQB; ++b) {
         const uint32_t kd = k_lo + (uint32_t)wrap(k_slot + b) * kStep;
@@ -334,7 +348,52 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
         k_turn ^= 1u;
       }
     };
-    for (int k = 0; ok; ++k) {
+    auto v_done = [&] {
+      mma_commit_elect(&sh->v_empty[vt]);
+      v_slot = wrap(v_slot + kTile);
+      if (++vt == kTiles) {
+        vt = 0;
+        v_turn ^= 1u;
+      }
+    };
+    // A lone Q tile: tile i of keys is warpgroup i mod 2's.
+    auto next_scores = [&](int w) {
+      if (!wait(&sh->k_full[kt], k_turn)) return false;
+      tc_fence_after();
+      scores(w);
+      k_done();
+      return true;
+    };
+    for (int k = 0; Work::kLone && ok; ++k) {
+      if (!wait(&sh->item_full[k & 1], (k >> 1) & 1)) break;
+      const int ntiles = uniform(sh->item[k & 1].ntiles);
+      give(k);
+      if (ntiles < 0) break;
+      if (ntiles == 0) continue;
+      ok = wait(&sh->q_full[0], pq);
+      pq ^= 1u;
+      for (int i = 0; ok && i < 2 && i < ntiles; ++i) ok = next_scores(i);
+      if (ntiles <= 2) mma_commit_elect(&sh->q_empty);
+      for (int i = 0; ok && i < ntiles; ++i) {
+        const int w = i & 1;
+        ok = wait(&sh->v_full[vt], v_turn);
+        if (ok && i < 2 && ((begun >> w) & 1)) ok = wait(&sh->o_free[w], ((po >> w) & 1) ^ 1);
+        ok = ok && wait(&sh->p_ready[w], (pp >> w) & 1);
+        if (!ok) break;
+        pp ^= 1u << w;
+        tc_fence_after();
+        output(w, i >= 2);
+        if (i + 2 >= ntiles) mma_commit_elect(&sh->o_done[w]);
+        v_done();
+        if (i < 2) {
+          po ^= 1u << w;
+          begun |= 1u << w;
+        }
+        if (i + 2 < ntiles) ok = next_scores(w);
+        if (i + 3 == ntiles) mma_commit_elect(&sh->q_empty);  // the item's last scores are issued
+      }
+    }
+    for (int k = 0; !Work::kLone && ok; ++k) {
       if (!wait(&sh->item_full[k & 1], (k >> 1) & 1)) break;
       const int ntiles = uniform(sh->item[k & 1].ntiles);
       const int nw = uniform(sh->item[k & 1].q1) + 1;
@@ -364,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
           tc_fence_after();
           output(w, i > 0);
           if (!more) mma_commit_elect(&sh->o_done[w]);
-          if (w == nw - 1) mma_commit_elect(&sh->v_empty[vt]);
+          if (w == nw - 1) v_done();
           if (more) {
             if (w == 0) {
               ok = wait(&sh->k_full[kt], k_turn);
@@ -379,11 +438,6 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
           }
         }
         if (!ok) break;
-        v_slot = wrap(v_slot + kTile);
-        if (++vt == kTiles) {
-          vt = 0;
-          v_turn ^= 1u;
-        }
         if (more) k_done();
         if (i + 2 == ntiles) mma_commit_elect(&sh->q_empty);  // the item's last scores are issued
       }
@@ -402,7 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
   const uint32_t s_col = tmem + ((uint32_t)(quarter * 32) << 16) + 256u * w, o_col = s_col + 128u;
   const int mtok = m / wk.group, mhead = m % wk.group;
   int t = 0;            // the CTA's tiles so far
-  int ns = 0, no = 0;   // score tiles, outputs of this Q tile so far
+  int ns = 0;           // score tiles of this warpgroup so far
+  int no[2] = {0, 0};   // items with an output w so far
   Item x;
   int guards[2] = {0, 0};  // tiles looked through for hidden values so far, by one Q tile, by two
   for (int k = 0;; ++k) {
@@ -410,19 +465,20 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
     bool alive = take(k, x) && !*abort_flag;
     if (!__all_sync(0xffffffffu, alive)) break;
     const bool q1 = x.q1;
-    const int tok = x.t0 + w * wk.tok_tile + mtok;  // this row's token
+    const int tok = x.t0 + (Work::kLone ? 0 : w * wk.tok_tile) + mtok;  // this row's token
     const bool row_ok = mtok < wk.tok_tile && tok < x.rows;
     const int n = x.past + x.rows;
     uint64_t see_lo = 0, see_hi = 0;  // a tree's row: the call's rows that it sees
     if (!Work::kExpanded) ancestors(sh->parent[k & 1], row_ok ? tok : -1, see_lo, see_hi);
     give(k);
-    if (w == 1 && !q1) {
+    if (!Work::kLone && w == 1 && !q1) {
       t += x.ntiles;
       continue;
     }
     const int seen = Work::kExpanded ? x.past + tok + 1 : x.past;  // keys [0, seen) are seen, and in a tree the row's ancestors
     float m_run = -INFINITY, l_run = 0.f;
-    for (int i = 0; i < x.ntiles; ++i, ++ns, ++t) {
+    constexpr int kTurns = Work::kLone ? 2 : 1;
+    for (int i = Work::kLone ? w : 0; i < x.ntiles; i += kTurns, ++ns) {
       alive = alive && wait(&sh->s_full[w], ns & 1);
       tc_fence_after();
       uint32_t sv[128];
@@ -477,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
       tmem_st32(s_col + 0, &sv[0]);
       tmem_st32(s_col + 32, &sv[32]);
       // O holds P V of the earlier tiles (complete: see the ordering note above).
-      if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+      if (i >= kTurns && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll
         for (int c = 0; c < 2 * NVB; ++c) {
           uint32_t ov[32];
@@ -490,9 +546,10 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
       }
       if (guard) {
         // ---- values that must not meet a weight of 0: the threads of the item's Q tiles share the tile's keys
-        alive = alive && wait(&sh->v_full[t % kTiles], (t / kTiles) & 1);
-        const int v_unit = t * kTile + NQB;
-        const int per = q1 ? 2 : 1, me = w * 128 + m;   // threads of a key; this one
+        const int tile = t + i;
+        alive = alive && wait(&sh->v_full[tile % kTiles], (tile / kTiles) & 1);
+        const int v_unit = tile * kTile + NQB;
+        const int per = !Work::kLone && q1 ? 2 : 1, me = (Work::kLone ? 0 : w * 128) + m;   // threads of a key; this one
         const int key = me / per, part = me % per;
         const bool gone = j0 + key >= n;
         bool bad = gone;
@@ -506,8 +563,8 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
         if (per == 2) bad = __shfl_xor_sync(0xffffffffu, bad, 1) || bad;
         if (bad)
           for (int c = part; c < kChunks; c += per) *chunk(c) = make_uint4(0, 0, 0, 0);
-        const int turn = q1 ? guards[1]++ : guards[0]++;
-        uint16_t* found = sh->bad[q1][turn & 1];
+        const int by = Work::kLone ? w : (int)q1, turn = by ? guards[1]++ : guards[0]++;
+        uint16_t* found = sh->bad[by][turn & 1];
         const uint32_t bits = __ballot_sync(0xffffffffu, bad && !gone);
         if (lane == 0) {
           if (per == 2) {
@@ -518,8 +575,8 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
           }
         }
         fence_proxy_async_smem();  // the tensor cores read V through the async proxy
-        mbar_arrive(&sh->guarded[q1]);
-        alive = alive && wait(&sh->guarded[q1], turn & 1);
+        mbar_arrive(&sh->guarded[by]);
+        alive = alive && wait(&sh->guarded[by], turn & 1);
         const uint4 y = *reinterpret_cast<const uint4*>(found);
         if ((vis[0] & (y.x | (uint64_t)y.y << 32)) | (vis[1] & (y.z | (uint64_t)y.w << 32))) l_run = __int_as_float(0x7fffffff);
       }
@@ -528,8 +585,64 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
       mbar_arrive(&sh->p_ready[w]);
     }
 
+    t += x.ntiles;
+
     // ---- output
-    if (x.ntiles > 0) alive = alive && wait(&sh->o_done[w], no & 1);
+    if constexpr (Work::kLone) {
+      // The two warpgroups' parts, of even and odd tiles, are joined: each writes half of the channels.
+      float k0 = 0.f, k1 = 0.f;  // factors of the parts
+      if (x.ntiles > 0) {
+        for (int v = 0; v < 2 && v < x.ntiles; ++v) alive = alive && wait(&sh->o_done[v], (v ? no[1] : no[0]) & 1);
+        float2* ml = reinterpret_cast<float2*>(smem + L::ml_off) + (no[0] & 1) * 256 + m;
+        ml[w * 128] = make_float2(m_run, l_run);
+        mbar_arrive(&sh->joined);
+        alive = alive && wait(&sh->joined, no[0] & 1);
+        tc_fence_after();
+        const float2 a = ml[0], b = ml[128];
+        const float top = fmaxf(a.x, b.x), z = top == -INFINITY ? 0.f : top;
+        k0 = ex2_approx(a.x - z);
+        k1 = ex2_approx(b.x - z);
+        const float l = a.y * k0 + b.y * k1, inv = l == 0.f ? 0.f : 1.f / l;  // a NaN stays
+        k0 *= inv;
+        k1 *= inv;
+      }
+      const uint32_t o0 = o_col - 256u * w;
+      uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(wk.out) + ((long long)(x.row0 + tok) * wk.hq + x.g) * (NVB * 64));
+#pragma unroll
+      for (int j = 0; j < NVB; ++j) {
+        const int c = w * NVB + j;
+        float o[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+        if (x.ntiles > 0) {
+          uint32_t ov[32];
+          tmem_ld32(o0 + 32 * c, ov);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(ov[e]) * k0;
+          if (x.ntiles > 1) {
+            tmem_ld32(o0 + 256 + 32 * c, ov);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(ov[e]), k1, o[e]);
+          }
+        }
+        if (row_ok && alive) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            out[4 * c + e] = make_uint4(pack2<T>(o[8 * e], o[8 * e + 1]), pack2<T>(o[8 * e + 2], o[8 * e + 3]),
+                                        pack2<T>(o[8 * e + 4], o[8 * e + 5]), pack2<T>(o[8 * e + 6], o[8 * e + 7]));
+        }
+      }
+      tc_fence_before();
+      for (int v = 0; v < 2 && v < x.ntiles; ++v) {
+        ++no[v];
+        mbar_arrive(&sh->o_free[v]);
+      }
+      if (!alive) *abort_flag = 1;
+      continue;
+    }
+    if (x.ntiles > 0) alive = alive && wait(&sh->o_done[w], no[0] & 1);
     tc_fence_after();
     const bool write = row_ok && alive;
     const long long row = (long long)(x.row0 + tok) * wk.hq + x.g * wk.group + mhead;
@@ -575,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
       }
     }
     if (x.ntiles > 0) {
-      ++no;
+      ++no[0];
       tc_fence_before();
       mbar_arrive(&sh->o_free[w]);
     }
@@ -592,8 +705,8 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
 
 template <typename T, int NQB, int NVB, typename Work>
 cudaError_t launch(const Maps& tm, const Work& wk, long long items, cudaStream_t st) {
-  using L = Layout<NQB>;
-  static_assert(L::units >= NQB + NVB, "a tile fits the ring");
+  using L = Layout<NQB, Work::kLone>;
+  static_assert(L::units >= NQB + NVB + (Work::kLone ? NQB : 0), "a tile fits the ring; of a lone Q tile's, the next one's K too");
   const auto kernel = pairs_kernel<T, NQB, NVB, Work>;
   // Raise the dynamic shared-memory limit once per device, so later calls --
   // including ones being captured into a CUDA graph -- only launch.

@@ -14,7 +14,7 @@ using pairs::Item;
 
 template <bool kPaged_>
 struct TreeWork : pairs::WorkBase {
-  static constexpr bool kPaged = kPaged_, kExpanded = false;
+  static constexpr bool kPaged = kPaged_, kExpanded = false, kLone = false;
   using Cursor = ShareCursor<TreeWork>;
   const int* past;
   int max_ctx, ctas;

@@ -428,7 +428,10 @@ def _check_expanded(dtype, q, k, kr, v, out, rows, keys, scale=0.0):
 
 
 @pytest.mark.parametrize("dtype,heads,dn,r,dv", [(BF16, 4, 128, 64, 128), (F16, 3, 64, 32, 64), (BF16, 1, 128, 16, 64),
-                                                 (F16, 2, 64, 0, 128), (BF16, 5, 64, 48, 64)])
+                                                 (F16, 2, 64, 0, 128), (BF16, 5, 64, 48, 64),
+                                                 # heads enough for pairs of Q tiles
+                                                 (BF16, 24, 128, 64, 128), (F16, 23, 64, 32, 64), (BF16, 21, 128, 16, 64),
+                                                 (F16, 22, 64, 0, 128), (BF16, 25, 64, 0, 64)])
 def test_expanded_chunks(dtype, heads, dn, r, dv):
     rows, keys = [1, 300, 37, 128, 2], [1, 300, 700, 257, 129]
     q, k, kr, v, out, status = _expanded(dtype, heads, dn, r, dv, rows, keys)
@@ -437,48 +440,52 @@ def test_expanded_chunks(dtype, heads, dn, r, dv):
 
 
 @pytest.mark.parametrize("rows,keys", [(1, 1), (127, 127), (128, 128), (129, 129), (255, 400), (257, 1025), (64, 64)])
-def test_expanded_equal_rows(rows, keys):
-    q, k, kr, v, out, status = _expanded(BF16, 2, 128, 64, 128, [rows] * 3, [keys] * 3, uniform=True, fused=False, scale=0.3)
+@pytest.mark.parametrize("heads", [2, 51])
+def test_expanded_equal_rows(rows, keys, heads):
+    q, k, kr, v, out, status = _expanded(BF16, heads, 128, 64, 128, [rows] * 3, [keys] * 3, uniform=True, fused=False, scale=0.3)
     assert int(status) == 0
     _check_expanded(BF16, q, k, kr, v, out, [rows] * 3, [keys] * 3, scale=0.3)
 
 
-def test_expanded_rows_that_see_nothing():
+@pytest.mark.parametrize("heads", [2, 26])
+def test_expanded_rows_that_see_nothing(heads):
     """More rows than keys: the first rows see none and get zeros; a sequence without keys gets zeros throughout."""
     rows, keys = [300, 5, 140], [10, 0, 139]
-    q, k, kr, v, out, status = _expanded(F16, 2, 64, 32, 64, rows, keys)
+    q, k, kr, v, out, status = _expanded(F16, heads, 64, 32, 64, rows, keys)
     assert int(status) == 0
     assert (out[:290] == 0).all() and (out[300:305] == 0).all() and (out[305] == 0).all()
     _check_expanded(F16, q, k, kr, v, out, rows, keys)
 
 
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
-def test_expanded_non_finite_values(value):
+@pytest.mark.parametrize("heads", [2, 31])
+def test_expanded_non_finite_values(value, heads):
     """A value that is not finite reaches the rows that see its key, and neither the earlier ones nor the sequence before."""
     rows, keys = [150, 300], [150, 333]
-    clean = _expanded(BF16, 2, 128, 64, 128, rows, keys)[4]
+    clean = _expanded(BF16, heads, 128, 64, 128, rows, keys)[4]
     for at in (150 + 33, 150 + 40, 150 + 200, 482):
         def poison(k, kr, v):
             v[at, 1, 5] = value
-        out = _expanded(BF16, 2, 128, 64, 128, rows, keys, poison=poison)[4]
+        out = _expanded(BF16, heads, 128, 64, 128, rows, keys, poison=poison)[4]
         first = max(0, at - 150 - 33) + 150  # the first row that sees it
         assert torch.equal(out[:first], clean[:first]) and torch.equal(out[:, 0], clean[:, 0])
         assert (~torch.isfinite(out[first:, 1].float())).any(-1).all()
     # In a key: the rows that see it, and no other; an infinite score of -inf weighs nothing.
     def poison_k(k, kr, v):
         kr[150 + 60, 3] = value
-    q, _, _, _, out, _ = _expanded(BF16, 2, 128, 64, 128, rows, keys, poison=poison_k)
+    q, _, _, _, out, _ = _expanded(BF16, heads, 128, 64, 128, rows, keys, poison=poison_k)
     first = 150 + 60 - 33
     assert torch.equal(out[:first], clean[:first])
     lost = ~torch.isfinite(out[first:].float()).all(-1)
     assert lost.all() if value != value else torch.equal(lost, q[first:, :, 128 + 3] > 0)
 
 
-def test_expanded_bad_offsets_and_padding():
+@pytest.mark.parametrize("heads", [2, 39])
+def test_expanded_bad_offsets_and_padding(heads):
     rows, keys = [40, 60, 50], [80, 90, 70]
     t, n = 150, 240
-    q, k, kr, v, want, _ = _expanded(BF16, 2, 128, 64, 128, rows, keys)
-    desc = cp.latent_desc(BF16, 1, 2, 512, 64, capacity=1)
+    q, k, kr, v, want, _ = _expanded(BF16, heads, 128, 64, 128, rows, keys)
+    desc = cp.latent_desc(BF16, 1, heads, 512, 64, capacity=1)
     for cr, ck, skipped in (([0, 40, 100, 150], [0, 80, 80 - 1, 240], {1}), ([0, 40, 100, 150], [0, 80, 170, 241], {2}),
                             ([0, 40, 40, 150], [0, 80, 170, 240], None), ([0, 40, 100, 100], [0, 80, 170, 240], {2})):
         out = torch.full_like(want, 7.0)
