@@ -187,7 +187,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sP = smem + L.p_off;
   Shared* sh = reinterpret_cast<Shared*>(smem + L.ctl_off);
 
-  pdl_launch_dependents();
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   // ---- set-up that reads no global memory: it may overlap the previous kernel
   if (threadIdx.x == 0) {
@@ -232,6 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return x.ntiles >= 0;
   };
   pdl_wait();  // everything below reads what earlier kernels wrote
+  pdl_launch_dependents();  // after it: the combine kernel's lookups read the same inputs
 
   if (warp == 2) {
     // ================================================================ scheduling
@@ -623,7 +623,6 @@ __global__ void __launch_bounds__(512) latent_combine_kernel(const Work a, const
   __shared__ float4 so[512];
   __shared__ float2 sml[4 * kSlices];
   pdl_launch_dependents();
-  pdl_wait();
   const int groups = (a.q_rows + per - 1) / per, lane = threadIdx.x & 31;
   int w = blockIdx.x / groups;   // tile of pairs of the call
   long long all = 0, before = 0;  // tiles of keys of the call; of the sequences before this one
@@ -651,10 +650,12 @@ __global__ void __launch_bounds__(512) latent_combine_kernel(const Work a, const
     }
     all += __shfl_sync(0xffffffffu, sum, 31);
   }
-  int r, p, row0;
-  if (s < 0 || !a.bounds(s, r, p, row0)) return;  // the same for all threads
-  const int each = a.key_tiles(s);
-  const UnitShares u(all, before + (long long)tile * (kStart + each), each, a.ctas);
+  int r = 0, p = 0, row0 = 0;
+  const bool found = s >= 0 && a.bounds(s, r, p, row0);  // the same for all threads
+  const int each = found ? a.key_tiles(s) : 1;
+  const UnitShares u(max(all, 1ll), found ? before + (long long)tile * (kStart + each) : 0, each, a.ctas);
+  pdl_wait();  // on all paths: this kernel's end stands for the parts' kernel's
+  if (!found) return;
   if (u.from == u.to) return;  // finished by its one CTA
   const int first = tile * kPairs, pairs = min(kPairs, r * a.hq - first);
   const int seen = p + (first + pairs - 1) / a.hq + 1;  // keys of the tile

@@ -142,7 +142,6 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
   uint8_t* sRing = smem + L::q_bytes;
   Shared* sh = reinterpret_cast<Shared*>(smem + L::ctl_off);
 
-  pdl_launch_dependents();
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   // ---- set-up that reads no global memory: it may overlap the previous kernel
   if (threadIdx.x == 0) {
@@ -194,6 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
     return x.ntiles >= 0;
   };
   pdl_wait();  // everything below reads what earlier kernels wrote
+  pdl_launch_dependents();  // after it: the combine kernel's lookups read the same inputs
 
   if (warp < 4) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));

@@ -58,7 +58,6 @@ constexpr int kCombineRows = 8;
 template <typename T, int NVB, bool kPaged>
 __global__ void __launch_bounds__(kCombineRows * NVB * 16) tree_combine_kernel(const TreeWork<kPaged> wk) {
   pdl_launch_dependents();
-  pdl_wait();
   const int groups = 128 / kCombineRows;
   const int group = blockIdx.x % groups, g = blockIdx.y, lane = threadIdx.x & 31;
   int w = blockIdx.x / groups;  // Q tile of the call
@@ -86,10 +85,12 @@ __global__ void __launch_bounds__(kCombineRows * NVB * 16) tree_combine_kernel(c
     }
     all += __shfl_sync(0xffffffffu, sum, 31);
   }
-  int r, p, row0;
-  if (s < 0 || !wk.bounds(s, r, p, row0)) return;
-  const int item = tile / 2, each = wk.key_tiles(s);
-  const UnitShares u(all, first + ((long long)g * wk.q_pairs(r) + item) * (kStart + each), each, wk.ctas);
+  int r = 0, p = 0, row0 = 0;
+  const bool known = s >= 0 && wk.bounds(s, r, p, row0);
+  const int item = tile / 2, each = known ? wk.key_tiles(s) : 1;
+  const UnitShares u(max(all, 1ll), known ? first + ((long long)g * wk.q_pairs(r) + item) * (kStart + each) : 0, each, wk.ctas);
+  pdl_wait();  // on all paths: this kernel's end stands for the parts' kernel's
+  if (!known) return;
   if (u.from == u.to) return;  // finished by its one CTA
   const int m = group * kCombineRows + threadIdx.x % kCombineRows, c4 = threadIdx.x / kCombineRows;
   const int tok = tile * wk.tok_tile + m / wk.group;
