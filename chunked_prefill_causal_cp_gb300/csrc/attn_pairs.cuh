@@ -6,12 +6,11 @@
 // An item is a pair of 128-row Q tiles (each whole tokens of G heads) of one
 // sequence and KV head, over a range of its keys; every K/V tile that a CTA loads
 // serves both Q tiles.  One persistent CTA an SM, 384 threads:
-//   warp 0      TMA producer: an item's Q tiles, then for each 128-key tile its K and V
+//   warps 0, 3  TMA producers: an item's Q tiles and the K of each 128-key tile, and its V,
 //               in units of 64 channels (16 KB) through a ring of as many units as fit;
 //               a tile's K, and its V, land and are given back as one
 //   warp 1      MMA issue:  S_w = Q_w K^T, O_w += P_w V for Q tile w = 0, 1
 //   warp 2      scheduling: finds this CTA's items, two ahead of the others
-//   warp 3      fills the control warpgroup, whose registers go to the others
 //   warps 4-7, 8-11  softmax of Q tile 0 and 1, a thread a row
 // TMEM: Q tile w has [256w, 256w + 128) for S and, over it, P in 16 bits;
 // [256w + 128, + channels) for O.  S_w(i + 1) is issued after O_w += P_w(i) V(i), and
@@ -147,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh->item_full[i], 1);
-      mbar_init(&sh->item_empty[i], 10);  // warps 0, 1 and the eight of softmax
+      mbar_init(&sh->item_empty[i], 11);  // warps 0, 1, 3 and the eight of softmax
       mbar_init(&sh->q_full[i], 1);
       mbar_init(&sh->s_full[i], 1);
       mbar_init(&sh->p_ready[i], 128);
@@ -220,14 +219,14 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
       ++k;
     }
     __syncwarp();
-  } else if (warp == 3) {
     if (blockIdx.x == 0) wk.report_empty(lane);
-  } else if (warp == 0) {
-    // ================================================================ producer
+  } else if (warp != 1) {
+    // ================================================================ producers: warp 0 of Q and K, warp 3 of V
+    const bool of_v = warp == 3;
+    const int n = of_v ? NVB : NQB;
     const int ps = Work::kPaged ? wk.page_size : kKeys, lps = 31 - __clz(ps);
     const int npg = kKeys / ps;  // boxes of a unit
     int t = 0;                   // tiles issued so far
-    int issued = 0;              // groups: K and V of each tile
     int queries = 0;             // items whose queries were loaded
     uint32_t last_q1 = 0;        // loads of Q tile 1
     bool ok = true;
@@ -235,19 +234,21 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
     for (int k = 0; ok && take(k, x); ++k) {
       give(k);
       if (x.ntiles == 0) continue;
-      if (queries > 0) ok = wait(&sh->q_empty, (queries - 1) & 1);
-      if (!ok) break;
-      const bool q1 = x.q1;
-      if (lane == 0)
-        for (int w = 0; w < (q1 ? 2 : 1); ++w) {
-          mbar_arrive_expect_tx(&sh->q_full[w], NQB * wk.tok_tile * wk.group * 128);
-          for (int b = 0; b < NQB; ++b)
-            tma_load_3d(smem + (w * NQB + b) * kUnit, &tm.q, &sh->q_full[w], b * 64, x.g * wk.group,
-                        x.row0 + x.t0 + w * wk.tok_tile);
-        }
-      __syncwarp();
-      ++queries;
-      last_q1 += q1;
+      if (!of_v) {
+        if (queries > 0) ok = wait(&sh->q_empty, (queries - 1) & 1);
+        if (!ok) break;
+        const bool q1 = x.q1;
+        if (lane == 0)
+          for (int w = 0; w < (q1 ? 2 : 1); ++w) {
+            mbar_arrive_expect_tx(&sh->q_full[w], NQB * wk.tok_tile * wk.group * 128);
+            for (int b = 0; b < NQB; ++b)
+              tma_load_3d(smem + (w * NQB + b) * kUnit, &tm.q, &sh->q_full[w], b * 64, x.g * wk.group,
+                          x.row0 + x.t0 + w * wk.tok_tile);
+          }
+        __syncwarp();
+        ++queries;
+        last_q1 += q1;
+      }
       for (int i = 0; ok && i < x.ntiles; ++i) {
         const int j0 = x.j_begin + i * kKeys;
         int plane = x.s * wk.hkv + x.g, off = j0;
@@ -261,42 +262,36 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
           }
           off = 0;
         }
-        for (int v = 0; ok && v < 2; ++v) {  // K, V
-          const int n = v ? NVB : NQB, u = t * kTile + (v ? NQB : 0);
-          // The units before them in the ring, the last of which is given back last (but for a lone Q tile: K before the
-          // V of the tile before it).
-          const int old = u + n - 1 - kRing;
-          if (old >= 0) {
-            const int to = old / kTile;
-            ok = wait(old % kTile < NQB ? &sh->k_empty[to % kTiles] : &sh->v_empty[to % kTiles], (to / kTiles) & 1);
-            if (Work::kLone && ok && to > 0 && old % kTile < n - 1 && old % kTile < NQB)
-              ok = wait(&sh->v_empty[(to - 1) % kTiles], ((to - 1) / kTiles) & 1);
-            if (!ok) break;
-          }
-          uint64_t* bar = v ? &sh->v_full[t % kTiles] : &sh->k_full[t % kTiles];
-          ++issued;
-          if (lane == 0) mbar_arrive_expect_tx(bar, n * kUnit);
-          __syncwarp();
-          for (int idx = lane; idx < npg * n; idx += 32) {  // npg divides 32: the page stays the lane's
-            const int e = idx / npg;
-            uint8_t* dst = sRing + (u + e) % kRing * kUnit + (idx % npg) * ps * 128;
-            if (!Work::kExpanded) tma_load_3d(dst, v ? &tm.v : &tm.k, bar, e * 64, off, plane);
-            else if (v) tma_load_3d(dst, &tm.v, bar, e * 64, x.g, x.key0 + j0);
-            else if (e * 64 < wk.dn) tma_load_3d(dst, &tm.k, bar, e * 64, x.g, x.key0 + j0);
-            else tma_load_3d(dst, &tm.kr, bar, 0, x.key0 + j0, 0);
-          }
+        // The units before them in the ring, the last of which is given back last (but for a lone Q tile: K before the V of
+        // the tile before it).
+        const int u = t * kTile + (of_v ? NQB : 0), old = u + n - 1 - kRing;
+        if (old >= 0) {
+          const int to = old / kTile;
+          ok = wait(old % kTile < NQB ? &sh->k_empty[to % kTiles] : &sh->v_empty[to % kTiles], (to / kTiles) & 1);
+          if (Work::kLone && ok && to > 0 && old % kTile < n - 1 && old % kTile < NQB)
+            ok = wait(&sh->v_empty[(to - 1) % kTiles], ((to - 1) / kTiles) & 1);
+          if (!ok) break;
         }
-        if (ok) ++t;
+        uint64_t* bar = of_v ? &sh->v_full[t % kTiles] : &sh->k_full[t % kTiles];
+        ++t;
+        if (lane == 0) mbar_arrive_expect_tx(bar, n * kUnit);
+        __syncwarp();
+        for (int idx = lane; idx < npg * n; idx += 32) {  // npg divides 32: the page stays the lane's
+          const int e = idx / npg;
+          uint8_t* dst = sRing + (u + e) % kRing * kUnit + (idx % npg) * ps * 128;
+          if (!Work::kExpanded) tma_load_3d(dst, of_v ? &tm.v : &tm.k, bar, e * 64, off, plane);
+          else if (of_v) tma_load_3d(dst, &tm.v, bar, e * 64, x.g, x.key0 + j0);
+          else if (e * 64 < wk.dn) tma_load_3d(dst, &tm.k, bar, e * 64, x.g, x.key0 + j0);
+          else tma_load_3d(dst, &tm.kr, bar, 0, x.key0 + j0, 0);
+        }
       }
     }
     // Every copy has landed before shared memory is released, also after an abort.
     volatile int zero = 0;
     if (queries > 0) mbar_wait(&sh->q_full[0], (queries - 1) & 1, &zero, wk.status);
     if (last_q1 > 0) mbar_wait(&sh->q_full[1], (last_q1 - 1) & 1, &zero, wk.status);
-    for (int i = max(0, issued - 2 * kTiles); i < issued; ++i) {
-      const int of = i / 2;
-      mbar_wait(i & 1 ? &sh->v_full[of % kTiles] : &sh->k_full[of % kTiles], (of / kTiles) & 1, &zero, wk.status);
-    }
+    for (int i = max(0, t - kTiles); i < t; ++i)
+      mbar_wait(of_v ? &sh->v_full[i % kTiles] : &sh->k_full[i % kTiles], (i / kTiles) & 1, &zero, wk.status);
     __syncwarp();
   } else {
     // ================================================================ MMA issuer
