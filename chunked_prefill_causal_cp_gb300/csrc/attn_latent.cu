@@ -399,6 +399,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit_elect(&sh->empty[pv.slot]);
         pv.advance(L.slots);
         if (v1 > 0) {
+          // The next tile's scores, where their keys are there: the softmax waits for them.
+          if (more && next + 1 == L.ngroups && ready(&sh->full[qk.slot], qk.turn)) ok = group(next++);
           output(v1 / 2, d + 2 * kPairs, v_lo + pv.slot * slot_step, idesc_pv, acc);
           mma_commit_elect(&sh->empty[pv.slot]);
           pv.advance(L.slots);
