@@ -60,6 +60,7 @@ constexpr int kMaxSlots = 8;
 constexpr int kPairs = 64;                // (row, head) pairs of a tile
 constexpr uint32_t kSmem = 232448;        // of a CTA, at most
 constexpr float kRescaleLog2 = 8.0f;
+constexpr int kCombineCtas = 2 * kSms;
 
 // A (tile of pairs, split) of the call: what the scheduling warp hands to the others.
 struct Item {
@@ -615,17 +616,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// A pair's splits are merged in four slices -- split i in slice i % 4, a slice's in
-// order -- and the slices in order.  dv threads a pair: a slice is dv / 4 of them, a
-// thread four channels.
-constexpr int kSlices = 4;
-
+// A pair's parts are merged in slices -- part i in slice i mod `slices`, a slice's in order
+// -- and the slices in order.  dv threads a pair, or a quarter of its channels (`cut` is 4):
+// four or sixteen slices, a thread four channels.
 template <typename T>
-__global__ void __launch_bounds__(512) latent_combine_kernel(const Work a, const int per) {
+__global__ void __launch_bounds__(512) latent_combine_kernel(const Work a, const int per, const int cut, const int groups) {
   __shared__ float4 so[512];
-  __shared__ float2 sml[4 * kSlices];
+  __shared__ float2 sml[16];
   pdl_launch_dependents();
-  const int groups = (a.q_rows + per - 1) / per, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31;
   int w = blockIdx.x / groups;   // tile of pairs of the call
   long long all = 0, before = 0;  // tiles of keys of the call; of the sequences before this one
   int s = -1, tile = 0;
@@ -655,73 +654,76 @@ __global__ void __launch_bounds__(512) latent_combine_kernel(const Work a, const
   int r = 0, p = 0, row0 = 0;
   const bool found = s >= 0 && a.bounds(s, r, p, row0);  // the same for all threads
   const int each = found ? a.key_tiles(s) : 1;
-  const UnitShares u(max(all, 1ll), found ? before + (long long)tile * (kStart + each) : 0, each, a.ctas);
-  pdl_wait();  // on all paths: this kernel's end stands for the parts' kernel's
-  if (!found) return;
-  if (u.from == u.to) return;  // finished by its one CTA
   const int first = tile * kPairs, pairs = min(kPairs, r * a.hq - first);
-  const int seen = p + (first + pairs - 1) / a.hq + 1;  // keys of the tile
-  const int c4 = a.dv / 4, mine = threadIdx.x / a.dv, slice = threadIdx.x % a.dv / c4, d4 = threadIdx.x % c4;
-  const int m = blockIdx.x % groups * per + mine;
-  const bool on = m < pairs;
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  float mx = -INFINITY, l = 0.f;
-  if (on) {
-    constexpr int kAhead = 4;
-    for (int c0 = u.from + slice; c0 <= u.to; c0 += kAhead * kSlices) {
-      float2 ml[kAhead];
-      float4 x[kAhead];
-      int n = 0;
+  const int seen = found ? (p + (first + pairs - 1) / a.hq) / kTile + 1 : 1;  // tiles of keys, by the last row
+  const UnitShares u(max(all, 1ll), found ? before + (long long)tile * (kStart + each) + kStart : 0, each, seen, a.ctas);
+  pdl_wait();  // on all paths: this kernel's end stands for the parts' kernel's
+  if (!found || u.whole) return;
+  const int slices = 4 * cut, c4 = a.dv / slices, mine = threadIdx.x / a.dv, slice = threadIdx.x % a.dv / c4;
+  const int group = blockIdx.x % groups, d4 = group % cut * c4 + threadIdx.x % c4;
+  for (int m0 = group / cut * per; m0 < pairs; m0 += groups / cut * per) {
+    const int m = m0 + mine;
+    const bool on = m < pairs;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    float mx = -INFINITY, l = 0.f;
+    if (on) {
+      constexpr int kAhead = 4;
+      for (int c0 = u.from + slice; c0 <= u.to; c0 += kAhead * slices) {
+        float2 ml[kAhead];
+        float4 x[kAhead];
+        int n = 0;
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int c = c0 + j * kSlices;
-        if (c > u.to || u.start(c) * kTile >= seen) break;
-        const long long row = (long long)u.part(c) * kPairs + m;
-        ml[j] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + row * 2));
-        x[j] = __ldcg(reinterpret_cast<const float4*>(a.part_o + row * a.dv + 4 * d4));
-        n = j + 1;
-      }
+        for (int j = 0; j < kAhead; ++j) {
+          const int c = c0 + j * slices;
+          if (c > u.to) break;
+          const int row = u.part(c) * kPairs + m;
+          ml[j] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + row * 2));
+          x[j] = __ldcg(reinterpret_cast<const float4*>(a.part_o) + row * (a.dv / 4) + d4);
+          n = j + 1;
+        }
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        if (j >= n) break;
-        const float mn = fmaxf(mx, ml[j].x), z = mn == -INFINITY ? 0.f : mn;
-        const float k0 = ex2_approx(mx - z), k1 = ex2_approx(ml[j].x - z);
-        v.x = v.x * k0 + x[j].x * k1;
-        v.y = v.y * k0 + x[j].y * k1;
-        v.z = v.z * k0 + x[j].z * k1;
-        v.w = v.w * k0 + x[j].w * k1;
-        l = l * k0 + ml[j].y * k1;
-        mx = mn;
+        for (int j = 0; j < kAhead; ++j) {
+          if (j >= n) break;
+          const float mn = fmaxf(mx, ml[j].x), z = mn == -INFINITY ? 0.f : mn;
+          const float k0 = ex2_approx(mx - z), k1 = ex2_approx(ml[j].x - z);
+          v.x = v.x * k0 + x[j].x * k1;
+          v.y = v.y * k0 + x[j].y * k1;
+          v.z = v.z * k0 + x[j].z * k1;
+          v.w = v.w * k0 + x[j].w * k1;
+          l = l * k0 + ml[j].y * k1;
+          mx = mn;
+        }
       }
     }
+    so[threadIdx.x] = v;
+    if (threadIdx.x % c4 == 0) sml[mine * slices + slice] = make_float2(mx, l);
+    __syncthreads();
+    if (slice == 0 && on) {
+      mx = -INFINITY;
+      for (int i = 0; i < slices; ++i) mx = fmaxf(mx, sml[mine * slices + i].x);
+      const float z = mx == -INFINITY ? 0.f : mx;
+      v = make_float4(0.f, 0.f, 0.f, 0.f);
+      l = 0.f;
+#pragma unroll 4
+      for (int i = 0; i < slices; ++i) {
+        const float4 x = so[threadIdx.x + i * c4];
+        const float2 y = sml[mine * slices + i];
+        const float k = ex2_approx(y.x - z);
+        v.x = fmaf(k, x.x, v.x);
+        v.y = fmaf(k, x.y, v.y);
+        v.z = fmaf(k, x.z, v.z);
+        v.w = fmaf(k, x.w, v.w);
+        l = fmaf(k, y.y, l);
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float o[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+      uint2 b;
+      b.x = Pack<T>::store(o);
+      b.y = Pack<T>::store(o + 2);
+      *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + ((long long)row0 * a.hq + first + m) * a.dv + 4 * d4) = b;
+    }
+    __syncthreads();  // the slices are read
   }
-  so[threadIdx.x] = v;
-  if (d4 == 0) sml[mine * kSlices + slice] = make_float2(mx, l);
-  __syncthreads();
-  if (slice != 0 || !on) return;
-  mx = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < kSlices; ++i) mx = fmaxf(mx, sml[mine * kSlices + i].x);
-  const float z = mx == -INFINITY ? 0.f : mx;
-  v = make_float4(0.f, 0.f, 0.f, 0.f);
-  l = 0.f;
-#pragma unroll
-  for (int i = 0; i < kSlices; ++i) {
-    const float4 x = so[threadIdx.x + i * c4];
-    const float2 y = sml[mine * kSlices + i];
-    const float k = ex2_approx(y.x - z);
-    v.x = fmaf(k, x.x, v.x);
-    v.y = fmaf(k, x.y, v.y);
-    v.z = fmaf(k, x.z, v.z);
-    v.w = fmaf(k, x.w, v.w);
-    l = fmaf(k, y.y, l);
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const float o[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
-  uint2 b;
-  b.x = Pack<T>::store(o);
-  b.y = Pack<T>::store(o + 2);
-  *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + ((long long)row0 * a.hq + first + m) * a.dv + 4 * d4) = b;
 }
 
 template <typename T, bool kPaged>
@@ -754,9 +756,13 @@ cudaError_t launch_t(const RowsAttnArgs& args, int dtype, cudaStream_t st) {
   const uint32_t smem = std::max(l.alloc, 120u * 1024u);  // one CTA an SM: each takes all of TMEM
   e = launch_pdl(latent_kernel<T, kPaged>, dim3(a.ctas), dim3(kThreads), smem, st, tq, tk, a, l);
   if (e != cudaSuccess || !a.split) return e;
-  const int per = std::max(1, 256 / a.dv);
-  return launch_pdl(latent_combine_kernel<T>, dim3((unsigned)(a.tiles * ((a.q_rows + per - 1) / per))), dim3(per * a.dv), 0, st,
-                    a, per);
+  // With few pairs, of up to 152 parts each, their channels go to four CTAs (one row of 32 heads over 8000 keys
+  // 22.8 -> 15.2 us in all; past one CTA an SM it was slower: two rows of 64 heads 19 -> 26 us); with many, a CTA
+  // takes several pairs of its tile, which it has to find but once (64 rows of 64 heads 168 -> 147 us).
+  const int cut = 4 * a.tiles * a.q_rows <= kSms ? 4 : 1, per = cut > 1 ? 1 : std::max(1, 256 / a.dv);
+  const long long most = std::max<long long>(1, kCombineCtas / a.tiles);
+  const int groups = cut * (int)std::min<long long>((a.q_rows + per - 1) / per, most);
+  return launch_pdl(latent_combine_kernel<T>, dim3((unsigned)(a.tiles * groups)), dim3(per * a.dv), 0, st, a, per, cut, groups);
 }
 
 }  // namespace

@@ -53,12 +53,12 @@ struct TreeWork : pairs::WorkBase {
 };
 
 constexpr int kCombineRows = 8;
+constexpr int kCombineCtas = 4 * kSms;
 
 // Eight rows of a Q tile of a split sequence; lanes by row first, as the parts lie.
 template <typename T, int NVB, bool kPaged>
-__global__ void __launch_bounds__(kCombineRows * NVB * 16) tree_combine_kernel(const TreeWork<kPaged> wk) {
+__global__ void __launch_bounds__(kCombineRows * NVB * 16) tree_combine_kernel(const TreeWork<kPaged> wk, const int groups) {
   pdl_launch_dependents();
-  const int groups = 128 / kCombineRows;
   const int group = blockIdx.x % groups, g = blockIdx.y, lane = threadIdx.x & 31;
   int w = blockIdx.x / groups;  // Q tile of the call
   long long all = 0, first = 0;  // tiles of keys of the call; of the sequences before this one
@@ -88,50 +88,50 @@ __global__ void __launch_bounds__(kCombineRows * NVB * 16) tree_combine_kernel(c
   int r = 0, p = 0, row0 = 0;
   const bool known = s >= 0 && wk.bounds(s, r, p, row0);
   const int item = tile / 2, each = known ? wk.key_tiles(s) : 1;
-  const UnitShares u(max(all, 1ll), known ? first + ((long long)g * wk.q_pairs(r) + item) * (kStart + each) : 0, each, wk.ctas);
+  const int seen = known ? (p + min(r, (item + 1) * 2 * wk.tok_tile) - 1) / pairs::kKeys + 1 : 1;  // tiles of keys
+  const UnitShares u(max(all, 1ll), known ? first + ((long long)g * wk.q_pairs(r) + item) * (kStart + each) + kStart : 0, each,
+                     seen, wk.ctas);
   pdl_wait();  // on all paths: this kernel's end stands for the parts' kernel's
-  if (!known) return;
-  if (u.from == u.to) return;  // finished by its one CTA
-  const int m = group * kCombineRows + threadIdx.x % kCombineRows, c4 = threadIdx.x / kCombineRows;
-  const int tok = tile * wk.tok_tile + m / wk.group;
-  if (m >= wk.tok_tile * wk.group || tok >= r) return;
-  const int row = (tile & 1) * 128 + m;
-  const int seen = p + min(r, (item + 1) * 2 * wk.tok_tile);  // keys of the unit
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  float mx = -INFINITY, l = 0.f;
-  constexpr int kAhead = 8;
-  for (int c0 = u.from; c0 <= u.to; c0 += kAhead) {
-    float2 ml[kAhead];
-    float4 x[kAhead];
-    int n = 0;
+  if (!known || u.whole) return;
+  const int c4 = threadIdx.x / kCombineRows, rows = min(wk.tok_tile, r - tile * wk.tok_tile) * wk.group;
+  for (int m = group * kCombineRows + threadIdx.x % kCombineRows; m < rows; m += groups * kCombineRows) {
+    const int row = (tile & 1) * 128 + m;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    float mx = -INFINITY, l = 0.f;
+    constexpr int kAhead = 8;
+    for (int c0 = u.from; c0 <= u.to; c0 += kAhead) {
+      float2 ml[kAhead];
+      float4 x[kAhead];
+      int n = 0;
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      if (c0 + j > u.to || u.start(c0 + j) * pairs::kKeys >= seen) break;
-      const long long part = u.part(c0 + j);
-      ml[j] = __ldcg(reinterpret_cast<const float2*>(wk.part_ml) + part * 256 + row);
-      x[j] = __ldcg(reinterpret_cast<const float4*>(wk.part_o) + (part * (NVB * 16) + c4) * 256 + row);
-      n = j + 1;
-    }
+      for (int j = 0; j < kAhead; ++j) {
+        if (c0 + j > u.to) break;
+        const int part = u.part(c0 + j);
+        ml[j] = __ldcg(reinterpret_cast<const float2*>(wk.part_ml) + part * 256 + row);
+        x[j] = __ldcg(reinterpret_cast<const float4*>(wk.part_o) + (part * (NVB * 16) + c4) * 256 + row);
+        n = j + 1;
+      }
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      if (j >= n) break;
-      const float mn = fmaxf(mx, ml[j].x), z = mn == -INFINITY ? 0.f : mn;
-      const float k0 = ex2_approx(mx - z), k1 = ex2_approx(ml[j].x - z);
-      v.x = v.x * k0 + x[j].x * k1;
-      v.y = v.y * k0 + x[j].y * k1;
-      v.z = v.z * k0 + x[j].z * k1;
-      v.w = v.w * k0 + x[j].w * k1;
-      l = l * k0 + ml[j].y * k1;
-      mx = mn;
+      for (int j = 0; j < kAhead; ++j) {
+        if (j >= n) break;
+        const float mn = fmaxf(mx, ml[j].x), z = mn == -INFINITY ? 0.f : mn;
+        const float k0 = ex2_approx(mx - z), k1 = ex2_approx(ml[j].x - z);
+        v.x = v.x * k0 + x[j].x * k1;
+        v.y = v.y * k0 + x[j].y * k1;
+        v.z = v.z * k0 + x[j].z * k1;
+        v.w = v.w * k0 + x[j].w * k1;
+        l = l * k0 + ml[j].y * k1;
+        mx = mn;
+      }
     }
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // a NaN stays
+    const float o[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+    uint2 b;
+    b.x = Pack<T>::store(o);
+    b.y = Pack<T>::store(o + 2);
+    const long long out = (long long)(row0 + tile * wk.tok_tile + m / wk.group) * wk.hq + g * wk.group + m % wk.group;
+    *reinterpret_cast<uint2*>(static_cast<T*>(wk.out) + out * (NVB * 64) + 4 * c4) = b;
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;  // a NaN stays
-  const float o[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
-  uint2 b;
-  b.x = Pack<T>::store(o);
-  b.y = Pack<T>::store(o + 2);
-  const long long out = (long long)(row0 + tok) * wk.hq + g * wk.group + m % wk.group;
-  *reinterpret_cast<uint2*>(static_cast<T*>(wk.out) + out * (NVB * 64) + 4 * c4) = b;
 }
 
 template <typename T, int NB, bool kPaged>
@@ -168,8 +168,12 @@ cudaError_t launch_t(const RowsAttnArgs& a, int dtype, cudaStream_t st) {
   tm.kr = tm.k;
   cudaError_t e = pairs::launch<T, NB, NB>(tm, wk, a.ctas, st);
   if (e != cudaSuccess || !a.split) return e;
-  const dim3 grid((unsigned)(a.tiles * (128 / kCombineRows)), a.hkv);
-  return launch_pdl(tree_combine_kernel<T, NB, kPaged>, grid, dim3(kCombineRows * NB * 16), 0, st, wk);
+  // A CTA takes several groups of rows of its Q tile, which it has to find but once (64 trees of 8 nodes 239 -> 203
+  // us in all).
+  const long long most = std::max<long long>(1, kCombineCtas / (a.tiles * a.hkv));
+  const int groups = (int)std::min<long long>(128 / kCombineRows, most);
+  return launch_pdl(tree_combine_kernel<T, NB, kPaged>, dim3((unsigned)(a.tiles * groups), a.hkv), dim3(kCombineRows * NB * 16), 0, st,
+                    wk, groups);
 }
 
 template <typename T>

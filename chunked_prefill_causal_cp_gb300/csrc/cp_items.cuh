@@ -151,15 +151,18 @@ struct ShareCursor {
   }
 };
 
-// The CTAs of a unit of n tiles, first to last, and the tile of keys from which on each has it.
+// The CTAs that have a unit's n tiles, from `first` of the call on (where the shares count), of which the first `seen` are
+// computed: those that left parts are [from, to], unless one has them all.
 struct UnitShares {
-  Shares shares;
-  long long first;  // of its tiles, where the shares count
   int from, to;
-  __device__ __forceinline__ UnitShares(long long all, long long unit, int n, int grid)
-      : shares(all, grid), first(unit + kStart), from(shares.of(first)), to(shares.of(first + n - 1)) {}
-  __device__ __forceinline__ long long start(int c) const { return max(shares.begin(c) - first, 0ll); }
-  __device__ __forceinline__ int part(int c) const { return 2 * c + (shares.begin(c) <= first); }
+  bool whole;
+  __device__ __forceinline__ UnitShares(long long all, long long first, int n, int seen, int grid) {
+    const Shares shares(all, grid);
+    from = shares.of(first);
+    to = shares.of(first + seen - 1);
+    whole = shares.of(first + n - 1) == from;
+  }
+  __device__ __forceinline__ int part(int c) const { return 2 * c + (c == from); }
 };
 
 // A sequence's parents of up to CP_TREE_MAX rows, as bytes: one out of range counts as -1 and sets CP_DEV_BOUNDS.

@@ -635,7 +635,7 @@ int cp_latent_append(const cp_latent_desc* desc, const cp_qk_prep* prep, const v
  *                 CP_ERR_INVALID_ARG; cp_latent_tree_commit advances them)
  * A row's result depends on its own sequence and, in its last bits, on the rows and
  * positions of the call's other sequences: the keys are shared out over the SMs by
- * the whole call's sizes (not by its bounds).  Scores, softmax sums and outputs are held in
+ * the whole call's sizes (not by max_ctx).  Scores, softmax sums and outputs are held in
  * 32 bits; the softmax's weights are rounded to the layer's type for their
  * product with the latents.  Slots past a sequence's positions may hold anything.  A NaN,
  * or an infinite value (x[0, C), v), makes the rows that see its position non-finite (in
