@@ -20,8 +20,8 @@
 // and only when some score passes its pair's maximum by more than 2^8 do they exchange
 // maxima, leave the factors in shared memory and pass over O.
 //
-// One persistent CTA an SM, 384 threads: warp 0 TMA producer, warp 1 TMEM and MMA issue,
-// warp 2 scheduling (finds the CTA's items, two ahead), warps 4-11 softmax and output.
+// One persistent CTA an SM, 384 threads: warps 0 and 3 TMA producers, warp 1 TMEM and MMA
+// issue, warp 2 scheduling (finds the CTA's items, two ahead), warps 4-11 softmax and output.
 // A stage's blocks of 64 channels land, and are given back, in two groups -- the first
 // 256 channels and the rotated part, and the next 256 -- so that with only two stages
 // the first half of a tile's scores fills the wait for the softmax of the one before, and
@@ -193,13 +193,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh->item_full[i], 1);
-      mbar_init(&sh->item_empty[i], 10);  // warps 0, 1 and the eight of softmax
+      mbar_init(&sh->item_empty[i], 11);  // warps 0, 1, 3 and the eight of softmax
       mbar_init(&sh->s_full[i], 1);
     }
     mbar_init(&sh->q_full, 1);
     mbar_init(&sh->q_empty, 1);
     for (int i = 0; i < L.slots; ++i) {
-      mbar_init(&sh->full[i], 1);
+      mbar_init(&sh->full[i], 2);  // both producers
       mbar_init(&sh->empty[i], 1);
     }
     mbar_init(&sh->p_ready, 256);
@@ -253,12 +253,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!more) break;
     }
     __syncwarp();
-  } else if (warp == 3) {
     if (blockIdx.x == 0 && a.status && a.rows.rows_uniform <= 0)
       for (int s = lane; s < a.rows.num_seqs; s += 32)
         if (seq_rows(a.rows, s) < 1) atomicOr(a.status, CP_DEV_BOUNDS);
-  } else if (warp == 0) {
-    // ================================================================ producer
+  } else if (warp != 1 && warp < 4) {
+    // ================================================================ producers: each of every other block
+    const int odd = warp == 3;
     const int ps = kPaged ? min(a.cache.page_size, kTile) : kTile, lps = kPaged ? 31 - __clz(a.cache.page_size) : 0;
     const int npg = kTile / ps;  // boxes of a block
     Ring ring, rot;
@@ -268,14 +268,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     Item x;
     for (int k = 0; ok && take(k, x); ++k) {
       give(k);
-      if (k > 0) ok = wait(&sh->q_empty, (k - 1) & 1);
+      if (k > 0 && !odd) ok = wait(&sh->q_empty, (k - 1) & 1);
       if (!ok) break;
-      if (lane == 0) {
+      if (lane == 0 && !odd) {
         mbar_arrive_expect_tx(&sh->q_full, L.nqb * a.q_rows * 128);
         for (int b = 0; b < L.nqb; ++b) tma_load_3d(smem + b * L.q_block, &tm_q, &sh->q_full, b * 64, x.row0 * a.hq + x.first, 0);
       }
       __syncwarp();
-      queries = k + 1;
+      queries = odd ? 0 : k + 1;
       for (int i = 0; ok && i < x.ntiles; ++i, rot.advance(L.rot_slots)) {
         const int j0 = x.j_begin + i * kTile;
         // This lane's boxes: idx = lane, lane + 32, ...: page idx % npg of block idx / npg.
@@ -294,13 +294,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int st = ring.slot, nv = min(4, L.nvb - 4 * j);
           if (groups >= L.slots) ok = wait(&sh->empty[st], ring.turn ^ 1);
           if (!ok) break;
-          const int nb = nv + (j == 0 ? L.nqb - L.nvb : 0);  // the first group also has the rotated part
+          // The first group also has the rotated part, behind its values.
+          const int nb = (nv + (j == 0 ? L.nqb - L.nvb : 0) + 1 - odd) / 2;  // this warp's blocks
           begun |= 1u << st;
           phase ^= 1u << st;
           if (lane == 0) mbar_arrive_expect_tx(&sh->full[st], nb * kBlock);
           __syncwarp();
           for (int idx = lane; idx < npg * nb; idx += 32) {  // npg divides 32: the page stays the lane's
-            const int e = idx / npg;
+            const int e = 2 * (idx / npg) + odd;
             uint8_t* to = e < nv ? sSlot + st * L.slot_bytes + e * kBlock : smem + L.rot_off + rot.slot * kBlock;
             tma_load_3d(to + (idx % npg) * ps * 128, &tm_k, &sh->full[st], (e < nv ? 4 * j + e : L.nvb) * 64, off, plane);
           }
