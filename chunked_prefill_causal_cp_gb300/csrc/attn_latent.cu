@@ -60,7 +60,7 @@ constexpr int kMaxSlots = 8;
 constexpr int kPairs = 64;                // (row, head) pairs of a tile
 constexpr uint32_t kSmem = 232448;        // of a CTA, at most
 constexpr float kRescaleLog2 = 8.0f;
-constexpr int kCombineCtas = 2 * kSms;
+constexpr int kCombineThreads = 1024 * kSms;
 
 // A (tile of pairs, split) of the call: what the scheduling warp hands to the others.
 struct Item {
@@ -761,7 +761,7 @@ cudaError_t launch_t(const RowsAttnArgs& args, int dtype, cudaStream_t st) {
   // 22.8 -> 15.2 us in all; past one CTA an SM it was slower: two rows of 64 heads 19 -> 26 us); with many, a CTA
   // takes several pairs of its tile, which it has to find but once (64 rows of 64 heads 168 -> 147 us).
   const int cut = 4 * a.tiles * a.q_rows <= kSms ? 4 : 1, per = cut > 1 ? 1 : std::max(1, 256 / a.dv);
-  const long long most = std::max<long long>(1, kCombineCtas / a.tiles);
+  const long long most = std::max<long long>(1, kCombineThreads / (per * a.dv * a.tiles));
   const int groups = cut * (int)std::min<long long>((a.q_rows + per - 1) / per, most);
   return launch_pdl(latent_combine_kernel<T>, dim3((unsigned)(a.tiles * groups)), dim3(per * a.dv), 0, st, a, per, cut, groups);
 }
