@@ -621,45 +621,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 // -- and the slices in order.  dv threads a pair, or a quarter of its channels (`cut` is 4):
 // four or sixteen slices, a thread four channels.
 template <typename T>
-__global__ void __launch_bounds__(512) latent_combine_kernel(const Work a, const int per, const int cut, const int groups) {
+__global__ void __launch_bounds__(512) latent_combine_kernel(const Work a, const int per, const int cut, const int groups,
+                                                              const bool by_share) {
   __shared__ float4 so[512];
   __shared__ float2 sml[16];
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  int w = blockIdx.x / groups;   // tile of pairs of the call
-  long long all = 0, before = 0;  // tiles of keys of the call; of the sequences before this one
-  int s = -1, tile = 0;
-  for (int q0 = 0; q0 < a.rows.num_seqs; q0 += 32) {
-    const int q = q0 + lane;
-    int r, p, row0;
-    long long tiles = 0, sum = 0;
-    if (q < a.rows.num_seqs && a.bounds(q, r, p, row0)) {
-      tiles = a.pair_tiles(r);
-      sum = tiles * (kStart + a.key_tiles(q));
-    }
-    const long long own = sum;
-    sum = warp_prefix(sum);
-    if (s < 0) {
-      const long long inc = warp_prefix(tiles), total = __shfl_sync(0xffffffffu, inc, 31);
-      if (w < total) {
-        const int at = __ffs(__ballot_sync(0xffffffffu, inc > w)) - 1;
-        s = q0 + at;
-        tile = (int)(w - __shfl_sync(0xffffffffu, inc - tiles, at));
-        before = all + __shfl_sync(0xffffffffu, sum - own, at);
-      } else {
-        w -= (int)total;
-      }
-    }
-    all += __shfl_sync(0xffffffffu, sum, 31);
-  }
+  const int nth = blockIdx.x / groups;
+  const MergedUnit<Work> x(a, nth, by_share, a.ctas);
   int r = 0, p = 0, row0 = 0;
-  const bool found = s >= 0 && a.bounds(s, r, p, row0);  // the same for all threads
-  const int each = found ? a.key_tiles(s) : 1;
-  const int first = tile * kPairs, pairs = min(kPairs, r * a.hq - first);
+  const bool found = x.s >= 0 && a.bounds(x.s, r, p, row0);  // the same for all threads
+  const int first = found ? x.unit * kPairs : 0, pairs = min(kPairs, r * a.hq - first);
   const int seen = found ? (p + (first + pairs - 1) / a.hq) / kTile + 1 : 1;  // tiles of keys, by the last row
-  const UnitShares u(max(all, 1ll), found ? before + (long long)tile * (kStart + each) + kStart : 0, each, seen, a.ctas);
+  const UnitShares u(x.all, found ? x.first : 0, found ? x.n : 1, seen, a.ctas);
   pdl_wait();  // on all paths: this kernel's end stands for the parts' kernel's
-  if (!found || u.whole) return;
+  if (!found || u.whole || (by_share && u.from != nth)) return;
   const int slices = 4 * cut, c4 = a.dv / slices, mine = threadIdx.x / a.dv, slice = threadIdx.x % a.dv / c4;
   const int group = blockIdx.x % groups, d4 = group % cut * c4 + threadIdx.x % c4;
   for (int m0 = group / cut * per; m0 < pairs; m0 += groups / cut * per) {
@@ -761,9 +736,10 @@ cudaError_t launch_t(const RowsAttnArgs& args, int dtype, cudaStream_t st) {
   // 22.8 -> 15.2 us in all; past one CTA an SM it was slower: two rows of 64 heads 19 -> 26 us); with many, a CTA
   // takes several pairs of its tile, which it has to find but once (64 rows of 64 heads 168 -> 147 us).
   const int cut = 4 * a.tiles * a.q_rows <= kSms ? 4 : 1, per = cut > 1 ? 1 : std::max(1, 256 / a.dv);
-  const long long most = std::max<long long>(1, kCombineThreads / (per * a.dv * a.tiles));
+  const bool by_share = a.tiles > a.ctas;  // only units between two CTAs are merged
+  const long long units = std::min<long long>(a.tiles, a.ctas), most = std::max<long long>(1, kCombineThreads / (per * a.dv * units));
   const int groups = cut * (int)std::min<long long>((a.q_rows + per - 1) / per, most);
-  return launch_pdl(latent_combine_kernel<T>, dim3((unsigned)(a.tiles * groups)), dim3(per * a.dv), 0, st, a, per, cut, groups);
+  return launch_pdl(latent_combine_kernel<T>, dim3((unsigned)(units * groups)), dim3(per * a.dv), 0, st, a, per, cut, groups, by_share);
 }
 
 }  // namespace

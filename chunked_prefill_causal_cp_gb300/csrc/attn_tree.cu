@@ -57,45 +57,21 @@ constexpr int kCombineCtas = 4 * kSms;
 
 // Eight rows of a Q tile of a split sequence; lanes by row first, as the parts lie.
 template <typename T, int NVB, bool kPaged>
-__global__ void __launch_bounds__(kCombineRows * NVB * 16) tree_combine_kernel(const TreeWork<kPaged> wk, const int groups) {
+__global__ void __launch_bounds__(kCombineRows * NVB * 16) tree_combine_kernel(const TreeWork<kPaged> wk, const int groups,
+                                                                                const bool by_share) {
   pdl_launch_dependents();
-  const int group = blockIdx.x % groups, g = blockIdx.y, lane = threadIdx.x & 31;
-  int w = blockIdx.x / groups;  // Q tile of the call
-  long long all = 0, first = 0;  // tiles of keys of the call; of the sequences before this one
-  int s = -1, tile = 0;
-  for (int q0 = 0; q0 < wk.rows.num_seqs; q0 += 32) {
-    const int q = q0 + lane;
-    int tiles = 0, r, p, row0;
-    long long mine = 0;
-    if (q < wk.rows.num_seqs && wk.bounds(q, r, p, row0)) {
-      tiles = (r - 1) / wk.tok_tile + 1;
-      mine = (long long)wk.q_pairs(r) * wk.hkv * (kStart + wk.key_tiles(q));
-    }
-    const long long sum = warp_prefix(mine);
-    if (s < 0) {
-      const int inc = (int)warp_prefix(tiles), total = __shfl_sync(0xffffffffu, inc, 31);
-      if (w < total) {
-        const int at = __ffs(__ballot_sync(0xffffffffu, inc > w)) - 1;
-        s = q0 + at;
-        tile = w - __shfl_sync(0xffffffffu, inc - tiles, at);
-        first = all + __shfl_sync(0xffffffffu, sum - mine, at);
-      } else {
-        w -= total;
-      }
-    }
-    all += __shfl_sync(0xffffffffu, sum, 31);
-  }
+  const int group = blockIdx.x % groups, nth = blockIdx.x / groups;
+  const MergedUnit<TreeWork<kPaged>> x(wk, nth, by_share, wk.ctas);
   int r = 0, p = 0, row0 = 0;
-  const bool known = s >= 0 && wk.bounds(s, r, p, row0);
-  const int item = tile / 2, each = known ? wk.key_tiles(s) : 1;
-  const int seen = known ? (p + min(r, (item + 1) * 2 * wk.tok_tile) - 1) / pairs::kKeys + 1 : 1;  // tiles of keys
-  const UnitShares u(max(all, 1ll), known ? first + ((long long)g * wk.q_pairs(r) + item) * (kStart + each) + kStart : 0, each,
-                     seen, wk.ctas);
+  const bool found = x.s >= 0 && wk.bounds(x.s, r, p, row0);
+  const int np = found ? wk.q_pairs(r) : 1, g = found ? x.unit / np : 0, t0 = found ? (x.unit - g * np) * 2 * wk.tok_tile : 0;
+  const int seen = found ? (p + min(r, t0 + 2 * wk.tok_tile) - 1) / pairs::kKeys + 1 : 1;  // tiles of keys
+  const UnitShares u(x.all, found ? x.first : 0, found ? x.n : 1, seen, wk.ctas);
   pdl_wait();  // on all paths: this kernel's end stands for the parts' kernel's
-  if (!known || u.whole) return;
-  const int c4 = threadIdx.x / kCombineRows, rows = min(wk.tok_tile, r - tile * wk.tok_tile) * wk.group;
+  if (!found || u.whole || (by_share && u.from != nth)) return;
+  const int c4 = threadIdx.x / kCombineRows, per = wk.tok_tile * wk.group, rows = min(2 * wk.tok_tile, r - t0) * wk.group;
   for (int m = group * kCombineRows + threadIdx.x % kCombineRows; m < rows; m += groups * kCombineRows) {
-    const int row = (tile & 1) * 128 + m;
+    const int row = m < per ? m : 128 + m - per;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     float mx = -INFINITY, l = 0.f;
     constexpr int kAhead = 8;
@@ -129,7 +105,7 @@ __global__ void __launch_bounds__(kCombineRows * NVB * 16) tree_combine_kernel(c
     uint2 b;
     b.x = Pack<T>::store(o);
     b.y = Pack<T>::store(o + 2);
-    const long long out = (long long)(row0 + tile * wk.tok_tile + m / wk.group) * wk.hq + g * wk.group + m % wk.group;
+    const long long out = (long long)(row0 + t0 + m / wk.group) * wk.hq + g * wk.group + m % wk.group;
     *reinterpret_cast<uint2*>(static_cast<T*>(wk.out) + out * (NVB * 64) + 4 * c4) = b;
   }
 }
@@ -168,12 +144,12 @@ cudaError_t launch_t(const RowsAttnArgs& a, int dtype, cudaStream_t st) {
   tm.kr = tm.k;
   cudaError_t e = pairs::launch<T, NB, NB>(tm, wk, a.ctas, st);
   if (e != cudaSuccess || !a.split) return e;
-  // A CTA takes several groups of rows of its Q tile, which it has to find but once (64 trees of 8 nodes 239 -> 203
+  // A CTA takes several groups of rows of its unit, which it has to find but once (64 trees of 8 nodes 239 -> 203
   // us in all).
-  const long long most = std::max<long long>(1, kCombineCtas / (a.tiles * a.hkv));
-  const int groups = (int)std::min<long long>(128 / kCombineRows, most);
-  return launch_pdl(tree_combine_kernel<T, NB, kPaged>, dim3((unsigned)(a.tiles * groups), a.hkv), dim3(kCombineRows * NB * 16), 0, st,
-                    wk, groups);
+  const long long all = a.tiles * a.hkv, units = std::min<long long>(all, a.ctas);
+  const int groups = (int)std::min<long long>(256 / kCombineRows, std::max<long long>(1, kCombineCtas / units));
+  return launch_pdl(tree_combine_kernel<T, NB, kPaged>, dim3((unsigned)(units * groups)), dim3(kCombineRows * NB * 16), 0, st, wk,
+                    groups, all > units);
 }
 
 template <typename T>
@@ -190,8 +166,8 @@ RowsPlan tree_plan(int hq, int hkv, int dv, bool uniform, long long num_seqs, lo
   const int group = hq / hkv, key_tiles = (max_ctx - 1) / pairs::kKeys + 1;
   p.tok_tile = 128 / group;
   const long long rows = std::min<long long>(uniform ? total_rows / num_seqs : total_rows, CP_TREE_MAX);
-  const long long each = (rows + p.tok_tile - 1) / p.tok_tile;  // Q tiles of a sequence, at most
-  p.tiles = uniform ? num_seqs * each : std::min(total_rows / p.tok_tile + num_seqs, num_seqs * each);
+  const long long each = (rows - 1) / (2 * p.tok_tile) + 1;  // pairs of Q tiles of a sequence, at most
+  p.tiles = uniform ? num_seqs * each : std::min(total_rows / (2 * p.tok_tile) + num_seqs, num_seqs * each);
   p.work = (double)p.tiles * hkv * (kStart + key_tiles);
   p.ctas = (int)std::min<double>(p.work, kSms);
   p.split = key_tiles > 1;

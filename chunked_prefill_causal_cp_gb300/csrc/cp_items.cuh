@@ -95,6 +95,26 @@ struct TurnCursor {
   }
 };
 
+// A call's tiles of keys, kStart a unit among them: of sequence s, with units(s) units (0: it is skipped) of key_tiles(s);
+// of all.
+template <typename Work>
+__device__ __forceinline__ int slots_of(const Work& wk, int s, bool report, int& units) {
+  units = s < wk.rows.num_seqs ? wk.units(s, report) : 0;
+  return units > 0 ? kStart + wk.key_tiles(s) : 1;
+}
+template <typename Work>
+__device__ __forceinline__ long long all_tiles(const Work& wk, bool report) {
+  long long all = 0;
+  for (int s = threadIdx.x & 31; s < wk.rows.num_seqs; s += 32) {
+    int units;
+    const int each = slots_of(wk, s, report, units);
+    all += (long long)units * each;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+  return all;
+}
+
 // This CTA's share of the call's tiles of keys (see cp_latent.h), unit by unit: sequence s has
 // units(s) (0: it is skipped) of key_tiles(s) tiles each; make(s, unit, k0, n, x) describes n
 // tiles of one from tile k0 on.
@@ -107,23 +127,22 @@ struct ShareCursor {
   int each;                   // of a unit,
   long long mine;             // of the sequence
   __device__ __forceinline__ explicit ShareCursor(const Work& wk) {
-    long long all = 0;
-    for (; q0 < wk.rows.num_seqs; q0 += 32) {
+    long long all;
+    if (wk.rows.num_seqs <= 32) {
       load(wk, blockIdx.x == 0);
-      all += __shfl_sync(0xffffffffu, sum, 31);
+      all = __shfl_sync(0xffffffffu, sum, 31);
+    } else {
+      all = all_tiles(wk, blockIdx.x == 0);
+      load(wk, false);
     }
     const Shares shares(all, gridDim.x);
     const int c = min((int)blockIdx.x, shares.ctas);
     at = shares.begin(c);
     end = shares.begin(min(c + 1, shares.ctas));
-    const bool again = q0 > 32;  // else the one chunk is here
-    q0 = 0;
-    if (again) load(wk, false);
   }
   __device__ __forceinline__ void load(const Work& wk, bool report) {
-    const int s = q0 + (threadIdx.x & 31);
-    const int units = s < wk.rows.num_seqs ? wk.units(s, report) : 0;
-    each = units > 0 ? kStart + wk.key_tiles(s) : 1;
+    int units;
+    each = slots_of(wk, q0 + (threadIdx.x & 31), report, units);
     mine = (long long)units * each;
     sum = warp_prefix(mine);
   }
@@ -151,8 +170,53 @@ struct ShareCursor {
   }
 };
 
-// The CTAs that have a unit's n tiles, from `first` of the call on (where the shares count), of which the first `seen` are
-// computed: those that left parts are [from, to], unless one has them all.
+// What a CTA of a merging kernel does: unit `nth` of the call, or (by_share, where units are more than shares) the one
+// that share nth leaves to the next.
+template <typename Work>
+struct MergedUnit {
+  int s = -1, unit;      // sequence (-1: none), unit of it
+  int n;                 // its tiles
+  long long all, first;  // tiles of the call; of them, the first of the unit's
+  __device__ __forceinline__ MergedUnit(const Work& wk, int nth, bool by_share, int grid) {
+    int q0 = 0, units, each;
+    long long mine, sum, base = 0;
+    auto load = [&]() {
+      each = slots_of(wk, q0 + (threadIdx.x & 31), false, units);
+      mine = (long long)units * each;
+      sum = warp_prefix(mine);
+    };
+    load();
+    all = max(wk.rows.num_seqs <= 32 ? __shfl_sync(0xffffffffu, sum, 31) : all_tiles(wk, false), 1ll);
+    long long at = nth;
+    if (by_share) {
+      const Shares shares(all, grid);
+      if (nth + 1 >= shares.ctas) return;
+      at = shares.begin(nth + 1);
+    }
+    for (;;) {
+      const long long key = by_share ? mine : units, upto = by_share ? sum : warp_prefix(key);
+      const long long total = __shfl_sync(0xffffffffu, upto, 31);
+      if (at < total) {
+        const int lane = __ffs(__ballot_sync(0xffffffffu, upto > at)) - 1;
+        const int slots = __shfl_sync(0xffffffffu, each, lane);
+        at -= __shfl_sync(0xffffffffu, upto - key, lane);
+        s = q0 + lane;
+        unit = (int)(by_share ? Shares::quotient(at, slots) : at);
+        n = slots - kStart;
+        first = base + __shfl_sync(0xffffffffu, sum - mine, lane) + (long long)unit * slots + kStart;
+        return;
+      }
+      at -= total;
+      base += __shfl_sync(0xffffffffu, sum, 31);
+      q0 += 32;
+      if (q0 >= wk.rows.num_seqs) return;
+      load();
+    }
+  }
+};
+
+// The CTAs that have a unit's n tiles, from `first` of the call on, of which the first `seen` are computed: those that
+// left parts are [from, to], unless one has them all.
 struct UnitShares {
   int from, to;
   bool whole;

@@ -80,7 +80,7 @@ struct RowsAttnArgs {
   int ctas;                // that share the work
   int q_rows;              // a latent cache's: pairs of a tile that the call can have, at most
   int tok_tile;            // a tree's: tokens of a Q tile
-  long long tiles;         // of pairs, or Q tiles, at most
+  long long tiles;         // of pairs, or pairs of Q tiles, at most
   bool split;              // whether units may be shared by CTAs
   float* part_o;           // parts: unnormalised outputs,
   float* part_ml;          // their maximum (log2 domain) and sum

@@ -203,6 +203,21 @@ def test_a_rows_bits_are_its_own_and_the_sizes(kw):
 
 
 @pytest.mark.parametrize("kw", BOTH)
+def test_many_short_sequences(kw):
+    """More tiles of rows than SMs, few of which are split; some sequences without context, one-row ones among them."""
+    heads, kw = kw["heads"], {k: v for k, v in kw.items() if k != "heads"}
+    seqs = 333
+    past = [(7919 * (i + 3)) % 301 if i % 7 else 0 for i in range(seqs)]
+    rows = [1 + (5 * i) % 7 for i in range(seqs)]
+    x = Cache(BF16, heads, seqs, 320, 16, **kw)
+    x.fill([p + r for p, r in zip(past, rows)])
+    q = x.queries(sum(rows))
+    parents = [tree(r, "random", s) for s, r in enumerate(rows)]
+    x.check(q, x.attend(q, past, rows, parents), past, rows, parents)
+    assert int(x.status) == 0
+
+
+@pytest.mark.parametrize("kw", BOTH)
 @pytest.mark.parametrize("seqs", [1, 2, 40])
 def test_long_contexts_of_few_and_many_sequences(kw, seqs):
     """Splits of every size: one sequence over all SMs, many sequences of several items each."""
