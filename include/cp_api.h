@@ -634,8 +634,8 @@ int cp_latent_append(const cp_latent_desc* desc, const cp_qk_prep* prep, const v
  *   commit        not 0: seqlens_k[s] += rows of s after the attention (with parents:
  *                 CP_ERR_INVALID_ARG; cp_latent_tree_commit advances them)
  * A row's result depends on its own sequence and, in its last bits, on the rows and
- * positions of the call's other sequences: the keys are shared out over the SMs by
- * the whole call's sizes (not by max_ctx).  Scores, softmax sums and outputs are held in
+ * positions of the call's other sequences: the keys are shared out over the SMs, and
+ * the shares merged, by the whole call's sizes (not by max_ctx).  Scores, softmax sums and outputs are held in
  * 32 bits; the softmax's weights are rounded to the layer's type for their
  * product with the latents.  Slots past a sequence's positions may hold anything.  A NaN,
  * or an infinite value (x[0, C), v), makes the rows that see its position non-finite (in
@@ -674,7 +674,8 @@ size_t cp_workspace_size_latent(const cp_latent_desc* desc, int32_t total_rows, 
  *                 they were
  * The description's cache fields are checked as always but not used; nothing is
  * allocated, and no workspace is needed.  Precision and non-finite values as in
- * cp_latent_attn. */
+ * cp_latent_attn; a row's result depends on its own sequence and, in its last bits, on
+ * whether the call's rows are few (all heads' tiles of 128 rows at once on the SMs). */
 int cp_latent_chunk_attn(const cp_latent_desc* desc, const void* q, const void* k_nope, int64_t k_row_stride,
                          int64_t k_head_stride, const void* k_rope, int64_t k_rope_stride, const void* v,
                          int64_t v_row_stride, int64_t v_head_stride, const int32_t* cu_rows, const int32_t* cu_keys,
