@@ -337,6 +337,62 @@ def test_latent_commit_advances_lengths():
     assert lens.tolist() == [31, 8]
 
 
+@pytest.mark.parametrize("page", [0, 16])
+def test_steps_one_behind_another(page):
+    """Append, attention and the lengths' advance, 40 steps without a wait, the workspace and the lengths shared: bit for
+    bit what the same steps give with a wait after each call."""
+    n, heads, steps, past = 5, 32, 40, [0, 700, 61, 2000, 127]
+    g = torch.Generator().manual_seed(5)
+    rows = torch.randn(steps, n, 512 + 64, generator=g).to(BF16).cuda()
+    q = torch.randn(steps, n, heads, 512 + 64, generator=g).to(BF16).cuda()
+    kept = []
+    for wait in (lambda: None, torch.cuda.synchronize):
+        x = Cache(BF16, heads, n, 2100, page, latent=512, rope=64)
+        x.fill(past)
+        lens, out = ints(past), torch.full((steps, n, heads, 512), float("nan"), dtype=BF16, device="cuda")
+        ws = torch.full((cp.cp_workspace_size_latent(x.desc, n, 2100, n),), 255, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        for i in range(steps):
+            call = dict(block_table=x.table, dev_status=x.status)
+            cp.cp_latent_append(x.desc, cp.qk_prep(rot_dim=0), rows[i, :, :512], rows[i, :, 512:], x.x, lens, n, n, 2100, **call)
+            wait()
+            cp.cp_latent_attn(x.desc, q[i], x.x, lens, n, n, 2100, out[i], ws, commit=True, **call)
+            wait()
+        assert lens.tolist() == [p + steps for p in past] and int(x.status) == 0
+        x.check(q[-1], out[-1], [p + steps - 1 for p in past], [1] * n)
+        kept.append(out)
+    assert torch.equal(*kept)
+
+
+def test_trees_one_behind_another():
+    """A draft's rows in, its attention, the accepted path to its places and the lengths' advance, 20 times without a wait."""
+    n, rows, rounds, past = 4, 9, 20, [0, 300, 1000, 63]
+    parents = tree(rows, "heap")
+    g = torch.Generator().manual_seed(6)
+    q = torch.randn(rounds, n * rows, 8, 64, generator=g).to(F16).cuda()
+    new = torch.randn(rounds, 2, n * rows, 2, 64, generator=g).to(F16).cuda()
+    path = ints([[0, 2, 7]] * n)
+    count, par = ints([1, 3, 2, 0]), ints(parents * n)
+    kept = []
+    for wait in (lambda: None, torch.cuda.synchronize):
+        x = Cache(F16, 8, n, 1200, 16, kv=2, d=64)
+        x.fill(past)
+        lens, out = ints(past), torch.full((rounds, n * rows, 8, 64), float("nan"), dtype=F16, device="cuda")
+        ws = torch.full((cp.cp_workspace_size_tree(x.desc, n * rows, 1200, n),), 255, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        for i in range(rounds):
+            cp.cp_kv_append(x.desc, new[i, 0], new[i, 1], rows, x.k, x.v, lens, 1150, x.table, x.status)
+            wait()
+            cp.cp_tree_attn(x.desc, q[i], x.k, x.v, lens, par, n, n * rows, 1200, out[i], ws, block_table=x.table,
+                            dev_status=x.status)
+            wait()
+            cp.cp_tree_commit(x.desc, x.k, x.v, path, count, lens, n, 3, 1200, block_table=x.table, dev_status=x.status)
+            wait()
+        assert lens.tolist() == [p + rounds * c for p, c in zip(past, count.tolist())] and int(x.status) == 0
+        kept.append(out)
+    assert torch.equal(*kept) and torch.isfinite(kept[0].float()).all()
+
+
 @pytest.mark.parametrize("kw", BOTH)
 def test_capture_replay_and_two_streams(kw):
     """A captured call reads its buffers' present contents; calls on two streams keep apart with workspaces of their own."""
