@@ -109,7 +109,7 @@ cudaError_t launch_t(const ExpandedArgs& a, int dtype, long long items, cudaStre
 // Items of so many rows, at most.
 long long items_of(const ExpandedArgs& a, int rows) {
   if (a.rows.rows_uniform > 0) return ((long long)(a.rows.rows_uniform - 1) / rows + 1) * a.rows.num_seqs * a.heads;
-  return ((long long)a.total_rows / rows + a.rows.num_seqs) * a.heads;
+  return tiles_at_most(a.total_rows, a.rows.num_seqs, rows) * a.heads;
 }
 
 // Items are of one Q tile where all find an SM at once: half the work each, at a higher price

@@ -762,7 +762,7 @@ RowsPlan latent_plan(int heads, int dv, bool uniform, long long num_seqs, long l
   const long long pairs = (uniform ? total_rows / num_seqs : total_rows) * heads;  // of a sequence, at most
   const int key_tiles = (max_ctx - 1) / kTile + 1;
   p.q_rows = (int)std::min<long long>(kPairs, pairs);
-  p.tiles = uniform ? num_seqs * ((pairs + kPairs - 1) / kPairs) : pairs / kPairs + num_seqs;
+  p.tiles = uniform ? num_seqs * ((pairs + kPairs - 1) / kPairs) : tiles_at_most(pairs, num_seqs, kPairs);
   p.work = (double)p.tiles * (kStart + key_tiles);
   p.ctas = (int)std::min<double>(p.work, kSms);
   p.split = key_tiles > 1;

@@ -170,7 +170,7 @@ RowsPlan tree_plan(int hq, int hkv, int dv, bool uniform, long long num_seqs, lo
   p.tok_tile = 128 / group;
   const long long rows = std::min<long long>(uniform ? total_rows / num_seqs : total_rows, CP_TREE_MAX);
   const long long each = (rows - 1) / (2 * p.tok_tile) + 1;  // pairs of Q tiles of a sequence, at most
-  p.tiles = uniform ? num_seqs * each : std::min(total_rows / (2 * p.tok_tile) + num_seqs, num_seqs * each);
+  p.tiles = uniform ? num_seqs * each : std::min(tiles_at_most(total_rows, num_seqs, 2 * p.tok_tile), num_seqs * each);
   p.work = (double)p.tiles * hkv * (kStart + key_tiles);
   p.ctas = (int)std::min<double>(p.work, kSms);
   p.split = key_tiles > 1;

@@ -40,7 +40,11 @@ struct LatentAppendArgs {
 // fixed length, of a sequence's own or by the number of sequences, left the last CTA with
 // 14 to 30% more than the mean, or had as much again in starts, ends and parts.)
 constexpr int kSms = 152;
-constexpr int kStart = 4;  // what the start and end of a unit cost, in tiles
+// Tiles of so many rows that num_seqs sequences of total_rows rows in all can have.
+inline long long tiles_at_most(long long total_rows, long long num_seqs, long long rows) {
+  return (total_rows + num_seqs * (rows - 1)) / rows;
+}
+constexpr int kStart = 4;  // what the start and end of a unit cost, in tiles (2 to 6 are within 3%, 1 is up to a fifth slower)
 // The shares of `all` tiles: each CTA's, the first `more` of them one tile longer.
 struct Shares {
   int ctas;         // that have one: of a grid, at most a CTA for each tile
