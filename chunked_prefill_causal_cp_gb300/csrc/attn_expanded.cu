@@ -112,14 +112,15 @@ long long items_of(const ExpandedArgs& a, int rows) {
   return tiles_at_most(a.total_rows, a.rows.num_seqs, rows) * a.heads;
 }
 
-// Items are of one Q tile where all find an SM at once: half the work each, at a higher price
-// (a tile of keys 1.05 us for a lone Q tile, 1.75 us for a pair; 8 heads of 1000 rows after
-// 4000: 40 us, as pairs 76; 4 heads of 4864 after 8000, 152 Q tiles: 107 us, as pairs 176).
-// With more, pairs, which read K and V half as often.
+// Items are of one Q tile up to ten for each SM, or where few tiles have a second one beside them: the work is shared out
+// more evenly, and both warpgroups have some (8 heads of 1000 rows after 4000: 76 us as pairs, 40; 20 heads of 2048 after
+// 2000, 320 tiles: 88, 77; 1280 tiles: 474, 458; 512 prompts of 40 rows: 314, 272).  With more, pairs, which read K and V
+// half as often (2048 tiles: 1.24 ms, lone 1.28).
 template <typename T>
 cudaError_t launch_type(const ExpandedArgs& a, int dtype, cudaStream_t st) {
-  const long long lone = items_of(a, 128);
-  return lone <= kSms ? launch_t<T, true>(a, dtype, lone, st) : launch_t<T, false>(a, dtype, items_of(a, 256), st);
+  const long long lone = items_of(a, 128), pairs = items_of(a, 256);
+  if (lone <= 10 * kSms || 4 * pairs > 3 * lone) return launch_t<T, true>(a, dtype, lone, st);
+  return launch_t<T, false>(a, dtype, pairs, st);
 }
 
 }  // namespace

@@ -675,7 +675,7 @@ size_t cp_workspace_size_latent(const cp_latent_desc* desc, int32_t total_rows, 
  * The description's cache fields are checked as always but not used; nothing is
  * allocated, and no workspace is needed.  Precision and non-finite values as in
  * cp_latent_attn; a row's result depends on its own sequence and, in its last bits, on
- * whether the call's rows are few (all heads' tiles of 128 rows at once on the SMs). */
+ * how many tiles of 128 rows the call has. */
 int cp_latent_chunk_attn(const cp_latent_desc* desc, const void* q, const void* k_nope, int64_t k_row_stride,
                          int64_t k_head_stride, const void* k_rope, int64_t k_rope_stride, const void* v,
                          int64_t v_row_stride, int64_t v_head_stride, const int32_t* cu_rows, const int32_t* cu_keys,
