@@ -6,7 +6,8 @@
 // nope_dim + rope_dim channels, the rotated part as 64 of which those past rope_dim
 // are zeros.  The path is bound by the tensor cores.  Items are handed out with the
 // most keys first, heads fastest.  8128 rows of 32 heads, 128 + 64 and 128 channels, after
-// 8128 keys: 1.26 ms, 1.61 PFLOP/s, 0.85 of a large product's rate.
+// 8128 keys: 1.24 ms, 1.64 PFLOP/s, 0.86 of a large product's rate (call after call, under the
+// power cap, 1.35 ms, 0.88 of what such a product sustains).
 #include "attn_pairs.cuh"
 
 namespace cp {

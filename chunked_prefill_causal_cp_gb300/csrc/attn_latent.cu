@@ -43,8 +43,8 @@
 // pairs that several of them have leaves unnormalised fp32 parts and (maximum, sum) in
 // the workspace, which the combine kernel merges in order.
 //
-// Measured (bf16, 512 + 64 channels): 32 rows of 32 heads over 12000 to 40000 keys 162 us,
-// 5.9 TB/s, 0.87 of a copy's rate, bound by the cache's bytes; 2 x 45 rows of 64 heads over
+// Measured (bf16, 512 + 64 channels): 32 rows of 32 heads over 12000 to 40000 keys 165 us,
+// 5.8 TB/s, 0.85 of a copy's rate, bound by the cache's bytes; 2 x 45 rows of 64 heads over
 // 8000 to 16000 keys 199 us, 760 TFLOP/s, bound by the chain of a tile -- softmax 1200
 // clocks, half of V's product 400, half of the next scores 600, 100 to 300 from each to the
 // next -- of which the tensor cores work two thirds; one row of 32 heads over 1025 keys 11

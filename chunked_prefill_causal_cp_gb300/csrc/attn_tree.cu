@@ -5,9 +5,9 @@
 // whole context, and the CTAs share their tiles of keys out evenly (cp_latent.h); a unit
 // of more than one leaves unnormalised fp32 parts in the workspace, which the combine
 // kernel merges in order.  Each key's bytes are read once for a KV head's up to 256 rows:
-// 24 trees of 61 nodes, 32/8 heads x 128, over 4000 to 24000 keys in pages of 16: 260 us,
-// 5.4 TB/s of a copy's 6.8 and 1.29 PFLOP/s, between the cache's bytes and the chain of a
-// tile; of 30 nodes 230 us, 6.0 TB/s; one tree of 16 nodes over 1024 keys 13.4 us, latency.
+// 24 trees of 61 nodes, 32/8 heads x 128, over 4000 to 24000 keys in pages of 16: 264 us,
+// 5.3 TB/s of a copy's 6.8 and 1.27 PFLOP/s, between the cache's bytes and the chain of a
+// tile; of 30 nodes 230 us, 6.0 TB/s; one tree of 16 nodes over 1024 keys 14 us, latency.
 #include "attn_pairs.cuh"
 
 namespace cp {
