@@ -605,12 +605,19 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
         const float top = fmaxf(a.x, b.x), z = top == -INFINITY ? 0.f : top;
         k0 = ex2_approx(a.x - z);
         k1 = ex2_approx(b.x - z);
-        const float l = a.y * k0 + b.y * k1, inv = l == 0.f ? 0.f : 1.f / l;  // a NaN stays
-        k0 *= inv;
-        k1 *= inv;
+        const float l = a.y * k0 + b.y * k1;
+        if (x.whole) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;  // a NaN stays
+          k0 *= inv;
+          k1 *= inv;
+        } else if (w == 0 && row_ok && alive) {
+          *reinterpret_cast<float2*>(wk.part_ml + ((long long)x.part * 256 + m) * 2) = make_float2(top, l);
+        }
       }
       const uint32_t o0 = o_col - 256u * w;
-      uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(wk.out) + ((long long)(x.row0 + tok) * wk.hq + x.g) * (NVB * 64));
+      const long long row = (long long)(x.row0 + tok) * wk.hq + x.g * wk.group + mhead;
+      uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(wk.out) + row * (NVB * 64));
+      float4* part = reinterpret_cast<float4*>(wk.part_o) + ((long long)x.part * (NVB * 16)) * 256 + m;
 #pragma unroll
       for (int j = 0; j < NVB; ++j) {
         const int c = w * NVB + j;
@@ -630,7 +637,12 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
             for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(ov[e]), k1, o[e]);
           }
         }
-        if (row_ok && alive) {
+        if (!Work::kExpanded && !x.whole) {
+          if (row_ok && alive) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) part[(8 * c + e) * 256] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+        } else if (row_ok && alive) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             out[4 * c + e] = make_uint4(pack2<T>(o[8 * e], o[8 * e + 1]), pack2<T>(o[8 * e + 2], o[8 * e + 3]),

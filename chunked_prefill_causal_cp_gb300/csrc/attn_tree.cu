@@ -1,7 +1,7 @@
 // attn_tree.cu -- attention of drafted trees over a K/V cache, on the kernel of
 // attn_pairs.cuh.
 //
-// A tree's up to 128 nodes x G heads are one to a few pairs of Q tiles that read the
+// A tree's up to 128 nodes x G heads are one to a few (pairs of) Q tiles that read the
 // whole context, and the CTAs share their tiles of keys out evenly (cp_latent.h); a unit
 // of more than one leaves unnormalised fp32 parts in the workspace, which the combine
 // kernel merges in order.  Each key's bytes are read once for a KV head's up to 256 rows:
@@ -15,9 +15,10 @@ namespace {
 
 using pairs::Item;
 
-template <bool kPaged_>
+template <bool kPaged_, bool kLone_>  // units of one Q tile, or of two
 struct TreeWork : pairs::WorkBase {
-  static constexpr bool kPaged = kPaged_, kExpanded = false, kLone = false;
+  static constexpr bool kPaged = kPaged_, kExpanded = false, kLone = kLone_;
+  static constexpr int kQ = kLone ? 1 : 2;
   using Cursor = ShareCursor<TreeWork>;
   const int* past;
   int max_ctx, ctas;
@@ -30,25 +31,25 @@ struct TreeWork : pairs::WorkBase {
     row0 = seq_row0(rows, s);
     return p >= 0 && (long long)p + r <= max_ctx && row0 >= 0 && row0 <= total_rows - r && r <= CP_TREE_MAX;
   }
-  __device__ __forceinline__ int q_pairs(int r) const { return (r - 1) / (2 * tok_tile) + 1; }
+  __device__ __forceinline__ int q_units(int r) const { return (r - 1) / (kQ * tok_tile) + 1; }
   __device__ __forceinline__ int units(int s, bool report) const {
     int r, p, row0;
-    if (bounds(s, r, p, row0)) return q_pairs(r) * hkv;
+    if (bounds(s, r, p, row0)) return q_units(r) * hkv;
     if (report && status && r >= 1) atomicOr(status, CP_DEV_BOUNDS);
     return 0;
   }
   __device__ __forceinline__ int key_tiles(int s) const { return (past[s] + seq_rows(rows, s) - 1) / pairs::kKeys + 1; }
-  // Unit u of a sequence: (KV head, pair of Q tiles).
+  // Unit u of a sequence: (KV head, Q tile or pair of them).
   __device__ __forceinline__ bool make(int s, int u, int k0, int n, Item& x) const {
     if (!bounds(s, x.rows, x.past, x.row0)) return false;
-    const int np = q_pairs(x.rows);
+    const int np = q_units(x.rows);
     x.s = s;
     x.g = u / np;
     x.key0 = 0;
-    x.t0 = (u - x.g * np) * 2 * tok_tile;
-    x.q1 = x.t0 + tok_tile < x.rows;
+    x.t0 = (u - x.g * np) * kQ * tok_tile;
+    x.q1 = !kLone && x.t0 + tok_tile < x.rows;
     x.j_begin = k0 * pairs::kKeys;
-    const int seen = x.past + min(x.rows, x.t0 + 2 * tok_tile);  // by the item's last row
+    const int seen = x.past + min(x.rows, x.t0 + kQ * tok_tile);  // by the item's last row
     x.ntiles = seen > x.j_begin ? min((seen - x.j_begin - 1) / pairs::kKeys + 1, n) : 0;
     x.all = x.past + (x.rows == 1 ? 1 : 0);
     return x.ntiles > 0;
@@ -59,20 +60,20 @@ constexpr int kCombineRows = 8;
 constexpr int kCombineCtas = 4 * kSms;
 
 // Eight rows of a Q tile of a split sequence; lanes by row first, as the parts lie.
-template <typename T, int NVB, bool kPaged>
-__global__ void __launch_bounds__(kCombineRows * NVB * 16) tree_combine_kernel(const TreeWork<kPaged> wk, const int groups,
+template <typename T, int NVB, typename Work>
+__global__ void __launch_bounds__(kCombineRows * NVB * 16) tree_combine_kernel(const Work wk, const int groups,
                                                                                 const bool by_share) {
   pdl_launch_dependents();
   const int group = blockIdx.x % groups, nth = blockIdx.x / groups;
-  const MergedUnit<TreeWork<kPaged>> x(wk, nth, by_share, wk.ctas);
+  const MergedUnit<Work> x(wk, nth, by_share, wk.ctas);
   int r = 0, p = 0, row0 = 0;
   const bool found = x.s >= 0 && wk.bounds(x.s, r, p, row0);
-  const int np = found ? wk.q_pairs(r) : 1, g = found ? x.unit / np : 0, t0 = found ? (x.unit - g * np) * 2 * wk.tok_tile : 0;
-  const int seen = found ? (p + min(r, t0 + 2 * wk.tok_tile) - 1) / pairs::kKeys + 1 : 1;  // tiles of keys
+  const int np = found ? wk.q_units(r) : 1, g = found ? x.unit / np : 0, t0 = found ? (x.unit - g * np) * Work::kQ * wk.tok_tile : 0;
+  const int seen = found ? (p + min(r, t0 + Work::kQ * wk.tok_tile) - 1) / pairs::kKeys + 1 : 1;  // tiles of keys
   const UnitShares u(x.all, found ? x.first : 0, found ? x.n : 1, seen, wk.ctas);
   pdl_wait();  // on all paths: this kernel's end stands for the parts' kernel's
   if (!found || u.whole || (by_share && u.from != nth)) return;
-  const int c4 = threadIdx.x / kCombineRows, per = wk.tok_tile * wk.group, rows = min(2 * wk.tok_tile, r - t0) * wk.group;
+  const int c4 = threadIdx.x / kCombineRows, per = wk.tok_tile * wk.group, rows = min(Work::kQ * wk.tok_tile, r - t0) * wk.group;
   for (int m = group * kCombineRows + threadIdx.x % kCombineRows; m < rows; m += groups * kCombineRows) {
     const int row = m < per ? m : 128 + m - per;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -113,9 +114,10 @@ __global__ void __launch_bounds__(kCombineRows * NVB * 16) tree_combine_kernel(c
   }
 }
 
-template <typename T, int NB, bool kPaged>
+template <typename T, int NB, bool kPaged, bool kLone>
 cudaError_t launch_t(const RowsAttnArgs& a, int dtype, cudaStream_t st) {
-  TreeWork<kPaged> wk;
+  using Work = TreeWork<kPaged, kLone>;
+  Work wk;
   wk.hq = a.hq;
   wk.hkv = a.hkv;
   wk.group = a.group;
@@ -151,15 +153,20 @@ cudaError_t launch_t(const RowsAttnArgs& a, int dtype, cudaStream_t st) {
   // us in all).
   const long long all = a.tiles * a.hkv, units = std::min<long long>(all, a.ctas);
   const int groups = (int)std::min<long long>(256 / kCombineRows, std::max<long long>(1, kCombineCtas / units));
-  return launch_pdl(tree_combine_kernel<T, NB, kPaged>, dim3((unsigned)(units * groups)), dim3(kCombineRows * NB * 16), 0, st, wk,
+  return launch_pdl(tree_combine_kernel<T, NB, Work>, dim3((unsigned)(units * groups)), dim3(kCombineRows * NB * 16), 0, st, wk,
                     groups, all > units);
+}
+
+template <typename T, int NB>
+cudaError_t launch_dim(const RowsAttnArgs& a, int dtype, cudaStream_t st) {
+  if (a.cache.kind == CP_CACHE_PAGED)
+    return a.lone ? launch_t<T, NB, true, true>(a, dtype, st) : launch_t<T, NB, true, false>(a, dtype, st);
+  return a.lone ? launch_t<T, NB, false, true>(a, dtype, st) : launch_t<T, NB, false, false>(a, dtype, st);
 }
 
 template <typename T>
 cudaError_t launch_type(const RowsAttnArgs& a, int dtype, cudaStream_t st) {
-  const bool paged = a.cache.kind == CP_CACHE_PAGED;
-  if (a.dv == 64) return paged ? launch_t<T, 1, true>(a, dtype, st) : launch_t<T, 1, false>(a, dtype, st);
-  return paged ? launch_t<T, 2, true>(a, dtype, st) : launch_t<T, 2, false>(a, dtype, st);
+  return a.dv == 64 ? launch_dim<T, 1>(a, dtype, st) : launch_dim<T, 2>(a, dtype, st);
 }
 
 }  // namespace
@@ -169,8 +176,16 @@ RowsPlan tree_plan(int hq, int hkv, int dv, bool uniform, long long num_seqs, lo
   const int group = hq / hkv, key_tiles = (max_ctx - 1) / pairs::kKeys + 1;
   p.tok_tile = 128 / group;
   const long long rows = std::min<long long>(uniform ? total_rows / num_seqs : total_rows, CP_TREE_MAX);
-  const long long each = (rows - 1) / (2 * p.tok_tile) + 1;  // pairs of Q tiles of a sequence, at most
-  p.tiles = uniform ? num_seqs * each : std::min(tiles_at_most(total_rows, num_seqs, 2 * p.tok_tile), num_seqs * each);
+  const auto units = [&](int tokens) {  // of a KV head, at most
+    const long long most = num_seqs * ((rows - 1) / tokens + 1);
+    return uniform ? most : std::min(tiles_at_most(total_rows, num_seqs, tokens), most);
+  };
+  // Lone Q tiles where few have a second one beside them: both warpgroups have keys then (24 trees of 16 nodes, 32/8
+  // heads x 64, over 4000 to 12000 keys: 101 -> 86 us; 64 of 8, x 128, over 2000 to 6000: 186 -> 180); else pairs, which
+  // read the keys half as often.
+  const long long lone = units(p.tok_tile), pairs = units(2 * p.tok_tile);
+  p.lone = 4 * pairs > 3 * lone;
+  p.tiles = p.lone ? lone : pairs;
   p.work = (double)p.tiles * hkv * (kStart + key_tiles);
   p.ctas = (int)std::min<double>(p.work, kSms);
   p.split = key_tiles > 1;

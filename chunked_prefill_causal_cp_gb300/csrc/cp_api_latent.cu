@@ -88,6 +88,7 @@ int rows_attention(const cp_layer_desc* d, bool latent, int dqk, int dv, float s
   a.q_rows = p.q_rows;
   a.tok_tile = p.tok_tile;
   a.tiles = p.tiles;
+  a.lone = p.lone;
   a.split = p.split;
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = a.part_o + p.part_floats;

@@ -84,7 +84,8 @@ struct RowsAttnArgs {
   int ctas;                // that share the work
   int q_rows;              // a latent cache's: pairs of a tile that the call can have, at most
   int tok_tile;            // a tree's: tokens of a Q tile
-  long long tiles;         // of pairs, or pairs of Q tiles, at most
+  long long tiles;         // of pairs, or (pairs of) Q tiles, at most
+  bool lone;               // a tree's units are of one Q tile
   bool split;              // whether units may be shared by CTAs
   float* part_o;           // parts: unnormalised outputs,
   float* part_ml;          // their maximum (log2 domain) and sum
@@ -94,7 +95,7 @@ struct RowsAttnArgs {
 struct RowsPlan {
   int ctas, q_rows, tok_tile;
   long long tiles;
-  bool split;
+  bool lone, split;
   double work;             // tiles of keys of all units, at most
   long long part_floats;   // of all parts' outputs
   long long bytes;         // of workspace

@@ -203,6 +203,19 @@ def test_a_rows_bits_are_its_own_and_the_sizes(kw):
 
 
 @pytest.mark.parametrize("kw", BOTH)
+def test_wide_trees_over_long_contexts(kw):
+    """Trees of several tiles of rows, their keys over many SMs."""
+    heads, kw = kw["heads"], {k: v for k, v in kw.items() if k != "heads"}
+    past, rows = [5000, 0, 9001], [61, 128, 100]
+    x = Cache(BF16, heads, 3, 9200, 16, **kw)
+    x.fill([p + r for p, r in zip(past, rows)])
+    q = x.queries(sum(rows))
+    parents = [tree(r, k, s) for s, (r, k) in enumerate(zip(rows, ("heap", "random", "chain")))]
+    x.check(q, x.attend(q, past, rows, parents), past, rows, parents)
+    assert int(x.status) == 0
+
+
+@pytest.mark.parametrize("kw", BOTH)
 def test_many_short_sequences(kw):
     """More tiles of rows than SMs, few of which are split; some sequences without context, one-row ones among them."""
     heads, kw = kw["heads"], {k: v for k, v in kw.items() if k != "heads"}
