@@ -141,11 +141,7 @@ Layout layout_of(int dqk, int dv, int q_rows) {
 struct Work : RowsAttnArgs {
   // A sequence within the call's bounds: its rows, positions before them, first row.
   __device__ __forceinline__ bool bounds(int s, int& r, int& p, int& row0) const {
-    r = seq_rows(rows, s);
-    if (r < 1) return false;
-    p = past[s];
-    row0 = seq_row0(rows, s);
-    return p >= 0 && (long long)p + r <= max_ctx && row0 >= 0 && row0 <= total_rows - r && !(parents && r > CP_TREE_MAX);
+    return seq_bounds(rows, past, total_rows, max_ctx, s, r, p, row0) && !(parents && r > CP_TREE_MAX);
   }
   __device__ __forceinline__ int pair_tiles(int r) const { return (r * hq - 1) / kPairs + 1; }
   __device__ __forceinline__ int units(int s, bool report) const {
@@ -715,6 +711,15 @@ __global__ void __launch_bounds__(512) latent_combine_kernel(const Work a, const
   }
 }
 
+// The lengths of the sequences that the attention took.
+__global__ void latent_commit_kernel(int* lens, const SeqRows rows, int total_rows, int max_ctx) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int s = blockIdx.x * blockDim.x + threadIdx.x;
+  int r, p, row0;
+  if (s < rows.num_seqs && seq_bounds(rows, lens, total_rows, max_ctx, s, r, p, row0)) lens[s] = p + r;
+}
+
 template <typename T, bool kPaged>
 cudaError_t launch_t(const RowsAttnArgs& args, int dtype, cudaStream_t st) {
   Work a;
@@ -775,6 +780,12 @@ cudaError_t launch_latent(const RowsAttnArgs& a, int dtype, cudaStream_t st) {
   const bool paged = a.cache.kind == CP_CACHE_PAGED;
   if (dtype == CP_BF16) return paged ? launch_t<__nv_bfloat16, true>(a, dtype, st) : launch_t<__nv_bfloat16, false>(a, dtype, st);
   return paged ? launch_t<__half, true>(a, dtype, st) : launch_t<__half, false>(a, dtype, st);
+}
+
+cudaError_t launch_latent_commit(int* lens, const SeqRows& rows, int total_rows, int max_ctx, cudaStream_t st) {
+  const int block = 128;
+  return launch_pdl(latent_commit_kernel, dim3((unsigned)((rows.num_seqs - 1) / block + 1)), dim3(block), 0, st, lens, rows,
+                    total_rows, max_ctx);
 }
 
 }  // namespace cp

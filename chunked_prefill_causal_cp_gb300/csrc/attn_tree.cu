@@ -25,11 +25,7 @@ struct TreeWork : pairs::WorkBase {
 
   // A sequence within the call's bounds: its rows, positions before them, first row.
   __device__ __forceinline__ bool bounds(int s, int& r, int& p, int& row0) const {
-    r = seq_rows(rows, s);
-    if (r < 1) return false;
-    p = past[s];
-    row0 = seq_row0(rows, s);
-    return p >= 0 && (long long)p + r <= max_ctx && row0 >= 0 && row0 <= total_rows - r && r <= CP_TREE_MAX;
+    return seq_bounds(rows, past, total_rows, max_ctx, s, r, p, row0) && r <= CP_TREE_MAX;
   }
   __device__ __forceinline__ int q_units(int r) const { return (r - 1) / (kQ * tok_tile) + 1; }
   __device__ __forceinline__ int units(int s, bool report) const {

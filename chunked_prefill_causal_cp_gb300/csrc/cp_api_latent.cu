@@ -213,8 +213,7 @@ int cp_latent_attn(const cp_latent_desc* desc, const void* q, const void* cache,
                      cache, seqlens_k, block_table, parents, cu_rows, num_seqs, total_rows, max_ctx, out, workspace,
                      workspace_bytes, dev_status, stream, &rows);
   if (r != CP_OK || total_rows == 0 || !commit) return r;
-  return launch_result(launch_commit(seqlens_k, rows, rows.rows_uniform > 0 ? rows.rows_uniform : -1, nullptr,
-                                     static_cast<cudaStream_t>(stream)));
+  return launch_result(launch_latent_commit(seqlens_k, rows, total_rows, max_ctx, static_cast<cudaStream_t>(stream)));
 }
 
 size_t cp_workspace_size_latent(const cp_latent_desc* desc, int32_t total_rows, int32_t max_ctx, int32_t num_seqs) {

@@ -134,6 +134,7 @@ struct CommitArgs {
 
 cudaError_t launch_latent_append(const LatentAppendArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_latent(const RowsAttnArgs& a, int dtype, cudaStream_t st);
+cudaError_t launch_latent_commit(int* lens, const SeqRows& rows, int total_rows, int max_ctx, cudaStream_t st);
 cudaError_t launch_tree(const RowsAttnArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_expanded(const ExpandedArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_tree_commit(const CommitArgs& a, cudaStream_t st);

@@ -1,6 +1,6 @@
 // cp_rows.cuh -- which sequence a row belongs to, where its position lives in
 // the cache, and conversions between a layer's type and fp32.  Shared by the
-// kernels before and around a 4-bit cache.
+// kernels around 4-bit caches, latent caches and drafted trees.
 #pragma once
 
 #include <cstdint>
@@ -28,6 +28,16 @@ __device__ __forceinline__ int row_seq(const SeqRows& r, int row) {
 __device__ __forceinline__ int row_place(const SeqRows& r, int s, int row) {
   const int i = row - seq_row0(r, s);
   return i < seq_rows(r, s) ? i : -1;
+}
+
+// A sequence within a call's bounds: its rows, positions before them, first row.  Calls skip the others.
+__device__ __forceinline__ bool seq_bounds(const SeqRows& rows, const int* past, int total_rows, int max_ctx, int s, int& r,
+                                           int& p, int& row0) {
+  r = seq_rows(rows, s);
+  if (r < 1) return false;
+  p = past[s];
+  row0 = seq_row0(rows, s);
+  return p >= 0 && (long long)p + r <= max_ctx && row0 >= 0 && row0 <= total_rows - r;
 }
 
 // Index of the (position, KV head) row of sequence s in a cache array, in rows,

@@ -631,8 +631,10 @@ int cp_latent_append(const cp_latent_desc* desc, const cp_qk_prep* prep, const v
  *                 cp_workspace_size_latent(desc, total_rows, max_ctx, num_seqs) bytes; its
  *                 contents before the call do not matter (NULL when that size is 0).
  *                 Calls whose work overlaps on the GPU need separate workspaces
- *   commit        not 0: seqlens_k[s] += rows of s after the attention (with parents:
- *                 CP_ERR_INVALID_ARG; cp_latent_tree_commit advances them)
+ *   commit        not 0: seqlens_k[s] += rows of s after the attention; a sequence that
+ *                 was skipped, or has no rows, keeps its length, one with a bad page
+ *                 does not (with parents: CP_ERR_INVALID_ARG; cp_latent_tree_commit
+ *                 advances them)
  * A row's result depends on its own sequence and, in its last bits, on the rows and
  * positions of the call's other sequences: the keys are shared out over the SMs, and
  * the shares merged, by the whole call's sizes (not by max_ctx).  Scores, softmax sums and outputs are held in
