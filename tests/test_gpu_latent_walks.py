@@ -1,0 +1,110 @@
+"""Long walks over the keys: scores whose maximum rises, falls or stays from tile to tile, so that outputs are rescaled
+while a CTA has a unit.  Against 64 bits."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import chunked_prefill_causal_cp_gb300 as cp
+from latent_util import Cache, f64, half_step, tree
+from oracle import latent as oracle
+
+pytestmark = pytest.mark.gpu
+
+BF16, F16 = torch.bfloat16, torch.float16
+SMS, START = 152, 4  # CTAs that share a call's tiles of keys; a unit counts as so many tiles more
+RISES = (-9.0, 0.0, 3.0, 9.0, 30.0)  # of a pair's scores at each step, in powers of two
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    from chunked_prefill_causal_cp_gb300 import _build
+    _build.build()
+
+
+def off(dtype, q, k, v, see, scale, got):
+    """The largest error of `got` [R, H, V] in units of its tolerance; q [R, H, K], k [n, G, K], v [n, G, V], see [R, n].
+    As oracle.attention, in 64 bits on the GPU."""
+    q, k, v = (x.double() for x in (q, k, v))
+    groups = k.shape[1]
+    x = q.unflatten(1, (groups, -1)).permute(1, 2, 0, 3)  # [G, H / G, R, K]
+    kt, vt = k.permute(1, 2, 0)[:, None], v.permute(1, 0, 2)[:, None]
+    hide = ~torch.from_numpy(see).to(q.device)
+    s = (x @ kt * scale).masked_fill(hide, -math.inf)
+    p = torch.softmax(s, -1)
+    p = p.masked_fill(hide.all(-1)[:, None], 0.0)  # rows that see nothing
+    ref, mag, big = p @ vt, p @ vt.abs(), (x.abs() @ kt.abs()).amax(-1, keepdim=True) * scale
+    ref, mag, big = (y.permute(2, 0, 1, 3).flatten(1, 2).cpu().numpy() for y in (ref, mag, big))
+    tol = oracle.tolerance(half_step(dtype), ref, mag, big, q.shape[2], k.shape[0], dtype == F16, float(v.abs().max()))
+    err = np.abs(f64(got) - ref)
+    assert np.isfinite(err).all()
+    return float((err / tol).max())
+
+
+def steps_of(n, tile):
+    """Steps up to each of n positions: one every third tile, and one more at the last."""
+    j = torch.arange(n)
+    return (j // tile // 3 + (j // tile == (n - 1) // tile)).float()
+
+
+def rising(x, q, channel, tile, lens, seed):
+    """Plants scores that change by RISES at every step: position's steps into `channel` of the keys, what a step is worth
+    into that of the queries.  Steps are whole numbers below 256, exact in both types."""
+    for s, n in enumerate(lens):
+        rows = x.at(x.arrays[0], s, 0, n).clone()
+        rows[..., channel] = steps_of(n, tile).to(x.dtype).cuda()[:, None]
+        x.put(x.arrays[0], s, 0, rows)
+    worth = torch.tensor(RISES)[torch.randint(0, len(RISES), q.shape[:2], generator=torch.Generator().manual_seed(seed))]
+    q[..., channel] = (worth / (x.scale * math.log2(math.e))).to(x.dtype).cuda()
+
+
+def check(x, q, out, past, rows, parents):
+    r0 = 0
+    for s, (p, r) in enumerate(zip(past, rows)):
+        k = x.at(x.arrays[0], s, 0, p + r)
+        v = k[..., :x.latent] if x.latent else x.at(x.v, s, 0, p + r)
+        see = oracle.sees(r, p, None if parents is None else parents[s])
+        assert off(x.dtype, q[r0:r0 + r], k, v, see, x.scale, out[r0:r0 + r]) <= 1.0, s
+        r0 += r
+
+
+@pytest.mark.parametrize("dtype,c,r,heads,seqs,rows,page,kind", [
+    (BF16, 512, 64, 32, 12, 16, 0, "heap"), (F16, 512, 64, 20, 12, 13, 64, None), (BF16, 512, 0, 16, 60, 1, 16, None),
+    (F16, 384, 48, 16, 60, 1, 32, None), (BF16, 384, 16, 40, 12, 20, 0, "random"), (BF16, 256, 32, 128, 10, 5, 128, None),
+    (F16, 128, 16, 40, 12, 17, 16, "heap"), (BF16, 128, 64, 8, 60, 3, 0, "star")])
+def test_latent_maxima_that_rise_along_a_walk(dtype, c, r, heads, seqs, rows, page, kind):
+    past = [500 + (7919 * (i + 3)) % 5501 for i in range(seqs)]
+    lens = [p + rows for p in past]
+    units = -(-rows * heads // 64)
+    assert sum(units * (START + -(-n // 64)) for n in lens) > 10 * SMS  # tiles of a CTA: rises of each kind among them
+    x = Cache(dtype, heads, seqs, 6100, page, latent=c, rope=r, scale=0.05)
+    x.fill(lens)
+    q = x.queries(seqs * rows)
+    rising(x, q, c + r - 1 if r else 0, 64, lens, seed=c + r)
+    parents = kind and [tree(rows, kind, s) for s in range(seqs)]
+    out = x.attend(q, past, [rows] * seqs, parents, uniform=True)
+    assert int(x.status) == 0
+    check(x, q, out, past, [rows] * seqs, parents)
+
+
+@pytest.mark.parametrize("dtype,heads,kv,d,seqs,rows,page,lone", [
+    (BF16, 32, 8, 128, 12, 16, 16, True), (F16, 32, 8, 64, 12, 30, 0, True), (BF16, 5, 5, 64, 24, 20, 64, True),
+    (F16, 32, 8, 128, 12, 61, 0, False), (BF16, 6, 2, 64, 24, 100, 32, False), (BF16, 48, 6, 128, 10, 128, 128, False)])
+def test_tree_maxima_that_rise_along_a_walk(dtype, heads, kv, d, seqs, rows, page, lone):
+    past = [500 + (7919 * (i + 3)) % 5501 for i in range(seqs)]
+    lens = [p + rows for p in past]
+    of = 128 // (heads // kv)  # tokens of a Q tile
+    tiles, two = -(-rows // of), -(-rows // (2 * of))
+    assert (4 * two > 3 * tiles) == lone
+    assert sum((tiles if lone else two) * kv * (START + -(-n // 128)) for n in lens) > 10 * SMS
+    x = Cache(dtype, heads, seqs, 6200, page, kv=kv, d=d)
+    x.fill(lens)
+    q = x.queries(seqs * rows)
+    rising(x, q, 0, 128, lens, seed=rows)
+    parents = [tree(rows, "heap" if s % 2 else "random", s) for s in range(seqs)]
+    out = x.attend(q, past, [rows] * seqs, parents, uniform=True)
+    assert int(x.status) == 0
+    check(x, q, out, past, [rows] * seqs, parents)
