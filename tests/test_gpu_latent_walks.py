@@ -1,5 +1,5 @@
 """Long walks over the keys: scores whose maximum rises, falls or stays from tile to tile, so that outputs are rescaled
-while a CTA has a unit.  Against 64 bits."""
+while a CTA has a unit; all heads of calls whose CTAs have several items.  Against 64 bits."""
 import math
 
 import numpy as np
@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import chunked_prefill_causal_cp_gb300 as cp
-from latent_util import Cache, f64, half_step, tree
+from latent_util import Cache, cu, f64, half_step, tree
 from oracle import latent as oracle
 
 pytestmark = pytest.mark.gpu
@@ -108,3 +108,39 @@ def test_tree_maxima_that_rise_along_a_walk(dtype, heads, kv, d, seqs, rows, pag
     out = x.attend(q, past, [rows] * seqs, parents, uniform=True)
     assert int(x.status) == 0
     check(x, q, out, past, [rows] * seqs, parents)
+
+
+@pytest.mark.parametrize("dtype,heads,dn,r,dv", [
+    (BF16, 40, 128, 64, 128), (F16, 90, 64, 32, 64), (BF16, 60, 128, 0, 64), (BF16, 200, 128, 64, 128),
+    (F16, 201, 64, 32, 64), (BF16, 210, 128, 16, 64), (F16, 195, 64, 0, 128), (BF16, 220, 64, 0, 64)])
+@pytest.mark.parametrize("rise", [False, True])
+def test_expanded_chunks_every_head(dtype, heads, dn, r, dv, rise):
+    """Several lone Q tiles a CTA, and heads enough for pairs of them: every head, with maxima that rise along the keys
+    and without."""
+    rows, keys = [1, 300, 37, 128, 2], [1, 300, 700, 257, 1300]
+    g = torch.Generator().manual_seed(heads)
+    t, n = sum(rows), sum(keys)
+    q = torch.randn(t, heads, dn + r, generator=g).to(dtype).cuda()
+    kv = torch.randn(n, heads, dn + dv, generator=g).to(dtype).cuda()
+    k, v = kv[..., :dn], kv[..., dn:]
+    kr = torch.randn(n, r, generator=g).to(dtype).cuda() if r else None
+    scale = (dn + r) ** -0.5
+    if rise:
+        level = torch.cat([steps_of(m, 128) * 2 for m in keys]).to(dtype).cuda()
+        if r:
+            kr[:, r - 1] = level
+        else:
+            k[..., dn - 1] = level[:, None]
+        worth = torch.tensor(RISES)[torch.randint(0, len(RISES), (t, heads), generator=g)]
+        q[..., dn + r - 1] = (worth / (scale * math.log2(math.e))).to(dtype).cuda()
+    out = torch.full((t, heads, dv), float("nan"), dtype=dtype, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    desc = cp.latent_desc(dtype, 1, heads, 512, r, nope_dim=dn, v_dim=dv, capacity=1)
+    cp.cp_latent_chunk_attn(desc, q, k, kr, v, out, len(rows), t, n, cu_rows=cu(rows), cu_keys=cu(keys), dev_status=status)
+    assert int(status) == 0
+    whole = k if kr is None else torch.cat([k, kr[:, None].expand(n, heads, r)], -1)
+    r0 = k0 = 0
+    for a, m in zip(rows, keys):
+        see = np.arange(m) <= (m - a + np.arange(a))[:, None]
+        assert off(dtype, q[r0:r0 + a], whole[k0:k0 + m], v[k0:k0 + m], see, scale, out[r0:r0 + a]) <= 1.0
+        r0, k0 = r0 + a, k0 + m
