@@ -1,5 +1,5 @@
 """Long walks over the keys: scores whose maximum rises, falls or stays from tile to tile, so that outputs are rescaled
-while a CTA has a unit; all heads of calls whose CTAs have several items.  Against 64 bits."""
+while a CTA has a unit; all heads of calls whose CTAs have several items; and calls one behind another.  Against 64 bits."""
 import math
 
 import numpy as np
@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import chunked_prefill_causal_cp_gb300 as cp
-from latent_util import Cache, cu, f64, half_step, tree
+from latent_util import Cache, cu, f64, half_step, ints, tree
 from oracle import latent as oracle
 
 pytestmark = pytest.mark.gpu
@@ -144,3 +144,36 @@ def test_expanded_chunks_every_head(dtype, heads, dn, r, dv, rise):
         see = np.arange(m) <= (m - a + np.arange(a))[:, None]
         assert off(dtype, q[r0:r0 + a], whole[k0:k0 + m], v[k0:k0 + m], see, scale, out[r0:r0 + a]) <= 1.0
         r0, k0 = r0 + a, k0 + m
+
+
+def test_drafts_one_behind_another_against_the_definition():
+    """A draft's rows in, its attention, the accepted path to its places and the lengths' advance, 20 times without a wait;
+    every round against 64 bits over the rows that each sequence must hold by then."""
+    n, rows, rounds, past = 4, 9, 20, [0, 300, 1000, 63]
+    path, count, parents = [0, 2, 7], [1, 3, 2, 0], tree(9, "heap")
+    g = torch.Generator().manual_seed(7)
+    q = torch.randn(rounds, n * rows, 8, 64, generator=g).to(F16).cuda()
+    new = torch.randn(rounds, 2, n * rows, 2, 64, generator=g).to(F16).cuda()
+    x = Cache(F16, 8, n, 1200, 16, kv=2, d=64)
+    x.fill(past)
+    held = [[x.at(a, s, 0, p).clone() for a in x.arrays] for s, p in enumerate(past)]
+    lens, out = ints(past), torch.full((rounds, n * rows, 8, 64), float("nan"), dtype=F16, device="cuda")
+    ws = torch.full((cp.cp_workspace_size_tree(x.desc, n * rows, 1200, n),), 255, dtype=torch.uint8, device="cuda")
+    par, places, counts = ints(parents * n), ints([path] * n), ints(count)
+    torch.cuda.synchronize()
+    for i in range(rounds):
+        cp.cp_kv_append(x.desc, new[i, 0], new[i, 1], rows, x.k, x.v, lens, 1150, x.table, x.status)
+        cp.cp_tree_attn(x.desc, q[i], x.k, x.v, lens, par, n, n * rows, 1200, out[i], ws, block_table=x.table,
+                        dev_status=x.status)
+        cp.cp_tree_commit(x.desc, x.k, x.v, places, counts, lens, n, 3, 1200, block_table=x.table, dev_status=x.status)
+    assert lens.tolist() == [p + rounds * c for p, c in zip(past, count)] and int(x.status) == 0
+    for i in range(rounds):
+        for s in range(n):
+            at = slice(s * rows, (s + 1) * rows)
+            k, v = (torch.cat([a, b[at]]) for a, b in zip(held[s], new[i]))
+            see = oracle.sees(rows, held[s][0].shape[0], parents)
+            assert off(F16, q[i, at], k, v, see, x.scale, out[i, at]) <= 1.0, (i, s)
+            held[s] = [torch.cat([a, b[at][path[:count[s]]]]) for a, b in zip(held[s], new[i])]
+    for s in range(n):
+        for a, b in zip(x.arrays, held[s]):
+            assert torch.equal(x.at(a, s, 0, b.shape[0]), b)
