@@ -72,6 +72,7 @@ bool encode_strided(CUtensorMap* m, int dtype, const void* base, uint64_t d0, ui
 
 template <typename T, bool kLone>
 cudaError_t launch_t(const ExpandedArgs& a, int dtype, long long items, cudaStream_t st) {
+  const int ctas = (int)std::min<long long>(items, kSms);
   ExpandedWork<kLone> wk;
   wk.hq = wk.hkv = a.heads;
   wk.group = 1;
@@ -100,11 +101,11 @@ cudaError_t launch_t(const ExpandedArgs& a, int dtype, long long items, cudaStre
   }
   const int nqb = a.dn / 64 + (a.r > 0 ? 1 : 0);
   if (a.dv == 64) {
-    if (nqb == 1) return pairs::launch<T, 1, 1>(tm, wk, items, st);
-    return nqb == 2 ? pairs::launch<T, 2, 1>(tm, wk, items, st) : pairs::launch<T, 3, 1>(tm, wk, items, st);
+    if (nqb == 1) return pairs::launch<T, 1, 1>(tm, wk, ctas, st);
+    return nqb == 2 ? pairs::launch<T, 2, 1>(tm, wk, ctas, st) : pairs::launch<T, 3, 1>(tm, wk, ctas, st);
   }
-  if (nqb == 1) return pairs::launch<T, 1, 2>(tm, wk, items, st);
-  return nqb == 2 ? pairs::launch<T, 2, 2>(tm, wk, items, st) : pairs::launch<T, 3, 2>(tm, wk, items, st);
+  if (nqb == 1) return pairs::launch<T, 1, 2>(tm, wk, ctas, st);
+  return nqb == 2 ? pairs::launch<T, 2, 2>(tm, wk, ctas, st) : pairs::launch<T, 3, 2>(tm, wk, ctas, st);
 }
 
 // Items of so many rows, at most.

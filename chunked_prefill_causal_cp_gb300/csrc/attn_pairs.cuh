@@ -719,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
 }
 
 template <typename T, int NQB, int NVB, typename Work>
-cudaError_t launch(const Maps& tm, const Work& wk, long long items, cudaStream_t st) {
+cudaError_t launch(const Maps& tm, const Work& wk, int ctas, cudaStream_t st) {
   using L = Layout<NQB, Work::kLone>;
   static_assert(L::units >= NQB + NVB + (Work::kLone ? NQB : 0), "a tile fits the ring; of a lone Q tile's, the next one's K too");
   const auto kernel = pairs_kernel<T, NQB, NVB, Work>;
@@ -742,7 +742,7 @@ cudaError_t launch(const Maps& tm, const Work& wk, long long items, cudaStream_t
     if (e != cudaSuccess) return e;
     ready_mask.fetch_or(bit, std::memory_order_release);
   }
-  return launch_pdl(kernel, dim3((unsigned)std::min<long long>(items, 152)), dim3(kThreads), smem, st, tm, wk);
+  return launch_pdl(kernel, dim3(ctas), dim3(kThreads), smem, st, tm, wk);
 }
 
 }  // namespace pairs

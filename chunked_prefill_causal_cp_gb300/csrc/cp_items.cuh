@@ -135,7 +135,7 @@ struct ShareCursor {
       all = all_tiles(wk, blockIdx.x == 0);
       load(wk, false);
     }
-    const Shares shares(all, gridDim.x);
+    const Shares shares(all, wk.ctas);  // as the merge has them: the grid is wk.ctas
     const int c = min((int)blockIdx.x, shares.ctas);
     at = shares.begin(c);
     end = shares.begin(min(c + 1, shares.ctas));

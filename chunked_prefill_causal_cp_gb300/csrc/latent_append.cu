@@ -160,8 +160,8 @@ template <typename T>
 cudaError_t launch_t(const LatentAppendArgs& a, cudaStream_t st) {
   const int blocks = a.r ? (a.heads + 1 + 32 / (a.r / 16) - 1) / (32 / (a.r / 16)) : 1;
   // One warp per token computes a token's angles once; with fewer tokens than warps that fill the
-  // GPU (152 SMs x 32), a token's blocks are shared out over more.
-  const int splits = (int)std::min<long long>(blocks, (152LL * 32 + a.total_rows - 1) / a.total_rows);
+  // GPU (32 an SM), a token's blocks are shared out over more.
+  const int splits = (int)std::min<long long>(blocks, (32LL * kSms + a.total_rows - 1) / a.total_rows);
   const int per_warp = (blocks + splits - 1) / splits;
   const dim3 grid((unsigned)(((long long)a.total_rows * 32 + kThreads - 1) / kThreads),
                   (unsigned)((blocks + per_warp - 1) / per_warp));
