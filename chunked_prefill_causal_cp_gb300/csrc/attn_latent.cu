@@ -240,8 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     x = sh->item[k & 1];
     return x.ntiles >= 0;
   };
-  pdl_wait();  // everything below reads what earlier kernels wrote
-  pdl_launch_dependents();  // after it: the combine kernel's lookups read the same inputs
+  pdl_wait_and_launch_dependents();  // everything below, and the combine kernel's lookups, read what earlier kernels wrote
 
   if (warp == 2) {
     // ================================================================ scheduling
@@ -635,6 +634,7 @@ __global__ void __launch_bounds__(512) latent_combine_kernel(const Work a, const
   __shared__ float4 so[512];
   __shared__ float2 sml[16];
   pdl_launch_dependents();
+  pdl_look_ahead();
   const int nth = blockIdx.x / groups;
   const MergedUnit<Work> x(a, nth, by_share, a.ctas);
   int r = 0, p = 0, row0 = 0;

@@ -199,8 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
     x = sh->item[k & 1];
     return x.ntiles >= 0;
   };
-  pdl_wait();  // everything below reads what earlier kernels wrote
-  pdl_launch_dependents();  // after it: the combine kernel's lookups read the same inputs
+  pdl_wait_and_launch_dependents();  // everything below, and the combine kernel's lookups, read what earlier kernels wrote
 
   if (warp < 4) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));

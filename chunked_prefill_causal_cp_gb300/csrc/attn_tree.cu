@@ -60,6 +60,7 @@ template <typename T, int NVB, typename Work>
 __global__ void __launch_bounds__(kCombineRows * NVB * 16) tree_combine_kernel(const Work wk, const int groups,
                                                                                 const bool by_share) {
   pdl_launch_dependents();
+  pdl_look_ahead();
   const int group = blockIdx.x % groups, nth = blockIdx.x / groups;
   const MergedUnit<Work> x(wk, nth, by_share, wk.ctas);
   int r = 0, p = 0, row0 = 0;

@@ -146,6 +146,27 @@ def test_expanded_chunks_every_head(dtype, heads, dn, r, dv, rise):
         r0, k0 = r0 + a, k0 + m
 
 
+@pytest.mark.parametrize("heads,rows,steps,page", [(4, 16, 40, 0), (4, 100, 12, 16), (32, 64, 16, 64)])
+def test_lengths_that_grow_behind_one_another(heads, rows, steps, page):
+    """Calls that advance the lengths themselves, enqueued without a wait: each takes its tiles, and merges its parts, by
+    the lengths that the one before left.  The first grids are smaller than the merge's, which runs on other SMs too."""
+    past = [0, 37]
+    x = Cache(BF16, heads, 2, rows * steps + 64, page, latent=512, rope=64)
+    x.fill([p + rows * steps for p in past])
+    t = 2 * rows
+    q = x.queries(steps * t).unflatten(0, (steps, t))
+    out = torch.full((steps, t, heads, 512), float("nan"), dtype=BF16, device="cuda")
+    ws = torch.full((cp.cp_workspace_size_latent(x.desc, t, rows * steps + 64, 2),), 255, dtype=torch.uint8, device="cuda")
+    lens = ints(past)
+    torch.cuda.synchronize()
+    for i in range(steps):
+        cp.cp_latent_attn(x.desc, q[i], x.x, lens, 2, t, rows * steps + 64, out[i], ws, block_table=x.table, commit=True,
+                          dev_status=x.status)
+    assert lens.tolist() == [p + rows * steps for p in past] and int(x.status) == 0
+    for i in range(steps):
+        check(x, q[i], out[i], [p + rows * i for p in past], [rows] * 2, None)
+
+
 def test_drafts_one_behind_another_against_the_definition():
     """A draft's rows in, its attention, the accepted path to its places and the lengths' advance, 20 times without a wait;
     every round against 64 bits over the rows that each sequence must hold by then."""
