@@ -668,7 +668,9 @@ size_t cp_workspace_size_latent(const cp_latent_desc* desc, int32_t total_rows, 
  *                 stride of at least the channels, a row stride of at least H head
  *                 strides), so that both may be slices of one product's output
  *   k_rope        device rows of R channels, k_rope_stride elements apart (0 = dense;
- *                 NULL when R is 0): it may be the cache's own rows
+ *                 NULL when R is 0).  For one sequence of a CONTIG cache they may be the
+ *                 cache's own, x[C, C + R) of its rows; pages, and a batch's sequences with
+ *                 room behind each, do not follow one another without gaps as cu_keys needs
  *   cu_rows, cu_keys  device int32 [num_seqs + 1], both given, or both NULL: total_rows /
  *                 num_seqs rows and total_keys / num_seqs keys each.  A sequence whose
  *                 rows or keys are not within the totals, or that has no rows, sets
