@@ -39,6 +39,14 @@
 // positions that hold a non-finite value; the pairs that see such a one become NaN by
 // their sum.
 //
+// Weights are rounded to the layer's type for O^T += V^T P^T (nothing else is, before the output: scores, maxima, sums,
+// O and parts are fp32, and the sums are of the weights before their rounding).  Both operands of that MMA are of one
+// type, and V is multiplied as it lies in the cache: weights in 32 bits would want V widened in shared memory, twice the
+// bytes of what bounds a tile, and weights in two 16-bit halves a second product with V.  What it costs against 64
+// bits, relative, root mean square, with the output's own rounding (alone 1.7e-3 in bf16, 2.1e-4 in fp16): 1.8e-3 to
+// 2.4e-3 and 2.5e-4.  (Weights of one size have errors of the output's own, independent ones: a factor of up to sqrt(2).)
+// A weight below fp16's normal range is off by up to 2^-25 of the largest.
+//
 // The CTAs share the tiles of keys of all tiles of pairs out evenly (cp_latent.h); a tile of
 // pairs that several of them have leaves unnormalised fp32 parts and (maximum, sum) in
 // the workspace, which the combine kernel merges in order.
@@ -524,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             x0 = ex2_approx(x0);
             x1 = ex2_approx(x1);
             fadd2(ps[2 * (c & 1)], ps[2 * (c & 1) + 1], x0, x1);
-            sv[c] = pack2<T>(x0, x1);
+            sv[c] = pack2<T>(x0, x1);  // V's type: see above
           }
           l_run += (ps[0] + ps[1]) + (ps[2] + ps[3]);
         }

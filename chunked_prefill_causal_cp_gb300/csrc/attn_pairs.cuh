@@ -30,6 +30,11 @@
 // value, are overwritten with zeros in shared memory; the rows that see such a key
 // become NaN by their sum.
 //
+// Weights are rounded to the layer's type for O_w += P_w V, and nothing else is before the output (the sums are of the
+// weights before their rounding): both operands of that MMA are of one type, and V is multiplied as it lies.  Weights in
+// two 16-bit halves would cost a second product, of a path that the tensor cores bound.  What the rounding costs in
+// accuracy: see attn_latent.cu.
+//
 // Measured: see attn_tree.cu and attn_expanded.cu.  With all in place a pair's tile of keys
 // takes about 3000 clocks: softmax 1400, then P V and the next Q K^T of its Q tile 1000 to
 // 1300, and two hand-overs of 200 to 300, during which the other Q tile has the tensor cores (2050
@@ -528,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) pairs_kernel(const __grid_constan
         x0 = ex2_approx(x0);
         x1 = ex2_approx(x1);
         fadd2(ps[2 * (c & 1)], ps[2 * (c & 1) + 1], x0, x1);
-        sv[c] = pack2<T>(x0, x1);
+        sv[c] = pack2<T>(x0, x1);  // V's type: see above
       }
       l_run = l_run * alpha + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
       m_run = m_new;
