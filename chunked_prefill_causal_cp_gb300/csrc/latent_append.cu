@@ -13,7 +13,7 @@
 //
 // Bound by the rows' bytes, with many tokens; the first loads are issued before a row's
 // place and angles are known, which took a seventh off.  8192 tokens of 512 + 64 channels
-// and 32 heads: 19.1 us for 85.9 MB, 4.5 TB/s; one token: 2.7 us, a launch.
+// and 32 heads: 19.3 us for 85.9 MB, 4.5 TB/s; one token: 2.9 us, a launch.
 #include <algorithm>
 #include <cstdint>
 
